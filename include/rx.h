@@ -249,6 +249,96 @@ rx_status rx_tail_append(void* k_tail, void* v_tail, int* tail_len, const void* 
                          const void* v_new, const int* active, int B, int tail_cap,
                          int Hkv, int D, int* overflow, void* stream);
 
+/* Append up to T tokens to each stream's 8-bit tail.  A token's vector x of
+ * one K/V head is stored as D e4m3 codes and one byte e, standing for
+ *   x_i ~ code_i * 2^(e - 127):
+ * e - 127 is the smallest exponent >= -127 with max_i |x_i| <= 448 * 2^(e - 127),
+ * and code_i = x_i * 2^(127 - e) rounded to nearest even.  The scaling is
+ * exact, so the code's rounding (at most 2^-4 of the value, or half of e4m3's
+ * smallest step, 2^-10 * 2^(e - 127)) is the only one.  All zeros: e = 0.  A
+ * vector with an infinity or a NaN: e = 255 and zero codes, which reads back
+ * as NaN.
+ * For stream b and t < n_new[b], K and V of new token t go to place
+ * tail_len[b] + t; tokens past tail_cap are dropped and bit 0 of *overflow is
+ * set (so is it, and nothing is stored, when tail_len[b] is outside
+ * [0, tail_cap] and n_new[b] > 0).  new_len[b] = min(tail_len[b] + n_new[b],
+ * tail_cap) (or tail_len[b] where that is outside).  tail_len itself is not
+ * changed, so the appends of all layers can share it; new_len is what the
+ * attention of the same step reads.
+ * k_tail, v_tail: e4m3 [B][tail_cap][Hkv][D]; k_exp, v_exp: uint8
+ * [B][tail_cap][Hkv]; k_new, v_new: bf16 [B][T][Hkv][D]; tail_len, new_len,
+ * n_new: DEVICE int32 [B] (n_new NULL: T for every stream; values are clamped
+ * to [0, T]; new_len NULL: not written; new_len may not overlap the others);
+ * overflow: DEVICE int32 or NULL.  D in {64, 128, 256}, B*T*Hkv <= 2^32.
+ * Errors: RX_ERR_ARG, RX_ERR_UNSUPPORTED (D), RX_ERR_CUDA. */
+rx_status rx_tail_append_quant(void* k_tail, void* v_tail, unsigned char* k_exp,
+                               unsigned char* v_exp, const int* tail_len, int* new_len,
+                               const void* k_new, const void* v_new, const int* n_new,
+                               int B, int T, int tail_cap, int Hkv, int D, int* overflow,
+                               void* stream);
+
+/* A dense batch of language streams with 8-bit tails (rx_tail_append_quant). */
+typedef struct rx_quant_streams {
+  const void* q;               /* bf16 [B][T][Hq][D]                              */
+  const void* k_tail;          /* e4m3 [B][tail_cap][Hkv][D], 16-byte aligned     */
+  const void* v_tail;          /* e4m3 [B][tail_cap][Hkv][D], 16-byte aligned     */
+  const unsigned char* k_exp;  /* [B][tail_cap][Hkv]                              */
+  const unsigned char* v_exp;  /* [B][tail_cap][Hkv]                              */
+  const int* tail_len;         /* DEVICE int32 [B]: keys held by each tail, the
+                                  query tokens' own among them; clamped to
+                                  [0, tail_cap] (read on the device)              */
+  const int* n_new;            /* DEVICE int32 [B] or NULL (T for every stream):
+                                  query tokens of each stream, at most T          */
+  void* out;                   /* bf16 [B][T][Hq][D]                              */
+  int B;                       /* streams, >= 0                                   */
+  int T;                       /* most query tokens of one stream, >= 1           */
+} rx_quant_streams;
+
+/* Attention of language streams over the shared store and their own 8-bit
+ * tails ("OxyGen ...", §"Core method": one read-only prefill cache, private
+ * appended KV).  The query tokens of stream b are the newest n_new[b] tokens
+ * of its tail; token t attends, with one softmax, over [pinned; window;
+ * tail_b[0, tail_len[b] - n_new[b] + t + 1)]: everything before it and itself,
+ * not the tokens after it.  The cached regions are read once for all streams,
+ * each tail once.  fp32 accumulation and softmax; out rounded once to bf16.
+ * Rows t >= n_new[b] of out are left as they were.  A row that sees no key
+ * gets zeros.  Nothing at or past tail_len[b] is used, whatever it holds; a
+ * NaN token (exponent byte 255) makes the rows that see it NaN and no others.
+ * Codes below tail_len[b] must not be NaN codes (the append stores none).
+ * B*T <= max_req, tail_cap is the cache's (>= 1); the cache's device has to be
+ * the current one.  out may not overlap an input.
+ * Errors: RX_ERR_ARG, RX_ERR_LAYER, RX_ERR_CAPACITY, RX_ERR_STATE (another
+ * device is current), RX_ERR_CUDA. */
+rx_status rx_attend_streams_quant(rx_cache_t cache, int layer, const rx_quant_streams* streams,
+                                  void* stream);
+
+/* Verification of drafted tokens against the target's probabilities, from
+ * given random numbers.  Stream b drafted n = n_draft[b] tokens x_0..x_{n-1}.
+ *   x_t is accepted while u[b][t] * q[b][t][x_t] < p[b][t][x_t];
+ *   a = the first t that is not, or n: n_accept[b] = a;
+ *   w_i = max(p[b][a][i] - q[b][a][i], 0) if a < n, p[b][n][i] if a = n;
+ *         p[b][a][i] where no such difference is positive;
+ *   next = the smallest i with w_0 + .. + w_i > r[b] * (w_0 + .. + w_{V-1}).
+ * tokens[b] = x_0..x_{a-1}, next, then -1.  Entries of w that are NaN or
+ * infinite count as 0; if none is positive, next = -1.  A token outside
+ * [0, V) is not accepted.  q NULL: the drafts carry no probabilities, q is 1
+ * at x_t and 0 elsewhere.  n_draft[b] < 0 marks an idle slot: n_accept = -1,
+ * tokens -1, new_len[b] = tail_len[b].  T = 0 samples one token from p[b][0].
+ * new_len[b] = tail_len[b] + 1 + a: the keys to keep when tail_len[b] counts
+ * those before the step, which appended the last token and the drafts.
+ * Products, differences and sums are taken in 64 bits, in a fixed order.
+ * p: [B][T+1][V], q: [B][T][V] or NULL, both of type prob_type; draft: int32
+ * [B][T]; u: fp32 [B][T], r: fp32 [B], all in [0, 1); n_draft: int32 [B] or
+ * NULL (T), clamped to T; tail_len, new_len: int32 [B] or NULL (new_len may
+ * be tail_len); tokens: int32 [B][T+1]; n_accept: int32 [B].  All DEVICE
+ * memory.  V <= 2^28.  Errors: RX_ERR_ARG, RX_ERR_CUDA. */
+#define RX_PROB_F32 0
+#define RX_PROB_BF16 1
+rx_status rx_verify_drafts(const void* p, const void* q, int prob_type, const int* draft,
+                           const float* u, const float* r, const int* n_draft, int B, int T,
+                           int V, const int* tail_len, int* tokens, int* n_accept,
+                           int* new_len, void* stream);
+
 /* Ring-state snapshot / restore (execution-state capsules as in the FlashRT
  * summary page: snapshot and restore of the named static buffers).  A
  * snapshot holds the pinned prefix, the window, the device-side ring state

@@ -1,0 +1,138 @@
+// quant_tail.cu -- appending tokens to the language streams' 8-bit tails.
+//
+// "OxyGen: Unified KV Cache Management for Vision-Language-Action Models under
+// Multi-Task Parallelism", §"Core method": every stream appends its own keys
+// and values to a private tail.  Here a token's vector x of one K/V head is
+// kept as D e4m3 codes and one byte, the exponent of a power-of-two scale
+// 2^(byte - 127):
+//   e    = the smallest integer >= -127 with max_i |x_i| <= 448 * 2^e
+//   code = x_i * 2^-e rounded to e4m3 (nearest, ties to even), byte = e + 127
+// so the largest code uses the top of the e4m3 range (448 is its largest
+// value) and the scaling itself is exact: the code's rounding, at most 2^-4 of
+// the value, is the only one.  An all-zero vector gets byte 0; a vector with
+// an infinity or a NaN gets byte 255, which stands for NaN, and zero codes:
+// it reads back as NaN without putting NaN codes where a masked product
+// would meet them.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "rx_internal.h"
+#include "sm103_ptx.cuh"
+
+namespace rx {
+namespace {
+
+constexpr int kAppendThreads = 256;
+
+// Two fp32 values -> two e4m3 codes (the first in the low byte).
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Quantise the vector that L = D/8 consecutive lanes hold, eight bf16 values
+// each: *codes = this lane's eight codes, returns the vector's exponent byte.
+// Every lane of the warp calls it.
+template <int L>
+__device__ __forceinline__ uint32_t quantise8(const uint4& x, uint2* codes) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  // The magnitudes' bf16 bits order like the magnitudes.
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  // 1.m * 2^(E-127) <= 448 * 2^e = 1.75 * 2^(8+e): e = E - 135, one more
+  // when the mantissa is above .75 (96/128).
+  const uint32_t E = top >> 7, M = top & 0x7Fu;
+  const int b = static_cast<int>(E) - 8 + (M > 96u ? 1 : 0);
+  const uint32_t byte = E == 255u ? 255u : static_cast<uint32_t>(max(b, 0));
+  // 2^-e; a poisoned vector's codes are zeros.
+  const float up = __uint_as_float((254u - min(byte, 254u)) << 23);
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = byte == 255u ? 0.f : __uint_as_float(w[i] << 16) * up;
+    f[2 * i + 1] = byte == 255u ? 0.f : __uint_as_float(w[i] & 0xFFFF0000u) * up;
+  }
+  *codes = make_uint2(e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16), e4m3x2(f[4], f[5]) | (e4m3x2(f[6], f[7]) << 16));
+  return byte;
+}
+
+// D/8 lanes per (stream, token, head); each lane moves 16 bytes of K and of V.
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads) tail_append_quant_kernel(
+    uint2* __restrict__ k_tail, uint2* __restrict__ v_tail, uint8_t* __restrict__ k_exp,
+    uint8_t* __restrict__ v_exp, const int* __restrict__ tail_len, int* __restrict__ new_len,
+    const uint4* __restrict__ k_new, const uint4* __restrict__ v_new, const int* __restrict__ n_new, int B, int T,
+    int tail_cap, int Hkv, int* overflow) {
+  constexpr int L = D / 8;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const long long i = static_cast<long long>(blockIdx.x) * kAppendThreads + threadIdx.x;
+  const long long vec = i / L;   // (b * T + t) * Hkv + h
+  const int sub = static_cast<int>(i % L);
+  const int h = static_cast<int>(vec % Hkv);
+  const long long bt = vec / Hkv;
+  const int t = static_cast<int>(bt % T);
+  const int b = static_cast<int>(bt / T);
+  bool store = false;
+  int at = 0;
+  if (b < B) {
+    const int len = tail_len[b];
+    const int n = n_new ? max(0, min(n_new[b], T)) : T;
+    const bool fine = len >= 0 && len <= tail_cap;
+    at = len + t;
+    store = fine && t < n && at < tail_cap;
+    if (sub == 0 && h == 0) {
+      if (t < n && !store && overflow) atomicOr(overflow, 1);
+      if (t == 0 && new_len) new_len[b] = fine ? min(len + n, tail_cap) : len;
+    }
+  }
+  uint4 kx = make_uint4(0u, 0u, 0u, 0u), vx = kx;
+  if (store) {
+    kx = k_new[i];
+    vx = v_new[i];
+  }
+  uint2 kc, vc;
+  const uint32_t kb = quantise8<L>(kx, &kc), vb = quantise8<L>(vx, &vc);
+  if (!store) return;
+  const long long dst = (static_cast<long long>(b) * tail_cap + at) * Hkv + h;
+  k_tail[dst * L + sub] = kc;
+  v_tail[dst * L + sub] = vc;
+  if (sub == 0) {
+    k_exp[dst] = static_cast<uint8_t>(kb);
+    v_exp[dst] = static_cast<uint8_t>(vb);
+  }
+}
+
+template <int D>
+cudaError_t launch_d(void* k_tail, void* v_tail, uint8_t* k_exp, uint8_t* v_exp, const int* tail_len, int* new_len,
+                     const void* k_new, const void* v_new, const int* n_new, int B, int T, int tail_cap, int Hkv,
+                     int* overflow, cudaStream_t s) {
+  const long long threads = static_cast<long long>(B) * T * Hkv * (D / 8);
+  const unsigned int blocks = static_cast<unsigned int>((threads + kAppendThreads - 1) / kAppendThreads);
+  const cudaError_t e = launch_k(tail_append_quant_kernel<D>, dim3(blocks), dim3(kAppendThreads), 0, s,
+                                 static_cast<uint2*>(k_tail), static_cast<uint2*>(v_tail), k_exp, v_exp, tail_len,
+                                 new_len, static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), n_new, B,
+                                 T, tail_cap, Hkv, overflow);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_tail_append_quant(void* k_tail, void* v_tail, uint8_t* k_exp, uint8_t* v_exp, const int* tail_len,
+                                     int* new_len, const void* k_new, const void* v_new, const int* n_new, int B,
+                                     int T, int tail_cap, int Hkv, int D, int* overflow, cudaStream_t s) {
+  switch (D) {
+    case 64: return launch_d<64>(k_tail, v_tail, k_exp, v_exp, tail_len, new_len, k_new, v_new, n_new, B, T, tail_cap, Hkv, overflow, s);
+    case 128: return launch_d<128>(k_tail, v_tail, k_exp, v_exp, tail_len, new_len, k_new, v_new, n_new, B, T, tail_cap, Hkv, overflow, s);
+    case 256: return launch_d<256>(k_tail, v_tail, k_exp, v_exp, tail_len, new_len, k_new, v_new, n_new, B, T, tail_cap, Hkv, overflow, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace rx

@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -46,6 +47,8 @@ rx_status cuda_fail(cudaError_t e, const char* what) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 
@@ -559,6 +562,136 @@ rx_status rx_tail_append(void* k_tail, void* v_tail, int* tail_len, const void* 
   cudaError_t e = rx::launch_tail_append(k_tail, v_tail, tail_len, k_new, v_new, active, B, tail_cap,
                                          Hkv, D, overflow, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rx_tail_append: launch");
+  return RX_OK;
+  RX_GUARD_END
+}
+
+rx_status rx_tail_append_quant(void* k_tail, void* v_tail, unsigned char* k_exp, unsigned char* v_exp,
+                               const int* tail_len, int* new_len, const void* k_new, const void* v_new,
+                               const int* n_new, int B, int T, int tail_cap, int Hkv, int D, int* overflow,
+                               void* stream) {
+  RX_GUARD_BEGIN
+  if (B < 0 || T < 1 || tail_cap < 1 || Hkv < 1 || T > (1 << 28) || tail_cap > (1 << 28))
+    return fail(RX_ERR_ARG, "rx_tail_append_quant: sizes out of range");
+  if (D != 64 && D != 128 && D != 256)
+    return fail(RX_ERR_UNSUPPORTED, "rx_tail_append_quant: head dim %d not in {64, 128, 256}", D);
+  if (static_cast<long long>(B) * T > (1LL << 32) / Hkv)   // also keeps the grid below 2^31 blocks
+    return fail(RX_ERR_ARG, "rx_tail_append_quant: B*T*Hkv above 2^32");
+  if (B == 0) return RX_OK;
+  if (!k_tail || !v_tail || !k_exp || !v_exp || !tail_len || !k_new || !v_new)
+    return fail(RX_ERR_ARG, "rx_tail_append_quant: null pointer");
+  if (!aligned16(k_tail) || !aligned16(v_tail) || !aligned16(k_new) || !aligned16(v_new) || !aligned4(tail_len) ||
+      !aligned4(new_len) || !aligned4(n_new) || !aligned4(overflow))
+    return fail(RX_ERR_ARG, "rx_tail_append_quant: misaligned pointer");
+  const long long lens = static_cast<long long>(B) * 4;
+  if (spans_overlap(new_len, lens, tail_len, lens) || spans_overlap(new_len, lens, n_new, lens))
+    return fail(RX_ERR_ARG, "rx_tail_append_quant: new_len may not overlap tail_len or n_new");
+  cudaError_t e = rx::launch_tail_append_quant(k_tail, v_tail, k_exp, v_exp, tail_len, new_len, k_new, v_new, n_new,
+                                               B, T, tail_cap, Hkv, D, overflow, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rx_tail_append_quant: launch");
+  return RX_OK;
+  RX_GUARD_END
+}
+
+rx_status rx_attend_streams_quant(rx_cache_t h, int layer, const rx_quant_streams* batch, void* stream) {
+  RX_GUARD_BEGIN
+  if (!h || !batch) return fail(RX_ERR_ARG, "rx_attend_streams_quant: null argument");
+  const rx_config& c = h->cfg;
+  const rx_quant_streams& b = *batch;
+  if (layer < 0 || layer >= c.L)
+    return fail(RX_ERR_LAYER, "rx_attend_streams_quant: layer %d not in [0, %d)", layer, c.L);
+  if (b.B < 0 || b.T < 1) return fail(RX_ERR_ARG, "rx_attend_streams_quant: B < 0 or T < 1");
+  if (static_cast<long long>(b.B) * b.T > c.max_req)
+    return fail(RX_ERR_CAPACITY, "rx_attend_streams_quant: B*T = %lld > max_req = %d",
+                static_cast<long long>(b.B) * b.T, c.max_req);
+  if (c.tail_cap < 1) return fail(RX_ERR_CAPACITY, "rx_attend_streams_quant: the cache has tail_cap = 0");
+  if (b.B == 0) return RX_OK;
+  if (!b.q || !b.k_tail || !b.v_tail || !b.k_exp || !b.v_exp || !b.tail_len || !b.out)
+    return fail(RX_ERR_ARG, "rx_attend_streams_quant: null pointer");
+  if (!aligned16(b.q) || !aligned16(b.k_tail) || !aligned16(b.v_tail) || !aligned16(b.out) || !aligned4(b.tail_len) ||
+      !aligned4(b.n_new))
+    return fail(RX_ERR_ARG, "rx_attend_streams_quant: misaligned pointer");
+  {
+    const long long qb = static_cast<long long>(b.B) * b.T * c.Hq * c.D * 2;
+    const long long eb = static_cast<long long>(b.B) * c.tail_cap * c.Hkv, tb = eb * c.D, lb = static_cast<long long>(b.B) * 4;
+    const Span in[7] = {{b.q, qb}, {b.k_tail, tb}, {b.v_tail, tb}, {b.k_exp, eb}, {b.v_exp, eb}, {b.tail_len, lb}, {b.n_new, lb}};
+    for (const Span& x : in)
+      if (spans_overlap(b.out, qb, x.p, x.bytes))
+        return fail(RX_ERR_ARG, "rx_attend_streams_quant: out overlaps an input");
+  }
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "rx_attend_streams_quant: cudaGetDevice");
+  if (dev != h->device)
+    return fail(RX_ERR_STATE, "rx_attend_streams_quant: the cache is on device %d, the current device is %d", h->device, dev);
+  const rx::AttnLaunch a = make_launch(h, layer);
+  rx::QuantStreams s{};
+  s.q = static_cast<const __nv_bfloat16*>(b.q);
+  s.k_tail = static_cast<const uint8_t*>(b.k_tail);
+  s.v_tail = static_cast<const uint8_t*>(b.v_tail);
+  s.k_exp = b.k_exp;
+  s.v_exp = b.v_exp;
+  s.tail_len = b.tail_len;
+  s.n_new = b.n_new;
+  s.out = static_cast<__nv_bfloat16*>(b.out);
+  s.B = b.B;
+  s.T = b.T;
+  s.Hq = c.Hq;
+  s.Hkv = c.Hkv;
+  s.D = c.D;
+  s.tail_cap = c.tail_cap;
+  s.pin_k = static_cast<const uint8_t*>(a.pin_k_tiles);
+  s.pin_v = static_cast<const uint8_t*>(a.pin_v_tiles);
+  s.win_k = static_cast<const uint8_t*>(a.win_k_tiles);
+  s.win_v = static_cast<const uint8_t*>(a.win_v_tiles);
+  s.pin_head_stride = a.pin_head_stride;
+  s.win_head_stride = a.win_head_stride;
+  s.st = a.st;
+  s.P = a.P;
+  s.F = a.F;
+  s.N = a.N;
+  s.slots = a.slots;
+  s.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(c.D)));
+  e = rx::launch_streams_quant(s, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rx_attend_streams_quant: launch");
+  return RX_OK;
+  RX_GUARD_END
+}
+
+rx_status rx_verify_drafts(const void* p, const void* q, int prob_type, const int* draft, const float* u,
+                           const float* r, const int* n_draft, int B, int T, int V, const int* tail_len,
+                           int* tokens, int* n_accept, int* new_len, void* stream) {
+  RX_GUARD_BEGIN
+  if (B < 0 || T < 0 || V < 1 || B > (1 << 20) || T > (1 << 20) || V > (1 << 28))
+    return fail(RX_ERR_ARG, "rx_verify_drafts: sizes out of range");
+  if (prob_type != RX_PROB_F32 && prob_type != RX_PROB_BF16)
+    return fail(RX_ERR_ARG, "rx_verify_drafts: prob_type %d", prob_type);
+  if (B == 0) return RX_OK;
+  if (!p || !r || !tokens || !n_accept || (T > 0 && (!draft || !u)))
+    return fail(RX_ERR_ARG, "rx_verify_drafts: null pointer");
+  if (new_len && !tail_len) return fail(RX_ERR_ARG, "rx_verify_drafts: new_len without tail_len");
+  const uintptr_t pm = prob_type == RX_PROB_F32 ? 3 : 1;
+  if ((reinterpret_cast<uintptr_t>(p) & pm) || (reinterpret_cast<uintptr_t>(q) & pm) || !aligned4(draft) ||
+      !aligned4(u) || !aligned4(r) || !aligned4(n_draft) || !aligned4(tail_len) || !aligned4(tokens) ||
+      !aligned4(n_accept) || !aligned4(new_len))
+    return fail(RX_ERR_ARG, "rx_verify_drafts: misaligned pointer");
+  const long long n_tok = static_cast<long long>(B) * (T + 1) * 4, n_b = static_cast<long long>(B) * 4;
+  const Span in[4] = {{draft, static_cast<long long>(B) * T * 4}, {u, static_cast<long long>(B) * T * 4}, {r, n_b}, {n_draft, n_b}};
+  const Span outs[3] = {{tokens, n_tok}, {n_accept, n_b}, {new_len, n_b}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Span& x : in)
+      if (spans_overlap(outs[i].p, outs[i].bytes, x.p, x.bytes))
+        return fail(RX_ERR_ARG, "rx_verify_drafts: an output overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (spans_overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+        return fail(RX_ERR_ARG, "rx_verify_drafts: outputs overlap");
+  }
+  if (spans_overlap(tokens, n_tok, tail_len, n_b) || spans_overlap(n_accept, n_b, tail_len, n_b) ||
+      (new_len != tail_len && spans_overlap(new_len, n_b, tail_len, n_b)))
+    return fail(RX_ERR_ARG, "rx_verify_drafts: an output overlaps tail_len (new_len may be the same array)");
+  cudaError_t e = rx::launch_verify_drafts(p, q, prob_type == RX_PROB_BF16, draft, u, r, n_draft, B, T, V, tail_len,
+                                           tokens, n_accept, new_len, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rx_verify_drafts: launch");
   return RX_OK;
   RX_GUARD_END
 }

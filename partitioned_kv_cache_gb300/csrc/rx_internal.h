@@ -97,6 +97,11 @@ cudaError_t launch_tail_append(void* k_tail, void* v_tail, int* tail_len, const 
                                const void* v_new, const int* active, int B, int tail_cap,
                                int Hkv, int D, int* overflow, cudaStream_t s);
 
+// Append up to T tokens per stream to 8-bit tails (quant_tail.cu).
+cudaError_t launch_tail_append_quant(void* k_tail, void* v_tail, uint8_t* k_exp, uint8_t* v_exp, const int* tail_len,
+                                     int* new_len, const void* k_new, const void* v_new, const int* n_new, int B,
+                                     int T, int tail_cap, int Hkv, int D, int* overflow, cudaStream_t s);
+
 // Inverse of the packing for one layer and token range (test aid):
 // dst [n][Hkv][D] <- tiles.
 cudaError_t launch_unpack_tiles(const void* k_tiles, const void* v_tiles, void* k_dst, void* v_dst,
@@ -181,6 +186,35 @@ struct AttnSegment {
 // when more than one split is used).  Both segments read the same shared K/V.
 cudaError_t launch_partitioned_attention(const AttnLaunch& a, const AttnSegment* segs, int nseg,
                                          cudaStream_t s, int* used_splits);
+
+// ---- language streams over 8-bit tails ---------------------------------------
+struct QuantStreams {
+  const __nv_bfloat16* q;    // [B][T][Hq][D]
+  const uint8_t* k_tail;     // e4m3 codes [B][tail_cap][Hkv][D]
+  const uint8_t* v_tail;
+  const uint8_t* k_exp;      // scale exponents [B][tail_cap][Hkv]
+  const uint8_t* v_exp;
+  const int* tail_len;       // device [B]
+  const int* n_new;          // device [B]; null: T for every stream
+  __nv_bfloat16* out;        // [B][T][Hq][D]
+  int B, T, Hq, Hkv, D, tail_cap;
+  // The shared store's tiles of one layer (head 0) and its ring state.
+  const uint8_t* pin_k;
+  const uint8_t* pin_v;
+  const uint8_t* win_k;
+  const uint8_t* win_v;
+  long long pin_head_stride;
+  long long win_head_stride;
+  const DevState* st;
+  int P, F, N, slots;
+  float scale_log2;          // log2(e) / sqrt(D)
+};
+cudaError_t launch_streams_quant(const QuantStreams& a, cudaStream_t s);
+
+// ---- verification of drafted tokens ------------------------------------------
+cudaError_t launch_verify_drafts(const void* p, const void* q, bool bf16, const int* draft, const float* u,
+                                 const float* r, const int* n_draft, int B, int T, int V, const int* tail_len,
+                                 int* tokens, int* n_accept, int* new_len, cudaStream_t s);
 
 // Tensor-map encoding through the driver entry point (no -lcuda link).
 bool encode_tmap_4d(CUtensorMap* tm, const void* base, const uint64_t dims[4],

@@ -32,7 +32,8 @@ EXPORTS = ("rx_cache_create", "rx_cache_destroy", "rx_pin_prefix", "rx_push_fram
            "rx_attend_regions_static", "rx_attend_suffix_block_causal", "rx_tail_append",
            "rx_snapshot_bytes", "rx_snapshot", "rx_restore", "rx_push_frame_async",
            "rx_set_attn_dparts", "rx_debug_inject_timeout", "rx_debug_choose_partition",
-           "rx_attend_suffix_norms", "rx_attend_batch_norms")
+           "rx_attend_suffix_norms", "rx_attend_batch_norms", "rx_tail_append_quant",
+           "rx_attend_streams_quant", "rx_verify_drafts")
 
 
 class RxConfig(ctypes.Structure):
@@ -45,6 +46,12 @@ class RxStreamBatch(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("k_tail", ctypes.c_void_p), ("v_tail", ctypes.c_void_p),
                 ("tail_len", ctypes.c_void_p), ("out", ctypes.c_void_p), ("B", ctypes.c_int),
                 ("T", ctypes.c_int)]
+
+
+class RxQuantStreams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("q", "k_tail", "v_tail", "k_exp", "v_exp", "tail_len", "n_new", "out")] + \
+               [("B", ctypes.c_int), ("T", ctypes.c_int)]
 
 
 class RxNormRows(ctypes.Structure):
@@ -88,6 +95,9 @@ _sigs = {
     "rx_attend_suffix_norms": (_i, [_vp, _i, _vp, _vp, _vp, _i, _vp, ctypes.POINTER(RxNormRows), _i, _vp]),
     "rx_attend_batch_norms": (_i, [_vp, _i, _vp, _vp, _vp, _i, _vp, ctypes.POINTER(RxStreamBatch),
                                    ctypes.POINTER(RxNormRows), _i, _vp]),
+    "rx_tail_append_quant": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp]),
+    "rx_attend_streams_quant": (_i, [_vp, _i, ctypes.POINTER(RxQuantStreams), _vp]),
+    "rx_verify_drafts": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]),
 }
 for _name, (_res, _args) in _sigs.items():
     _fn = getattr(_lib, _name)
@@ -131,6 +141,15 @@ def _shape(t: Optional[torch.Tensor], shape, name: str) -> None:
     caller's buffer)."""
     if t is not None and tuple(t.shape) != tuple(shape):
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _one_device(*tensors: Optional[torch.Tensor]) -> None:
+    """Refuse tensors that are not all on the current device, where the
+    library launches."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != cur:
+            raise ValueError("every tensor must be on the current device (cuda:%d), got %s" % (cur, t.device))
 
 
 def _norm_jobs(norms) -> Tuple[Optional[ctypes.Array], int]:
@@ -324,6 +343,42 @@ class Cache:
                                         _stream(stream)), "rx_attend_batch")
         return (out_act if action is not None else None), (out_lang if lang is not None else None)
 
+    def attend_streams_quant(self, layer: int, q: torch.Tensor, k_tail: torch.Tensor, v_tail: torch.Tensor,
+                             k_exp: torch.Tensor, v_exp: torch.Tensor, tail_len: torch.Tensor,
+                             n_new: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                             stream=None) -> torch.Tensor:
+        """Language streams over the shared store and their own 8-bit tails.
+
+        q: bf16 [B][T][Hq][D], the newest n_new[b] <= T tokens of each tail
+        (n_new None: T); tails: float8_e4m3fn [B][tail_cap][Hkv][D] with
+        uint8 exponents [B][tail_cap][Hkv] (tail_append_quant); tail_len:
+        int32 [B], the query tokens' own keys among them.  Query token t sees
+        the cached regions and its stream's keys up to its own.  Rows
+        t >= n_new[b] of out are left as they were.
+        """
+        c = self.cfg
+        if q.dim() != 4:
+            raise ValueError("q must have shape [B][T][Hq][D]")
+        B, T = q.shape[:2]
+        _shape(q, (B, T, c.Hq, c.D), "q")
+        _shape(k_tail, (B, c.tail_cap, c.Hkv, c.D), "k_tail")
+        _shape(v_tail, k_tail.shape, "v_tail")
+        _shape(k_exp, k_tail.shape[:3], "k_exp")
+        _shape(v_exp, k_tail.shape[:3], "v_exp")
+        _shape(tail_len, (B,), "tail_len")
+        _shape(n_new, (B,), "n_new")
+        _shape(out, q.shape, "out")
+        if out is None:
+            out = torch.empty_like(q)
+        batch = RxQuantStreams(_ptr(q, name="q"), _ptr(k_tail, torch.float8_e4m3fn, "k_tail"),
+                               _ptr(v_tail, torch.float8_e4m3fn, "v_tail"), _ptr(k_exp, torch.uint8, "k_exp"),
+                               _ptr(v_exp, torch.uint8, "v_exp"), _ptr(tail_len, torch.int32, "tail_len"),
+                               _ptr(n_new, torch.int32, "n_new"), _ptr(out, name="out"), B, T)
+        _one_device(q, k_tail, v_tail, k_exp, v_exp, tail_len, n_new, out)
+        _check(_lib.rx_attend_streams_quant(self._h, layer, ctypes.byref(batch), _stream(stream)),
+               "rx_attend_streams_quant")
+        return out
+
     def get_state(self, stream=None) -> Tuple[int, int, int]:
         h, v, p = _i(0), _i(0), ctypes.c_longlong(0)
         _check(_lib.rx_get_state(self._h, ctypes.byref(h), ctypes.byref(v), ctypes.byref(p),
@@ -453,3 +508,77 @@ def tail_append(k_tail: torch.Tensor, v_tail: torch.Tensor, tail_len: torch.Tens
                                _ptr(v_new, name="v_new"), _ptr(active, torch.int32, "active"), B,
                                tail_cap, Hkv, D, _ptr(overflow, torch.int32, "overflow"),
                                _stream(stream)), "rx_tail_append")
+
+
+def tail_append_quant(k_tail: torch.Tensor, v_tail: torch.Tensor, k_exp: torch.Tensor, v_exp: torch.Tensor,
+                      tail_len: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                      n_new: Optional[torch.Tensor] = None, new_len: Optional[torch.Tensor] = None,
+                      overflow: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Append up to T tokens per stream to 8-bit tails: codes float8_e4m3fn
+    [B][tail_cap][Hkv][D], exponents uint8 [B][tail_cap][Hkv] (a code stands
+    for code * 2^(exponent - 127)), new tokens bf16 [B][T][Hkv][D], of which
+    stream b appends n_new[b] (None: T) at tail_len[b].  tail_len stays as it
+    is; new_len, if given, receives the lengths after the append."""
+    if k_tail.dim() != 4 or k_new.dim() != 4:
+        raise ValueError("tails must have shape [B][tail_cap][Hkv][D] and new tokens [B][T][Hkv][D]")
+    B, tail_cap, Hkv, D = k_tail.shape
+    T = k_new.shape[1]
+    _shape(v_tail, k_tail.shape, "v_tail")
+    _shape(k_exp, k_tail.shape[:3], "k_exp")
+    _shape(v_exp, k_tail.shape[:3], "v_exp")
+    _shape(tail_len, (B,), "tail_len")
+    _shape(k_new, (B, T, Hkv, D), "k_new")
+    _shape(v_new, (B, T, Hkv, D), "v_new")
+    _shape(n_new, (B,), "n_new")
+    _shape(new_len, (B,), "new_len")
+    if overflow is not None and overflow.numel() < 1:
+        raise ValueError("overflow must hold one int32")
+    args = (_ptr(k_tail, torch.float8_e4m3fn, "k_tail"), _ptr(v_tail, torch.float8_e4m3fn, "v_tail"),
+            _ptr(k_exp, torch.uint8, "k_exp"), _ptr(v_exp, torch.uint8, "v_exp"),
+            _ptr(tail_len, torch.int32, "tail_len"), _ptr(new_len, torch.int32, "new_len"),
+            _ptr(k_new, name="k_new"), _ptr(v_new, name="v_new"), _ptr(n_new, torch.int32, "n_new"), B, T,
+            tail_cap, Hkv, D, _ptr(overflow, torch.int32, "overflow"))
+    _one_device(k_tail, v_tail, k_exp, v_exp, tail_len, new_len, k_new, v_new, n_new, overflow)
+    _check(_lib.rx_tail_append_quant(*args, _stream(stream)), "rx_tail_append_quant")
+
+
+_PROB_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def verify_drafts(p: torch.Tensor, q: Optional[torch.Tensor], draft: torch.Tensor, u: torch.Tensor, r: torch.Tensor,
+                  n_draft: Optional[torch.Tensor] = None, tail_len: Optional[torch.Tensor] = None,
+                  new_len: Optional[torch.Tensor] = None, stream=None):
+    """Accept or refuse drafted tokens and draw the token that follows them
+    (rx_verify_drafts).  p [B][T+1][V] target and q [B][T][V] draft
+    probabilities (fp32 or bf16; q None: drafts without probabilities), draft
+    int32 [B][T], u fp32 [B][T] and r fp32 [B] uniform in [0, 1), n_draft int32
+    [B] (None: T; negative: an idle slot).
+
+    Returns (tokens int32 [B][T+1], n_accept int32 [B], new_len int32 [B]);
+    new_len = tail_len + 1 + n_accept, and None without tail_len."""
+    if p.dim() != 3 or draft.dim() != 2:
+        raise ValueError("p must have shape [B][T+1][V] and draft [B][T]")
+    if p.dtype not in _PROB_TYPES:
+        raise TypeError("p must be float32 or bfloat16, got %s" % p.dtype)
+    B, T = draft.shape
+    V = p.shape[2]
+    _shape(p, (B, T + 1, V), "p")
+    _shape(q, (B, T, V), "q")
+    _shape(u, (B, T), "u")
+    _shape(r, (B,), "r")
+    _shape(n_draft, (B,), "n_draft")
+    _shape(tail_len, (B,), "tail_len")
+    _shape(new_len, (B,), "new_len")
+    if new_len is not None and tail_len is None:
+        raise ValueError("new_len needs tail_len")
+    tokens = torch.empty((B, T + 1), dtype=torch.int32, device=p.device)
+    n_accept = torch.empty((B,), dtype=torch.int32, device=p.device)
+    if tail_len is not None and new_len is None:
+        new_len = torch.empty_like(tail_len)
+    args = (_ptr(p, p.dtype, "p"), _ptr(q, p.dtype, "q"), _PROB_TYPES[p.dtype], _ptr(draft, torch.int32, "draft"),
+            _ptr(u, torch.float32, "u"), _ptr(r, torch.float32, "r"), _ptr(n_draft, torch.int32, "n_draft"), B, T, V,
+            _ptr(tail_len, torch.int32, "tail_len"), _ptr(tokens, torch.int32, "tokens"),
+            _ptr(n_accept, torch.int32, "n_accept"), _ptr(new_len, torch.int32, "new_len"))
+    _one_device(p, q, draft, u, r, n_draft, tail_len, tokens, n_accept, new_len)
+    _check(_lib.rx_verify_drafts(*args, _stream(stream)), "rx_verify_drafts")
+    return tokens, n_accept, new_len

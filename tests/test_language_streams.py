@@ -1,0 +1,172 @@
+"""Language streams over 8-bit tails, without a GPU: the oracle's own pins and
+the refusals of the library and of the binding."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from oracle import streams as OS
+from tests._util import LIB, ensure_built
+
+
+@pytest.fixture(scope="module")
+def lib():
+    try:
+        ensure_built()
+    except RuntimeError as e:  # pragma: no cover
+        pytest.skip("cannot build librx.so here: %s" % e)
+    return ctypes.CDLL(LIB)
+
+
+# ------------------------------------------------------------------- oracle
+def test_e4m3_codes_match_torch():
+    import torch
+    every = torch.arange(256, dtype=torch.uint8)
+    np.testing.assert_array_equal(OS.e4m3_decode(every.numpy()), every.view(torch.float8_e4m3fn).double().numpy())
+    x = np.concatenate([np.linspace(-448, 448, 9001), 2.0 ** np.arange(-12, 8), 0.0625 + 2.0 ** -7 * np.arange(20)])
+    x = x.astype(np.float32)
+    np.testing.assert_array_equal(OS.e4m3_encode(x.astype(np.float64)),
+                                  torch.from_numpy(x).to(torch.float8_e4m3fn).view(torch.uint8).numpy())
+
+
+def test_quantised_vectors_use_the_top_of_the_range():
+    g = np.random.default_rng(0)
+    x = g.standard_normal((50, 64)) * 2.0 ** g.integers(-40, 40, (50, 1))
+    codes, byte = OS.quantise(x)
+    back = OS.dequantise(codes, byte)
+    top = np.abs(OS.e4m3_decode(codes)).max(-1)
+    assert np.all((top >= 224) & (top <= 448))
+    step = 2.0 ** -10 * 2.0 ** (byte.astype(np.float64) - 127)
+    assert np.all(np.abs(back - x) <= np.maximum(2.0 ** -4 * np.abs(x), step[:, None]))
+
+
+def test_verify_keeps_the_targets_distribution():
+    """Over all (u, r) the first token is distributed as p: the total over a
+    fine grid, for a draft from each possible token weighted by q."""
+    p = np.array([[0.5, 0.2, 0.3], [1, 0, 0]])
+    q = np.array([[0.2, 0.6, 0.2]])
+    grid = (np.arange(60) + 0.5) / 60
+    got = np.zeros(3)
+    for x in range(3):
+        for u in grid:
+            for r in grid:
+                tokens, _ = OS.verify(p, q, [x], [u], r, 1)
+                got[tokens[0]] += q[0, x] / len(grid) ** 2
+    np.testing.assert_allclose(got, p[0], atol=0.02)   # the grid's cells are 1/60 wide
+
+
+# ----------------------------------------------------------------- refusals
+def _buf(n=1 << 14):
+    b = ctypes.create_string_buffer(n + 64)
+    return b, ctypes.addressof(b) + (-ctypes.addressof(b)) % 64
+
+
+def test_append_refuses_bad_arguments(lib):
+    from partitioned_kv_cache_gb300 import rx
+    keep, p = _buf()
+    f = rx._lib.rx_tail_append_quant
+    good = dict(kt=p, vt=p + 256, ke=p + 512, ve=p + 528, tl=p + 544, nl=p + 560, kn=p + 1024, vn=p + 2048, nn=None,
+                B=1, T=1, cap=4, Hkv=1, D=64, ov=None)
+
+    def call(**kw):
+        a = dict(good, **kw)
+        return f(a["kt"], a["vt"], a["ke"], a["ve"], a["tl"], a["nl"], a["kn"], a["vn"], a["nn"], a["B"], a["T"], a["cap"],
+                 a["Hkv"], a["D"], a["ov"], None)
+    assert call(B=-1) == -1
+    assert call(T=0) == -1
+    assert call(cap=0) == -1
+    assert call(Hkv=0) == -1
+    assert call(T=(1 << 28) + 1) == -1
+    assert call(B=1 << 20, T=1 << 13) == -1
+    assert call(D=96) == -6
+    assert call(B=0) == 0
+    for name in ("kt", "vt", "ke", "ve", "tl", "kn", "vn"):
+        assert call(**{name: None}) == -1, name
+    for name in ("kt", "vt", "kn", "vn"):
+        assert call(**{name: good[name] + 8}) == -1, name
+    for name in ("tl", "nl"):
+        assert call(**{name: good[name] + 2}) == -1, name
+    assert call(nl=good["tl"]) == -1
+    assert call(nn=p + 576, nl=p + 576) == -1
+    del keep
+
+
+def test_attention_refuses_a_null_handle(lib):
+    from partitioned_kv_cache_gb300 import rx
+    assert rx._lib.rx_attend_streams_quant(None, 0, ctypes.byref(rx.RxQuantStreams()), None) == -1
+    assert rx._lib.rx_attend_streams_quant(None, 0, None, None) == -1
+
+
+def test_verify_refuses_bad_arguments(lib):
+    from partitioned_kv_cache_gb300 import rx
+    keep, p = _buf()
+    f = rx._lib.rx_verify_drafts
+    good = dict(p=p, q=p + 512, t=0, d=p + 1024, u=p + 1056, r=p + 1088, n=None, B=2, T=2, V=8, tl=p + 1120,
+                tok=p + 1152, na=p + 1184, nl=p + 1216)
+
+    def call(**kw):
+        a = dict(good, **kw)
+        return f(a["p"], a["q"], a["t"], a["d"], a["u"], a["r"], a["n"], a["B"], a["T"], a["V"], a["tl"], a["tok"], a["na"],
+                 a["nl"], None)
+    assert call(B=-1) == -1
+    assert call(T=-1) == -1
+    assert call(V=0) == -1
+    assert call(V=(1 << 28) + 1) == -1
+    assert call(t=2) == -1
+    assert call(B=0) == 0
+    for name in ("p", "r", "tok", "na", "d", "u"):
+        assert call(**{name: None}) == -1, name
+    assert call(tl=None) == -1                     # new_len without tail_len
+    assert call(p=p + 2) == -1
+    assert call(d=good["d"] + 2) == -1
+    assert call(tok=good["d"]) == -1               # outputs over inputs or each other
+    assert call(na=good["r"]) == -1
+    assert call(na=good["tok"]) == -1
+    assert call(nl=good["tl"] + 4) == -1           # neither the same array nor apart
+    assert call(tok=good["tl"]) == -1
+    del keep
+
+
+def test_binding_refuses_shapes_and_types(lib):
+    import torch
+    from partitioned_kv_cache_gb300 import rx
+    z = torch.zeros
+    e4, u8, i32, bf = torch.float8_e4m3fn, torch.uint8, torch.int32, torch.bfloat16
+    kt, ke = z(2, 5, 1, 64, dtype=u8).view(e4), z(2, 5, 1, dtype=u8)
+    tl, x = z(2, dtype=i32), z(2, 3, 1, 64, dtype=bf)
+    f = rx.tail_append_quant
+    with pytest.raises(ValueError, match="v_tail"):
+        f(kt, kt[:1], ke, ke, tl, x, x)
+    with pytest.raises(ValueError, match="k_exp"):
+        f(kt, kt, ke[:, :4], ke, tl, x, x)
+    with pytest.raises(ValueError, match="v_new"):
+        f(kt, kt, ke, ke, tl, x, x[:, :2])
+    with pytest.raises(ValueError, match="n_new"):
+        f(kt, kt, ke, ke, tl, x, x, n_new=tl[:1])
+    with pytest.raises(TypeError, match="k_tail"):
+        f(kt.view(u8), kt, ke, ke, tl, x, x)
+    with pytest.raises(ValueError, match="CUDA"):
+        f(kt, kt, ke, ke, tl, x, x)
+    c = rx.Cache.__new__(rx.Cache)
+    c.cfg = rx.RxConfig(1, 8, 1, 64, 16, 4, 32, 51, 5, 6, 0)
+    c._h = None
+    q = z(2, 3, 8, 64, dtype=bf)
+    with pytest.raises(ValueError, match="k_tail"):
+        c.attend_streams_quant(0, q, kt[:, :4], kt, ke, ke, tl)
+    with pytest.raises(ValueError, match="q"):
+        c.attend_streams_quant(0, q[:, :, :4], kt, kt, ke, ke, tl)
+    with pytest.raises(ValueError, match="out"):
+        c.attend_streams_quant(0, q, kt, kt, ke, ke, tl, out=q[:1])
+    with pytest.raises(ValueError, match="contiguous"):
+        c.attend_streams_quant(0, q.transpose(0, 1).contiguous().transpose(0, 1), kt, kt, ke, ke, tl)
+    p, d, u, r = z(2, 4, 9), z(2, 3, dtype=i32), z(2, 3), z(2)
+    with pytest.raises(ValueError, match="p must"):
+        rx.verify_drafts(p[:, :3], None, d, u, r)
+    with pytest.raises(ValueError, match="q must"):
+        rx.verify_drafts(p, p, d, u, r)
+    with pytest.raises(TypeError, match="float32 or bfloat16"):
+        rx.verify_drafts(p.half(), None, d, u, r)
+    with pytest.raises(ValueError, match="tail_len"):
+        rx.verify_drafts(p, None, d, u, r, new_len=z(2, dtype=i32))
+    with pytest.raises(ValueError, match="CUDA"):
+        rx.verify_drafts(p, None, d, u, r)

@@ -1,0 +1,560 @@
+"""Language streams over 8-bit tails: append, attention, verification of
+drafts, against the fp64 oracle, and the three run together.
+
+Tolerances of the attention.  A weight alpha_j enters its product with V as at
+most one rounding to bf16 (2^-8 relative), the output is rounded once to bf16
+(2^-8 of its value), and the fp32 steps (scores, exponentials, sums, merges)
+move a weight by less than 2^-12 of itself at these sizes: a score is a sum of
+D <= 256 products with |s| below 40, off by at most 40 * 256 * 2^-24 in the
+worst case.  So |got - ref| <= (2^-8 + 2^-11) * spread + 2^-8 * |ref| with
+spread = sum_j alpha_j |v_j|, plus 1e-30 for zeros.
+"""
+import numpy as np
+import pytest
+
+from oracle import streams as OS
+from partitioned_kv_cache_gb300 import workload as W
+from tests._util import dev, ensure_built, host64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def rx():
+    ensure_built()
+    from partitioned_kv_cache_gb300 import rx as m
+    return m
+
+
+def _int(a):
+    import torch
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")
+
+
+def _bits(g, shape, scale=1.0):
+    return W.to_bf16_bits(scale * g.standard_normal(shape, dtype=np.float32))
+
+
+def _codes(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda().view(torch.float8_e4m3fn)
+
+
+def _u8(t):
+    import torch
+    return t.view(torch.uint8).cpu().numpy()
+
+
+def _tails(g, B, cap, Hkv, D):
+    """Quantised random tails: codes, exponent bytes and the values they stand for."""
+    f = W.bf16_bits_to_f64
+    out = []
+    for _ in range(2):
+        codes, byte = OS.quantise(f(_bits(g, (B, cap, Hkv, D))))
+        out += [codes, byte]
+    return out   # kc, ke, vc, ve
+
+
+# ------------------------------------------------------------------ append
+def _append_case(rx, xk, xv, cap, lens, new=None, T_none=False):
+    """Append bf16 bits xk, xv [B][T][Hkv][D] and compare every byte of the
+    tails, places that nothing was written to among them."""
+    import torch
+    B, T, Hkv, D = xk.shape
+    kt = torch.full((B, cap, Hkv, D), 0x5A, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    vt = torch.full((B, cap, Hkv, D), 0x33, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    ke = torch.full((B, cap, Hkv), 7, dtype=torch.uint8, device="cuda")
+    ve = torch.full((B, cap, Hkv), 9, dtype=torch.uint8, device="cuda")
+    nl, ov = _int([-5] * B), _int([0])
+    tl = _int(lens)
+    rx.tail_append_quant(kt, vt, ke, ve, tl, dev(xk), dev(xv), n_new=None if new is None else _int(new), new_len=nl,
+                         overflow=ov)
+    torch.cuda.synchronize()
+    n = [T] * B if new is None else [min(max(x, 0), T) for x in new]
+    over = 0
+    for got_c, got_e, x, fill, fe in ((kt, ke, xk, 0x5A, 7), (vt, ve, xv, 0x33, 9)):
+        want_c, want_e = np.full((B, cap, Hkv, D), fill, np.uint8), np.full((B, cap, Hkv), fe, np.uint8)
+        codes, byte = OS.quantise(W.bf16_bits_to_f64(x))
+        for b in range(B):
+            if not 0 <= lens[b] <= cap:
+                over |= n[b] > 0
+                continue
+            m = min(n[b], cap - lens[b])
+            over |= m < n[b]
+            want_c[b, lens[b]:lens[b] + m] = codes[b, :m]
+            want_e[b, lens[b]:lens[b] + m] = byte[b, :m]
+        np.testing.assert_array_equal(got_e.cpu().numpy(), want_e)
+        np.testing.assert_array_equal(_u8(got_c), want_c)
+    want_len = [min(ln + k, cap) if 0 <= ln <= cap else ln for ln, k in zip(lens, n)]
+    assert nl.tolist() == want_len
+    assert tl.tolist() == list(lens)
+    assert ov.item() == int(over)
+
+
+@pytest.mark.parametrize("B,T,Hkv,D,cap,lens,new", [
+    (1, 1, 1, 64, 1, [0], None),
+    (3, 1, 1, 256, 32, [0, 31, 32], None),                 # the last one is full
+    (5, 4, 2, 128, 9, [0, 3, 6, 9, 7], [4, 0, 4, 1, 2]),   # one overflows in part
+    (4, 7, 3, 64, 40, [-1, 41, 5, 0], [7, 7, 99, -3]),     # lengths and counts out of range
+    (2, 33, 8, 256, 50, [1, 17], [33, 32]),
+    (9, 5, 1, 128, 21, [0, 1, 2, 3, 4, 5, 6, 7, 8], [5, 4, 3, 2, 1, 0, 1, 2, 3]),
+])
+def test_append_stores_codes_and_exponents(rx, B, T, Hkv, D, cap, lens, new):
+    g = np.random.default_rng(B * 100 + T)
+    _append_case(rx, _bits(g, (B, T, Hkv, D)), _bits(g, (B, T, Hkv, D), 30.0), cap, lens, new)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_append_over_the_whole_range_of_bf16(rx, D):
+    """Vectors of every magnitude, ties, zeros of both signs, subnormals, the
+    largest value, infinities and NaN."""
+    g = np.random.default_rng(D)
+    x = _bits(g, (2, 254, 1, D))
+    e = np.arange(254, dtype=np.uint32)[None, :, None, None]          # exponent field of each vector's largest
+    drop = g.integers(0, 20, x.shape).astype(np.uint32)
+    x = ((x & 0x807F) | (np.maximum(e.astype(np.int64) - drop, 0) << 7).astype(np.uint32)).astype(np.uint16)
+    x[0, :, 0, 3] = (np.arange(254) << 7) | g.integers(90, 102, 254)   # tops around 1.75 * 2^k
+    x[1, 0] = 0
+    x[1, 1] = 0x8000
+    x[1, 2, 0, 5] = 0x7F80      # inf
+    x[1, 3, 0, D - 1] = 0xFF80  # -inf
+    x[1, 4, 0, 0] = 0x7FC0      # NaN
+    x[1, 5, 0, 1] = 0x7F7F      # the largest bf16
+    x[1, 6] = 1                 # the smallest subnormal
+    _append_case(rx, x, x[::-1].copy(), 260, [0, 3])
+
+
+def test_append_follows_lengths_on_the_device_in_a_graph(rx):
+    import torch
+    g = np.random.default_rng(3)
+    B, T, Hkv, D, cap = 2, 2, 1, 64, 9
+    xk, xv = _bits(g, (B, T, Hkv, D)), _bits(g, (B, T, Hkv, D))
+    kt = torch.zeros((B, cap, Hkv, D), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    vt, ke = kt.clone(), torch.zeros((B, cap, Hkv), dtype=torch.uint8, device="cuda")
+    ve, tl, nl = ke.clone(), _int([0, 3]), _int([0, 0])
+    dk, dv = dev(xk), dev(xv)
+    rx.tail_append_quant(kt, vt, ke, ve, tl, dk, dv, new_len=nl)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rx.tail_append_quant(kt, vt, ke, ve, tl, dk, dv, new_len=nl)
+        tl.copy_(nl)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert tl.tolist() == [4, 7]
+    codes, byte = OS.quantise(W.bf16_bits_to_f64(xk))
+    got = _u8(kt)
+    np.testing.assert_array_equal(got[0, 0:4], np.concatenate([codes[0], codes[0]]))
+    np.testing.assert_array_equal(got[1, 3:7], np.concatenate([codes[1], codes[1]]))
+    np.testing.assert_array_equal(ke.cpu().numpy()[1, 3:7], np.concatenate([byte[1], byte[1]]))
+
+
+# --------------------------------------------------------------- attention
+class Store:
+    """A one-layer store and its keys in oracle form."""
+
+    def __init__(self, rx, g, Hq, Hkv, D, P, N, F, cap, req, pushes, spare=0, layers=1):
+        f = W.bf16_bits_to_f64
+        self.Hq, self.Hkv, self.D, self.cap = Hq, Hkv, D, cap
+        self.cache = rx.Cache(layers, Hq, Hkv, D, P, N, F, 4, cap, req, spare)
+        pk, pv = _bits(g, (layers, P, Hkv, D)), _bits(g, (layers, P, Hkv, D))
+        self.cache.pin_prefix(dev(pk), dev(pv))
+        fk, fv = [], []
+        for _ in range(pushes):
+            k, v = _bits(g, (layers, F, Hkv, D)), _bits(g, (layers, F, Hkv, D))
+            self.cache.push_frame(dev(k), dev(v))
+            fk.append(k)
+            fv.append(v)
+        self.k = [f(np.concatenate([pk[i]] + [x[i] for x in fk[-N:]])) for i in range(layers)]
+        self.v = [f(np.concatenate([pv[i]] + [x[i] for x in fv[-N:]])) for i in range(layers)]
+
+
+def _check(got, ref, spread):
+    bound = (2.0 ** -8 + 2.0 ** -11) * spread + 2.0 ** -8 * np.abs(ref) + 1e-30
+    off = np.abs(got - ref)
+    assert np.all(np.isfinite(got))
+    assert np.all(off <= bound), "worst %.3f of the bound" % np.max(off / bound)
+
+
+def _attend(rx, st, g, lens, new, T, layer=0, tails=None, garbage=True):
+    """Run a batch and check every row; rows past n_new keep their bits."""
+    import torch
+    B = len(lens)
+    kc, ke, vc, ve = tails if tails is not None else _tails(g, B, st.cap, st.Hkv, st.D)
+    q = _bits(g, (B, T, st.Hq, st.D))
+    kd, vd, ked, ved = kc.copy(), vc.copy(), ke.copy(), ve.copy()
+    if garbage:   # whatever lies behind a tail's end: NaN codes and any exponent
+        for b in range(B):
+            kd[b, lens[b]:], vd[b, lens[b]:] = 0x7F, 0xFF
+            ked[b, lens[b]:] = g.integers(0, 256, ked[b, lens[b]:].shape)
+            ved[b, lens[b]:] = g.integers(0, 256, ved[b, lens[b]:].shape)
+    out = torch.full((B, T, st.Hq, st.D), -3.0, dtype=torch.bfloat16, device="cuda")
+    args = (dev(q), _codes(kd), _codes(vd), torch.from_numpy(ked).cuda(), torch.from_numpy(ved).cuda(), _int(lens))
+    res = st.cache.attend_streams_quant(layer, *args, n_new=None if new is None else _int(new), out=out)
+    assert res is out
+    got = host64(out)
+    again = st.cache.attend_streams_quant(layer, *args, n_new=None if new is None else _int(new), out=out.clone())
+    assert torch.equal(again.view(torch.int16), out.view(torch.int16))   # the same bits every time
+    for b in range(B):
+        n = T if new is None else min(max(new[b], 0), T)
+        k, v = OS.dequantise(kc[b, :lens[b]], ke[b, :lens[b]]), OS.dequantise(vc[b, :lens[b]], ve[b, :lens[b]])
+        ref, spread = OS.stream_attention(W.bf16_bits_to_f64(q[b, :n]), st.k[layer], st.v[layer], k, v)
+        _check(got[b, :n], ref, spread)
+        assert np.all(got[b, n:] == -3.0)
+    assert st.cache.check_device_error() == 0
+    return args, out
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 1, 256), (8, 2, 128), (4, 4, 64), (2, 1, 64), (32, 1, 128), (128, 1, 64),
+                                      (1, 1, 256), (16, 8, 256)])
+@pytest.mark.parametrize("T,lens,new", [
+    (1, [0, 1, 130], None),
+    (3, [3, 64, 129, 300], [3, 1, 2, 0]),
+])
+def test_attention_head_layouts(rx, Hq, Hkv, D, T, lens, new):
+    g = np.random.default_rng(Hq * 1000 + D + T)
+    st = Store(rx, g, Hq, Hkv, D, 20, 2, 48, 301, len(lens) * T, pushes=3)
+    _attend(rx, st, g, lens, new, T)
+
+
+@pytest.mark.parametrize("lens", [[31, 32, 33], [63, 64, 65], [127, 128, 129], [255, 256, 257], [511, 512, 513],
+                                  [1023, 1025, 1500], [0, 0, 0], [1, 1500, 0]])
+@pytest.mark.parametrize("D", [64, 256])
+def test_attention_tail_lengths(rx, lens, D):
+    g = np.random.default_rng(lens[1] + D)
+    st = Store(rx, g, 8, 1, D, 64, 1, 64, 1500, 6, pushes=1)
+    _attend(rx, st, g, lens, [1, 2, 1] if lens[0] else None, 2)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(5, 8, 1, 256), (8, 8, 1, 128), (9, 8, 1, 256), (16, 8, 1, 64), (17, 16, 2, 128),
+                                        (40, 8, 1, 256), (130, 1, 1, 64)])
+def test_attention_drafts_and_prompts_are_causal(rx, T, Hq, Hkv, D):
+    """Several query tokens: each sees its own tail up to itself; T * G crosses
+    one and several tiles of query rows."""
+    g = np.random.default_rng(T)
+    st = Store(rx, g, Hq, Hkv, D, 30, 2, 64, 400, 3 * T, pushes=1)
+    _attend(rx, st, g, [T, 400, T + 61], [T, T, max(1, T - 3)], T)
+
+
+def test_attention_prompt_longer_than_its_tail(rx):
+    """More query tokens than keys: the first rows see no tail key."""
+    g = np.random.default_rng(7)
+    st = Store(rx, g, 8, 1, 64, 5, 1, 16, 40, 12, pushes=1)
+    _attend(rx, st, g, [2, 0], None, 6)
+
+
+@pytest.mark.parametrize("P,pushes,spare,F", [(0, 0, 0, 16), (0, 1, 0, 16), (7, 0, 0, 64), (40, 5, 1, 64),
+                                              (64, 4, 1, 128), (3, 3, 0, 100)])
+def test_attention_store_states(rx, P, pushes, spare, F):
+    """No prefix, no frame, a partly and a fully filled window, a spare slot."""
+    g = np.random.default_rng(P + pushes)
+    st = Store(rx, g, 8, 1, 128, P, 3, F, 70, 8, pushes=pushes, spare=spare)
+    _attend(rx, st, g, [0, 1, 70, 33], [1, 1, 2, 2], 2)
+
+
+def test_attention_second_layer(rx):
+    g = np.random.default_rng(17)
+    st = Store(rx, g, 8, 1, 256, 64, 8, 256, 32, 16, pushes=8, layers=3)
+    _attend(rx, st, g, [0, 2, 4, 6, 8, 10, 12, 14, 16, 18, 20, 22, 24, 26, 28, 30], None, 1, layer=2)
+
+
+def test_attention_many_streams_of_odd_lengths(rx):
+    g = np.random.default_rng(18)
+    st = Store(rx, g, 4, 2, 64, 10, 1, 32, 250, 200, pushes=1)
+    lens = [int(x) for x in g.integers(0, 251, 67)]
+    new = [int(min(max(1, x), y)) for x, y in zip(g.integers(0, 4, 67), np.maximum(lens, 1))]
+    _attend(rx, st, g, lens, new, 2)
+
+
+def test_attention_outliers_far_apart(rx):
+    """Scales that differ by many powers of two between neighbouring tokens."""
+    g = np.random.default_rng(19)
+    st = Store(rx, g, 8, 1, 256, 16, 1, 16, 300, 4, pushes=1)
+    f = W.bf16_bits_to_f64
+    kx = f(_bits(g, (2, 300, 1, 256)))
+    vx = f(_bits(g, (2, 300, 1, 256))) * 2.0 ** g.integers(-30, 30, (2, 300, 1, 1))
+    kx *= 2.0 ** g.integers(-6, 1, (2, 300, 1, 1))
+    kc, ke = OS.quantise(kx)
+    vc, ve = OS.quantise(vx)
+    _attend(rx, st, g, [300, 211], [2, 2], 2, tails=(kc, ke, vc, ve))
+
+
+def test_attention_score_range(rx):
+    """Scores that grow along the tail by hundreds: the running maximum moves
+    at every tile, and early keys vanish."""
+    g = np.random.default_rng(20)
+    st = Store(rx, g, 2, 1, 64, 4, 1, 16, 700, 4, pushes=1)
+    f = W.bf16_bits_to_f64
+    kc, ke = OS.quantise(f(_bits(g, (2, 700, 1, 64))) * np.linspace(0.01, 6, 700)[None, :, None, None])
+    vc, ve = OS.quantise(f(_bits(g, (2, 700, 1, 64))))
+    _attend(rx, st, g, [700, 650], None, 2, tails=(kc, ke, vc, ve))
+
+
+def test_nan_tokens_reach_only_the_rows_that_see_them(rx):
+    import torch
+    g = np.random.default_rng(21)
+    T, D = 3, 128
+    st = Store(rx, g, 8, 1, D, 16, 1, 16, 200, 3 * T, pushes=1)
+    kc, ke, vc, ve = _tails(g, 3, 200, 1, D)
+    lens = [150, 200, 90]
+    ve[0, 148], vc[0, 148] = 255, 0      # seen by query tokens 1 and 2 of stream 0
+    ke[1, 199], kc[1, 199] = 255, 0      # seen by query token 2 of stream 1
+    q = dev(_bits(g, (3, T, 8, D)))
+    out = st.cache.attend_streams_quant(0, q, _codes(kc), _codes(vc), torch.from_numpy(ke).cuda(),
+                                        torch.from_numpy(ve).cuda(), _int(lens))
+    nan = torch.isnan(out).cpu().numpy()
+    want = np.zeros((3, T, 8, D), bool)
+    want[0, 1:] = want[1, 2] = True
+    np.testing.assert_array_equal(nan, want)
+
+
+def test_attention_places_beyond_32_bits(rx):
+    """The third stream's tail starts past 2^31 bytes."""
+    import torch
+    g = np.random.default_rng(22)
+    cap, D, B = (1 << 22) + 5, 256, 3
+    st = Store(rx, g, 8, 1, D, 16, 1, 16, cap, 2 * B, pushes=1)
+    kt = torch.full((B, cap, 1, D), 0x7F, dtype=torch.uint8, device="cuda")
+    vt = torch.full((B, cap, 1, D), 0xFF, dtype=torch.uint8, device="cuda")
+    ke = torch.full((B, cap, 1), 255, dtype=torch.uint8, device="cuda")
+    ve = ke.clone()
+    kc, kb, vc, vb = _tails(g, B, 400, 1, D)
+    lens = [10, 399, 400]
+    for b in range(B):
+        for t, c in ((kt, kc), (vt, vc), (ke, kb), (ve, vb)):
+            t[b, :lens[b]] = torch.from_numpy(c[b, :lens[b]]).cuda()
+    q = _bits(g, (B, 2, 8, D))
+    out = st.cache.attend_streams_quant(0, dev(q), kt.view(torch.float8_e4m3fn), vt.view(torch.float8_e4m3fn), ke, ve,
+                                        _int(lens))
+    got = host64(out)
+    for b in range(B):
+        ref, spread = OS.stream_attention(W.bf16_bits_to_f64(q[b]), st.k[0], st.v[0],
+                                          OS.dequantise(kc[b, :lens[b]], kb[b, :lens[b]]),
+                                          OS.dequantise(vc[b, :lens[b]], vb[b, :lens[b]]))
+        _check(got[b], ref, spread)
+    # ... and the append writes there.
+    xk, xv = _bits(g, (B, 2, 1, D)), _bits(g, (B, 2, 1, D))
+    rx.tail_append_quant(kt.view(torch.float8_e4m3fn), vt.view(torch.float8_e4m3fn), ke, ve,
+                         _int([cap - 2, cap - 2, cap - 2]), dev(xk), dev(xv))
+    codes, byte = OS.quantise(W.bf16_bits_to_f64(xk))
+    np.testing.assert_array_equal(kt[2, cap - 2:].cpu().numpy(), codes[2])
+    np.testing.assert_array_equal(ke[2, cap - 2:].cpu().numpy(), byte[2])
+
+
+def test_attention_long_tail(rx):
+    """One stream with a tail of 20000 tokens beside short ones."""
+    g = np.random.default_rng(23)
+    st = Store(rx, g, 8, 1, 64, 64, 1, 64, 20000, 9, pushes=1)
+    kc, ke, vc, ve = _tails(g, 1, 20000, 1, 64)
+    tails = [np.concatenate([x, x[:, ::-1], x]) for x in (kc, ke, vc, ve)]
+    _attend(rx, st, g, [20000, 3, 777], [3, 3, 1], 3, tails=tails)
+
+
+def test_attention_graph_follows_growing_tails(rx):
+    import torch
+    g = np.random.default_rng(24)
+    B, D, cap = 3, 256, 300
+    st = Store(rx, g, 8, 1, D, 16, 2, 64, cap, B, pushes=2)
+    kc, ke, vc, ve = _tails(g, B, cap, 1, D)
+    q = _bits(g, (B, 1, 8, D))
+    out = torch.zeros((B, 1, 8, D), dtype=torch.bfloat16, device="cuda")
+    tl = _int([0, 0, 0])
+    args = (dev(q), _codes(kc), _codes(vc), torch.from_numpy(ke).cuda(), torch.from_numpy(ve).cuda(), tl)
+    st.cache.attend_streams_quant(0, *args, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        st.cache.attend_streams_quant(0, *args, out=out)
+    for lens in ([0, 1, 300], [299, 128, 7], [5, 0, 0]):
+        tl.copy_(_int(lens))
+        graph.replay()
+        got = host64(out)
+        for b in range(B):
+            ref, spread = OS.stream_attention(W.bf16_bits_to_f64(q[b]), st.k[0], st.v[0],
+                                              OS.dequantise(kc[b, :lens[b]], ke[b, :lens[b]]),
+                                              OS.dequantise(vc[b, :lens[b]], ve[b, :lens[b]]))
+            _check(got[b], ref, spread)
+
+
+def test_attention_on_another_stream(rx):
+    import torch
+    g = np.random.default_rng(25)
+    st = Store(rx, g, 8, 1, 64, 16, 1, 16, 40, 4, pushes=1)
+    kc, ke, vc, ve = _tails(g, 2, 40, 1, 64)
+    q = dev(_bits(g, (2, 1, 8, 64)))
+    args = (q, _codes(kc), _codes(vc), torch.from_numpy(ke).cuda(), torch.from_numpy(ve).cuda(), _int([40, 13]))
+    here = st.cache.attend_streams_quant(0, *args)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    there = torch.empty_like(here)
+    st.cache.attend_streams_quant(0, *args, out=there, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(here, there)
+
+
+def test_attention_agrees_with_the_16_bit_tails(rx):
+    """Tails whose values e4m3 holds exactly: the same answer as rx_attend_batch
+    on 16-bit tails, within both calls' roundings."""
+    import torch
+    g = np.random.default_rng(26)
+    B, D, cap = 16, 256, 32
+    st = Store(rx, g, 8, 1, D, 64, 8, 256, cap, B, pushes=9)
+    kc, ke, vc, ve = _tails(g, B, cap, 1, D)
+    lens = [int(x) for x in g.integers(0, 31, B)]
+    q = dev(_bits(g, (B, 1, 8, D)))
+    k16 = torch.from_numpy(OS.dequantise(kc, ke)).to(torch.bfloat16).cuda()
+    v16 = torch.from_numpy(OS.dequantise(vc, ve)).to(torch.bfloat16).cuda()
+    _, want = st.cache.attend_batch(0, None, (q, k16, v16, _int(lens)))
+    got = st.cache.attend_streams_quant(0, q, _codes(kc), _codes(vc), torch.from_numpy(ke).cuda(),
+                                        torch.from_numpy(ve).cuda(), _int(lens))
+    # attend_batch rounds weights, partials and output: 3 * 2^-8 of spread <= max|v| < 6 there, 2 here.
+    assert (got.float() - want.float()).abs().max().item() <= 5 * 2.0 ** -8 * 6
+
+
+# ------------------------------------------------------------ verification
+def _verify(rx, p, q, draft, u, r, n, dtype, lens=True):
+    import torch
+    B, T1, V = p.shape
+    T = T1 - 1
+    pt = torch.from_numpy(p).to(dtype).cuda()
+    qt = None if q is None else torch.from_numpy(q).to(dtype).cuda()
+    tl = _int(np.arange(B) * 3)
+    got = rx.verify_drafts(pt, qt, _int(np.reshape(draft, (B, T))), torch.from_numpy(u).cuda(), torch.from_numpy(r).cuda(),
+                           n_draft=None if n is None else _int(n), tail_len=tl if lens else None)
+    tokens, count = got[0].cpu().numpy(), got[1].cpu().numpy()
+    p64 = pt.double().cpu().numpy()
+    q64 = None if q is None else qt.double().cpu().numpy()
+    for b in range(B):
+        m = T if n is None else min(n[b], T)
+        if m < 0:
+            want, a = [], -1
+        else:
+            want, a = OS.verify(p64[b], None if q is None else q64[b], draft[b], u[b].astype(np.float64), float(r[b]), m)
+        assert count[b] == a, (b, count[b], a)
+        assert tokens[b].tolist() == want + [-1] * (T + 1 - len(want)), b
+    if lens:
+        assert got[2].tolist() == [3 * b + 1 + int(count[b]) for b in range(B)]
+    else:
+        assert got[2] is None
+
+
+def _softmax(x):
+    x = np.exp(x - x.max(-1, keepdims=True))
+    return (x / x.sum(-1, keepdims=True)).astype(np.float32)
+
+
+@pytest.mark.parametrize("B,T,V", [(1, 1, 1), (3, 2, 2), (5, 1, 31), (4, 3, 33), (7, 8, 1000), (6, 4, 1023), (2, 33, 257),
+                                   (16, 7, 50257), (3, 2, 151936), (9, 5, 4100), (64, 4, 515), (2, 3, 257153)])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("with_q", [True, False])
+def test_verify_accepts_and_draws(rx, B, T, V, dtype, with_q):
+    import torch
+    g = np.random.default_rng(B * 10000 + V)
+    z = g.standard_normal((B, T + 1, V)) * 2
+    p = _softmax(z)
+    q = _softmax(z[:, :T] + 0.5 * g.standard_normal((B, T, V))) if with_q else None
+    draft = np.argmax(z[:, :T] + g.gumbel(size=(B, T, V)), -1)
+    n = [int(x) for x in g.integers(-1, T + 2, B)]
+    _verify(rx, p, q, draft, g.random((B, T), dtype=np.float32), g.random(B, dtype=np.float32), n, getattr(torch, dtype))
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_verify_without_drafts_samples(rx, dtype):
+    import torch
+    g = np.random.default_rng(5)
+    p = _softmax(g.standard_normal((70, 1, 777)) * 3)
+    r = g.random(70, dtype=np.float32)
+    r[0], r[1] = 0.0, np.float32(1 - 2.0 ** -24)
+    _verify(rx, p, None, np.zeros((70, 0), np.int64), np.zeros((70, 0), np.float32), r, None, getattr(torch, dtype), lens=False)
+
+
+def test_verify_edges(rx):
+    """Equal distributions, drafts without probability, tokens out of range,
+    NaN and infinite entries, rows without any weight."""
+    import torch
+    g = np.random.default_rng(6)
+    B, T, V = 12, 3, 300
+    p = _softmax(g.standard_normal((B, T + 1, V)))
+    q = _softmax(g.standard_normal((B, T, V)))
+    draft = g.integers(0, V, (B, T))
+    u, r = g.random((B, T), dtype=np.float32), g.random(B, dtype=np.float32)
+    q[0] = p[0, :T]                                   # equal: accepted whatever u < 1 is
+    p[1, 0, draft[1, 0]] = 0                          # p = 0: refused
+    q[2, 0, draft[2, 0]] = 0                          # q = 0 < p: accepted
+    draft[3, 1], draft[4, 0], draft[5, 2] = -1, V, 1 << 30
+    u[6] = 0                                          # accepted wherever p > 0
+    p[7, 0], q[7, 0] = 0.5 * q[7, 0], q[7, 0]         # no positive difference: drawn from p
+    u[7, 0] = np.float32(0.99)
+    p[8, 0, 5], p[8, 0, 9] = np.nan, np.inf
+    p[9, 0] = 0                                       # nothing at all
+    p[10, 0, :] = 0
+    p[10, 0, V - 1] = 1                               # all weight on the last
+    r[11] = 0
+    _verify(rx, p, q, draft, u, r, None, torch.float32)
+    _verify(rx, p, None, draft, u, r, [T, T, 0, 1, 2, T, T, 0, 0, 0, 0, -7], torch.float32)
+
+
+def test_verify_lengths_in_place_and_graph(rx):
+    import torch
+    g = np.random.default_rng(8)
+    B, T, V = 4, 2, 100
+    p, q = _softmax(g.standard_normal((B, T + 1, V))), _softmax(g.standard_normal((B, T, V)))
+    args = (torch.from_numpy(p).cuda(), torch.from_numpy(q).cuda(), _int(g.integers(0, V, (B, T))),
+            torch.rand((B, T), device="cuda"), torch.rand((B,), device="cuda"))
+    tl = _int([0, 10, 20, 30])
+    _, n, _ = rx.verify_drafts(*args, tail_len=tl, new_len=tl)
+    n = n.tolist()
+    assert tl.tolist() == [10 * b + 1 + n[b] for b in range(B)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rx.verify_drafts(*args, tail_len=tl, new_len=tl)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert tl.tolist() == [10 * b + 4 * (1 + n[b]) for b in range(B)]
+
+
+# ------------------------------------------------------------- run together
+def test_streams_decode_with_drafts(rx):
+    """Four steps of append, attention on every layer and verification, with
+    the lengths kept on the device throughout, beside frames that arrive."""
+    import torch
+    g = np.random.default_rng(30)
+    L, B, T, Hq, Hkv, D, cap, V = 2, 3, 4, 8, 1, 128, 64, 500
+    st = Store(rx, g, Hq, Hkv, D, 32, 2, 64, cap, B * T, pushes=2, layers=L)
+    kt = [torch.full((B, cap, Hkv, D), 0x7F, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(L)]
+    vt = [x.clone() for x in kt]
+    ke = [torch.full((B, cap, Hkv), 255, dtype=torch.uint8, device="cuda") for _ in range(L)]
+    ve = [x.clone() for x in ke]
+    length, total = _int([0, 0, 0]), _int([0, 0, 0])
+    held = [[(np.zeros((0, Hkv, D)), np.zeros((0, Hkv, D))) for _ in range(B)] for _ in range(L)]
+    kept = [0] * B
+    for step in range(4):
+        n = [T, 1 + step % T, T - 1]               # the last token and up to T - 1 drafts
+        new = _int(n)
+        for i in range(L):
+            xk, xv, q = (_bits(g, (B, T, h, D)) for h in (Hkv, Hkv, Hq))
+            rx.tail_append_quant(kt[i], vt[i], ke[i], ve[i], length, dev(xk), dev(xv), n_new=new, new_len=total)
+            out = host64(st.cache.attend_streams_quant(i, dev(q), kt[i], vt[i], ke[i], ve[i], total, n_new=new))
+            for b in range(B):
+                k, v = (np.concatenate([held[i][b][j][:kept[b]], OS.dequantise(*OS.quantise(W.bf16_bits_to_f64(x[b, :n[b]])))])
+                        for j, x in enumerate((xk, xv)))
+                held[i][b] = (k, v)
+                ref, spread = OS.stream_attention(W.bf16_bits_to_f64(q[b, :n[b]]), st.k[i], st.v[i], k, v)
+                _check(out[b, :n[b]], ref, spread)
+        z = g.standard_normal((B, T, V))
+        p, qd = _softmax(z), _softmax(z[:, :T - 1] + 0.3 * g.standard_normal((B, T - 1, V)))
+        draft = np.argmax(z[:, :T - 1] + g.gumbel(size=(B, T - 1, V)), -1)
+        u, r = g.random((B, T - 1), dtype=np.float32), g.random(B, dtype=np.float32)
+        tokens, count, _ = rx.verify_drafts(torch.from_numpy(p).cuda(), torch.from_numpy(qd).cuda(), _int(draft),
+                                            torch.from_numpy(u).cuda(), torch.from_numpy(r).cuda(),
+                                            n_draft=_int([x - 1 for x in n]), tail_len=length, new_len=length)
+        for b in range(B):
+            want, a = OS.verify(p[b].astype(np.float64), qd[b].astype(np.float64), draft[b], u[b].astype(np.float64), float(r[b]), n[b] - 1)
+            assert count[b].item() == a and tokens[b, :a + 1].tolist() == want
+            kept[b] += 1 + a
+        assert length.tolist() == kept
+    assert max(kept) > 4
+    st.cache.close()
