@@ -76,6 +76,7 @@ constexpr int kRingDeepKB = 160;
 constexpr int kShallowTiles = 4;
 constexpr int kMergeWide = 32;               // build tags: see attn_kernel's CM
 constexpr int kNoClusterMerge = 0;
+constexpr int kPartials = -1;
 
 template <int D, int RING_KB>
 struct Layout {
@@ -240,6 +241,21 @@ __device__ __forceinline__ float2* xchg_ml(const AttnParams& p, int DV, int spli
          (u * p.n_splits + split) * kBM;
 }
 
+// fp32 partials (kPartials), per (tile, head) unit: O / l [splits][D/8 pieces]
+// [128 rows] of 32 bytes for every unit, then (m, l) [splits][128].
+template <int D>
+__device__ __forceinline__ float4* partial_o(const AttnParams& p, int split) {
+  const size_t u = static_cast<size_t>(blockIdx.z) * gridDim.x + blockIdx.x;
+  return reinterpret_cast<float4*>(p.xchg) + (u * p.n_splits + split) * (D / 4) * kBM;
+}
+template <int D>
+__device__ __forceinline__ float2* partial_ml(const AttnParams& p, int split) {
+  const size_t u = static_cast<size_t>(blockIdx.z) * gridDim.x + blockIdx.x;
+  return reinterpret_cast<float2*>(reinterpret_cast<float4*>(p.xchg) +
+                                   static_cast<size_t>(gridDim.x) * gridDim.z * p.n_splits * (D / 4) * kBM) +
+         (u * p.n_splits + split) * kBM;
+}
+
 // The cluster merge's last step: rows [r0, r0 + nr) of the tile from the C
 // partial slots of the cluster.  An item is PP adjacent 16-byte pieces of one
 // row; items go rows fastest (a warp's loads of one split are consecutive
@@ -342,7 +358,10 @@ __device__ __noinline__ void run_norm_rows(const AttnParams& p, int sw, int lane
 // loads in flight per thread), or kMergeWide: up to kMaxClusterSplits splits
 // whose rows hold more (row, piece) items than the CTA has threads, taken two
 // pieces per thread so that one pass finishes them; or kNoClusterMerge, for
-// launches whose splits are merged by attn_combine_kernel.
+// launches whose splits are merged by attn_combine_kernel; or kPartials, for
+// launches that end with every split's partial in the exchange area in fp32
+// (launch_attention_partials), for a merge with partials of other keys that
+// adds no rounding of its own.
 template <int D, int RING_KB, int CM = kMaxClusterSplits>
 __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ AttnParams p) {
   using Lay = Layout<D, RING_KB>;
@@ -727,7 +746,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     if (ok) ok = warp_wait(BAR(B_PV + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag);
     if (ok) {
       tc_fence_after();
-      if (p.n_splits == 1) {
+      if constexpr (CM == kPartials) {
+        const float inv = l > 0.f ? 1.f / l : l;   // l = 0: zeros; l = NaN: NaN
+        float4* dst = partial_o<D>(p, split) + row * 2;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(tO + c + lane_off, o);
+          if (row_valid) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[static_cast<size_t>(c / 8 + i / 2) * 2 * kBM + (i & 1)] =
+                  make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+          }
+        }
+        if (row_valid) partial_ml<D>(p, split)[row] = make_float2(m_used, l);
+      } else if (p.n_splits == 1) {
         const int tok = Rs / p.G;
         const int h = g * p.G + Rs % p.G;
         __nv_bfloat16* dst = sg.out + (static_cast<size_t>(tok) * p.Hq + h) * D + dcol;
@@ -772,6 +806,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         }
         if (row_valid) xchg_ml(p, DV, split)[row] = make_float2(m_used, l);
       }
+    } else if (CM == kPartials) {
+      // A split without keys, or one that gave up.
+      if (row_valid) {
+        float4* dst = partial_o<D>(p, split) + row * 2;
+        for (int c = 0; c < D / 4; ++c)
+          dst[static_cast<size_t>(c / 2) * 2 * kBM + (c & 1)] = make_float4(0.f, 0.f, 0.f, 0.f);
+        partial_ml<D>(p, split)[row] = make_float2(-INFINITY, 0.f);
+      }
     } else if (!p.fused && p.n_splits > 1 && row_valid) {
       // A split without keys (or one that gave up): zeros and l = 0, which
       // the combine skips.
@@ -781,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
   }
 
-  if constexpr (CM != kNoClusterMerge) if (p.fused) {
+  if constexpr (CM != kNoClusterMerge && CM != kPartials) if (p.fused) {
     // ---------------------------------------------------------- cluster merge
     // The C splits of this (tile, head, column share) exchange their partials
     // through L2: each softmax thread writes its row's normalised partial
@@ -1048,7 +1090,7 @@ cudaError_t launch_one(const AttnParams& prm, int m_tiles, int Hkv, cudaStream_t
     e = launch_k(attn_kernel<D, RING_KB, CM>, grid, dim3(kThreads), Lay::ALLOC, s, prm);
   }
   if (e == cudaSuccess) e = cudaGetLastError();
-  if (e != cudaSuccess || prm.n_splits == 1 || prm.fused) return e;
+  if (e != cudaSuccess || prm.n_splits == 1 || prm.fused || CM == kPartials) return e;
   dim3 cgrid(m_tiles * 8, D / prm.dparts / 64, Hkv * prm.dparts);
   e = launch_k(attn_combine_kernel<D>, cgrid, dim3(256), 0, s, static_cast<const uint4*>(prm.xchg),
                prm.seg[0].out, prm.seg[0].rows, prm.seg[0].m_tiles, prm.seg[1].out, prm.seg[1].rows,
@@ -1111,13 +1153,14 @@ const int* cluster_capacity() {
 
 }  // namespace
 
-cudaError_t launch_partitioned_attention(const AttnLaunch& a, const AttnSegment* segs, int nseg,
-                                         cudaStream_t s, int* used_splits) {
+// The kernel's parameters but for the partition.
+static cudaError_t fill_params(const AttnLaunch& a, const AttnSegment* segs, int nseg, AttnParams& prm, int& m_total,
+                               int& t_max) {
   if (nseg < 1 || nseg > 2) return cudaErrorInvalidValue;
   const int G = a.Hq / a.Hkv;
-  AttnParams prm;
   memset(&prm, 0, sizeof(prm));
-  int m_total = 0, t_max = 0;
+  m_total = 0;
+  t_max = 0;
   const int t_shared = (a.P + kBN - 1) / kBN + (a.N * a.F + kBN - 1) / kBN;
   for (int i = 0; i < nseg; ++i) {
     const AttnSegment& q = segs[i];
@@ -1192,6 +1235,15 @@ cudaError_t launch_partitioned_attention(const AttnLaunch& a, const AttnSegment*
   prm.G = G;
   prm.rows_pad = m_total * kBM;
   prm.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(a.D)));
+  return cudaSuccess;
+}
+
+cudaError_t launch_partitioned_attention(const AttnLaunch& a, const AttnSegment* segs, int nseg,
+                                         cudaStream_t s, int* used_splits) {
+  AttnParams prm;
+  int m_total = 0, t_max = 0;
+  const cudaError_t pe = fill_params(a, segs, nseg, prm, m_total, t_max);
+  if (pe != cudaSuccess) return pe;
   // Partition (partition.h): `splits` slices of the key sequence times
   // `dparts` shares of the output columns per (tile, head), from the
   // device's cluster capacity.
@@ -1227,6 +1279,38 @@ cudaError_t launch_partitioned_attention(const AttnLaunch& a, const AttnSegment*
     case 64: return launch_d<64>(prm, m_total, a.Hkv, s, deep, cm);
     case 128: return launch_d<128>(prm, m_total, a.Hkv, s, deep, cm);
     case 256: return launch_d<256>(prm, m_total, a.Hkv, s, deep, cm);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_attention_partials(const AttnLaunch& a, const void* q, int tokens, size_t xchg_bytes, cudaStream_t s,
+                                      int* splits, int* m_tiles) {
+  const AttnSegment seg{q, nullptr, nullptr, nullptr, tokens, 0, nullptr, 1, 0, 0};
+  AttnParams prm;
+  int m_total = 0, t_max = 0;
+  const cudaError_t e = fill_params(a, &seg, 1, prm, m_total, t_max);
+  if (e != cudaSuccess) return e;
+  // One wave of CTAs; at most 32 partials a row (the merge takes them one per
+  // lane) and as many as the exchange area holds; the fewest splits whose
+  // longest is as short.
+  const int units = m_total * a.Hkv;
+  const size_t per_split = static_cast<size_t>(units) * kBM * (4 * static_cast<size_t>(a.D) + 8);
+  long long sp = a.num_sms / units;
+  sp = sp > 32 ? 32 : sp;
+  sp = sp > t_max ? t_max : sp;
+  sp = sp > static_cast<long long>(xchg_bytes / per_split) ? static_cast<long long>(xchg_bytes / per_split) : sp;
+  sp = sp < 1 ? 1 : sp;
+  const int longest = static_cast<int>((t_max + sp - 1) / sp);
+  if (longest > 0) sp = (t_max + longest - 1) / longest;
+  prm.n_splits = static_cast<int>(sp < 1 ? 1 : sp);
+  prm.dparts = 1;
+  prm.prefetch_l2 = a.prefetch_l2;
+  *splits = prm.n_splits;
+  *m_tiles = m_total;
+  switch (a.D) {
+    case 64: return launch_one<64, kRingDeepKB, kPartials>(prm, m_total, a.Hkv, s);
+    case 128: return launch_one<128, kRingDeepKB, kPartials>(prm, m_total, a.Hkv, s);
+    case 256: return launch_one<256, kRingDeepKB, kPartials>(prm, m_total, a.Hkv, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -13,7 +13,6 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
-#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -91,8 +90,8 @@ static EncodeTiledFn encode_tiled() {
   return fn;
 }
 
-bool encode_tmap_4d(CUtensorMap* tm, const void* base, const uint64_t dims[4],
-                    const uint64_t strides_bytes[3], const uint32_t box[4]) {
+static bool encode_4d(CUtensorMap* tm, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* base,
+                      const uint64_t dims[4], const uint64_t strides_bytes[3], const uint32_t box[4]) {
   EncodeTiledFn f = encode_tiled();
   if (!f) return false;
   cuuint64_t gd[4], gs[3];
@@ -102,11 +101,20 @@ bool encode_tmap_4d(CUtensorMap* tm, const void* base, const uint64_t dims[4],
     bx[i] = box[i];
   }
   for (int i = 0; i < 3; ++i) gs[i] = strides_bytes[i];
-  const CUresult r =
-      f(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), gd, gs, bx, es,
-        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = f(tm, type, 4, const_cast<void*>(base), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+bool encode_tmap_4d(CUtensorMap* tm, const void* base, const uint64_t dims[4],
+                    const uint64_t strides_bytes[3], const uint32_t box[4]) {
+  return encode_4d(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, base, dims, strides_bytes, box);
+}
+
+bool encode_tmap_u8_4d(CUtensorMap* tm, const void* base, const uint64_t dims[4],
+                       const uint64_t strides_bytes[3], const uint32_t box[4]) {
+  return encode_4d(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                   box[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, base, dims, strides_bytes, box);
 }
 
 }  // namespace rx
@@ -123,6 +131,8 @@ struct rx_cache {
   __nv_bfloat16* v_win = nullptr;
   rx::DevState* dstate = nullptr;
   void* xchg = nullptr;
+  size_t xchg_bytes = 0;
+  void* stream_ws = nullptr;   // partials of the language streams' 8-bit tails
   int max_splits = 0;
   int T_pin = 0;         // tiles of the pinned region per (layer, head), >= 1
   int T_win = 0;         // tiles of the window per (layer, head)
@@ -216,7 +226,9 @@ rx_status rx_cache_create(const rx_config* cfg, rx_cache_t* out) {
   const size_t part_rows = static_cast<size_t>(c.Hkv) * h->max_splits * rows_pad;
   const size_t xchg_b = round_up(part_rows * (2 * static_cast<size_t>(c.D) + 8 * 4), 256);
   const size_t st_b = 256;
-  h->mem_bytes = 2 * pin_b + 2 * win_b + st_b + xchg_b;
+  const size_t stream_b = c.max_req > 0 && c.tail_cap > 0
+                              ? rx::streams_quant_workspace(c.max_req, c.Hkv, G, c.D, h->num_sms) : 0;
+  h->mem_bytes = 2 * pin_b + 2 * win_b + st_b + xchg_b + stream_b;
   int l2 = 0;
   if (cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, dev) != cudaSuccess) l2 = 0;
   cudaGetLastError();
@@ -239,7 +251,9 @@ rx_status rx_cache_create(const rx_config* cfg, rx_cache_t* out) {
   h->k_win = reinterpret_cast<__nv_bfloat16*>(p); p += win_b;
   h->v_win = reinterpret_cast<__nv_bfloat16*>(p); p += win_b;
   h->dstate = reinterpret_cast<rx::DevState*>(p); p += st_b;
-  h->xchg = p;
+  h->xchg = p; p += xchg_b;
+  h->xchg_bytes = xchg_b;
+  h->stream_ws = p;
   if (c.spare_slot) {
     e = cudaEventCreateWithFlags(&h->consumer_done, cudaEventDisableTiming);
     if (e == cudaSuccess) e = cudaEventCreateWithFlags(&h->push_done, cudaEventDisableTiming);
@@ -640,19 +654,7 @@ rx_status rx_attend_streams_quant(rx_cache_t h, int layer, const rx_quant_stream
   s.Hkv = c.Hkv;
   s.D = c.D;
   s.tail_cap = c.tail_cap;
-  s.pin_k = static_cast<const uint8_t*>(a.pin_k_tiles);
-  s.pin_v = static_cast<const uint8_t*>(a.pin_v_tiles);
-  s.win_k = static_cast<const uint8_t*>(a.win_k_tiles);
-  s.win_v = static_cast<const uint8_t*>(a.win_v_tiles);
-  s.pin_head_stride = a.pin_head_stride;
-  s.win_head_stride = a.win_head_stride;
-  s.st = a.st;
-  s.P = a.P;
-  s.F = a.F;
-  s.N = a.N;
-  s.slots = a.slots;
-  s.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(c.D)));
-  e = rx::launch_streams_quant(s, static_cast<cudaStream_t>(stream));
+  e = rx::launch_streams_quant(s, a, h->xchg_bytes, h->stream_ws, c.max_req, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rx_attend_streams_quant: launch");
   return RX_OK;
   RX_GUARD_END

@@ -37,6 +37,7 @@ __device__ __forceinline__ void publish_ring_state(DevState* st, int head, int v
 constexpr int kErrAttnTimeout = 1;    // attention kernel: a bounded wait gave up
 constexpr int kErrBatchTimeout = 2;   // batched attention: a bounded wait gave up
 constexpr int kErrAppendTimeout = 4;  // ring append: a bounded wait gave up
+constexpr int kErrStreamTimeout = 8;  // language streams' tails: a bounded wait gave up
 
 constexpr int kMaxCond = 16;          // rx_ada_gamma: conditioning vectors per call
 constexpr int kMaxHidden = 2048;      // rx_ada_gamma: hidden width
@@ -198,26 +199,30 @@ struct QuantStreams {
   const int* n_new;          // device [B]; null: T for every stream
   __nv_bfloat16* out;        // [B][T][Hq][D]
   int B, T, Hq, Hkv, D, tail_cap;
-  // The shared store's tiles of one layer (head 0) and its ring state.
-  const uint8_t* pin_k;
-  const uint8_t* pin_v;
-  const uint8_t* win_k;
-  const uint8_t* win_v;
-  long long pin_head_stride;
-  long long win_head_stride;
-  const DevState* st;
-  int P, F, N, slots;
-  float scale_log2;          // log2(e) / sqrt(D)
 };
-cudaError_t launch_streams_quant(const QuantStreams& a, cudaStream_t s);
+// `al`: the layer's shared store, as for the partitioned attention, with its
+// exchange area of xchg_bytes; ws: streams_quant_workspace(...) bytes of the
+// cache, for the tails' partials.
+cudaError_t launch_streams_quant(const QuantStreams& a, const AttnLaunch& al, size_t xchg_bytes, void* ws, int max_req,
+                                 cudaStream_t s);
+size_t streams_quant_workspace(int max_req, int Hkv, int G, int D, int num_sms);
 
 // ---- verification of drafted tokens ------------------------------------------
 cudaError_t launch_verify_drafts(const void* p, const void* q, bool bf16, const int* draft, const float* u,
                                  const float* r, const int* n_draft, int B, int T, int V, const int* tail_len,
                                  int* tokens, int* n_accept, int* new_len, cudaStream_t s);
 
-// Tensor-map encoding through the driver entry point (no -lcuda link).
+// The shared regions against `tokens` query tokens, left as fp32 partials in
+// the exchange area: O_s / l_s in [unit][split][D/8][128 rows][8], unit = head
+// * *m_tiles + 128-row tile, then (m_s, l_s) [unit][split][128].
+cudaError_t launch_attention_partials(const AttnLaunch& a, const void* q, int tokens, size_t xchg_bytes, cudaStream_t s,
+                                      int* splits, int* m_tiles);
+
+// Tensor-map encoding through the driver entry point (no -lcuda link); the
+// second for bytes, with the swizzle of the box's row (64 or 128 bytes).
 bool encode_tmap_4d(CUtensorMap* tm, const void* base, const uint64_t dims[4],
                     const uint64_t strides_bytes[3], const uint32_t box[4]);
+bool encode_tmap_u8_4d(CUtensorMap* tm, const void* base, const uint64_t dims[4],
+                       const uint64_t strides_bytes[3], const uint32_t box[4]);
 
 }  // namespace rx
