@@ -23,11 +23,10 @@
 //   O^T [D x N]       += V^T [D x 128] . W^T    (V codes as loaded, MN-major)
 // and the codes go from TMA to kind::f8f6f4 products without a conversion.
 // The bf16 queries and fp32 weights enter as sums of e4m3 terms whose products
-// accumulate in one fp32 accumulator: a query row, scaled by a power of two, is
-// hi + lo exactly (8 significant bits in two 4-bit terms; what lies 2^-18 below
-// the row's largest entry is rounded away); a weight is hi + mid + lo, within
-// 2^-12 of itself or 2^-18 of the row's largest weight, so it adds nothing
-// visible to the bf16 rounding of the output.
+// meet in fp32: a query row, scaled by a power of two, is hi + lo exactly (8
+// significant bits in two 4-bit terms; what lies 2^-18 below the row's largest
+// entry is rounded away); a weight is hi + mid + lo, within 2^-10 of itself or
+// 2^-18 of the row's largest weight, a quarter of a bf16 rounding.
 //   x_jn = S_jn * 2^(k_exp_j - 127) * (row scale) * log2(e) / sqrt(D)
 //   l_n  = sum_j 2^(x_jn - m_n),   w_jn = 2^(x_jn + v_exp_j - 127 - M_n + 8)
 // m_n and M_n are running maxima of x_jn and of x_jn + v_exp_j - 127: the
@@ -38,13 +37,14 @@
 // each CTA takes an equal run of consecutive tiles (lengths are read on the
 // device), and writes one fp32 partial per unit that it touches, to slot
 // cta + unit (distinct, because a run that moves to a later CTA or a later unit
-// never moves back).  Inside a unit, CT tiles form a chunk with one pair of
-// maxima, one rescale of O and one synchronisation of the softmax warps; the
-// scores of the next chunk are computed meanwhile.
+// never moves back).  The scores of tile i + 1 are computed while tile i is in
+// the softmax, and the weights have two buffers, so that a tile's softmax does
+// not wait for the product before it unless a maximum grew.
 //
-// Warp roles (192 threads): warp 0 = TMA producer, warp 1 = TMEM allocator and
-// MMA issuer, warps 2..5 = softmax and epilogue (thread = key of the tile for
-// S^T, output column for O^T; TMEM lane quarter = warp % 4).
+// Warp roles: warp 0 = TMA producer, warp 1 = TMEM allocator and MMA issuer,
+// the others = softmax and epilogue, in warpgroups of 4 warps that share up to
+// 16 query rows (thread = key of the tile for S^T, output column for O^T; TMEM
+// lane quarter = warp % 4).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -59,10 +59,12 @@
 namespace rx {
 namespace {
 
-constexpr int kTailThreads = 192;
 constexpr int kTK = 128;            // keys per tile
 constexpr int kTerms = 3;           // e4m3 terms of a weight
 constexpr float kTop = 8.f;         // log2 of a row's largest weight in e4m3 units
+// A running maximum before any key: below every score, and finite, so that its
+// differences need no care (2^(-inf - kNoMax) = 2^(kNoMax - m) = 0).
+constexpr float kNoMax = -3.0e38f;
 
 // ------------------------------------------------------------------- helpers
 // 2^(byte - 127); byte 255 stands for NaN.
@@ -97,10 +99,6 @@ __device__ __forceinline__ float warp_max(float v) {
   float r;
   asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
-}
-
-__device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // 8 or 16 consecutive fp32 columns of this thread's TMEM lane.
@@ -154,24 +152,35 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
-// Instruction descriptor, kind::f8f6f4 with e4m3 A/B and fp32 D.
-constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn) {
-  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
+// Instruction descriptor, kind::f8f6f4 with e4m3 A/B and fp32 D; mn: both
+// operands MN-major.
+constexpr uint32_t idesc_e4m3_f32(int M, int N, bool mn) {
+  return (1u << 4) | ((mn ? 3u : 0u) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// Shared-memory matrix descriptor with rows of ROW bytes, 128- or 64-byte
-// swizzle: as sdesc_sw128, layout type 4 (SWIZZLE_64B) for 64-byte rows.
+// Shared-memory matrix descriptor with rows of ROW bytes, swizzled over their
+// length: as sdesc_sw128, layout type 4 (SWIZZLE_64B) or 6 (SWIZZLE_32B) for
+// rows of 64 or 32 bytes.
 template <int ROW>
 __device__ __forceinline__ uint64_t sdesc_rows(uint32_t saddr, uint32_t lbo_bytes) {
   uint64_t d = sdesc_sw128(saddr, lbo_bytes, 8 * ROW);
   if (ROW == 64) d ^= (2ull ^ 4ull) << 61;
+  if (ROW == 32) d ^= (2ull ^ 6ull) << 61;
   return d;
+}
+// Its low word is (address / 16) | ..., so a step of n bytes adds n / 16 there.
+__device__ __forceinline__ uint64_t desc_step(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+// Keep the compiler from computing a loop's descriptors ahead of it, all of
+// them at once: the registers are the softmax warps'.
+__device__ __forceinline__ uint32_t here(uint32_t x) {
+  asm volatile("" : "+r"(x));
+  return x;
 }
 // Byte offset of byte c of row r in such a layout (rows of ROW bytes).
 template <int ROW>
 __device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c) {
-  const uint32_t x = ROW == 128 ? (r & 7u) : ((r >> 1) & 3u);
+  const uint32_t x = ROW == 128 ? (r & 7u) : ROW == 64 ? ((r >> 1) & 3u) : ((r >> 2) & 1u);
   return r * ROW + (((c >> 4) ^ x) << 4) + (c & 15u);
 }
 
@@ -266,68 +275,75 @@ struct Walk {
 
 template <int D, int RT>
 struct TailLayout {
-  static constexpr int N = RT < 16 ? 16 : RT;             // MMA N (a multiple of 16 at M = 128)
+  // Up to 32 rows the e4m3 terms of Q and W are further rows of one operand,
+  // so that a product reads the K or V codes from shared memory once for all
+  // terms (128 x 32 codes take as long to read as 64 columns to multiply); at
+  // 64 rows they are separate products into one accumulator.
+  static constexpr bool STACK = RT <= 32;
+  static constexpr int NQ = STACK ? 2 * RT : RT;                      // MMA N of the scores
+  static constexpr int NW = STACK ? 4 * RT : RT;                      // ... of the output (a term's place is spare)
+  static constexpr int QT = STACK ? 1 : 2;                            // products per K step
+  static constexpr int WT = STACK ? 1 : kTerms;
+  static constexpr int CW = RT < 16 ? RT : 16;            // rows of one softmax warpgroup
+  static constexpr int WG = RT / CW;                      // softmax warpgroups
+  static constexpr int THREADS = 64 + 128 * WG;
   static constexpr int ROW = D < 128 ? D : 128;           // bytes of a stored row (one column block)
   static constexpr int KB = D / ROW;                      // column blocks of a tile
   static constexpr int TILE = kTK * D;
   static constexpr int BLOCK = kTK * ROW;                 // one column block of a tile
   static constexpr int OB = D == 256 ? 2 : 1;             // 128-row blocks of O^T
-  // Tiles per chunk, so that two chunks of scores and O fit in 512 columns of
-  // TMEM (D = 256: one CTA per SM) or 256 (two CTAs per SM).
-  static constexpr int CT = RT <= 16 ? 4 : RT == 32 ? (D == 256 ? 4 : 2) : (D == 256 ? 2 : 1);
-  static constexpr int TM_O = 2 * CT * N;
-  static constexpr int TM_USED = TM_O + OB * N;
+  static constexpr int TM_O = 2 * NQ;                     // TMEM: two tiles' scores, then O
+  static constexpr int TM_USED = TM_O + OB * NW;
   static constexpr int TM_COLS = TM_USED <= 128 ? 128 : TM_USED <= 256 ? 256 : 512;
-  static constexpr int CTAS = D == 256 ? 1 : 2;           // per SM
-  static constexpr int Q_BLOCK = N * ROW;                 // one column block of one term
-  static constexpr int Q_BYTES = 2 * KB * Q_BLOCK;
-  static constexpr int W_BLOCK = N * kTK;                 // one term of one tile's weights
-  static constexpr int W_BYTES = CT * kTerms * W_BLOCK;
-  static constexpr int MISC = 5120;
+  static constexpr int CTAS = D == 256 || RT == 64 ? 1 : 2;   // per SM
+  static constexpr int Q_BLOCK = NQ * ROW;                // one column block of one product's Q
+  static constexpr int Q_BYTES = QT * KB * Q_BLOCK;
+  static constexpr int W_BLOCK = NW * kTK;                // one product's weights of a tile: [key][NW]
+  static constexpr int W_BYTES = WT * W_BLOCK;            // ... of all its products; two tiles are kept
+  static constexpr int MISC = RT == 64 ? 9728 : 5632;
   static constexpr int BUDGET = (CTAS == 1 ? 227 : 113) * 1024 - 1024;   // less the alignment slack
-  static constexpr int NS_FIT = (BUDGET - Q_BYTES - W_BYTES - MISC) / TILE;
+  static constexpr int NS_FIT = (BUDGET - Q_BYTES - 2 * W_BYTES - MISC) / TILE;
   static constexpr int NS = NS_FIT > 12 ? 12 : NS_FIT;    // ring slots of one K or V tile
   static constexpr int OFF_RING = 0;
   static constexpr int OFF_Q = NS * TILE;
   static constexpr int OFF_W = OFF_Q + Q_BYTES;
-  static constexpr int OFF_MISC = OFF_W + W_BYTES;
+  static constexpr int OFF_MISC = OFF_W + 2 * W_BYTES;
   static constexpr int BYTES = OFF_MISC + MISC;
   static constexpr int ALLOC = BYTES + 1024;
-  // A chunk's V tiles are all resident before its products begin.
-  static_assert(NS >= 3 && NS >= CT, "ring depth");
-  static_assert(TM_USED <= 512 / CTAS, "tensor memory");
+  static_assert(NS >= 3, "ring depth");
+  static_assert(TM_USED <= 512 / CTAS && TM_COLS <= 512 / CTAS, "tensor memory");
+  // A term's place in the Q operand.
+  static constexpr int q_off(int term) { return STACK ? term * RT * ROW : term * KB * Q_BLOCK; }
 };
 
 // The MISC area.
 template <int RT>
 struct TailMisc {
-  unsigned long long bar[12 + 12 + 6];   // full, empty, Q ready, S full[2], W ready, PV done, drain
+  unsigned long long bar[12 + 12 + 8];   // full, empty, Q ready, S full[2], W ready[2], PV done[2], drain
   uint32_t tmem;
   int abort;
   int b0, skip_unit;                     // first unit of the run: stream, and unit within it
   int skip_tile;
   int pad0;
   long long left;
-  long long scan[kTailThreads / 32 + 1];
+  long long scan[32];
   float qs[RT];                          // 2^e of the query rows
   int seen[RT];                          // tail keys each row sees
-  float m[RT], mv[RT];                   // running maxima (m_n, M_n)
-  float ms[RT], mvs[RT];                 // ... as subtracted: m, M - kTop (0 while -inf)
-  float al[RT], ao[RT];                  // factors of l and O of this chunk
-  float wm[4][RT], wv[4][RT];            // the warps' maxima, then their sums of l
-  int rescale;
+  float wm[2][4][RT], wv[2][4][RT];      // the warps' maxima, for even and odd tiles
+  float row[RT / 4][4][RT < 16 ? RT : 16];   // per warp: m, M - kTop, factors of l and O
 };
 
-enum : int { TB_FULL = 0, TB_EMPTY = 12, TB_Q = 24, TB_S = 25, TB_W = 27, TB_PV = 28, TB_DRAIN = 29 };
+enum : int { TB_FULL = 0, TB_EMPTY = 12, TB_Q = 24, TB_S = 25, TB_W = 27, TB_PV = 29, TB_DRAIN = 31 };
 
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 
 template <int D, int RT>
-__global__ void __launch_bounds__(kTailThreads, TailLayout<D, RT>::CTAS)
+__global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>::CTAS)
     stream_tail_kernel(const __grid_constant__ TailParams p) {
   using L = TailLayout<D, RT>;
-  constexpr int N = L::N, CT = L::CT, NS = L::NS, ROW = L::ROW;
-  constexpr int CB = RT < 16 ? RT : 16;   // columns taken at a time
+  constexpr int NS = L::NS, ROW = L::ROW, CW = L::CW, THREADS = L::THREADS;
   extern __shared__ uint8_t tail_smem[];
   const uint32_t raw = smem_u32(tail_smem);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -345,11 +361,12 @@ __global__ void __launch_bounds__(kTailThreads, TailLayout<D, RT>::CTAS)
       mbar_init(BAR(TB_FULL + i), 1);
       mbar_init(BAR(TB_EMPTY + i), 1);
     }
-    mbar_init(BAR(TB_Q), 128);
-    mbar_init(BAR(TB_S), 1);
-    mbar_init(BAR(TB_S + 1), 1);
-    mbar_init(BAR(TB_W), 128);
-    mbar_init(BAR(TB_PV), 1);
+    mbar_init(BAR(TB_Q), 128 * L::WG);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(BAR(TB_S + i), 1);
+      mbar_init(BAR(TB_W + i), 128 * L::WG);
+      mbar_init(BAR(TB_PV + i), 1);
+    }
     mbar_init(BAR(TB_DRAIN), 1);
     ms.abort = 0;
     fence_barrier_init();
@@ -368,8 +385,8 @@ __global__ void __launch_bounds__(kTailThreads, TailLayout<D, RT>::CTAS)
   grid_launch_dependents();
 
   // ------------------------------------------------------ this CTA's tiles
-  // Tiles before each stream, by a scan over the block's threads, 192 streams
-  // a round; with more streams a second sweep finds the run's first.
+  // Tiles before each stream, by a scan over the block's threads, THREADS
+  // streams a round; with more streams a second sweep finds the run's first.
   {
     auto scan_round = [&](int b, long long carry, long long* mine) {   // returns the carry after the round
       long long c = 0;
@@ -384,7 +401,7 @@ __global__ void __launch_bounds__(kTailThreads, TailLayout<D, RT>::CTAS)
       if (lane == 31) ms.scan[warp] = inc;
       __syncthreads();
       long long before = carry, total = carry;
-      for (int w = 0; w < kTailThreads / 32; ++w) {
+      for (int w = 0; w < THREADS / 32; ++w) {
         if (w < warp) before += ms.scan[w];
         total += ms.scan[w];
       }
@@ -393,7 +410,7 @@ __global__ void __launch_bounds__(kTailThreads, TailLayout<D, RT>::CTAS)
       return total;
     };
     long long mine[2], total = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kTailThreads) total = scan_round(b0 + threadIdx.x, total, mine);
+    for (int b0 = 0; b0 < p.B; b0 += THREADS) total = scan_round(b0 + threadIdx.x, total, mine);
     const unsigned long long C = static_cast<unsigned long long>(total);
     const unsigned long long A = min(static_cast<unsigned long long>(gridDim.x), C);
     const bool active = blockIdx.x < A;
@@ -403,9 +420,9 @@ __global__ void __launch_bounds__(kTailThreads, TailLayout<D, RT>::CTAS)
       if (blockIdx.x == 0) p.head[0] = C;
     }
     long long carry = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kTailThreads) {
+    for (int b0 = 0; b0 < p.B; b0 += THREADS) {
       const int b = b0 + threadIdx.x;
-      if (p.B > kTailThreads) carry = scan_round(b, carry, mine);
+      if (p.B > THREADS) carry = scan_round(b, carry, mine);
       if (b < p.B) {
         if (blockIdx.x == 0) p.head[1 + b] = static_cast<unsigned long long>(mine[0]);
         if (active && first >= mine[0] && first < mine[0] + mine[1]) {
@@ -436,8 +453,8 @@ __global__ void __launch_bounds__(kTailThreads, TailLayout<D, RT>::CTAS)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    // Per segment: K of chunk 0, then K of chunk c + 1 and V of chunk c in
-    // turn, the order in which the MMA issuer takes them.
+    // Per segment: K_0, then K_{i+1} and V_i in turn, the order in which the
+    // MMA issuer takes them.
     if (lane == 0) {
       unsigned int item = 0;
       bool stop = false;
@@ -453,11 +470,10 @@ __global__ void __launch_bounds__(kTailThreads, TailLayout<D, RT>::CTAS)
         ++item;
       };
       while (!stop && wk.next(p, RT)) {
-        const int nt = wk.ntiles;
-        for (int i = 0; i < min(CT, nt) && !stop; ++i) load(&p.tm_k, wk.tile0 + i);
-        for (int c0 = 0; c0 < nt && !stop; c0 += CT) {
-          for (int i = c0 + CT; i < min(c0 + 2 * CT, nt) && !stop; ++i) load(&p.tm_k, wk.tile0 + i);
-          for (int i = c0; i < min(c0 + CT, nt) && !stop; ++i) load(&p.tm_v, wk.tile0 + i);
+        load(&p.tm_k, wk.tile0);
+        for (int i = 0; i < wk.ntiles && !stop; ++i) {
+          if (i + 1 < wk.ntiles) load(&p.tm_k, wk.tile0 + i + 1);
+          if (!stop) load(&p.tm_v, wk.tile0 + i);
         }
         wk.done(p);
       }
@@ -469,69 +485,64 @@ __global__ void __launch_bounds__(kTailThreads, TailLayout<D, RT>::CTAS)
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     if (lane == 0) {
-      constexpr uint32_t kIdescS = idesc_e4m3_f32(kTK, N, false);
-      constexpr uint32_t kIdescO = idesc_e4m3_f32(128, N, true);
-      unsigned int item = 0, chunk = 0, seg = 0;
+      constexpr uint32_t kIdescS = idesc_e4m3_f32(kTK, L::NQ, false);
+      constexpr uint32_t kIdescO = idesc_e4m3_f32(128, L::NW, true);
+      unsigned int item = 0, tile = 0, seg = 0;
       bool ok = true;
-      auto scores = [&](unsigned int ck, int tiles) {   // S^T of one chunk
-        for (int i = 0; i < tiles && ok; ++i) {
-          const int slot = item % NS;
-          if (!mbar_wait(BAR(TB_FULL + slot), (item / NS) & 1, abort_flag)) {
-            ok = false;
-            return;
-          }
-          tc_fence_after();
-          const uint32_t kt = sRing + slot * L::TILE;
-          const uint32_t d = tmem + ((ck & 1) * CT + i) * N;
-#pragma unroll
-          for (int term = 0; term < 2; ++term)
-#pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk) {
-              const uint32_t kb = kk * 32 / ROW, ko = kk * 32 % ROW;
-              umma_e4m3(d, sdesc_rows<ROW>(kt + kb * L::BLOCK + ko, 16),
-                        sdesc_rows<ROW>(sQ + (term * L::KB + kb) * L::Q_BLOCK + ko, 16), kIdescS, (term | kk) ? 1u : 0u);
-            }
-          umma_commit(BAR(TB_EMPTY + slot));
-          ++item;
+      auto scores = [&](unsigned int t) {   // S^T of the tile whose K is the next item
+        const int slot = item % NS;
+        if (!mbar_wait(BAR(TB_FULL + slot), (item / NS) & 1, abort_flag)) {
+          ok = false;
+          return;
         }
-        umma_commit(BAR(TB_S + (ck & 1)));
+        tc_fence_after();
+        const uint64_t kd = sdesc_rows<ROW>(here(sRing + slot * L::TILE), 16);
+        const uint64_t qd = sdesc_rows<ROW>(here(sQ), 16);
+        const uint32_t acc = here(tmem + (t & 1) * L::NQ);
+#pragma unroll
+        for (int term = 0; term < L::QT; ++term)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk) {
+            const uint32_t kb = kk * 32 / ROW, ko = kk * 32 % ROW;
+            umma_e4m3(acc, desc_step(kd, kb * L::BLOCK + ko), desc_step(qd, (term * L::KB + kb) * L::Q_BLOCK + ko), kIdescS,
+                      (term | kk) ? 1u : 0u);
+          }
+        umma_commit(BAR(TB_EMPTY + slot));
+        umma_commit(BAR(TB_S + (t & 1)));
+        ++item;
       };
       while (ok && wk.next(p, RT)) {
-        const int nt = wk.ntiles;
         if (!mbar_wait(BAR(TB_Q), seg & 1, abort_flag)) break;
         tc_fence_after();
-        scores(chunk, min(CT, nt));
-        for (int c0 = 0; c0 < nt && ok; c0 += CT, ++chunk) {
-          if (c0 + CT < nt) scores(chunk + 1, min(CT, nt - c0 - CT));
-          if (!ok || !mbar_wait(BAR(TB_W), chunk & 1, abort_flag)) {
+        scores(tile);
+        for (int i = 0; i < wk.ntiles && ok; ++i, ++tile) {
+          // S buffer (tile + 1) & 1 was read before W of tile - 1 was ready.
+          if (i + 1 < wk.ntiles) scores(tile + 1);
+          const int slot = item % NS;
+          if (!ok || !mbar_wait(BAR(TB_W + (tile & 1)), (tile >> 1) & 1, abort_flag) ||
+              !mbar_wait(BAR(TB_FULL + slot), (item / NS) & 1, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          for (int i = 0; i < min(CT, nt - c0); ++i) {
-            const int slot = item % NS;
-            if (!mbar_wait(BAR(TB_FULL + slot), (item / NS) & 1, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t vt = sRing + slot * L::TILE;
+          // A: V codes, D along the stored rows (MN-major), 8-key groups
+          // 8 * ROW apart.  At D = 64 the product's upper 64 rows read the
+          // bytes one tile further on and are not used.
+          const uint64_t vd = sdesc_rows<ROW>(here(sRing + slot * L::TILE), L::BLOCK);
+          // B: weights, rows n along the stored bytes of a key, likewise.
+          const uint64_t wd = sdesc_rows<L::NW>(here(sW + (tile & 1) * L::W_BYTES), 16);
+          const uint32_t acc = here(tmem + L::TM_O);
 #pragma unroll
-            for (int ob = 0; ob < L::OB; ++ob)
+          for (int ob = 0; ob < L::OB; ++ob)
 #pragma unroll
-              for (int term = 0; term < kTerms; ++term)
+            for (int term = 0; term < L::WT; ++term)
 #pragma unroll
-                for (int kk = 0; kk < kTK / 32; ++kk)
-                  // A: V codes, D along the stored rows (MN-major), 8-key
-                  // groups 8 * ROW apart.  At D = 64 the product's upper 64
-                  // rows read the bytes one tile further on and are not used.
-                  umma_e4m3(tmem + L::TM_O + ob * N, sdesc_rows<ROW>(vt + ob * L::BLOCK + kk * 32 * ROW, L::BLOCK),
-                            sdesc_rows<128>(sW + (i * kTerms + term) * L::W_BLOCK + kk * 32, 16), kIdescO,
-                            (c0 | i | term | kk) ? 1u : 0u);
-            umma_commit(BAR(TB_EMPTY + slot));
-            ++item;
-          }
-          umma_commit(BAR(TB_PV));
+              for (int kk = 0; kk < kTK / 32; ++kk)
+                umma_e4m3(acc + ob * L::NW, desc_step(vd, ob * L::BLOCK + kk * 32 * ROW),
+                          desc_step(wd, term * L::W_BLOCK + kk * 32 * L::NW), kIdescO, (i | term | kk) ? 1u : 0u);
+          umma_commit(BAR(TB_EMPTY + slot));
+          umma_commit(BAR(TB_PV + (tile & 1)));
+          ++item;
         }
         wk.done(p);
         ++seg;
@@ -543,254 +554,273 @@ __global__ void __launch_bounds__(kTailThreads, TailLayout<D, RT>::CTAS)
     }
   } else {
     // ------------------------------------------------- softmax and epilogue
+    // Warpgroup wg has the rows n0 .. n0 + CW - 1; a thread one key of the tile
+    // for all of them (TMEM lane = key), and at the end one output column.
     // After a wait that gave up the loops run on (their waits return at once)
-    // so that all four warps meet at every barrier; the results are void and
-    // the error bit says so.
+    // so that the warps meet at every barrier; the results are void and the
+    // error bit says so.
     const int quarter = warp & 3;
-    const int st = threadIdx.x - 64;                        // 0..127
+    const int st = threadIdx.x - 64;
+    const int wg = st >> 7;
+    const int n0 = wg * CW;
+    const int in_wg = st & 127;
     const int key_in_tile = quarter * 32 + lane;            // TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    unsigned int item0 = 0, chunk = 0;
-    if (RT < N)   // rows of the operands past RT stay zero
-      for (int i = st * 16; i < L::Q_BYTES + L::W_BYTES; i += 128 * 16) st_shared_v4(sQ + i, 0u, 0u, 0u, 0u);
+    float (&row)[4][CW] = ms.row[st >> 5];
+    unsigned int item0 = 0, tile = 0;
+    if (L::STACK)   // the spare rows of W stay zero
+      for (int i = st * 16; i < 2 * L::W_BYTES; i += 128 * L::WG * 16) st_shared_v4(sW + i, 0u, 0u, 0u, 0u);
     while (wk.next(p, RT)) {
       const int nt = wk.ntiles;
       const int row0 = wk.rt * RT;
       const int rows = min(RT, wk.s.n * p.G - row0);        // rows with a query token
       const int kmax = keys_seen(wk.s, min(wk.s.n - 1, (row0 + RT - 1) / p.G));   // keys any row sees
       const int kmin = keys_seen(wk.s, row0 / p.G);                               // ... every row sees
-      softmax_sync();   // the previous segment's row state is no longer read
-      if (st < RT) {
-        ms.seen[st] = st < rows ? keys_seen(wk.s, (row0 + st) / p.G) : 0;
-        ms.m[st] = -INFINITY;
-        ms.mv[st] = -INFINITY;
-      }
+      // The exponents of a thread's key, loaded a tile ahead of their use.
+      const long long exp_base = (static_cast<long long>(wk.b) * p.tail_cap) * p.Hkv + wk.g;
+      uint32_t kb, vb;
+      auto load_exps = [&](int key) {
+        kb = vb = 0;
+        if (key < kmax) {
+          const long long at = exp_base + static_cast<long long>(key) * p.Hkv;
+          kb = p.k_exp[at];
+          vb = p.v_exp[at];
+        }
+      };
+      load_exps(wk.tile0 * kTK + key_in_tile);
+      named_sync(8, 128 * L::WG);   // the previous segment's row state is no longer read
+      if (st < RT) ms.seen[st] = st < rows ? keys_seen(wk.s, (row0 + st) / p.G) : 0;
       // Q rows: 2^-e q = hi + lo, e as the append chooses it.
-      for (int n = st >> 5; n < RT; n += 4) {
+      for (int n = st >> 5; n < RT; n += 4 * L::WG) {
         constexpr int E = D / 32;
-        uint32_t bits[E];
+        uint32_t w32[E / 2];
         uint32_t top = 0;
         const int r = row0 + n;
         const __nv_bfloat16* src =
             p.q + ((static_cast<long long>(wk.b) * p.T + r / p.G) * p.Hkv * p.G + wk.g * p.G + r % p.G) * D + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          bits[e] = n < rows ? __bfloat16_as_ushort(src[e]) : 0u;
-          top = max(top, bits[e] & 0x7FFFu);
-        }
+        for (int e = 0; e < E / 2; ++e) w32[e] = n < rows ? __ldg(reinterpret_cast<const uint32_t*>(src) + e) : 0u;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) top = max(top, max(w32[e] & 0x7FFFu, (w32[e] >> 16) & 0x7FFFu));
         top = __reduce_max_sync(0xffffffffu, top);
         const int ex = max(static_cast<int>(top >> 7) - 8 + ((top & 0x7Fu) > 96u ? 1 : 0), 1);
         const bool poison = (top >> 7) == 255u;
         if (lane == 0) ms.qs[n] = poison ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(ex) << 23);
         const float up = __uint_as_float(static_cast<uint32_t>(254 - min(ex, 253)) << 23);
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float a = poison ? 0.f : __uint_as_float(bits[e] << 16) * up;
-          const float b = poison ? 0.f : __uint_as_float(bits[e + 1] << 16) * up;
+        for (int e = 0; e < E / 2; ++e) {
+          const float a = poison ? 0.f : __uint_as_float(w32[e] << 16) * up;
+          const float b = poison ? 0.f : __uint_as_float(w32[e] & 0xFFFF0000u) * up;
           const uint32_t hi = to_e4m3x2(a, b);
           const float2 h = from_e4m3x2(hi);
           const uint32_t lo = to_e4m3x2(a - h.x, b - h.y);
-          const uint32_t d = static_cast<uint32_t>(lane * E + e);
-          const uint32_t off = (d / ROW) * L::Q_BLOCK + swizzled<ROW>(n, d % ROW);
-          asm volatile("st.shared.u16 [%0], %1;" ::"r"(sQ + off), "h"(static_cast<uint16_t>(hi)) : "memory");
-          asm volatile("st.shared.u16 [%0], %1;" ::"r"(sQ + L::KB * L::Q_BLOCK + off), "h"(static_cast<uint16_t>(lo))
+          const uint32_t d = static_cast<uint32_t>(lane * E + 2 * e);
+          const uint32_t off = sQ + (d / ROW) * L::Q_BLOCK;
+          // (a term's rows are a multiple of 8, so they keep the row's swizzle)
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(off + swizzled<ROW>(n, d % ROW)), "h"(static_cast<uint16_t>(hi)) : "memory");
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(off + L::q_off(1) + swizzled<ROW>(n, d % ROW)), "h"(static_cast<uint16_t>(lo))
                        : "memory");
         }
       }
       fence_proxy_async_smem();
       tc_fence_before();   // the previous segment's reads of O
       mbar_arrive(BAR(TB_Q));
-      softmax_sync();      // row state visible
+      named_sync(8, 128 * L::WG);      // row state visible
 
-      float l[RT];
+      float l[CW];
 #pragma unroll
-      for (int n = 0; n < RT; ++n) l[n] = 0.f;
-      const long long exp_base = (static_cast<long long>(wk.b) * p.tail_cap) * p.Hkv + wk.g;
-      for (int c0 = 0; c0 < nt; c0 += CT, ++chunk) {
-        const int tiles = min(CT, nt - c0);
-        const int buf = chunk & 1;
-        const uint32_t tS = tmem + buf * CT * N + lane_off;
-        const int key0 = (wk.tile0 + c0) * kTK + key_in_tile;
-        float ks[CT], ev[CT];
-#pragma unroll
-        for (int i = 0; i < CT; ++i) {
-          const int key = key0 + i * kTK;
-          uint32_t kb = 0, vb = 0;
-          if (i < tiles && key < kmax) {
-            const long long at = exp_base + static_cast<long long>(key) * p.Hkv;
-            kb = p.k_exp[at];
-            vb = p.v_exp[at];
-          }
-          ks[i] = exp_scale(kb) * p.scale_log2;
-          ev[i] = vb == 255u ? __uint_as_float(0x7FC00000u) : static_cast<float>(vb) - 127.f;
-        }
-        mbar_wait(BAR(TB_S + buf), (chunk >> 1) & 1, abort_flag);
+      for (int j = 0; j < CW; ++j) l[j] = 0.f;
+      float m = kNoMax, mv = kNoMax;   // lane j < CW: the running maxima of row n0 + j
+      if (lane < CW) row[0][lane] = row[1][lane] = kNoMax;
+      __syncwarp();
+      for (int i = 0; i < nt; ++i, ++tile) {
+        const int buf = tile & 1;
+        const int key = (wk.tile0 + i) * kTK + key_in_tile;
+        const float ks = exp_scale(kb) * p.scale_log2;
+        const float ev = vb == 255u ? __uint_as_float(0x7FC00000u) : static_cast<float>(vb) - 127.f;
+        load_exps(i + 1 < nt ? key + kTK : kmax);   // the next tile's, a tile ahead
+        const bool masked = (wk.tile0 + i + 1) * kTK > kmin;
+        mbar_wait(BAR(TB_S + buf), (tile >> 1) & 1, abort_flag);
         __syncwarp();
         tc_fence_after();
-        // ---- maxima of the chunk
+        float x[CW];
+        tmem_ld_cols(tmem + buf * L::NQ + n0 + lane_off, x);
+        if constexpr (L::STACK) {
+          float lo[CW];
+          tmem_ld_cols(tmem + buf * L::NQ + RT + n0 + lane_off, lo);
 #pragma unroll
-        for (int n0 = 0; n0 < RT; n0 += CB) {
-          float mx[CB], my[CB];
+          for (int j = 0; j < CW; ++j) x[j] += lo[j];
+        }
 #pragma unroll
-          for (int j = 0; j < CB; ++j) mx[j] = my[j] = -INFINITY;
+        for (int j = 0; j < CW; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&ms.qs[n0 + j]);
+          x[j] *= ks * f.x;
+          x[j + 1] *= ks * f.y;
+          x[j + 2] *= ks * f.z;
+          x[j + 3] *= ks * f.w;
+        }
+        if (masked) {
 #pragma unroll
-          for (int i = 0; i < CT; ++i) {
-            if (i < tiles) {
-              float s[CB];
-              tmem_ld_cols(tS + i * N + n0, s);
-              const bool masked = (wk.tile0 + c0 + i + 1) * kTK > kmin;
+          for (int j = 0; j < CW; ++j)
+            if (key >= ms.seen[n0 + j]) x[j] = -INFINITY;
+        }
+        // ---- the tile's maxima: over the warp's keys, then over the four
+        // warps, lane j for row n0 + j; almost always none grew.
+        float hx = kNoMax, hy = kNoMax;
 #pragma unroll
-              for (int j = 0; j < CB; ++j) {
-                float x = s[j] * (ks[i] * ms.qs[n0 + j]);
-                if (masked && key0 + i * kTK >= ms.seen[n0 + j]) x = -INFINITY;
-                mx[j] = fmaxf(mx[j], x);
-                my[j] = fmaxf(my[j], x + ev[i]);
-              }
-            }
-          }
-          float hx = 0.f, hy = 0.f;
-#pragma unroll
-          for (int j = 0; j < CB; ++j) {
-            const float a = warp_max(mx[j]), b = warp_max(my[j]);
-            if (lane == j) {
-              hx = a;
-              hy = b;
-            }
-          }
-          if (lane < CB) {
-            ms.wm[quarter][n0 + lane] = hx;
-            ms.wv[quarter][n0 + lane] = hy;
+        for (int j = 0; j < CW; ++j) {
+          const float a = warp_max(x[j]), b = warp_max(x[j] + ev);
+          if (lane == j) {
+            hx = a;
+            hy = b;
           }
         }
-        softmax_sync();
-        if (st < 32) {
-          bool grow = false;
-          for (int n = st; n < RT; n += 32) {
-            const float mo = ms.m[n], vo = ms.mv[n];
-            const float mn = fmaxf(fmaxf(fmaxf(ms.wm[0][n], ms.wm[1][n]), fmaxf(ms.wm[2][n], ms.wm[3][n])), mo);
-            const float vn = fmaxf(fmaxf(fmaxf(ms.wv[0][n], ms.wv[1][n]), fmaxf(ms.wv[2][n], ms.wv[3][n])), vo);
-            ms.m[n] = mn;
-            ms.mv[n] = vn;
-            ms.ms[n] = mn == -INFINITY ? 0.f : mn;
-            ms.mvs[n] = vn == -INFINITY ? 0.f : vn - kTop;
-            ms.al[n] = mo == -INFINITY ? 0.f : ex2(mo - mn);
-            ms.ao[n] = vo == -INFINITY ? 1.f : ex2(vo - vn);   // nothing accumulated yet: zeros (or NaN) stay
-            grow |= c0 > 0 && vo != vn && vo != -INFINITY;
-          }
-          const bool any = __any_sync(0xffffffffu, grow);
-          if (st == 0) ms.rescale = any;
+        if (lane < CW) {
+          ms.wm[buf][quarter][n0 + lane] = hx;
+          ms.wv[buf][quarter][n0 + lane] = hy;
         }
-        softmax_sync();
-        // ---- the previous chunk's product: W is free, and O may be rescaled
-        if (c0 > 0) {
-          mbar_wait(BAR(TB_PV), (chunk - 1) & 1, abort_flag);
+        named_sync(1 + wg, 128);
+        if (lane < CW) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            hx = fmaxf(hx, ms.wm[buf][w][n0 + lane]);
+            hy = fmaxf(hy, ms.wv[buf][w][n0 + lane]);
+          }
+        }
+        if (__any_sync(0xffffffffu, hx > m || hy > mv)) {   // alike in the four warps
+          const float mn = fmaxf(hx, m), vn = fmaxf(hy, mv);
+          if (lane < CW) {
+            row[0][lane] = mn;
+            row[1][lane] = vn - kTop;
+            row[2][lane] = ex2(m - mn);
+            row[3][lane] = ex2(mv - vn);
+          }
+          m = mn;
+          mv = vn;
           __syncwarp();
-          tc_fence_after();
-          if (ms.rescale) {
 #pragma unroll
-            for (int ob = 0; ob < L::OB; ++ob)
-#pragma unroll
-              for (int n0 = 0; n0 < RT; n0 += CB) {
-                float o[CB];
-                tmem_ld_cols(tmem + L::TM_O + ob * N + n0 + lane_off, o);
-#pragma unroll
-                for (int j = 0; j < CB; ++j) o[j] *= ms.ao[n0 + j];
-                tmem_st_cols(tmem + L::TM_O + ob * N + n0 + lane_off, o);
-              }
+          for (int j = 0; j < CW; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&row[2][j]);
+            l[j] *= f.x;
+            l[j + 1] *= f.y;
+            l[j + 2] *= f.z;
+            l[j + 3] *= f.w;
           }
-        }
-        // ---- weights
+          if (i > 0) {
+            // O holds the tiles before: wait for their last product, then rescale.
+            mbar_wait(BAR(TB_PV + (buf ^ 1)), ((tile - 1) >> 1) & 1, abort_flag);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < L::OB * (L::STACK ? kTerms : 1); ++c) {
+              const uint32_t at = tmem + L::TM_O + (c % L::OB) * L::NW + (c / L::OB) * RT + n0 + lane_off;
+              float o[CW];
+              tmem_ld_cols(at, o);
 #pragma unroll
-        for (int n0 = 0; n0 < RT; n0 += CB) {
-#pragma unroll
-          for (int j = 0; j < CB; ++j) l[n0 + j] *= ms.al[n0 + j];
-#pragma unroll
-          for (int i = 0; i < CT; ++i) {
-            if (i < tiles) {
-              float s[CB];
-              tmem_ld_cols(tS + i * N + n0, s);
-              const bool masked = (wk.tile0 + c0 + i + 1) * kTK > kmin;
-              const uint32_t wrow = sW + i * kTerms * L::W_BLOCK;
-#pragma unroll
-              for (int j = 0; j < CB; j += 2) {
-                float w[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int n = n0 + j + e;
-                  const float x = s[j + e] * (ks[i] * ms.qs[n]);
-                  float pr = ex2(x - ms.ms[n]);
-                  w[e] = ex2(x + ev[i] - ms.mvs[n]);
-                  if (masked && key0 + i * kTK >= ms.seen[n]) pr = w[e] = 0.f;
-                  l[n] += pr;
-                }
-                const uint32_t c1 = to_e4m3x2(w[0], w[1]);
-                const float2 f1 = from_e4m3x2(c1);
-                const float r0 = w[0] - f1.x, r1 = w[1] - f1.y;
-                const uint32_t c2 = to_e4m3x2(r0, r1);
-                const float2 f2 = from_e4m3x2(c2);
-                const uint32_t c3 = to_e4m3x2(r0 - f2.x, r1 - f2.y);
-                const uint32_t a0 = wrow + swizzled<128>(n0 + j, key_in_tile);
-                const uint32_t a1 = wrow + swizzled<128>(n0 + j + 1, key_in_tile);
-                st_shared_u8(a0, c1 & 0xFFu);
-                st_shared_u8(a1, c1 >> 8);
-                st_shared_u8(a0 + L::W_BLOCK, c2 & 0xFFu);
-                st_shared_u8(a1 + L::W_BLOCK, c2 >> 8);
-                st_shared_u8(a0 + 2 * L::W_BLOCK, c3 & 0xFFu);
-                st_shared_u8(a1 + 2 * L::W_BLOCK, c3 >> 8);
-              }
+              for (int j = 0; j < CW; ++j) o[j] *= row[3][j];
+              tmem_st_cols(at, o);
             }
           }
+        }
+        // ---- weights, once the product that read this W buffer is done
+        if (i > 1) {
+          mbar_wait(BAR(TB_PV + buf), ((tile - 2) >> 1) & 1, abort_flag);
+          __syncwarp();
+        }
+        uint32_t codes[kTerms][CW / 4];
+#pragma unroll
+        for (int j = 0; j < CW; j += 4) {
+          const float4 m4 = *reinterpret_cast<const float4*>(&row[0][j]);
+          const float4 v4 = *reinterpret_cast<const float4*>(&row[1][j]);
+          const float mj[4] = {m4.x, m4.y, m4.z, m4.w}, vj[4] = {v4.x, v4.y, v4.z, v4.w};
+          uint32_t hi[4], mid[4];
+          float lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            l[j + e] += ex2(x[j + e] - mj[e]);
+            // (a masked score is -inf: its weight is zero even where ev is NaN)
+            const float w = x[j + e] == -INFINITY ? 0.f : ex2(x[j + e] + ev - vj[e]);
+            // Four leading bits at a time: exact remainders, and terms that
+            // e4m3 holds exactly (or, below its normal range, to 2^-10).
+            hi[e] = __float_as_uint(w) & 0xFFF00000u;
+            const float r1 = w - __uint_as_float(hi[e]);
+            mid[e] = __float_as_uint(r1) & 0xFFF00000u;
+            lo[e] = r1 - __uint_as_float(mid[e]);
+          }
+          codes[0][j / 4] = to_e4m3x2(__uint_as_float(hi[0]), __uint_as_float(hi[1])) |
+                            to_e4m3x2(__uint_as_float(hi[2]), __uint_as_float(hi[3])) << 16;
+          codes[1][j / 4] = to_e4m3x2(__uint_as_float(mid[0]), __uint_as_float(mid[1])) |
+                            to_e4m3x2(__uint_as_float(mid[2]), __uint_as_float(mid[3])) << 16;
+          codes[2][j / 4] = to_e4m3x2(lo[0], lo[1]) | to_e4m3x2(lo[2], lo[3]) << 16;
+        }
+        // The CW bytes of each term side by side in the key's stored row.
+        const uint32_t wb = sW + buf * L::W_BYTES;
+#pragma unroll
+        for (int term = 0; term < kTerms; ++term) {
+          const uint32_t at = wb + (L::STACK ? swizzled<L::NW>(key_in_tile, term * RT + n0)
+                                             : term * L::W_BLOCK + swizzled<L::NW>(key_in_tile, n0));
+          if constexpr (CW == 16)
+            st_shared_v4(at, codes[term][0], codes[term][1], codes[term][2], codes[term][3]);
+          else
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(codes[term][0]), "r"(codes[term][1]) : "memory");
         }
         // ---- stored rows past the last key: whatever they hold (NaN codes
         // among it) would meet a zero weight in the product, so they become
         // zeros once the tile has landed.
-        const int last = wk.tile0 + c0 + tiles - 1;
-        if ((last + 1) * kTK > kmax) {
-          const int vi = tiles - 1;
-          const unsigned int it = item0 + min(c0 + 2 * CT, nt) + c0 + vi;
+        if (wg == 0 && (wk.tile0 + i + 1) * kTK > kmax) {
+          const unsigned int it = item0 + min(i + 2, nt) + i;   // K_0, then K_{i+1} and V_i in turn
           const int slot = it % NS;
           mbar_wait(BAR(TB_FULL + slot), (it / NS) & 1, abort_flag);
-          if (last * kTK + key_in_tile >= kmax) {
-            for (int kb = 0; kb < L::KB; ++kb)
-              for (int x = 0; x < ROW; x += 16)
-                st_shared_v4(sRing + slot * L::TILE + kb * L::BLOCK + key_in_tile * ROW + x, 0u, 0u, 0u, 0u);
+          if (key >= kmax) {
+            for (int c = 0; c < L::KB; ++c)
+              for (int y = 0; y < ROW; y += 16)
+                st_shared_v4(sRing + slot * L::TILE + c * L::BLOCK + key_in_tile * ROW + y, 0u, 0u, 0u, 0u);
           }
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(BAR(TB_W));
+        mbar_arrive(BAR(TB_W + buf));
       }
       // ---- the segment's partial: O relative to m, and (m, l)
       const long long unit = (static_cast<long long>(wk.b) * p.Hkv + wk.g) * p.row_tiles + wk.rt;
-      const long long slot_row = (unit + blockIdx.x) * RT;
-      softmax_sync();   // wm is free
+      const long long slot_row = (unit + blockIdx.x) * RT + n0;
+      named_sync(1 + wg, 128);   // wm is free
 #pragma unroll
-      for (int n = 0; n < RT; ++n) {
-        float v = l[n];
+      for (int j = 0; j < CW; ++j) {
+        float v = l[j];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) ms.wm[quarter][n] = v;
+        if (lane == 0) ms.wm[0][quarter][n0 + j] = v;
       }
-      softmax_sync();
-      if (st < rows)
-        p.ml[slot_row + st] = make_float2(ms.m[st], (ms.wm[0][st] + ms.wm[1][st]) + (ms.wm[2][st] + ms.wm[3][st]));
-      if (st < RT) ms.ao[st] = ms.mv[st] == -INFINITY ? 1.f : exp2f(ms.mvs[st] - ms.ms[st]);
-      softmax_sync();
-      mbar_wait(BAR(TB_PV), (chunk - 1) & 1, abort_flag);
+      if (lane < CW) row[2][lane] = exp2f(mv - kTop - m);   // O's reference to m
+      named_sync(1 + wg, 128);
+      if (in_wg < CW && n0 + in_wg < rows)
+        p.ml[slot_row + in_wg] = make_float2(m == kNoMax ? -INFINITY : m,
+                                             (ms.wm[0][0][n0 + in_wg] + ms.wm[0][1][n0 + in_wg]) +
+                                                 (ms.wm[0][2][n0 + in_wg] + ms.wm[0][3][n0 + in_wg]));
+      mbar_wait(BAR(TB_PV + ((tile - 1) & 1)), ((tile - 1) >> 1) & 1, abort_flag);
       __syncwarp();
       tc_fence_after();
       if (D >= 128 || quarter < D / 32) {
 #pragma unroll
-        for (int ob = 0; ob < L::OB; ++ob)
+        for (int ob = 0; ob < L::OB; ++ob) {
+          float o[CW];
+          const uint32_t at = tmem + L::TM_O + ob * L::NW + n0 + lane_off;
+          tmem_ld_cols(at, o);
+          if constexpr (L::STACK) {
 #pragma unroll
-          for (int n0 = 0; n0 < RT; n0 += CB) {
-            float o[CB];
-            tmem_ld_cols(tmem + L::TM_O + ob * N + n0 + lane_off, o);
-            float* dst = p.o + (slot_row + n0) * D + ob * 128 + key_in_tile;
+            for (int term = 1; term < kTerms; ++term) {
+              float t[CW];
+              tmem_ld_cols(at + term * RT, t);
 #pragma unroll
-            for (int j = 0; j < CB; ++j)
-              if (n0 + j < rows) dst[j * D] = o[j] * ms.ao[n0 + j];
+              for (int j = 0; j < CW; ++j) o[j] += t[j];
+            }
           }
+          float* dst = p.o + slot_row * D + ob * 128 + key_in_tile;
+#pragma unroll
+          for (int j = 0; j < CW; ++j)
+            if (n0 + j < rows) dst[j * D] = o[j] * row[2][j];
+        }
       }
       item0 += 2 * nt;
       wk.done(p);
@@ -953,7 +983,7 @@ cudaError_t launch_tails(TailParams& p, int num_sms, int* ctas, cudaStream_t s) 
   const cudaError_t e = cudaFuncSetAttribute(stream_tail_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
   if (e != cudaSuccess) return e;
   *ctas = num_sms * L::CTAS;
-  return launch_k(stream_tail_kernel<D, RT>, dim3(*ctas), dim3(kTailThreads), L::ALLOC, s, p);
+  return launch_k(stream_tail_kernel<D, RT>, dim3(*ctas), dim3(L::THREADS), L::ALLOC, s, p);
 }
 
 template <int D>
