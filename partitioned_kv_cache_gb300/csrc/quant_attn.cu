@@ -26,12 +26,13 @@
 // meet in fp32: a query row, scaled by a power of two, is hi + lo exactly (8
 // significant bits in two 4-bit terms; what lies 2^-18 below the row's largest
 // entry is rounded away); a weight is hi + mid + lo, within 2^-10 of itself or
-// 2^-18 of the row's largest weight, a quarter of a bf16 rounding.
+// 2^-15 of the row's largest weight, a quarter of a bf16 rounding.
 //   x_jn = S_jn * 2^(k_exp_j - 127) * (row scale) * log2(e) / sqrt(D)
-//   l_n  = sum_j 2^(x_jn - m_n),   w_jn = 2^(x_jn + v_exp_j - 127 - M_n + 8)
+//   l_n  = sum_j 2^(x_jn - m_n),   w_jn = 2^(x_jn + v_exp_j - 127 - M_n + 5)
 // m_n and M_n are running maxima of x_jn and of x_jn + v_exp_j - 127: the
-// weights' own reference keeps them at the top of the e4m3 range whatever the
-// values' scales are.
+// weights' own reference keeps them in the upper e4m3 range whatever the
+// values' scales are.  Both are kept until some exponent outgrows them by 3.5
+// or more, which after a segment's first tile is rare.
 //
 // Work is cut into tiles of 128 keys of one (stream, K/V head, row tile) unit;
 // each CTA takes an equal run of consecutive tiles (lengths are read on the
@@ -61,7 +62,10 @@ namespace {
 
 constexpr int kTK = 128;            // keys per tile
 constexpr int kTerms = 3;           // e4m3 terms of a weight
-constexpr float kTop = 8.f;         // log2 of a row's largest weight in e4m3 units
+// log2 of a row's largest weight, in e4m3 units, where its reference is taken,
+// and the most it may grow to before a new one is (448 is the largest code).
+constexpr float kTop = 5.f;
+constexpr float kRoom = 8.5f;
 // A running maximum before any key: below every score, and finite, so that its
 // differences need no care (2^(-inf - kNoMax) = 2^(kNoMax - m) = 0).
 constexpr float kNoMax = -3.0e38f;
@@ -337,6 +341,17 @@ enum : int { TB_FULL = 0, TB_EMPTY = 12, TB_Q = 24, TB_S = 25, TB_W = 27, TB_PV 
 
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// ... and whether any of its threads' predicates holds.
+__device__ __forceinline__ bool named_any(int id, int threads, bool mine) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(mine)), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
 }
 
 template <int D, int RT>
@@ -664,32 +679,42 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
           for (int j = 0; j < CW; ++j)
             if (key >= ms.seen[n0 + j]) x[j] = -INFINITY;
         }
-        // ---- the tile's maxima: over the warp's keys, then over the four
-        // warps, lane j for row n0 + j; almost always none grew.
-        float hx = kNoMax, hy = kNoMax;
+        // ---- references: those of the tile before serve while no exponent
+        // rises above kRoom (weights up to 2^kRoom fit e4m3).  The first tile
+        // of a segment always takes new ones.
+        float top = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < CW; ++j) {
-          const float a = warp_max(x[j]), b = warp_max(x[j] + ev);
-          if (lane == j) {
-            hx = a;
-            hy = b;
-          }
+        for (int j = 0; j < CW; j += 4) {
+          const float4 m4 = *reinterpret_cast<const float4*>(&row[0][j]);
+          const float4 v4 = *reinterpret_cast<const float4*>(&row[1][j]);
+          top = fmaxf(top, fmaxf(fmaxf(x[j] - m4.x, x[j + 1] - m4.y), fmaxf(x[j + 2] - m4.z, x[j + 3] - m4.w)));
+          top = fmaxf(top, fmaxf(fmaxf(x[j] + ev - v4.x, x[j + 1] + ev - v4.y),
+                                 fmaxf(x[j + 2] + ev - v4.z, x[j + 3] + ev - v4.w)));
         }
-        if (lane < CW) {
-          ms.wm[buf][quarter][n0 + lane] = hx;
-          ms.wv[buf][quarter][n0 + lane] = hy;
-        }
-        named_sync(1 + wg, 128);
-        if (lane < CW) {
+        if (named_any(1 + wg, 128, top > kRoom)) {
+          // The tile's maxima: over the warp's keys, then over the four warps,
+          // lane j for row n0 + j.
+          float hx = kNoMax, hy = kNoMax;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            hx = fmaxf(hx, ms.wm[buf][w][n0 + lane]);
-            hy = fmaxf(hy, ms.wv[buf][w][n0 + lane]);
+          for (int j = 0; j < CW; ++j) {
+            const float a = warp_max(x[j]), b = warp_max(x[j] + ev);
+            if (lane == j) {
+              hx = a;
+              hy = b;
+            }
           }
-        }
-        if (__any_sync(0xffffffffu, hx > m || hy > mv)) {   // alike in the four warps
-          const float mn = fmaxf(hx, m), vn = fmaxf(hy, mv);
           if (lane < CW) {
+            ms.wm[buf][quarter][n0 + lane] = hx;
+            ms.wv[buf][quarter][n0 + lane] = hy;
+          }
+          named_sync(1 + wg, 128);
+          float mn = m, vn = mv;
+          if (lane < CW) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              mn = fmaxf(mn, ms.wm[buf][w][n0 + lane]);
+              vn = fmaxf(vn, ms.wv[buf][w][n0 + lane]);
+            }
             row[0][lane] = mn;
             row[1][lane] = vn - kTop;
             row[2][lane] = ex2(m - mn);
