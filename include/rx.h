@@ -326,9 +326,10 @@ rx_status rx_attend_streams_quant(rx_cache_t cache, int layer, const rx_quant_st
  * tokens -1, new_len[b] = tail_len[b].  T = 0 samples one token from p[b][0].
  * new_len[b] = tail_len[b] + 1 + a: the keys to keep when tail_len[b] counts
  * those before the step, which appended the last token and the drafts.
- * Products, differences and sums are taken in 64 bits, in a fixed order.
+ * Products are taken in 64 bits, differences and sums to 46 bits or more, in
+ * a fixed order.
  * p: [B][T+1][V], q: [B][T][V] or NULL, both of type prob_type; draft: int32
- * [B][T]; u: fp32 [B][T], r: fp32 [B], all in [0, 1); n_draft: int32 [B] or
+ * [B][T]; u: fp32 [B][T], r: fp32 [B], all in [0, 1) (r is clamped to it); n_draft: int32 [B] or
  * NULL (T), clamped to T; tail_len, new_len: int32 [B] or NULL (new_len may
  * be tail_len); tokens: int32 [B][T+1]; n_accept: int32 [B].  All DEVICE
  * memory.  V <= 2^28.  Errors: RX_ERR_ARG, RX_ERR_CUDA. */

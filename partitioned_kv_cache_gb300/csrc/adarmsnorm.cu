@@ -36,16 +36,6 @@ __device__ __forceinline__ void unpack8(const uint4& v, float* f) {
   }
 }
 
-// SM count of device `dev`, queried once per device.
-cudaError_t device_sm_count(int dev, int* out) {
-  static std::atomic<int> cache[64];
-  const bool cached = dev >= 0 && dev < 64;
-  if (cached && (*out = cache[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
-  const cudaError_t e = cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess && cached) cache[dev].store(*out, std::memory_order_relaxed);
-  return e;
-}
-
 // One warp per row (adarmsnorm_row).  MAXV = 16-byte vectors per lane kept
 // in registers (d <= 256 * MAXV); MAXV = 0 selects the two-pass path for
 // wider rows.
@@ -396,6 +386,15 @@ __global__ void __launch_bounds__(kGThreads, 1) ada_gamma_kernel(const __grid_co
 }
 
 }  // namespace
+
+cudaError_t device_sm_count(int dev, int* out) {
+  static std::atomic<int> cache[64];
+  const bool cached = dev >= 0 && dev < 64;
+  if (cached && (*out = cache[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  const cudaError_t e = cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && cached) cache[dev].store(*out, std::memory_order_relaxed);
+  return e;
+}
 
 cudaError_t launch_adarmsnorm(const __nv_bfloat16* x, const float* gamma, int rows, int d,
                               float eps, __nv_bfloat16* y, cudaStream_t s) {

@@ -45,6 +45,9 @@ constexpr int kMaxHidden = 2048;      // rx_ada_gamma: hidden width
 // Count of kernel launches made by the library (for benchmark accounting).
 void count_launch(int n = 1);
 
+// SM count of device `dev`, queried once per device.
+cudaError_t device_sm_count(int dev, int* out);
+
 // Whether kernels are launched with programmatic stream serialization (the
 // next kernel may start its prologue while the previous one drains).  On by
 // default; RX_PDL=0 in the environment turns it off.
