@@ -589,8 +589,8 @@ rx_status rx_tail_append_quant(void* k_tail, void* v_tail, unsigned char* k_exp,
     return fail(RX_ERR_ARG, "rx_tail_append_quant: sizes out of range");
   if (D != 64 && D != 128 && D != 256)
     return fail(RX_ERR_UNSUPPORTED, "rx_tail_append_quant: head dim %d not in {64, 128, 256}", D);
-  if (static_cast<long long>(B) * T > (1LL << 32) / Hkv)   // also keeps the grid below 2^31 blocks
-    return fail(RX_ERR_ARG, "rx_tail_append_quant: B*T*Hkv above 2^32");
+  if (static_cast<long long>(B) * T > (1LL << 31) / Hkv)   // also keeps the grid below 2^31 blocks
+    return fail(RX_ERR_ARG, "rx_tail_append_quant: B*T*Hkv above 2^31");
   if (B == 0) return RX_OK;
   if (!k_tail || !v_tail || !k_exp || !v_exp || !tail_len || !k_new || !v_new)
     return fail(RX_ERR_ARG, "rx_tail_append_quant: null pointer");

@@ -143,13 +143,42 @@ def _shape(t: Optional[torch.Tensor], shape, name: str) -> None:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
-def _one_device(*tensors: Optional[torch.Tensor]) -> None:
-    """Refuse tensors that are not all on the current device, where the
-    library launches."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != cur:
-            raise ValueError("every tensor must be on the current device (cuda:%d), got %s" % (cur, t.device))
+def _addresses(dev: int, *specs) -> list:
+    """The addresses of tensors (or None) that the library will take to be
+    contiguous, of these types and shapes, on the current device `dev`:
+    (tensor, dtype, shape, name) each.  Anything else is refused, shapes
+    first.  (One test for the good case: a call of the language streams' entry
+    points is short beside a check for each property.)"""
+    out = []
+    for t, dtype, shape, _ in specs:
+        if t is None:
+            out.append(None)
+        elif t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev:
+            out.append(t.data_ptr())
+        else:
+            break
+    else:
+        return out
+    for t, _, shape, name in specs:
+        _shape(t, shape, name)
+    for t, dtype, _, name in specs:
+        _ptr(t, dtype, name)
+    for t, _, _, name in specs:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("%s must be on the current device (cuda:%d), got %s" % (name, dev, t.device))
+    raise ValueError("tensors changed while they were checked")
+
+
+def _here(stream) -> Tuple[int, int]:
+    """The current device, or -2 without one, and the address of `stream` (or
+    of that device's current stream)."""
+    try:
+        dev = torch.cuda.current_device()
+    except (RuntimeError, AssertionError):   # no device: every tensor is refused
+        dev = -2
+    if stream is not None:
+        return dev, stream.cuda_stream
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else 0
 
 
 def _norm_jobs(norms) -> Tuple[Optional[ctypes.Array], int]:
@@ -360,23 +389,16 @@ class Cache:
         if q.dim() != 4:
             raise ValueError("q must have shape [B][T][Hq][D]")
         B, T = q.shape[:2]
-        _shape(q, (B, T, c.Hq, c.D), "q")
-        _shape(k_tail, (B, c.tail_cap, c.Hkv, c.D), "k_tail")
-        _shape(v_tail, k_tail.shape, "v_tail")
-        _shape(k_exp, k_tail.shape[:3], "k_exp")
-        _shape(v_exp, k_tail.shape[:3], "v_exp")
-        _shape(tail_len, (B,), "tail_len")
-        _shape(n_new, (B,), "n_new")
-        _shape(out, q.shape, "out")
+        dev, st = _here(stream)
         if out is None:
             out = torch.empty_like(q)
-        batch = RxQuantStreams(_ptr(q, name="q"), _ptr(k_tail, torch.float8_e4m3fn, "k_tail"),
-                               _ptr(v_tail, torch.float8_e4m3fn, "v_tail"), _ptr(k_exp, torch.uint8, "k_exp"),
-                               _ptr(v_exp, torch.uint8, "v_exp"), _ptr(tail_len, torch.int32, "tail_len"),
-                               _ptr(n_new, torch.int32, "n_new"), _ptr(out, name="out"), B, T)
-        _one_device(q, k_tail, v_tail, k_exp, v_exp, tail_len, n_new, out)
-        _check(_lib.rx_attend_streams_quant(self._h, layer, ctypes.byref(batch), _stream(stream)),
-               "rx_attend_streams_quant")
+        e4m3, u8, i32, bf16 = torch.float8_e4m3fn, torch.uint8, torch.int32, torch.bfloat16
+        rows, tail, exps, each = (B, T, c.Hq, c.D), (B, c.tail_cap, c.Hkv, c.D), (B, c.tail_cap, c.Hkv), (B,)
+        ptrs = _addresses(dev, (q, bf16, rows, "q"), (k_tail, e4m3, tail, "k_tail"), (v_tail, e4m3, tail, "v_tail"),
+                          (k_exp, u8, exps, "k_exp"), (v_exp, u8, exps, "v_exp"), (tail_len, i32, each, "tail_len"),
+                          (n_new, i32, each, "n_new"), (out, bf16, rows, "out"))
+        batch = RxQuantStreams(*ptrs, B, T)
+        _check(_lib.rx_attend_streams_quant(self._h, layer, ctypes.byref(batch), st), "rx_attend_streams_quant")
         return out
 
     def get_state(self, stream=None) -> Tuple[int, int, int]:
@@ -521,25 +543,20 @@ def tail_append_quant(k_tail: torch.Tensor, v_tail: torch.Tensor, k_exp: torch.T
     is; new_len, if given, receives the lengths after the append."""
     if k_tail.dim() != 4 or k_new.dim() != 4:
         raise ValueError("tails must have shape [B][tail_cap][Hkv][D] and new tokens [B][T][Hkv][D]")
-    B, tail_cap, Hkv, D = k_tail.shape
+    tail = B, tail_cap, Hkv, D = tuple(k_tail.shape)
     T = k_new.shape[1]
-    _shape(v_tail, k_tail.shape, "v_tail")
-    _shape(k_exp, k_tail.shape[:3], "k_exp")
-    _shape(v_exp, k_tail.shape[:3], "v_exp")
-    _shape(tail_len, (B,), "tail_len")
-    _shape(k_new, (B, T, Hkv, D), "k_new")
-    _shape(v_new, (B, T, Hkv, D), "v_new")
-    _shape(n_new, (B,), "n_new")
-    _shape(new_len, (B,), "new_len")
+    exps, new, each = (B, tail_cap, Hkv), (B, T, Hkv, D), (B,)
+    e4m3, u8, i32, bf16 = torch.float8_e4m3fn, torch.uint8, torch.int32, torch.bfloat16
     if overflow is not None and overflow.numel() < 1:
         raise ValueError("overflow must hold one int32")
-    args = (_ptr(k_tail, torch.float8_e4m3fn, "k_tail"), _ptr(v_tail, torch.float8_e4m3fn, "v_tail"),
-            _ptr(k_exp, torch.uint8, "k_exp"), _ptr(v_exp, torch.uint8, "v_exp"),
-            _ptr(tail_len, torch.int32, "tail_len"), _ptr(new_len, torch.int32, "new_len"),
-            _ptr(k_new, name="k_new"), _ptr(v_new, name="v_new"), _ptr(n_new, torch.int32, "n_new"), B, T,
-            tail_cap, Hkv, D, _ptr(overflow, torch.int32, "overflow"))
-    _one_device(k_tail, v_tail, k_exp, v_exp, tail_len, new_len, k_new, v_new, n_new, overflow)
-    _check(_lib.rx_tail_append_quant(*args, _stream(stream)), "rx_tail_append_quant")
+    dev, st = _here(stream)
+    kt, vt, ke, ve, tl, nl, kn, vn, nn, ov = _addresses(
+        dev, (k_tail, e4m3, tail, "k_tail"), (v_tail, e4m3, tail, "v_tail"), (k_exp, u8, exps, "k_exp"),
+        (v_exp, u8, exps, "v_exp"), (tail_len, i32, each, "tail_len"), (new_len, i32, each, "new_len"),
+        (k_new, bf16, new, "k_new"), (v_new, bf16, new, "v_new"), (n_new, i32, each, "n_new"),
+        (overflow, i32, None if overflow is None else overflow.shape, "overflow"))
+    _check(_lib.rx_tail_append_quant(kt, vt, ke, ve, tl, nl, kn, vn, nn, B, T, tail_cap, Hkv, D, ov, st),
+           "rx_tail_append_quant")
 
 
 _PROB_TYPES = {torch.float32: 0, torch.bfloat16: 1}
@@ -562,23 +579,18 @@ def verify_drafts(p: torch.Tensor, q: Optional[torch.Tensor], draft: torch.Tenso
         raise TypeError("p must be float32 or bfloat16, got %s" % p.dtype)
     B, T = draft.shape
     V = p.shape[2]
-    _shape(p, (B, T + 1, V), "p")
-    _shape(q, (B, T, V), "q")
-    _shape(u, (B, T), "u")
-    _shape(r, (B,), "r")
-    _shape(n_draft, (B,), "n_draft")
-    _shape(tail_len, (B,), "tail_len")
-    _shape(new_len, (B,), "new_len")
+    each, i32, f32 = (B,), torch.int32, torch.float32
     if new_len is not None and tail_len is None:
         raise ValueError("new_len needs tail_len")
-    tokens = torch.empty((B, T + 1), dtype=torch.int32, device=p.device)
-    n_accept = torch.empty((B,), dtype=torch.int32, device=p.device)
+    dev, st = _here(stream)
     if tail_len is not None and new_len is None:
         new_len = torch.empty_like(tail_len)
-    args = (_ptr(p, p.dtype, "p"), _ptr(q, p.dtype, "q"), _PROB_TYPES[p.dtype], _ptr(draft, torch.int32, "draft"),
-            _ptr(u, torch.float32, "u"), _ptr(r, torch.float32, "r"), _ptr(n_draft, torch.int32, "n_draft"), B, T, V,
-            _ptr(tail_len, torch.int32, "tail_len"), _ptr(tokens, torch.int32, "tokens"),
-            _ptr(n_accept, torch.int32, "n_accept"), _ptr(new_len, torch.int32, "new_len"))
-    _one_device(p, q, draft, u, r, n_draft, tail_len, tokens, n_accept, new_len)
-    _check(_lib.rx_verify_drafts(*args, _stream(stream)), "rx_verify_drafts")
+    pp, qp, dp, up, rp, np_, tl, nl = _addresses(
+        dev, (p, p.dtype, (B, T + 1, V), "p"), (q, p.dtype, (B, T, V), "q"), (draft, i32, (B, T), "draft"),
+        (u, f32, (B, T), "u"), (r, f32, each, "r"), (n_draft, i32, each, "n_draft"), (tail_len, i32, each, "tail_len"),
+        (new_len, i32, each, "new_len"))
+    tokens = torch.empty((B, T + 1), dtype=i32, device=p.device)
+    n_accept = torch.empty(each, dtype=i32, device=p.device)
+    args = (pp, qp, _PROB_TYPES[p.dtype], dp, up, rp, np_, B, T, V, tl, tokens.data_ptr(), n_accept.data_ptr(), nl, st)
+    _check(_lib.rx_verify_drafts(*args), "rx_verify_drafts")
     return tokens, n_accept, new_len
