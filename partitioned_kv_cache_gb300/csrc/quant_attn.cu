@@ -279,15 +279,17 @@ struct Walk {
 
 template <int D, int RT>
 struct TailLayout {
-  // Up to 32 rows the e4m3 terms of Q and W are further rows of one operand,
-  // so that a product reads the K or V codes from shared memory once for all
-  // terms (128 x 32 codes take as long to read as 64 columns to multiply); at
-  // 64 rows they are separate products into one accumulator.
+  // The e4m3 terms of W, and up to 32 rows those of Q, are further rows of one
+  // operand.  These products are bound by their operands' way out of shared
+  // memory, 64 bytes a clock: one of 128 x 32 codes with N rows takes about
+  // (4096 + 32 N) / 64 clocks (measured: 96 at N = 64, 72 at N = 16), so the
+  // codes should be read once for all terms.  (At 64 rows, Q's terms are two
+  // products into one accumulator: TMEM holds no more than that.)
   static constexpr bool STACK = RT <= 32;
-  static constexpr int NQ = STACK ? 2 * RT : RT;                      // MMA N of the scores
-  static constexpr int NW = STACK ? 4 * RT : RT;                      // ... of the output (a term's place is spare)
-  static constexpr int QT = STACK ? 1 : 2;                            // products per K step
-  static constexpr int WT = STACK ? 1 : kTerms;
+  static constexpr int NQ = STACK ? 2 * RT : RT;          // MMA N of the scores
+  static constexpr int QT = STACK ? 1 : 2;                // products per K step
+  static constexpr int NW = RT == 64 ? 3 * RT : 4 * RT;   // MMA N of the output (up to 32 rows a term's place is spare)
+  static constexpr int WROW = RT == 64 ? RT : NW;         // bytes of a key's stored weights in one block
   static constexpr int CW = RT < 16 ? RT : 16;            // rows of one softmax warpgroup
   static constexpr int WG = RT / CW;                      // softmax warpgroups
   static constexpr int THREADS = 64 + 128 * WG;
@@ -302,8 +304,8 @@ struct TailLayout {
   static constexpr int CTAS = D == 256 || RT == 64 ? 1 : 2;   // per SM
   static constexpr int Q_BLOCK = NQ * ROW;                // one column block of one product's Q
   static constexpr int Q_BYTES = QT * KB * Q_BLOCK;
-  static constexpr int W_BLOCK = NW * kTK;                // one product's weights of a tile: [key][NW]
-  static constexpr int W_BYTES = WT * W_BLOCK;            // ... of all its products; two tiles are kept
+  static constexpr int W_BLOCK = WROW * kTK;              // [key][WROW]: all terms, or at 64 rows one
+  static constexpr int W_BYTES = NW * kTK;                // a tile's weights; two tiles are kept
   static constexpr int MISC = RT == 64 ? 9728 : 5632;
   static constexpr int BUDGET = (CTAS == 1 ? 227 : 113) * 1024 - 1024;   // less the alignment slack
   static constexpr int NS_FIT = (BUDGET - Q_BYTES - 2 * W_BYTES - MISC) / TILE;
@@ -331,10 +333,12 @@ struct TailMisc {
   int pad0;
   long long left;
   long long scan[32];
-  float qs[RT];                          // 2^e of the query rows
+  float qs[RT];                          // 2^e of the query rows, times log2(e) / sqrt(D)
   int seen[RT];                          // tail keys each row sees
   float wm[2][4][RT], wv[2][4][RT];      // the warps' maxima, for even and odd tiles
-  float row[RT / 4][4][RT < 16 ? RT : 16];   // per warp: m, M - kTop, factors of l and O
+  // Per softmax warp, for its warpgroup's rows: m, d = m - M + kTop, and the
+  // last factors of l and O.
+  float row[RT < 16 ? 4 : RT / 4][4][RT < 16 ? RT : 16];
 };
 
 enum : int { TB_FULL = 0, TB_EMPTY = 12, TB_Q = 24, TB_S = 25, TB_W = 27, TB_PV = 29, TB_DRAIN = 31 };
@@ -544,17 +548,16 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
           // 8 * ROW apart.  At D = 64 the product's upper 64 rows read the
           // bytes one tile further on and are not used.
           const uint64_t vd = sdesc_rows<ROW>(here(sRing + slot * L::TILE), L::BLOCK);
-          // B: weights, rows n along the stored bytes of a key, likewise.
-          const uint64_t wd = sdesc_rows<L::NW>(here(sW + (tile & 1) * L::W_BYTES), 16);
+          // B: weights, rows n along the stored bytes of a key, likewise (at
+          // 64 rows, three blocks of them).
+          const uint64_t wd = sdesc_rows<L::WROW>(here(sW + (tile & 1) * L::W_BYTES), L::W_BLOCK);
           const uint32_t acc = here(tmem + L::TM_O);
 #pragma unroll
           for (int ob = 0; ob < L::OB; ++ob)
 #pragma unroll
-            for (int term = 0; term < L::WT; ++term)
-#pragma unroll
-              for (int kk = 0; kk < kTK / 32; ++kk)
-                umma_e4m3(acc + ob * L::NW, desc_step(vd, ob * L::BLOCK + kk * 32 * ROW),
-                          desc_step(wd, term * L::W_BLOCK + kk * 32 * L::NW), kIdescO, (i | term | kk) ? 1u : 0u);
+            for (int kk = 0; kk < kTK / 32; ++kk)
+              umma_e4m3(acc + ob * L::NW, desc_step(vd, ob * L::BLOCK + kk * 32 * ROW),
+                        desc_step(wd, kk * 32 * L::WROW), kIdescO, (i | kk) ? 1u : 0u);
           umma_commit(BAR(TB_EMPTY + slot));
           umma_commit(BAR(TB_PV + (tile & 1)));
           ++item;
@@ -583,7 +586,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     float (&row)[4][CW] = ms.row[st >> 5];
     unsigned int item0 = 0, tile = 0;
-    if (L::STACK)   // the spare rows of W stay zero
+    if (L::NW > kTerms * RT)   // the spare rows of W stay zero
       for (int i = st * 16; i < 2 * L::W_BYTES; i += 128 * L::WG * 16) st_shared_v4(sW + i, 0u, 0u, 0u, 0u);
     while (wk.next(p, RT)) {
       const int nt = wk.ntiles;
@@ -620,7 +623,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
         top = __reduce_max_sync(0xffffffffu, top);
         const int ex = max(static_cast<int>(top >> 7) - 8 + ((top & 0x7Fu) > 96u ? 1 : 0), 1);
         const bool poison = (top >> 7) == 255u;
-        if (lane == 0) ms.qs[n] = poison ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(ex) << 23);
+        if (lane == 0) ms.qs[n] = poison ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(ex) << 23) * p.scale_log2;
         const float up = __uint_as_float(static_cast<uint32_t>(254 - min(ex, 253)) << 23);
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) {
@@ -646,58 +649,66 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
 #pragma unroll
       for (int j = 0; j < CW; ++j) l[j] = 0.f;
       float m = kNoMax, mv = kNoMax;   // lane j < CW: the running maxima of row n0 + j
-      if (lane < CW) row[0][lane] = row[1][lane] = kNoMax;
+      float dmax = 0.f;                // the largest d
+      if (lane < CW) {
+        row[0][lane] = kNoMax;
+        row[1][lane] = 0.f;
+      }
       __syncwarp();
       for (int i = 0; i < nt; ++i, ++tile) {
         const int buf = tile & 1;
         const int key = (wk.tile0 + i) * kTK + key_in_tile;
-        const float ks = exp_scale(kb) * p.scale_log2;
-        const float ev = vb == 255u ? __uint_as_float(0x7FC00000u) : static_cast<float>(vb) - 127.f;
+        // A NaN value poisons the scores of the rows that see it, as a NaN key
+        // does: the whole row is NaN either way, and ev stays finite.
+        const float ks = exp_scale(vb == 255u ? 255u : kb);
+        const float ev = static_cast<float>(vb) - 127.f;
         load_exps(i + 1 < nt ? key + kTK : kmax);   // the next tile's, a tile ahead
         const bool masked = (wk.tile0 + i + 1) * kTK > kmin;
         mbar_wait(BAR(TB_S + buf), (tile >> 1) & 1, abort_flag);
         __syncwarp();
         tc_fence_after();
-        float x[CW];
-        tmem_ld_cols(tmem + buf * L::NQ + n0 + lane_off, x);
-        if constexpr (L::STACK) {
-          float lo[CW];
-          tmem_ld_cols(tmem + buf * L::NQ + RT + n0 + lane_off, lo);
+        // x_n - c_n for this key and the warpgroup's rows; c: an array in shared memory.
+        auto scores_less = [&](float (&x)[CW], const float* c) {
+          tmem_ld_cols(tmem + buf * L::NQ + n0 + lane_off, x);
+          if constexpr (L::STACK) {
+            float lo[CW];
+            tmem_ld_cols(tmem + buf * L::NQ + RT + n0 + lane_off, lo);
 #pragma unroll
-          for (int j = 0; j < CW; ++j) x[j] += lo[j];
-        }
+            for (int j = 0; j < CW; ++j) x[j] += lo[j];
+          }
 #pragma unroll
-        for (int j = 0; j < CW; j += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&ms.qs[n0 + j]);
-          x[j] *= ks * f.x;
-          x[j + 1] *= ks * f.y;
-          x[j + 2] *= ks * f.z;
-          x[j + 3] *= ks * f.w;
-        }
-        if (masked) {
+          for (int j = 0; j < CW; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&ms.qs[n0 + j]);
+            const float4 g = c ? *reinterpret_cast<const float4*>(c + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[j] = fmaf(x[j], ks * f.x, -g.x);
+            x[j + 1] = fmaf(x[j + 1], ks * f.y, -g.y);
+            x[j + 2] = fmaf(x[j + 2], ks * f.z, -g.z);
+            x[j + 3] = fmaf(x[j + 3], ks * f.w, -g.w);
+          }
+          if (masked) {
 #pragma unroll
-          for (int j = 0; j < CW; ++j)
-            if (key >= ms.seen[n0 + j]) x[j] = -INFINITY;
-        }
+            for (int j = 0; j < CW; ++j)
+              if (key >= ms.seen[n0 + j]) x[j] = -INFINITY;
+          }
+        };
         // ---- references: those of the tile before serve while no exponent
-        // rises above kRoom (weights up to 2^kRoom fit e4m3).  The first tile
-        // of a segment always takes new ones.
-        float top = -INFINITY;
+        // can rise above kRoom (weights up to 2^kRoom fit e4m3): the largest
+        // x - m of the thread's key, its value's exponent and the largest
+        // row offset d bound them all.  The first tile of a segment always
+        // takes new ones.
+        float u[CW];
+        scores_less(u, row[0]);
+        float top = u[0];
 #pragma unroll
-        for (int j = 0; j < CW; j += 4) {
-          const float4 m4 = *reinterpret_cast<const float4*>(&row[0][j]);
-          const float4 v4 = *reinterpret_cast<const float4*>(&row[1][j]);
-          top = fmaxf(top, fmaxf(fmaxf(x[j] - m4.x, x[j + 1] - m4.y), fmaxf(x[j + 2] - m4.z, x[j + 3] - m4.w)));
-          top = fmaxf(top, fmaxf(fmaxf(x[j] + ev - v4.x, x[j + 1] + ev - v4.y),
-                                 fmaxf(x[j + 2] + ev - v4.z, x[j + 3] + ev - v4.w)));
-        }
-        if (named_any(1 + wg, 128, top > kRoom)) {
+        for (int j = 1; j < CW; ++j) top = fmaxf(top, u[j]);
+        if (named_any(1 + wg, 128, top > kRoom || top + (ev + dmax) > kRoom)) {
           // The tile's maxima: over the warp's keys, then over the four warps,
           // lane j for row n0 + j.
+          scores_less(u, nullptr);
           float hx = kNoMax, hy = kNoMax;
 #pragma unroll
           for (int j = 0; j < CW; ++j) {
-            const float a = warp_max(x[j]), b = warp_max(x[j] + ev);
+            const float a = warp_max(u[j]), b = warp_max(u[j] + ev);
             if (lane == j) {
               hx = a;
               hy = b;
@@ -715,21 +726,30 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
               mn = fmaxf(mn, ms.wm[buf][w][n0 + lane]);
               vn = fmaxf(vn, ms.wv[buf][w][n0 + lane]);
             }
+          }
+          const float d = mn - vn + kTop;   // a row without a key so far: kTop
+          if (lane < CW) {
             row[0][lane] = mn;
-            row[1][lane] = vn - kTop;
+            row[1][lane] = d;
             row[2][lane] = ex2(m - mn);
             row[3][lane] = ex2(mv - vn);
           }
+          dmax = warp_max(lane < CW ? d : -INFINITY);
           m = mn;
           mv = vn;
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < CW; j += 4) {
             const float4 f = *reinterpret_cast<const float4*>(&row[2][j]);
+            const float4 g = *reinterpret_cast<const float4*>(&row[0][j]);
             l[j] *= f.x;
             l[j + 1] *= f.y;
             l[j + 2] *= f.z;
             l[j + 3] *= f.w;
+            u[j] -= g.x;
+            u[j + 1] -= g.y;
+            u[j + 2] -= g.z;
+            u[j + 3] -= g.w;
           }
           if (i > 0) {
             // O holds the tiles before: wait for their last product, then rescale.
@@ -737,7 +757,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
             __syncwarp();
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < L::OB * (L::STACK ? kTerms : 1); ++c) {
+            for (int c = 0; c < L::OB * kTerms; ++c) {
               const uint32_t at = tmem + L::TM_O + (c % L::OB) * L::NW + (c / L::OB) * RT + n0 + lane_off;
               float o[CW];
               tmem_ld_cols(at, o);
@@ -755,16 +775,14 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
         uint32_t codes[kTerms][CW / 4];
 #pragma unroll
         for (int j = 0; j < CW; j += 4) {
-          const float4 m4 = *reinterpret_cast<const float4*>(&row[0][j]);
-          const float4 v4 = *reinterpret_cast<const float4*>(&row[1][j]);
-          const float mj[4] = {m4.x, m4.y, m4.z, m4.w}, vj[4] = {v4.x, v4.y, v4.z, v4.w};
+          const float4 d4 = *reinterpret_cast<const float4*>(&row[1][j]);
+          const float dj[4] = {d4.x, d4.y, d4.z, d4.w};
           uint32_t hi[4], mid[4];
           float lo[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            l[j + e] += ex2(x[j + e] - mj[e]);
-            // (a masked score is -inf: its weight is zero even where ev is NaN)
-            const float w = x[j + e] == -INFINITY ? 0.f : ex2(x[j + e] + ev - vj[e]);
+            l[j + e] += ex2(u[j + e]);
+            const float w = ex2(u[j + e] + ev + dj[e]);
             // Four leading bits at a time: exact remainders, and terms that
             // e4m3 holds exactly (or, below its normal range, to 2^-10).
             hi[e] = __float_as_uint(w) & 0xFFF00000u;
@@ -782,8 +800,8 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
         const uint32_t wb = sW + buf * L::W_BYTES;
 #pragma unroll
         for (int term = 0; term < kTerms; ++term) {
-          const uint32_t at = wb + (L::STACK ? swizzled<L::NW>(key_in_tile, term * RT + n0)
-                                             : term * L::W_BLOCK + swizzled<L::NW>(key_in_tile, n0));
+          const uint32_t at = wb + (L::WROW == L::NW ? swizzled<L::WROW>(key_in_tile, term * RT + n0)
+                                                     : term * L::W_BLOCK + swizzled<L::WROW>(key_in_tile, n0));
           if constexpr (CW == 16)
             st_shared_v4(at, codes[term][0], codes[term][1], codes[term][2], codes[term][3]);
           else
@@ -832,14 +850,12 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
           float o[CW];
           const uint32_t at = tmem + L::TM_O + ob * L::NW + n0 + lane_off;
           tmem_ld_cols(at, o);
-          if constexpr (L::STACK) {
 #pragma unroll
-            for (int term = 1; term < kTerms; ++term) {
-              float t[CW];
-              tmem_ld_cols(at + term * RT, t);
+          for (int term = 1; term < kTerms; ++term) {
+            float t[CW];
+            tmem_ld_cols(at + term * RT, t);
 #pragma unroll
-              for (int j = 0; j < CW; ++j) o[j] += t[j];
-            }
+            for (int j = 0; j < CW; ++j) o[j] += t[j];
           }
           float* dst = p.o + slot_row * D + ob * 128 + key_in_tile;
 #pragma unroll
