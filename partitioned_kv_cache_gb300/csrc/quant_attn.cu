@@ -197,7 +197,7 @@ struct TailParams {
   const uint8_t* v_exp;
   const int* tail_len;
   const int* n_new;
-  unsigned long long* head;   // [0] tiles of all streams, [1 + b] tiles before stream b
+  int2* ctas;                 // [unit] the first and the last CTA with a tile of it
   float2* ml;                 // (m, l) [slot][RT]
   float* o;                   // [slot][RT][D], relative to m
   int* err;
@@ -233,9 +233,6 @@ __device__ __forceinline__ long long head_tiles(const StreamLen& s, int row_tile
 // Active CTAs and the first tile of each: CTA c of A takes [c*C/A, (c+1)*C/A).
 __device__ __forceinline__ unsigned long long first_tile(unsigned long long c, unsigned long long C, unsigned long long A) {
   return c * C / A;
-}
-__device__ __forceinline__ unsigned long long cta_of_tile(unsigned long long x, unsigned long long C, unsigned long long A) {
-  return ((x + 1) * A - 1) / C;
 }
 
 // A CTA's run of tiles, unit by unit.  Every role walks it for itself.
@@ -434,16 +431,13 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
     const unsigned long long A = min(static_cast<unsigned long long>(gridDim.x), C);
     const bool active = blockIdx.x < A;
     const long long first = active ? static_cast<long long>(first_tile(blockIdx.x, C, A)) : 0;
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0)
       ms.left = active ? static_cast<long long>(first_tile(blockIdx.x + 1ull, C, A)) - first : 0;
-      if (blockIdx.x == 0) p.head[0] = C;
-    }
     long long carry = 0;
     for (int b0 = 0; b0 < p.B; b0 += THREADS) {
       const int b = b0 + threadIdx.x;
       if (p.B > THREADS) carry = scan_round(b, carry, mine);
       if (b < p.B) {
-        if (blockIdx.x == 0) p.head[1 + b] = static_cast<unsigned long long>(mine[0]);
         if (active && first >= mine[0] && first < mine[0] + mine[1]) {
           ms.b0 = b;
           long long off = first - mine[0];
@@ -827,6 +821,10 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
       // ---- the segment's partial: O relative to m, and (m, l)
       const long long unit = (static_cast<long long>(wk.b) * p.Hkv + wk.g) * p.row_tiles + wk.rt;
       const long long slot_row = (unit + blockIdx.x) * RT + n0;
+      if (st == 0) {
+        if (wk.tile0 == 0) p.ctas[unit].x = blockIdx.x;
+        if (wk.tile0 + nt == unit_tiles(wk.s, wk.rt, RT, p.G)) p.ctas[unit].y = blockIdx.x;
+      }
       named_sync(1 + wg, 128);   // wm is free
 #pragma unroll
       for (int j = 0; j < CW; ++j) {
@@ -877,70 +875,63 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
 // ---------------------------------------------------------------- the merge
 // out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over a row's partials:
 // those of the shared store (O_s / l_s, pieces of eight fp32 values
-// [D/8][128 rows]) and those of its tail.  kRowWarps warps share a row: warp w
-// takes the partials w, w + kRowWarps, ..., kMergeChunk of them in flight, and
-// the warps' sums meet in shared memory.
+// [D/8][128 rows]) and those of its tail.  WPR warps share a row: warp w takes
+// the partials w, w + WPR, ..., kMergeChunk of them in flight, and the warps'
+// sums meet in shared memory.  Bound by the latency of dependent loads: the
+// row's CTAs, then its partials.
 struct MergeParams {
   const float* shared_o;      // [unit][split][D/8][128][8]
   const float2* shared_ml;    // [unit][split][128]
-  const unsigned long long* head;
+  const int2* ctas;
   const float2* tail_ml;
   const float* tail_o;
   const int* tail_len;
   const int* n_new;
   __nv_bfloat16* out;
-  int B, T, Hq, Hkv, G, tail_cap, row_tiles, RT;
-  int splits, m_tiles, tail_ctas;
+  int rows;                   // B * T * Hq
+  int T, Hq, Hkv, G, tail_cap, row_tiles, RT;
+  int splits, m_tiles;
 };
 
-constexpr int kRowWarps = 4;
-constexpr int kMergeRows = 2;      // rows of one CTA
+constexpr int kMergeWarps = 8;
 constexpr int kMergeChunk = 8;
 
-template <int D>
-__global__ void __launch_bounds__(kMergeRows * kRowWarps * 32) stream_merge_kernel(const MergeParams p) {
+template <int D, int WPR>
+__global__ void __launch_bounds__(kMergeWarps * 32) stream_merge_kernel(const MergeParams p) {
   constexpr int E = D / 32;   // elements per lane
-  __shared__ float sm[kMergeRows][kRowWarps], sl[kMergeRows][kRowWarps], so[kMergeRows][kRowWarps][D];
+  constexpr int ROWS = kMergeWarps / WPR;
+  __shared__ float sm[ROWS][WPR], sl[ROWS][WPR], so[ROWS][WPR][WPR > 1 ? D : 1];
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int mine = warp / kRowWarps, part = warp % kRowWarps;
-  const long long rr = static_cast<long long>(blockIdx.x) * kMergeRows + mine;   // (b * T + t) * Hq + h
-  bool live = rr < static_cast<long long>(p.B) * p.T * p.Hq;
+  const int mine = warp / WPR, part = warp % WPR;
+  const int rr = blockIdx.x * ROWS + mine;   // (b * T + t) * Hq + h
+  bool live = rr < p.rows;
   float M = -INFINITY, L = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   if (live) {
-    const int h = static_cast<int>(rr % p.Hq);
-    const long long bt = rr / p.Hq;
-    const int t = static_cast<int>(bt % p.T), b = static_cast<int>(bt / p.T);
-    const int g = h / p.G, gh = h % p.G;
-    const unsigned long long C = p.head[0];
-    unsigned long long first = p.head[1 + b];
+    const int bt = rr / p.Hq, h = rr - bt * p.Hq;
+    const int b = bt / p.T, t = bt - b * p.T;
+    const int g = h / p.G, gh = h - g * p.G;
+    const int r = t * p.G + gh, rt = r / p.RT;
+    const int unit = (b * p.Hkv + g) * p.row_tiles + rt;
+    const int2 ctas = __ldcg(p.ctas + unit);   // (read beside the lengths; used only where the unit has tiles)
     const StreamLen s = stream_len(p.tail_len, p.n_new, b, p.T, p.tail_cap);
     live = t < s.n;
-    const long long row = bt * p.G + gh;   // row of the shared segment
-    const long long su = (g * static_cast<long long>(p.m_tiles) + (row >> 7)) * p.splits;
-    const int si = static_cast<int>(row & 127);
-    const int r = t * p.G + gh, rt = r / p.RT;
     const int ut = live ? unit_tiles(s, rt, p.RT, p.G) : 0;
-    long long tail_row = 0;   // the first tail partial's row
-    int tails = 0;
-    if (ut > 0) {
-      const unsigned long long A = min(static_cast<unsigned long long>(p.tail_ctas), C);
-      if (g > 0) first += g * head_tiles(s, p.row_tiles, p.RT, p.G);
-      for (int k = 0; k < rt; ++k) first += unit_tiles(s, k, p.RT, p.G);
-      const long long c0 = static_cast<long long>(cta_of_tile(first, C, A));
-      tails = static_cast<int>(static_cast<long long>(cta_of_tile(first + ut - 1, C, A)) - c0) + 1;
-      tail_row = ((static_cast<long long>(b) * p.Hkv + g) * p.row_tiles + rt + c0) * p.RT + r % p.RT;
-    }
+    const int tails = ut > 0 ? ctas.y - ctas.x + 1 : 0;
+    const long long tail_row = (static_cast<long long>(unit) + ctas.x) * p.RT + r % p.RT;   // the first tail partial's row
+    const int row = bt * p.G + gh;             // row of the shared segment
+    const long long su = (g * static_cast<long long>(p.m_tiles) + (row >> 7)) * p.splits;
+    const int si = row & 127;
     const int count = live ? p.splits + tails : 0;
-    for (int i0 = part; i0 < count; i0 += kRowWarps * kMergeChunk) {
+    for (int i0 = part; i0 < count; i0 += WPR * kMergeChunk) {
       float2 ml[kMergeChunk];
       float v[kMergeChunk][E];
 #pragma unroll
       for (int u = 0; u < kMergeChunk; ++u) {
-        const int i = i0 + u * kRowWarps;
+        const int i = i0 + u * WPR;
         ml[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
         for (int e = 0; e < E; ++e) v[u][e] = 0.f;
@@ -978,7 +969,7 @@ __global__ void __launch_bounds__(kMergeRows * kRowWarps * 32) stream_merge_kern
         // A sum without a maximum is zero, or NaN, which has to stay.
         const float f = ml[u].x == -INFINITY ? (ml[u].y == 0.f ? 0.f : 1.f) : exp2f(ml[u].x - Mn);
         const float wl = f * ml[u].y;
-        const float w = i0 + u * kRowWarps < p.splits ? wl : f;
+        const float w = i0 + u * WPR < p.splits ? wl : f;
         L += wl;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[u][e], acc[e]);
@@ -986,54 +977,61 @@ __global__ void __launch_bounds__(kMergeRows * kRowWarps * 32) stream_merge_kern
       M = Mn;
     }
   }
-  if (lane == 0) {
-    sm[mine][part] = M;
-    sl[mine][part] = L;
-  }
+  if constexpr (WPR == 1) {
+    if (!live) return;
+    const float inv = L == 0.f ? 0.f : 1.f / L;   // a row with no key at all gets zeros
+    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(p.out + static_cast<long long>(rr) * D + lane * E);
 #pragma unroll
-  for (int e = 0; e < E; ++e) so[mine][part][lane * E + e] = acc[e];
-  __syncthreads();
-  if (!live) return;
-  float Mt = -INFINITY, Lt = 0.f;
-#pragma unroll
-  for (int w = 0; w < kRowWarps; ++w) Mt = fmaxf(Mt, sm[mine][w]);
-  float f[kRowWarps];
-#pragma unroll
-  for (int w = 0; w < kRowWarps; ++w) {
-    f[w] = sm[mine][w] == -INFINITY ? 1.f : exp2f(sm[mine][w] - Mt);   // 1: zeros (or NaN)
-    Lt += f[w] * sl[mine][w];
-  }
-  const float inv = Lt == 0.f ? 0.f : 1.f / Lt;   // a row with no key at all gets zeros
-  // The row's D values over its kRowWarps * 32 threads.
-  const int d0 = (part * 32 + lane) * 2;
-  if (d0 < D) {
-    float x = 0.f, y = 0.f;
-#pragma unroll
-    for (int w = 0; w < kRowWarps; ++w) {
-      x = fmaf(f[w], so[mine][w][d0], x);
-      y = fmaf(f[w], so[mine][w][d0 + 1], y);
+    for (int e = 0; e < E; e += 2) dst[e / 2] = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+  } else {
+    if (lane == 0) {
+      sm[mine][part] = M;
+      sl[mine][part] = L;
     }
-    *reinterpret_cast<__nv_bfloat162*>(p.out + rr * D + d0) = __floats2bfloat162_rn(x * inv, y * inv);
+#pragma unroll
+    for (int e = 0; e < E; ++e) so[mine][part][lane * E + e] = acc[e];
+    __syncthreads();
+    if (!live) return;
+    float Mt = -INFINITY, Lt = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) Mt = fmaxf(Mt, sm[mine][w]);
+    float f[WPR];
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) {
+      f[w] = sm[mine][w] == -INFINITY ? 1.f : exp2f(sm[mine][w] - Mt);   // 1: zeros (or NaN)
+      Lt += f[w] * sl[mine][w];
+    }
+    const float inv = Lt == 0.f ? 0.f : 1.f / Lt;
+    // The row's D values over its WPR * 32 threads.
+    const int d0 = (part * 32 + lane) * 2;
+    if (d0 < D) {
+      float x = 0.f, y = 0.f;
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) {
+        x = fmaf(f[w], so[mine][w][d0], x);
+        y = fmaf(f[w], so[mine][w][d0 + 1], y);
+      }
+      *reinterpret_cast<__nv_bfloat162*>(p.out + static_cast<long long>(rr) * D + d0) = __floats2bfloat162_rn(x * inv, y * inv);
+    }
   }
 }
 
 // ------------------------------------------------------------------ launches
 template <int D, int RT>
-cudaError_t launch_tails(TailParams& p, int num_sms, int* ctas, cudaStream_t s) {
+cudaError_t launch_tails(TailParams& p, int num_sms, cudaStream_t s) {
   using L = TailLayout<D, RT>;
   const cudaError_t e = cudaFuncSetAttribute(stream_tail_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
   if (e != cudaSuccess) return e;
-  *ctas = num_sms * L::CTAS;
-  return launch_k(stream_tail_kernel<D, RT>, dim3(*ctas), dim3(L::THREADS), L::ALLOC, s, p);
+  return launch_k(stream_tail_kernel<D, RT>, dim3(num_sms * L::CTAS), dim3(L::THREADS), L::ALLOC, s, p);
 }
 
 template <int D>
-cudaError_t launch_tails_d(TailParams& p, int RT, int num_sms, int* ctas, cudaStream_t s) {
+cudaError_t launch_tails_d(TailParams& p, int RT, int num_sms, cudaStream_t s) {
   switch (RT) {
-    case 8: return launch_tails<D, 8>(p, num_sms, ctas, s);
-    case 16: return launch_tails<D, 16>(p, num_sms, ctas, s);
-    case 32: return launch_tails<D, 32>(p, num_sms, ctas, s);
-    default: return launch_tails<D, 64>(p, num_sms, ctas, s);
+    case 8: return launch_tails<D, 8>(p, num_sms, s);
+    case 16: return launch_tails<D, 16>(p, num_sms, s);
+    case 32: return launch_tails<D, 32>(p, num_sms, s);
+    default: return launch_tails<D, 64>(p, num_sms, s);
   }
 }
 
@@ -1041,16 +1039,36 @@ cudaError_t launch_tails_d(TailParams& p, int RT, int num_sms, int* ctas, cudaSt
 // head's T * G rows, or tiles of 64.
 int unit_rows(long long rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
-size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+template <int D>
+cudaError_t launch_merge(const MergeParams& p, cudaStream_t s) {
+  // Many rows keep the GPU's loads in flight by themselves; few, or many
+  // partials a row, are shared out over four warps.
+  if (p.rows > 2048 && p.splits <= kMergeChunk)
+    return launch_k(stream_merge_kernel<D, 1>, dim3((p.rows + kMergeWarps - 1) / kMergeWarps), dim3(kMergeWarps * 32), 0, s, p);
+  constexpr int rows = kMergeWarps / 4;
+  return launch_k(stream_merge_kernel<D, 4>, dim3((p.rows + rows - 1) / rows), dim3(kMergeWarps * 32), 0, s, p);
+}
+
+// The workspace of a cache's stream calls.  A unit has at most 2 * T * G rows
+// (or 8), so all units together 2 * max_req * G (or 8 * max_req) per K/V head,
+// in units of 8 rows or more; each CTA adds the rows of one unit.
+struct StreamWorkspace {
+  size_t ctas, ml, o, bytes;   // offsets
+  StreamWorkspace(int max_req, int Hkv, int G, int D, int num_sms) {
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    const size_t unit_rows_all = static_cast<size_t>(max_req) * Hkv * (2 * G > 8 ? 2 * G : 8);
+    const size_t rows = unit_rows_all + 2 * static_cast<size_t>(num_sms) * unit_rows(static_cast<long long>(max_req) * G);
+    ctas = 0;
+    ml = up(unit_rows_all / 8 * sizeof(int2));
+    o = ml + up(rows * sizeof(float2));
+    bytes = o + up(rows * D * sizeof(float));
+  }
+};
 
 }  // namespace
 
-// Partial rows: each unit has at most 2 * T * G rows (or 8), and each CTA adds
-// one unit's.
 size_t streams_quant_workspace(int max_req, int Hkv, int G, int D, int num_sms) {
-  const size_t mine = static_cast<size_t>(unit_rows(static_cast<long long>(max_req) * G));
-  const size_t rows = static_cast<size_t>(max_req) * Hkv * (2 * G > 8 ? 2 * G : 8) + 2 * static_cast<size_t>(num_sms) * mine;
-  return up256((static_cast<size_t>(max_req) + 1) * 8) + up256(rows * 8) + up256(rows * D * 4);
+  return StreamWorkspace(max_req, Hkv, G, D, num_sms).bytes;
 }
 
 cudaError_t launch_streams_quant(const QuantStreams& a, const AttnLaunch& al, size_t xchg_bytes, void* ws, int max_req,
@@ -1071,14 +1089,11 @@ cudaError_t launch_streams_quant(const QuantStreams& a, const AttnLaunch& al, si
   const uint32_t box[4] = {static_cast<uint32_t>(a.D < 128 ? a.D : 128), 1u, static_cast<uint32_t>(kTK), 1u};
   if (!encode_tmap_u8_4d(&tp.tm_k, a.k_tail, dims, strides, box) || !encode_tmap_u8_4d(&tp.tm_v, a.v_tail, dims, strides, box))
     return cudaErrorInvalidValue;
-  const size_t mine = static_cast<size_t>(unit_rows(static_cast<long long>(max_req) * G));
-  const size_t rows = static_cast<size_t>(max_req) * a.Hkv * (2 * G > 8 ? 2 * G : 8) + 2 * static_cast<size_t>(al.num_sms) * mine;
-  char* w = static_cast<char*>(ws);
-  tp.head = reinterpret_cast<unsigned long long*>(w);
-  w += up256((static_cast<size_t>(max_req) + 1) * 8);
-  tp.ml = reinterpret_cast<float2*>(w);
-  w += up256(rows * 8);
-  tp.o = reinterpret_cast<float*>(w);
+  const StreamWorkspace w(max_req, a.Hkv, G, a.D, al.num_sms);
+  char* mem = static_cast<char*>(ws);
+  tp.ctas = reinterpret_cast<int2*>(mem + w.ctas);
+  tp.ml = reinterpret_cast<float2*>(mem + w.ml);
+  tp.o = reinterpret_cast<float*>(mem + w.o);
   tp.q = a.q;
   tp.k_exp = a.k_exp;
   tp.v_exp = a.v_exp;
@@ -1093,11 +1108,10 @@ cudaError_t launch_streams_quant(const QuantStreams& a, const AttnLaunch& al, si
   tp.row_tiles = (a.T * G + RT - 1) / RT;
   tp.inject_tx = al.inject_tx;
   tp.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(a.D)));
-  int ctas = 0;
   switch (a.D) {
-    case 64: e = launch_tails_d<64>(tp, RT, al.num_sms, &ctas, s); break;
-    case 128: e = launch_tails_d<128>(tp, RT, al.num_sms, &ctas, s); break;
-    case 256: e = launch_tails_d<256>(tp, RT, al.num_sms, &ctas, s); break;
+    case 64: e = launch_tails_d<64>(tp, RT, al.num_sms, s); break;
+    case 128: e = launch_tails_d<128>(tp, RT, al.num_sms, s); break;
+    case 256: e = launch_tails_d<256>(tp, RT, al.num_sms, s); break;
     default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess) return e;
@@ -1107,13 +1121,13 @@ cudaError_t launch_streams_quant(const QuantStreams& a, const AttnLaunch& al, si
   const size_t units = static_cast<size_t>(m_tiles) * a.Hkv;
   mp.shared_o = static_cast<const float*>(al.xchg);
   mp.shared_ml = reinterpret_cast<const float2*>(static_cast<const char*>(al.xchg) + units * splits * 128 * a.D * 4);
-  mp.head = tp.head;
+  mp.ctas = tp.ctas;
   mp.tail_ml = tp.ml;
   mp.tail_o = tp.o;
   mp.tail_len = a.tail_len;
   mp.n_new = a.n_new;
   mp.out = a.out;
-  mp.B = a.B;
+  mp.rows = a.B * a.T * a.Hq;
   mp.T = a.T;
   mp.Hq = a.Hq;
   mp.Hkv = a.Hkv;
@@ -1123,14 +1137,10 @@ cudaError_t launch_streams_quant(const QuantStreams& a, const AttnLaunch& al, si
   mp.RT = RT;
   mp.splits = splits;
   mp.m_tiles = m_tiles;
-  mp.tail_ctas = ctas;
-  const long long out_rows = static_cast<long long>(a.B) * a.T * a.Hq;
-  const dim3 grid(static_cast<unsigned int>((out_rows + kMergeRows - 1) / kMergeRows));
-  const dim3 block(kMergeRows * kRowWarps * 32);
   switch (a.D) {
-    case 64: e = launch_k(stream_merge_kernel<64>, grid, block, 0, s, mp); break;
-    case 128: e = launch_k(stream_merge_kernel<128>, grid, block, 0, s, mp); break;
-    default: e = launch_k(stream_merge_kernel<256>, grid, block, 0, s, mp); break;
+    case 64: e = launch_merge<64>(mp, s); break;
+    case 128: e = launch_merge<128>(mp, s); break;
+    default: e = launch_merge<256>(mp, s); break;
   }
   return e != cudaSuccess ? e : cudaGetLastError();
 }
