@@ -25,8 +25,11 @@
 // The bf16 queries and fp32 weights enter as sums of e4m3 terms whose products
 // meet in fp32: a query row, scaled by a power of two, is hi + lo exactly (8
 // significant bits in two 4-bit terms; what lies 2^-18 below the row's largest
-// entry is rounded away); a weight is hi + mid + lo, within 2^-10 of itself or
-// 2^-15 of the row's largest weight, a quarter of a bf16 rounding.
+// entry is rounded away); a weight is hi + mid/16 + lo/256, each term the e4m3
+// rounding of what is left, within 2^-12 of itself or 2^-24 of the row's
+// largest weight (e4m3's smallest step is 2^-9, and the steps of 16 go along
+// with the remainders, so that many small weights beside a large one keep their
+// share): a sixteenth of a bf16 rounding.
 //   x_jn = S_jn * 2^(k_exp_j - 127) * (row scale) * log2(e) / sqrt(D)
 //   l_n  = sum_j 2^(x_jn - m_n),   w_jn = 2^(x_jn + v_exp_j - 127 - M_n + 5)
 // m_n and M_n are running maxima of x_jn and of x_jn + v_exp_j - 127: the
@@ -61,7 +64,9 @@ namespace rx {
 namespace {
 
 constexpr int kTK = 128;            // keys per tile
-constexpr int kTerms = 3;           // e4m3 terms of a weight
+constexpr int kTerms = 3;           // e4m3 terms of a weight, each standing for 1/16 of the one before
+constexpr float kTermStep = 16.f;
+constexpr int kExpAhead = 4;        // tiles ahead that scale exponents are fetched into L2
 // log2 of a row's largest weight, in e4m3 units, where its reference is taken,
 // and the most it may grow to before a new one is (448 is the largest code).
 constexpr float kTop = 5.f;
@@ -74,6 +79,10 @@ constexpr float kNoMax = -3.0e38f;
 // 2^(byte - 127); byte 255 stands for NaN.
 __device__ __forceinline__ float exp_scale(uint32_t byte) {
   return __uint_as_float(byte == 0u ? 0x00400000u : byte == 255u ? 0x7FC00000u : byte << 23);
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -599,7 +608,18 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
           vb = p.v_exp[at];
         }
       };
+      // ... and fetched into L2 some tiles before that: behind the tiles'
+      // copies a load from DRAM takes longer than a tile.
+      auto fetch_exps = [&](int tile_in_unit) {
+        const int key = tile_in_unit * kTK + key_in_tile;
+        if (wg == 0 && tile_in_unit < wk.tile0 + nt && key < kmax) {
+          const long long at = exp_base + static_cast<long long>(key) * p.Hkv;
+          prefetch_l2(p.k_exp + at);
+          prefetch_l2(p.v_exp + at);
+        }
+      };
       load_exps(wk.tile0 * kTK + key_in_tile);
+      for (int a = 1; a < kExpAhead; ++a) fetch_exps(wk.tile0 + a);
       named_sync(8, 128 * L::WG);   // the previous segment's row state is no longer read
       if (st < RT) ms.seen[st] = st < rows ? keys_seen(wk.s, (row0 + st) / p.G) : 0;
       // Q rows: 2^-e q = hi + lo, e as the append chooses it.
@@ -657,6 +677,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
         const float ks = exp_scale(vb == 255u ? 255u : kb);
         const float ev = static_cast<float>(vb) - 127.f;
         load_exps(i + 1 < nt ? key + kTK : kmax);   // the next tile's, a tile ahead
+        fetch_exps(wk.tile0 + i + kExpAhead);
         const bool masked = (wk.tile0 + i + 1) * kTK > kmin;
         mbar_wait(BAR(TB_S + buf), (tile >> 1) & 1, abort_flag);
         __syncwarp();
@@ -686,16 +707,24 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
           }
         };
         // ---- references: those of the tile before serve while no exponent
-        // can rise above kRoom (weights up to 2^kRoom fit e4m3): the largest
-        // x - m of the thread's key, its value's exponent and the largest
-        // row offset d bound them all.  The first tile of a segment always
-        // takes new ones.
+        // rises above kRoom (weights up to 2^kRoom fit e4m3).  The largest
+        // x - m of the thread's key, its value's exponent and the largest row
+        // offset d bound them all; only where that bound fails the rows are
+        // looked at one by one.  The first tile of a segment always takes
+        // new references.
         float u[CW];
         scores_less(u, row[0]);
         float top = u[0];
 #pragma unroll
         for (int j = 1; j < CW; ++j) top = fmaxf(top, u[j]);
-        if (named_any(1 + wg, 128, top > kRoom || top + (ev + dmax) > kRoom)) {
+        bool over = top > kRoom || top + (ev + dmax) > kRoom;
+        if (__any_sync(0xffffffffu, over)) {
+          float t = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < CW; ++j) t = fmaxf(t, u[j] + row[1][j]);
+          over = top > kRoom || t + ev > kRoom;
+        }
+        if (named_any(1 + wg, 128, over)) {
           // The tile's maxima: over the warp's keys, then over the four warps,
           // lane j for row n0 + j.
           scores_less(u, nullptr);
@@ -771,24 +800,25 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
         for (int j = 0; j < CW; j += 4) {
           const float4 d4 = *reinterpret_cast<const float4*>(&row[1][j]);
           const float dj[4] = {d4.x, d4.y, d4.z, d4.w};
-          uint32_t hi[4], mid[4];
-          float lo[4];
+          float w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             l[j + e] += ex2(u[j + e]);
-            const float w = ex2(u[j + e] + ev + dj[e]);
-            // Four leading bits at a time: exact remainders, and terms that
-            // e4m3 holds exactly (or, below its normal range, to 2^-10).
-            hi[e] = __float_as_uint(w) & 0xFFF00000u;
-            const float r1 = w - __uint_as_float(hi[e]);
-            mid[e] = __float_as_uint(r1) & 0xFFF00000u;
-            lo[e] = r1 - __uint_as_float(mid[e]);
+            w[e] = ex2(u[j + e] + ev + dj[e]);
           }
-          codes[0][j / 4] = to_e4m3x2(__uint_as_float(hi[0]), __uint_as_float(hi[1])) |
-                            to_e4m3x2(__uint_as_float(hi[2]), __uint_as_float(hi[3])) << 16;
-          codes[1][j / 4] = to_e4m3x2(__uint_as_float(mid[0]), __uint_as_float(mid[1])) |
-                            to_e4m3x2(__uint_as_float(mid[2]), __uint_as_float(mid[3])) << 16;
-          codes[2][j / 4] = to_e4m3x2(lo[0], lo[1]) | to_e4m3x2(lo[2], lo[3]) << 16;
+          // Each term is what e4m3 left of the weight so far, 16 times larger.
+#pragma unroll
+          for (int term = 0; term < kTerms; ++term) {
+            const uint32_t c01 = to_e4m3x2(w[0], w[1]), c23 = to_e4m3x2(w[2], w[3]);
+            codes[term][j / 4] = c01 | c23 << 16;
+            if (term + 1 < kTerms) {
+              const float2 f01 = from_e4m3x2(c01), f23 = from_e4m3x2(c23);
+              w[0] = (w[0] - f01.x) * kTermStep;
+              w[1] = (w[1] - f01.y) * kTermStep;
+              w[2] = (w[2] - f23.x) * kTermStep;
+              w[3] = (w[3] - f23.y) * kTermStep;
+            }
+          }
         }
         // The CW bytes of each term side by side in the key's stored row.
         const uint32_t wb = sW + buf * L::W_BYTES;
@@ -852,8 +882,9 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
           for (int term = 1; term < kTerms; ++term) {
             float t[CW];
             tmem_ld_cols(at + term * RT, t);
+            const float f = term == 1 ? 1.f / kTermStep : 1.f / (kTermStep * kTermStep);
 #pragma unroll
-            for (int j = 0; j < CW; ++j) o[j] += t[j];
+            for (int j = 0; j < CW; ++j) o[j] = fmaf(t[j], f, o[j]);
           }
           float* dst = p.o + slot_row * D + ob * 128 + key_in_tile;
 #pragma unroll
