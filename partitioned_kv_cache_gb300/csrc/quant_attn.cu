@@ -239,9 +239,13 @@ __device__ __forceinline__ long long head_tiles(const StreamLen& s, int row_tile
   for (int rt = 0; rt < row_tiles; ++rt) c += unit_tiles(s, rt, RT, G);
   return c;
 }
-// Active CTAs and the first tile of each: CTA c of A takes [c*C/A, (c+1)*C/A).
-__device__ __forceinline__ unsigned long long first_tile(unsigned long long c, unsigned long long C, unsigned long long A) {
-  return c * C / A;
+// The first tile of CTA c of A, which share C tiles: floor(c * C / A).  With
+// C = q A + r it is c q + floor(c r / A), in 32 bits but for the product (C is
+// below 2^32 unless the tails fill memory many times over).
+__device__ __forceinline__ unsigned long long first_tile(unsigned int c, unsigned long long C, unsigned int A) {
+  if (C >> 32) return c * C / A;
+  const unsigned int q = static_cast<unsigned int>(C) / A, r = static_cast<unsigned int>(C) - q * A;
+  return static_cast<unsigned long long>(c) * q + c * r / A;
 }
 
 // A CTA's run of tiles, unit by unit.  Every role walks it for itself.
@@ -414,8 +418,9 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
   // streams a round; with more streams a second sweep finds the run's first.
   {
     auto scan_round = [&](int b, long long carry, long long* mine) {   // returns the carry after the round
-      long long c = 0;
-      if (b < p.B) c = p.Hkv * head_tiles(stream_len(p.tail_len, p.n_new, b, p.T, p.tail_cap), p.row_tiles, RT, p.G);
+      long long per_head = 0;
+      if (b < p.B) per_head = head_tiles(stream_len(p.tail_len, p.n_new, b, p.T, p.tail_cap), p.row_tiles, RT, p.G);
+      const long long c = p.Hkv * per_head;
       long long inc = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -431,29 +436,28 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
         total += ms.scan[w];
       }
       mine[0] = before + inc - c;
-      mine[1] = c;
+      mine[1] = per_head;
       return total;
     };
     long long mine[2], total = 0;
     for (int b0 = 0; b0 < p.B; b0 += THREADS) total = scan_round(b0 + threadIdx.x, total, mine);
     const unsigned long long C = static_cast<unsigned long long>(total);
-    const unsigned long long A = min(static_cast<unsigned long long>(gridDim.x), C);
+    const unsigned int A = static_cast<unsigned int>(min(static_cast<unsigned long long>(gridDim.x), C));
     const bool active = blockIdx.x < A;
     const long long first = active ? static_cast<long long>(first_tile(blockIdx.x, C, A)) : 0;
     if (threadIdx.x == 0)
-      ms.left = active ? static_cast<long long>(first_tile(blockIdx.x + 1ull, C, A)) - first : 0;
+      ms.left = active ? static_cast<long long>(first_tile(blockIdx.x + 1, C, A)) - first : 0;
     long long carry = 0;
     for (int b0 = 0; b0 < p.B; b0 += THREADS) {
       const int b = b0 + threadIdx.x;
       if (p.B > THREADS) carry = scan_round(b, carry, mine);
       if (b < p.B) {
-        if (active && first >= mine[0] && first < mine[0] + mine[1]) {
+        if (active && first >= mine[0] && first < mine[0] + p.Hkv * mine[1]) {
           ms.b0 = b;
           long long off = first - mine[0];
           const StreamLen s = stream_len(p.tail_len, p.n_new, b, p.T, p.tail_cap);
-          const long long per_head = mine[1] / p.Hkv;
-          const int g = static_cast<int>(off / per_head);
-          off -= g * per_head;
+          int g = 0;
+          for (; off >= mine[1]; ++g) off -= mine[1];
           int rt = 0;
           for (int ut; off >= (ut = unit_tiles(s, rt, RT, p.G)); ++rt) off -= ut;
           ms.skip_unit = g * p.row_tiles + rt;
@@ -622,36 +626,63 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
       for (int a = 1; a < kExpAhead; ++a) fetch_exps(wk.tile0 + a);
       named_sync(8, 128 * L::WG);   // the previous segment's row state is no longer read
       if (st < RT) ms.seen[st] = st < rows ? keys_seen(wk.s, (row0 + st) / p.G) : 0;
-      // Q rows: 2^-e q = hi + lo, e as the append chooses it.
-      for (int n = st >> 5; n < RT; n += 4 * L::WG) {
-        constexpr int E = D / 32;
-        uint32_t w32[E / 2];
-        uint32_t top = 0;
-        const int r = row0 + n;
-        const __nv_bfloat16* src =
-            p.q + ((static_cast<long long>(wk.b) * p.T + r / p.G) * p.Hkv * p.G + wk.g * p.G + r % p.G) * D + lane * E;
+      // Q rows: 2^-e q = hi + lo, e as the append chooses it.  A warp's rows
+      // are all asked for before the first is converted.
+      {
+        constexpr int E = D / 32, NR = RT / (4 * L::WG);
+        uint32_t w32[NR][E / 2];
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) w32[e] = n < rows ? __ldg(reinterpret_cast<const uint32_t*>(src) + e) : 0u;
+        for (int k = 0; k < NR; ++k) {
+          const int n = (st >> 5) + k * 4 * L::WG, r = row0 + n;
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) top = max(top, max(w32[e] & 0x7FFFu, (w32[e] >> 16) & 0x7FFFu));
-        top = __reduce_max_sync(0xffffffffu, top);
-        const int ex = max(static_cast<int>(top >> 7) - 8 + ((top & 0x7Fu) > 96u ? 1 : 0), 1);
-        const bool poison = (top >> 7) == 255u;
-        if (lane == 0) ms.qs[n] = poison ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(ex) << 23) * p.scale_log2;
-        const float up = __uint_as_float(static_cast<uint32_t>(254 - min(ex, 253)) << 23);
+          for (int e = 0; e < E / 2; ++e) w32[k][e] = 0u;
+          if (n < rows) {
+            const __nv_bfloat16* src = p.q + ((static_cast<long long>(wk.b) * p.T + r / p.G) * p.Hkv * p.G + wk.g * p.G + r % p.G) * D + lane * E;
+            if constexpr (E == 8) {
+              const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
+              w32[k][0] = x.x, w32[k][1] = x.y, w32[k][2] = x.z, w32[k][3] = x.w;
+            } else if constexpr (E == 4) {
+              const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+              w32[k][0] = x.x, w32[k][1] = x.y;
+            } else {
+              w32[k][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+            }
+          }
+        }
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) {
-          const float a = poison ? 0.f : __uint_as_float(w32[e] << 16) * up;
-          const float b = poison ? 0.f : __uint_as_float(w32[e] & 0xFFFF0000u) * up;
-          const uint32_t hi = to_e4m3x2(a, b);
-          const float2 h = from_e4m3x2(hi);
-          const uint32_t lo = to_e4m3x2(a - h.x, b - h.y);
-          const uint32_t d = static_cast<uint32_t>(lane * E + 2 * e);
-          const uint32_t off = sQ + (d / ROW) * L::Q_BLOCK;
+        for (int k = 0; k < NR; ++k) {
+          const int n = (st >> 5) + k * 4 * L::WG;
+          uint32_t top = 0;
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) top = max(top, max(w32[k][e] & 0x7FFFu, (w32[k][e] >> 16) & 0x7FFFu));
+          top = __reduce_max_sync(0xffffffffu, top);
+          const int ex = max(static_cast<int>(top >> 7) - 8 + ((top & 0x7Fu) > 96u ? 1 : 0), 1);
+          const bool poison = (top >> 7) == 255u;
+          if (lane == 0)
+            ms.qs[n] = poison ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(ex) << 23) * p.scale_log2;
+          const float up = __uint_as_float(static_cast<uint32_t>(254 - min(ex, 253)) << 23);
+          uint32_t hi[E / 2], lo[E / 2];
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) {
+            const float a = poison ? 0.f : __uint_as_float(w32[k][e] << 16) * up;
+            const float b = poison ? 0.f : __uint_as_float(w32[k][e] & 0xFFFF0000u) * up;
+            hi[e] = to_e4m3x2(a, b);
+            const float2 h = from_e4m3x2(hi[e]);
+            lo[e] = to_e4m3x2(a - h.x, b - h.y);
+          }
           // (a term's rows are a multiple of 8, so they keep the row's swizzle)
-          asm volatile("st.shared.u16 [%0], %1;" ::"r"(off + swizzled<ROW>(n, d % ROW)), "h"(static_cast<uint16_t>(hi)) : "memory");
-          asm volatile("st.shared.u16 [%0], %1;" ::"r"(off + L::q_off(1) + swizzled<ROW>(n, d % ROW)), "h"(static_cast<uint16_t>(lo))
-                       : "memory");
+          const uint32_t d = static_cast<uint32_t>(lane * E);
+          const uint32_t at = sQ + (d / ROW) * L::Q_BLOCK + swizzled<ROW>(n, d % ROW);
+          if constexpr (E == 8) {
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0] | hi[1] << 16), "r"(hi[2] | hi[3] << 16) : "memory");
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + L::q_off(1)), "r"(lo[0] | lo[1] << 16), "r"(lo[2] | lo[3] << 16) : "memory");
+          } else if constexpr (E == 4) {
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(hi[0] | hi[1] << 16) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + L::q_off(1)), "r"(lo[0] | lo[1] << 16) : "memory");
+          } else {
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(hi[0])) : "memory");
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + L::q_off(1)), "h"(static_cast<uint16_t>(lo[0])) : "memory");
+          }
         }
       }
       fence_proxy_async_smem();
