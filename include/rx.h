@@ -419,7 +419,9 @@ rx_status rx_check_device_error(rx_cache_t cache, int* code, void* stream);
  * after their time limit (2 s), the kernel unwinds (waiting, bounded, for its
  * own copies and tensor-core work) and sets bit 1 of the error word, which
  * rx_check_device_error reports; that launch's output is undefined.  Later
- * launches are unaffected.  bytes: a multiple of 16 in [0, 2^20]; 0 cancels.
+ * launches are unaffected.  (rx_attend_streams_quant takes it in the launch over
+ * the tails, if they hold a key, and sets bit 3, value 8, of the error word.)
+ * bytes: a multiple of 16 in [0, 2^20]; 0 cancels.
  * Errors: RX_ERR_ARG. */
 rx_status rx_debug_inject_timeout(rx_cache_t cache, int bytes);
 

@@ -1168,7 +1168,7 @@ cudaError_t launch_streams_quant(const QuantStreams& a, const AttnLaunch& al, si
   tp.Hkv = a.Hkv;
   tp.tail_cap = a.tail_cap;
   tp.row_tiles = (a.T * G + RT - 1) / RT;
-  tp.inject_tx = al.inject_tx;
+  tp.inject_tx = al.inject_tx < (1 << 19) ? al.inject_tx : 1 << 19;   // a barrier counts fewer than 2^20 bytes
   tp.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(a.D)));
   switch (a.D) {
     case 64: e = launch_tails_d<64>(tp, RT, al.num_sms, s); break;

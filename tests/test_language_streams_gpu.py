@@ -291,6 +291,87 @@ def test_attention_score_range(rx):
     _attend(rx, st, g, [700, 650], None, 2, tails=(kc, ke, vc, ve))
 
 
+def test_attention_more_streams_than_threads_of_a_cta(rx):
+    g = np.random.default_rng(27)
+    st = Store(rx, g, 2, 1, 64, 4, 1, 16, 140, 500, pushes=1)
+    lens = [int(x) for x in g.integers(0, 141, 500)]
+    _attend(rx, st, g, lens, None, 1)
+
+
+@pytest.mark.parametrize("D", [64, 256])
+def test_attention_few_new_tokens_in_a_wide_batch(rx, D):
+    """Streams with one, all and some of 40 query tokens: row tiles without rows."""
+    g = np.random.default_rng(28)
+    st = Store(rx, g, 8, 1, D, 10, 1, 16, 260, 160, pushes=1)
+    _attend(rx, st, g, [260, 40, 133, 1], [1, 40, 17, 0], 40)
+
+
+@pytest.mark.parametrize("T", [1, 2, 4, 8])
+@pytest.mark.parametrize("gap", [6.0, 9.7, 12.5])
+def test_attention_many_small_weights_beside_a_large_one(rx, T, gap):
+    """One key `gap` nats above 16000 equal ones: together these weigh up to
+    40 times as much, or far less; their share must not be rounded away."""
+    g = np.random.default_rng(29)
+    n, D = 16000, 64
+    st = Store(rx, g, 8, 1, D, 0, 1, 16, n, T, pushes=0)
+    f = W.bf16_bits_to_f64
+    k = np.zeros((1, n, 1, D))
+    k[0, 7777] = gap / np.sqrt(D)      # against q = 1: gap nats
+    kc, ke = OS.quantise(f(W.to_bf16_bits(k.astype(np.float32))))
+    vc, ve = OS.quantise(f(_bits(g, (1, n, 1, D))) + 0.25)
+    import torch
+    q = np.ones((1, T, 8, D), np.float32)
+    out = st.cache.attend_streams_quant(0, dev(W.to_bf16_bits(q)), _codes(kc), _codes(vc), torch.from_numpy(ke).cuda(),
+                                        torch.from_numpy(ve).cuda(), _int([n]))
+    ref, spread = OS.stream_attention(q[0].astype(np.float64), st.k[0], st.v[0], OS.dequantise(kc[0], ke[0]), OS.dequantise(vc[0], ve[0]))
+    _check(host64(out)[0], ref, spread)
+
+
+def test_attention_wait_that_runs_out_is_reported(rx):
+    g = np.random.default_rng(31)
+    st = Store(rx, g, 8, 1, 64, 16, 1, 16, 200, 4, pushes=1)
+    kc, ke, vc, ve = _tails(g, 2, 200, 1, 64)
+    import torch
+    args = (dev(_bits(g, (2, 2, 8, 64))), _codes(kc), _codes(vc), torch.from_numpy(ke).cuda(), torch.from_numpy(ve).cuda(),
+            _int([200, 31]))
+    good = st.cache.attend_streams_quant(0, *args)
+    st.cache.debug_inject_timeout(1024)
+    st.cache.attend_streams_quant(0, *args)
+    assert st.cache.check_device_error() == 8
+    again = st.cache.attend_streams_quant(0, *args)
+    assert st.cache.check_device_error() == 0
+    assert torch.equal(good, again)
+
+
+def test_attention_refusals(rx):
+    import torch
+    g = np.random.default_rng(32)
+    st = Store(rx, g, 8, 1, 64, 16, 1, 16, 40, 4, pushes=1)
+    kc, ke, vc, ve = _tails(g, 3, 40, 1, 64)
+    kt, vt, ke, ve = _codes(kc), _codes(vc), torch.from_numpy(ke).cuda(), torch.from_numpy(ve).cuda()
+    q = dev(_bits(g, (3, 1, 8, 64)))
+    call = st.cache.attend_streams_quant
+    with pytest.raises(rx.RxError) as e:
+        call(1, q, kt, vt, ke, ve, _int([1, 2, 3]))                       # layer
+    assert e.value.status == -2
+    with pytest.raises(rx.RxError) as e:
+        call(0, dev(_bits(g, (3, 2, 8, 64))), kt, vt, ke, ve, _int([1, 2, 3]))   # 6 query tokens > max_req = 4
+    assert e.value.status == -3
+    with pytest.raises(rx.RxError) as e:
+        call(0, q, kt, vt, ke, ve, _int([1, 2, 3]), out=q)                # out is q
+    assert e.value.status == -1
+    with pytest.raises(ValueError, match="tail_len"):
+        call(0, q, kt, vt, ke, ve, torch.tensor([1, 2, 3], dtype=torch.int32))   # host memory
+    with pytest.raises(TypeError, match="k_tail"):
+        call(0, q, kt.view(torch.uint8), vt, ke, ve, _int([1, 2, 3]))
+    small = rx.Cache(1, 8, 1, 64, 16, 1, 16, 4)                            # no language streams
+    with pytest.raises(rx.RxError) as e:
+        small.attend_streams_quant(0, q, kt[:, :0], vt[:, :0], ke[:, :0], ve[:, :0], _int([1, 2, 3]))
+    assert e.value.status == -3
+    empty = call(0, q[:0], kt[:0], vt[:0], ke[:0], ve[:0], _int([]))
+    assert empty.shape == (0, 1, 8, 64)
+
+
 def test_nan_tokens_reach_only_the_rows_that_see_them(rx):
     import torch
     g = np.random.default_rng(21)
