@@ -341,14 +341,16 @@ struct TailMisc {
   int b0, skip_unit;                     // first unit of the run: stream, and unit within it
   int skip_tile;
   int pad0;
+  StreamLen s0;
   long long left;
   long long scan[32];
-  float qs[RT];                          // 2^e of the query rows, times log2(e) / sqrt(D)
+  // (read four at a time)
+  alignas(16) float qs[RT];              // 2^e of the query rows, times log2(e) / sqrt(D)
   int seen[RT];                          // tail keys each row sees
   float wm[2][4][RT], wv[2][4][RT];      // the warps' maxima, for even and odd tiles
   // Per softmax warp, for its warpgroup's rows: m, d = m - M + kTop, and the
   // last factors of l and O.
-  float row[RT < 16 ? 4 : RT / 4][4][RT < 16 ? RT : 16];
+  alignas(16) float row[RT < 16 ? 4 : RT / 4][4][RT < 16 ? RT : 16];
 };
 
 enum : int { TB_FULL = 0, TB_EMPTY = 12, TB_Q = 24, TB_S = 25, TB_W = 27, TB_PV = 29, TB_DRAIN = 31 };
@@ -378,7 +380,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = tail_smem + (base - raw);
   const uint32_t sRing = base + L::OFF_RING, sQ = base + L::OFF_Q, sW = base + L::OFF_W;
-  static_assert(sizeof(TailMisc<RT>) <= L::MISC, "misc area");
+  static_assert(sizeof(TailMisc<RT>) <= L::MISC && L::OFF_MISC % 16 == 0, "misc area");
   TailMisc<RT>& ms = *reinterpret_cast<TailMisc<RT>*>(gbase + L::OFF_MISC);
   volatile int* abort_flag = &ms.abort;
   const uint32_t sBar = base + L::OFF_MISC;
@@ -456,6 +458,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
           ms.b0 = b;
           long long off = first - mine[0];
           const StreamLen s = stream_len(p.tail_len, p.n_new, b, p.T, p.tail_cap);
+          ms.s0 = s;
           int g = 0;
           for (; off >= mine[1]; ++g) off -= mine[1];
           int rt = 0;
@@ -474,7 +477,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
     wk.g = ms.skip_unit / p.row_tiles;
     wk.rt = ms.skip_unit % p.row_tiles;
     wk.skip = ms.skip_tile;
-    wk.s = stream_len(p.tail_len, p.n_new, wk.b, p.T, p.tail_cap);
+    wk.s = ms.s0;
   }
 
   if (warp == 0) {
