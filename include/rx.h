@@ -306,7 +306,9 @@ typedef struct rx_quant_streams {
  * NaN token (exponent byte 255) makes the rows that see it NaN and no others.
  * Codes below tail_len[b] must not be NaN codes (the append stores none).
  * B*T <= max_req, tail_cap is the cache's (>= 1); the cache's device has to be
- * the current one.  out may not overlap an input.
+ * the current one.  out may not overlap an input.  The cache reads its store on
+ * a stream of its own meanwhile, forked from `stream` and joined to it again
+ * within the call (under capture too): to the caller it is ordered on `stream`.
  * Errors: RX_ERR_ARG, RX_ERR_LAYER, RX_ERR_CAPACITY, RX_ERR_STATE (another
  * device is current), RX_ERR_CUDA. */
 rx_status rx_attend_streams_quant(rx_cache_t cache, int layer, const rx_quant_streams* streams,

@@ -126,4 +126,46 @@ inline bool choose_partition(const PartitionRequest& r, PartitionChoice* out) {
   return true;
 }
 
+// How a call over language streams shares the GPU between the two kernels that
+// run at the same time: the shared store against all rows (units of 128 rows
+// x K/V heads, each `t_max` key tiles of 64, cut into `splits`) and the tails.
+// Both take one CTA an SM, so whatever SMs the first holds the second waits
+// for.  A 64-key tile of the store takes about half as long as a 128-key tile
+// of a tail, of which there are at most `tail_tiles`.
+//  * The store gets its share of the work in SMs; where that is small, enough
+//    for two tiles a CTA (the tails may be much shorter than their capacity);
+//    at most half of the SMs, and one CTA a unit at least.
+//  * The tails get the other SMs, or, where the store holds far more than its
+//    share, all of them, some after the store.
+// Measured (SMs for the store / for the tails; one call): 80 queries over 8448
+// shared keys and tails to 2000 tokens, 76/76: 26.4 us, 32/120: 33.6, 135/152:
+// 37.4; 64 queries over these and tails to 4096, 48/104: 27.8, 76/152: 38.5;
+// 64 x 8 queries over 2304 keys and tails to 16384, 64/152: 116.6, 64/88: 168;
+// 32 queries, tails to 16000, 34/118: 39.2, 76/76: 45.6.  One after the other
+// the first, third and fourth took 39.3, 133 and 48.1 us.
+struct StreamPartition {
+  int splits;     // key slices of each unit of the store
+  int tail_sms;   // SMs that the tails' grid is made for
+};
+inline StreamPartition choose_stream_partition(int units, int t_max, long long tail_tiles, int num_sms, int max_splits) {
+  const long long store = static_cast<long long>(units) * t_max;
+  const long long share = num_sms * store / (store + 2 * tail_tiles + 1);   // the store's SMs by work
+  long long want = share >= num_sms / 8 ? share : (store + 1) / 2;
+  want = want < num_sms / 2 ? want : num_sms / 2;
+  long long sp = want / units;
+  sp = sp < max_splits ? sp : max_splits;
+  sp = sp < t_max ? sp : t_max;
+  sp = sp > 1 ? sp : 1;
+  if (t_max > 0) {   // the fewest splits whose longest is as short
+    const long long longest = (t_max + sp - 1) / sp;
+    sp = (t_max + longest - 1) / longest;
+  }
+  const long long held = sp * units;
+  StreamPartition r;
+  r.splits = static_cast<int>(sp);
+  r.tail_sms = held <= share + share / 4 || held <= num_sms / 4 ? static_cast<int>(num_sms - held) : num_sms;
+  if (r.tail_sms < 1) r.tail_sms = num_sms;
+  return r;
+}
+
 }  // namespace rx

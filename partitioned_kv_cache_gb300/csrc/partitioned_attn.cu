@@ -1283,26 +1283,20 @@ cudaError_t launch_partitioned_attention(const AttnLaunch& a, const AttnSegment*
   }
 }
 
-cudaError_t launch_attention_partials(const AttnLaunch& a, const void* q, int tokens, size_t xchg_bytes, cudaStream_t s,
-                                      int* splits, int* m_tiles) {
+cudaError_t launch_attention_partials(const AttnLaunch& a, const void* q, int tokens, long long tail_tiles,
+                                      size_t xchg_bytes, cudaStream_t s, int* splits, int* m_tiles, int* tail_sms) {
   const AttnSegment seg{q, nullptr, nullptr, nullptr, tokens, 0, nullptr, 1, 0, 0};
   AttnParams prm;
   int m_total = 0, t_max = 0;
   const cudaError_t e = fill_params(a, &seg, 1, prm, m_total, t_max);
   if (e != cudaSuccess) return e;
-  // One wave of CTAs; at most 32 partials a row (the merge takes them one per
-  // lane) and as many as the exchange area holds; the fewest splits whose
-  // longest is as short.
+  // At most 32 partials a row, and as many as the exchange area holds.
   const int units = m_total * a.Hkv;
   const size_t per_split = static_cast<size_t>(units) * kBM * (4 * static_cast<size_t>(a.D) + 8);
-  long long sp = a.num_sms / units;
-  sp = sp > 32 ? 32 : sp;
-  sp = sp > t_max ? t_max : sp;
-  sp = sp > static_cast<long long>(xchg_bytes / per_split) ? static_cast<long long>(xchg_bytes / per_split) : sp;
-  sp = sp < 1 ? 1 : sp;
-  const int longest = static_cast<int>((t_max + sp - 1) / sp);
-  if (longest > 0) sp = (t_max + longest - 1) / longest;
-  prm.n_splits = static_cast<int>(sp < 1 ? 1 : sp);
+  const size_t fit = xchg_bytes / per_split;
+  const StreamPartition sp = choose_stream_partition(units, t_max, tail_tiles, a.num_sms, fit < 32 ? static_cast<int>(fit) : 32);
+  prm.n_splits = sp.splits;
+  *tail_sms = sp.tail_sms;
   prm.dparts = 1;
   prm.prefetch_l2 = a.prefetch_l2;
   *splits = prm.n_splits;

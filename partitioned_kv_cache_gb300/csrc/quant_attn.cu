@@ -13,7 +13,8 @@
 // Three launches:
 //   1. the shared store against the query rows of all streams together, by
 //      the partitioned attention kernel, which writes fp32 partials;
-//   2. stream_tail_kernel: every tail against its own stream's rows;
+//   2. stream_tail_kernel: every tail against its own stream's rows, at the
+//      same time (partition.h shares out the SMs);
 //   3. stream_merge_kernel: one row's partials into its bf16 output.
 //
 // stream_tail_kernel.  A tail is read by the G * n_new rows of one stream and
@@ -1137,14 +1138,9 @@ size_t streams_quant_workspace(int max_req, int Hkv, int G, int D, int num_sms) 
 }
 
 cudaError_t launch_streams_quant(const QuantStreams& a, const AttnLaunch& al, size_t xchg_bytes, void* ws, int max_req,
-                                 cudaStream_t s) {
+                                 const StreamFork& fork, cudaStream_t s) {
   const int G = a.Hq / a.Hkv;
   const int RT = unit_rows(static_cast<long long>(a.T) * G);
-  // 1. the shared store
-  int splits = 0, m_tiles = 0;
-  cudaError_t e = launch_attention_partials(al, a.q, a.B * a.T, xchg_bytes, s, &splits, &m_tiles);
-  if (e != cudaSuccess) return e;
-  // 2. the tails
   TailParams tp;
   memset(&tp, 0, sizeof(tp));
   const uint64_t dims[4] = {static_cast<uint64_t>(a.D), static_cast<uint64_t>(a.Hkv), static_cast<uint64_t>(a.tail_cap),
@@ -1173,14 +1169,26 @@ cudaError_t launch_streams_quant(const QuantStreams& a, const AttnLaunch& al, si
   tp.row_tiles = (a.T * G + RT - 1) / RT;
   tp.inject_tx = al.inject_tx < (1 << 19) ? al.inject_tx : 1 << 19;   // a barrier counts fewer than 2^20 bytes
   tp.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(a.D)));
-  switch (a.D) {
-    case 64: e = launch_tails_d<64>(tp, RT, al.num_sms, s); break;
-    case 128: e = launch_tails_d<128>(tp, RT, al.num_sms, s); break;
-    case 256: e = launch_tails_d<256>(tp, RT, al.num_sms, s); break;
-    default: return cudaErrorInvalidValue;
-  }
+  // The shared store on the cache's own stream, the tails beside it on the
+  // caller's; joined again whatever happens, so that a capture stays whole.
+  const long long tail_tiles =
+      static_cast<long long>(a.B) * a.Hkv * tp.row_tiles * ((a.tail_cap + kTK - 1) / kTK);
+  int splits = 0, m_tiles = 0, tail_sms = 0;
+  cudaError_t e = cudaEventRecord(fork.forked, s);
+  if (e == cudaSuccess) e = cudaStreamWaitEvent(fork.side, fork.forked, 0);
   if (e != cudaSuccess) return e;
-  // 3. the merge
+  e = launch_attention_partials(al, a.q, a.B * a.T, tail_tiles, xchg_bytes, fork.side, &splits, &m_tiles, &tail_sms);
+  if (e == cudaSuccess) {
+    switch (a.D) {
+      case 64: e = launch_tails_d<64>(tp, RT, tail_sms, s); break;
+      case 128: e = launch_tails_d<128>(tp, RT, tail_sms, s); break;
+      default: e = launch_tails_d<256>(tp, RT, tail_sms, s); break;
+    }
+  }
+  cudaError_t j = cudaEventRecord(fork.joined, fork.side);
+  if (j == cudaSuccess) j = cudaStreamWaitEvent(s, fork.joined, 0);
+  if (e == cudaSuccess) e = j;
+  if (e != cudaSuccess) return e;
   MergeParams mp;
   memset(&mp, 0, sizeof(mp));
   const size_t units = static_cast<size_t>(m_tiles) * a.Hkv;

@@ -132,6 +132,7 @@ struct rx_cache {
   rx::DevState* dstate = nullptr;
   void* xchg = nullptr;
   size_t xchg_bytes = 0;
+  rx::StreamFork fork;         // rx_attend_streams_quant: the store is read on a stream of the cache
   void* stream_ws = nullptr;   // partials of the language streams' 8-bit tails
   int max_splits = 0;
   int T_pin = 0;         // tiles of the pinned region per (layer, head), >= 1
@@ -263,6 +264,20 @@ rx_status rx_cache_create(const rx_config* cfg, rx_cache_t* out) {
       return cuda_fail(e, "rx_cache_create: cudaEventCreate");
     }
   }
+  if (stream_b) {
+    e = cudaStreamCreateWithFlags(&h->fork.side, cudaStreamNonBlocking);
+    if (e == cudaSuccess) e = cudaEventCreateWithFlags(&h->fork.forked, cudaEventDisableTiming);
+    if (e == cudaSuccess) e = cudaEventCreateWithFlags(&h->fork.joined, cudaEventDisableTiming);
+    if (e != cudaSuccess) {
+      if (h->fork.side) cudaStreamDestroy(h->fork.side);
+      if (h->fork.forked) cudaEventDestroy(h->fork.forked);
+      if (h->consumer_done) cudaEventDestroy(h->consumer_done);
+      if (h->push_done) cudaEventDestroy(h->push_done);
+      cudaFree(h->mem);
+      delete h;
+      return cuda_fail(e, "rx_cache_create: cudaStreamCreate");
+    }
+  }
   *out = h;
   return RX_OK;
   RX_GUARD_END
@@ -274,6 +289,9 @@ rx_status rx_cache_destroy(rx_cache_t h) {
   cudaError_t e = cudaDeviceSynchronize();
   if (h->consumer_done) cudaEventDestroy(h->consumer_done);
   if (h->push_done) cudaEventDestroy(h->push_done);
+  if (h->fork.side) cudaStreamDestroy(h->fork.side);
+  if (h->fork.forked) cudaEventDestroy(h->fork.forked);
+  if (h->fork.joined) cudaEventDestroy(h->fork.joined);
   cudaError_t e2 = cudaFree(h->mem);
   delete h;
   if (e != cudaSuccess) return cuda_fail(e, "rx_cache_destroy: synchronize");
@@ -654,7 +672,7 @@ rx_status rx_attend_streams_quant(rx_cache_t h, int layer, const rx_quant_stream
   s.Hkv = c.Hkv;
   s.D = c.D;
   s.tail_cap = c.tail_cap;
-  e = rx::launch_streams_quant(s, a, h->xchg_bytes, h->stream_ws, c.max_req, static_cast<cudaStream_t>(stream));
+  e = rx::launch_streams_quant(s, a, h->xchg_bytes, h->stream_ws, c.max_req, h->fork, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rx_attend_streams_quant: launch");
   return RX_OK;
   RX_GUARD_END

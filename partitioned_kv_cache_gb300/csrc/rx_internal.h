@@ -206,8 +206,14 @@ struct QuantStreams {
 // `al`: the layer's shared store, as for the partitioned attention, with its
 // exchange area of xchg_bytes; ws: streams_quant_workspace(...) bytes of the
 // cache, for the tails' partials.
+// The store is read on `side`, a stream of the cache, between the two events.
+struct StreamFork {
+  cudaStream_t side = nullptr;
+  cudaEvent_t forked = nullptr;
+  cudaEvent_t joined = nullptr;
+};
 cudaError_t launch_streams_quant(const QuantStreams& a, const AttnLaunch& al, size_t xchg_bytes, void* ws, int max_req,
-                                 cudaStream_t s);
+                                 const StreamFork& fork, cudaStream_t s);
 size_t streams_quant_workspace(int max_req, int Hkv, int G, int D, int num_sms);
 
 // ---- verification of drafted tokens ------------------------------------------
@@ -217,9 +223,10 @@ cudaError_t launch_verify_drafts(const void* p, const void* q, bool bf16, const 
 
 // The shared regions against `tokens` query tokens, left as fp32 partials in
 // the exchange area: O_s / l_s in [unit][split][D/8][128 rows][8], unit = head
-// * *m_tiles + 128-row tile, then (m_s, l_s) [unit][split][128].
-cudaError_t launch_attention_partials(const AttnLaunch& a, const void* q, int tokens, size_t xchg_bytes, cudaStream_t s,
-                                      int* splits, int* m_tiles);
+// * *m_tiles + 128-row tile, then (m_s, l_s) [unit][split][128].  tail_tiles:
+// the most key tiles of the kernel that runs beside it on *tail_sms SMs.
+cudaError_t launch_attention_partials(const AttnLaunch& a, const void* q, int tokens, long long tail_tiles,
+                                      size_t xchg_bytes, cudaStream_t s, int* splits, int* m_tiles, int* tail_sms);
 
 // Tensor-map encoding through the driver entry point (no -lcuda link); the
 // second for bytes, with the swizzle of the box's row (64 or 128 bytes).
