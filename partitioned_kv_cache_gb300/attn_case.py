@@ -30,6 +30,14 @@ input:
     python -m partitioned_kv_cache_gb300.attn_case --workload c3 --op push --layers 18 --calls 6
     python -m partitioned_kv_cache_gb300.attn_case --workload c3 --op norm --calls 6
 
+--op streams appends --tail tokens to the 8-bit tails of --streams language
+streams over the workload's store, and then --drafts tokens a call, which
+attend over the store and their tail; --op verify verifies --drafts drafted
+tokens of --streams streams over a vocabulary of --vocab:
+
+    python -m partitioned_kv_cache_gb300.attn_case --workload c5 --op streams --streams 64 --tail 4096 --drafts 8
+    python -m partitioned_kv_cache_gb300.attn_case --op verify --streams 64 --vocab 257152 --drafts 4
+
 Inputs are seeded random bf16; nothing is checked here (the tests compare with
 the oracle).
 """
@@ -46,13 +54,17 @@ def main(argv=None) -> None:
     ap.add_argument("--workload", default="c3", choices=sorted(W.WORKLOADS))
     ap.add_argument("--layers", type=int, default=2)
     ap.add_argument("--calls", type=int, default=6)
-    ap.add_argument("--op", default="attention", choices=["attention", "batch", "gamma", "push", "norm"])
+    ap.add_argument("--op", default="attention", choices=["attention", "batch", "gamma", "push", "norm", "streams", "verify"])
     ap.add_argument("--norms", action="store_true")
     ap.add_argument("--frame-mult", type=int, default=1)
     ap.add_argument("--rows", type=int, default=0)
     ap.add_argument("--suffix", type=int, default=0)
     ap.add_argument("--splits", type=int, default=0)
     ap.add_argument("--dparts", type=int, default=0)
+    ap.add_argument("--streams", type=int, default=16)
+    ap.add_argument("--tail", type=int, default=1024)
+    ap.add_argument("--drafts", type=int, default=1)
+    ap.add_argument("--vocab", type=int, default=32000)
     a = ap.parse_args(argv)
     wl = W.WORKLOADS[a.workload]
     L = max(1, min(a.layers, wl.L))
@@ -98,6 +110,43 @@ def main(argv=None) -> None:
         if not all(bool(torch.isfinite(y.float()).all()) for y in ys):
             raise SystemExit("non-finite norm output")
         print("%s: %d norms of %d x %d" % (wl.name, a.calls, rows, wl.d_model))
+        return
+
+    if a.op == "streams":
+        B, T, cap = a.streams, a.drafts, a.tail + a.drafts * a.calls
+        cache = rx.Cache(1, wl.Hq, wl.Hkv, wl.D, wl.P, wl.N, wl.F, 1, cap, B * T)
+        cache.pin_prefix(r(1, wl.P, wl.Hkv, wl.D), r(1, wl.P, wl.Hkv, wl.D))
+        for _ in range(wl.N):
+            cache.push_frame(r(1, wl.F, wl.Hkv, wl.D), r(1, wl.F, wl.Hkv, wl.D))
+        tails = [torch.zeros((B, cap, wl.Hkv, wl.D), dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2)]
+        tails += [torch.zeros((B, cap, wl.Hkv), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        lens, now = (torch.zeros(B, dtype=torch.int32, device="cuda") for _ in range(2))
+        if a.tail:
+            rx.tail_append_quant(*tails, lens, r(B, a.tail, wl.Hkv, wl.D), r(B, a.tail, wl.Hkv, wl.D), new_len=now)
+        for _ in range(a.calls):
+            lens, now = now, lens
+            rx.tail_append_quant(*tails, lens, r(B, T, wl.Hkv, wl.D), r(B, T, wl.Hkv, wl.D), new_len=now)
+            out = cache.attend_streams_quant(0, r(B, T, wl.Hq, wl.D), *tails, now)
+        torch.cuda.synchronize()
+        if cache.check_device_error() != 0:
+            raise SystemExit("a kernel reported a device-side timeout")
+        if not bool(torch.isfinite(out.float()).all()):
+            raise SystemExit("non-finite attention output")
+        cache.close()
+        print("%s: %d steps of %d streams x %d tokens, tails of %d" % (wl.name, a.calls, B, T, a.tail))
+        return
+    if a.op == "verify":
+        B, T, V = a.streams, a.drafts, a.vocab
+        for _ in range(a.calls):
+            p = torch.softmax(2.5 * torch.randn(B, T + 1, V, generator=g, device="cuda"), -1)
+            q = torch.softmax(2.5 * torch.randn(B, T, V, generator=g, device="cuda"), -1)
+            draft = torch.randint(0, V, (B, T), generator=g, device="cuda", dtype=torch.int32)
+            u, w = torch.rand(B, T, generator=g, device="cuda"), torch.rand(B, generator=g, device="cuda")
+            tokens, n, _ = rx.verify_drafts(p, q, draft, u, w)
+        torch.cuda.synchronize()
+        if not bool(((tokens >= -1) & (tokens < V)).all()):
+            raise SystemExit("a token out of range")
+        print("%d verifications of %d streams x %d drafts, vocabulary %d" % (a.calls, B, T, V))
         return
 
     S = a.suffix if a.suffix > 0 else wl.S
