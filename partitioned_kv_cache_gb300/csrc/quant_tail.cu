@@ -38,25 +38,29 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 // Every lane of the warp calls it.
 template <int L>
 __device__ __forceinline__ uint32_t quantise8(const uint4& x, uint2* codes) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  // The magnitudes' bf16 bits order like the magnitudes.
-  uint32_t top = 0;
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  // The magnitudes' bf16 bits order like the magnitudes; two at a time.
+  const uint32_t two = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+  uint32_t top = max(two & 0xFFFFu, two >> 16);
+  if constexpr (L == 32) {
+    top = __reduce_max_sync(0xffffffffu, top);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-#pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  }
   // 1.m * 2^(E-127) <= 448 * 2^e = 1.75 * 2^(8+e): e = E - 135, one more
-  // when the mantissa is above .75 (96/128).
-  const uint32_t E = top >> 7, M = top & 0x7Fu;
-  const int b = static_cast<int>(E) - 8 + (M > 96u ? 1 : 0);
-  const uint32_t byte = E == 255u ? 255u : static_cast<uint32_t>(max(b, 0));
+  // when the mantissa is above .75 (96/128), which adding 31 carries into E.
+  const bool poison = top >= 0x7F80u;
+  const uint32_t byte = poison ? 255u : static_cast<uint32_t>(max(static_cast<int>((top + 31u) >> 7) - 8, 0));
   // 2^-e; a poisoned vector's codes are zeros.
   const float up = __uint_as_float((254u - min(byte, 254u)) << 23);
   float f[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[2 * i] = byte == 255u ? 0.f : __uint_as_float(w[i] << 16) * up;
-    f[2 * i + 1] = byte == 255u ? 0.f : __uint_as_float(w[i] & 0xFFFF0000u) * up;
+    if (poison) w[i] = 0u;
+    f[2 * i] = __uint_as_float(w[i] << 16) * up;
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * up;
   }
   *codes = make_uint2(e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16), e4m3x2(f[4], f[5]) | (e4m3x2(f[6], f[7]) << 16));
   return byte;
