@@ -38,11 +38,15 @@
 // values' scales are.  Both are kept until some exponent outgrows them by 3.5
 // or more, which after a segment's first tile is rare.
 //
-// Work is cut into tiles of 128 keys of one (stream, K/V head, row tile) unit;
-// each CTA takes an equal run of consecutive tiles (lengths are read on the
-// device), and writes one fp32 partial per unit that it touches, to slot
-// cta + unit (distinct, because a run that moves to a later CTA or a later unit
-// never moves back).  The scores of tile i + 1 are computed while tile i is in
+// Work is cut into tiles of 128 keys of one (stream, K/V head, row tile) unit.
+// The tiles of one head, all streams' in a row, are cut into equal runs
+// (lengths are read on the device); a CTA takes one run of one head, and the
+// CTAs next to it the same run of the other heads, so that what a stored token
+// holds for all heads, side by side in memory, is read at about the same time
+// (64 streams of 8 heads, D = 128: 5.8 TB/s, against 4.1 when one head's tiles
+// followed the other's).  A run leaves one fp32 partial per unit that it
+// touches, in its head's slot run + unit (distinct, because going on to a
+// later run or a later unit never goes back in the other).  The scores of tile i + 1 are computed while tile i is in
 // the softmax, and the weights have two buffers, so that a tile's softmax does
 // not wait for the product before it unless a maximum grew.
 //
@@ -207,12 +211,14 @@ struct TailParams {
   const uint8_t* v_exp;
   const int* tail_len;
   const int* n_new;
-  int2* ctas;                 // [unit] the first and the last CTA with a tile of it
+  int2* runs_of;              // [unit] the first and the last run with a tile of it
   float2* ml;                 // (m, l) [slot][RT]
   float* o;                   // [slot][RT][D], relative to m
   int* err;
   int B, T, G, Hkv, tail_cap;
   int row_tiles;              // row tiles of one stream and head: ceil(T * G / RT)
+  int heads;                  // heads taken side by side: CTA c has run c / heads of head c % heads (and every
+  int runs;                   // heads-th one after it); runs of one head
   int inject_tx;              // test aid: extra bytes CTA 0 expects on its first tile
   float scale_log2;
 };
@@ -249,7 +255,15 @@ __device__ __forceinline__ unsigned long long first_tile(unsigned int c, unsigne
   return static_cast<unsigned long long>(c) * q + c * r / A;
 }
 
-// A CTA's run of tiles, unit by unit.  Every role walks it for itself.
+// Where a run starts: the stream, row tile and tile, the stream's lengths, and
+// the run's tiles.
+struct RunStart {
+  int b, rt, skip;
+  StreamLen s;
+  long long left;
+};
+// A CTA's run of tiles, unit by unit, for each of its heads.  Every role walks
+// it for itself.
 struct Walk {
   int b, g, rt;         // the unit
   int skip;             // tiles of the unit before this run
@@ -257,28 +271,37 @@ struct Walk {
   StreamLen s;
   int tile0, ntiles;    // the segment: tiles [tile0, tile0 + ntiles) of the unit
 
-  __device__ __forceinline__ bool next(const TailParams& p, int RT) {
-    while (left > 0 && b < p.B) {
-      const int ut = unit_tiles(s, rt, RT, p.G);
-      if (ut > skip) {
-        tile0 = skip;
-        ntiles = static_cast<int>(min(static_cast<long long>(ut - skip), left));
-        left -= ntiles;
-        return true;
+  __device__ __forceinline__ void begin(const RunStart& r) {
+    b = r.b;
+    rt = r.rt;
+    skip = r.skip;
+    s = r.s;
+    left = r.left;
+  }
+  __device__ __forceinline__ bool next(const TailParams& p, const RunStart& r, int RT) {
+    while (true) {
+      while (left > 0 && b < p.B) {
+        const int ut = unit_tiles(s, rt, RT, p.G);
+        if (ut > skip) {
+          tile0 = skip;
+          ntiles = static_cast<int>(min(static_cast<long long>(ut - skip), left));
+          left -= ntiles;
+          return true;
+        }
+        skip -= ut;
+        advance(p);
       }
-      skip -= ut;
-      advance(p);
+      g += p.heads;
+      if (g >= p.Hkv) return false;
+      begin(r);
+      if (left <= 0) return false;
     }
-    return false;
   }
   __device__ __forceinline__ void advance(const TailParams& p) {
     if (++rt == p.row_tiles) {
       rt = 0;
-      if (++g == p.Hkv) {
-        g = 0;
-        ++b;   // a run ends at the last tile, so b < B whenever tiles are left
-        if (b < p.B) s = stream_len(p.tail_len, p.n_new, b, p.T, p.tail_cap);
-      }
+      ++b;   // a run ends at the last tile, so b < B whenever tiles are left
+      if (b < p.B) s = stream_len(p.tail_len, p.n_new, b, p.T, p.tail_cap);
     }
   }
   // After a segment: the unit is finished for this run.
@@ -339,11 +362,7 @@ struct TailMisc {
   unsigned long long bar[12 + 12 + 8];   // full, empty, Q ready, S full[2], W ready[2], PV done[2], drain
   uint32_t tmem;
   int abort;
-  int b0, skip_unit;                     // first unit of the run: stream, and unit within it
-  int skip_tile;
-  int pad0;
-  StreamLen s0;
-  long long left;
+  RunStart start;
   long long scan[32];
   // (read four at a time)
   alignas(16) float qs[RT];              // 2^e of the query rows, times log2(e) / sqrt(D)
@@ -417,13 +436,13 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
   grid_launch_dependents();
 
   // ------------------------------------------------------ this CTA's tiles
-  // Tiles before each stream, by a scan over the block's threads, THREADS
-  // streams a round; with more streams a second sweep finds the run's first.
+  // Tiles of one head before each stream, by a scan over the block's threads,
+  // THREADS streams a round; with more streams a second sweep finds the run's
+  // first.
   {
     auto scan_round = [&](int b, long long carry, long long* mine) {   // returns the carry after the round
-      long long per_head = 0;
-      if (b < p.B) per_head = head_tiles(stream_len(p.tail_len, p.n_new, b, p.T, p.tail_cap), p.row_tiles, RT, p.G);
-      const long long c = p.Hkv * per_head;
+      long long c = 0;
+      if (b < p.B) c = head_tiles(stream_len(p.tail_len, p.n_new, b, p.T, p.tail_cap), p.row_tiles, RT, p.G);
       long long inc = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -439,47 +458,38 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
         total += ms.scan[w];
       }
       mine[0] = before + inc - c;
-      mine[1] = per_head;
+      mine[1] = c;
       return total;
     };
     long long mine[2], total = 0;
     for (int b0 = 0; b0 < p.B; b0 += THREADS) total = scan_round(b0 + threadIdx.x, total, mine);
     const unsigned long long C = static_cast<unsigned long long>(total);
-    const unsigned int A = static_cast<unsigned int>(min(static_cast<unsigned long long>(gridDim.x), C));
-    const bool active = blockIdx.x < A;
-    const long long first = active ? static_cast<long long>(first_tile(blockIdx.x, C, A)) : 0;
-    if (threadIdx.x == 0)
-      ms.left = active ? static_cast<long long>(first_tile(blockIdx.x + 1, C, A)) - first : 0;
+    const unsigned int A = static_cast<unsigned int>(min(static_cast<unsigned long long>(p.runs), C));
+    const unsigned int run = blockIdx.x / p.heads;
+    const bool active = run < A;
+    const long long first = active ? static_cast<long long>(first_tile(run, C, A)) : 0;
+    if (threadIdx.x == 0) ms.start.left = active ? static_cast<long long>(first_tile(run + 1, C, A)) - first : 0;
     long long carry = 0;
     for (int b0 = 0; b0 < p.B; b0 += THREADS) {
       const int b = b0 + threadIdx.x;
       if (p.B > THREADS) carry = scan_round(b, carry, mine);
-      if (b < p.B) {
-        if (active && first >= mine[0] && first < mine[0] + p.Hkv * mine[1]) {
-          ms.b0 = b;
-          long long off = first - mine[0];
-          const StreamLen s = stream_len(p.tail_len, p.n_new, b, p.T, p.tail_cap);
-          ms.s0 = s;
-          int g = 0;
-          for (; off >= mine[1]; ++g) off -= mine[1];
-          int rt = 0;
-          for (int ut; off >= (ut = unit_tiles(s, rt, RT, p.G)); ++rt) off -= ut;
-          ms.skip_unit = g * p.row_tiles + rt;
-          ms.skip_tile = static_cast<int>(off);
-        }
+      if (b < p.B && active && first >= mine[0] && first < mine[0] + mine[1]) {
+        long long off = first - mine[0];
+        const StreamLen s = stream_len(p.tail_len, p.n_new, b, p.T, p.tail_cap);
+        int rt = 0;
+        for (int ut; off >= (ut = unit_tiles(s, rt, RT, p.G)); ++rt) off -= ut;
+        ms.start.b = b;
+        ms.start.rt = rt;
+        ms.start.skip = static_cast<int>(off);
+        ms.start.s = s;
       }
     }
     __syncthreads();
   }
   Walk wk;
-  wk.left = ms.left;
-  if (wk.left > 0) {
-    wk.b = ms.b0;
-    wk.g = ms.skip_unit / p.row_tiles;
-    wk.rt = ms.skip_unit % p.row_tiles;
-    wk.skip = ms.skip_tile;
-    wk.s = ms.s0;
-  }
+  wk.g = blockIdx.x % p.heads;
+  wk.left = ms.start.left;
+  if (wk.left > 0) wk.begin(ms.start); else wk.g = p.Hkv;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -499,7 +509,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
           tma_load_4d(sRing + slot * L::TILE + kb * L::BLOCK, tm, kb * ROW, wk.g, tile * kTK, wk.b, BAR(TB_FULL + slot));
         ++item;
       };
-      while (!stop && wk.next(p, RT)) {
+      while (!stop && wk.next(p, ms.start, RT)) {
         load(&p.tm_k, wk.tile0);
         for (int i = 0; i < wk.ntiles && !stop; ++i) {
           if (i + 1 < wk.ntiles) load(&p.tm_k, wk.tile0 + i + 1);
@@ -541,7 +551,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
         umma_commit(BAR(TB_S + (t & 1)));
         ++item;
       };
-      while (ok && wk.next(p, RT)) {
+      while (ok && wk.next(p, ms.start, RT)) {
         if (!mbar_wait(BAR(TB_Q), seg & 1, abort_flag)) break;
         tc_fence_after();
         scores(tile);
@@ -599,7 +609,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
     unsigned int item0 = 0, tile = 0;
     if (L::NW > kTerms * RT)   // the spare rows of W stay zero
       for (int i = st * 16; i < 2 * L::W_BYTES; i += 128 * L::WG * 16) st_shared_v4(sW + i, 0u, 0u, 0u, 0u);
-    while (wk.next(p, RT)) {
+    while (wk.next(p, ms.start, RT)) {
       const int nt = wk.ntiles;
       const int row0 = wk.rt * RT;
       const int rows = min(RT, wk.s.n * p.G - row0);        // rows with a query token
@@ -884,11 +894,13 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
         mbar_arrive(BAR(TB_W + buf));
       }
       // ---- the segment's partial: O relative to m, and (m, l)
-      const long long unit = (static_cast<long long>(wk.b) * p.Hkv + wk.g) * p.row_tiles + wk.rt;
-      const long long slot_row = (unit + blockIdx.x) * RT + n0;
+      const int run = blockIdx.x / p.heads;
+      const long long in_head = static_cast<long long>(wk.b) * p.row_tiles + wk.rt;   // the unit among its head's
+      const long long slot_row = (wk.g * (static_cast<long long>(p.B) * p.row_tiles + p.runs) + in_head + run) * RT + n0;
       if (st == 0) {
-        if (wk.tile0 == 0) p.ctas[unit].x = blockIdx.x;
-        if (wk.tile0 + nt == unit_tiles(wk.s, wk.rt, RT, p.G)) p.ctas[unit].y = blockIdx.x;
+        int2* r = p.runs_of + (static_cast<long long>(wk.b) * p.Hkv + wk.g) * p.row_tiles + wk.rt;
+        if (wk.tile0 == 0) r->x = run;
+        if (wk.tile0 + nt == unit_tiles(wk.s, wk.rt, RT, p.G)) r->y = run;
       }
       named_sync(1 + wg, 128);   // wm is free
 #pragma unroll
@@ -944,11 +956,11 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
 // [D/8][128 rows]) and those of its tail.  WPR warps share a row: warp w takes
 // the partials w, w + WPR, ..., kMergeChunk of them in flight, and the warps'
 // sums meet in shared memory.  Bound by the latency of dependent loads: the
-// row's CTAs, then its partials.
+// unit's runs, then its partials.
 struct MergeParams {
   const float* shared_o;      // [unit][split][D/8][128][8]
   const float2* shared_ml;    // [unit][split][128]
-  const int2* ctas;
+  const int2* runs_of;
   const float2* tail_ml;
   const float* tail_o;
   const int* tail_len;
@@ -957,6 +969,7 @@ struct MergeParams {
   int rows;                   // B * T * Hq
   int T, Hq, Hkv, G, tail_cap, row_tiles, RT;
   int splits, m_tiles;
+  int head_slots;             // partial slots of one head: its units and runs
 };
 
 constexpr int kMergeWarps = 8;
@@ -982,12 +995,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32) stream_merge_kernel(const Me
     const int g = h / p.G, gh = h - g * p.G;
     const int r = t * p.G + gh, rt = r / p.RT;
     const int unit = (b * p.Hkv + g) * p.row_tiles + rt;
-    const int2 ctas = __ldcg(p.ctas + unit);   // (read beside the lengths; used only where the unit has tiles)
+    const int2 runs = __ldcg(p.runs_of + unit);   // (read beside the lengths; used only where the unit has tiles)
     const StreamLen s = stream_len(p.tail_len, p.n_new, b, p.T, p.tail_cap);
     live = t < s.n;
     const int ut = live ? unit_tiles(s, rt, p.RT, p.G) : 0;
-    const int tails = ut > 0 ? ctas.y - ctas.x + 1 : 0;
-    const long long tail_row = (static_cast<long long>(unit) + ctas.x) * p.RT + r % p.RT;   // the first tail partial's row
+    const int tails = ut > 0 ? runs.y - runs.x + 1 : 0;
+    const long long tail_row =   // the first tail partial's row
+        (static_cast<long long>(g) * p.head_slots + b * p.row_tiles + rt + runs.x) * p.RT + r % p.RT;
     const int row = bt * p.G + gh;             // row of the shared segment
     const long long su = (g * static_cast<long long>(p.m_tiles) + (row >> 7)) * p.splits;
     const int si = row & 127;
@@ -1088,7 +1102,10 @@ cudaError_t launch_tails(TailParams& p, int num_sms, cudaStream_t s) {
   using L = TailLayout<D, RT>;
   const cudaError_t e = cudaFuncSetAttribute(stream_tail_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
   if (e != cudaSuccess) return e;
-  return launch_k(stream_tail_kernel<D, RT>, dim3(num_sms * L::CTAS), dim3(L::THREADS), L::ALLOC, s, p);
+  const int ctas = num_sms * L::CTAS;
+  p.heads = p.Hkv < ctas ? p.Hkv : ctas;
+  p.runs = ctas / p.heads;
+  return launch_k(stream_tail_kernel<D, RT>, dim3(p.runs * p.heads), dim3(L::THREADS), L::ALLOC, s, p);
 }
 
 template <int D>
@@ -1117,14 +1134,16 @@ cudaError_t launch_merge(const MergeParams& p, cudaStream_t s) {
 
 // The workspace of a cache's stream calls.  A unit has at most 2 * T * G rows
 // (or 8), so all units together 2 * max_req * G (or 8 * max_req) per K/V head,
-// in units of 8 rows or more; each CTA adds the rows of one unit.
+// in units of 8 rows or more; each run (two CTAs an SM, or one run a head if
+// there are more heads) adds the rows of one unit.
 struct StreamWorkspace {
-  size_t ctas, ml, o, bytes;   // offsets
+  size_t runs_of, ml, o, bytes;   // offsets
   StreamWorkspace(int max_req, int Hkv, int G, int D, int num_sms) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     const size_t unit_rows_all = static_cast<size_t>(max_req) * Hkv * (2 * G > 8 ? 2 * G : 8);
-    const size_t rows = unit_rows_all + 2 * static_cast<size_t>(num_sms) * unit_rows(static_cast<long long>(max_req) * G);
-    ctas = 0;
+    const size_t runs = static_cast<size_t>(2 * num_sms > Hkv ? 2 * num_sms : Hkv);
+    const size_t rows = unit_rows_all + runs * unit_rows(static_cast<long long>(max_req) * G);
+    runs_of = 0;
     ml = up(unit_rows_all / 8 * sizeof(int2));
     o = ml + up(rows * sizeof(float2));
     bytes = o + up(rows * D * sizeof(float));
@@ -1152,7 +1171,7 @@ cudaError_t launch_streams_quant(const QuantStreams& a, const AttnLaunch& al, si
     return cudaErrorInvalidValue;
   const StreamWorkspace w(max_req, a.Hkv, G, a.D, al.num_sms);
   char* mem = static_cast<char*>(ws);
-  tp.ctas = reinterpret_cast<int2*>(mem + w.ctas);
+  tp.runs_of = reinterpret_cast<int2*>(mem + w.runs_of);
   tp.ml = reinterpret_cast<float2*>(mem + w.ml);
   tp.o = reinterpret_cast<float*>(mem + w.o);
   tp.q = a.q;
@@ -1194,7 +1213,8 @@ cudaError_t launch_streams_quant(const QuantStreams& a, const AttnLaunch& al, si
   const size_t units = static_cast<size_t>(m_tiles) * a.Hkv;
   mp.shared_o = static_cast<const float*>(al.xchg);
   mp.shared_ml = reinterpret_cast<const float2*>(static_cast<const char*>(al.xchg) + units * splits * 128 * a.D * 4);
-  mp.ctas = tp.ctas;
+  mp.runs_of = tp.runs_of;
+  mp.head_slots = a.B * tp.row_tiles + tp.runs;
   mp.tail_ml = tp.ml;
   mp.tail_o = tp.o;
   mp.tail_len = a.tail_len;

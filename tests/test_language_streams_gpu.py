@@ -291,6 +291,14 @@ def test_attention_score_range(rx):
     _attend(rx, st, g, [700, 650], None, 2, tails=(kc, ke, vc, ve))
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(6, 3, 128), (14, 7, 64), (320, 320, 64), (40, 20, 256)])
+def test_attention_head_counts(rx, Hq, Hkv, D):
+    """Head counts that do not divide the GPU's SMs, and more heads than CTAs."""
+    g = np.random.default_rng(Hkv)
+    st = Store(rx, g, Hq, Hkv, D, 6, 1, 16, 400, 9, pushes=1)
+    _attend(rx, st, g, [400, 129, 5], [3, 1, 2], 3)
+
+
 def test_attention_more_streams_than_threads_of_a_cta(rx):
     g = np.random.default_rng(27)
     st = Store(rx, g, 2, 1, 64, 4, 1, 16, 140, 500, pushes=1)
