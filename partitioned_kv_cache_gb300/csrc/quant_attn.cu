@@ -313,15 +313,13 @@ struct Walk {
 
 template <int D, int RT>
 struct TailLayout {
-  // The e4m3 terms of W, and up to 32 rows those of Q, are further rows of one
-  // operand.  These products are bound by their operands' way out of shared
-  // memory, 64 bytes a clock: one of 128 x 32 codes with N rows takes about
-  // (4096 + 32 N) / 64 clocks (measured: 96 at N = 64, 72 at N = 16), so the
-  // codes should be read once for all terms.  (At 64 rows, Q's terms are two
-  // products into one accumulator: TMEM holds no more than that.)
-  static constexpr bool STACK = RT <= 32;
-  static constexpr int NQ = STACK ? 2 * RT : RT;          // MMA N of the scores
-  static constexpr int QT = STACK ? 1 : 2;                // products per K step
+  // The e4m3 terms of Q and W are further rows of one operand.  These products
+  // are bound by their operands' way out of shared memory, 64 bytes a clock:
+  // one of 128 x 32 codes with N rows takes about (4096 + 32 N) / 64 clocks
+  // (measured: 96 at N = 64, 72 at N = 16), so the codes are read once for all
+  // terms.  At 64 rows that leaves TMEM one tile's scores instead of two.
+  static constexpr int NQ = 2 * RT;                       // MMA N of the scores
+  static constexpr int SB = RT == 64 ? 1 : 2;             // tiles of scores
   static constexpr int NW = RT == 64 ? 3 * RT : 4 * RT;   // MMA N of the output (up to 32 rows a term's place is spare)
   static constexpr int WROW = RT == 64 ? RT : NW;         // bytes of a key's stored weights in one block
   static constexpr int CW = RT < 16 ? RT : 16;            // rows of one softmax warpgroup
@@ -332,12 +330,12 @@ struct TailLayout {
   static constexpr int TILE = kTK * D;
   static constexpr int BLOCK = kTK * ROW;                 // one column block of a tile
   static constexpr int OB = D == 256 ? 2 : 1;             // 128-row blocks of O^T
-  static constexpr int TM_O = 2 * NQ;                     // TMEM: two tiles' scores, then O
+  static constexpr int TM_O = SB * NQ;                    // TMEM: scores, then O
   static constexpr int TM_USED = TM_O + OB * NW;
   static constexpr int TM_COLS = TM_USED <= 128 ? 128 : TM_USED <= 256 ? 256 : 512;
   static constexpr int CTAS = D == 256 || RT == 64 ? 1 : 2;   // per SM
-  static constexpr int Q_BLOCK = NQ * ROW;                // one column block of one product's Q
-  static constexpr int Q_BYTES = QT * KB * Q_BLOCK;
+  static constexpr int Q_BLOCK = NQ * ROW;                // one column block of Q
+  static constexpr int Q_BYTES = KB * Q_BLOCK;
   static constexpr int W_BLOCK = WROW * kTK;              // [key][WROW]: all terms, or at 64 rows one
   static constexpr int W_BYTES = NW * kTK;                // a tile's weights; two tiles are kept
   static constexpr int MISC = RT == 64 ? 9728 : 5632;
@@ -352,14 +350,12 @@ struct TailLayout {
   static constexpr int ALLOC = BYTES + 1024;
   static_assert(NS >= 3, "ring depth");
   static_assert(TM_USED <= 512 / CTAS && TM_COLS <= 512 / CTAS, "tensor memory");
-  // A term's place in the Q operand.
-  static constexpr int q_off(int term) { return STACK ? term * RT * ROW : term * KB * Q_BLOCK; }
 };
 
 // The MISC area.
 template <int RT>
 struct TailMisc {
-  unsigned long long bar[12 + 12 + 8];   // full, empty, Q ready, S full[2], W ready[2], PV done[2], drain
+  unsigned long long bar[12 + 12 + 10];  // full, empty, Q ready, S full[2], W ready[2], PV done[2], drain, S read
   uint32_t tmem;
   int abort;
   RunStart start;
@@ -373,7 +369,7 @@ struct TailMisc {
   alignas(16) float row[RT < 16 ? 4 : RT / 4][4][RT < 16 ? RT : 16];
 };
 
-enum : int { TB_FULL = 0, TB_EMPTY = 12, TB_Q = 24, TB_S = 25, TB_W = 27, TB_PV = 29, TB_DRAIN = 31 };
+enum : int { TB_FULL = 0, TB_EMPTY = 12, TB_Q = 24, TB_S = 25, TB_W = 27, TB_PV = 29, TB_DRAIN = 31, TB_SR = 32 };
 
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -419,6 +415,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
       mbar_init(BAR(TB_PV + i), 1);
     }
     mbar_init(BAR(TB_DRAIN), 1);
+    mbar_init(BAR(TB_SR), 128 * L::WG);
     ms.abort = 0;
     fence_barrier_init();
     tma_prefetch_desc(&p.tm_k);
@@ -538,17 +535,14 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
         tc_fence_after();
         const uint64_t kd = sdesc_rows<ROW>(here(sRing + slot * L::TILE), 16);
         const uint64_t qd = sdesc_rows<ROW>(here(sQ), 16);
-        const uint32_t acc = here(tmem + (t & 1) * L::NQ);
+        const uint32_t acc = here(tmem + t % L::SB * L::NQ);
 #pragma unroll
-        for (int term = 0; term < L::QT; ++term)
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk) {
-            const uint32_t kb = kk * 32 / ROW, ko = kk * 32 % ROW;
-            umma_e4m3(acc, desc_step(kd, kb * L::BLOCK + ko), desc_step(qd, (term * L::KB + kb) * L::Q_BLOCK + ko), kIdescS,
-                      (term | kk) ? 1u : 0u);
-          }
+        for (int kk = 0; kk < D / 32; ++kk) {
+          const uint32_t kb = kk * 32 / ROW, ko = kk * 32 % ROW;
+          umma_e4m3(acc, desc_step(kd, kb * L::BLOCK + ko), desc_step(qd, kb * L::Q_BLOCK + ko), kIdescS, kk ? 1u : 0u);
+        }
         umma_commit(BAR(TB_EMPTY + slot));
-        umma_commit(BAR(TB_S + (t & 1)));
+        umma_commit(BAR(TB_S + t % L::SB));
         ++item;
       };
       while (ok && wk.next(p, ms.start, RT)) {
@@ -556,8 +550,16 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
         tc_fence_after();
         scores(tile);
         for (int i = 0; i < wk.ntiles && ok; ++i, ++tile) {
-          // S buffer (tile + 1) & 1 was read before W of tile - 1 was ready.
-          if (i + 1 < wk.ntiles) scores(tile + 1);
+          // Of two S buffers, the next tile's was read before W of tile - 1 was
+          // ready; a single one is free when this tile's scores are read.
+          if (i + 1 < wk.ntiles) {
+            if (L::SB == 1 && !mbar_wait(BAR(TB_SR), tile & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            scores(tile + 1);
+          }
           const int slot = item % NS;
           if (!ok || !mbar_wait(BAR(TB_W + (tile & 1)), (tile >> 1) & 1, abort_flag) ||
               !mbar_wait(BAR(TB_FULL + slot), (item / NS) & 1, abort_flag)) {
@@ -689,13 +691,13 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
           const uint32_t at = sQ + (d / ROW) * L::Q_BLOCK + swizzled<ROW>(n, d % ROW);
           if constexpr (E == 8) {
             asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0] | hi[1] << 16), "r"(hi[2] | hi[3] << 16) : "memory");
-            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + L::q_off(1)), "r"(lo[0] | lo[1] << 16), "r"(lo[2] | lo[3] << 16) : "memory");
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + RT * ROW), "r"(lo[0] | lo[1] << 16), "r"(lo[2] | lo[3] << 16) : "memory");
           } else if constexpr (E == 4) {
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(hi[0] | hi[1] << 16) : "memory");
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + L::q_off(1)), "r"(lo[0] | lo[1] << 16) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + RT * ROW), "r"(lo[0] | lo[1] << 16) : "memory");
           } else {
             asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(hi[0])) : "memory");
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + L::q_off(1)), "h"(static_cast<uint16_t>(lo[0])) : "memory");
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + RT * ROW), "h"(static_cast<uint16_t>(lo[0])) : "memory");
           }
         }
       }
@@ -724,18 +726,17 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
         load_exps(i + 1 < nt ? key + kTK : kmax);   // the next tile's, a tile ahead
         fetch_exps(wk.tile0 + i + kExpAhead);
         const bool masked = (wk.tile0 + i + 1) * kTK > kmin;
-        mbar_wait(BAR(TB_S + buf), (tile >> 1) & 1, abort_flag);
+        mbar_wait(BAR(TB_S + tile % L::SB), tile / L::SB & 1, abort_flag);
         __syncwarp();
         tc_fence_after();
         // x_n - c_n for this key and the warpgroup's rows; c: an array in shared memory.
         auto scores_less = [&](float (&x)[CW], const float* c) {
-          tmem_ld_cols(tmem + buf * L::NQ + n0 + lane_off, x);
-          if constexpr (L::STACK) {
-            float lo[CW];
-            tmem_ld_cols(tmem + buf * L::NQ + RT + n0 + lane_off, lo);
+          const uint32_t at = tmem + tile % L::SB * L::NQ + n0 + lane_off;
+          float lo[CW];
+          tmem_ld_cols(at, x);
+          tmem_ld_cols(at + RT, lo);
 #pragma unroll
-            for (int j = 0; j < CW; ++j) x[j] += lo[j];
-          }
+          for (int j = 0; j < CW; ++j) x[j] += lo[j];
 #pragma unroll
           for (int j = 0; j < CW; j += 4) {
             const float4 f = *reinterpret_cast<const float4*>(&ms.qs[n0 + j]);
@@ -834,6 +835,10 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
               tmem_st_cols(at, o);
             }
           }
+        }
+        if (L::SB == 1) {   // the next tile's scores may take this one's place
+          tc_fence_before();
+          mbar_arrive(BAR(TB_SR));
         }
         // ---- weights, once the product that read this W buffer is done
         if (i > 1) {
