@@ -26,11 +26,11 @@
 // The bf16 queries and fp32 weights enter as sums of e4m3 terms whose products
 // meet in fp32: a query row, scaled by a power of two, is hi + lo exactly (8
 // significant bits in two 4-bit terms; what lies 2^-18 below the row's largest
-// entry is rounded away); a weight is hi + mid/16 + lo/256, each term the e4m3
-// rounding of what is left, within 2^-12 of itself or 2^-24 of the row's
-// largest weight (e4m3's smallest step is 2^-9, and the steps of 16 go along
-// with the remainders, so that many small weights beside a large one keep their
-// share): a sixteenth of a bf16 rounding.
+// entry is rounded away); a weight, rounded to f16, is hi + mid/16 + lo/256, each
+// term the e4m3 rounding of what is left, so it is within 2^-11 of its value or
+// 2^-24 of the row's largest weight (e4m3's smallest step is 2^-9, and the
+// steps of 16 go along with the remainders, so that many small weights beside
+// a large one keep their share): an eighth of a bf16 rounding.
 //   x_jn = S_jn * 2^(k_exp_j - 127) * (row scale) * log2(e) / sqrt(D)
 //   l_n  = sum_j 2^(x_jn - m_n),   w_jn = 2^(x_jn + v_exp_j - 127 - M_n + 5)
 // m_n and M_n are running maxima of x_jn and of x_jn + v_exp_j - 127: the
@@ -111,13 +111,55 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
       : "r"(h));
   return f;
 }
-
-// Largest value over the warp's lanes; NaN is passed over.
-__device__ __forceinline__ float warp_max(float v) {
-  float r;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+// Two fp32 values -> f16x2, and f16x2 -> two e4m3 codes.
+__device__ __forceinline__ uint32_t to_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
+  return r;
+}
+// 16 (x - c) for e4m3 codes c of the f16x2 values x: exact.
+__device__ __forceinline__ uint32_t e4m3x2_rest(uint32_t x, uint32_t c) {
+  uint32_t f, r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(static_cast<uint16_t>(c)));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(f));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0x4C004C00u));
+  return r;
+}
+
+// Column-wise combination over the warp's lanes of N values a lane, halving
+// the values with each exchange: lane l gets that of column l / (32 / N).
+// (A redux for each column took longer: 32 of them in each of 16 warps held up
+// a segment's first tile by about 2 us.)
+template <int N, typename Op>
+__device__ __forceinline__ float across_lanes(const float (&in)[N], int lane, Op op) {
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = in[i];
+  int off = 16;
+#pragma unroll
+  for (int n = N / 2; n > 0; n /= 2, off /= 2) {
+    const bool upper = lane & off;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = upper ? v[i] : v[i + n];
+      v[i] = op(upper ? v[i + n] : v[i], __shfl_xor_sync(0xffffffffu, give, off));
+    }
+  }
+#pragma unroll
+  for (; off > 0; off /= 2) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], off));
+  return v[0];
+}
+struct MaxOp {   // NaN is passed over
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct SumOp {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
 
 // 8 or 16 consecutive fp32 columns of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[8]) {
@@ -429,6 +471,15 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms.tmem;
+  // The query rows are fetched into L2, an equal part by each CTA, before the
+  // tiles' copies fill the memory's queues: behind those a row took 3 to 5 us.
+  // (A hint with no effect on what a load returns: safe before the wait.)
+  {
+    const long long bytes = static_cast<long long>(p.B) * p.T * p.Hkv * p.G * D * 2;
+    const long long part = (bytes / gridDim.x + 127) / 128 * 128;
+    for (long long at = blockIdx.x * part + threadIdx.x * 128ll; at < min(bytes, (blockIdx.x + 1) * part); at += THREADS * 128ll)
+      prefetch_l2(reinterpret_cast<const char*>(p.q) + at);
+  }
   grid_dependency_wait();
   grid_launch_dependents();
 
@@ -774,18 +825,14 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
           // The tile's maxima: over the warp's keys, then over the four warps,
           // lane j for row n0 + j.
           scores_less(u, nullptr);
-          float hx = kNoMax, hy = kNoMax;
+          const float hx = across_lanes(u, lane, MaxOp());
+          float y[CW];
 #pragma unroll
-          for (int j = 0; j < CW; ++j) {
-            const float a = warp_max(u[j]), b = warp_max(u[j] + ev);
-            if (lane == j) {
-              hx = a;
-              hy = b;
-            }
-          }
-          if (lane < CW) {
-            ms.wm[buf][quarter][n0 + lane] = hx;
-            ms.wv[buf][quarter][n0 + lane] = hy;
+          for (int j = 0; j < CW; ++j) y[j] = u[j] + ev;
+          const float hy = across_lanes(y, lane, MaxOp());
+          if (lane % (32 / CW) == 0) {
+            ms.wm[buf][quarter][n0 + lane / (32 / CW)] = hx;
+            ms.wv[buf][quarter][n0 + lane / (32 / CW)] = hy;
           }
           named_sync(1 + wg, 128);
           float mn = m, vn = mv;
@@ -803,7 +850,9 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
             row[2][lane] = ex2(m - mn);
             row[3][lane] = ex2(mv - vn);
           }
-          dmax = warp_max(lane < CW ? d : -INFINITY);
+          dmax = lane < CW ? d : -INFINITY;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) dmax = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, o));
           m = mn;
           mv = vn;
           __syncwarp();
@@ -856,17 +905,16 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
             l[j + e] += ex2(u[j + e]);
             w[e] = ex2(u[j + e] + ev + dj[e]);
           }
-          // Each term is what e4m3 left of the weight so far, 16 times larger.
+          // Each term is what e4m3 left of the f16 weight so far, 16 times
+          // larger: three of 4 bits hold f16's 11.
+          uint32_t h01 = to_f16x2(w[0], w[1]), h23 = to_f16x2(w[2], w[3]);
 #pragma unroll
           for (int term = 0; term < kTerms; ++term) {
-            const uint32_t c01 = to_e4m3x2(w[0], w[1]), c23 = to_e4m3x2(w[2], w[3]);
+            const uint32_t c01 = f16x2_to_e4m3x2(h01), c23 = f16x2_to_e4m3x2(h23);
             codes[term][j / 4] = c01 | c23 << 16;
             if (term + 1 < kTerms) {
-              const float2 f01 = from_e4m3x2(c01), f23 = from_e4m3x2(c23);
-              w[0] = (w[0] - f01.x) * kTermStep;
-              w[1] = (w[1] - f01.y) * kTermStep;
-              w[2] = (w[2] - f23.x) * kTermStep;
-              w[3] = (w[3] - f23.y) * kTermStep;
+              h01 = e4m3x2_rest(h01, c01);
+              h23 = e4m3x2_rest(h23, c23);
             }
           }
         }
@@ -908,13 +956,8 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
         if (wk.tile0 + nt == unit_tiles(wk.s, wk.rt, RT, p.G)) r->y = run;
       }
       named_sync(1 + wg, 128);   // wm is free
-#pragma unroll
-      for (int j = 0; j < CW; ++j) {
-        float v = l[j];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) ms.wm[0][quarter][n0 + j] = v;
-      }
+      const float sum = across_lanes(l, lane, SumOp());
+      if (lane % (32 / CW) == 0) ms.wm[0][quarter][n0 + lane / (32 / CW)] = sum;
       if (lane < CW) row[2][lane] = exp2f(mv - kTop - m);   // O's reference to m
       named_sync(1 + wg, 128);
       if (in_wg < CW && n0 + in_wg < rows)
