@@ -268,8 +268,8 @@ rx_status rx_tail_append(void* k_tail, void* v_tail, int* tail_len, const void* 
  * k_tail, v_tail: e4m3 [B][tail_cap][Hkv][D]; k_exp, v_exp: uint8
  * [B][tail_cap][Hkv]; k_new, v_new: bf16 [B][T][Hkv][D]; tail_len, new_len,
  * n_new: DEVICE int32 [B] (n_new NULL: T for every stream; values are clamped
- * to [0, T]; new_len NULL: not written; new_len may not overlap the others);
- * overflow: DEVICE int32 or NULL.  D in {64, 128, 256}, B*T*Hkv <= 2^31.
+ * to [0, T]; new_len NULL: not written); overflow: DEVICE int32 or NULL.  No
+ * output may overlap an input or another output.  D in {64, 128, 256}, B*T*Hkv <= 2^31.
  * Errors: RX_ERR_ARG, RX_ERR_UNSUPPORTED (D), RX_ERR_CUDA. */
 rx_status rx_tail_append_quant(void* k_tail, void* v_tail, unsigned char* k_exp,
                                unsigned char* v_exp, const int* tail_len, int* new_len,

@@ -618,6 +618,20 @@ rx_status rx_tail_append_quant(void* k_tail, void* v_tail, unsigned char* k_exp,
   const long long lens = static_cast<long long>(B) * 4;
   if (spans_overlap(new_len, lens, tail_len, lens) || spans_overlap(new_len, lens, n_new, lens))
     return fail(RX_ERR_ARG, "rx_tail_append_quant: new_len may not overlap tail_len or n_new");
+  {
+    const long long eb = static_cast<long long>(B) * tail_cap * Hkv, tb = eb * D;
+    const long long nb = static_cast<long long>(B) * T * Hkv * D * 2;
+    const Span outs[6] = {{k_tail, tb}, {v_tail, tb}, {k_exp, eb}, {v_exp, eb}, {new_len, lens}, {overflow, 4}};
+    const Span in[4] = {{k_new, nb}, {v_new, nb}, {tail_len, lens}, {n_new, lens}};
+    for (int i = 0; i < 6; ++i) {
+      for (const Span& x : in)
+        if (spans_overlap(outs[i].p, outs[i].bytes, x.p, x.bytes))
+          return fail(RX_ERR_ARG, "rx_tail_append_quant: an output overlaps an input");
+      for (int j = 0; j < i; ++j)
+        if (spans_overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+          return fail(RX_ERR_ARG, "rx_tail_append_quant: outputs overlap");
+    }
+  }
   cudaError_t e = rx::launch_tail_append_quant(k_tail, v_tail, k_exp, v_exp, tail_len, new_len, k_new, v_new, n_new,
                                                B, T, tail_cap, Hkv, D, overflow, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rx_tail_append_quant: launch");
@@ -696,7 +710,9 @@ rx_status rx_verify_drafts(const void* p, const void* q, int prob_type, const in
       !aligned4(n_accept) || !aligned4(new_len))
     return fail(RX_ERR_ARG, "rx_verify_drafts: misaligned pointer");
   const long long n_tok = static_cast<long long>(B) * (T + 1) * 4, n_b = static_cast<long long>(B) * 4;
-  const Span in[4] = {{draft, static_cast<long long>(B) * T * 4}, {u, static_cast<long long>(B) * T * 4}, {r, n_b}, {n_draft, n_b}};
+  const long long row = static_cast<long long>(V) * (prob_type == RX_PROB_F32 ? 4 : 2);
+  const Span in[6] = {{draft, static_cast<long long>(B) * T * 4}, {u, static_cast<long long>(B) * T * 4}, {r, n_b}, {n_draft, n_b},
+                      {p, B * (T + 1ll) * row}, {q, static_cast<long long>(B) * T * row}};
   const Span outs[3] = {{tokens, n_tok}, {n_accept, n_b}, {new_len, n_b}};
   for (int i = 0; i < 3; ++i) {
     for (const Span& x : in)

@@ -6,6 +6,7 @@ fails loudly when the library has not been built -- there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import List, Optional, Sequence, Tuple
@@ -179,6 +180,12 @@ def _here(stream) -> Tuple[int, int]:
     if stream is not None:
         return dev, stream.cuda_stream
     return dev, torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else 0
+
+
+def _outputs(stream):
+    """Where a call's own outputs are allocated: on the stream that writes
+    them, so that their memory is not in use by work still pending elsewhere."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _norm_jobs(norms) -> Tuple[Optional[ctypes.Array], int]:
@@ -383,7 +390,7 @@ class Cache:
         uint8 exponents [B][tail_cap][Hkv] (tail_append_quant); tail_len:
         int32 [B], the query tokens' own keys among them.  Query token t sees
         the cached regions and its stream's keys up to its own.  Rows
-        t >= n_new[b] of out are left as they were.
+        t >= n_new[b] of out are left as they were (of a new one: undefined).
         """
         c = self.cfg
         if q.dim() != 4:
@@ -391,7 +398,8 @@ class Cache:
         B, T = q.shape[:2]
         dev, st = _here(stream)
         if out is None:
-            out = torch.empty_like(q)
+            with _outputs(stream):
+                out = torch.empty_like(q)
         e4m3, u8, i32, bf16 = torch.float8_e4m3fn, torch.uint8, torch.int32, torch.bfloat16
         rows, tail, exps, each = (B, T, c.Hq, c.D), (B, c.tail_cap, c.Hkv, c.D), (B, c.tail_cap, c.Hkv), (B,)
         ptrs = _addresses(dev, (q, bf16, rows, "q"), (k_tail, e4m3, tail, "k_tail"), (v_tail, e4m3, tail, "v_tail"),
@@ -583,14 +591,15 @@ def verify_drafts(p: torch.Tensor, q: Optional[torch.Tensor], draft: torch.Tenso
     if new_len is not None and tail_len is None:
         raise ValueError("new_len needs tail_len")
     dev, st = _here(stream)
-    if tail_len is not None and new_len is None:
-        new_len = torch.empty_like(tail_len)
+    with _outputs(stream):
+        tokens = torch.empty((B, T + 1), dtype=i32, device=p.device)
+        n_accept = torch.empty(each, dtype=i32, device=p.device)
+        if tail_len is not None and new_len is None:
+            new_len = torch.empty_like(tail_len)
     pp, qp, dp, up, rp, np_, tl, nl = _addresses(
         dev, (p, p.dtype, (B, T + 1, V), "p"), (q, p.dtype, (B, T, V), "q"), (draft, i32, (B, T), "draft"),
         (u, f32, (B, T), "u"), (r, f32, each, "r"), (n_draft, i32, each, "n_draft"), (tail_len, i32, each, "tail_len"),
         (new_len, i32, each, "new_len"))
-    tokens = torch.empty((B, T + 1), dtype=i32, device=p.device)
-    n_accept = torch.empty(each, dtype=i32, device=p.device)
     args = (pp, qp, _PROB_TYPES[p.dtype], dp, up, rp, np_, B, T, V, tl, tokens.data_ptr(), n_accept.data_ptr(), nl, st)
     _check(_lib.rx_verify_drafts(*args), "rx_verify_drafts")
     return tokens, n_accept, new_len

@@ -88,6 +88,10 @@ def test_append_refuses_bad_arguments(lib):
         assert call(**{name: good[name] + 2}) == -1, name
     assert call(nl=good["tl"]) == -1
     assert call(nn=p + 576, nl=p + 576) == -1
+    assert call(vt=good["kt"]) == -1               # K and V in one place
+    assert call(ve=good["ke"] + 3) == -1
+    assert call(kn=good["vt"] + 128) == -1         # new values inside a tail
+    assert call(ov=good["tl"]) == -1
     del keep
 
 
@@ -124,6 +128,7 @@ def test_verify_refuses_bad_arguments(lib):
     assert call(na=good["tok"]) == -1
     assert call(nl=good["tl"] + 4) == -1           # neither the same array nor apart
     assert call(tok=good["tl"]) == -1
+    assert call(na=good["p"] + 64) == -1
     del keep
 
 

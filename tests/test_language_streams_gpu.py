@@ -478,8 +478,9 @@ def test_attention_on_another_stream(rx):
     side.wait_stream(torch.cuda.current_stream())
     there = torch.empty_like(here)
     st.cache.attend_streams_quant(0, *args, out=there, stream=side)
+    fresh = st.cache.attend_streams_quant(0, *args, stream=side)   # allocated there
     torch.cuda.current_stream().wait_stream(side)
-    assert torch.equal(here, there)
+    assert torch.equal(here, there) and torch.equal(here, fresh)
 
 
 def test_attention_agrees_with_the_16_bit_tails(rx):
