@@ -257,7 +257,8 @@ struct TailParams {
   float2* ml;                 // (m, l) [slot][RT]
   float* o;                   // [slot][RT][D], relative to m
   int* err;
-  int B, T, G, Hkv, tail_cap;
+  int B, T, Hkv, tail_cap;
+  int gs;                     // log2 of the query heads per K/V head G
   int row_tiles;              // row tiles of one stream and head: ceil(T * G / RT)
   int heads;                  // heads taken side by side: CTA c has run c / heads of head c % heads (and every
   int runs;                   // heads-th one after it); runs of one head
@@ -278,14 +279,14 @@ __device__ __forceinline__ StreamLen stream_len(const int* tail_len, const int* 
 // Tail keys that query token t sees.
 __device__ __forceinline__ int keys_seen(const StreamLen& s, int t) { return max(0, min(s.len, s.len - s.n + t + 1)); }
 // Key tiles of row tile rt: those its last row sees (none without a row).
-__device__ __forceinline__ int unit_tiles(const StreamLen& s, int rt, int RT, int G) {
-  if (rt * RT >= s.n * G) return 0;
-  return (keys_seen(s, min(s.n - 1, (rt * RT + RT - 1) / G)) + kTK - 1) / kTK;
+__device__ __forceinline__ int unit_tiles(const StreamLen& s, int rt, int RT, int gs) {
+  if (rt * RT >= s.n << gs) return 0;
+  return (keys_seen(s, min(s.n - 1, (rt * RT + RT - 1) >> gs)) + kTK - 1) / kTK;
 }
 // Tiles of all row tiles of one stream and head.
-__device__ __forceinline__ long long head_tiles(const StreamLen& s, int row_tiles, int RT, int G) {
+__device__ __forceinline__ long long head_tiles(const StreamLen& s, int row_tiles, int RT, int gs) {
   long long c = 0;
-  for (int rt = 0; rt < row_tiles; ++rt) c += unit_tiles(s, rt, RT, G);
+  for (int rt = 0; rt < row_tiles; ++rt) c += unit_tiles(s, rt, RT, gs);
   return c;
 }
 // The first tile of CTA c of A, which share C tiles: floor(c * C / A).  With
@@ -323,7 +324,7 @@ struct Walk {
   __device__ __forceinline__ bool next(const TailParams& p, const RunStart& r, int RT) {
     while (true) {
       while (left > 0 && b < p.B) {
-        const int ut = unit_tiles(s, rt, RT, p.G);
+        const int ut = unit_tiles(s, rt, RT, p.gs);
         if (ut > skip) {
           tile0 = skip;
           ntiles = static_cast<int>(min(static_cast<long long>(ut - skip), left));
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
   // tiles' copies fill the memory's queues: behind those a row took 3 to 5 us.
   // (A hint with no effect on what a load returns: safe before the wait.)
   {
-    const long long bytes = static_cast<long long>(p.B) * p.T * p.Hkv * p.G * D * 2;
+    const long long bytes = (static_cast<long long>(p.B) * p.T * p.Hkv << p.gs) * D * 2;
     const long long part = (bytes / gridDim.x + 127) / 128 * 128;
     for (long long at = blockIdx.x * part + threadIdx.x * 128ll; at < min(bytes, (blockIdx.x + 1) * part); at += THREADS * 128ll)
       prefetch_l2(reinterpret_cast<const char*>(p.q) + at);
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
   {
     auto scan_round = [&](int b, long long carry, long long* mine) {   // returns the carry after the round
       long long c = 0;
-      if (b < p.B) c = head_tiles(stream_len(p.tail_len, p.n_new, b, p.T, p.tail_cap), p.row_tiles, RT, p.G);
+      if (b < p.B) c = head_tiles(stream_len(p.tail_len, p.n_new, b, p.T, p.tail_cap), p.row_tiles, RT, p.gs);
       long long inc = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
         long long off = first - mine[0];
         const StreamLen s = stream_len(p.tail_len, p.n_new, b, p.T, p.tail_cap);
         int rt = 0;
-        for (int ut; off >= (ut = unit_tiles(s, rt, RT, p.G)); ++rt) off -= ut;
+        for (int ut; off >= (ut = unit_tiles(s, rt, RT, p.gs)); ++rt) off -= ut;
         ms.start.b = b;
         ms.start.rt = rt;
         ms.start.skip = static_cast<int>(off);
@@ -665,9 +666,9 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
     while (wk.next(p, ms.start, RT)) {
       const int nt = wk.ntiles;
       const int row0 = wk.rt * RT;
-      const int rows = min(RT, wk.s.n * p.G - row0);        // rows with a query token
-      const int kmax = keys_seen(wk.s, min(wk.s.n - 1, (row0 + RT - 1) / p.G));   // keys any row sees
-      const int kmin = keys_seen(wk.s, row0 / p.G);                               // ... every row sees
+      const int rows = min(RT, (wk.s.n << p.gs) - row0);        // rows with a query token
+      const int kmax = keys_seen(wk.s, min(wk.s.n - 1, (row0 + RT - 1) >> p.gs));   // keys any row sees
+      const int kmin = keys_seen(wk.s, row0 >> p.gs);                               // ... every row sees
       // The exponents of a thread's key, loaded a tile ahead of their use.
       const long long exp_base = (static_cast<long long>(wk.b) * p.tail_cap) * p.Hkv + wk.g;
       uint32_t kb, vb;
@@ -692,36 +693,39 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
       load_exps(wk.tile0 * kTK + key_in_tile);
       for (int a = 1; a < kExpAhead; ++a) fetch_exps(wk.tile0 + a);
       named_sync(8, 128 * L::WG);   // the previous segment's row state is no longer read
-      if (st < RT) ms.seen[st] = st < rows ? keys_seen(wk.s, (row0 + st) / p.G) : 0;
-      // Q rows: 2^-e q = hi + lo, e as the append chooses it.  A warp's rows
-      // are all asked for before the first is converted.
+      if (st < RT) ms.seen[st] = st < rows ? keys_seen(wk.s, (row0 + st) >> p.gs) : 0;
+      // Q rows: 2^-e q = hi + lo, e as the append chooses it; the next row is
+      // loaded while one is converted.
       {
-        constexpr int E = D / 32, NR = RT / (4 * L::WG);
-        uint32_t w32[NR][E / 2];
+        constexpr int E = D / 32;
+        uint32_t ahead[E / 2];
+        auto load_row = [&](int n) {
 #pragma unroll
-        for (int k = 0; k < NR; ++k) {
-          const int n = (st >> 5) + k * 4 * L::WG, r = row0 + n;
-#pragma unroll
-          for (int e = 0; e < E / 2; ++e) w32[k][e] = 0u;
-          if (n < rows) {
-            const __nv_bfloat16* src = p.q + ((static_cast<long long>(wk.b) * p.T + r / p.G) * p.Hkv * p.G + wk.g * p.G + r % p.G) * D + lane * E;
-            if constexpr (E == 8) {
-              const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
-              w32[k][0] = x.x, w32[k][1] = x.y, w32[k][2] = x.z, w32[k][3] = x.w;
-            } else if constexpr (E == 4) {
-              const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
-              w32[k][0] = x.x, w32[k][1] = x.y;
-            } else {
-              w32[k][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-            }
+          for (int e = 0; e < E / 2; ++e) ahead[e] = 0u;
+          if (n >= rows) return;
+          const int r = row0 + n;
+          const long long token = static_cast<long long>(wk.b) * p.T + (r >> p.gs);
+          const __nv_bfloat16* src = p.q + (((token * p.Hkv + wk.g) << p.gs) + (r & ((1 << p.gs) - 1))) * D + lane * E;
+          if constexpr (E == 8) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
+            ahead[0] = x.x, ahead[1] = x.y, ahead[2] = x.z, ahead[3] = x.w;
+          } else if constexpr (E == 4) {
+            const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+            ahead[0] = x.x, ahead[1] = x.y;
+          } else {
+            ahead[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
           }
-        }
+        };
+        load_row(st >> 5);
+#pragma unroll 1
+        for (int n = st >> 5; n < RT; n += 4 * L::WG) {
+          uint32_t w32[E / 2];
 #pragma unroll
-        for (int k = 0; k < NR; ++k) {
-          const int n = (st >> 5) + k * 4 * L::WG;
+          for (int e = 0; e < E / 2; ++e) w32[e] = ahead[e];
+          load_row(n + 4 * L::WG);
           uint32_t top = 0;
 #pragma unroll
-          for (int e = 0; e < E / 2; ++e) top = max(top, max(w32[k][e] & 0x7FFFu, (w32[k][e] >> 16) & 0x7FFFu));
+          for (int e = 0; e < E / 2; ++e) top = max(top, max(w32[e] & 0x7FFFu, (w32[e] >> 16) & 0x7FFFu));
           top = __reduce_max_sync(0xffffffffu, top);
           const int ex = max(static_cast<int>(top >> 7) - 8 + ((top & 0x7Fu) > 96u ? 1 : 0), 1);
           const bool poison = (top >> 7) == 255u;
@@ -731,8 +735,8 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
           uint32_t hi[E / 2], lo[E / 2];
 #pragma unroll
           for (int e = 0; e < E / 2; ++e) {
-            const float a = poison ? 0.f : __uint_as_float(w32[k][e] << 16) * up;
-            const float b = poison ? 0.f : __uint_as_float(w32[k][e] & 0xFFFF0000u) * up;
+            const float a = poison ? 0.f : __uint_as_float(w32[e] << 16) * up;
+            const float b = poison ? 0.f : __uint_as_float(w32[e] & 0xFFFF0000u) * up;
             hi[e] = to_e4m3x2(a, b);
             const float2 h = from_e4m3x2(hi[e]);
             lo[e] = to_e4m3x2(a - h.x, b - h.y);
@@ -953,7 +957,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
       if (st == 0) {
         int2* r = p.runs_of + (static_cast<long long>(wk.b) * p.Hkv + wk.g) * p.row_tiles + wk.rt;
         if (wk.tile0 == 0) r->x = run;
-        if (wk.tile0 + nt == unit_tiles(wk.s, wk.rt, RT, p.G)) r->y = run;
+        if (wk.tile0 + nt == unit_tiles(wk.s, wk.rt, RT, p.gs)) r->y = run;
       }
       named_sync(1 + wg, 128);   // wm is free
       const float sum = across_lanes(l, lane, SumOp());
@@ -1015,7 +1019,7 @@ struct MergeParams {
   const int* n_new;
   __nv_bfloat16* out;
   int rows;                   // B * T * Hq
-  int T, Hq, Hkv, G, tail_cap, row_tiles, RT;
+  int T, Hq, Hkv, gs, tail_cap, row_tiles, RT;
   int splits, m_tiles;
   int head_slots;             // partial slots of one head: its units and runs
 };
@@ -1040,17 +1044,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) stream_merge_kernel(const Me
   if (live) {
     const int bt = rr / p.Hq, h = rr - bt * p.Hq;
     const int b = bt / p.T, t = bt - b * p.T;
-    const int g = h / p.G, gh = h - g * p.G;
-    const int r = t * p.G + gh, rt = r / p.RT;
+    const int g = h >> p.gs, gh = h & ((1 << p.gs) - 1);
+    const int r = (t << p.gs) + gh, rt = r / p.RT;
     const int unit = (b * p.Hkv + g) * p.row_tiles + rt;
     const int2 runs = __ldcg(p.runs_of + unit);   // (read beside the lengths; used only where the unit has tiles)
     const StreamLen s = stream_len(p.tail_len, p.n_new, b, p.T, p.tail_cap);
     live = t < s.n;
-    const int ut = live ? unit_tiles(s, rt, p.RT, p.G) : 0;
+    const int ut = live ? unit_tiles(s, rt, p.RT, p.gs) : 0;
     const int tails = ut > 0 ? runs.y - runs.x + 1 : 0;
     const long long tail_row =   // the first tail partial's row
         (static_cast<long long>(g) * p.head_slots + b * p.row_tiles + rt + runs.x) * p.RT + r % p.RT;
-    const int row = bt * p.G + gh;             // row of the shared segment
+    const int row = (bt << p.gs) + gh;             // row of the shared segment
     const long long su = (g * static_cast<long long>(p.m_tiles) + (row >> 7)) * p.splits;
     const int si = row & 127;
     const int count = live ? p.splits + tails : 0;
@@ -1230,7 +1234,7 @@ cudaError_t launch_streams_quant(const QuantStreams& a, const AttnLaunch& al, si
   tp.err = al.err;
   tp.B = a.B;
   tp.T = a.T;
-  tp.G = G;
+  while (1 << tp.gs < G) ++tp.gs;   // G is a power of two
   tp.Hkv = a.Hkv;
   tp.tail_cap = a.tail_cap;
   tp.row_tiles = (a.T * G + RT - 1) / RT;
@@ -1272,7 +1276,7 @@ cudaError_t launch_streams_quant(const QuantStreams& a, const AttnLaunch& al, si
   mp.T = a.T;
   mp.Hq = a.Hq;
   mp.Hkv = a.Hkv;
-  mp.G = G;
+  mp.gs = tp.gs;
   mp.tail_cap = a.tail_cap;
   mp.row_tiles = tp.row_tiles;
   mp.RT = RT;
