@@ -489,7 +489,10 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
   // THREADS streams a round; with more streams a second sweep finds the run's
   // first.
   {
-    auto scan_round = [&](int b, long long carry, long long* mine) {   // returns the carry after the round
+    // One round over the streams from b0 on; returns the carry after it.
+    auto scan_round = [&](int b0, long long carry, long long* mine) {
+      const int b = b0 + threadIdx.x;
+      const int warps = (min(p.B - b0, THREADS) + 31) / 32;   // that have a stream
       long long c = 0;
       if (b < p.B) c = head_tiles(stream_len(p.tail_len, p.n_new, b, p.T, p.tail_cap), p.row_tiles, RT, p.gs);
       long long inc = c;
@@ -502,7 +505,8 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
       if (lane == 31) ms.scan[warp] = inc;
       __syncthreads();
       long long before = carry, total = carry;
-      for (int w = 0; w < THREADS / 32; ++w) {
+#pragma unroll 1
+      for (int w = 0; w < warps; ++w) {
         if (w < warp) before += ms.scan[w];
         total += ms.scan[w];
       }
@@ -511,7 +515,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
       return total;
     };
     long long mine[2], total = 0;
-    for (int b0 = 0; b0 < p.B; b0 += THREADS) total = scan_round(b0 + threadIdx.x, total, mine);
+    for (int b0 = 0; b0 < p.B; b0 += THREADS) total = scan_round(b0, total, mine);
     const unsigned long long C = static_cast<unsigned long long>(total);
     const unsigned int A = static_cast<unsigned int>(min(static_cast<unsigned long long>(p.runs), C));
     const unsigned int run = blockIdx.x / p.heads;
@@ -521,7 +525,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
     long long carry = 0;
     for (int b0 = 0; b0 < p.B; b0 += THREADS) {
       const int b = b0 + threadIdx.x;
-      if (p.B > THREADS) carry = scan_round(b, carry, mine);
+      if (p.B > THREADS) carry = scan_round(b0, carry, mine);
       if (b < p.B && active && first >= mine[0] && first < mine[0] + mine[1]) {
         long long off = first - mine[0];
         const StreamLen s = stream_len(p.tail_len, p.n_new, b, p.T, p.tail_cap);
@@ -941,7 +945,9 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
           const int slot = it % NS;
           mbar_wait(BAR(TB_FULL + slot), (it / NS) & 1, abort_flag);
           if (key >= kmax) {
+#pragma unroll 1
             for (int c = 0; c < L::KB; ++c)
+#pragma unroll
               for (int y = 0; y < ROW; y += 16)
                 st_shared_v4(sRing + slot * L::TILE + c * L::BLOCK + key_in_tile * ROW + y, 0u, 0u, 0u, 0u);
           }
@@ -972,7 +978,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
       __syncwarp();
       tc_fence_after();
       if (D >= 128 || quarter < D / 32) {
-#pragma unroll
+#pragma unroll 1
         for (int ob = 0; ob < L::OB; ++ob) {
           float o[CW];
           const uint32_t at = tmem + L::TM_O + ob * L::NW + n0 + lane_off;
