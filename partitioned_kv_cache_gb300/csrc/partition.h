@@ -137,12 +137,13 @@ inline bool choose_partition(const PartitionRequest& r, PartitionChoice* out) {
 //    at most half of the SMs, and one CTA a unit at least.
 //  * The tails get the other SMs, or, where the store holds far more than its
 //    share, all of them, some after the store.
-// Measured (SMs for the store / for the tails; one call): 80 queries over 8448
-// shared keys and tails to 2000 tokens, 76/76: 26.4 us, 32/120: 33.6, 135/152:
-// 37.4; 64 queries over these and tails to 4096, 48/104: 27.8, 76/152: 38.5;
-// 64 x 8 queries over 2304 keys and tails to 16384, 64/152: 116.6, 64/88: 168;
-// 32 queries, tails to 16000, 34/118: 39.2, 76/76: 45.6.  One after the other
-// the first, third and fourth took 39.3, 133 and 48.1 us.
+// Measured (SMs for the store / for the tails, us a call): 80 queries over 8448
+// shared keys and tails to 2000 tokens, 76/76 25.0, 32/120 32.9, 152/152 35.7;
+// 64 queries over these and tails to 4096, 48/104 28.2, 76/152 37.1; 64 x 8
+// queries over 2304 keys and tails to 16384, 76/152 108.6, 64/88 134.8, 128/152
+// 113.3; 32 queries, tails to 16000, 34/118 40.5, 76/76 46.0.  One kernel after
+// the other these took 38.5, 43.7, 124.3 and 47.6 us, and 16 queries over 2112
+// keys with tails to 30 tokens 21.0 instead of 14.2.
 struct StreamPartition {
   int splits;     // key slices of each unit of the store
   int tail_sms;   // SMs that the tails' grid is made for

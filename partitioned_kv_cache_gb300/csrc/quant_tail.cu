@@ -70,10 +70,10 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& x, uint2* codes) {
 // of K and of V for kPerThread vectors, all loads in flight before the first
 // conversion.  A CTA's vectors are consecutive in the stream's new tokens, so
 // their codes land in consecutive places too.  Bound by memory: 24 prompts of
-// up to 8191 tokens at D = 256 (170 MB) take 32.3 us, 5.3 TB/s, with four
-// vectors a thread, 33.1 with two and 38.6 with one; calls that fit on the GPU
+// up to 8191 tokens at D = 256 (170 MB) take 28.2 us, 6.0 TB/s, with four
+// vectors a thread, 29.3 with two and 33.3 with one; calls that fit on the GPU
 // at once are bound by latency and faster with one (16 tokens: 1.7 against
-// 2.2 us, 61 x 8 tokens of 8 heads: 2.6 against 3.2 us).
+// 1.9 us, 61 x 8 tokens of 8 heads: 2.5 against 3.1 us).
 template <int D, int kPerThread>
 __global__ void __launch_bounds__(kAppendThreads) tail_append_quant_kernel(
     uint2* __restrict__ k_tail, uint2* __restrict__ v_tail, uint8_t* __restrict__ k_exp,
