@@ -264,7 +264,8 @@ rx_status rx_tail_append(void* k_tail, void* v_tail, int* tail_len, const void* 
  * [0, tail_cap] and n_new[b] > 0).  new_len[b] = min(tail_len[b] + n_new[b],
  * tail_cap) (or tail_len[b] where that is outside).  tail_len itself is not
  * changed, so the appends of all layers can share it; new_len is what the
- * attention of the same step reads.
+ * attention of the same step reads.  (A stream that overflowed no longer holds
+ * its newest tokens: it has to be retired before it attends.)
  * k_tail, v_tail: e4m3 [B][tail_cap][Hkv][D]; k_exp, v_exp: uint8
  * [B][tail_cap][Hkv]; k_new, v_new: bf16 [B][T][Hkv][D]; tail_len, new_len,
  * n_new: DEVICE int32 [B] (n_new NULL: T for every stream; values are clamped
@@ -326,6 +327,7 @@ rx_status rx_attend_streams_quant(rx_cache_t cache, int layer, const rx_quant_st
  * [0, V) is not accepted.  q NULL: the drafts carry no probabilities, q is 1
  * at x_t and 0 elsewhere.  n_draft[b] < 0 marks an idle slot: n_accept = -1,
  * tokens -1, new_len[b] = tail_len[b].  T = 0 samples one token from p[b][0].
+ * The entries of p and q are probabilities: at least 0, their sums finite.
  * new_len[b] = tail_len[b] + 1 + a: the keys to keep when tail_len[b] counts
  * those before the step, which appended the last token and the drafts.
  * Products are taken in 64 bits, differences and sums to 46 bits or more, in

@@ -119,21 +119,19 @@ __device__ __forceinline__ double lane_scan(double v, int lane) {
   return v;
 }
 
-// The totals of this CTA's warps, one per lane of warp 0 (zeros past them),
-// as an inclusive sum.
-__device__ __forceinline__ double warp_totals(const float2* s_warp, int lane) {
+// The total of warp `lane` of this CTA (0 past the last).
+__device__ __forceinline__ double warp_total(const float2* s_warp, int lane) {
   const float2 t = lane < kVerifyWarps ? s_warp[lane] : make_float2(0.f, 0.f);
-  return lane_scan(static_cast<double>(t.x) + static_cast<double>(t.y), lane);
+  return static_cast<double>(t.x) + static_cast<double>(t.y);
 }
 
-// The first lane whose inclusive sum on top of `base` is above `want`; where
-// rounding hides the crossing, the last one that added something (-1: none).
-// *before: the sum in front of that lane, base included.
-__device__ __forceinline__ int crossing(double inclusive, double base, double want, int lane, double* before) {
-  const double up = __shfl_up_sync(0xffffffffu, inclusive, 1);
-  const bool adds = inclusive > (lane ? up : 0.0);
-  const uint32_t over = __ballot_sync(0xffffffffu, adds && base + inclusive > want);
-  const uint32_t some = __ballot_sync(0xffffffffu, adds);
+// The first lane with something of its own (own > 0) whose inclusive sum on
+// top of `base` is above `want`; where rounding hides the crossing, the last
+// one with something (-1: none).  *before: the sum in front of that lane, base
+// included.
+__device__ __forceinline__ int crossing(double own, double inclusive, double base, double want, int lane, double* before) {
+  const uint32_t over = __ballot_sync(0xffffffffu, own > 0.0 && base + inclusive > want);
+  const uint32_t some = __ballot_sync(0xffffffffu, own > 0.0);
   const int w = over ? __ffs(over) - 1 : 31 - __clz(some);
   const double in = __shfl_sync(0xffffffffu, inclusive, max(w, 1) - 1);
   *before = w > 0 ? base + in : base;
@@ -171,7 +169,7 @@ __device__ __forceinline__ TwoSum span_sum(const P* pr, const P* qr, int out, in
         float pf[E], qf[E];
         widen(pv[k], pf);
         widen(qv[k], qf);
-        if (static_cast<unsigned>(out - at) < static_cast<unsigned>(E)) {   // one vector of the row, if any
+        if (static_cast<unsigned>(out) - static_cast<unsigned>(at) < static_cast<unsigned>(E)) {   // one vector of the row, if any
 #pragma unroll
           for (int e = 0; e < E; ++e)
             if (at + e == out) pf[e] = 0.f;
@@ -273,9 +271,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_drafts_kernel(const 
     const TwoSum t = span_sum<P, VEC>(pr, qr, out, v0, v1, lane);
     if (lane == 0) s_warp[warp] = make_float2(t.sum, t.rest);
     __syncthreads();
-    double inclusive = 0.0;
+    double own = 0.0, inclusive = 0.0;
     if (warp == 0) {
-      inclusive = warp_totals(s_warp, lane);
+      own = warp_total(s_warp, lane);
+      inclusive = lane_scan(own, lane);
       const double cta = __shfl_sync(0xffffffffu, inclusive, 31);
       if (lane < a.cluster) st_cluster_f64(smem_u32(&s_cta[form][rank]), lane, cta);
     }
@@ -284,12 +283,12 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_drafts_kernel(const 
     // ---- which warp's span holds the threshold
     if (warp == 0) {
       const double r = fminf(fmaxf(a.r[b], 0.f), 0x1.fffffep-1f);   // [0, 1); NaN: 0
-      const double ctas = lane_scan(lane < a.cluster ? s_cta[form][lane] : 0.0, lane);
+      const double cta = lane < a.cluster ? s_cta[form][lane] : 0.0, ctas = lane_scan(cta, lane);
       const double total = __shfl_sync(0xffffffffu, ctas, 31);
       const double want = r * total;
       double base, inner;
-      const int c = crossing(ctas, 0.0, want, lane, &base);
-      const int w = crossing(inclusive, base, want, lane, &inner);   // meaningful in CTA c
+      const int c = crossing(cta, ctas, 0.0, want, lane, &base);
+      const int w = crossing(own, inclusive, base, want, lane, &inner);   // meaningful in CTA c
       if (lane == 0) {
         s_any = total > 0.0;
         s_pick = c == rank ? w : -1;
@@ -317,7 +316,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_drafts_kernel(const 
     const double want = s_want;
     if (warp == 0) {
       double inner;
-      const int w = crossing(warp_totals(s_warp, lane), s_base, want, lane, &inner);
+      const double own = warp_total(s_warp, lane);
+      const int w = crossing(own, lane_scan(own, lane), s_base, want, lane, &inner);
       __syncwarp();
       if (lane == 0) {
         s_pick = w;

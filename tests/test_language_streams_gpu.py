@@ -585,6 +585,29 @@ def test_verify_edges(rx):
     _verify(rx, p, None, draft, u, r, [T, T, 0, 1, 2, T, T, 0, 0, 0, 0, -7], torch.float32)
 
 
+@pytest.mark.parametrize("V", [300, 5000, 40000, 257153])
+def test_verify_weights_far_apart(rx, V):
+    """Few tokens with weight, in different CTAs' and warps' parts, and
+    thresholds at the ends: never a token without weight."""
+    import torch
+    at = sorted({0, 5, V // 3, V // 2 + 1, V - 7, V - 1})
+    rows, r = [], []
+    for i in at:
+        p = np.zeros(V, np.float32)
+        p[i] = 1
+        rows += [p, p]
+        r += [0.0, 1 - 2.0 ** -24]
+    for i, j in zip(at, at[1:]):
+        p = np.zeros(V, np.float32)
+        p[i], p[j] = 0.25, 0.75
+        rows += [p] * 4
+        r += [0.0, 0.25 - 2.0 ** -26, 0.25, 1 - 2.0 ** -24]
+    p = np.stack(rows)[:, None]
+    n = len(rows)
+    _verify(rx, p, None, np.zeros((n, 0), np.int64), np.zeros((n, 0), np.float32), np.array(r, np.float32), None,
+            torch.float32)
+
+
 def test_verify_lengths_in_place_and_graph(rx):
     import torch
     g = np.random.default_rng(8)
