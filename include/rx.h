@@ -310,8 +310,10 @@ typedef struct rx_quant_streams {
  * the current one.  out may not overlap an input.  The cache reads its store on
  * a stream of its own meanwhile, forked from `stream` and joined to it again
  * within the call (under capture too): to the caller it is ordered on `stream`.
+ * From the first captured call to the end of its capture, calls of this cache
+ * outside that capture are refused.
  * Errors: RX_ERR_ARG, RX_ERR_LAYER, RX_ERR_CAPACITY, RX_ERR_STATE (another
- * device is current), RX_ERR_CUDA. */
+ * device is current, another stream is capturing), RX_ERR_CUDA. */
 rx_status rx_attend_streams_quant(rx_cache_t cache, int layer, const rx_quant_streams* streams,
                                   void* stream);
 

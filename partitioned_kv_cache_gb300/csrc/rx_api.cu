@@ -670,6 +670,17 @@ rx_status rx_attend_streams_quant(rx_cache_t h, int layer, const rx_quant_stream
   if (e != cudaSuccess) return cuda_fail(e, "rx_attend_streams_quant: cudaGetDevice");
   if (dev != h->device)
     return fail(RX_ERR_STATE, "rx_attend_streams_quant: the cache is on device %d, the current device is %d", h->device, dev);
+  // While a capture holds the cache's stream, a call from outside of it could
+  // not be forked, and trying would end the capture.
+  cudaStreamCaptureStatus held = cudaStreamCaptureStatusNone, own = cudaStreamCaptureStatusNone;
+  unsigned long long held_id = 0, own_id = 0;
+  e = cudaStreamGetCaptureInfo(h->fork.side, &held, &held_id);
+  if (e == cudaSuccess && held != cudaStreamCaptureStatusNone) {
+    e = cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &own, &own_id);
+    if (e == cudaSuccess && (own == cudaStreamCaptureStatusNone || own_id != held_id))
+      return fail(RX_ERR_STATE, "rx_attend_streams_quant: a call of this cache is being captured on another stream");
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "rx_attend_streams_quant: cudaStreamGetCaptureInfo");
   const rx::AttnLaunch a = make_launch(h, layer);
   rx::QuantStreams s{};
   s.q = static_cast<const __nv_bfloat16*>(b.q);

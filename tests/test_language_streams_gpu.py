@@ -466,6 +466,33 @@ def test_attention_graph_follows_growing_tails(rx):
             _check(got[b], ref, spread)
 
 
+def test_attention_outside_a_capture_is_refused(rx):
+    """A call on another stream while one of this cache is being captured: it
+    is refused, the capture goes on, and both work once it has ended."""
+    import torch
+    g = np.random.default_rng(28)
+    st = Store(rx, g, 8, 1, 64, 16, 1, 16, 40, 4, pushes=1)
+    kc, ke, vc, ve = _tails(g, 2, 40, 1, 64)
+    q = dev(_bits(g, (2, 1, 8, 64)))
+    args = (q, _codes(kc), _codes(vc), torch.from_numpy(ke).cuda(), torch.from_numpy(ve).cuda(), _int([40, 13]))
+    first = st.cache.attend_streams_quant(0, *args)
+    outs = [torch.zeros_like(first) for _ in range(3)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        st.cache.attend_streams_quant(0, *args, out=outs[0])
+        with pytest.raises(rx.RxError) as e:
+            st.cache.attend_streams_quant(0, *args, out=outs[2], stream=side)
+        assert e.value.status == -7
+        st.cache.attend_streams_quant(0, *args, out=outs[1])
+    graph.replay()
+    torch.cuda.synchronize()
+    st.cache.attend_streams_quant(0, *args, out=outs[2], stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(first, o) for o in outs)
+
+
 def test_attention_on_another_stream(rx):
     import torch
     g = np.random.default_rng(25)
