@@ -92,6 +92,16 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// A CTA may write into a peer's shared memory only once that peer has started:
+// every thread of the cluster arrives early, and waits before the first such
+// write (no ordering of memory is needed for that, hence relaxed).
+__device__ __forceinline__ void cluster_arrive_started() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_started() {
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // Every thread of every CTA in the cluster must call this the same number of
 // times.  Release/acquire at cluster scope: memory writes made before it by
 // any thread of the cluster are visible to the cluster's reads after it.

@@ -228,6 +228,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_drafts_kernel(const 
     }
     return;
   }
+  // Totals are pushed into the peers' shared memory below; the matching wait
+  // in front of them guarantees that every CTA of the cluster has started.
+  if (a.cluster > 1) cluster_arrive_started();
   // ---- accepted tokens, 32 positions at a time
   if (warp == 0) {
     int acc = n;
@@ -271,6 +274,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_drafts_kernel(const 
     const TwoSum t = span_sum<P, VEC>(pr, qr, out, v0, v1, lane);
     if (lane == 0) s_warp[warp] = make_float2(t.sum, t.rest);
     __syncthreads();
+    if (form == 0 && a.cluster > 1) cluster_wait_started();
     double own = 0.0, inclusive = 0.0;
     if (warp == 0) {
       own = warp_total(s_warp, lane);

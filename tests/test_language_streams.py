@@ -175,3 +175,19 @@ def test_binding_refuses_shapes_and_types(lib):
         rx.verify_drafts(p, None, d, u, r, new_len=z(2, dtype=i32))
     with pytest.raises(ValueError, match="CUDA"):
         rx.verify_drafts(p, None, d, u, r)
+
+
+# ------------------------------------------------------------ cluster starts
+@pytest.mark.parametrize("name,write", [("verify_drafts.cu", "st_cluster_f64("), ("adarmsnorm.cu", "mapa.")])
+def test_peers_have_started_before_their_shared_memory_is_written(name, write):
+    """A kernel that stores into its cluster's shared memory arrives on the
+    cluster's barrier early and waits for it in front of the first store."""
+    import os
+    import re
+    from tests._util import ROOT
+    src = open(os.path.join(ROOT, "partitioned_kv_cache_gb300", "csrc", name)).read()
+    src = re.sub(r"//[^\n]*", "", src)
+    kernel = [k for k in src.split("__global__")[1:] if write in k]
+    assert len(kernel) == 1
+    at = [kernel[0].find(x) for x in ("cluster_arrive_started();", "cluster_wait_started();", write)]
+    assert -1 < at[0] < at[1] < at[2], at

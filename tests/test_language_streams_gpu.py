@@ -635,6 +635,38 @@ def test_verify_weights_far_apart(rx, V):
             torch.float32)
 
 
+@pytest.mark.parametrize("V", [5000, 10000, 60000])
+def test_verify_clusters_beside_other_work(rx, V):
+    """Clusters of 2, 4 and 8 CTAs whose CTAs start at different times, because
+    other kernels hold SMs: every call gives what it gives alone, idle slots
+    and rows without any difference among them."""
+    import torch
+    g = np.random.default_rng(V)
+    B, T = 24, 2
+    p = _softmax(g.standard_normal((B, T + 1, V)))
+    q = _softmax(g.standard_normal((B, T, V)))
+    q[3] = p[3, :T]
+    p[4, 0], q[4, 0] = 0.5 * q[4, 0], q[4, 0]
+    u, r = g.random((B, T), dtype=np.float32), g.random(B, dtype=np.float32)
+    n = [T] * B
+    n[5] = n[23] = -1
+    draft = g.integers(0, V, (B, T))
+    _verify(rx, p, q, draft, u, r, n, torch.float32)
+    args = [torch.from_numpy(x).cuda() for x in (p, q)] + [_int(draft), torch.from_numpy(u).cuda(), torch.from_numpy(r).cuda()]
+    n = _int(n)
+    want = rx.verify_drafts(*args, n_draft=n)
+    side = torch.cuda.Stream()
+    busy = torch.randn(4096, 4096, device="cuda", dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(40):
+        with torch.cuda.stream(side):
+            busy @ busy
+        got.append(rx.verify_drafts(*args, n_draft=n))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for a in got for x, y in zip(a[:2], want))
+
+
 def test_verify_lengths_in_place_and_graph(rx):
     import torch
     g = np.random.default_rng(8)
