@@ -451,6 +451,18 @@ rx_status rx_debug_choose_partition(int t_max, int units, int D, int num_sms, in
                                     int forced_splits, int forced_dparts, const int* cluster_capacity,
                                     int* splits, int* dparts, int* fused);
 
+/* Test aid: how rx_attend_streams_quant shares out the GPU, computed on the
+ * host.  The shared store is read by units x *splits CTAs (units = 128-row
+ * query tiles x K/V heads, t_max key tiles of 64 each), the tails, which hold
+ * at most tail_tiles key tiles of 128, by a grid made for *tail_sms SMs.
+ * max_splits: the most slices of the store that the cache's workspace holds
+ * (the call takes 32 at most).  Touches no device.
+ * Errors: RX_ERR_ARG (a null pointer, units, num_sms or max_splits below 1, a
+ * negative size, or one above 2^20 (t_max, units), 2^48 (tail_tiles) or 2^16
+ * (num_sms, max_splits)). */
+rx_status rx_debug_choose_stream_partition(int t_max, int units, long long tail_tiles, int num_sms,
+                                           int max_splits, int* splits, int* tail_sms);
+
 /* Number of split-KV partitions for attention launches of this cache
  * (0 = chosen from the SM count, the default).  A tuning knob: results are
  * the same for every value up to rounding order.  Errors: RX_ERR_ARG (null

@@ -133,17 +133,22 @@ inline bool choose_partition(const PartitionRequest& r, PartitionChoice* out) {
 // for.  A 64-key tile of the store takes about half as long as a 128-key tile
 // of a tail, of which there are at most `tail_tiles`.
 //  * The store gets its share of the work in SMs; where that is small, enough
-//    for two tiles a CTA (the tails may be much shorter than their capacity);
-//    at most half of the SMs, and one CTA a unit at least.
-//  * The tails get the other SMs, or, where the store holds far more than its
-//    share, all of them, some after the store.
-// Measured (SMs for the store / for the tails, us a call): 80 queries over 8448
-// shared keys and tails to 2000 tokens, 76/76 25.0, 32/120 32.9, 152/152 35.7;
-// 64 queries over these and tails to 4096, 48/104 28.2, 76/152 37.1; 64 x 8
-// queries over 2304 keys and tails to 16384, 76/152 108.6, 64/88 134.8, 128/152
-// 113.3; 32 queries, tails to 16000, 34/118 40.5, 76/76 46.0.  One kernel after
-// the other these took 38.5, 43.7, 124.3 and 47.6 us, and 16 queries over 2112
-// keys with tails to 30 tokens 21.0 instead of 14.2.
+//    for two or three tiles a CTA (the tails may be much shorter than their
+//    capacity); at most half of the SMs, and one CTA a unit at least.
+//  * The tails get the other SMs, if those are at least three quarters of what
+//    their own work is worth; otherwise, and where the store holds far more
+//    than its share, they get all SMs, some after the store.
+// Measured (SMs for the store / for the tails, us a call; the first is taken):
+// 80 queries over 8448 shared keys and tails to 2000 tokens, 75/77 24.8, 30/122
+// 33.2, 75/152 32.8; 64 x 8 queries over 2304 keys and tails to 16384, 64/152
+// 108.7, 64/88 134.0, 128/152 113.6; 32 queries over 2112 keys and tails to
+// 16000, 22/130 39.8, 34/118 41.0, 22/152 41.3; 72 x 4 queries of 64/8 heads
+// (D = 128) over 8448 keys and tails to 512, 144/152 135.6, 144/8 333; 8 prompts
+// of 302 tokens over 8448 keys, 151/152 204, 151/1 4043.  (64 queries over 8448
+// keys and tails to 4096 would gain from another choice: 76/152 40.9, 48/104
+// 33.1.)  One kernel after the other the first three took 38.5, 124.3 and 47.6
+// us, and 16 queries over 2112 keys with tails to 30 tokens 21.0 instead of 14.2
+// (17/135).
 struct StreamPartition {
   int splits;     // key slices of each unit of the store
   int tail_sms;   // SMs that the tails' grid is made for
@@ -164,8 +169,9 @@ inline StreamPartition choose_stream_partition(int units, int t_max, long long t
   const long long held = sp * units;
   StreamPartition r;
   r.splits = static_cast<int>(sp);
-  r.tail_sms = held <= share + share / 4 || held <= num_sms / 4 ? static_cast<int>(num_sms - held) : num_sms;
-  if (r.tail_sms < 1) r.tail_sms = num_sms;
+  const long long rest = num_sms - held;
+  const bool beside = held <= share + share / 4 || held <= num_sms / 4;
+  r.tail_sms = static_cast<int>(beside && 4 * rest >= 3 * (num_sms - share) ? rest : num_sms);
   return r;
 }
 

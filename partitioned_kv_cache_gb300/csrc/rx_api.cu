@@ -1083,6 +1083,20 @@ rx_status rx_debug_choose_partition(int t_max, int units, int D, int num_sms, in
   RX_GUARD_END
 }
 
+rx_status rx_debug_choose_stream_partition(int t_max, int units, long long tail_tiles, int num_sms, int max_splits,
+                                           int* splits, int* tail_sms) {
+  RX_GUARD_BEGIN
+  if (!splits || !tail_sms) return fail(RX_ERR_ARG, "rx_debug_choose_stream_partition: null pointer");
+  if (t_max < 0 || units < 1 || tail_tiles < 0 || num_sms < 1 || max_splits < 1 || t_max > (1 << 20) ||
+      units > (1 << 20) || tail_tiles > (1LL << 48) || num_sms > (1 << 16) || max_splits > (1 << 16))
+    return fail(RX_ERR_ARG, "rx_debug_choose_stream_partition: sizes out of range");
+  const rx::StreamPartition sp = rx::choose_stream_partition(units, t_max, tail_tiles, num_sms, max_splits);
+  *splits = sp.splits;
+  *tail_sms = sp.tail_sms;
+  return RX_OK;
+  RX_GUARD_END
+}
+
 rx_status rx_set_attn_dparts(rx_cache_t h, int dparts) {
   RX_GUARD_BEGIN
   if (!h) return fail(RX_ERR_ARG, "rx_set_attn_dparts: null cache");

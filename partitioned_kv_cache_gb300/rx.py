@@ -34,7 +34,7 @@ EXPORTS = ("rx_cache_create", "rx_cache_destroy", "rx_pin_prefix", "rx_push_fram
            "rx_snapshot_bytes", "rx_snapshot", "rx_restore", "rx_push_frame_async",
            "rx_set_attn_dparts", "rx_debug_inject_timeout", "rx_debug_choose_partition",
            "rx_attend_suffix_norms", "rx_attend_batch_norms", "rx_tail_append_quant",
-           "rx_attend_streams_quant", "rx_verify_drafts")
+           "rx_attend_streams_quant", "rx_verify_drafts", "rx_debug_choose_stream_partition")
 
 
 class RxConfig(ctypes.Structure):
@@ -98,6 +98,8 @@ _sigs = {
                                    ctypes.POINTER(RxNormRows), _i, _vp]),
     "rx_tail_append_quant": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp]),
     "rx_attend_streams_quant": (_i, [_vp, _i, ctypes.POINTER(RxQuantStreams), _vp]),
+    "rx_debug_choose_stream_partition": (_i, [_i, _i, ctypes.c_longlong, _i, _i, ctypes.POINTER(_i),
+                                              ctypes.POINTER(_i)]),
     "rx_verify_drafts": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]),
 }
 for _name, (_res, _args) in _sigs.items():
@@ -220,6 +222,15 @@ def choose_partition(t_max: int, units: int, D: int, num_sms: int, max_splits: i
                                           ctypes.byref(sp), ctypes.byref(dp), ctypes.byref(fu)),
            "rx_debug_choose_partition")
     return sp.value, dp.value, bool(fu.value)
+
+
+def choose_stream_partition(t_max: int, units: int, tail_tiles: int, num_sms: int, max_splits: int = 32):
+    """Test aid: (splits, tail_sms) of an attention call over language streams
+    with 8-bit tails (rx_debug_choose_stream_partition)."""
+    sp, ts = _i(0), _i(0)
+    _check(_lib.rx_debug_choose_stream_partition(t_max, units, tail_tiles, num_sms, max_splits, ctypes.byref(sp),
+                                                 ctypes.byref(ts)), "rx_debug_choose_stream_partition")
+    return sp.value, ts.value
 
 
 def library_path() -> str:

@@ -191,3 +191,45 @@ def test_peers_have_started_before_their_shared_memory_is_written(name, write):
     assert len(kernel) == 1
     at = [kernel[0].find(x) for x in ("cluster_arrive_started();", "cluster_wait_started();", write)]
     assert -1 < at[0] < at[1] < at[2], at
+
+
+# ------------------------------------- the SMs of the store and of the tails
+SMS = 152
+
+
+def test_stream_partition_leaves_the_tails_their_share(lib):
+    """Whatever the sizes, the tails' grid gets at least three quarters of the
+    SMs that its part of the work is worth, and what runs beside it fits."""
+    from partitioned_kv_cache_gb300 import rx
+    for units in range(1, 201):
+        for t_max in (0, 1, 6, 33, 36, 132, 500, 5000):
+            for tail_tiles in (0, 1, 16, 300, 2304, 2432, 8192, 10 ** 5, 10 ** 7):
+                splits, tail_sms = rx.choose_stream_partition(t_max, units, tail_tiles, SMS)
+                assert 1 <= splits <= max(1, min(t_max, 32))
+                assert tail_sms == SMS or tail_sms == SMS - splits * units
+                store = units * t_max
+                share = SMS * 2 * tail_tiles / (store + 2 * tail_tiles + 1)
+                assert 1 <= tail_sms and tail_sms >= 0.75 * share - 1, (units, t_max, tail_tiles, splits, tail_sms)
+
+
+@pytest.mark.parametrize("name,units,t_max,tail_tiles,want", [
+    ("64/8 heads of 128, 72 x 4 tokens, 8448 keys, tails of 512", 144, 132, 2304, (1, 152)),
+    ("8 prompts of 302 tokens, 8448 keys, tails of 1024", 151, 132, 2432, (1, 152)),
+    ("16 tokens, 2112 keys, tails of 32", 1, 33, 16, (17, 135)),
+    ("16 x 5 tokens, 8448 keys, tails of 2048", 5, 132, 256, (15, 77)),
+    ("7 x 3 tokens, 32/8 heads of 128, 337 keys, tails of 1001", 8, 6, 448, (3, 128)),
+    ("32 tokens, 2112 keys, tails of 16384", 2, 33, 4096, (11, 130)),
+    ("64 x 8 tokens, 2304 keys, tails of 16384", 32, 36, 8192, (2, 152)),
+    ("64 tokens, 8448 keys, tails of 4096", 4, 132, 2048, (19, 152)),
+])
+def test_stream_partition_choices(lib, name, units, t_max, tail_tiles, want):
+    from partitioned_kv_cache_gb300 import rx
+    assert rx.choose_stream_partition(t_max, units, tail_tiles, SMS) == want, name
+
+
+def test_stream_partition_refuses_sizes_out_of_range(lib):
+    from partitioned_kv_cache_gb300 import rx
+    for a in ((-1, 1, 1, 152, 32), (1, 0, 1, 152, 32), (1, 1, -1, 152, 32), (1, 1, 1, 0, 32), (1, 1, 1, 152, 0),
+              ((1 << 20) + 1, 1, 1, 152, 32), (1, (1 << 20) + 1, 1, 152, 32), (1, 1, (1 << 48) + 1, 152, 32)):
+        with pytest.raises(rx.RxError):
+            rx.choose_stream_partition(*a)
