@@ -247,9 +247,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_drafts_kernel(const 
         if (x >= 0 && x < V) {
           const float px = prob(p, (bt + b) * V + x);
           const float qx = q ? prob(q, bt * V + x) : 1.f;
-          // u * q < p with the product in full: rounded, and its exact error.
-          const float ux = ut * qx, rest = fmaf(ut, qx, -ux);
-          refuse = !(ux < px || (ux == px && rest < 0.f));
+          // u * q < p with the product in full: 48 bits, whose exponent fits
+          // a double whatever the factors are (fp32 with its rounding error
+          // lost the error of products near the smallest subnormal).
+          refuse = !(static_cast<double>(ut) * static_cast<double>(qx) < static_cast<double>(px));
         }
       }
       const uint32_t ballot = __ballot_sync(0xffffffffu, refuse);

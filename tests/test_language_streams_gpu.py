@@ -635,6 +635,24 @@ def test_verify_weights_far_apart(rx, V):
             torch.float32)
 
 
+def test_verify_probabilities_near_the_smallest_number(rx):
+    """u * q(x) and p(x) within a few steps of 2^-149 of each other, where the
+    product's rounding error is no fp32 number."""
+    import torch
+    g = np.random.default_rng(41)
+    B, T, V = 256, 1, 40
+    p, q = _softmax(g.standard_normal((B, T + 1, V))), _softmax(g.standard_normal((B, T, V)))
+    draft = g.integers(0, V, (B, T))
+    m, k = g.integers(1, 9, B), g.integers(0, 6, B)
+    at = np.arange(B)
+    q[at, 0, draft[:, 0]] = (m * 2.0 ** -149).astype(np.float32)
+    p[at, 0, draft[:, 0]] = (k * 2.0 ** -149).astype(np.float32)
+    u, r = g.random((B, T), dtype=np.float32), g.random(B, dtype=np.float32)
+    near = np.abs(u[:, 0].astype(np.float64) * m - k) < 0.5
+    assert near.sum() > 20 and ((u[:, 0].astype(np.float64) * m < k) & near).sum() > 5
+    _verify(rx, p, q, draft, u, r, None, torch.float32)
+
+
 @pytest.mark.parametrize("V", [5000, 10000, 60000])
 def test_verify_clusters_beside_other_work(rx, V):
     """Clusters of 2, 4 and 8 CTAs whose CTAs start at different times, because
