@@ -332,8 +332,11 @@ rx_status rx_attend_streams_quant(rx_cache_t cache, int layer, const rx_quant_st
  * The entries of p and q are probabilities: at least 0, their sums finite.
  * new_len[b] = tail_len[b] + 1 + a: the keys to keep when tail_len[b] counts
  * those before the step, which appended the last token and the drafts.
- * Products are taken in 64 bits, differences and sums to 46 bits or more, in
- * a fixed order.
+ * Products and differences are taken without a rounding, sums in pairs of fp32
+ * that are put away into 64 bits every 128 terms of a lane: a sum is within
+ * 2^-35 of itself at worst and about 2^-46 in practice, whatever V is.  Their
+ * order, and with it the last of these bits, depends on B, V and the rows'
+ * alignment; calls that agree in these give the same tokens.
  * p: [B][T+1][V], q: [B][T][V] or NULL, both of type prob_type; draft: int32
  * [B][T]; u: fp32 [B][T], r: fp32 [B], all in [0, 1) (r is clamped to it); n_draft: int32 [B] or
  * NULL (T), clamped to T; tail_len, new_len: int32 [B] or NULL (new_len may

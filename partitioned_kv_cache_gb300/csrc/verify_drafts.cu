@@ -10,18 +10,24 @@
 //   positive, w = p_a;
 //   next token = the smallest i with w_0 + .. + w_i > r * (w_0 + .. + w_{V-1}).
 // The accepted tokens and the next one are then distributed as if the target
-// had been sampled token by token.  Products, differences and sums keep 64
-// bits' worth: the choice of i compares a sum over V terms with a threshold,
-// and 32 bits would move its border by more than a token's probability.
+// had been sampled token by token.  The choice of i compares a sum over V
+// terms with a threshold, and plain fp32 sums would move its border by more
+// than a token's probability: products and differences keep every bit, sums
+// about 46.
 //
-// Only row a of p and of q is read, once.  A cluster of up to 8 CTAs shares a
-// stream's row, each warp a contiguous span of it, so that one stream alone
+// Of p and q only row a is read: once for the totals, the span of the warp that
+// holds the threshold a second time and a sixteenth of that a third (and p's
+// row again where no difference is positive).  A cluster of up to 8 CTAs shares
+// a stream's row, each warp a contiguous span of it, so that one stream alone
 // still uses 8 SMs' load bandwidth.  A difference p - q > 0 is two fp32 numbers
 // (the rounded difference and its exact remainder) and a sum another two (each
-// addition's rounding error is kept): about 46 bits at fp32 speed.  Double
-// additions run at 1/64 of that rate on this GPU: one for each term, or even
-// one warp reduction in every warp, would take longer than the loads, so they
-// are kept to one warp's few totals.  The CTAs push their totals into each
+// addition's rounding error is kept, in a sum of its own).  With n terms that
+// second sum's roundings come to n^2 / 2 * 2^-48 of the first at worst, so a
+// lane puts both away into a double every 128 terms: 2^-35 at worst; over terms
+// of a softmax about 2^-47 (65536 in one pair: 2^-33).  Double additions run at
+// 1/64 of the fp32 rate on this GPU: one for each term, or even one warp
+// reduction in every warp, would take longer than the loads, so besides these
+// they are kept to one warp's few totals.  The CTAs push their totals into each
 // other's shared memory; the CTA whose interval holds the threshold cuts the
 // crossing warp's span over its 16 warps, and the crossing warp of those walks
 // its terms, four a lane.  Bound by memory for many streams (64 x 257152 fp32:
@@ -56,7 +62,7 @@ struct VerifyParams {
   int* new_len;
   int T, V;
   int cluster;   // CTAs of one stream
-  int span;      // terms of one warp: a multiple of 512
+  int span;      // terms of one warp: a multiple of 32, and so of a 16-byte load's
 };
 
 __device__ __forceinline__ float prob(const float* p, long long i) { return __ldg(p + i); }
@@ -102,6 +108,10 @@ struct TwoSum {
     }
   }
   __device__ __forceinline__ double value() const { return static_cast<double>(sum) + static_cast<double>(rest); }
+  __device__ __forceinline__ void set(double v) {
+    sum = static_cast<float>(v);
+    rest = static_cast<float>(v - static_cast<double>(sum));
+  }
 };
 
 __device__ __forceinline__ double weight(float p, float q) {
@@ -144,10 +154,10 @@ __device__ __forceinline__ void st_cluster_f64(uint32_t local, int rank, double 
   asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(remote), "d"(v) : "memory");
 }
 
-// The pair sum of the terms [v0, v1) over the warp's lanes.  VEC: 16-byte
-// loads (v0 and V are multiples of a load's terms).
+// This lane's terms of [v0, v1).  VEC: 16-byte loads (v0 and V are multiples of
+// a load's terms).
 template <typename P, bool VEC>
-__device__ __forceinline__ TwoSum span_sum(const P* pr, const P* qr, int out, int v0, int v1, int lane) {
+__device__ __forceinline__ TwoSum lane_sum(const P* pr, const P* qr, int out, int v0, int v1, int lane) {
   TwoSum t;
   if constexpr (VEC) {
     constexpr int E = 16 / sizeof(P);
@@ -191,6 +201,32 @@ __device__ __forceinline__ TwoSum span_sum(const P* pr, const P* qr, int out, in
 #pragma unroll
       for (int k = 0; k < U; ++k) t.add_difference(pf[k], qf[k]);
     }
+  }
+  return t;
+}
+
+// More than kFold terms a lane, a double for each kFold.  (In a function of its
+// own: inline, its doubles were computed for short spans too, and took 2.5 us.)
+constexpr int kFold = 128;
+template <typename P, bool VEC>
+__device__ __noinline__ float2 long_lane_sum(const P* pr, const P* qr, int out, int v0, int v1, int lane) {
+  double away = 0.0;
+  for (int c0 = v0; c0 < v1; c0 += 32 * kFold) away += lane_sum<P, VEC>(pr, qr, out, c0, min(c0 + 32 * kFold, v1), lane).value();
+  TwoSum t;
+  t.set(away);
+  return make_float2(t.sum, t.rest);
+}
+
+// The pair sum of the terms [v0, v1) over the warp's lanes.
+template <typename P, bool VEC>
+__device__ __forceinline__ TwoSum span_sum(const P* pr, const P* qr, int out, int v0, int v1, int lane) {
+  TwoSum t;
+  if (v1 - v0 > 32 * kFold) {
+    const float2 x = long_lane_sum<P, VEC>(pr, qr, out, v0, v1, lane);
+    t.sum = x.x;
+    t.rest = x.y;
+  } else {
+    t = lane_sum<P, VEC>(pr, qr, out, v0, v1, lane);
   }
   t.add_lanes();
   return t;

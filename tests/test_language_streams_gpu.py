@@ -653,6 +653,45 @@ def test_verify_probabilities_near_the_smallest_number(rx):
     _verify(rx, p, q, draft, u, r, None, torch.float32)
 
 
+@pytest.mark.parametrize("seed", [0, 3])
+def test_verify_sums_over_many_terms(rx, seed):
+    """A row of 2^26 terms whose threshold lies between tokens of 2^-43 of the
+    total.  The terms before it are alike in every lane of the kernel, so that
+    the lanes' rounding errors add up instead of cancelling; those after it add
+    without rounding.  Every number is an integer of 2^-45, and r = 1/2 falls
+    into the middle of the 2001 small tokens, with 2^-44 of the total to either
+    side.  Sums that are off by 2^-46 move the threshold by a quarter of that
+    (half of the total is the terms before it, and it moves by half as much)."""
+    import torch
+    g = np.random.default_rng(seed)
+    V, half, small, unit = 1 << 26, 1 << 25, 2001, 2.0 ** -45
+    base = np.exp(2.5 * g.standard_normal(4096)).astype(np.float32)
+    base = np.maximum(np.float32(2.0 ** -21), base / np.float32(2.0 ** 6))   # 24 bits of at least 2^-21: integers of 2^-45
+    steps = np.tile(base, half // 4096 // 128)
+    first = np.repeat(steps, 128)                                  # each value at 128 places: one per lane, four terms a load
+    total = 128 * (half // 4096 // 128) * sum(int(x) for x in base.astype(np.float64) / unit)
+    w = float(2.0 ** round(np.log2(total * unit)) * 2.0 ** -42)    # a small token, 2^-43 of the total
+    assert (w / unit).is_integer()
+    row = np.zeros(V, np.float32)
+    row[:half] = first
+    row[half:half + small] = w
+    rest = V - half - small - 4
+    c = 2.0 ** np.floor(np.log2(total * unit / rest))
+    row[half + small:half + small + rest] = c
+    left = total - rest * int(c / unit)                            # in up to three pieces of 24 bits
+    for i in range(4):
+        bits = max(0, left.bit_length() - 24)
+        piece = (left >> bits) << bits
+        row[V - 4 + i] = piece * unit
+        left -= piece
+    assert left == 0
+    p = torch.from_numpy(row).cuda().view(1, 1, V)
+    none = torch.zeros((1, 0), dtype=torch.int32, device="cuda")
+    tokens, n, _ = rx.verify_drafts(p, None, none, none.float(), torch.full((1,), 0.5, device="cuda"))
+    assert n.item() == 0
+    assert tokens.item() == half + small // 2
+
+
 @pytest.mark.parametrize("V", [5000, 10000, 60000])
 def test_verify_clusters_beside_other_work(rx, V):
     """Clusters of 2, 4 and 8 CTAs whose CTAs start at different times, because
