@@ -35,8 +35,9 @@
 //   l_n  = sum_j 2^(x_jn - m_n),   w_jn = 2^(x_jn + v_exp_j - 127 - M_n + 5)
 // m_n and M_n are running maxima of x_jn and of x_jn + v_exp_j - 127: the
 // weights' own reference keeps them in the upper e4m3 range whatever the
-// values' scales are.  Both are kept until some exponent outgrows them by 3.5
-// or more, which after a segment's first tile is rare.
+// values' scales are.  (M_n is held as M_n - m_n: scores may be large enough to
+// round an exponent away.)  Both are kept until some exponent outgrows them by
+// 3.5 or more, which after a segment's first tile is rare.
 //
 // Work is cut into tiles of 128 keys of one (stream, K/V head, row tile) unit.
 // The tiles of one head, all streams' in a row, are cut into equal runs
@@ -412,7 +413,7 @@ struct TailMisc {
   // (read four at a time)
   alignas(16) float qs[RT];              // 2^e of the query rows, times log2(e) / sqrt(D)
   int seen[RT];                          // tail keys each row sees
-  float wm[2][4][RT], wv[2][4][RT];      // the warps' maxima, for even and odd tiles
+  alignas(16) float wm[2][4][RT], wv[2][4][RT];   // the warps' maxima, for even and odd tiles
   // Per softmax warp, for its warpgroup's rows: m, d = m - M + kTop, and the
   // last factors of l and O.
   alignas(16) float row[RT < 16 ? 4 : RT / 4][4][RT < 16 ? RT : 16];
@@ -774,7 +775,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
       float l[CW];
 #pragma unroll
       for (int j = 0; j < CW; ++j) l[j] = 0.f;
-      float m = kNoMax, mv = kNoMax;   // lane j < CW: the running maxima of row n0 + j
+      float m = kNoMax, mv = 0.f;   // lane j < CW: row n0 + j's m and M - m
       float dmax = 0.f;                // the largest d
       if (lane < CW) {
         row[0][lane] = kNoMax;
@@ -837,34 +838,41 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
         }
         if (named_any(1 + wg, 128, over)) {
           // The tile's maxima: over the warp's keys, then over the four warps,
-          // lane j for row n0 + j.
+          // lane j for row n0 + j.  Those of the values' exponents are taken
+          // beside what the scores lie below their maximum (the warp's, then
+          // the new one): beside a score of 2^24 or more they would be rounded
+          // away.  (A column without a key in this warp: -inf and NaN, which
+          // the maxima pass over.)
           scores_less(u, nullptr);
+          float* wm = &ms.wm[buf][quarter][n0];
           const float hx = across_lanes(u, lane, MaxOp());
+          if (lane % (32 / CW) == 0) wm[lane / (32 / CW)] = hx;
+          __syncwarp();
           float y[CW];
 #pragma unroll
-          for (int j = 0; j < CW; ++j) y[j] = u[j] + ev;
-          const float hy = across_lanes(y, lane, MaxOp());
-          if (lane % (32 / CW) == 0) {
-            ms.wm[buf][quarter][n0 + lane / (32 / CW)] = hx;
-            ms.wv[buf][quarter][n0 + lane / (32 / CW)] = hy;
+          for (int j = 0; j < CW; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&wm[j]);
+            y[j] = u[j] - f.x + ev;
+            y[j + 1] = u[j + 1] - f.y + ev;
+            y[j + 2] = u[j + 2] - f.z + ev;
+            y[j + 3] = u[j + 3] - f.w + ev;
           }
+          const float hy = across_lanes(y, lane, MaxOp());
+          if (lane % (32 / CW) == 0) ms.wv[buf][quarter][n0 + lane / (32 / CW)] = hy;
           named_sync(1 + wg, 128);
           float mn = m, vn = mv;
           if (lane < CW) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              mn = fmaxf(mn, ms.wm[buf][w][n0 + lane]);
-              vn = fmaxf(vn, ms.wv[buf][w][n0 + lane]);
-            }
-          }
-          const float d = mn - vn + kTop;   // a row without a key so far: kTop
-          if (lane < CW) {
+            for (int w = 0; w < 4; ++w) mn = fmaxf(mn, ms.wm[buf][w][n0 + lane]);
+            vn += m - mn;   // a row without a key so far: 0
+#pragma unroll
+            for (int w = 0; w < 4; ++w) vn = fmaxf(vn, ms.wv[buf][w][n0 + lane] + (ms.wm[buf][w][n0 + lane] - mn));
             row[0][lane] = mn;
-            row[1][lane] = d;
+            row[1][lane] = kTop - vn;
             row[2][lane] = ex2(m - mn);
-            row[3][lane] = ex2(mv - vn);
+            row[3][lane] = ex2((m - mn) + (mv - vn));
           }
-          dmax = lane < CW ? d : -INFINITY;
+          dmax = lane < CW ? kTop - vn : -INFINITY;
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) dmax = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, o));
           m = mn;
@@ -974,7 +982,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
       named_sync(1 + wg, 128);   // wm is free
       const float sum = across_lanes(l, lane, SumOp());
       if (lane % (32 / CW) == 0) ms.wm[0][quarter][n0 + lane / (32 / CW)] = sum;
-      if (lane < CW) row[2][lane] = exp2f(mv - kTop - m);   // O's reference to m
+      if (lane < CW) row[2][lane] = exp2f(mv - kTop);   // O's reference to m
       named_sync(1 + wg, 128);
       if (in_wg < CW && n0 + in_wg < rows)
         p.ml[slot_row + in_wg] = make_float2(m == kNoMax ? -INFINITY : m,

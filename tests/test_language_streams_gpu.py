@@ -291,6 +291,34 @@ def test_attention_score_range(rx):
     _attend(rx, st, g, [700, 650], None, 2, tails=(kc, ke, vc, ve))
 
 
+@pytest.mark.parametrize("T", [1, 4, 8])
+@pytest.mark.parametrize("power", [18, 23, 24, 25, 26, 28, 31])
+def test_attention_large_scores(rx, T, power):
+    """Scores of 2^power (in units of log 2) whose order is plain, and values
+    of very different scales: two keys share the top score, every other key is
+    at half of it or less, so the output is the mean of their two values."""
+    import torch
+    g = np.random.default_rng(power)
+    D, n, f = 256, 300, W.bf16_bits_to_f64
+    st = Store(rx, g, 8, 1, D, 16, 1, 16, n, 2 * T, pushes=1)
+    # q . k / sqrt(D) / log 2 = 2^a * 2^b * c * 256 / 16 / log 2 for q = 2^a, k = 2^b c
+    a = (power - 4) // 2
+    b = power - 4 - a
+    q = np.full((2, T, 8, D), 2.0 ** a, np.float32)
+    c = g.choice([0.5, 0.25, -1.0], (2, n, 1, 1)) * np.ones(D)
+    c[0, [40, 200]] = c[1, [130, 131]] = 1.0
+    kc, ke = OS.quantise(c * 2.0 ** b)
+    scale = g.integers(-40, 41, (2, 1, 1, 1)) + g.integers(-5, 6, (2, n, 1, 1))
+    vc, ve = OS.quantise(f(_bits(g, (2, n, 1, D))) * 2.0 ** scale)
+    out = st.cache.attend_streams_quant(0, dev(W.to_bf16_bits(q)), _codes(kc), _codes(vc), torch.from_numpy(ke).cuda(),
+                                        torch.from_numpy(ve).cuda(), _int([n, n]))
+    got = host64(out)
+    for b in range(2):
+        ref, spread = OS.stream_attention(q[b].astype(np.float64), st.k[0], st.v[0], OS.dequantise(kc[b], ke[b]),
+                                          OS.dequantise(vc[b], ve[b]))
+        _check(got[b], ref, spread)
+
+
 @pytest.mark.parametrize("Hq,Hkv,D", [(6, 3, 128), (14, 7, 64), (320, 320, 64), (40, 20, 256)])
 def test_attention_head_counts(rx, Hq, Hkv, D):
     """Head counts that do not divide the GPU's SMs, and more heads than CTAs."""
