@@ -91,8 +91,9 @@ typedef struct rx_config {
  * RX_ERR_UNSUPPORTED (D, G, or a GPU without sm_103a tcgen05), RX_ERR_CUDA. */
 rx_status rx_cache_create(const rx_config* cfg, rx_cache_t* out);
 
-/* Free everything the cache owns.  Synchronises the device first.  NULL is a
- * no-op.  Errors: RX_ERR_CUDA (the synchronisation or the free failed). */
+/* Free everything the cache owns.  Synchronises the device first, so it may not
+ * be called while a stream of the process is being captured.  The handle is
+ * gone whatever the status is.  NULL is a no-op.  Errors: RX_ERR_CUDA (the synchronisation or the free failed). */
 rx_status rx_cache_destroy(rx_cache_t cache);
 
 /* Copy the instruction prefix into the pinned region ("Reflex ...", §III

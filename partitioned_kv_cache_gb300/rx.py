@@ -237,11 +237,26 @@ def library_path() -> str:
     return _LIB_PATH
 
 
+#: Handles of caches that the garbage collector took while the current stream
+#: was being captured; freed when the next cache is made outside a capture.
+_parked: list = []
+
+
+def _capturing() -> bool:
+    return torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
+
+
+def _free_parked() -> None:
+    while _parked and not _capturing():
+        _check(_lib.rx_cache_destroy(_parked.pop()), "rx_cache_destroy")
+
+
 class Cache:
     """The partitioned KV store of one stream (rx_cache_t)."""
 
     def __init__(self, L: int, Hq: int, Hkv: int, D: int, P_cap: int, N: int, F: int,
                  S_cap: int, tail_cap: int = 0, max_req: int = 0, spare_slot: int = 0):
+        _free_parked()
         self.cfg = RxConfig(L, Hq, Hkv, D, P_cap, N, F, S_cap, tail_cap, max_req, spare_slot)
         h = _vp()
         _check(_lib.rx_cache_create(ctypes.byref(self.cfg), ctypes.byref(h)), "rx_cache_create")
@@ -252,13 +267,20 @@ class Cache:
         return self._h
 
     def close(self) -> None:
-        if getattr(self, "_h", None):
-            _check(_lib.rx_cache_destroy(self._h), "rx_cache_destroy")
-            self._h = None
+        """Free the cache's memory (synchronises the device, so not while a
+        stream is being captured)."""
+        h, self._h = getattr(self, "_h", None), None   # freed whatever the status is
+        if h:
+            _check(_lib.rx_cache_destroy(h), "rx_cache_destroy")
 
     def __del__(self):
         try:
-            self.close()
+            if _capturing():   # collected within a capture, which freeing would end
+                h, self._h = getattr(self, "_h", None), None
+                if h:
+                    _parked.append(h)
+            else:
+                self.close()
         except Exception:
             pass
 

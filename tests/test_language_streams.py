@@ -233,3 +233,40 @@ def test_stream_partition_refuses_sizes_out_of_range(lib):
               ((1 << 20) + 1, 1, 1, 152, 32), (1, (1 << 20) + 1, 1, 152, 32), (1, 1, (1 << 48) + 1, 152, 32)):
         with pytest.raises(rx.RxError):
             rx.choose_stream_partition(*a)
+
+
+# --------------------------------------------------- caches that are collected
+def test_a_cache_is_freed_once_and_not_within_a_capture(lib, monkeypatch):
+    """A cache that is collected while the current stream is being captured is
+    freed when the next one is made; one whose freeing fails is not freed twice."""
+    from partitioned_kv_cache_gb300 import rx
+    freed, capturing, status = [], [False], [0]
+
+    def destroy(h):
+        freed.append(h)
+        return status[0]
+    monkeypatch.setattr(rx._lib, "rx_cache_destroy", destroy)
+    monkeypatch.setattr(rx, "_capturing", lambda: capturing[0])
+
+    def cache(h):
+        c = rx.Cache.__new__(rx.Cache)
+        c._h = h
+        return c
+    c = cache(1)
+    del c
+    assert freed == [1]
+    capturing[0] = True
+    c = cache(2)
+    del c
+    rx._free_parked()
+    assert freed == [1]
+    capturing[0] = False
+    rx._free_parked()
+    rx._free_parked()
+    assert freed == [1, 2]
+    status[0] = -4
+    c = cache(3)
+    with pytest.raises(rx.RxError):
+        c.close()
+    del c
+    assert freed == [1, 2, 3]

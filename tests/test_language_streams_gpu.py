@@ -521,6 +521,37 @@ def test_attention_outside_a_capture_is_refused(rx):
     assert all(torch.equal(first, o) for o in outs)
 
 
+def test_a_cache_collected_within_a_capture_leaves_it_whole(rx):
+    """The garbage collector may run at any place, within a capture too."""
+    import gc
+    import torch
+    g = np.random.default_rng(44)
+    st = Store(rx, g, 8, 1, 64, 16, 1, 16, 40, 4, pushes=1)
+    kc, ke, vc, ve = _tails(g, 2, 40, 1, 64)
+    q = dev(_bits(g, (2, 1, 8, 64)))
+    args = (q, _codes(kc), _codes(vc), torch.from_numpy(ke).cuda(), torch.from_numpy(ve).cuda(), _int([40, 13]))
+    first = st.cache.attend_streams_quant(0, *args)
+    out = torch.zeros_like(first)
+    gc.collect()
+    free = torch.cuda.mem_get_info()[0]
+    cycle = [rx.Cache(1, 8, 1, 256, 1024, 1, 64, 4)]
+    cycle.append(cycle)
+    assert torch.cuda.mem_get_info()[0] < free
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        st.cache.attend_streams_quant(0, *args, out=out)
+        del cycle
+        gc.collect()
+        st.cache.attend_streams_quant(0, *args, out=out)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(first, out)
+    assert rx._parked
+    rx.Cache(1, 8, 1, 64, 16, 1, 16, 4).close()
+    assert not rx._parked
+
+
 def test_attention_on_another_stream(rx):
     import torch
     g = np.random.default_rng(25)
