@@ -27,10 +27,12 @@
 // meet in fp32: a query row, scaled by a power of two, is hi + lo exactly (8
 // significant bits in two 4-bit terms; what lies 2^-18 below the row's largest
 // entry is rounded away); a weight, rounded to f16, is hi + mid/16 + lo/256, each
-// term the e4m3 rounding of what is left, so it is within 2^-11 of its value or
-// 2^-24 of the row's largest weight (e4m3's smallest step is 2^-9, and the
-// steps of 16 go along with the remainders, so that many small weights beside
-// a large one keep their share): an eighth of a bf16 rounding.
+// term the e4m3 rounding of what is left, so it is within 2^-11 of its value,
+// an eighth of a bf16 rounding, or within 2^-23 of the largest weight that its
+// row has so far (half of lo's smallest step, 2^-17, below a reference of 2^5;
+// weights are compared with their values' scales).  Equal small weights beside
+// a large one all lose the same, so a sum of products is closed after kSegment
+// tiles: 16384 keys lose at most 2^-9 of the largest weight together.
 //   x_jn = S_jn * 2^(k_exp_j - 127) * (row scale) * log2(e) / sqrt(D)
 //   l_n  = sum_j 2^(x_jn - m_n),   w_jn = 2^(x_jn + v_exp_j - 127 - M_n + 5)
 // m_n and M_n are running maxima of x_jn and of x_jn + v_exp_j - 127: the
@@ -68,6 +70,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "rx_internal.h"
 #include "sm103_ptx.cuh"
@@ -79,6 +82,7 @@ constexpr int kTK = 128;            // keys per tile
 constexpr int kTerms = 3;           // e4m3 terms of a weight, each standing for 1/16 of the one before
 constexpr float kTermStep = 16.f;
 constexpr int kExpAhead = 4;        // tiles ahead that scale exponents are fetched into L2
+constexpr int kSegment = 128;       // most tiles of one unit that are summed under one pair of references
 // log2 of a row's largest weight, in e4m3 units, where its reference is taken,
 // and the most it may grow to before a new one is (448 is the largest code).
 constexpr float kTop = 5.f;
@@ -319,7 +323,7 @@ struct Walk {
   int skip;             // tiles of the unit before this run
   long long left;       // tiles of the run from here on
   StreamLen s;
-  int tile0, ntiles;    // the segment: tiles [tile0, tile0 + ntiles) of the unit
+  int tile0, ntiles;    // the segment: tiles [tile0, tile0 + ntiles) of the unit, kSegment at most
 
   __device__ __forceinline__ void begin(const RunStart& r) {
     b = r.b;
@@ -334,7 +338,7 @@ struct Walk {
         const int ut = unit_tiles(s, rt, RT, p.gs);
         if (ut > skip) {
           tile0 = skip;
-          ntiles = static_cast<int>(min(static_cast<long long>(ut - skip), left));
+          ntiles = static_cast<int>(min(static_cast<long long>(min(ut - skip, kSegment)), left));
           left -= ntiles;
           return true;
         }
@@ -354,10 +358,11 @@ struct Walk {
       if (b < p.B) s = stream_len(p.tail_len, p.n_new, b, p.T, p.tail_cap);
     }
   }
-  // After a segment: the unit is finished for this run.
-  __device__ __forceinline__ void done(const TailParams& p) {
-    skip = 0;
-    advance(p);
+  // After a segment.
+  __device__ __forceinline__ void done() { skip += ntiles; }
+  // Whether the run's segment before this one ended inside the same unit.
+  __device__ __forceinline__ bool again(const RunStart& r) const {
+    return tile0 != (b == r.b && rt == r.rt ? r.skip : 0);
   }
 };
 
@@ -575,7 +580,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
           if (i + 1 < wk.ntiles) load(&p.tm_k, wk.tile0 + i + 1);
           if (!stop) load(&p.tm_v, wk.tile0 + i);
         }
-        wk.done(p);
+        wk.done();
       }
       // Every copy issued must land before the CTA exits, even after an abort.
       volatile int no_abort = 0;
@@ -648,7 +653,7 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
           umma_commit(BAR(TB_PV + (tile & 1)));
           ++item;
         }
-        wk.done(p);
+        wk.done();
         ++seg;
       }
       // No tensor-core work may be in flight when TMEM is released.
@@ -979,40 +984,67 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
         if (wk.tile0 == 0) r->x = run;
         if (wk.tile0 + nt == unit_tiles(wk.s, wk.rt, RT, p.gs)) r->y = run;
       }
-      named_sync(1 + wg, 128);   // wm is free
-      const float sum = across_lanes(l, lane, SumOp());
-      if (lane % (32 / CW) == 0) ms.wm[0][quarter][n0 + lane / (32 / CW)] = sum;
-      if (lane < CW) row[2][lane] = exp2f(mv - kTop);   // O's reference to m
-      named_sync(1 + wg, 128);
-      if (in_wg < CW && n0 + in_wg < rows)
-        p.ml[slot_row + in_wg] = make_float2(m == kNoMax ? -INFINITY : m,
-                                             (ms.wm[0][0][n0 + in_wg] + ms.wm[0][1][n0 + in_wg]) +
-                                                 (ms.wm[0][2][n0 + in_wg] + ms.wm[0][3][n0 + in_wg]));
-      mbar_wait(BAR(TB_PV + ((tile - 1) & 1)), ((tile - 1) >> 1) & 1, abort_flag);
-      __syncwarp();
-      tc_fence_after();
-      if (D >= 128 || quarter < D / 32) {
-#pragma unroll 1
-        for (int ob = 0; ob < L::OB; ++ob) {
-          float o[CW];
-          const uint32_t at = tmem + L::TM_O + ob * L::NW + n0 + lane_off;
-          tmem_ld_cols(at, o);
-#pragma unroll
-          for (int term = 1; term < kTerms; ++term) {
-            float t[CW];
-            tmem_ld_cols(at + term * RT, t);
-            const float f = term == 1 ? 1.f / kTermStep : 1.f / (kTermStep * kTermStep);
-#pragma unroll
-            for (int j = 0; j < CW; ++j) o[j] = fmaf(t[j], f, o[j]);
-          }
-          float* dst = p.o + slot_row * D + ob * 128 + key_in_tile;
-#pragma unroll
-          for (int j = 0; j < CW; ++j)
-            if (n0 + j < rows) dst[j * D] = o[j] * row[2][j];
+      auto finish = [&](auto more) {
+        constexpr bool again = decltype(more)::value;
+        named_sync(1 + wg, 128);   // wm is free
+        const float sum = across_lanes(l, lane, SumOp());
+        if (lane % (32 / CW) == 0) ms.wm[0][quarter][n0 + lane / (32 / CW)] = sum;
+        const float top = m == kNoMax ? -INFINITY : m;
+        float all = top, before = 0.f;
+        if (lane < CW) row[2][lane] = exp2f(mv - kTop);   // O's reference to m
+        // A segment that goes on from another adds to what that one left, which
+        // this thread (or for (m, l) its warpgroup) has written.
+        if (again && lane < CW) {
+          const float2 old = n0 + lane < rows ? p.ml[slot_row + lane] : make_float2(-INFINITY, 0.f);
+          all = fmaxf(top, old.x);
+          // A sum without a maximum is zero, or NaN, which has to stay.
+          const float f = top == -INFINITY ? 1.f : exp2f(top - all);
+          const float g = old.x == -INFINITY ? 1.f : exp2f(old.x - all);
+          before = old.y * g;
+          row[2][lane] *= f;
+          row[3][lane] = g;
+          row[0][lane] = f;
         }
-      }
+        named_sync(1 + wg, 128);
+        if (in_wg < CW && n0 + in_wg < rows) {
+          const float here = (ms.wm[0][0][n0 + in_wg] + ms.wm[0][1][n0 + in_wg]) + (ms.wm[0][2][n0 + in_wg] + ms.wm[0][3][n0 + in_wg]);
+          p.ml[slot_row + in_wg] = make_float2(all, again ? fmaf(here, row[0][in_wg], before) : here);
+        }
+        mbar_wait(BAR(TB_PV + ((tile - 1) & 1)), ((tile - 1) >> 1) & 1, abort_flag);
+        __syncwarp();
+        tc_fence_after();
+        if (D >= 128 || quarter < D / 32) {
+#pragma unroll 1
+          for (int ob = 0; ob < L::OB; ++ob) {
+            float o[CW];
+            const uint32_t at = tmem + L::TM_O + ob * L::NW + n0 + lane_off;
+            tmem_ld_cols(at, o);
+#pragma unroll
+            for (int term = 1; term < kTerms; ++term) {
+              float t[CW];
+              tmem_ld_cols(at + term * RT, t);
+              const float f = term == 1 ? 1.f / kTermStep : 1.f / (kTermStep * kTermStep);
+#pragma unroll
+              for (int j = 0; j < CW; ++j) o[j] = fmaf(t[j], f, o[j]);
+            }
+            float* dst = p.o + slot_row * D + ob * 128 + key_in_tile;
+#pragma unroll
+            for (int j = 0; j < CW; ++j) o[j] *= row[2][j];
+            if (again) {
+#pragma unroll
+              for (int j = 0; j < CW; ++j)
+                if (n0 + j < rows) o[j] = fmaf(dst[j * D], row[3][j], o[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < CW; ++j)
+              if (n0 + j < rows) dst[j * D] = o[j];
+          }
+        }
+      };
+      if (wk.again(ms.start)) finish(std::true_type());   // (a copy of its own: most runs have none)
+      else finish(std::false_type());
       item0 += 2 * nt;
-      wk.done(p);
+      wk.done();
     }
   }
   tc_fence_before();

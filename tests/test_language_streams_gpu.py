@@ -363,6 +363,72 @@ def test_attention_many_small_weights_beside_a_large_one(rx, T, gap):
     _check(host64(out)[0], ref, spread)
 
 
+@pytest.mark.parametrize("T", [1, 8])
+def test_attention_very_many_small_weights_beside_a_large_one(rx, T):
+    """One key 16.7 nats above 196607 equal ones, on so many heads that a CTA
+    reads all of a head's keys, or half of them, one after the other.  Each of
+    these weighs a little less than half of what a weight can be told apart
+    by, so all of them are lost beside the large one: of 16384 keys that is
+    16384 * e^-16.7 * 2 = 0.0018, of all 0.022, and the bound is 0.0085 (the
+    large key's values are 1 or -1, the others' 2)."""
+    import torch
+    g = np.random.default_rng(42)
+    n, D, H = 196608, 64, 152
+    st = Store(rx, g, 8 * H, H, D, 0, 1, 16, n, T, pushes=0)
+    k = np.zeros((1, D))
+    k[0] = 2.0
+    k[0, :23] = 2.25                      # against q = 1: (41 * 2 + 23 * 2.25) / 8 = 16.72 nats
+    sign = np.where(g.random((1, D)) < 0.5, -1.0, 1.0)
+    (kc, ke), (vc, ve), (sc, se) = OS.quantise(k), OS.quantise(sign), OS.quantise(np.full((1, D), 2.0))
+    kt = torch.zeros((1, n, H, D), dtype=torch.uint8, device="cuda")
+    kx = torch.zeros((1, n, H), dtype=torch.uint8, device="cuda")
+    vt = torch.from_numpy(sc).cuda().view(1, 1, 1, D).repeat(1, n, H, 1)
+    vx = torch.full((1, n, H), int(se[0]), dtype=torch.uint8, device="cuda")
+    kt[0, 7777], kx[0, 7777] = torch.from_numpy(kc).cuda(), int(ke[0])
+    vt[0, 7777], vx[0, 7777] = torch.from_numpy(vc).cuda(), int(ve[0])
+    q = torch.ones((1, T, 8 * H, D), dtype=torch.bfloat16, device="cuda")
+    out = st.cache.attend_streams_quant(0, q, kt.view(torch.float8_e4m3fn), vt.view(torch.float8_e4m3fn), kx, vx, _int([n]))
+    got = host64(out)[0]
+    for t in range(T):
+        others = (n - T + t) * np.exp(-np.sum(OS.dequantise(kc, ke)) / np.sqrt(D))
+        ref = (sign[0] + 2.0 * others) / (1 + others)
+        spread = (1 + 2.0 * others) / (1 + others)
+        for h in range(8 * H):
+            _check(got[t, h], ref, spread * np.ones(D))
+    assert st.cache.check_device_error() == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,T", [(8, 1, 256, 1), (32, 2, 64, 8), (16, 2, 128, 1)])
+def test_attention_tails_of_several_segments(rx, Hq, Hkv, D, T):
+    """More keys of one stream in a CTA's run than are summed under one pair of
+    references: 160 streams' worth of the GPU's runs in one, a second stream of
+    an odd length behind it, and scores that grow and fall along the tail."""
+    import torch
+    g = np.random.default_rng(43)
+    H, n = 160, 16384 * 2 + 77
+    G = Hq // Hkv
+    st = Store(rx, g, H * G, H, D, 3, 1, 16, n, 2 * T, pushes=1)
+    tails = []
+    for scale in (np.sin(np.arange(n) / 9000.0)[None, :, None, None] + 1.5, 1.0):
+        codes, byte = OS.quantise((g.standard_normal((2, n, 1, D)) * scale).astype(np.float32).astype(np.float64))
+        tails += [codes, byte]
+    kc, ke, vc, ve = (np.ascontiguousarray(x) for x in tails)
+    lens = [n, 16384 + 130]
+    on = lambda x: torch.from_numpy(x).cuda().expand(2, n, H, *x.shape[3:]).contiguous()
+    q1 = W.to_bf16_bits(0.3 * g.standard_normal((2, T, 1, G, D), dtype=np.float32))
+    q = dev(np.ascontiguousarray(np.broadcast_to(q1, (2, T, H, G, D))).reshape(2, T, H * G, D))
+    out = st.cache.attend_streams_quant(0, q, on(kc).view(torch.float8_e4m3fn), on(vc).view(torch.float8_e4m3fn), on(ke),
+                                        on(ve), _int(lens))
+    got = host64(out).reshape(2, T, H, G, D)
+    for b in range(2):
+        for h in (0, 1, 80, H - 1):
+            ref, spread = OS.stream_attention(W.bf16_bits_to_f64(q1[b, :, 0]), st.k[0][:, h:h + 1], st.v[0][:, h:h + 1],
+                                              OS.dequantise(kc[b, :lens[b]], ke[b, :lens[b]]),
+                                              OS.dequantise(vc[b, :lens[b]], ve[b, :lens[b]]))
+            _check(got[b, :, h], ref, spread)
+    assert st.cache.check_device_error() == 0
+
+
 def test_attention_wait_that_runs_out_is_reported(rx):
     g = np.random.default_rng(31)
     st = Store(rx, g, 8, 1, 64, 16, 1, 16, 200, 4, pushes=1)
