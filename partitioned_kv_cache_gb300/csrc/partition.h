@@ -131,24 +131,24 @@ inline bool choose_partition(const PartitionRequest& r, PartitionChoice* out) {
 // x K/V heads, each `t_max` key tiles of 64, cut into `splits`) and the tails.
 // Both take one CTA an SM, so whatever SMs the first holds the second waits
 // for.  A 64-key tile of the store takes about half as long as a 128-key tile
-// of a tail, of which there are at most `tail_tiles`.
-//  * The store gets its share of the work in SMs; where that is small, enough
-//    for two or three tiles a CTA (the tails may be much shorter than their
-//    capacity); at most half of the SMs, and one CTA a unit at least.
+// of a tail, of which there are at most `tail_tiles`, or a little more.
+//  * The store gets its share of the work in SMs, at most 5/8 of them; where
+//    that share is small, enough for two or three tiles a CTA (the tails may be
+//    much shorter than their capacity), at most half of the SMs; and one CTA a
+//    unit at least.
 //  * The tails get the other SMs, if those are at least three quarters of what
 //    their own work is worth; otherwise, and where the store holds far more
 //    than its share, they get all SMs, some after the store.
 // Measured (SMs for the store / for the tails, us a call; the first is taken):
-// 80 queries over 8448 shared keys and tails to 2000 tokens, 75/77 24.8, 30/122
-// 33.2, 75/152 32.8; 64 x 8 queries over 2304 keys and tails to 16384, 64/152
-// 108.7, 64/88 134.0, 128/152 113.6; 32 queries over 2112 keys and tails to
-// 16000, 22/130 39.8, 34/118 41.0, 22/152 41.3; 72 x 4 queries of 64/8 heads
-// (D = 128) over 8448 keys and tails to 512, 144/152 135.6, 144/8 333; 8 prompts
-// of 302 tokens over 8448 keys, 151/152 204, 151/1 4043.  (64 queries over 8448
-// keys and tails to 4096 would gain from another choice: 76/152 40.9, 48/104
-// 33.1.)  One kernel after the other the first three took 38.5, 124.3 and 47.6
-// us, and 16 queries over 2112 keys with tails to 30 tokens 21.0 instead of 14.2
-// (17/135).
+// 80 queries over 8448 shared keys and tails to 2000 tokens, 85/67 28.0, 75/77
+// 28.7, 95/57 27.8, 60/92 30.1, 75/87 34.2; 64 x 8 queries over 2304 keys and
+// tails to 16384, 64/152 114.0, 32/120 112.1, 96/152 114.7, 128/152 117.6; 32
+// queries over 2112 keys and tails to 16000, 22/130 39.4, 34/118 40.6; 16
+// queries over 2112 keys and tails to 30, 17/135 14.8, 33/119 16.6.  Before the
+// store's weights had a second term: 72 x 4 queries of 64/8 heads (D = 128) over
+// 8448 keys and tails to 512, 144/152 135.6, 144/8 333; 8 prompts of 302 tokens
+// over 8448 keys, 151/152 204, 151/1 4043; and one kernel after the other, the
+// first four took 38.5 (25.5 beside), 124.3 (108.4), 47.6 (40.5) and 21.0 (14.2).
 struct StreamPartition {
   int splits;     // key slices of each unit of the store
   int tail_sms;   // SMs that the tails' grid is made for
@@ -156,8 +156,10 @@ struct StreamPartition {
 inline StreamPartition choose_stream_partition(int units, int t_max, long long tail_tiles, int num_sms, int max_splits) {
   const long long store = static_cast<long long>(units) * t_max;
   const long long share = num_sms * store / (store + 2 * tail_tiles + 1);   // the store's SMs by work
-  long long want = share >= num_sms / 8 ? share : (store + 1) / 2;
-  want = want < num_sms / 2 ? want : num_sms / 2;
+  const bool heavy = share >= num_sms / 8;
+  long long want = heavy ? share : (store + 1) / 2;
+  const long long most = heavy ? num_sms * 5 / 8 : num_sms / 2;
+  want = want < most ? want : most;
   long long sp = want / units;
   sp = sp < max_splits ? sp : max_splits;
   sp = sp < t_max ? sp : t_max;

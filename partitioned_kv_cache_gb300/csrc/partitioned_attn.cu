@@ -99,7 +99,9 @@ struct Layout {
   static constexpr int OFF_MISC = OFF_BAR + 80 * 8;
   static constexpr int BYTES = OFF_MISC + 64;
   static constexpr int ALLOC = BYTES + 1024;        // slack for 1024-byte alignment
-  static constexpr int TMEM_COLS = (D + 3 * kBN) <= 256 ? 256 : 512;   // O, S x 2, P x 2
+  // TMEM columns: O, S x 2, P x 2 (a P of 32 columns for each bf16 term).
+  static constexpr int tmem_cols(int p_terms) { return D + 2 * kBN + p_terms * kBN <= 256 ? 256 : 512; }
+  static_assert(D + 4 * kBN <= 512, "tensor memory");
   static_assert(ALLOC <= 232448, "shared memory budget");
   static_assert(SPLIT ? (NK >= 2 && V_BYTES >= 2 * TILE) : (NS >= 4), "ring depth");
 };
@@ -361,11 +363,20 @@ __device__ __noinline__ void run_norm_rows(const AttnParams& p, int sw, int lane
 // launches whose splits are merged by attn_combine_kernel; or kPartials, for
 // launches that end with every split's partial in the exchange area in fp32
 // (launch_attention_partials), for a merge with partials of other keys that
-// adds no rounding of its own.
+// adds no rounding of its own.  There a weight enters P V as two bf16 terms
+// (its upper half and what that leaves: 16 bits), so that the bf16 output is
+// the only rounding that is felt: error against 64 bits 0.00167 where rounding
+// the exact result gives 0.00166 (one term: 0.0018 to 0.0022).  It costs a
+// second pass of P V, about 0.2 us a key tile at D = 256: 16 x 5 queries over
+// 8448 keys and tails to 2000 tokens 28.0 us (25.5), 64 x 8 over 2304 keys and
+// tails to 16384 114.0 (109.4), 16 over 2112 keys 14.8 (14.3).
 template <int D, int RING_KB, int CM = kMaxClusterSplits>
 __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ AttnParams p) {
   using Lay = Layout<D, RING_KB>;
   extern __shared__ uint8_t smem_raw[];
+  // bf16 terms of a weight.
+  constexpr int kTermsP = CM == kPartials ? 2 : 1;
+  constexpr int kTmemCols = Lay::tmem_cols(kTermsP);
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
@@ -405,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), Lay::TMEM_COLS);
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
   if (warp == 0 && lane == 0) {   // prefetch only the descriptors this CTA uses
@@ -502,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   const uint32_t tmem = *tmem_slot;
   const uint32_t tO = tmem;                               // columns [0, D)
   const uint32_t tS = tmem + static_cast<uint32_t>(D);    // two buffers of 64 columns
-  const uint32_t tP = tS + 2 * kBN;                       // two P buffers of 32 columns (bf16 pairs)
+  const uint32_t tP = tS + 2 * kBN;                       // two P buffers of 32 columns (bf16 pairs) a term
 
   const int qtok = kBM / p.G;   // query tokens per tile
   const int ns = Lay::NS;                                    // single ring: slots
@@ -639,7 +650,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           // along the 128-byte rows, 64-column blocks 8 KB apart (LBO), 8-key
           // groups 1 KB apart (SBO), 16 keys = 2 KB per K step.
           const uint64_t b = sdesc_sw128(vt + kk * 16 * 128, 8192, 1024);
-          umma_bf16_ts(tO, tP + st * (kBN / 2) + kk * 8, b, kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+          for (int term = 0; term < kTermsP; ++term)
+            umma_bf16_ts(tO, tP + (st * kTermsP + term) * (kBN / 2) + kk * 8, b, kIdescO,
+                         (j > 0 || kk > 0 || term > 0) ? 1u : 0u);
         }
         umma_commit(BAR(bvempty + slot));
         umma_commit(BAR(B_PV + st));
@@ -727,19 +741,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       }
       // p = 2^(s * scale - m): one FMA feeds each exponential.
       const float nmb = m_used == -INFINITY ? 0.f : -m_used;
-      uint32_t pk[kBN / 2];
+      uint32_t pk[kTermsP * kBN / 2];
       float rs[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < kBN / 2; ++c) {
         const float a = exp2f(fmaf(s[2 * c], p.scale_log2, nmb));
         const float b = exp2f(fmaf(s[2 * c + 1], p.scale_log2, nmb));
         rs[c & 3] += a + b;
-        pk[c] = pack_bf16x2(a, b);
+        if constexpr (kTermsP == 1) {
+          pk[c] = pack_bf16x2(a, b);
+        } else {   // the upper halves, and what they leave
+          pk[c] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+          pk[kBN / 2 + c] = pack_bf16x2(a - __uint_as_float(__float_as_uint(a) & 0xFFFF0000u),
+                                        b - __uint_as_float(__float_as_uint(b) & 0xFFFF0000u));
+        }
       }
       l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
       // P buffer `st` was last read by P_{j-2} V_{j-2}.
       if (j >= 2 && !warp_wait(BAR(B_PV + st), ((j - 2) >> 1) & 1, abort_flag)) { ok = false; break; }
-      tmem_st32(tP + st * (kBN / 2) + lane_off, reinterpret_cast<const float*>(pk));
+      if constexpr (kTermsP == 1) tmem_st32(tP + st * (kBN / 2) + lane_off, reinterpret_cast<const float*>(pk));
+      else tmem_st64(tP + st * kBN + lane_off, pk);
       tc_fence_before();
       mbar_arrive(BAR(B_PF + st));
     }
@@ -946,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, Lay::TMEM_COLS);
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
   if (threadIdx.x == 0 && *abort_flag) atomicOr(p.err, kErrAttnTimeout);
 }
 

@@ -216,7 +216,7 @@ def test_stream_partition_leaves_the_tails_their_share(lib):
     ("64/8 heads of 128, 72 x 4 tokens, 8448 keys, tails of 512", 144, 132, 2304, (1, 152)),
     ("8 prompts of 302 tokens, 8448 keys, tails of 1024", 151, 132, 2432, (1, 152)),
     ("16 tokens, 2112 keys, tails of 32", 1, 33, 16, (17, 135)),
-    ("16 x 5 tokens, 8448 keys, tails of 2048", 5, 132, 256, (15, 77)),
+    ("16 x 5 tokens, 8448 keys, tails of 2048", 5, 132, 256, (17, 67)),
     ("7 x 3 tokens, 32/8 heads of 128, 337 keys, tails of 1001", 8, 6, 448, (3, 128)),
     ("32 tokens, 2112 keys, tails of 16384", 2, 33, 4096, (11, 130)),
     ("64 x 8 tokens, 2304 keys, tails of 16384", 32, 36, 8192, (2, 152)),

@@ -291,6 +291,30 @@ def test_attention_score_range(rx):
     _attend(rx, st, g, [700, 650], None, 2, tails=(kc, ke, vc, ve))
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 1, 256), (32, 8, 128), (4, 4, 64)])
+@pytest.mark.parametrize("P,pushes,T", [(2, 0, 1), (5, 1, 3), (0, 1, 8)])
+def test_attention_weights_are_not_rounded_to_16_bits(rx, Hq, Hkv, D, P, pushes, T):
+    """Few keys, so that roundings of the weights do not average out, and a
+    bound without a bf16 rounding of them: 2^-11 of a weight for the tails'
+    terms, 2^-12 for the fp32 steps, and 2^-8 of the output for its own."""
+    import torch
+    g = np.random.default_rng(50 + D + P)
+    B = 24
+    st = Store(rx, g, Hq, Hkv, D, P, 1, 16, 40, B * T, pushes=pushes)
+    kc, ke, vc, ve = _tails(g, B, 40, Hkv, D)
+    lens = [int(x) for x in g.integers(T, T + 3, B)]
+    q = _bits(g, (B, T, Hq, D))
+    got = host64(st.cache.attend_streams_quant(0, dev(q), _codes(kc), _codes(vc), torch.from_numpy(ke).cuda(),
+                                               torch.from_numpy(ve).cuda(), _int(lens)))
+    for b in range(B):
+        ref, spread = OS.stream_attention(W.bf16_bits_to_f64(q[b]), st.k[0], st.v[0],
+                                          OS.dequantise(kc[b, :lens[b]], ke[b, :lens[b]]),
+                                          OS.dequantise(vc[b, :lens[b]], ve[b, :lens[b]]))
+        bound = (2.0 ** -11 + 2.0 ** -12) * spread + 2.0 ** -8 * np.abs(ref) + 1e-30
+        off = np.abs(got[b] - ref)
+        assert np.all(off <= bound), "worst %.3f of the bound" % np.max(off / bound)
+
+
 @pytest.mark.parametrize("T", [1, 4, 8])
 @pytest.mark.parametrize("power", [18, 23, 24, 25, 26, 28, 31])
 def test_attention_large_scores(rx, T, power):
