@@ -388,7 +388,7 @@ struct TailLayout {
   static constexpr int TM_O = SB * NQ;                    // TMEM: scores, then O
   static constexpr int TM_USED = TM_O + OB * NW;
   static constexpr int TM_COLS = TM_USED <= 128 ? 128 : TM_USED <= 256 ? 256 : 512;
-  static constexpr int CTAS = D == 256 || RT == 64 ? 1 : 2;   // per SM
+  static constexpr int CTAS = D == 256 || RT == 64 ? 1 : 2;   // per SM (StreamWorkspace counts on it)
   static constexpr int Q_BLOCK = NQ * ROW;                // one column block of Q
   static constexpr int Q_BYTES = KB * Q_BLOCK;
   static constexpr int W_BLOCK = WROW * kTK;              // [key][WROW]: all terms, or at 64 rows one
@@ -1238,15 +1238,17 @@ cudaError_t launch_merge(const MergeParams& p, cudaStream_t s) {
 
 // The workspace of a cache's stream calls.  A unit has at most 2 * T * G rows
 // (or 8), so all units together 2 * max_req * G (or 8 * max_req) per K/V head,
-// in units of 8 rows or more; each run (two CTAs an SM, or one run a head if
-// there are more heads) adds the rows of one unit.
+// in units of 8 rows or more; each run adds the rows of one unit: as many runs
+// as CTAs, or one a head if there are more heads.  (Units of 32 rows or fewer
+// may have twice the CTAs of 64-row units, and take no more for it.)
 struct StreamWorkspace {
   size_t runs_of, ml, o, bytes;   // offsets
   StreamWorkspace(int max_req, int Hkv, int G, int D, int num_sms) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     const size_t unit_rows_all = static_cast<size_t>(max_req) * Hkv * (2 * G > 8 ? 2 * G : 8);
-    const size_t runs = static_cast<size_t>(2 * num_sms > Hkv ? 2 * num_sms : Hkv);
-    const size_t rows = unit_rows_all + runs * unit_rows(static_cast<long long>(max_req) * G);
+    const int most_rows = unit_rows(static_cast<long long>(max_req) * G);
+    const int ctas = num_sms * (D == 256 || most_rows == 64 ? 1 : 2);
+    const size_t rows = unit_rows_all + static_cast<size_t>(ctas > Hkv ? ctas : Hkv) * most_rows;
     runs_of = 0;
     ml = up(unit_rows_all / 8 * sizeof(int2));
     o = ml + up(rows * sizeof(float2));

@@ -469,6 +469,24 @@ def test_attention_wait_that_runs_out_is_reported(rx):
     assert torch.equal(good, again)
 
 
+def test_the_tails_take_one_cta_an_sm_of_workspace(rx):
+    """What a cache with language streams holds for the tails' partials: units
+    of 64 rows for one CTA an SM and the batch's own rows, (D + 2) fp32 each."""
+    import torch
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    torch.cuda.synchronize()
+
+    def held(tail_cap):
+        free = torch.cuda.mem_get_info()[0]
+        c = rx.Cache(1, 8, 1, 256, 64, 1, 64, 4, tail_cap, 16)
+        used = free - torch.cuda.mem_get_info()[0]
+        c.close()
+        return used
+    held(32)
+    need = (64 * sms + 2 * 16 * 8) * (256 + 2) * 4
+    assert held(32) - held(0) <= need + (4 << 20)   # whole pages of 2 MiB
+
+
 def test_attention_refusals(rx):
     import torch
     g = np.random.default_rng(32)
