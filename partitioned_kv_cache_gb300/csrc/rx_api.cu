@@ -677,6 +677,12 @@ rx_status rx_attend_streams_quant(rx_cache_t h, int layer, const rx_quant_stream
   e = cudaStreamGetCaptureInfo(h->fork.side, &held, &held_id);
   if (e == cudaSuccess && held != cudaStreamCaptureStatusNone) {
     e = cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &own, &own_id);
+    // (the legacy stream beside a capture on a blocking one has no status)
+    if (e == cudaErrorStreamCaptureImplicit) {
+      cudaGetLastError();
+      e = cudaSuccess;
+      own = cudaStreamCaptureStatusNone;
+    }
     if (e == cudaSuccess && (own == cudaStreamCaptureStatusNone || own_id != held_id))
       return fail(RX_ERR_STATE, "rx_attend_streams_quant: a call of this cache is being captured on another stream");
   }

@@ -629,6 +629,42 @@ def test_attention_outside_a_capture_is_refused(rx):
     assert all(torch.equal(first, o) for o in outs)
 
 
+def test_attention_on_the_legacy_stream_beside_a_capture_is_refused(rx):
+    """The capturing stream waits on the legacy one (it is no torch stream, but
+    one made by cudaStreamCreate): a call there is refused with the same status,
+    and the capture goes on."""
+    import ctypes
+    import torch
+    g = np.random.default_rng(45)
+    st = Store(rx, g, 8, 1, 64, 16, 1, 16, 40, 4, pushes=1)
+    kc, ke, vc, ve = _tails(g, 2, 40, 1, 64)
+    q = dev(_bits(g, (2, 1, 8, 64)))
+    args = (q, _codes(kc), _codes(vc), torch.from_numpy(ke).cuda(), torch.from_numpy(ve).cuda(), _int([40, 13]))
+    first = st.cache.attend_streams_quant(0, *args)
+    outs = [torch.zeros_like(first) for _ in range(3)]
+    legacy = torch.cuda.default_stream()
+    assert legacy.cuda_stream == 0
+    cudart = ctypes.CDLL([line.split()[-1] for line in open("/proc/self/maps") if "libcudart.so" in line][0])
+    made = ctypes.c_void_p()
+    assert cudart.cudaStreamCreate(ctypes.byref(made)) == 0
+    blocking = torch.cuda.ExternalStream(made.value)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=blocking):
+        st.cache.attend_streams_quant(0, *args, out=outs[0])
+        with pytest.raises(rx.RxError) as e:
+            st.cache.attend_streams_quant(0, *args, out=outs[2], stream=legacy)
+        assert e.value.status == -7
+        st.cache.attend_streams_quant(0, *args, out=outs[1])
+    graph.replay()
+    torch.cuda.synchronize()
+    st.cache.attend_streams_quant(0, *args, out=outs[2], stream=legacy)
+    torch.cuda.synchronize()
+    assert all(torch.equal(first, o) for o in outs)
+    del graph
+    assert cudart.cudaStreamDestroy(made) == 0
+
+
 def test_a_cache_collected_within_a_capture_leaves_it_whole(rx):
     """The garbage collector may run at any place, within a capture too."""
     import gc
