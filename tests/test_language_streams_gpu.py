@@ -696,6 +696,100 @@ def test_a_cache_collected_within_a_capture_leaves_it_whole(rx):
     assert not rx._parked
 
 
+def test_attention_shares_the_exchange_area(rx):
+    """The suffix's and the batch's attention in front of and behind it, and all
+    of them in one captured graph: they use one exchange area, which the store's
+    kernel writes from a stream of the cache."""
+    import torch
+    g = np.random.default_rng(46)
+    B, T, D, cap, S = 12, 4, 256, 200, 51
+    cache = rx.Cache(1, 8, 1, D, 64, 8, 256, S, cap, B * T)
+    pk, pv = _bits(g, (1, 64, 1, D)), _bits(g, (1, 64, 1, D))
+    cache.pin_prefix(dev(pk), dev(pv))
+    for _ in range(8):
+        cache.push_frame(dev(_bits(g, (1, 256, 1, D))), dev(_bits(g, (1, 256, 1, D))))
+    kc, ke, vc, ve = _tails(g, B, cap, 1, D)
+    lens = [int(x) for x in g.integers(T, cap + 1, B)]
+    held = _int(lens)
+    tails = (_codes(kc), _codes(vc), torch.from_numpy(ke).cuda(), torch.from_numpy(ve).cuda(), held)
+    q8 = dev(_bits(g, (B, T, 8, D)))
+    qs, ks, vs = dev(_bits(g, (S, 8, D))), dev(_bits(g, (S, 1, D))), dev(_bits(g, (S, 1, D)))
+    qb = dev(_bits(g, (B, 1, 8, D)))
+    k16, v16 = (torch.from_numpy(OS.dequantise(c, e)).to(torch.bfloat16).cuda() for c, e in ((kc, ke), (vc, ve)))
+    order = "8s8b8bs8s"
+    run = {"8": lambda o: cache.attend_streams_quant(0, q8, *tails, out=o),
+           "s": lambda o: cache.attend_suffix(0, qs, ks, vs, out=o),
+           "b": lambda o: cache.attend_batch(0, None, (qb, k16, v16, held), out_lang=o)}
+    like = {"8": q8, "s": qs, "b": qb}
+    alone = {}
+    for k in "8sb":
+        alone[k] = torch.zeros_like(like[k])
+        run[k](alone[k])
+        torch.cuda.synchronize()
+    outs = [torch.zeros_like(like[k]) for k in order]
+    for k, o in zip(order, outs):
+        run[k](o)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, alone[k]) for k, o in zip(order, outs))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for k, o in zip(order, outs):
+            run[k](o)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, alone[k]) for k, o in zip(order, outs))
+    assert cache.check_device_error() == 0
+    cache.close()
+
+
+@pytest.mark.parametrize("B,T,lo,hi", [(32, 1, 1, 16000), (64, 8, 8000, 16384)])
+def test_attention_at_full_size(rx, B, T, lo, hi):
+    """Long dialogues and the largest drafts, at the sizes they are measured at."""
+    import torch
+    g = np.random.default_rng(47)
+    D, cap, P = 256, 16384, 256
+    st = Store(rx, g, 8, 1, D, P, 8, 256, cap, B * T, pushes=8)
+    gen = torch.Generator(device="cuda").manual_seed(47)
+
+    def tails():   # normal values of a random scale, as codes and exponents
+        code = torch.randn((B, cap, 1, D), generator=gen, device="cuda").mul_(100).clamp_(-448, 448).to(torch.float8_e4m3fn)
+        return code, torch.randint(119, 122, (B, cap, 1), generator=gen, device="cuda", dtype=torch.uint8)
+    (kt, ke), (vt, ve) = tails(), tails()
+    lens = [lo + (hi - lo) * ((7 * b) % B) // (B - 1) for b in range(B)]
+    q = _bits(g, (B, T, 8, D), 0.2)
+    got = host64(st.cache.attend_streams_quant(0, dev(q), kt, vt, ke, ve, _int(lens)))
+    for b in list(range(0, B, 21)) + [B - 1]:
+        k, v = (OS.dequantise(_u8(c[b, :lens[b]]), e[b, :lens[b]].cpu().numpy()) for c, e in ((kt, ke), (vt, ve)))
+        ref, spread = OS.stream_attention(W.bf16_bits_to_f64(q[b]), st.k[0], st.v[0], k, v)
+        _check(got[b], ref, spread)
+    assert st.cache.check_device_error() == 0
+
+
+def test_calls_with_their_outputs_given_allocate_nothing(rx):
+    import torch
+    g = np.random.default_rng(48)
+    st = Store(rx, g, 8, 1, 128, 16, 1, 64, 300, 12, pushes=1)
+    kc, ke, vc, ve = _tails(g, 3, 300, 1, 128)
+    tails = (_codes(kc), _codes(vc), torch.from_numpy(ke).cuda(), torch.from_numpy(ve).cuda())
+    q, xk, xv = dev(_bits(g, (3, 4, 8, 128))), dev(_bits(g, (3, 4, 1, 128))), dev(_bits(g, (3, 4, 1, 128)))
+    out, held, now = torch.empty_like(q), _int([0, 100, 290]), _int([0, 0, 0])
+
+    def step():
+        rx.tail_append_quant(*tails, held, xk, xv, new_len=now)
+        st.cache.attend_streams_quant(0, q, *tails, now, out=out)
+    step()
+    torch.cuda.synchronize()
+    before = torch.cuda.mem_get_info()[0], torch.cuda.memory_allocated(), torch.cuda.memory_stats()["allocation.all.allocated"]
+    for _ in range(5):
+        step()
+    torch.cuda.synchronize()
+    assert before == (torch.cuda.mem_get_info()[0], torch.cuda.memory_allocated(),
+                      torch.cuda.memory_stats()["allocation.all.allocated"])
+
+
 def test_attention_on_another_stream(rx):
     import torch
     g = np.random.default_rng(25)
@@ -925,6 +1019,30 @@ def test_verify_clusters_beside_other_work(rx, V):
         got.append(rx.verify_drafts(*args, n_draft=n))
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for a in got for x, y in zip(a[:2], want))
+
+
+@pytest.mark.parametrize("V", [4099, 32000, 151936])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_verify_does_not_depend_on_the_batch(rx, V, dtype):
+    """The batch's size sets the CTAs of a stream and with them the order of the
+    sums: the same rows give the same tokens whatever stands beside them."""
+    import torch
+    g = np.random.default_rng(49)
+    T, most = 2, 160
+    z = g.standard_normal((8, T + 1, V)) * 2
+    p = torch.from_numpy(_softmax(z)).to(getattr(torch, dtype)).cuda()
+    q = torch.from_numpy(_softmax(z[:, :T] + 0.5 * g.standard_normal((8, T, V)))).to(p.dtype).cuda()
+    draft = _int(np.argmax(z[:, :T] + g.gumbel(size=(8, T, V)), -1))
+    u = torch.from_numpy(g.random((8, T), dtype=np.float32)).cuda()
+    r = torch.from_numpy(g.random(8, dtype=np.float32)).cuda()
+    at = torch.arange(most, device="cuda") % 8
+    want = None
+    for B in (8, 1, 20, 40, 80, most):
+        i = at[:B]
+        tokens, n, _ = rx.verify_drafts(p[i], q[i], draft[i], u[i], r[i])
+        if want is None:
+            want = tokens, n
+        assert torch.equal(tokens, want[0][i]) and torch.equal(n, want[1][i])
 
 
 def test_verify_lengths_in_place_and_graph(rx):
