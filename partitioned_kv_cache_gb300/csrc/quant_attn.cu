@@ -1302,7 +1302,15 @@ cudaError_t launch_streams_quant(const QuantStreams& a, const AttnLaunch& al, si
   cudaError_t e = cudaEventRecord(fork.forked, s);
   if (e == cudaSuccess) e = cudaStreamWaitEvent(fork.side, fork.forked, 0);
   if (e != cudaSuccess) return e;
-  e = launch_attention_partials(al, a.q, a.B * a.T, tail_tiles, xchg_bytes, fork.side, &splits, &m_tiles, &tail_sms);
+  // A push on another stream may publish a window at any time, and the CTAs of
+  // a large batch start in several waves: all of them read the state of now.
+  AttnLaunch store = al;
+  if (fork.held) {
+    store.st = fork.held;
+    e = launch_hold_ring_state(al.st, fork.held, fork.side);
+  }
+  if (e == cudaSuccess)
+    e = launch_attention_partials(store, a.q, a.B * a.T, tail_tiles, xchg_bytes, fork.side, &splits, &m_tiles, &tail_sms);
   if (e == cudaSuccess) {
     switch (a.D) {
       case 64: e = launch_tails_d<64>(tp, RT, tail_sms, s); break;

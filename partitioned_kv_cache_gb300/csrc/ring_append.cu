@@ -241,7 +241,21 @@ __global__ void __launch_bounds__(32) pack_tiles_tma_kernel(const __grid_constan
   }
 }
 
+__global__ void hold_ring_state_kernel(const DevState* st, DevState* held) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  int head, valid;
+  load_ring_state(st, &head, &valid);
+  asm volatile("fence.acq_rel.gpu;" ::: "memory");
+  publish_ring_state(held, head, valid);
+}
+
 }  // namespace
+
+cudaError_t launch_hold_ring_state(const DevState* st, DevState* held, cudaStream_t s) {
+  const cudaError_t e = launch_k(hold_ring_state_kernel, dim3(1), dim3(1), 0, s, st, held);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
 
 cudaError_t launch_pack_tiles(const void* k_src, const void* v_src, void* k_dst, void* v_dst,
                               int L, int n, int Hkv, int D, int T, int tok0, DevState* st, int F,

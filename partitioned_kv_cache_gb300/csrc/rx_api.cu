@@ -251,7 +251,10 @@ rx_status rx_cache_create(const rx_config* cfg, rx_cache_t* out) {
   h->v_pin = reinterpret_cast<__nv_bfloat16*>(p); p += pin_b;
   h->k_win = reinterpret_cast<__nv_bfloat16*>(p); p += win_b;
   h->v_win = reinterpret_cast<__nv_bfloat16*>(p); p += win_b;
-  h->dstate = reinterpret_cast<rx::DevState*>(p); p += st_b;
+  h->dstate = reinterpret_cast<rx::DevState*>(p);
+  if (c.spare_slot) h->fork.held = h->dstate + 1;
+  static_assert(2 * sizeof(rx::DevState) <= 256, "state block");
+  p += st_b;
   h->xchg = p; p += xchg_b;
   h->xchg_bytes = xchg_b;
   h->stream_ws = p;

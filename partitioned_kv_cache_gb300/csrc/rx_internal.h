@@ -106,6 +106,10 @@ cudaError_t launch_tail_append_quant(void* k_tail, void* v_tail, uint8_t* k_exp,
                                      int* new_len, const void* k_new, const void* v_new, const int* n_new, int B,
                                      int T, int tail_cap, int Hkv, int D, int* overflow, cudaStream_t s);
 
+// held <- {head, valid} of st.  Frames that a push has published are visible to
+// the kernels after it.
+cudaError_t launch_hold_ring_state(const DevState* st, DevState* held, cudaStream_t s);
+
 // Inverse of the packing for one layer and token range (test aid):
 // dst [n][Hkv][D] <- tiles.
 cudaError_t launch_unpack_tiles(const void* k_tiles, const void* v_tiles, void* k_dst, void* v_dst,
@@ -211,6 +215,7 @@ struct StreamFork {
   cudaStream_t side = nullptr;
   cudaEvent_t forked = nullptr;
   cudaEvent_t joined = nullptr;
+  DevState* held = nullptr;    // ring with a spare slot: the state that a whole call reads
 };
 cudaError_t launch_streams_quant(const QuantStreams& a, const AttnLaunch& al, size_t xchg_bytes, void* ws, int max_req,
                                  const StreamFork& fork, cudaStream_t s);

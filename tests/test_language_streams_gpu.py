@@ -629,6 +629,52 @@ def test_attention_outside_a_capture_is_refused(rx):
     assert all(torch.equal(first, o) for o in outs)
 
 
+def test_a_push_within_an_attention_call_changes_none_of_its_rows(rx):
+    """Ring with a spare slot: a batch whose query tiles take many waves of CTAs,
+    and a push on another stream that publishes its frame in the middle.  All
+    rows see the window before the push, or all of them the one after it."""
+    import torch
+    g = np.random.default_rng(60)
+    B, T, Hq, Hkv, D, N, F = 16, 256, 64, 8, 64, 8, 256
+    cache = rx.Cache(1, Hq, Hkv, D, 64, N, F, 4, 64, B * T, 1)
+    draw = lambda *shape: torch.from_numpy(g.standard_normal(shape, dtype=np.float32)).to(torch.bfloat16).cuda()
+    cache.pin_prefix(draw(1, 64, Hkv, D), draw(1, 64, Hkv, D))
+    for _ in range(N):
+        cache.push_frame(draw(1, F, Hkv, D), draw(1, F, Hkv, D))
+    tail = torch.zeros((B, 64, Hkv, D), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    exps = torch.zeros((B, 64, Hkv), dtype=torch.uint8, device="cuda")
+    none = _int([0] * B)
+    q = torch.randn((B, T, Hq, D), generator=torch.Generator(device="cuda").manual_seed(60), device="cuda").to(torch.bfloat16)
+    attend = lambda out, s=None: cache.attend_streams_quant(0, q, tail, tail, exps, exps, none, out=out, stream=s)
+    before, after = torch.empty_like(q), torch.empty_like(q)
+    attend(before)
+    torch.cuda.synchronize()
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    attend(before)
+    end.record()
+    torch.cuda.synchronize()
+    ms = start.elapsed_time(end)
+    prod, cons = torch.cuda.Stream(priority=-1), torch.cuda.Stream()
+    got = [torch.empty_like(q) for _ in range(8)]
+    frames = [(draw(1, F, Hkv, D), draw(1, F, Hkv, D)) for _ in got]
+    torch.cuda.synchronize()
+    for i, (out, (fk, fv)) in enumerate(zip(got, frames)):
+        attend(before)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(prod):
+            torch.cuda._sleep(int(ms * 1e6 * 1.9 * (i + 1) / 9))     # cycles: into the call that follows
+        cache.push_frame_async(fk, fv, prod, cons)
+        attend(out, cons)
+        torch.cuda.synchronize()
+        attend(after)
+        torch.cuda.synchronize()
+        assert not torch.equal(before, after)
+        assert torch.equal(out, before) or torch.equal(out, after), i
+    assert cache.check_device_error() == 0
+    cache.close()
+
+
 def test_attention_on_the_legacy_stream_beside_a_capture_is_refused(rx):
     """The capturing stream waits on the legacy one (it is no torch stream, but
     one made by cudaStreamCreate): a call there is refused with the same status,
