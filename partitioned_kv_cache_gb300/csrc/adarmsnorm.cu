@@ -310,10 +310,8 @@ __global__ void __launch_bounds__(kGThreads, 1) ada_gamma_kernel(const __grid_co
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v0), "=r"(v1), "=r"(v2), "=r"(v3) : "r"(src));
       for (int pr = 0; pr < csize; ++pr) {
         if (pr == crank) continue;
-        uint32_t dst;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(src), "r"(pr));
-        asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v0), "r"(v1), "r"(v2),
-                     "r"(v3)
+        asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_peer(src, pr)), "r"(v0), "r"(v1),
+                     "r"(v2), "r"(v3)
                      : "memory");
       }
     }

@@ -107,12 +107,7 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Two fp32 values -> two e4m3 codes (the first in the low byte), and back.
-__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
+// Two e4m3 codes -> fp32.
 __device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(v)));

@@ -26,13 +26,6 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 
-// Two fp32 values -> two e4m3 codes (the first in the low byte).
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // Quantise the vector that L = D/8 consecutive lanes hold, eight bf16 values
 // each: *codes = this lane's eight codes, returns the vector's exponent byte.
 // Every lane of the warp calls it.
@@ -62,7 +55,7 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& x, uint2* codes) {
     f[2 * i] = __uint_as_float(w[i] << 16) * up;
     f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * up;
   }
-  *codes = make_uint2(e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16), e4m3x2(f[4], f[5]) | (e4m3x2(f[6], f[7]) << 16));
+  *codes = make_uint2(to_e4m3x2(f[0], f[1]) | (to_e4m3x2(f[2], f[3]) << 16), to_e4m3x2(f[4], f[5]) | (to_e4m3x2(f[6], f[7]) << 16));
   return byte;
 }
 

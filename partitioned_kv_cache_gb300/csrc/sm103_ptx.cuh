@@ -101,6 +101,20 @@ __device__ __forceinline__ void cluster_arrive_started() {
 __device__ __forceinline__ void cluster_wait_started() {
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
+// The address of this CTA's `local` in the shared memory of CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_peer(uint32_t local, int rank) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
+  return remote;
+}
+
+// -------------------------------------------------------------------- e4m3
+// Two fp32 values -> two e4m3 codes (the first in the low byte).
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 
 // Every thread of every CTA in the cluster must call this the same number of
 // times.  Release/acquire at cluster scope: memory writes made before it by

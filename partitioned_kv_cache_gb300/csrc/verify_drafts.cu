@@ -149,9 +149,7 @@ __device__ __forceinline__ int crossing(double own, double inclusive, double bas
 }
 
 __device__ __forceinline__ void st_cluster_f64(uint32_t local, int rank, double v) {
-  uint32_t remote;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
-  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(remote), "d"(v) : "memory");
+  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(cluster_peer(local, rank)), "d"(v) : "memory");
 }
 
 // This lane's terms of [v0, v1).  VEC: 16-byte loads (v0 and V are multiples of

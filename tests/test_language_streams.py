@@ -178,7 +178,7 @@ def test_binding_refuses_shapes_and_types(lib):
 
 
 # ------------------------------------------------------------ cluster starts
-@pytest.mark.parametrize("name,write", [("verify_drafts.cu", "st_cluster_f64("), ("adarmsnorm.cu", "mapa.")])
+@pytest.mark.parametrize("name,write", [("verify_drafts.cu", "st_cluster_f64("), ("adarmsnorm.cu", "cluster_peer(")])
 def test_peers_have_started_before_their_shared_memory_is_written(name, write):
     """A kernel that stores into its cluster's shared memory arrives on the
     cluster's barrier early and waits for it in front of the first store."""
