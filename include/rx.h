@@ -78,7 +78,8 @@ typedef struct rx_config {
   int F;        /* tokens per frame (>= 1)                                  */
   int S_cap;    /* most query tokens of one attention call (>= 1)           */
   int tail_cap; /* private tail capacity of a language stream (>= 0)        */
-  int max_req;  /* most language query tokens (B*T) of one rx_attend_batch  */
+  int max_req;  /* most language query tokens (B*T) of one rx_attend_batch or
+                   rx_attend_streams_quant (>= 0)                           */
   int spare_slot; /* 1: keep one spare frame slot (N+1 slots) so that pushes
                      can run concurrently with attention (rx_push_frame_async);
                      requires F % 64 == 0.  0: N slots.                      */
@@ -93,7 +94,8 @@ rx_status rx_cache_create(const rx_config* cfg, rx_cache_t* out);
 
 /* Free everything the cache owns.  Synchronises the device first, so it may not
  * be called while a stream of the process is being captured.  The handle is
- * gone whatever the status is.  NULL is a no-op.  Errors: RX_ERR_CUDA (the synchronisation or the free failed). */
+ * gone whatever the status is.  NULL is a no-op.  Errors: RX_ERR_CUDA (the
+ * synchronisation or the free failed). */
 rx_status rx_cache_destroy(rx_cache_t cache);
 
 /* Copy the instruction prefix into the pinned region ("Reflex ...", §III
@@ -128,6 +130,10 @@ rx_status rx_push_frame(rx_cache_t cache, const void* k, const void* v,
  * the window after the previous push or after this one, and the slot this push
  * overwrites can only be read by work that the producer waited for.  The push
  * runs concurrently with consumer work enqueued after the call.
+ * (rx_attend_streams_quant reads the state once for a whole call.  In the other
+ * attention calls each CTA reads it as it starts: a push that publishes while
+ * they start, which takes about a microsecond if all are resident together and
+ * most of the call if they are not, is seen by those after it.)
  * Errors: RX_ERR_STATE (cache without a spare slot), RX_ERR_ARG, RX_ERR_CUDA. */
 rx_status rx_push_frame_async(rx_cache_t cache, const void* k, const void* v,
                               int* evicted, void* producer_stream,
@@ -301,8 +307,12 @@ typedef struct rx_quant_streams {
  * appended KV).  The query tokens of stream b are the newest n_new[b] tokens
  * of its tail; token t attends, with one softmax, over [pinned; window;
  * tail_b[0, tail_len[b] - n_new[b] + t + 1)]: everything before it and itself,
- * not the tokens after it.  The cached regions are read once for all streams,
- * each tail once.  fp32 accumulation and softmax; out rounded once to bf16.
+ * not the tokens after it.  The cached regions are read once for each 128 rows
+ * (query tokens x query heads of one K/V head) of the whole batch, a tail once
+ * for each 64 rows of its stream.  fp32 accumulation and softmax; a weight
+ * enters its product with V with 16 bits over the store, and over a tail with
+ * 11, or to 2^-23 of the largest weight of its row (each times its value's
+ * scale) where that is coarser; out rounded once to bf16.
  * Rows t >= n_new[b] of out are left as they were.  A row that sees no key
  * gets zeros.  Nothing at or past tail_len[b] is used, whatever it holds; a
  * NaN token (exponent byte 255) makes the rows that see it NaN and no others.
@@ -312,7 +322,9 @@ typedef struct rx_quant_streams {
  * a stream of its own meanwhile, forked from `stream` and joined to it again
  * within the call (under capture too): to the caller it is ordered on `stream`.
  * From the first captured call to the end of its capture, calls of this cache
- * outside that capture are refused.
+ * outside that capture are refused.  All rows of a call see the same window of
+ * a ring with a spare slot.  rx_set_attn_splits and rx_set_attn_dparts have no
+ * effect here.
  * Errors: RX_ERR_ARG, RX_ERR_LAYER, RX_ERR_CAPACITY, RX_ERR_STATE (another
  * device is current, another stream is capturing), RX_ERR_CUDA. */
 rx_status rx_attend_streams_quant(rx_cache_t cache, int layer, const rx_quant_streams* streams,
@@ -339,10 +351,10 @@ rx_status rx_attend_streams_quant(rx_cache_t cache, int layer, const rx_quant_st
  * order, and with it the last of these bits, depends on B, V and the rows'
  * alignment; calls that agree in these give the same tokens.
  * p: [B][T+1][V], q: [B][T][V] or NULL, both of type prob_type; draft: int32
- * [B][T]; u: fp32 [B][T], r: fp32 [B], all in [0, 1) (r is clamped to it); n_draft: int32 [B] or
- * NULL (T), clamped to T; tail_len, new_len: int32 [B] or NULL (new_len may
- * be tail_len); tokens: int32 [B][T+1]; n_accept: int32 [B].  All DEVICE
- * memory.  V <= 2^28.  Errors: RX_ERR_ARG, RX_ERR_CUDA. */
+ * [B][T]; u: fp32 [B][T], r: fp32 [B], all in [0, 1) (r is clamped to it);
+ * n_draft: int32 [B] or NULL (T), clamped to T; tail_len, new_len: int32 [B] or
+ * NULL (new_len may be tail_len); tokens: int32 [B][T+1]; n_accept: int32 [B].
+ * All DEVICE memory.  V <= 2^28.  Errors: RX_ERR_ARG, RX_ERR_CUDA. */
 #define RX_PROB_F32 0
 #define RX_PROB_BF16 1
 rx_status rx_verify_drafts(const void* p, const void* q, int prob_type, const int* draft,
@@ -469,8 +481,9 @@ rx_status rx_debug_choose_stream_partition(int t_max, int units, long long tail_
 
 /* Number of split-KV partitions for attention launches of this cache
  * (0 = chosen from the SM count, the default).  A tuning knob: results are
- * the same for every value up to rounding order.  Errors: RX_ERR_ARG (null
- * cache, or splits outside [0, the workspace's capacity]). */
+ * the same for every value up to rounding order.  (rx_attend_streams_quant
+ * shares out its own work.)  Errors: RX_ERR_ARG (null cache, or splits outside
+ * [0, the workspace's capacity]). */
 rx_status rx_set_attn_splits(rx_cache_t cache, int splits);
 
 /* Number of CTAs that share the output columns of one (query tile, split):

@@ -12,7 +12,8 @@
 //
 // Three launches:
 //   1. the shared store against the query rows of all streams together, by
-//      the partitioned attention kernel, which writes fp32 partials;
+//      the partitioned attention kernel, which writes fp32 partials (behind a
+//      copy of the ring's state where pushes may run meanwhile);
 //   2. stream_tail_kernel: every tail against its own stream's rows, at the
 //      same time (partition.h shares out the SMs);
 //   3. stream_merge_kernel: one row's partials into its bf16 output.
@@ -46,18 +47,20 @@
 // (lengths are read on the device); a CTA takes one run of one head, and the
 // CTAs next to it the same run of the other heads, so that what a stored token
 // holds for all heads, side by side in memory, is read at about the same time
-// (64 streams of 8 heads, D = 128: 5.8 TB/s, against 4.1 when one head's tiles
-// followed the other's).  A run leaves one fp32 partial per unit that it
-// touches, in its head's slot run + unit (distinct, because going on to a
-// later run or a later unit never goes back in the other).  The scores of tile i + 1 are computed while tile i is in
-// the softmax, and the weights have two buffers, so that a tile's softmax does
-// not wait for the product before it unless a maximum grew.
+// (8 heads of 128: 6.0 TB/s, against 4.1 when one head's tiles followed the
+// other's).  A run leaves one fp32 partial per unit that it touches, in its
+// head's slot run + unit (distinct, because going on to a later run or a later
+// unit never goes back in the other).  The scores of tile i + 1 are computed
+// while tile i is in the softmax, and the weights have two buffers, so that a
+// tile's softmax does not wait for the product before it unless a maximum grew.
 //
-// What bounds it: memory up to 32 rows a unit (5.5 to 5.9 TB/s over 0.5 to 1 GB
-// of tails at D = 256), the softmax warps' issue slots at 64 rows (a tile takes
-// 3100 cycles, 2400 of them theirs, where its bytes would take 2760: 4.1 TB/s)
-// and at D = 64 (3.7 TB/s); for small calls the chain of loads and the code's
-// own arrival: one tile takes 7 us from the lengths to its partial.
+// What bounds it, over 0.54 GB of tails: memory at few rows a unit (D = 256: 6.0,
+// 5.8 and 5.75 TB/s at 8, 16 and 32 rows; D = 128: 6.0, 5.85 and 5.2; D = 64, 8
+// rows: 5.4 to 5.8); the softmax warps' issue slots beyond (64 rows at D = 256:
+// a tile takes 3100 cycles, 2400 of them theirs, where its bytes would take
+// 2760, 4.3 TB/s; at D = 128 3.0; D = 64: 3.8 at 16 rows, 1.8 at 64, where a
+// tile is 16 KB and its softmax the same); for small calls the chain of loads and
+// the code's own arrival: one tile takes 7 us from the lengths to its partial.
 //
 // Warp roles: warp 0 = TMA producer, warp 1 = TMEM allocator and MMA issuer,
 // the others = softmax and epilogue, in warpgroups of 4 warps that share up to
