@@ -309,10 +309,12 @@ typedef struct rx_quant_streams {
  * tail_b[0, tail_len[b] - n_new[b] + t + 1)]: everything before it and itself,
  * not the tokens after it.  The cached regions are read once for each 128 rows
  * (query tokens x query heads of one K/V head) of the whole batch, a tail once
- * for each 64 rows of its stream.  fp32 accumulation and softmax; a weight
- * enters its product with V with 16 bits over the store, and over a tail with
- * 11, or to 2^-23 of the largest weight of its row (each times its value's
- * scale) where that is coarser; out rounded once to bf16.
+ * for each 64 rows of its stream.  fp32 accumulation and softmax.  Against a
+ * tail's keys an entry of q keeps its 8 bits down to 2^-9 of its row's largest
+ * and is within 2^-17 of that below.  A weight enters its product with V
+ * with 16 bits over the store, and over a tail with 11, or to 2^-23 of the
+ * largest weight of its row (each times its value's scale) where that is
+ * coarser.  out is rounded once to bf16.
  * Rows t >= n_new[b] of out are left as they were.  A row that sees no key
  * gets zeros.  Nothing at or past tail_len[b] is used, whatever it holds; a
  * NaN token (exponent byte 255) makes the rows that see it NaN and no others.

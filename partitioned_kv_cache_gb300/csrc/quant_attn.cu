@@ -26,14 +26,15 @@
 // and the codes go from TMA to kind::f8f6f4 products without a conversion.
 // The bf16 queries and fp32 weights enter as sums of e4m3 terms whose products
 // meet in fp32: a query row, scaled by a power of two, is hi + lo exactly (8
-// significant bits in two 4-bit terms; what lies 2^-18 below the row's largest
-// entry is rounded away); a weight, rounded to f16, is hi + mid/16 + lo/256, each
-// term the e4m3 rounding of what is left, so it is within 2^-11 of its value,
-// an eighth of a bf16 rounding, or within 2^-23 of the largest weight that its
-// row has so far (half of lo's smallest step, 2^-17, below a reference of 2^5;
-// weights are compared with their values' scales).  Equal small weights beside
-// a large one all lose the same, so a sum of products is closed after kSegment
-// tiles: 16384 keys lose at most 2^-9 of the largest weight together.
+// significant bits in two 4-bit terms) down to 2^-9 of the row's largest entry,
+// and within 2^-17 of that (half of lo's smallest step) below.  A weight,
+// rounded to f16, is hi + mid/16 + lo/256, each term the e4m3 rounding of what
+// is left, so it is within 2^-11 of its value, an eighth of a bf16 rounding, or
+// within 2^-23 of the largest weight that its row has so far (half of lo's
+// smallest step, 2^-17, below a reference of 2^5; weights are compared with
+// their values' scales).  Equal small weights beside a large one all lose the
+// same, so a sum of products is closed after kSegment tiles: 16384 keys lose at
+// most 2^-9 of the largest weight together.
 //   x_jn = S_jn * 2^(k_exp_j - 127) * (row scale) * log2(e) / sqrt(D)
 //   l_n  = sum_j 2^(x_jn - m_n),   w_jn = 2^(x_jn + v_exp_j - 127 - M_n + 5)
 // m_n and M_n are running maxima of x_jn and of x_jn + v_exp_j - 127: the

@@ -248,7 +248,7 @@ def _capturing() -> bool:
 
 def _free_parked() -> None:
     while _parked and not _capturing():
-        _check(_lib.rx_cache_destroy(_parked.pop()), "rx_cache_destroy")
+        _lib.rx_cache_destroy(_parked.pop())   # (as in __del__, nobody is there to hear of a failure)
 
 
 class Cache:
