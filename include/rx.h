@@ -122,8 +122,8 @@ rx_status rx_push_frame(rx_cache_t cache, const void* k, const void* v,
  * into the ring buffer while Thread B reads the latest tokens and denoises).
  * Needs a cache created with spare_slot = 1.  The frame is written into the
  * spare slot, which no published window contains; the last CTA then
- * publishes {head, valid} in one 64-bit store, so an attention kernel reads
- * either the previous window or the new one, never a mix.  Ordering, by CUDA
+ * publishes {head, valid} in one 64-bit store, so a reader finds either the
+ * previous window or the new one, never a mix.  Ordering, by CUDA
  * events (no device spinning): producer_stream first waits for all work
  * already enqueued on consumer_stream, and consumer_stream waits for the
  * previous asynchronous push.  So every attention enqueued after this call sees

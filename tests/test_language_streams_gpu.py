@@ -675,6 +675,39 @@ def test_a_push_within_an_attention_call_changes_none_of_its_rows(rx):
     cache.close()
 
 
+@pytest.mark.parametrize("spare", [0, 1])
+def test_attention_graph_follows_the_ring(rx, spare):
+    """A captured call sees the frames that are pushed between its replays."""
+    import torch
+    g = np.random.default_rng(61 + spare)
+    B, T, D, N = 3, 2, 128, 3
+    st = Store(rx, g, 8, 1, D, 20, N, 64, 50, B * T, pushes=0, spare=spare)
+    kc, ke, vc, ve = _tails(g, B, 50, 1, D)
+    lens = [2, 50, 31]
+    q = _bits(g, (B, T, 8, D))
+    args = (dev(q), _codes(kc), _codes(vc), torch.from_numpy(ke).cuda(), torch.from_numpy(ve).cuda(), _int(lens))
+    out = torch.empty((B, T, 8, D), dtype=torch.bfloat16, device="cuda")
+    st.cache.attend_streams_quant(0, *args, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        st.cache.attend_streams_quant(0, *args, out=out)
+    f = W.bf16_bits_to_f64
+    frames = []
+    for _ in range(N + 3):
+        fk, fv = _bits(g, (1, 64, 1, D)), _bits(g, (1, 64, 1, D))
+        st.cache.push_frame(dev(fk), dev(fv))
+        frames.append((f(fk[0]), f(fv[0])))
+        graph.replay()
+        got = host64(out)
+        k, v = (np.concatenate([x] + [y[i] for y in frames[-N:]]) for i, x in enumerate((st.k[0], st.v[0])))
+        for b in range(B):
+            ref, spread = OS.stream_attention(f(q[b]), k, v, OS.dequantise(kc[b, :lens[b]], ke[b, :lens[b]]),
+                                              OS.dequantise(vc[b, :lens[b]], ve[b, :lens[b]]))
+            _check(got[b], ref, spread)
+    assert st.cache.check_device_error() == 0
+
+
 def test_attention_on_the_legacy_stream_beside_a_capture_is_refused(rx):
     """The capturing stream waits on the legacy one (it is no torch stream, but
     one made by cudaStreamCreate): a call there is refused with the same status,
