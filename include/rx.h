@@ -312,7 +312,7 @@ typedef struct rx_quant_streams {
  * for each 64 rows of its stream.  fp32 accumulation and softmax.  Against a
  * tail's keys an entry of q keeps its 8 bits down to 2^-9 of its row's largest
  * and is within 2^-17 of that below.  A weight enters its product with V
- * with 16 bits over the store, and over a tail with 11, or to 2^-23 of the
+ * with 16 bits over the store, and over a tail with 12, or to 2^-23 of the
  * largest weight of its row (each times its value's scale) where that is
  * coarser.  out is rounded once to bf16.
  * Rows t >= n_new[b] of out are left as they were.  A row that sees no key

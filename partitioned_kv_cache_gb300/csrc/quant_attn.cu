@@ -27,10 +27,11 @@
 // The bf16 queries and fp32 weights enter as sums of e4m3 terms whose products
 // meet in fp32: a query row, scaled by a power of two, is hi + lo exactly (8
 // significant bits in two 4-bit terms) down to 2^-9 of the row's largest entry,
-// and within 2^-17 of that (half of lo's smallest step) below.  A weight,
-// rounded to f16, is hi + mid/16 + lo/256, each term the e4m3 rounding of what
-// is left, so it is within 2^-11 of its value, an eighth of a bf16 rounding, or
-// within 2^-23 of the largest weight that its row has so far (half of lo's
+// and within 2^-17 of that (half of lo's smallest step) below.  A weight
+// is hi + mid/16 + lo/256, each term the e4m3 rounding of what is left, so it is
+// within 2^-12 of its value, a sixteenth of a bf16 rounding (rounded to f16
+// first it was within 2^-11, and 64 x 8 queries took 113.9 instead of 114.8 us
+// over tails to 16384), or within 2^-23 of the largest weight that its row has so far (half of lo's
 // smallest step, 2^-17, below a reference of 2^5; weights are compared with
 // their values' scales).  Equal small weights beside a large one all lose the
 // same, so a sum of products is closed after kSegment tiles: 16384 keys lose at
@@ -931,16 +932,20 @@ __global__ void __launch_bounds__(TailLayout<D, RT>::THREADS, TailLayout<D, RT>:
             l[j + e] += ex2(u[j + e]);
             w[e] = ex2(u[j + e] + ev + dj[e]);
           }
-          // Each term is what e4m3 left of the f16 weight so far, 16 times
-          // larger: three of 4 bits hold f16's 11.
-          uint32_t h01 = to_f16x2(w[0], w[1]), h23 = to_f16x2(w[2], w[3]);
+          // Each term is what e4m3 left of the weight so far, 16 times larger;
+          // what the first left fits f16's 11 bits but for 2^-15 of the weight.
+          const uint32_t c01 = to_e4m3x2(w[0], w[1]), c23 = to_e4m3x2(w[2], w[3]);
+          codes[0][j / 4] = c01 | c23 << 16;
+          const float2 f01 = from_e4m3x2(c01), f23 = from_e4m3x2(c23);
+          uint32_t h01 = to_f16x2((w[0] - f01.x) * kTermStep, (w[1] - f01.y) * kTermStep);
+          uint32_t h23 = to_f16x2((w[2] - f23.x) * kTermStep, (w[3] - f23.y) * kTermStep);
 #pragma unroll
-          for (int term = 0; term < kTerms; ++term) {
-            const uint32_t c01 = f16x2_to_e4m3x2(h01), c23 = f16x2_to_e4m3x2(h23);
-            codes[term][j / 4] = c01 | c23 << 16;
+          for (int term = 1; term < kTerms; ++term) {
+            const uint32_t d01 = f16x2_to_e4m3x2(h01), d23 = f16x2_to_e4m3x2(h23);
+            codes[term][j / 4] = d01 | d23 << 16;
             if (term + 1 < kTerms) {
-              h01 = e4m3x2_rest(h01, c01);
-              h23 = e4m3x2_rest(h23, c23);
+              h01 = e4m3x2_rest(h01, d01);
+              h23 = e4m3x2_rest(h23, d23);
             }
           }
         }

@@ -315,6 +315,35 @@ def test_attention_weights_are_not_rounded_to_16_bits(rx, Hq, Hkv, D, P, pushes,
         assert np.all(off <= bound), "worst %.3f of the bound" % np.max(off / bound)
 
 
+@pytest.mark.parametrize("T", [1, 2, 8])
+def test_attention_weights_over_a_tail_keep_12_bits(rx, T):
+    """Two keys whose values nearly cancel, so that the output's own rounding is
+    small beside the weights' errors: three e4m3 terms are within 2^-12 of a
+    weight (2^-4 of a remainder each), the fp32 steps at scores below 8 within
+    2^-16."""
+    import torch
+    g = np.random.default_rng(70 + T)
+    B, D, f = 120, 64, W.bf16_bits_to_f64
+    st = Store(rx, g, 8, 1, D, 0, 1, 16, 8, B * T, pushes=0)
+    kc, ke = OS.quantise(f(_bits(g, (B, 8, 1, D))))
+    v = np.ones((B, 8, 1, D))
+    v[:, 1:] = -2.0 ** g.integers(-3, 4, (B, 7, 1, D)) * (1 + g.integers(0, 8, (B, 7, 1, D)) / 8)   # e4m3 holds them
+    vc, ve = OS.quantise(v)
+    lens = [T + 1] * B
+    q = _bits(g, (B, T, 8, D), 0.5)
+    got = host64(st.cache.attend_streams_quant(0, dev(q), _codes(kc), _codes(vc), torch.from_numpy(ke).cuda(),
+                                               torch.from_numpy(ve).cuda(), _int(lens)))
+    near = 0
+    for b in range(B):
+        ref, spread = OS.stream_attention(f(q[b]), st.k[0], st.v[0], OS.dequantise(kc[b, :T + 1], ke[b, :T + 1]),
+                                          OS.dequantise(vc[b, :T + 1], ve[b, :T + 1]))
+        bound = (2.0 ** -12 + 2.0 ** -16) * spread + 2.0 ** -8 * np.abs(ref)
+        near += np.sum(np.abs(ref) < 0.02 * spread)
+        off = np.abs(got[b] - ref)
+        assert np.all(off <= bound), "worst %.3f of the bound" % np.max(off / bound)
+    assert near > 300
+
+
 @pytest.mark.parametrize("T", [1, 4, 8])
 @pytest.mark.parametrize("power", [18, 23, 24, 25, 26, 28, 31])
 def test_attention_large_scores(rx, T, power):
