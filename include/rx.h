@@ -364,6 +364,138 @@ rx_status rx_verify_drafts(const void* p, const void* q, int prob_type, const in
                            int V, const int* tail_len, int* tokens, int* n_accept,
                            int* new_len, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Language streams over a paged cache.  A layer's keys and values live in a
+ * pool of pages that streams take as they grow ("OxyGen ...", §"Core method":
+ * streams append private KV to a shared prefill cache); place j of stream b is
+ * row j % page of page table[b][j / page].  An entry of a table that is read
+ * while it lies outside [0, n_pages) names no page: nothing is stored there and
+ * the attention does not see its keys.  The new tokens of a step are packed:
+ * those of stream b are [q_start[b], q_start[b+1]) of N, so prompts' chunks and
+ * single tokens share a call; tokens outside every such range are left alone.
+ * Lengths and tables are read on the device, so a captured graph follows them. */
+typedef struct rx_pages {
+  void* k;            /* bf16 [n_pages][page][Hkv][D]                            */
+  void* v;            /* bf16 [n_pages][page][Hkv][D]                            */
+  float* weight;      /* fp32 [n_pages][page][Hkv] or NULL: the attention weight
+                         that each key has gathered (rx_weigh_pages)             */
+  const int* table;   /* DEVICE int32 [B][max_pages]                             */
+  int n_pages;        /* >= 1                                                    */
+  int page;           /* tokens of a page: 16, 32, 64, 128 or 256                */
+  int max_pages;      /* >= 1; a stream holds at most 2^30 keys                  */
+  int B;              /* streams, 0 to 1024                                      */
+} rx_pages;
+
+/* What the heads of a projection become: an RMS norm of each query and key head
+ * (where its weight is given), y_i = x_i * rsqrt(mean x^2 + eps) * w_i, then the
+ * rotation of its pairs by the token's position, pair i by the angle
+ * pos[axis(i)] * freq[i]:
+ *   (a, b) -> (a cos - b sin, b cos + a sin).
+ * Pair i is elements (i, i + R/2), or (2i, 2i + 1) with adjacent = 1, where R/2
+ * is the sum of the sections; elements from R on are not rotated.  The first
+ * sections[0] pairs turn with axis 0, the next sections[1] with axis 1, and so
+ * on (time, height and width of a video's tokens).  Angles keep their fraction
+ * of a turn to 2^-31 at every 32-bit position. */
+#define RX_MAX_AXES 4
+typedef struct rx_heads {
+  const float* freq;       /* DEVICE fp32 [R/2], finite                          */
+  const float* q_weight;   /* DEVICE fp32 [D] or NULL: queries are not normed    */
+  const float* k_weight;   /* DEVICE fp32 [D] or NULL: keys are not normed       */
+  int Hq, Hkv;
+  int D;                   /* 64, 128 or 256                                     */
+  int n_axes;              /* 1 to RX_MAX_AXES                                   */
+  int sections[RX_MAX_AXES];   /* pairs of each axis, >= 0; the sum R/2 is a
+                                  multiple of 8 in [0, D/2]                      */
+  int adjacent;            /* 0 or 1                                             */
+  float eps;               /* >= 0                                               */
+} rx_heads;
+
+/* Heads of N tokens: x bf16 [N][Hq + 2*Hkv][D] (queries, keys, values; rows of
+ * tokens row_stride elements apart, a multiple of 8, at least (Hq+2*Hkv)*D);
+ * pos int32 [n_axes][N].  q [N][Hq][D] and k [N][Hkv][D] are normed and rotated,
+ * v [N][Hkv][D] is copied: what rx_attend_suffix and rx_push_frame take.  fp32
+ * arithmetic, one rounding to bf16.  No output may overlap an input or another
+ * output.  Errors: RX_ERR_ARG, RX_ERR_UNSUPPORTED (D), RX_ERR_CUDA. */
+rx_status rx_rotate_heads(const void* x, long long row_stride, int N, const rx_heads* heads,
+                          const int* pos, void* q, void* k, void* v, void* stream);
+
+/* rx_rotate_heads with the keys and values stored in the pages: token t of stream
+ * b's new ones at place held[b] + t, its weight (where the pages have any) set to
+ * 0.  Tokens past the table's capacity or in a page that the table does not name
+ * are dropped, and bit 0 of *overflow is set (so is it, and nothing is stored,
+ * for a stream whose held[b] is outside [0, max_pages*page]).  new_len[b] =
+ * min(held[b] + its new tokens, max_pages*page) (held[b] where that is outside).
+ * held is not changed, so all layers of a step share it.  A place may not be
+ * written by two tokens of one call.  q_start: int32 [B+1], not decreasing, held
+ * and new_len: int32 [B], all DEVICE; new_len, overflow may be NULL.
+ * Errors: RX_ERR_ARG, RX_ERR_UNSUPPORTED (D), RX_ERR_CUDA. */
+rx_status rx_rotate_heads_paged(const void* x, long long row_stride, int N, const rx_heads* heads,
+                                const int* pos, void* q, const rx_pages* pages, const int* q_start,
+                                const int* held, int* new_len, int* overflow, void* stream);
+
+/* Attention of a step's new tokens.  With n = q_start[b+1] - q_start[b] new
+ * tokens of stream b, whose keys are the newest n of its len[b], token t attends
+ * with one softmax over
+ *   [pinned; window; places below max(len[b] - n + t + 1, min(prefix[b], len[b]))]
+ * : everything before it and itself, and all of a prefix (prefix NULL: none).
+ * The cached regions are those of `layer` of `cache`; cache NULL: pages only.
+ * q, out: bf16 [N][Hq][D]; lse: fp32 [N][Hq] or NULL, the logarithm of the sum of
+ * the exponentials of the row's scores.  fp32 accumulation and softmax; a weight
+ * enters its product with V rounded to bf16, out is rounded once to bf16.  A row
+ * that sees no key gets zeros and lse -infinity.  Rows of tokens in no stream's
+ * range are left as they were.  Whatever lies at places that a row does not see,
+ * infinities and NaN among it, has no part in it; a row that sees a key or value
+ * that is not finite is not finite.  q_start: int32 [B+1], not decreasing; len,
+ * prefix: int32 [B] (len clamped to [0, max_pages*page]), all DEVICE.  Hq, Hkv and
+ * D are the cache's where one is given.  workspace: DEVICE memory of
+ * rx_attend_pages_workspace bytes, 256-byte aligned, for this call alone while
+ * it runs.  out, lse and the workspace may not overlap an input or each other.
+ * All rows of a call see the same window of a ring with a spare slot.  A wait
+ * that gives up makes its rows NaN and, with a cache, sets bit 3 of its error
+ * word.  Errors: RX_ERR_ARG, RX_ERR_LAYER, RX_ERR_UNSUPPORTED (D, Hq/Hkv),
+ * RX_ERR_CAPACITY (workspace_bytes), RX_ERR_STATE (the cache is on another
+ * device), RX_ERR_CUDA. */
+rx_status rx_attend_pages(rx_cache_t cache, int layer, const void* q, int N, int Hq, int Hkv, int D,
+                          const rx_pages* pages, const int* q_start, const int* len, const int* prefix,
+                          void* out, float* lse, void* workspace, long long workspace_bytes,
+                          void* stream);
+rx_status rx_attend_pages_workspace(int N, int Hq, int Hkv, int D, long long* bytes);
+
+/* The attention weight that keys gather from a step's new tokens: for every key j
+ * of a stream with new tokens and every K/V head h
+ *   out[j][h] = decay * weight[j][h] + sum exp(q . k_j / sqrt(D) - lse)
+ * over the new tokens that see j (as in rx_attend_pages, with the same q, lens and
+ * prefix, after it) and the query heads of group h.  decay 0: weight is not read.
+ * out: fp32 [n_pages][page][Hkv], may be the pages' weight; NULL means that.  Other
+ * places of out are left as they were.  A page may belong to one stream of a call
+ * only.  The same inputs give the same bits.  lse: fp32 [N][Hq] DEVICE (-infinity:
+ * the row weighs nothing).  out may not overlap another input.
+ * Errors: RX_ERR_ARG, RX_ERR_UNSUPPORTED (D, Hq/Hkv), RX_ERR_CUDA. */
+rx_status rx_weigh_pages(const void* q, const float* lse, int N, int Hq, int Hkv, int D,
+                         const rx_pages* pages, const int* q_start, const int* len, const int* prefix,
+                         float decay, float* out, void* stream);
+
+/* Cut streams back to `budget` keys.  Of a stream with len[b] > budget, every K/V
+ * head keeps its first `sink` keys, its last `recent`, and of those between the
+ * budget - sink - recent with the largest weight (ties: the earlier key; NaN, and
+ * a key in a page that the table does not name, last).  Kept keys close up in
+ * their order, with their weights: place i now holds what was at
+ * kept[b][h][i].  Shorter streams keep all.  new_len[b] = min(len[b], budget);
+ * kept is -1 from there on.
+ * to NULL: in place, in pages that belong to one stream of the call each.  Else
+ * the new places are those of the table `to` [B][to_max_pages], whose pages of the
+ * same pool are in no other stream's table and not among the old ones (so that a
+ * prefix which streams share can be cut for one of them), and the old pages keep
+ * what they hold.  A kept key whose old or new page is not named is dropped, and
+ * bit 0 of *overflow is set.
+ * len, new_len: int32 [B], new_len may be len, or NULL; kept: int32
+ * [B][Hkv][budget]; overflow: int32 or NULL; all DEVICE.  0 <= sink, recent,
+ * sink + recent <= budget, 1 <= budget <= 2^30.
+ * Errors: RX_ERR_ARG, RX_ERR_UNSUPPORTED (D), RX_ERR_CUDA. */
+rx_status rx_evict_pages(const rx_pages* pages, int Hkv, int D, const int* len, int sink, int recent,
+                         int budget, const int* to, int to_max_pages, int* new_len, int* kept,
+                         int* overflow, void* stream);
+
 /* Ring-state snapshot / restore (execution-state capsules as in the FlashRT
  * summary page: snapshot and restore of the named static buffers).  A
  * snapshot holds the pinned prefix, the window, the device-side ring state
@@ -480,6 +612,16 @@ rx_status rx_debug_choose_partition(int t_max, int units, int D, int num_sms, in
  * (num_sms, max_splits)). */
 rx_status rx_debug_choose_stream_partition(int t_max, int units, long long tail_tiles, int num_sms,
                                            int max_splits, int* splits, int* tail_sms);
+
+/* Test aid: how rx_attend_pages numbers its work, computed on the host.  A stream
+ * with n new tokens, len keys and a prefix reads `shared` 64-key tiles of the store
+ * for every row tile of 128/G tokens, G = Hq/Hkv.  *before: key tiles of row tiles
+ * [0, r) of one head; *row_tile: the row tile that tile *before belongs to (r), -1
+ * for r = the number of row tiles.  Touches no device.  Errors: RX_ERR_ARG (a null
+ * pointer, n < 1, a negative size or one above 2^30, G no power of two up to 128,
+ * r outside [0, row tiles]). */
+rx_status rx_debug_page_plan(int n, int len, int prefix, int shared, int G, int r, long long* before,
+                             int* row_tile);
 
 /* Number of split-KV partitions for attention launches of this cache
  * (0 = chosen from the SM count, the default).  A tuning knob: results are

@@ -25,11 +25,13 @@ LIB = os.path.join(PKG, "librx.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
           "--expt-relaxed-constexpr"]
-# The attention kernel's softmax uses the fast exp2 path; the gamma MLP keeps
-# precise sin/cos/pow/exp.
-PER_FILE = {"partitioned_attn.cu": ["--use_fast_math"]}
+# The attention kernels' softmax (and the weights that keys gather) uses the
+# fast exp2 path; the gamma MLP and the rotation of heads keep precise
+# sin/cos/pow/exp.
+PER_FILE = {f: ["--use_fast_math"] for f in ("partitioned_attn.cu", "page_attn.cu", "page_weigh.cu")}
 SOURCES = ["rx_api.cu", "ring_append.cu", "adarmsnorm.cu", "partitioned_attn.cu", "attend_static.cu",
-           "quant_tail.cu", "quant_attn.cu", "verify_drafts.cu"]
+           "quant_tail.cu", "quant_attn.cu", "verify_drafts.cu", "rotate_heads.cu", "page_attn.cu",
+           "page_weigh.cu", "page_evict.cu"]
 
 
 def nvcc() -> str:

@@ -1,0 +1,941 @@
+// page_attn.cu -- attention of packed new tokens over a paged cache, behind the
+// shared store, on tcgen05 (sm_103a).
+//
+// "OxyGen: Unified KV Cache Management for Vision-Language-Action Models under
+// Multi-Task Parallelism", §"Core method": language streams share a read-only
+// prefill cache and append keys of their own; here those keys live in pages,
+// and a step may bring any number of new tokens to a stream (one when it
+// decodes, a chunk when a prompt enters).  With n new tokens at the end of len
+// keys, token t attends with one softmax over
+//   [pinned; window; places below max(len - n + t + 1, min(prefix, len))],
+// and lse = log of the sum of the exponentials of its scores.
+//
+// Work.  A unit is (stream, K/V head, 128 query rows), row r = token r / G, head
+// r % G of the group.  All units' 64-key tiles are numbered in a row
+// (page_plan.h) and cut into equal runs, one per CTA; a CTA works its run off
+// unit by unit, its rings of K and V tiles never stopping in between.  A unit
+// that lies in one run is finished there; of a cut unit every CTA leaves its
+// part (O, m, l) in fp32 in the workspace and merge_kernel joins the parts in
+// the order of the keys.  Lengths are read on the device.
+//
+// Inside a CTA the steps are those of the suffix's attention: S = Q K^T and
+// O += P V on tcgen05 with accumulators in tensor memory, P (bf16) back to
+// tensor memory as the A operand, one thread per row for the softmax, O
+// rescaled only when a row's maximum grows by more than 2^8.  A weight enters
+// P V rounded to bf16 (2^-9 of it): beside the output's own rounding it is felt
+// as 0.0017 -> 0.002 in the relative error, and two terms would cost half of
+// P V again.
+//
+// Masked places.  Scores are masked by selection, so whatever a place behind
+// the stream's end, in a page that the table does not name, or after a token
+// holds, it weighs nothing.  A weight of 0 times an infinity or NaN in V would
+// still be NaN: in tiles where not every row sees every key the softmax warps
+// read V's tile in shared memory first and write zeros over rows that are
+// outside or not finite; rows that see a key whose value is not finite become
+// NaN.
+//
+// Warps (224 threads): 0 = copies (lane 0 K, lane 1 V, lane 2 Q), 1 = tensor
+// memory and Q K^T, 2..5 = softmax and epilogue, 6 = P V.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "page_plan.h"
+#include "pages.h"
+#include "rx_internal.h"
+#include "sm103_ptx.cuh"
+
+namespace rx {
+namespace {
+
+constexpr int kThreads = 224;
+constexpr float kRescale = 8.0f;   // log2 units
+constexpr int kMinRun = 4;         // key tiles of a CTA, at least
+constexpr int kMergeThreads = 256;
+constexpr int kMergeFew = 8;       // parts that one thread of the merge takes
+
+template <int D>
+struct Layout {
+  static constexpr int KB = D / 64;
+  static constexpr int CTAS = D == 256 ? 1 : 2;             // per SM
+  static constexpr int Q_BLOCK = kBM * 128;
+  static constexpr int Q_BYTES = KB * Q_BLOCK;
+  static constexpr int TILE = static_cast<int>(tile_bytes(D));
+  static constexpr int NK = D == 256 ? 3 : D == 128 ? 2 : 5;
+  static constexpr int NV = D == 256 ? 2 : D == 128 ? 2 : 5;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = Q_BYTES;
+  static constexpr int OFF_V = OFF_K + NK * TILE;
+  static constexpr int OFF_BAR = OFF_V + NV * TILE;
+  static constexpr int OFF_MISC = OFF_BAR + 40 * 8;
+  static constexpr int BYTES = OFF_MISC + 128;
+  static constexpr int ALLOC = BYTES + 1024;
+  // Tensor memory: O, two S buffers, and P: at D = 128 in the columns of the
+  // scores that it was made from (two CTAs share the 512), else beside them.
+  static constexpr bool P_IN_S = D == 128;
+  static constexpr int TMEM = D == 256 ? 512 : 256;
+  static_assert(D + 2 * kBN + (P_IN_S ? 0 : kBN) <= TMEM, "tensor memory");
+  static_assert(CTAS * (ALLOC + 1024) <= 233472, "shared memory");
+};
+
+// Barriers: Q full / empty, K full / empty [5], V full / empty [5], S full [2],
+// P full [2], P V done [2], O read, values checked, drained.
+enum : int {
+  B_QF = 0, B_QE = 1, B_KF = 2, B_KE = 7, B_VF = 12, B_VE = 17, B_SF = 22, B_PF = 24, B_PV = 26, B_OR = 28,
+  B_CHK = 29, B_DRAIN = 30
+};
+
+// The parts that merge_kernel joins: those of the unit that CTA c's run begins
+// and does not end (rows 0: none).
+struct CutUnit {
+  int token;   // first of the row tile
+  int rows;
+  int head;    // K/V head
+  int parts;
+};
+
+struct PageAttnParams {
+  CUtensorMap tm_q;            // (D, G, Hkv, N), box (64, G, 1, 128/G)
+  CUtensorMap tm_k;            // (D, Hkv, page, n_pages), box (64, 1, min(page, 64), 1)
+  CUtensorMap tm_v;
+  const uint8_t* k_tiles[2];   // store: pinned, window of (layer, head 0)
+  const uint8_t* v_tiles[2];
+  long long head_stride[2];
+  const DevState* st;          // null: no store
+  int P, F, frames, slots;
+  PagePool pool;
+  const int* q_start;
+  const int* len;
+  const int* prefix;
+  int N, Hq, Hkv, log_g;
+  __nv_bfloat16* out;
+  float* lse;
+  float4* part;                // [2 * grid][D/4][part_rows]
+  float2* part_ml;             // [2 * grid][part_rows]
+  CutUnit* cut;                // [grid]
+  int part_rows;
+  int* err;
+  int inject_tx;
+  float scale_log2;
+};
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  const bool ok = mbar_wait(bar, parity, abort);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// The store's tiles: pinned, then the window in slot order, past the spare slot.
+struct StoreTiles {
+  int n_pin, n_win, P, win_len, hole0, hole_n;
+  __device__ __forceinline__ int count() const { return n_pin + n_win; }
+  __device__ __forceinline__ int valid(int t) const {
+    return min(kBN, t < n_pin ? P - t * kBN : win_len - (t - n_pin) * kBN);
+  }
+};
+
+__device__ __forceinline__ StoreTiles store_tiles(const PageAttnParams& p, int head, int valid) {
+  StoreTiles s{0, 0, 0, 0, 0, 0};
+  if (!p.st) return s;
+  const bool hole = p.slots > p.frames && valid == p.frames;
+  s.P = p.P;
+  s.win_len = hole ? (p.slots - 1) * p.F : valid * p.F;
+  s.hole0 = hole ? head * p.F / kBN : 0;
+  s.hole_n = hole ? p.F / kBN : 0;
+  s.n_pin = (p.P + kBN - 1) / kBN;
+  s.n_win = (s.win_len + kBN - 1) / kBN;
+  return s;
+}
+
+struct Stream {
+  StreamPlan plan;
+  int q0;
+  int prefix;   // min(prefix, len), 0 without one
+};
+
+__device__ __forceinline__ Stream load_stream(const PageAttnParams& p, int shared, int b) {
+  Stream s;
+  s.q0 = max(0, min(__ldg(p.q_start + b), p.N));
+  const int q1 = max(0, min(__ldg(p.q_start + b + 1), p.N));
+  s.plan.n = max(0, q1 - s.q0);
+  s.plan.len = held_keys(p.pool, p.len, b);
+  s.prefix = p.prefix ? max(0, min(__ldg(p.prefix + b), s.plan.len)) : 0;
+  s.plan.floor = max(1, s.prefix);
+  s.plan.shared = shared;
+  s.plan.log_a = 7 - p.log_g;
+  return s;
+}
+
+// Where a run begins: tile `at` of stream b; `left` tiles from there.
+struct RunStart {
+  long long at;
+  long long left;
+  int b;
+};
+
+// A walk over the parts of units in a run.
+struct Walk {
+  Stream s;
+  int b, h, rt;
+  int t0, count, tiles;   // the part: tiles [t0, t0 + count) of the unit's `tiles`
+  long long left;
+
+  __device__ __forceinline__ bool begin(const PageAttnParams& p, int shared, const RunStart& r) {
+    left = r.left;
+    if (left <= 0) return false;
+    b = r.b;
+    s = load_stream(p, shared, b);
+    const long long per_head = s.plan.tiles_before(s.plan.row_tiles());
+    h = static_cast<int>(r.at / per_head);
+    const long long o = r.at - h * per_head;
+    rt = s.plan.row_tile_of(o);
+    t0 = static_cast<int>(o - s.plan.tiles_before(rt));
+    measure();
+    return true;
+  }
+  __device__ __forceinline__ void measure() {
+    tiles = s.plan.tiles(rt);
+    count = static_cast<int>(min(left, static_cast<long long>(tiles - t0)));
+  }
+  __device__ __forceinline__ bool next(const PageAttnParams& p) {
+    left -= count;
+    if (left <= 0) return false;
+    t0 = 0;
+    if (++rt == s.plan.row_tiles()) {
+      rt = 0;
+      if (++h == p.Hkv) {
+        h = 0;
+        do {
+          if (++b >= p.pool.B) return false;
+          s = load_stream(p, s.plan.shared, b);
+        } while (s.plan.n == 0);
+      }
+    }
+    measure();
+    return true;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, Layout<D>::CTAS) page_attn_kernel(const __grid_constant__ PageAttnParams p) {
+  using Lay = Layout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const uint32_t sQ = base + Lay::OFF_Q, sK = base + Lay::OFF_K, sV = base + Lay::OFF_V, sBar = base + Lay::OFF_BAR;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + Lay::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + Lay::OFF_MISC + 4);
+  int* ring_word = reinterpret_cast<int*>(gbase + Lay::OFF_MISC + 8);
+  RunStart* run_start = reinterpret_cast<RunStart*>(gbase + Lay::OFF_MISC + 16);      // 24 bytes
+  int* run_len = reinterpret_cast<int*>(gbase + Lay::OFF_MISC + 40);
+  uint16_t* not_finite = reinterpret_cast<uint16_t*>(gbase + Lay::OFF_MISC + 64);     // [2][4]
+  auto BAR = [&](int i) { return sBar + 8u * static_cast<uint32_t>(i); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 31; ++i) {
+      const bool all = (i >= B_PF && i < B_PF + 2) || i == B_OR || i == B_CHK;
+      mbar_init(BAR(i), all ? 128 : i == B_DRAIN ? 2 : 1);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), Lay::TMEM);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&p.tm_q);
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  // ---- this CTA's run.  The streams' tiles go through shared memory that the
+  // rings use afterwards.
+  if (threadIdx.x == 0 && p.st) load_ring_state(p.st, ring_word, ring_word + 1);
+  __syncthreads();
+  const StoreTiles store = store_tiles(p, ring_word[0], ring_word[1]);
+  const int shared = store.count();
+  long long* before = reinterpret_cast<long long*>(gbase + Lay::OFF_K);   // [B + 1]
+  for (int b = threadIdx.x; b < p.pool.B; b += kThreads) {
+    const Stream s = load_stream(p, shared, b);
+    before[b + 1] = p.Hkv * s.plan.tiles_before(s.plan.row_tiles());
+  }
+  __syncthreads();
+  if (warp == 0) {
+    long long sum = 0;
+    for (int b0 = 0; b0 < p.pool.B; b0 += 32) {
+      long long x = b0 + lane < p.pool.B ? before[b0 + lane + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (b0 + lane < p.pool.B) before[b0 + lane + 1] = sum + x;
+      sum += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) before[0] = 0;
+    __syncwarp();
+    if (lane == 0) {
+      const long long each = max(static_cast<long long>(kMinRun), (sum + gridDim.x - 1) / gridDim.x);
+      const long long w0 = each * blockIdx.x, w1 = min(sum, w0 + each);
+      int lo = 0, hi = p.pool.B - 1;
+      while (lo < hi) {   // the last stream that begins at or before w0
+        const int mid = (lo + hi + 1) >> 1;
+        if (before[mid] <= w0) lo = mid;
+        else hi = mid - 1;
+      }
+      run_start->at = w0 - before[lo];
+      run_start->left = w1 - w0;
+      run_start->b = lo;
+      *run_len = static_cast<int>(each);
+    }
+  }
+  // The scratch was written by the generic proxy; copies will write it next.
+  fence_proxy_async_smem();
+  __syncthreads();
+  const RunStart run = *run_start;
+
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tO = tmem, tS = tmem + D, tP = Lay::P_IN_S ? tS : tS + 2 * kBN;
+  constexpr int kPStride = Lay::P_IN_S ? kBN : kBN / 2;   // columns between the two P buffers
+  const int lp = p.pool.log_page;
+  const int box = lp < 6 ? 1 << lp : kBN;                 // tokens of one page copy
+
+  Walk w;
+  const bool some = w.begin(p, shared, run);
+  if (some && warp == 0) {
+    // ------------------------------------------------------------ copies
+    if (lane < 2) {
+      const bool isv = lane == 1;
+      const CUtensorMap* tm = isv ? &p.tm_v : &p.tm_k;
+      const int slots = isv ? Lay::NV : Lay::NK;
+      const int bf = isv ? B_VF : B_KF, be = isv ? B_VE : B_KE;
+      const uint32_t ring = isv ? sV : sK;
+      int slot = 0, round = 0, issued = 0;
+      bool more = true, stop = false;
+      do {
+        const int* table = p.pool.table + static_cast<long long>(w.b) * p.pool.max_pages;
+        for (int t = w.t0; t < w.t0 + w.count; ++t) {
+          int pg[4];
+          const int key0 = (t - shared) * kBN;
+          if (t >= shared) {   // the table's entries are asked for before the wait for a slot
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int place = key0 + i * box;
+              pg[i] = i * box < kBN && place < w.s.plan.len ? __ldg(table + (place >> lp)) : -1;
+            }
+          }
+          if (round > 0 && !mbar_wait(BAR(be + slot), (round - 1) & 1, abort_flag)) {
+            stop = true;
+            break;
+          }
+          const uint32_t dst = ring + slot * Lay::TILE, bar = BAR(bf + slot);
+          const uint32_t extra = issued == 0 && !isv && blockIdx.x == 0 ? static_cast<uint32_t>(p.inject_tx) : 0u;
+          if (t < shared) {
+            const int region = t < store.n_pin ? 0 : 1;
+            int at = region ? t - store.n_pin : t;
+            if (region && at >= store.hole0) at += store.hole_n;
+            const uint8_t* tiles = isv ? p.v_tiles[region] : p.k_tiles[region];
+            mbar_arrive_expect_tx(bar, Lay::TILE + extra);
+            bulk_load(dst, tiles + w.h * p.head_stride[region] + static_cast<long long>(at) * Lay::TILE, Lay::TILE, bar);
+          } else {
+            uint32_t named = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              named += static_cast<unsigned int>(pg[i]) < static_cast<unsigned int>(p.pool.n_pages);
+            mbar_arrive_expect_tx(bar, named * box * (D * 2) + extra);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (static_cast<unsigned int>(pg[i]) >= static_cast<unsigned int>(p.pool.n_pages)) continue;
+              const int row = lp > 6 ? key0 & ((1 << lp) - 1) : 0;
+              for (int kb = 0; kb < Lay::KB; ++kb)
+                tma_load_4d(dst + kb * 8192 + i * box * 128, tm, kb * 64, w.h, row, pg[i], bar);
+            }
+          }
+          ++issued;
+          if (++slot == slots) {
+            slot = 0;
+            ++round;
+          }
+        }
+        more = !stop && w.next(p);
+      } while (more);
+      // Every copy issued lands before the CTA exits, after an abort too.
+      volatile int no_abort = 0;
+      for (int i = max(0, issued - slots); i < issued; ++i) mbar_wait(BAR(bf + i % slots), (i / slots) & 1, &no_abort);
+    } else if (lane == 2) {
+      int u = 0;
+      do {
+        if (u > 0 && !mbar_wait(BAR(B_QE), (u - 1) & 1, abort_flag)) break;
+        mbar_arrive_expect_tx(BAR(B_QF), Lay::Q_BYTES);
+        const int token = w.s.q0 + (w.rt << w.s.plan.log_a);
+        for (int kb = 0; kb < Lay::KB; ++kb) tma_load_4d(sQ + kb * Lay::Q_BLOCK, &p.tm_q, kb * 64, 0, w.h, token, BAR(B_QF));
+        ++u;
+      } while (w.next(p));
+      volatile int no_abort = 0;
+      if (u > 0) mbar_wait(BAR(B_QF), (u - 1) & 1, &no_abort);
+    }
+  } else if (some && warp == 1) {
+    // ------------------------------------------------------------ Q K^T
+    if (lane == 0) {
+      constexpr uint32_t kIdesc = idesc_bf16_f32(kBM, kBN, false, false);
+      int j = 0, slot = 0, round = 0, u = 0;
+      bool ok = true;
+      do {
+        ok = mbar_wait(BAR(B_QF), u & 1, abort_flag);
+        for (int t = 0; ok && t < w.count; ++t, ++j) {
+          const int st = j & 1;
+          // The buffer held the scores of tile j - 2: read by the softmax once
+          // it has published P, or (P in its columns) once P V is done.
+          if (j >= 2 && !mbar_wait(BAR((Lay::P_IN_S ? B_PV : B_PF) + st), ((j - 2) >> 1) & 1, abort_flag)) { ok = false; break; }
+          if (!mbar_wait(BAR(B_KF + slot), round & 1, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t kt = sK + slot * Lay::TILE;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t kb = kk >> 2, ko = (kk & 3) * 32;
+            umma_bf16(tS + st * kBN, sdesc_sw128(sQ + kb * Lay::Q_BLOCK + ko, 16, 1024),
+                      sdesc_sw128(kt + kb * 8192 + ko, 16, 1024), kIdesc, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(BAR(B_KE + slot));
+          if (t == w.count - 1) umma_commit(BAR(B_QE));
+          umma_commit(BAR(B_SF + st));
+          if (++slot == Lay::NK) {
+            slot = 0;
+            ++round;
+          }
+        }
+        ++u;
+      } while (ok && w.next(p));
+      umma_commit(BAR(B_DRAIN));
+      volatile int no_abort = 0;
+      mbar_wait(BAR(B_DRAIN), 0, &no_abort);
+    }
+  } else if (some && warp == 6) {
+    // ------------------------------------------------------------ P V
+    if (lane == 0) {
+      constexpr uint32_t kIdesc = idesc_bf16_f32(kBM, D, false, true);
+      int j = 0, slot = 0, round = 0, u = 0;
+      bool ok = true;
+      do {
+        for (int t = 0; t < w.count; ++t, ++j) {
+          const int st = j & 1;
+          if (!mbar_wait(BAR(B_PF + st), (j >> 1) & 1, abort_flag)) { ok = false; break; }
+          if (!mbar_wait(BAR(B_VF + slot), round & 1, abort_flag)) { ok = false; break; }
+          // O still holds the last unit until the softmax warps have read it.
+          if (t == 0 && u > 0 && !mbar_wait(BAR(B_OR), (u - 1) & 1, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t vt = sV + slot * Lay::TILE;
+#pragma unroll
+          for (int kk = 0; kk < kBN / 16; ++kk)
+            umma_bf16_ts(tO, tP + st * kPStride + kk * 8, sdesc_sw128(vt + kk * 16 * 128, 8192, 1024), kIdesc,
+                         (t > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(BAR(B_VE + slot));
+          umma_commit(BAR(B_PV + st));
+          if (++slot == Lay::NV) {
+            slot = 0;
+            ++round;
+          }
+        }
+        ++u;
+      } while (ok && w.next(p));
+      umma_commit(BAR(B_DRAIN));
+      volatile int no_abort = 0;
+      mbar_wait(BAR(B_DRAIN), 0, &no_abort);
+    }
+  } else if (warp >= 2 && warp <= 5) {
+    // ------------------------------------------------------------ softmax
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const bool first_thread = threadIdx.x == 64;
+    if (first_thread) p.cut[blockIdx.x] = CutUnit{0, 0, 0, 0};
+    int j = 0, vslot = 0, vround = 0, checks = 0;
+    bool ok = true, more = some;
+    while (more) {
+      const int t_row = (w.rt << w.s.plan.log_a) + (row >> p.log_g);
+      const bool row_valid = t_row < w.s.plan.n;
+      const int x0 = w.s.plan.len - w.s.plan.n;
+      // Places below lim are seen by this row, those below all by every row.
+      const int lim = row_valid ? max(x0 + t_row + 1, w.s.prefix) : 0;
+      const int all = max(x0 + (w.rt << w.s.plan.log_a) + 1, w.s.prefix);
+      const int* table = p.pool.table + static_cast<long long>(w.b) * p.pool.max_pages;
+      // This lane's table entry for a tile: its page i = lane, or the tile's page.
+      const int own_at = lp < 6 ? (lane & ((kBN >> lp) - 1)) << lp : 0;
+      auto entry = [&](int t) {
+        const int place = (t - shared) * kBN + own_at;
+        return t >= shared && place < w.s.plan.len ? __ldg(table + (place >> lp)) : 0;
+      };
+      int ent = entry(w.t0);
+      float m_used = -INFINITY, l = 0.f;
+      bool poison = false;
+      for (int t = w.t0; ok && t < w.t0 + w.count; ++t, ++j) {
+        const int st = j & 1;
+        // Keys of the tile that are there.
+        uint64_t there = ~0ull, mine;
+        bool check;
+        if (t < shared) {
+          const int nv = store.valid(t);
+          if (nv < kBN) there = (1ull << nv) - 1;
+          check = nv < kBN;
+          mine = there;
+        } else {
+          const int key0 = (t - shared) * kBN;
+          const int nv = w.s.plan.len - key0;
+          const uint32_t named = __ballot_sync(0xffffffffu, static_cast<unsigned int>(ent) < static_cast<unsigned int>(p.pool.n_pages));
+          if (named != 0xffffffffu) {
+            if (lp >= 6) {
+              there = 0;
+            } else {
+              there = 0;
+              for (int i = 0; i < (kBN >> lp); ++i)
+                if (named >> i & 1) there |= ((1ull << (1 << lp)) - 1) << (i << lp);
+            }
+          }
+          if (nv < kBN) there = nv > 0 ? there & ((1ull << nv) - 1) : 0;
+          check = there != ~0ull || key0 + kBN > all;
+          mine = there;
+          const int seen = lim - key0;
+          if (seen < kBN) mine = seen > 0 ? mine & ((1ull << seen) - 1) : 0;
+        }
+        ent = entry(t + 1);
+        if (!warp_wait(BAR(B_SF + st), (j >> 1) & 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        float s[kBN];
+        tmem_ld32(tS + st * kBN + lane_off, s);
+        tmem_ld32(tS + st * kBN + 32 + lane_off, s + 32);
+        if (check) {
+          const uint32_t lo = static_cast<uint32_t>(mine), hi = static_cast<uint32_t>(mine >> 32);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            if (!(lo >> c & 1)) s[c] = -INFINITY;
+            if (!(hi >> c & 1)) s[32 + c] = -INFINITY;
+          }
+          // V's rows: two threads each.  P V of tile j - 2 first: until then
+          // V's barrier may be one phase behind, and its parity would pass.
+          if (j >= 2 && !warp_wait(BAR(B_PV + st), ((j - 2) >> 1) & 1, abort_flag)) { ok = false; break; }
+          if (!warp_wait(BAR(B_VF + vslot), vround & 1, abort_flag)) { ok = false; break; }
+          const int vr = row >> 1;
+          const uint32_t at = sV + vslot * Lay::TILE + vr * 128;
+          constexpr int kChunks = D / 16;
+          const int c0 = (row & 1) * kChunks;
+          const bool outside = !(there >> vr & 1);
+          uint32_t odd = 0;
+          if (!outside) {
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+              const int c = c0 + i;
+              uint32_t x[4];
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                           : "r"(at + (c >> 3) * 8192 + (((c & 7) ^ (vr & 7)) << 4)));
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                odd |= ((x[e] & 0x7F80u) == 0x7F80u) | ((x[e] & 0x7F800000u) == 0x7F800000u);
+            }
+          }
+          odd |= __shfl_xor_sync(0xffffffffu, odd, 1);
+          if (outside || odd) {
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) st_shared_v4(at + ((c0 + i) >> 3) * 8192 + (((c0 + i) & 7) << 4), 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          uint32_t pairs = __ballot_sync(0xffffffffu, odd != 0) & 0x55555555u;   // even lanes -> 16 bits
+          pairs = (pairs | pairs >> 1) & 0x33333333u;
+          pairs = (pairs | pairs >> 2) & 0x0F0F0F0Fu;
+          pairs = (pairs | pairs >> 4) & 0x00FF00FFu;
+          pairs = (pairs | pairs >> 8) & 0x0000FFFFu;
+          volatile uint16_t* bits = not_finite + (checks & 1) * 4;
+          if (lane == 0) bits[quarter] = static_cast<uint16_t>(pairs);
+          mbar_arrive(BAR(B_CHK));
+          if (!warp_wait(BAR(B_CHK), checks & 1, abort_flag)) { ok = false; break; }
+          ++checks;
+          uint64_t bad = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) bad |= static_cast<uint64_t>(bits[i]) << (16 * i);
+          poison = poison || (bad & mine) != 0;
+        }
+        if (++vslot == Lay::NV) {
+          vslot = 0;
+          ++vround;
+        }
+        float t32[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) t32[c] = fmaxf(s[c], s[c + 32]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+          for (int c = 0; c < o; ++c) t32[c] = fmaxf(t32[c], t32[c + o]);
+        const float m_new = fmaxf(m_used, t32[0] * p.scale_log2);
+        const bool need = m_new > m_used + kRescale;
+        float fac = 1.f;
+        if (need) {
+          fac = exp2f(m_used - m_new);
+          l *= fac;
+          m_used = m_new;
+        }
+        if (__any_sync(0xffffffffu, need && t > w.t0)) {
+          if (!warp_wait(BAR(B_PV + ((j - 1) & 1)), ((j - 1) >> 1) & 1, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(tO + c + lane_off, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= fac;
+            tmem_st32(tO + c + lane_off, o);
+          }
+        }
+        const float nmb = m_used == -INFINITY ? 0.f : -m_used;
+        uint32_t pk[kBN / 2];
+        float sums[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kBN / 2; ++c) {
+          const float a = exp2f(fmaf(s[2 * c], p.scale_log2, nmb));
+          const float b = exp2f(fmaf(s[2 * c + 1], p.scale_log2, nmb));
+          sums[c & 3] += a + b;
+          pk[c] = pack_bf16x2(a, b);
+        }
+        l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+        if (j >= 2 && !warp_wait(BAR(B_PV + st), ((j - 2) >> 1) & 1, abort_flag)) { ok = false; break; }
+        tmem_st32(tP + st * kPStride + lane_off, reinterpret_cast<const float*>(pk));
+        tc_fence_before();
+        mbar_arrive(BAR(B_PF + st));
+      }
+      if (ok) ok = warp_wait(BAR(B_PV + ((j - 1) & 1)), ((j - 1) >> 1) & 1, abort_flag);
+      tc_fence_after();
+      if (poison || !ok) l = NAN;
+      // ---- the part's end
+      const bool begins = w.t0 == 0, ends = w.t0 + w.count == w.tiles;
+      const int first = (w.rt << w.s.plan.log_a);
+      const int h = w.h * (1 << p.log_g) + (row & ((1 << p.log_g) - 1));
+      const size_t at = static_cast<size_t>(w.s.q0 + t_row) * p.Hq + h;
+      if (begins && ends) {
+        const float inv = l > 0.f ? 1.f / l : l;   // l = 0: a row without keys gets zeros; NaN stays
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          if (ok) {
+            tmem_ld32(tO + c + lane_off, o);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+          }
+          if (row_valid) {
+            uint4* d4 = reinterpret_cast<uint4*>(p.out + at * D + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              d4[i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                 pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+          }
+        }
+        if (row_valid && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.693147180559945309f;
+      } else {
+        const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (begins ? 1 : 0);
+        float4* dst = p.part + slot * (D / 4) * p.part_rows + row;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          if (ok) {
+            tmem_ld32(tO + c + lane_off, o);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+          }
+          if (row_valid) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[static_cast<size_t>(c / 4 + i) * p.part_rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        if (row_valid) p.part_ml[slot * p.part_rows + row] = make_float2(m_used, l);
+        if (first_thread && begins) {
+          const int rest = w.tiles - w.count, each = *run_len;
+          p.cut[blockIdx.x] = CutUnit{w.s.q0 + first, min(1 << w.s.plan.log_a, w.s.plan.n - first) << p.log_g, w.h,
+                                      1 + (rest + each - 1) / each};
+        }
+      }
+      if (ok) {
+        tc_fence_before();
+        mbar_arrive(BAR(B_OR));
+      }
+      more = w.next(p);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, Lay::TMEM);
+  if (threadIdx.x == 0 && *abort_flag && p.err) atomicOr(p.err, kErrStreamTimeout);
+}
+
+// Joins the parts of cut units: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
+// Part s of CTA c's unit is in slot 2 c + 1 (s = 0) or 2 (c + s).  An item is four
+// columns of a row, rows fastest.  Units of up to kMergeFew parts: a thread per
+// item; of more: a warp takes every eighth part of 32 items and the eight warps
+// meet in shared memory.
+struct MergeParams {
+  const float4* part;
+  const float2* part_ml;
+  const CutUnit* cut;
+  int ctas;
+  int part_rows;
+  __nv_bfloat16* out;
+  float* lse;
+  int Hq, log_g;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) page_merge_kernel(const __grid_constant__ MergeParams p) {
+  extern __shared__ int s_before[];   // chunks before CTA c's unit [ctas + 1]
+  __shared__ float4 s_o[8][32];
+  __shared__ float2 s_ml[8][32];
+  __shared__ int s_sum[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  int sum = 0;
+  for (int c0 = 0; c0 < p.ctas; c0 += kMergeThreads) {
+    const int c = c0 + threadIdx.x;
+    int x = 0;
+    if (c < p.ctas) {
+      const CutUnit u = p.cut[c];
+      const int per = u.parts <= kMergeFew ? kMergeThreads : 32;
+      x = (u.rows * (D / 4) + per - 1) / per;
+    }
+    int y = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    if (lane == 31) s_sum[warp] = y;
+    __syncthreads();
+    int add = sum;
+    for (int i = 0; i < 8; ++i) {
+      if (i < warp) add += s_sum[i];
+      sum += s_sum[i];
+    }
+    if (c < p.ctas) s_before[c] = add + y - x;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) s_before[p.ctas] = sum;
+  __syncthreads();
+  for (int chunk = blockIdx.x; chunk < sum; chunk += gridDim.x) {
+    int lo = 0, hi = p.ctas - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_before[mid] <= chunk) lo = mid;
+      else hi = mid - 1;
+    }
+    const CutUnit u = p.cut[lo];
+    const bool few = u.parts <= kMergeFew;
+    const int items = u.rows * (D / 4);
+    const int want = (chunk - s_before[lo]) * (few ? kMergeThreads : 32) + (few ? static_cast<int>(threadIdx.x) : lane);
+    const int item = min(want, items - 1);
+    const int row = item % u.rows, k = item / u.rows;
+    const float4* po = p.part + static_cast<size_t>(k) * p.part_rows + row;
+    const float2* pm = p.part_ml + row;
+    const size_t stride = static_cast<size_t>(D / 4) * p.part_rows;
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int first = few ? 0 : warp, step = few ? 1 : 8;
+    for (int s0 = first; s0 < u.parts; s0 += 8 * step) {
+      float4 o[8];
+      float2 ml[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int s = s0 + i * step;
+        ml[i] = make_float2(-INFINITY, 0.f);
+        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s < u.parts) {
+          const size_t slot = s == 0 ? 2 * static_cast<size_t>(lo) + 1 : 2 * static_cast<size_t>(lo + s);
+          ml[i] = __ldcg(pm + slot * p.part_rows);
+          o[i] = __ldcg(po + slot * stride);
+        }
+      }
+      float m = M;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, ml[i].x);
+      const float ref = m == -INFINITY ? 0.f : m;
+      const float f = exp2f(M - ref);
+      M = m;
+      L *= f;
+      acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float g = exp2f(ml[i].x - ref);   // 0 for a part that saw nothing
+        L = fmaf(g, ml[i].y, L);
+        acc.x = fmaf(g, o[i].x, acc.x);
+        acc.y = fmaf(g, o[i].y, acc.y);
+        acc.z = fmaf(g, o[i].z, acc.z);
+        acc.w = fmaf(g, o[i].w, acc.w);
+      }
+    }
+    if (!few) {
+      s_o[warp][lane] = acc;
+      s_ml[warp][lane] = make_float2(M, L);
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) M = fmaxf(M, s_ml[i][lane].x);
+        const float ref = M == -INFINITY ? 0.f : M;
+        L = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 ml = s_ml[i][lane];
+          const float4 o = s_o[i][lane];
+          const float g = exp2f(ml.x - ref);
+          L = fmaf(g, ml.y, L);
+          acc.x = fmaf(g, o.x, acc.x);
+          acc.y = fmaf(g, o.y, acc.y);
+          acc.z = fmaf(g, o.z, acc.z);
+          acc.w = fmaf(g, o.w, acc.w);
+        }
+      }
+    }
+    if (want < items && (few || warp == 0)) {
+      const float inv = L > 0.f ? 1.f / L : L;
+      const int G = 1 << p.log_g;
+      const size_t at = static_cast<size_t>(u.token + (row >> p.log_g)) * p.Hq + u.head * G + (row & (G - 1));
+      *reinterpret_cast<uint2*>(p.out + at * D + k * 4) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (k == 0 && p.lse) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
+    }
+    if (!few) __syncthreads();
+  }
+}
+
+struct Workspace {
+  int ctas, part_rows;
+  size_t part, ml, cut, bytes;   // offsets
+};
+
+Workspace workspace(int N, int G, int D, int num_sms) {
+  Workspace w;
+  w.ctas = num_sms * (D == 256 ? 1 : 2);
+  const long long rows = static_cast<long long>(N) * G;
+  w.part_rows = static_cast<int>(rows < kBM ? (rows + 7) / 8 * 8 : kBM);
+  const size_t slots = 2 * static_cast<size_t>(w.ctas);
+  w.part = 0;
+  w.ml = w.part + slots * w.part_rows * D * 4;
+  w.cut = w.ml + slots * w.part_rows * 8;
+  w.bytes = w.cut + static_cast<size_t>(w.ctas) * sizeof(CutUnit);
+  return w;
+}
+
+template <int D>
+cudaError_t launch_d(const PageAttnParams& p, const Workspace& w, int dev, int num_sms, cudaStream_t s) {
+  using Lay = Layout<D>;
+  static std::atomic<unsigned long long> ready{0};
+  cudaError_t e = once_per_device(ready, dev, [] {
+    return cudaFuncSetAttribute(page_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::ALLOC);
+  });
+  if (e != cudaSuccess) return e;
+  e = launch_k(page_attn_kernel<D>, dim3(w.ctas), dim3(kThreads), Lay::ALLOC, s, p);
+  if (e != cudaSuccess) return e;
+  MergeParams m{p.part, p.part_ml, p.cut, w.ctas, p.part_rows, p.out, p.lse, p.Hq, p.log_g};
+  e = launch_k(page_merge_kernel<D>, dim3(num_sms * 4), dim3(kMergeThreads), (w.ctas + 1) * sizeof(int), s, m);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attend_pages_workspace(int N, int Hq, int Hkv, int D, int num_sms) {
+  return workspace(N, Hq / Hkv, D, num_sms).bytes;
+}
+
+cudaError_t launch_attend_pages(const PageAttention& a, const PagePool& pool, const AttnLaunch* al, void* ws,
+                                cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = device_sm_count(dev, &sms);
+  if (e != cudaSuccess) return e;
+  const int G = a.Hq / a.Hkv, D = a.D, page = 1 << pool.log_page;
+  PageAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  {
+    const uint64_t u = 2, dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(G), static_cast<uint64_t>(a.Hkv), static_cast<uint64_t>(a.N)};
+    const uint64_t strides[3] = {D * u, D * u * G, D * u * a.Hq};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(G), 1, static_cast<uint32_t>(kBM / G)};
+    if (!encode_tmap_4d(&p.tm_q, a.q, dims, strides, box)) return cudaErrorInvalidValue;
+    const uint64_t pd[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.Hkv), static_cast<uint64_t>(page), static_cast<uint64_t>(pool.n_pages)};
+    const uint64_t ps[3] = {D * u, D * u * a.Hkv, D * u * a.Hkv * page};
+    const uint32_t pb[4] = {64, 1, static_cast<uint32_t>(page < kBN ? page : kBN), 1};
+    if (!encode_tmap_4d(&p.tm_k, pool.k, pd, ps, pb) || !encode_tmap_4d(&p.tm_v, pool.v, pd, ps, pb)) return cudaErrorInvalidValue;
+  }
+  if (al) {
+    p.k_tiles[0] = static_cast<const uint8_t*>(al->pin_k_tiles);
+    p.k_tiles[1] = static_cast<const uint8_t*>(al->win_k_tiles);
+    p.v_tiles[0] = static_cast<const uint8_t*>(al->pin_v_tiles);
+    p.v_tiles[1] = static_cast<const uint8_t*>(al->win_v_tiles);
+    p.head_stride[0] = al->pin_head_stride;
+    p.head_stride[1] = al->win_head_stride;
+    p.st = al->st;
+    p.P = al->P;
+    p.F = al->F;
+    p.frames = al->N;
+    p.slots = al->slots;
+    p.err = al->err;
+    p.inject_tx = al->inject_tx;
+  }
+  p.pool = pool;
+  p.q_start = a.q_start;
+  p.len = a.len;
+  p.prefix = a.prefix;
+  p.N = a.N;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  while ((1 << p.log_g) < G) ++p.log_g;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.lse = a.lse;
+  const Workspace w = workspace(a.N, G, D, sms);
+  char* at = static_cast<char*>(ws);
+  p.part = reinterpret_cast<float4*>(at + w.part);
+  p.part_ml = reinterpret_cast<float2*>(at + w.ml);
+  p.cut = reinterpret_cast<CutUnit*>(at + w.cut);
+  p.part_rows = w.part_rows;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
+  switch (D) {
+    case 64: return launch_d<64>(p, w, dev, sms, s);
+    case 128: return launch_d<128>(p, w, dev, sms, s);
+    case 256: return launch_d<256>(p, w, dev, sms, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace rx

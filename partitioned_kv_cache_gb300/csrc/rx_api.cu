@@ -23,6 +23,8 @@
 #include <string>
 
 #include "rx.h"
+#include "page_plan.h"
+#include "pages.h"
 #include "partition.h"
 #include "rx_internal.h"
 
@@ -748,6 +750,319 @@ rx_status rx_verify_drafts(const void* p, const void* q, int prob_type, const in
   cudaError_t e = rx::launch_verify_drafts(p, q, prob_type == RX_PROB_BF16, draft, u, r, n_draft, B, T, V, tail_len,
                                            tokens, n_accept, new_len, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rx_verify_drafts: launch");
+  return RX_OK;
+  RX_GUARD_END
+}
+
+// ---- language streams over a paged cache
+
+static int log2_of(int x) {
+  int l = 0;
+  while ((1 << l) < x) ++l;
+  return l;
+}
+
+// Checks a pool of pages with Hkv heads of D values and gives its device form
+// and its size; `spans` receives k, v, weight and table.
+static rx_status check_pages(const char* where, const rx_pages* g, int Hkv, int D, rx::PagePool* pool, Span spans[4]) {
+  if (!g) return fail(RX_ERR_ARG, "%s: null pages", where);
+  if (Hkv < 1 || Hkv > (1 << 16)) return fail(RX_ERR_ARG, "%s: Hkv = %d", where, Hkv);
+  if (D != 64 && D != 128 && D != 256) return fail(RX_ERR_UNSUPPORTED, "%s: head dim %d not in {64, 128, 256}", where, D);
+  if (g->page < 16 || g->page > 256 || !pow2(g->page))
+    return fail(RX_ERR_ARG, "%s: a page of %d tokens is not one of 16, 32, 64, 128, 256", where, g->page);
+  if (g->n_pages < 1 || g->max_pages < 1 || g->B < 0 || g->B > rx::kMaxPagedStreams)
+    return fail(RX_ERR_ARG, "%s: n_pages, max_pages or B out of range", where);
+  const long long rows = static_cast<long long>(g->n_pages) * g->page;
+  if (rows > (1LL << 46) / (static_cast<long long>(Hkv) * D)) return fail(RX_ERR_ARG, "%s: the pool is too large", where);
+  if (g->B > 0 && (!g->k || !g->v || !g->table)) return fail(RX_ERR_ARG, "%s: null pointer in the pages", where);
+  if (!aligned16(g->k) || !aligned16(g->v) || !aligned4(g->weight) || !aligned4(g->table))
+    return fail(RX_ERR_ARG, "%s: misaligned pointer in the pages", where);
+  const long long kb = rows * Hkv * D * 2, wb = rows * Hkv * 4, tb = static_cast<long long>(g->B) * g->max_pages * 4;
+  spans[0] = {g->k, kb};
+  spans[1] = {g->v, kb};
+  spans[2] = {g->weight, wb};
+  spans[3] = {g->table, tb};
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < i; ++j)
+      if (spans_overlap(spans[i].p, spans[i].bytes, spans[j].p, spans[j].bytes))
+        return fail(RX_ERR_ARG, "%s: keys, values, weights and table of the pages overlap", where);
+  *pool = rx::PagePool{g->k, g->v, g->weight, g->table, g->n_pages, log2_of(g->page), g->max_pages, g->B};
+  return RX_OK;
+}
+
+// No output may overlap an input or another output.
+static rx_status check_apart(const char* where, const Span* outs, int n_out, const Span* in, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      if (spans_overlap(outs[i].p, outs[i].bytes, in[j].p, in[j].bytes))
+        return fail(RX_ERR_ARG, "%s: an output overlaps an input", where);
+    for (int j = 0; j < i; ++j)
+      if (spans_overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+        return fail(RX_ERR_ARG, "%s: outputs overlap", where);
+  }
+  return RX_OK;
+}
+
+static rx_status check_heads(const char* where, const void* x, long long row_stride, int N, const rx_heads* heads,
+                             const int* pos, const void* q, rx::HeadRotation* r) {
+  if (!heads) return fail(RX_ERR_ARG, "%s: null heads", where);
+  const rx_heads& t = *heads;
+  if (t.Hq < 1 || t.Hkv < 1 || t.Hq > (1 << 16) || t.Hkv > (1 << 16) || N < 0)
+    return fail(RX_ERR_ARG, "%s: Hq, Hkv or N out of range", where);
+  if (t.D != 64 && t.D != 128 && t.D != 256)
+    return fail(RX_ERR_UNSUPPORTED, "%s: head dim %d not in {64, 128, 256}", where, t.D);
+  if (t.n_axes < 1 || t.n_axes > RX_MAX_AXES) return fail(RX_ERR_ARG, "%s: n_axes = %d not in [1, %d]", where, t.n_axes, RX_MAX_AXES);
+  if (t.adjacent != 0 && t.adjacent != 1) return fail(RX_ERR_ARG, "%s: adjacent must be 0 or 1", where);
+  if (!(t.eps >= 0.f)) return fail(RX_ERR_ARG, "%s: eps must be >= 0", where);
+  long long pairs = 0;
+  for (int a = 0; a < RX_MAX_AXES; ++a) {
+    if (a < t.n_axes) {
+      if (t.sections[a] < 0 || t.sections[a] > t.D) return fail(RX_ERR_ARG, "%s: sections[%d] = %d", where, a, t.sections[a]);
+      pairs += t.sections[a];
+    }
+    r->section_end[a] = static_cast<int>(pairs);
+  }
+  if (pairs % 8 || pairs > t.D / 2)
+    return fail(RX_ERR_ARG, "%s: the sections hold %lld pairs: not a multiple of 8 up to D/2", where, pairs);
+  const long long width = static_cast<long long>(t.Hq + 2 * t.Hkv) * t.D;
+  if (row_stride < width || row_stride % 8 || row_stride > (1LL << 40))
+    return fail(RX_ERR_ARG, "%s: row_stride = %lld must be a multiple of 8, at least %lld", where, row_stride, width);
+  if (static_cast<long long>(N) * (t.Hq + 2 * t.Hkv) > (1LL << 31) - 1) return fail(RX_ERR_ARG, "%s: N*(Hq+2*Hkv) above 2^31", where);
+  if (N > 0) {
+    if (!x || !pos || !q || (pairs > 0 && !t.freq)) return fail(RX_ERR_ARG, "%s: null pointer", where);
+    if (!aligned16(x) || !aligned16(q) || !aligned4(pos) || !aligned4(t.freq) || !aligned4(t.q_weight) || !aligned4(t.k_weight))
+      return fail(RX_ERR_ARG, "%s: misaligned pointer", where);
+  }
+  r->freq = t.freq;
+  r->q_weight = t.q_weight;
+  r->k_weight = t.k_weight;
+  r->Hq = t.Hq;
+  r->Hkv = t.Hkv;
+  r->D = t.D;
+  r->pairs = static_cast<int>(pairs);
+  r->axes = t.n_axes;
+  r->adjacent = t.adjacent;
+  r->eps = t.eps;
+  return RX_OK;
+}
+
+// The inputs of a call that rotates heads.
+static int heads_inputs(const void* x, long long row_stride, int N, const rx_heads& t, int pairs, const int* pos, Span* in) {
+  const long long width = static_cast<long long>(t.Hq + 2 * t.Hkv) * t.D;
+  in[0] = {x, N > 0 ? ((N - 1) * row_stride + width) * 2 : 0};
+  in[1] = {pos, static_cast<long long>(t.n_axes) * N * 4};
+  in[2] = {t.freq, pairs * 4LL};
+  in[3] = {t.q_weight, t.D * 4LL};
+  in[4] = {t.k_weight, t.D * 4LL};
+  return 5;
+}
+
+rx_status rx_rotate_heads(const void* x, long long row_stride, int N, const rx_heads* heads, const int* pos, void* q,
+                          void* k, void* v, void* stream) {
+  RX_GUARD_BEGIN
+  rx::HeadRotation r{};
+  rx_status st = check_heads("rx_rotate_heads", x, row_stride, N, heads, pos, q, &r);
+  if (st != RX_OK) return st;
+  if (N == 0) return RX_OK;
+  if (!k || !v) return fail(RX_ERR_ARG, "rx_rotate_heads: null pointer");
+  if (!aligned16(k) || !aligned16(v)) return fail(RX_ERR_ARG, "rx_rotate_heads: misaligned pointer");
+  Span in[5];
+  const int n_in = heads_inputs(x, row_stride, N, *heads, r.pairs, pos, in);
+  const long long kb = static_cast<long long>(N) * r.Hkv * r.D * 2;
+  const Span outs[3] = {{q, static_cast<long long>(N) * r.Hq * r.D * 2}, {k, kb}, {v, kb}};
+  st = check_apart("rx_rotate_heads", outs, 3, in, n_in);
+  if (st != RX_OK) return st;
+  const cudaError_t e = rx::launch_rotate_heads(x, row_stride, N, r, pos, q, k, v, rx::PagePool{}, nullptr, nullptr, nullptr,
+                                                nullptr, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rx_rotate_heads: launch");
+  return RX_OK;
+  RX_GUARD_END
+}
+
+rx_status rx_rotate_heads_paged(const void* x, long long row_stride, int N, const rx_heads* heads, const int* pos,
+                                void* q, const rx_pages* pages, const int* q_start, const int* held, int* new_len,
+                                int* overflow, void* stream) {
+  RX_GUARD_BEGIN
+  const char* where = "rx_rotate_heads_paged";
+  rx::HeadRotation r{};
+  rx_status st = check_heads(where, x, row_stride, N, heads, pos, q, &r);
+  if (st != RX_OK) return st;
+  rx::PagePool pool{};
+  Span g[4];
+  st = check_pages(where, pages, r.Hkv, r.D, &pool, g);
+  if (st != RX_OK) return st;
+  if (pool.B == 0) return RX_OK;
+  if (!q_start || !held) return fail(RX_ERR_ARG, "%s: null pointer", where);
+  if (!aligned4(q_start) || !aligned4(held) || !aligned4(new_len) || !aligned4(overflow))
+    return fail(RX_ERR_ARG, "%s: misaligned pointer", where);
+  const long long lens = pool.B * 4LL;
+  Span in[8];
+  int n_in = heads_inputs(x, row_stride, N, *heads, r.pairs, pos, in);
+  in[n_in++] = g[3];
+  in[n_in++] = {q_start, lens + 4};
+  in[n_in++] = {held, lens};
+  const Span outs[6] = {{q, static_cast<long long>(N) * r.Hq * r.D * 2}, g[0], g[1], g[2], {new_len, lens}, {overflow, 4}};
+  st = check_apart(where, outs, 6, in, n_in);
+  if (st != RX_OK) return st;
+  const cudaError_t e = rx::launch_rotate_heads(x, row_stride, N, r, pos, q, nullptr, nullptr, pool, q_start, held, new_len,
+                                                overflow, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rx_rotate_heads_paged: launch");
+  return RX_OK;
+  RX_GUARD_END
+}
+
+// Query heads over the pages' K/V heads, and the packed tokens.
+static rx_status check_queries(const char* where, const void* q, int N, int Hq, int Hkv, const int* q_start, const int* len,
+                               const int* prefix) {
+  if (N < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv) return fail(RX_ERR_ARG, "%s: N, Hq or Hkv out of range", where);
+  const int G = Hq / Hkv;
+  if (!pow2(G) || G > rx::kBM) return fail(RX_ERR_UNSUPPORTED, "%s: Hq/Hkv = %d must be a power of two <= 128", where, G);
+  if (static_cast<long long>(N) * Hq > (1LL << 31) - 1) return fail(RX_ERR_ARG, "%s: N*Hq above 2^31", where);
+  if (N > 0 && (!q || !q_start || !len)) return fail(RX_ERR_ARG, "%s: null pointer", where);
+  if (!aligned16(q) || !aligned4(q_start) || !aligned4(len) || !aligned4(prefix))
+    return fail(RX_ERR_ARG, "%s: misaligned pointer", where);
+  return RX_OK;
+}
+
+rx_status rx_attend_pages_workspace(int N, int Hq, int Hkv, int D, long long* bytes) {
+  RX_GUARD_BEGIN
+  const char* where = "rx_attend_pages_workspace";
+  if (!bytes) return fail(RX_ERR_ARG, "%s: null pointer", where);
+  if (N < 0) return fail(RX_ERR_ARG, "%s: N < 0", where);
+  rx_status st = check_queries(where, nullptr, 0, Hq, Hkv, nullptr, nullptr, nullptr);
+  if (st != RX_OK) return st;
+  if (D != 64 && D != 128 && D != 256) return fail(RX_ERR_UNSUPPORTED, "%s: head dim %d not in {64, 128, 256}", where, D);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = rx::device_sm_count(dev, &sms);
+  if (e != cudaSuccess) return cuda_fail(e, where);
+  *bytes = static_cast<long long>(rx::attend_pages_workspace(N, Hq, Hkv, D, sms));
+  return RX_OK;
+  RX_GUARD_END
+}
+
+rx_status rx_attend_pages(rx_cache_t h, int layer, const void* q, int N, int Hq, int Hkv, int D, const rx_pages* pages,
+                          const int* q_start, const int* len, const int* prefix, void* out, float* lse, void* workspace,
+                          long long workspace_bytes, void* stream) {
+  RX_GUARD_BEGIN
+  const char* where = "rx_attend_pages";
+  if (h) {
+    if (layer < 0 || layer >= h->cfg.L) return fail(RX_ERR_LAYER, "%s: layer %d not in [0, %d)", where, layer, h->cfg.L);
+    if (Hq != h->cfg.Hq || Hkv != h->cfg.Hkv || D != h->cfg.D)
+      return fail(RX_ERR_ARG, "%s: heads %d/%d of %d, the cache has %d/%d of %d", where, Hq, Hkv, D, h->cfg.Hq, h->cfg.Hkv, h->cfg.D);
+  }
+  rx::PagePool pool{};
+  Span g[4];
+  rx_status st = check_pages(where, pages, Hkv, D, &pool, g);
+  if (st == RX_OK) st = check_queries(where, q, N, Hq, Hkv, q_start, len, prefix);
+  if (st != RX_OK) return st;
+  if (N == 0 || pool.B == 0) return RX_OK;
+  if (!out || !workspace) return fail(RX_ERR_ARG, "%s: null pointer", where);
+  if (!aligned16(out) || !aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return fail(RX_ERR_ARG, "%s: misaligned pointer", where);
+  const long long qb = static_cast<long long>(N) * Hq * D * 2, lens = pool.B * 4LL;
+  const Span in[7] = {{q, qb}, g[0], g[1], g[3], {q_start, lens + 4}, {len, lens}, {prefix, lens}};
+  const Span outs[3] = {{out, qb}, {lse, static_cast<long long>(N) * Hq * 4}, {workspace, workspace_bytes}};
+  st = check_apart(where, outs, 3, in, 7);
+  if (st != RX_OK) return st;
+  int dev = -1, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = rx::device_sm_count(dev, &sms);
+  if (e != cudaSuccess) return cuda_fail(e, where);
+  if (h && dev != h->device)
+    return fail(RX_ERR_STATE, "%s: the cache is on device %d, the current device is %d", where, h->device, dev);
+  const long long need = static_cast<long long>(rx::attend_pages_workspace(N, Hq, Hkv, D, sms));
+  if (workspace_bytes < need)
+    return fail(RX_ERR_CAPACITY, "%s: the workspace has %lld bytes, the call needs %lld", where, workspace_bytes, need);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  rx::AttnLaunch al{};
+  if (h) {
+    al = make_launch(h, layer);
+    if (h->fork.held) {   // a push may publish meanwhile: one state for all CTAs
+      e = rx::launch_hold_ring_state(h->dstate, h->fork.held, s);
+      if (e != cudaSuccess) return cuda_fail(e, "rx_attend_pages: launch");
+      al.st = h->fork.held;
+    }
+  }
+  const rx::PageAttention a{q, out, lse, q_start, len, prefix, N, Hq, Hkv, D};
+  e = rx::launch_attend_pages(a, pool, h ? &al : nullptr, workspace, s);
+  if (e != cudaSuccess) return cuda_fail(e, "rx_attend_pages: launch");
+  return RX_OK;
+  RX_GUARD_END
+}
+
+rx_status rx_weigh_pages(const void* q, const float* lse, int N, int Hq, int Hkv, int D, const rx_pages* pages,
+                         const int* q_start, const int* len, const int* prefix, float decay, float* out, void* stream) {
+  RX_GUARD_BEGIN
+  const char* where = "rx_weigh_pages";
+  rx::PagePool pool{};
+  Span g[4];
+  rx_status st = check_pages(where, pages, Hkv, D, &pool, g);
+  if (st == RX_OK) st = check_queries(where, q, N, Hq, Hkv, q_start, len, prefix);
+  if (st != RX_OK) return st;
+  if (!(decay >= 0.f) || decay > 3.0e38f) return fail(RX_ERR_ARG, "%s: decay must be finite and >= 0", where);
+  if (N == 0 || pool.B == 0) return RX_OK;
+  if (!out) out = pool.weight;
+  if (!out || !lse || (decay != 0.f && !pool.weight)) return fail(RX_ERR_ARG, "%s: null pointer", where);
+  if (!aligned4(out) || !aligned4(lse)) return fail(RX_ERR_ARG, "%s: misaligned pointer", where);
+  const long long lens = pool.B * 4LL;
+  const long long wb = static_cast<long long>(pool.n_pages) * pages->page * Hkv * 4;
+  const Span in[8] = {{q, static_cast<long long>(N) * Hq * D * 2}, {lse, static_cast<long long>(N) * Hq * 4}, g[0], g[3],
+                      {q_start, lens + 4}, {len, lens}, {prefix, lens}, out == pool.weight ? Span{nullptr, 0} : g[2]};
+  const Span outs[1] = {{out, wb}};
+  st = check_apart(where, outs, 1, in, 8);
+  if (st != RX_OK) return st;
+  if (spans_overlap(out, wb, g[1].p, g[1].bytes)) return fail(RX_ERR_ARG, "%s: out overlaps the values", where);
+  const rx::PageWeights a{q, lse, q_start, len, prefix, out, decay, N, Hq, Hkv, D};
+  const cudaError_t e = rx::launch_weigh_pages(a, pool, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rx_weigh_pages: launch");
+  return RX_OK;
+  RX_GUARD_END
+}
+
+rx_status rx_evict_pages(const rx_pages* pages, int Hkv, int D, const int* len, int sink, int recent, int budget,
+                         const int* to, int to_max_pages, int* new_len, int* kept, int* overflow, void* stream) {
+  RX_GUARD_BEGIN
+  const char* where = "rx_evict_pages";
+  rx::PagePool pool{};
+  Span g[4];
+  rx_status st = check_pages(where, pages, Hkv, D, &pool, g);
+  if (st != RX_OK) return st;
+  if (sink < 0 || recent < 0 || budget < 1 || budget > (1 << 30) || static_cast<long long>(sink) + recent > budget)
+    return fail(RX_ERR_ARG, "%s: sink = %d, recent = %d, budget = %d", where, sink, recent, budget);
+  if (to && to_max_pages < 1) return fail(RX_ERR_ARG, "%s: to_max_pages < 1", where);
+  if (pool.B == 0) return RX_OK;
+  if (!pool.weight || !len || !kept) return fail(RX_ERR_ARG, "%s: null pointer", where);
+  if (!aligned4(len) || !aligned4(to) || !aligned4(new_len) || !aligned4(kept) || !aligned4(overflow))
+    return fail(RX_ERR_ARG, "%s: misaligned pointer", where);
+  const long long lens = pool.B * 4LL;
+  const Span in[3] = {g[3], {to, lens * to_max_pages}, {len, lens}};
+  const Span outs[6] = {g[0], g[1], g[2], {kept, lens * Hkv * budget}, {overflow, 4}, {new_len == len ? nullptr : new_len, lens}};
+  st = check_apart(where, outs, 6, in, 3);
+  if (st != RX_OK) return st;
+  const cudaError_t e = rx::launch_evict_pages(pool, Hkv, D, len, sink, recent, budget, to, to_max_pages, new_len, kept,
+                                               overflow, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rx_evict_pages: launch");
+  return RX_OK;
+  RX_GUARD_END
+}
+
+rx_status rx_debug_page_plan(int n, int len, int prefix, int shared, int G, int r, long long* before, int* row_tile) {
+  RX_GUARD_BEGIN
+  const int most = 1 << 30;
+  if (!before || !row_tile || n < 1 || n > most || len < 0 || len > most || prefix < 0 || shared < 0 || shared > most ||
+      !pow2(G) || G > rx::kBM)
+    return fail(RX_ERR_ARG, "rx_debug_page_plan: argument out of range");
+  rx::StreamPlan s;
+  s.n = n;
+  s.len = len;
+  s.floor = prefix < len ? prefix : len;
+  if (s.floor < 1) s.floor = 1;
+  s.shared = shared;
+  s.log_a = 7 - log2_of(G);
+  if (r < 0 || r > s.row_tiles()) return fail(RX_ERR_ARG, "rx_debug_page_plan: r = %d not in [0, %d]", r, s.row_tiles());
+  *before = s.tiles_before(r);
+  *row_tile = r < s.row_tiles() ? s.row_tile_of(*before) : -1;
   return RX_OK;
   RX_GUARD_END
 }

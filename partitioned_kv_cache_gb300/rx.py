@@ -9,7 +9,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
-from typing import List, Optional, Sequence, Tuple
+from typing import List, NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
@@ -34,7 +34,9 @@ EXPORTS = ("rx_cache_create", "rx_cache_destroy", "rx_pin_prefix", "rx_push_fram
            "rx_snapshot_bytes", "rx_snapshot", "rx_restore", "rx_push_frame_async",
            "rx_set_attn_dparts", "rx_debug_inject_timeout", "rx_debug_choose_partition",
            "rx_attend_suffix_norms", "rx_attend_batch_norms", "rx_tail_append_quant",
-           "rx_attend_streams_quant", "rx_verify_drafts", "rx_debug_choose_stream_partition")
+           "rx_attend_streams_quant", "rx_verify_drafts", "rx_debug_choose_stream_partition",
+           "rx_rotate_heads", "rx_rotate_heads_paged", "rx_attend_pages", "rx_attend_pages_workspace",
+           "rx_weigh_pages", "rx_evict_pages", "rx_debug_page_plan")
 
 
 class RxConfig(ctypes.Structure):
@@ -58,6 +60,20 @@ class RxQuantStreams(ctypes.Structure):
 class RxNormRows(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("gamma", ctypes.c_void_p), ("y", ctypes.c_void_p),
                 ("rows", ctypes.c_int), ("d", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
+MAX_AXES = 4
+
+
+class RxPages(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "weight", "table")] + \
+               [(n, ctypes.c_int) for n in ("n_pages", "page", "max_pages", "B")]
+
+
+class RxHeads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("freq", "q_weight", "k_weight")] + \
+               [(n, ctypes.c_int) for n in ("Hq", "Hkv", "D", "n_axes")] + \
+               [("sections", ctypes.c_int * MAX_AXES), ("adjacent", ctypes.c_int), ("eps", ctypes.c_float)]
 
 
 MAX_NORM_JOBS = 2
@@ -100,6 +116,15 @@ _sigs = {
     "rx_attend_streams_quant": (_i, [_vp, _i, ctypes.POINTER(RxQuantStreams), _vp]),
     "rx_debug_choose_stream_partition": (_i, [_i, _i, ctypes.c_longlong, _i, _i, ctypes.POINTER(_i),
                                               ctypes.POINTER(_i)]),
+    "rx_rotate_heads": (_i, [_vp, ctypes.c_longlong, _i, ctypes.POINTER(RxHeads), _vp, _vp, _vp, _vp, _vp]),
+    "rx_rotate_heads_paged": (_i, [_vp, ctypes.c_longlong, _i, ctypes.POINTER(RxHeads), _vp, _vp,
+                                   ctypes.POINTER(RxPages), _vp, _vp, _vp, _vp, _vp]),
+    "rx_attend_pages": (_i, [_vp, _i, _vp, _i, _i, _i, _i, ctypes.POINTER(RxPages), _vp, _vp, _vp, _vp, _vp, _vp,
+                             ctypes.c_longlong, _vp]),
+    "rx_attend_pages_workspace": (_i, [_i, _i, _i, _i, ctypes.POINTER(ctypes.c_longlong)]),
+    "rx_weigh_pages": (_i, [_vp, _vp, _i, _i, _i, _i, ctypes.POINTER(RxPages), _vp, _vp, _vp, _f, _vp, _vp]),
+    "rx_evict_pages": (_i, [ctypes.POINTER(RxPages), _i, _i, _vp, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _vp]),
+    "rx_debug_page_plan": (_i, [_i] * 6 + [ctypes.POINTER(ctypes.c_longlong), ctypes.POINTER(_i)]),
     "rx_verify_drafts": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]),
 }
 for _name, (_res, _args) in _sigs.items():
@@ -231,6 +256,15 @@ def choose_stream_partition(t_max: int, units: int, tail_tiles: int, num_sms: in
     _check(_lib.rx_debug_choose_stream_partition(t_max, units, tail_tiles, num_sms, max_splits, ctypes.byref(sp),
                                                  ctypes.byref(ts)), "rx_debug_choose_stream_partition")
     return sp.value, ts.value
+
+
+def page_plan(n: int, length: int, prefix: int, shared: int, G: int, r: int):
+    """Test aid: (key tiles before row tile r, that tile's row tile) of a stream in
+    attend_pages (rx_debug_page_plan)."""
+    before, row_tile = ctypes.c_longlong(0), _i(0)
+    _check(_lib.rx_debug_page_plan(n, length, prefix, shared, G, r, ctypes.byref(before), ctypes.byref(row_tile)),
+           "rx_debug_page_plan")
+    return before.value, row_tile.value
 
 
 def library_path() -> str:
@@ -442,6 +476,13 @@ class Cache:
         _check(_lib.rx_attend_streams_quant(self._h, layer, ctypes.byref(batch), st), "rx_attend_streams_quant")
         return out
 
+    def attend_pages(self, layer: int, q: torch.Tensor, pages: "Pages", q_start: torch.Tensor, length: torch.Tensor,
+                     prefix: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, lse=None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+        """New tokens of language streams over the shared store of `layer` and
+        their own pages (see attend_pages)."""
+        return _attend_pages(self, layer, q, pages, q_start, length, prefix, out, lse, workspace, stream)
+
     def get_state(self, stream=None) -> Tuple[int, int, int]:
         h, v, p = _i(0), _i(0), ctypes.c_longlong(0)
         _check(_lib.rx_get_state(self._h, ctypes.byref(h), ctypes.byref(v), ctypes.byref(p),
@@ -636,3 +677,221 @@ def verify_drafts(p: torch.Tensor, q: Optional[torch.Tensor], draft: torch.Tenso
     args = (pp, qp, _PROB_TYPES[p.dtype], dp, up, rp, np_, B, T, V, tl, tokens.data_ptr(), n_accept.data_ptr(), nl, st)
     _check(_lib.rx_verify_drafts(*args), "rx_verify_drafts")
     return tokens, n_accept, new_len
+
+
+class Pages(NamedTuple):
+    """One layer's pages of language streams: k, v bf16 [n_pages][page][Hkv][D]
+    with pages of 16, 32, 64, 128 or 256 tokens; table int32 [B][max_pages],
+    place j of stream b being row j % page of page table[b][j // page]; weight
+    fp32 [n_pages][page][Hkv] or None, the attention weight that keys have
+    gathered (weigh_pages, evict_pages)."""
+    k: torch.Tensor
+    v: torch.Tensor
+    table: torch.Tensor
+    weight: Optional[torch.Tensor] = None
+
+
+def _pages(dev: int, g: Pages, more=()):
+    """The C form of pages and the addresses of further tensors (_addresses)."""
+    if g.k.dim() != 4 or g.table.dim() != 2:
+        raise ValueError("pages must have shape [n_pages][page][Hkv][D] and their table [B][max_pages]")
+    pool, table = g.k.shape, g.table.shape
+    bf16, i32 = torch.bfloat16, torch.int32
+    ptrs = _addresses(dev, (g.k, bf16, pool, "pages.k"), (g.v, bf16, pool, "pages.v"),
+                      (g.weight, torch.float32, pool[:3], "pages.weight"), (g.table, i32, table, "pages.table"), *more)
+    return RxPages(*ptrs[:4], pool[0], pool[1], table[1], table[0]), ptrs[4:]
+
+
+class Heads:
+    """What a layer's heads become (rx_heads): Hq query and Hkv key heads of D
+    values, normed where their weight (fp32 [D]) is given, then rotated: freq
+    fp32 [R/2] holds the pairs' angles per position, the first sections[0] of
+    them turn with axis 0 of the positions, the next sections[1] with axis 1 and
+    so on.  Pair i is elements (i, i + R/2), or (2i, 2i + 1) with adjacent."""
+
+    def __init__(self, Hq: int, Hkv: int, D: int, freq: torch.Tensor, sections: Sequence[int] = (),
+                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 adjacent: bool = False):
+        sections = tuple(int(n) for n in sections) or (freq.shape[0],)
+        if len(sections) > MAX_AXES:
+            raise ValueError("at most %d axes" % MAX_AXES)
+        if sum(sections) != freq.shape[0]:
+            raise ValueError("the sections %s hold %d pairs, freq %d" % (sections, sum(sections), freq.shape[0]))
+        self.Hq, self.Hkv, self.D, self.axes, self.eps = Hq, Hkv, D, len(sections), float(eps)
+        self.freq, self.q_weight, self.k_weight = freq, q_weight, k_weight
+        self._sections, self._adjacent = (_i * MAX_AXES)(*sections), int(bool(adjacent))
+
+    def _specs(self):
+        f32 = torch.float32
+        return ((self.freq, f32, self.freq.shape, "freq"), (self.q_weight, f32, (self.D,), "q_weight"),
+                (self.k_weight, f32, (self.D,), "k_weight"))
+
+    def _c(self, ptrs) -> RxHeads:
+        return RxHeads(*ptrs, self.Hq, self.Hkv, self.D, self.axes, self._sections, self._adjacent, self.eps)
+
+
+def _heads_input(x: torch.Tensor, heads: Heads, pos: torch.Tensor, dev: int):
+    """(tokens, row stride) of a projection's rows, which may be apart, and the
+    positions as [axes][N]."""
+    width = (heads.Hq + 2 * heads.Hkv) * heads.D
+    if x.dim() != 2 or x.shape[1] != width:
+        raise ValueError("x must have shape [N][%d], got %s" % (width, tuple(x.shape)))
+    if x.dtype != torch.bfloat16:
+        raise TypeError("x must be %s, got %s" % (torch.bfloat16, x.dtype))
+    if x.stride(1) != 1:
+        raise ValueError("the values of a row of x must be contiguous")
+    if x.get_device() != dev:
+        raise ValueError("x must be on the current device (cuda:%d), got %s" % (dev, x.device))
+    N = x.shape[0]
+    return N, x.stride(0) if N > 1 else width, pos if pos.dim() == 2 else pos.view(1, -1)
+
+
+def rotate_heads(x: torch.Tensor, heads: Heads, pos: torch.Tensor, q: Optional[torch.Tensor] = None,
+                 k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None, stream=None):
+    """Norm and rotate the heads of N tokens: x bf16 [N][(Hq + 2*Hkv)*D]
+    (queries, keys, values; rows may be apart), pos int32 [axes][N] (or [N]).
+    Returns q [N][Hq][D], k and v [N][Hkv][D]."""
+    dev, st = _here(stream)
+    N, stride, pos = _heads_input(x, heads, pos, dev)
+    qs, ks, bf16 = (N, heads.Hq, heads.D), (N, heads.Hkv, heads.D), torch.bfloat16
+    if q is None or k is None or v is None:
+        with _outputs(stream):
+            q = torch.empty(qs, dtype=bf16, device=x.device) if q is None else q
+            k = torch.empty(ks, dtype=bf16, device=x.device) if k is None else k
+            v = torch.empty(ks, dtype=bf16, device=x.device) if v is None else v
+    pp, qp, kp, vp, *h = _addresses(dev, (pos, torch.int32, (heads.axes, N), "pos"), (q, bf16, qs, "q"), (k, bf16, ks, "k"),
+                                    (v, bf16, ks, "v"), *heads._specs())
+    _check(_lib.rx_rotate_heads(x.data_ptr(), stride, N, ctypes.byref(heads._c(h)), pp, qp, kp, vp, st), "rx_rotate_heads")
+    return q, k, v
+
+
+def rotate_heads_paged(x: torch.Tensor, heads: Heads, pos: torch.Tensor, pages: Pages, q_start: torch.Tensor,
+                       held: torch.Tensor, q: Optional[torch.Tensor] = None, new_len: Optional[torch.Tensor] = None,
+                       overflow: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """rotate_heads with the keys and values stored in pages: the new tokens of
+    stream b, [q_start[b], q_start[b+1]) of x, at places from held[b] on, their
+    gathered weight set to 0.  held stays as it is; new_len, if given, receives
+    the lengths after the step.  Returns q (rows of tokens in no stream are left
+    as they were; of a new one: undefined)."""
+    dev, st = _here(stream)
+    N, stride, pos = _heads_input(x, heads, pos, dev)
+    B = pages.table.shape[0]
+    qs, i32 = (N, heads.Hq, heads.D), torch.int32
+    if overflow is not None and overflow.numel() < 1:
+        raise ValueError("overflow must hold one int32")
+    if pages.k.dim() == 4 and tuple(pages.k.shape[2:]) != (heads.Hkv, heads.D):
+        raise ValueError("pages have heads %s, expected %s" % (tuple(pages.k.shape[2:]), (heads.Hkv, heads.D)))
+    if q is None:
+        with _outputs(stream):
+            q = torch.empty(qs, dtype=torch.bfloat16, device=x.device)
+    g, (pp, qp, sp, hp, np_, op, *h) = _pages(dev, pages, (
+        (pos, i32, (heads.axes, N), "pos"), (q, torch.bfloat16, qs, "q"), (q_start, i32, (B + 1,), "q_start"),
+        (held, i32, (B,), "held"), (new_len, i32, (B,), "new_len"),
+        (overflow, i32, None if overflow is None else overflow.shape, "overflow"), *heads._specs()))
+    _check(_lib.rx_rotate_heads_paged(x.data_ptr(), stride, N, ctypes.byref(heads._c(h)), pp, qp, ctypes.byref(g), sp, hp,
+                                      np_, op, st), "rx_rotate_heads_paged")
+    return q
+
+
+def attend_pages_workspace(N: int, Hq: int, Hkv: int, D: int) -> int:
+    """Bytes of workspace that attend_pages needs for N new tokens."""
+    n = ctypes.c_longlong(0)
+    _check(_lib.rx_attend_pages_workspace(N, Hq, Hkv, D, ctypes.byref(n)), "rx_attend_pages_workspace")
+    return n.value
+
+
+def _attend_pages(cache, layer, q, pages, q_start, length, prefix, out, lse, workspace, stream):
+    if q.dim() != 3 or pages.k.dim() != 4:
+        raise ValueError("q must have shape [N][Hq][D] and pages [n_pages][page][Hkv][D]")
+    N, Hq, D = q.shape
+    B, Hkv = pages.table.shape[0], pages.k.shape[2]
+    bf16, f32, i32, u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+    if pages.k.shape[3] != D or Hkv < 1 or Hq % Hkv:
+        raise ValueError("q has heads %s, the pages %s" % ((Hq, D), tuple(pages.k.shape[2:])))
+    dev, st = _here(stream)
+    wants_lse = lse is not None and lse is not False
+    with _outputs(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        lse = torch.empty((N, Hq), dtype=f32, device=q.device) if lse is True else lse if wants_lse else None
+        if workspace is None and dev >= 0:
+            workspace = torch.empty(attend_pages_workspace(N, Hq, Hkv, D), dtype=u8, device=q.device)
+    rows, each = (N, Hq, D), (B,)
+    g, (qp, sp, lp, pp, op, ep, wp) = _pages(dev, pages, (
+        (q, bf16, rows, "q"), (q_start, i32, (B + 1,), "q_start"), (length, i32, each, "length"),
+        (prefix, i32, each, "prefix"), (out, bf16, rows, "out"), (lse, f32, (N, Hq), "lse"),
+        (workspace, u8, None if workspace is None else workspace.shape, "workspace")))
+    _check(_lib.rx_attend_pages(None if cache is None else cache._h, layer, qp, N, Hq, Hkv, D, ctypes.byref(g), sp, lp, pp,
+                                op, ep, wp, 0 if workspace is None else workspace.numel(), st), "rx_attend_pages")
+    return (out, lse) if wants_lse else out
+
+
+def attend_pages(q: torch.Tensor, pages: Pages, q_start: torch.Tensor, length: torch.Tensor,
+                 prefix: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, lse=None,
+                 workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of a step's new tokens over their streams' pages (with a shared
+    store: Cache.attend_pages).  q bf16 [N][Hq][D], packed: stream b's new tokens
+    are rows [q_start[b], q_start[b+1]) (int32 [B+1]) and the newest of its
+    length[b] keys (int32 [B]).  A token sees everything before it and itself,
+    and the first prefix[b] places (int32 [B] or None).  lse: True, or an fp32
+    [N][Hq] tensor, for the logarithm of the sum of the exponentials too: the
+    call then returns (out, lse).  Rows of tokens in no stream are left as they
+    were (of a new out: undefined).  workspace: uint8, attend_pages_workspace()
+    bytes, for this call alone while it runs; allocated if not given."""
+    return _attend_pages(None, 0, q, pages, q_start, length, prefix, out, lse, workspace, stream)
+
+
+def weigh_pages(q: torch.Tensor, lse: torch.Tensor, pages: Pages, q_start: torch.Tensor, length: torch.Tensor,
+                prefix: Optional[torch.Tensor] = None, decay: float = 1.0, out: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """Add the attention weight of a step's new tokens to the keys that they saw:
+    out = decay * pages.weight + the sum of exp(score - lse), for every key of a
+    stream with new tokens (rx_weigh_pages).  Arguments as of attend_pages, lse
+    its second result.  out: fp32 like pages.weight (None: in place)."""
+    if q.dim() != 3 or pages.k.dim() != 4:
+        raise ValueError("q must have shape [N][Hq][D] and pages [n_pages][page][Hkv][D]")
+    N, Hq, D = q.shape
+    B, Hkv = pages.table.shape[0], pages.k.shape[2]
+    f32, i32, each = torch.float32, torch.int32, (B,)
+    if pages.k.shape[3] != D or Hkv < 1 or Hq % Hkv:
+        raise ValueError("q has heads %s, the pages %s" % ((Hq, D), tuple(pages.k.shape[2:])))
+    if out is None:
+        out = pages.weight
+    if out is None:
+        raise ValueError("the pages have no weight")
+    dev, st = _here(stream)
+    g, (qp, ep, sp, lp, pp, op) = _pages(dev, pages, (
+        (q, torch.bfloat16, (N, Hq, D), "q"), (lse, f32, (N, Hq), "lse"), (q_start, i32, (B + 1,), "q_start"),
+        (length, i32, each, "length"), (prefix, i32, each, "prefix"), (out, f32, pages.k.shape[:3], "out")))
+    _check(_lib.rx_weigh_pages(qp, ep, N, Hq, Hkv, D, ctypes.byref(g), sp, lp, pp, float(decay), op, st), "rx_weigh_pages")
+    return out
+
+
+def evict_pages(pages: Pages, length: torch.Tensor, budget: int, sink: int = 0, recent: int = 0,
+                to: Optional[torch.Tensor] = None, new_len: Optional[torch.Tensor] = None,
+                kept: Optional[torch.Tensor] = None, overflow: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Cut streams of more than `budget` keys back to it: every K/V head keeps its
+    first `sink` keys, its last `recent` and the heaviest between them by
+    pages.weight, closed up in their order, in place or in the pages of the table
+    `to` int32 [B][...] (rx_evict_pages).  length int32 [B]; new_len, if given,
+    receives the lengths afterwards and may be length itself.  Returns kept int32
+    [B][Hkv][budget]: the old place of every new one, -1 behind the last."""
+    if pages.k.dim() != 4 or pages.table.dim() != 2:
+        raise ValueError("pages must have shape [n_pages][page][Hkv][D] and their table [B][max_pages]")
+    if pages.weight is None:
+        raise ValueError("the pages have no weight")
+    if to is not None and (to.dim() != 2 or to.shape[0] != pages.table.shape[0]):
+        raise ValueError("to must have shape [B][pages], got %s" % (tuple(to.shape),))
+    if overflow is not None and overflow.numel() < 1:
+        raise ValueError("overflow must hold one int32")
+    B, (Hkv, D), i32 = pages.table.shape[0], pages.k.shape[2:], torch.int32
+    dev, st = _here(stream)
+    if kept is None:
+        with _outputs(stream):
+            kept = torch.empty((B, Hkv, max(0, budget)), dtype=i32, device=pages.k.device)
+    g, (lp, tp, np_, kp, op) = _pages(dev, pages, (
+        (length, i32, (B,), "length"), (to, i32, None if to is None else to.shape, "to"), (new_len, i32, (B,), "new_len"),
+        (kept, i32, (B, Hkv, budget), "kept"), (overflow, i32, None if overflow is None else overflow.shape, "overflow")))
+    _check(_lib.rx_evict_pages(ctypes.byref(g), Hkv, D, lp, sink, recent, budget, tp, 0 if to is None else to.shape[1], np_,
+                               kp, op, st), "rx_evict_pages")
+    return kept
