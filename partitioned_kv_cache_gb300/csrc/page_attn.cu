@@ -20,7 +20,7 @@
 //
 // Inside a CTA the steps are those of the suffix's attention: S = Q K^T and
 // O += P V on tcgen05 with accumulators in tensor memory, P (bf16) back to
-// tensor memory as the A operand, one thread per row for the softmax, O
+// tensor memory as the A operand, O
 // rescaled only when a row's maximum grows by more than 2^8.  A weight enters
 // P V rounded to bf16 (2^-9 of it): beside the output's own rounding it is felt
 // as 0.0017 -> 0.002 in the relative error, and two terms would cost half of
@@ -34,8 +34,8 @@
 // outside or not finite; rows that see a key whose value is not finite become
 // NaN.
 //
-// Warps (224 threads): 0 = copies (lane 0 K, lane 1 V, lane 2 Q), 1 = tensor
-// memory and Q K^T, 2..5 = softmax and epilogue, 6 = P V.
+// Warps: 0 = copies of K, 1 = tensor memory, copies of Q and Q K^T, 2 = P V, 3 =
+// copies of V, 4..11 = softmax and epilogue.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -52,41 +52,44 @@
 namespace rx {
 namespace {
 
-constexpr int kThreads = 224;
 constexpr float kRescale = 8.0f;   // log2 units
 constexpr int kMinRun = 4;         // key tiles of a CTA, at least
 constexpr int kMergeThreads = 256;
 constexpr int kMergeFew = 8;       // parts that one thread of the merge takes
 
+constexpr int kThreads = 384;
+constexpr int kSoftmax = 256;      // of them two per query row
+
 template <int D>
 struct Layout {
   static constexpr int KB = D / 64;
-  static constexpr int CTAS = D == 256 ? 1 : 2;             // per SM
   static constexpr int Q_BLOCK = kBM * 128;
   static constexpr int Q_BYTES = KB * Q_BLOCK;
   static constexpr int TILE = static_cast<int>(tile_bytes(D));
-  static constexpr int NK = D == 256 ? 3 : D == 128 ? 2 : 5;
-  static constexpr int NV = D == 256 ? 2 : D == 128 ? 2 : 5;
+  static constexpr int NK = D == 256 ? 3 : D == 128 ? 6 : 10;
+  static constexpr int NV = D == 256 ? 2 : D == 128 ? 6 : 10;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = Q_BYTES;
   static constexpr int OFF_V = OFF_K + NK * TILE;
   static constexpr int OFF_BAR = OFF_V + NV * TILE;
-  static constexpr int OFF_MISC = OFF_BAR + 40 * 8;
-  static constexpr int BYTES = OFF_MISC + 128;
+  static constexpr int OFF_MISC = OFF_BAR + 64 * 8;
+  static constexpr int OFF_SUM = OFF_MISC + 128;            // floats [2 halves][128 rows]
+  static constexpr int BYTES = OFF_SUM + 2 * kBM * 4;
   static constexpr int ALLOC = BYTES + 1024;
-  // Tensor memory: O, two S buffers, and P: at D = 128 in the columns of the
-  // scores that it was made from (two CTAs share the 512), else beside them.
-  static constexpr bool P_IN_S = D == 128;
-  static constexpr int TMEM = D == 256 ? 512 : 256;
-  static_assert(D + 2 * kBN + (P_IN_S ? 0 : kBN) <= TMEM, "tensor memory");
-  static_assert(CTAS * (ALLOC + 1024) <= 233472, "shared memory");
+  // Tensor memory: O, Q (bf16 pairs), scores (one tile at D = 256, else two), P of
+  // two tiles (bf16 pairs).
+  static constexpr int NS = D == 256 ? 1 : 2;
+  static constexpr int T_Q = D, T_S = T_Q + D / 2, T_P = T_S + NS * kBN;
+  static_assert(T_P + kBN <= 512, "tensor memory");
+  static_assert(ALLOC <= 232448, "shared memory");
 };
 
-// Barriers: Q full / empty, K full / empty [5], V full / empty [5], S full [2],
-// P full [2], P V done [2], O read, values checked, drained.
+// Barriers: K full / empty [10], V full / empty [10], Q full / empty (shared
+// memory), Q in tensor memory, scores full / read [2], P full [2], P V done [2],
+// O read, values checked, row sums there, drained.
 enum : int {
-  B_QF = 0, B_QE = 1, B_KF = 2, B_KE = 7, B_VF = 12, B_VE = 17, B_SF = 22, B_PF = 24, B_PV = 26, B_OR = 28,
-  B_CHK = 29, B_DRAIN = 30
+  B_KF = 0, B_KE = 10, B_VF = 20, B_VE = 30, B_QF = 40, B_QE = 41, B_QT = 42, B_SF = 43, B_SR = 45, B_PF = 47, B_PV = 49,
+  B_OR = 51, B_CHK = 52, B_SUM = 53, B_DRAIN = 54, B_COUNT = 55
 };
 
 // The parts that merge_kernel joins: those of the unit that CTA c's run begins
@@ -138,12 +141,64 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
       : "memory");
 }
 
+// Pairs of fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+
+// The largest of 32 values, NaN left out where there is another.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max32(const float (&x)[32]) {
+  float a = x[0], b = x[1], c = x[2], d = x[3];
+#pragma unroll
+  for (int i = 4; i < 28; i += 8) {
+    a = max3(a, x[i], x[i + 1]);
+    b = max3(b, x[i + 2], x[i + 3]);
+    c = max3(c, x[i + 4], x[i + 5]);
+    d = max3(d, x[i + 6], x[i + 7]);
+  }
+  a = max3(a, x[28], x[29]);
+  b = max3(b, x[30], x[31]);
+  return fmaxf(max3(a, b, c), d);
+}
+
+// Scores of keys that the row does not see.
+__device__ __forceinline__ void hide(float (&x)[32], uint32_t seen) {
+#pragma unroll
+  for (int c = 0; c < 32; ++c)
+    if (!(seen >> c & 1)) x[c] = -INFINITY;
+}
+
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
       "l"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(one));
+  return one != 0;
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   const bool ok = mbar_wait(bar, parity, abort);
@@ -242,7 +297,7 @@ struct Walk {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, Layout<D>::CTAS) page_attn_kernel(const __grid_constant__ PageAttnParams p) {
+__global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_constant__ PageAttnParams p) {
   using Lay = Layout<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -254,20 +309,22 @@ __global__ void __launch_bounds__(kThreads, Layout<D>::CTAS) page_attn_kernel(co
   int* ring_word = reinterpret_cast<int*>(gbase + Lay::OFF_MISC + 8);
   RunStart* run_start = reinterpret_cast<RunStart*>(gbase + Lay::OFF_MISC + 16);      // 24 bytes
   int* run_len = reinterpret_cast<int*>(gbase + Lay::OFF_MISC + 40);
-  uint16_t* not_finite = reinterpret_cast<uint16_t*>(gbase + Lay::OFF_MISC + 64);     // [2][4]
+  uint8_t* not_finite = gbase + Lay::OFF_MISC + 64;                                    // [2][8]
+  float* row_sum = reinterpret_cast<float*>(gbase + Lay::OFF_SUM);
   auto BAR = [&](int i) { return sBar + 8u * static_cast<uint32_t>(i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 31; ++i) {
-      const bool all = (i >= B_PF && i < B_PF + 2) || i == B_OR || i == B_CHK;
-      mbar_init(BAR(i), all ? 128 : i == B_DRAIN ? 2 : 1);
+    for (int i = 0; i < B_COUNT; ++i) {
+      const bool all = i == B_QE || i == B_QT || (i >= B_SR && i < B_SR + 2) || (i >= B_PF && i < B_PF + 2) ||
+                       i == B_OR || i == B_CHK || i == B_SUM;
+      mbar_init(BAR(i), all ? kSoftmax : i == B_DRAIN ? 2 : 1);
     }
     *abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), Lay::TMEM);
+    tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
   if (warp == 0 && lane == 0) {
@@ -328,162 +385,206 @@ __global__ void __launch_bounds__(kThreads, Layout<D>::CTAS) page_attn_kernel(co
   const RunStart run = *run_start;
 
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tO = tmem, tS = tmem + D, tP = Lay::P_IN_S ? tS : tS + 2 * kBN;
-  constexpr int kPStride = Lay::P_IN_S ? kBN : kBN / 2;   // columns between the two P buffers
+  const uint32_t tO = tmem, tQ = tmem + Lay::T_Q, tS = tmem + Lay::T_S, tP = tmem + Lay::T_P;
   const int lp = p.pool.log_page;
   const int box = lp < 6 ? 1 << lp : kBN;                 // tokens of one page copy
 
   Walk w;
   const bool some = w.begin(p, shared, run);
-  if (some && warp == 0) {
-    // ------------------------------------------------------------ copies
-    if (lane < 2) {
-      const bool isv = lane == 1;
-      const CUtensorMap* tm = isv ? &p.tm_v : &p.tm_k;
-      const int slots = isv ? Lay::NV : Lay::NK;
-      const int bf = isv ? B_VF : B_KF, be = isv ? B_VE : B_KE;
-      const uint32_t ring = isv ? sV : sK;
-      int slot = 0, round = 0, issued = 0;
-      bool more = true, stop = false;
-      do {
-        const int* table = p.pool.table + static_cast<long long>(w.b) * p.pool.max_pages;
-        for (int t = w.t0; t < w.t0 + w.count; ++t) {
-          int pg[4];
-          const int key0 = (t - shared) * kBN;
-          if (t >= shared) {   // the table's entries are asked for before the wait for a slot
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int place = key0 + i * box;
-              pg[i] = i * box < kBN && place < w.s.plan.len ? __ldg(table + (place >> lp)) : -1;
-            }
-          }
-          if (round > 0 && !mbar_wait(BAR(be + slot), (round - 1) & 1, abort_flag)) {
-            stop = true;
-            break;
-          }
-          const uint32_t dst = ring + slot * Lay::TILE, bar = BAR(bf + slot);
-          const uint32_t extra = issued == 0 && !isv && blockIdx.x == 0 ? static_cast<uint32_t>(p.inject_tx) : 0u;
-          if (t < shared) {
+  if (some && (warp == 0 || warp == 3)) {
+    // ------------------------------------------------------------ copies of K, of V
+    // All lanes of a warp go along: they hold the table's next 64 entries (asked
+    // for a round ahead), and each issues one of a tile's boxes.
+    const bool isv = warp == 3;
+    const CUtensorMap* tm = isv ? &p.tm_v : &p.tm_k;
+    const int slots = isv ? Lay::NV : Lay::NK;
+    const int bf = isv ? B_VF : B_KF, be = isv ? B_VE : B_KE;
+    const uint32_t ring = isv ? sV : sK;
+    const int log_e = lp < 6 ? 6 - lp : 0;                 // pages of a tile
+    const int i = lane & ((1 << log_e) - 1), kb = lane >> log_e;   // this lane's box
+    int slot = 0, round = 0, issued = 0;
+    bool more = true, stop = false;
+    do {
+      const int* table = p.pool.table + static_cast<long long>(w.b) * p.pool.max_pages;
+      const int len = w.s.plan.len;
+      auto entry = [&](int e) { return (static_cast<long long>(e) << lp) < len ? __ldg(table + e) : -1; };
+      const int t_end = w.t0 + w.count;
+      int e_base = max(0, (w.t0 - shared) * kBN) >> lp;
+      int now = entry(e_base + lane), then = entry(e_base + 32 + lane);
+      for (int t = w.t0; t < t_end; ++t) {
+        const int key0 = (t - shared) * kBN;
+        if (round > 0 && !warp_wait(BAR(be + slot), (round - 1) & 1, abort_flag)) {
+          stop = true;
+          break;
+        }
+        const uint32_t dst = ring + slot * Lay::TILE, bar = BAR(bf + slot);
+        const uint32_t extra = issued == 0 && !isv && blockIdx.x == 0 ? static_cast<uint32_t>(p.inject_tx) : 0u;
+        if (t < shared) {
+          if (lane == 0) {
             const int region = t < store.n_pin ? 0 : 1;
             int at = region ? t - store.n_pin : t;
             if (region && at >= store.hole0) at += store.hole_n;
             const uint8_t* tiles = isv ? p.v_tiles[region] : p.k_tiles[region];
             mbar_arrive_expect_tx(bar, Lay::TILE + extra);
             bulk_load(dst, tiles + w.h * p.head_stride[region] + static_cast<long long>(at) * Lay::TILE, Lay::TILE, bar);
-          } else {
-            uint32_t named = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              named += static_cast<unsigned int>(pg[i]) < static_cast<unsigned int>(p.pool.n_pages);
-            mbar_arrive_expect_tx(bar, named * box * (D * 2) + extra);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (static_cast<unsigned int>(pg[i]) >= static_cast<unsigned int>(p.pool.n_pages)) continue;
-              const int row = lp > 6 ? key0 & ((1 << lp) - 1) : 0;
-              for (int kb = 0; kb < Lay::KB; ++kb)
-                tma_load_4d(dst + kb * 8192 + i * box * 128, tm, kb * 64, w.h, row, pg[i], bar);
-            }
           }
-          ++issued;
-          if (++slot == slots) {
-            slot = 0;
-            ++round;
+        } else {
+          const int e0 = key0 >> lp;
+          if (e0 - e_base >= 32) {
+            e_base += 32;
+            now = then;
+            then = entry(e_base + 32 + lane);
           }
+          const int pg = __shfl_sync(0xffffffffu, now, e0 - e_base + i);
+          const bool named = static_cast<unsigned int>(pg) < static_cast<unsigned int>(p.pool.n_pages);
+          const uint32_t pages = __popc(__ballot_sync(0xffffffffu, named && kb == 0));
+          if (lane == 0) mbar_arrive_expect_tx(bar, pages * box * (D * 2) + extra);
+          __syncwarp();
+          if (named && kb < Lay::KB)
+            tma_load_4d(dst + kb * 8192 + i * box * 128, tm, kb * 64, w.h, lp > 6 ? key0 & ((1 << lp) - 1) : 0, pg, bar);
         }
-        more = !stop && w.next(p);
-      } while (more);
-      // Every copy issued lands before the CTA exits, after an abort too.
-      volatile int no_abort = 0;
-      for (int i = max(0, issued - slots); i < issued; ++i) mbar_wait(BAR(bf + i % slots), (i / slots) & 1, &no_abort);
-    } else if (lane == 2) {
-      int u = 0;
-      do {
-        if (u > 0 && !mbar_wait(BAR(B_QE), (u - 1) & 1, abort_flag)) break;
-        mbar_arrive_expect_tx(BAR(B_QF), Lay::Q_BYTES);
-        const int token = w.s.q0 + (w.rt << w.s.plan.log_a);
-        for (int kb = 0; kb < Lay::KB; ++kb) tma_load_4d(sQ + kb * Lay::Q_BLOCK, &p.tm_q, kb * 64, 0, w.h, token, BAR(B_QF));
-        ++u;
-      } while (w.next(p));
-      volatile int no_abort = 0;
-      if (u > 0) mbar_wait(BAR(B_QF), (u - 1) & 1, &no_abort);
-    }
+        ++issued;
+        if (++slot == slots) {
+          slot = 0;
+          ++round;
+        }
+      }
+      more = !stop && w.next(p);
+    } while (more);
+    // Every copy issued lands before the CTA exits, after an abort too.
+    volatile int no_abort = 0;
+    for (int n = max(0, issued - slots); n < issued; ++n) mbar_wait(BAR(bf + n % slots), (n / slots) & 1, &no_abort);
   } else if (some && warp == 1) {
     // ------------------------------------------------------------ Q K^T
-    if (lane == 0) {
-      constexpr uint32_t kIdesc = idesc_bf16_f32(kBM, kBN, false, false);
-      int j = 0, slot = 0, round = 0, u = 0;
-      bool ok = true;
-      do {
-        ok = mbar_wait(BAR(B_QF), u & 1, abort_flag);
-        for (int t = 0; ok && t < w.count; ++t, ++j) {
-          const int st = j & 1;
-          // The buffer held the scores of tile j - 2: read by the softmax once
-          // it has published P, or (P in its columns) once P V is done.
-          if (j >= 2 && !mbar_wait(BAR((Lay::P_IN_S ? B_PV : B_PF) + st), ((j - 2) >> 1) & 1, abort_flag)) { ok = false; break; }
-          if (!mbar_wait(BAR(B_KF + slot), round & 1, abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t kt = sK + slot * Lay::TILE;
+    // Q is the A operand from tensor memory.  All lanes run the loop, so that its
+    // values are the same for the whole warp, and one issues the products.
+    constexpr uint32_t kIdesc = idesc_bf16_f32(kBM, kBN, false, false);
+    const bool leader = elect_one();
+    int j = 0, slot = 0, round = 0, u = 0, asked = 0;
+    bool ok = true, more = true;
+    auto ask_q = [&](const Walk& x) {        // a unit's Q into shared memory
+      if (leader) {
+        mbar_arrive_expect_tx(BAR(B_QF), Lay::Q_BYTES);
+        for (int kb = 0; kb < Lay::KB; ++kb)
+          tma_load_4d(sQ + kb * Lay::Q_BLOCK, &p.tm_q, kb * 64, 0, x.h, x.s.q0 + (x.rt << x.s.plan.log_a), BAR(B_QF));
+      }
+      __syncwarp();
+      ++asked;
+    };
+    ask_q(w);
+    while (more) {
+      const int count = uniform(w.count);
+      Walk coming = w;
+      more = coming.next(p);
+      ok = warp_wait(BAR(B_QT), u & 1, abort_flag);
+      // This unit's is in tensor memory: the next one's can come.
+      if (ok && more) {
+        ok = warp_wait(BAR(B_QE), u & 1, abort_flag);
+        if (ok) ask_q(coming);
+      }
+      for (int t = 0; ok && t < count; ++t) {
+        const int st = Lay::NS == 1 ? 0 : j & 1;
+        // The softmax has read the scores of tile j - NS.
+        if (j >= Lay::NS && !warp_wait(BAR(B_SR + st), (j / Lay::NS - 1) & 1, abort_flag)) { ok = false; break; }
+        if (!warp_wait(BAR(B_KF + slot), round & 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t desc = sdesc_sw128(sK + slot * Lay::TILE, 16, 1024);
+        if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t kb = kk >> 2, ko = (kk & 3) * 32;
-            umma_bf16(tS + st * kBN, sdesc_sw128(sQ + kb * Lay::Q_BLOCK + ko, 16, 1024),
-                      sdesc_sw128(kt + kb * 8192 + ko, 16, 1024), kIdesc, kk > 0 ? 1u : 0u);
-          }
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16_ts(tS + st * kBN, tQ + kk * 8, desc + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), kIdesc, kk > 0 ? 1u : 0u);
           umma_commit(BAR(B_KE + slot));
-          if (t == w.count - 1) umma_commit(BAR(B_QE));
           umma_commit(BAR(B_SF + st));
-          if (++slot == Lay::NK) {
-            slot = 0;
-            ++round;
-          }
         }
-        ++u;
-      } while (ok && w.next(p));
-      umma_commit(BAR(B_DRAIN));
-      volatile int no_abort = 0;
-      mbar_wait(BAR(B_DRAIN), 0, &no_abort);
+        __syncwarp();
+        ++j;
+        if (++slot == Lay::NK) {
+          slot = 0;
+          ++round;
+        }
+      }
+      ++u;
+      w = coming;
+      more = more && ok;
     }
-  } else if (some && warp == 6) {
+    if (leader) umma_commit(BAR(B_DRAIN));
+    volatile int no_abort = 0;
+    mbar_wait(BAR(B_QF), (asked - 1) & 1, &no_abort);
+    mbar_wait(BAR(B_DRAIN), 0, &no_abort);
+  } else if (some && warp == 2) {
     // ------------------------------------------------------------ P V
-    if (lane == 0) {
-      constexpr uint32_t kIdesc = idesc_bf16_f32(kBM, D, false, true);
-      int j = 0, slot = 0, round = 0, u = 0;
-      bool ok = true;
-      do {
-        for (int t = 0; t < w.count; ++t, ++j) {
-          const int st = j & 1;
-          if (!mbar_wait(BAR(B_PF + st), (j >> 1) & 1, abort_flag)) { ok = false; break; }
-          if (!mbar_wait(BAR(B_VF + slot), round & 1, abort_flag)) { ok = false; break; }
-          // O still holds the last unit until the softmax warps have read it.
-          if (t == 0 && u > 0 && !mbar_wait(BAR(B_OR), (u - 1) & 1, abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t vt = sV + slot * Lay::TILE;
+    constexpr uint32_t kIdesc = idesc_bf16_f32(kBM, D, false, true);
+    const bool leader = elect_one();
+    int j = 0, slot = 0, round = 0, u = 0;
+    bool ok = true;
+    do {
+      const int count = uniform(w.count);
+      for (int t = 0; t < count; ++t) {
+        const int st = j & 1;
+        if (!warp_wait(BAR(B_PF + st), (j >> 1) & 1, abort_flag)) { ok = false; break; }
+        if (!warp_wait(BAR(B_VF + slot), round & 1, abort_flag)) { ok = false; break; }
+        // O still holds the last unit until the softmax warps have read it.
+        if (t == 0 && u > 0 && !warp_wait(BAR(B_OR), (u - 1) & 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t desc = sdesc_sw128(sV + slot * Lay::TILE, 8192, 1024);
+        const uint32_t more = t > 0 ? 1u : 0u;
+        if (leader) {
 #pragma unroll
           for (int kk = 0; kk < kBN / 16; ++kk)
-            umma_bf16_ts(tO, tP + st * kPStride + kk * 8, sdesc_sw128(vt + kk * 16 * 128, 8192, 1024), kIdesc,
-                         (t > 0 || kk > 0) ? 1u : 0u);
+            umma_bf16_ts(tO, tP + st * (kBN / 2) + kk * 8, desc + ((kk * 16 * 128) >> 4), kIdesc, kk > 0 ? 1u : more);
           umma_commit(BAR(B_VE + slot));
           umma_commit(BAR(B_PV + st));
-          if (++slot == Lay::NV) {
-            slot = 0;
-            ++round;
-          }
         }
-        ++u;
-      } while (ok && w.next(p));
-      umma_commit(BAR(B_DRAIN));
-      volatile int no_abort = 0;
-      mbar_wait(BAR(B_DRAIN), 0, &no_abort);
-    }
-  } else if (warp >= 2 && warp <= 5) {
+        __syncwarp();
+        ++j;
+        if (++slot == Lay::NV) {
+          slot = 0;
+          ++round;
+        }
+      }
+      ++u;
+    } while (ok && w.next(p));
+    if (leader) umma_commit(BAR(B_DRAIN));
+    volatile int no_abort = 0;
+    mbar_wait(BAR(B_DRAIN), 0, &no_abort);
+  } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax
-    const int quarter = warp & 3;
+    // A row has two threads, in warps w and w + 4 (a warp reaches the tensor memory
+    // lanes of its quarter): each looks at all scores of the row for the maximum, so
+    // that both arrive at the same reference without a word, takes the exponentials
+    // of its 32 columns and, later, its half of O's columns.
+    constexpr int kOCols = D / 2;
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
     const int row = quarter * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const bool first_thread = threadIdx.x == 64;
+    const bool first_thread = threadIdx.x == 128;
     if (first_thread) p.cut[blockIdx.x] = CutUnit{0, 0, 0, 0};
-    int j = 0, vslot = 0, vround = 0, checks = 0;
+    int j = 0, vslot = 0, vround = 0, checks = 0, u = 0;
     bool ok = true, more = some;
+    const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
+    // Unit n's Q from shared into tensor memory, this thread's half of its row.
+    // The scores of the last unit's tiles are all done: this thread waited for them.
+    auto load_q = [&](int n) {
+      if (!warp_wait(BAR(B_QF), n & 1, abort_flag)) return false;
+      constexpr int kChunks = D / 16;   // of 16 bytes
+#pragma unroll
+      for (int c0 = 0; c0 < kChunks; c0 += 4) {
+        uint32_t x[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = half * kChunks + c0 + i;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(x[4 * i]), "=r"(x[4 * i + 1]), "=r"(x[4 * i + 2]), "=r"(x[4 * i + 3])
+                       : "r"(sQ + (c >> 3) * Lay::Q_BLOCK + row * 128 + (((c & 7) ^ (row & 7)) << 4)));
+        }
+        tmem_st16(tQ + (half * kChunks + c0) * 4 + lane_off, x);
+      }
+      tc_fence_before();
+      mbar_arrive(BAR(B_QT));
+      mbar_arrive(BAR(B_QE));
+      return true;
+    };
+    if (more) ok = load_q(0);
     while (more) {
       const int t_row = (w.rt << w.s.plan.log_a) + (row >> p.log_g);
       const bool row_valid = t_row < w.s.plan.n;
@@ -499,58 +600,58 @@ __global__ void __launch_bounds__(kThreads, Layout<D>::CTAS) page_attn_kernel(co
         return t >= shared && place < w.s.plan.len ? __ldg(table + (place >> lp)) : 0;
       };
       int ent = entry(w.t0);
-      float m_used = -INFINITY, l = 0.f;
+      float m_used = -INFINITY;
+      float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       bool poison = false;
       for (int t = w.t0; ok && t < w.t0 + w.count; ++t, ++j) {
         const int st = j & 1;
-        // Keys of the tile that are there.
-        uint64_t there = ~0ull, mine;
+        // Keys of the tile that are there, and those that this row sees.
+        uint64_t there = ~0ull, mine = ~0ull;
         bool check;
         if (t < shared) {
           const int nv = store.valid(t);
-          if (nv < kBN) there = (1ull << nv) - 1;
           check = nv < kBN;
-          mine = there;
+          if (check) there = mine = (1ull << nv) - 1;
         } else {
           const int key0 = (t - shared) * kBN;
           const int nv = w.s.plan.len - key0;
           const uint32_t named = __ballot_sync(0xffffffffu, static_cast<unsigned int>(ent) < static_cast<unsigned int>(p.pool.n_pages));
-          if (named != 0xffffffffu) {
-            if (lp >= 6) {
+          check = named != 0xffffffffu || nv < kBN || key0 + kBN > all;
+          if (check) {
+            if (named != 0xffffffffu) {
               there = 0;
-            } else {
-              there = 0;
-              for (int i = 0; i < (kBN >> lp); ++i)
-                if (named >> i & 1) there |= ((1ull << (1 << lp)) - 1) << (i << lp);
+              if (lp < 6)
+                for (int i = 0; i < (kBN >> lp); ++i)
+                  if (named >> i & 1) there |= ((1ull << (1 << lp)) - 1) << (i << lp);
             }
+            if (nv < kBN) there = nv > 0 ? there & ((1ull << nv) - 1) : 0;
+            mine = there;
+            const int seen = lim - key0;
+            if (seen < kBN) mine = seen > 0 ? mine & ((1ull << seen) - 1) : 0;
           }
-          if (nv < kBN) there = nv > 0 ? there & ((1ull << nv) - 1) : 0;
-          check = there != ~0ull || key0 + kBN > all;
-          mine = there;
-          const int seen = lim - key0;
-          if (seen < kBN) mine = seen > 0 ? mine & ((1ull << seen) - 1) : 0;
         }
         ent = entry(t + 1);
-        if (!warp_wait(BAR(B_SF + st), (j >> 1) & 1, abort_flag)) { ok = false; break; }
+        const int sb = j % Lay::NS;
+        if (!warp_wait(BAR(B_SF + sb), (j / Lay::NS) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        float s[kBN];
-        tmem_ld32(tS + st * kBN + lane_off, s);
-        tmem_ld32(tS + st * kBN + 32 + lane_off, s + 32);
+        float s[32], r[32];   // this thread's columns, the rest of the row
+        tmem_ld32x2(tS + sb * kBN + half * 32 + lane_off, s, tS + sb * kBN + (half ^ 1) * 32 + lane_off, r);
+        tc_fence_before();
+        mbar_arrive(BAR(B_SR + sb));
         if (check) {
-          const uint32_t lo = static_cast<uint32_t>(mine), hi = static_cast<uint32_t>(mine >> 32);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            if (!(lo >> c & 1)) s[c] = -INFINITY;
-            if (!(hi >> c & 1)) s[32 + c] = -INFINITY;
-          }
-          // V's rows: two threads each.  P V of tile j - 2 first: until then
+          hide(s, static_cast<uint32_t>(mine >> (32 * half)));
+          hide(r, static_cast<uint32_t>(mine >> (32 - 32 * half)));
+        }
+        if (check) {
+          // V's rows: four threads each.  P V of tile j - 2 first: until then
           // V's barrier may be one phase behind, and its parity would pass.
           if (j >= 2 && !warp_wait(BAR(B_PV + st), ((j - 2) >> 1) & 1, abort_flag)) { ok = false; break; }
           if (!warp_wait(BAR(B_VF + vslot), vround & 1, abort_flag)) { ok = false; break; }
-          const int vr = row >> 1;
+          constexpr int kShare = kSoftmax / kBN;   // threads of a V row
+          const int vr = (threadIdx.x - 128) / kShare;
           const uint32_t at = sV + vslot * Lay::TILE + vr * 128;
-          constexpr int kChunks = D / 16;
-          const int c0 = (row & 1) * kChunks;
+          constexpr int kChunks = D / 8 / kShare;
+          const int c0 = (lane & (kShare - 1)) * kChunks;
           const bool outside = !(there >> vr & 1);
           uint32_t odd = 0;
           if (!outside) {
@@ -567,50 +668,42 @@ __global__ void __launch_bounds__(kThreads, Layout<D>::CTAS) page_attn_kernel(co
             }
           }
           odd |= __shfl_xor_sync(0xffffffffu, odd, 1);
+          odd |= __shfl_xor_sync(0xffffffffu, odd, 2);
           if (outside || odd) {
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) st_shared_v4(at + ((c0 + i) >> 3) * 8192 + (((c0 + i) & 7) << 4), 0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
-          uint32_t pairs = __ballot_sync(0xffffffffu, odd != 0) & 0x55555555u;   // even lanes -> 16 bits
-          pairs = (pairs | pairs >> 1) & 0x33333333u;
-          pairs = (pairs | pairs >> 2) & 0x0F0F0F0Fu;
-          pairs = (pairs | pairs >> 4) & 0x00FF00FFu;
-          pairs = (pairs | pairs >> 8) & 0x0000FFFFu;
-          volatile uint16_t* bits = not_finite + (checks & 1) * 4;
-          if (lane == 0) bits[quarter] = static_cast<uint16_t>(pairs);
+          uint32_t rows = __ballot_sync(0xffffffffu, odd != 0);
+          volatile uint8_t* bits = not_finite + (checks & 1) * 8;
+          rows &= 0x11111111u;   // every fourth lane -> 8 bits
+          rows = (rows | rows >> 3) & 0x03030303u;
+          rows = (rows | rows >> 6) & 0x000F000Fu;
+          rows = (rows | rows >> 12) & 0x000000FFu;
+          if (lane == 0) bits[warp - 4] = static_cast<uint8_t>(rows);
           mbar_arrive(BAR(B_CHK));
           if (!warp_wait(BAR(B_CHK), checks & 1, abort_flag)) { ok = false; break; }
           ++checks;
-          uint64_t bad = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) bad |= static_cast<uint64_t>(bits[i]) << (16 * i);
-          poison = poison || (bad & mine) != 0;
+          poison = poison || (*reinterpret_cast<volatile uint64_t*>(bits) & mine) != 0;
         }
         if (++vslot == Lay::NV) {
           vslot = 0;
           ++vround;
         }
-        float t32[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) t32[c] = fmaxf(s[c], s[c + 32]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-          for (int c = 0; c < o; ++c) t32[c] = fmaxf(t32[c], t32[c + o]);
-        const float m_new = fmaxf(m_used, t32[0] * p.scale_log2);
+        const float m_new = fmaxf(m_used, fmaxf(max32(s), max32(r)) * p.scale_log2);
         const bool need = m_new > m_used + kRescale;
         float fac = 1.f;
         if (need) {
           fac = exp2f(m_used - m_new);
-          l *= fac;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) l2[i] = make_float2(l2[i].x * fac, l2[i].y * fac);
           m_used = m_new;
         }
         if (__any_sync(0xffffffffu, need && t > w.t0)) {
           if (!warp_wait(BAR(B_PV + ((j - 1) & 1)), ((j - 1) >> 1) & 1, abort_flag)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
+          for (int c = half * kOCols; c < (half + 1) * kOCols; c += 32) {
             float o[32];
             tmem_ld32(tO + c + lane_off, o);
 #pragma unroll
@@ -619,86 +712,88 @@ __global__ void __launch_bounds__(kThreads, Layout<D>::CTAS) page_attn_kernel(co
           }
         }
         const float nmb = m_used == -INFINITY ? 0.f : -m_used;
-        uint32_t pk[kBN / 2];
-        float sums[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 nmb2 = make_float2(nmb, nmb);
+        uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < kBN / 2; ++c) {
-          const float a = exp2f(fmaf(s[2 * c], p.scale_log2, nmb));
-          const float b = exp2f(fmaf(s[2 * c + 1], p.scale_log2, nmb));
-          sums[c & 3] += a + b;
-          pk[c] = pack_bf16x2(a, b);
+        for (int c = 0; c < 16; ++c) {
+          float2 e = fma2(make_float2(s[2 * c], s[2 * c + 1]), scale2, nmb2);
+          e = make_float2(exp2f(e.x), exp2f(e.y));
+          l2[c & 1] = add2(l2[c & 1], e);
+          pk[c] = pack_bf16x2(e.x, e.y);
         }
-        l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
         if (j >= 2 && !warp_wait(BAR(B_PV + st), ((j - 2) >> 1) & 1, abort_flag)) { ok = false; break; }
-        tmem_st32(tP + st * kPStride + lane_off, reinterpret_cast<const float*>(pk));
+        tmem_st16(tP + st * (kBN / 2) + half * 16 + lane_off, pk);
         tc_fence_before();
         mbar_arrive(BAR(B_PF + st));
       }
+      // The next unit's Q, so that its scores are on their way during this one's end.
+      Walk coming = w;
+      more = coming.next(p);
+      if (more && ok) ok = load_q(u + 1);
       if (ok) ok = warp_wait(BAR(B_PV + ((j - 1) & 1)), ((j - 1) >> 1) & 1, abort_flag);
       tc_fence_after();
+      float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+      if (ok) {
+        // (The next unit's sums are written behind its last P V, which waits for
+        // every thread of this one to have come on.)
+        row_sum[half * kBM + row] = l;
+        mbar_arrive(BAR(B_SUM));
+        ok = warp_wait(BAR(B_SUM), u & 1, abort_flag);
+        l = row_sum[row] + row_sum[kBM + row];   // the same in both threads
+      }
       if (poison || !ok) l = NAN;
       // ---- the part's end
       const bool begins = w.t0 == 0, ends = w.t0 + w.count == w.tiles;
       const int first = (w.rt << w.s.plan.log_a);
       const int h = w.h * (1 << p.log_g) + (row & ((1 << p.log_g) - 1));
       const size_t at = static_cast<size_t>(w.s.q0 + t_row) * p.Hq + h;
-      if (begins && ends) {
-        const float inv = l > 0.f ? 1.f / l : l;   // l = 0: a row without keys gets zeros; NaN stays
+      const bool whole = begins && ends;
+      const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (begins ? 1 : 0);
+      float4* dst = p.part + slot * (D / 4) * p.part_rows + row;
+      const float inv = l > 0.f ? 1.f / l : l;   // l = 0: a row without keys gets zeros; NaN stays
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          if (ok) {
-            tmem_ld32(tO + c + lane_off, o);
-          } else {
+      for (int c = half * kOCols; c < (half + 1) * kOCols; c += 32) {
+        float o[32];
+        if (ok) {
+          tmem_ld32(tO + c + lane_off, o);
+        } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0.f;
-          }
-          if (row_valid) {
-            uint4* d4 = reinterpret_cast<uint4*>(p.out + at * D + c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              d4[i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                 pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-          }
+          for (int i = 0; i < 32; ++i) o[i] = 0.f;
         }
-        if (row_valid && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.693147180559945309f;
-      } else {
-        const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (begins ? 1 : 0);
-        float4* dst = p.part + slot * (D / 4) * p.part_rows + row;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          if (ok) {
-            tmem_ld32(tO + c + lane_off, o);
-          } else {
+        if (row_valid && whole) {
+          uint4* d4 = reinterpret_cast<uint4*>(p.out + at * D + c);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0.f;
-          }
-          if (row_valid) {
+          for (int i = 0; i < 4; ++i)
+            d4[i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                               pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+        } else if (row_valid) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[static_cast<size_t>(c / 4 + i) * p.part_rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          }
-        }
-        if (row_valid) p.part_ml[slot * p.part_rows + row] = make_float2(m_used, l);
-        if (first_thread && begins) {
-          const int rest = w.tiles - w.count, each = *run_len;
-          p.cut[blockIdx.x] = CutUnit{w.s.q0 + first, min(1 << w.s.plan.log_a, w.s.plan.n - first) << p.log_g, w.h,
-                                      1 + (rest + each - 1) / each};
+          for (int i = 0; i < 8; ++i)
+            dst[static_cast<size_t>(c / 4 + i) * p.part_rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       }
       if (ok) {
         tc_fence_before();
         mbar_arrive(BAR(B_OR));
       }
-      more = w.next(p);
+      if (half == 0 && row_valid) {
+        if (!whole) p.part_ml[slot * p.part_rows + row] = make_float2(m_used, l);
+        else if (p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.693147180559945309f;
+      }
+      if (!whole && begins && first_thread) {
+        const int rest = w.tiles - w.count, each = *run_len;
+        p.cut[blockIdx.x] = CutUnit{w.s.q0 + first, min(1 << w.s.plan.log_a, w.s.plan.n - first) << p.log_g, w.h,
+                                    1 + (rest + each - 1) / each};
+      }
+      ++u;
+      w = coming;
     }
   }
 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, Lay::TMEM);
+  if (warp == 1) tmem_dealloc(tmem, 512);
   if (threadIdx.x == 0 && *abort_flag && p.err) atomicOr(p.err, kErrStreamTimeout);
 }
 
@@ -845,9 +940,9 @@ struct Workspace {
   size_t part, ml, cut, bytes;   // offsets
 };
 
-Workspace workspace(int N, int G, int D, int num_sms) {
+Workspace workspace(int N, int G, int D, int num_sms) {   // one CTA per SM
   Workspace w;
-  w.ctas = num_sms * (D == 256 ? 1 : 2);
+  w.ctas = num_sms;
   const long long rows = static_cast<long long>(N) * G;
   w.part_rows = static_cast<int>(rows < kBM ? (rows + 7) / 8 * 8 : kBM);
   const size_t slots = 2 * static_cast<size_t>(w.ctas);
