@@ -614,14 +614,14 @@ rx_status rx_debug_choose_stream_partition(int t_max, int units, long long tail_
                                            int max_splits, int* splits, int* tail_sms);
 
 /* Test aid: how rx_attend_pages numbers its work, computed on the host.  A stream
- * with n new tokens, len keys and a prefix reads `shared` 64-key tiles of the store
- * for every row tile of 128/G tokens, G = Hq/Hkv.  *before: key tiles of row tiles
+ * with n new tokens, len keys and a prefix reads `shared` tiles of the store and tiles
+ * of `keys` = 64 or 128 keys of its pages for every row tile of 128/G tokens, G = Hq/Hkv.  *before: key tiles of row tiles
  * [0, r) of one head; *row_tile: the row tile that tile *before belongs to (r), -1
  * for r = the number of row tiles.  Touches no device.  Errors: RX_ERR_ARG (a null
  * pointer, n < 1, a negative size or one above 2^30, G no power of two up to 128,
- * r outside [0, row tiles]). */
-rx_status rx_debug_page_plan(int n, int len, int prefix, int shared, int G, int r, long long* before,
-                             int* row_tile);
+ * other keys, r outside [0, row tiles]). */
+rx_status rx_debug_page_plan(int n, int len, int prefix, int shared, int G, int keys, int r,
+                             long long* before, int* row_tile);
 
 /* Number of split-KV partitions for attention launches of this cache
  * (0 = chosen from the SM count, the default).  A tuning knob: results are

@@ -11,7 +11,7 @@
 // and lse = log of the sum of the exponentials of its scores.
 //
 // Work.  A unit is (stream, K/V head, 128 query rows), row r = token r / G, head
-// r % G of the group.  All units' 64-key tiles are numbered in a row
+// r % G of the group.  All units' key tiles are numbered in a row
 // (page_plan.h) and cut into equal runs, one per CTA; a CTA works its run off
 // unit by unit, its rings of K and V tiles never stopping in between.  A unit
 // that lies in one run is finished there; of a cut unit every CTA leaves its
@@ -53,7 +53,7 @@ namespace rx {
 namespace {
 
 constexpr float kRescale = 8.0f;   // log2 units
-constexpr int kMinRun = 4;         // key tiles of a CTA, at least
+constexpr int kMinRunKeys = 256;   // keys of a CTA's run, at least
 constexpr int kMergeThreads = 256;
 constexpr int kMergeFew = 8;       // parts that one thread of the merge takes
 
@@ -65,9 +65,13 @@ struct Layout {
   static constexpr int KB = D / 64;
   static constexpr int Q_BLOCK = kBM * 128;
   static constexpr int Q_BYTES = KB * Q_BLOCK;
-  static constexpr int TILE = static_cast<int>(tile_bytes(D));
-  static constexpr int NK = D == 256 ? 3 : D == 128 ? 6 : 10;
-  static constexpr int NV = D == 256 ? 2 : D == 128 ? 6 : 10;
+  // Keys of a tile.  A tile's waits, barriers and masks cost the softmax as much as
+  // 64 columns do: 128 keys are better where tensor memory has room for their scores.
+  static constexpr int BN = D == 256 ? 64 : 128;
+  static constexpr int BLOCK = BN * 128;                    // 64 columns of a K or V tile
+  static constexpr int TILE = KB * BLOCK;
+  static constexpr int NK = D == 64 ? 5 : 3;
+  static constexpr int NV = D == 64 ? 5 : D == 128 ? 3 : 2;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = Q_BYTES;
   static constexpr int OFF_V = OFF_K + NK * TILE;
@@ -76,11 +80,11 @@ struct Layout {
   static constexpr int OFF_SUM = OFF_MISC + 128;            // floats [2 halves][128 rows]
   static constexpr int BYTES = OFF_SUM + 2 * kBM * 4;
   static constexpr int ALLOC = BYTES + 1024;
-  // Tensor memory: O, Q (bf16 pairs), scores (one tile at D = 256, else two), P of
-  // two tiles (bf16 pairs).
-  static constexpr int NS = D == 256 ? 1 : 2;
-  static constexpr int T_Q = D, T_S = T_Q + D / 2, T_P = T_S + NS * kBN;
-  static_assert(T_P + kBN <= 512, "tensor memory");
+  // Tensor memory: O, Q (bf16 pairs), scores and P (bf16 pairs); of the last two
+  // one has room for two tiles: P at D = 256, else the scores.
+  static constexpr int NS = D == 256 ? 1 : 2, NP = 3 - NS;
+  static constexpr int T_Q = D, T_S = T_Q + D / 2, T_P = T_S + NS * BN;
+  static_assert(T_P + NP * (BN / 2) <= 512, "tensor memory");
   static_assert(ALLOC <= 232448, "shared memory");
 };
 
@@ -103,7 +107,7 @@ struct CutUnit {
 
 struct PageAttnParams {
   CUtensorMap tm_q;            // (D, G, Hkv, N), box (64, G, 1, 128/G)
-  CUtensorMap tm_k;            // (D, Hkv, page, n_pages), box (64, 1, min(page, 64), 1)
+  CUtensorMap tm_k;            // (D, Hkv, page, n_pages), box (64, 1, min(page, BN), 1)
   CUtensorMap tm_v;
   const uint8_t* k_tiles[2];   // store: pinned, window of (layer, head 0)
   const uint8_t* v_tiles[2];
@@ -175,6 +179,20 @@ __device__ __forceinline__ float max32(const float (&x)[32]) {
   return fmaxf(max3(a, b, c), d);
 }
 
+// A bit for every key of a tile.
+template <int BN>
+struct Bits {
+  uint64_t w[BN / 64];
+};
+// The first n of 64 bits (n may be below 0 or above 64).
+__device__ __forceinline__ uint64_t first_bits(int n) { return n >= 64 ? ~0ull : n > 0 ? (1ull << n) - 1 : 0ull; }
+
+// 32 values of an array.
+template <int N>
+__device__ __forceinline__ float (&part(float (&x)[N], int at))[32] {
+  return *reinterpret_cast<float(*)[32]>(x + at);
+}
+
 // Scores of keys that the row does not see.
 __device__ __forceinline__ void hide(float (&x)[32], uint32_t seen) {
 #pragma unroll
@@ -205,12 +223,14 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, ok);
 }
 
-// The store's tiles: pinned, then the window in slot order, past the spare slot.
+// The store's tiles of 64 keys: pinned, then the window in slot order, past the
+// spare slot.  A tile of 128 keys is two of them in a row.
 struct StoreTiles {
   int n_pin, n_win, P, win_len, hole0, hole_n;
   __device__ __forceinline__ int count() const { return n_pin + n_win; }
+  // Keys of its tile t of 64 (0 behind the last).
   __device__ __forceinline__ int valid(int t) const {
-    return min(kBN, t < n_pin ? P - t * kBN : win_len - (t - n_pin) * kBN);
+    return max(0, min(kTileTok, t < n_pin ? P - t * kTileTok : win_len - (t - n_pin) * kTileTok));
   }
 };
 
@@ -220,10 +240,10 @@ __device__ __forceinline__ StoreTiles store_tiles(const PageAttnParams& p, int h
   const bool hole = p.slots > p.frames && valid == p.frames;
   s.P = p.P;
   s.win_len = hole ? (p.slots - 1) * p.F : valid * p.F;
-  s.hole0 = hole ? head * p.F / kBN : 0;
-  s.hole_n = hole ? p.F / kBN : 0;
-  s.n_pin = (p.P + kBN - 1) / kBN;
-  s.n_win = (s.win_len + kBN - 1) / kBN;
+  s.hole0 = hole ? head * p.F / kTileTok : 0;
+  s.hole_n = hole ? p.F / kTileTok : 0;
+  s.n_pin = (p.P + kTileTok - 1) / kTileTok;
+  s.n_win = (s.win_len + kTileTok - 1) / kTileTok;
   return s;
 }
 
@@ -233,7 +253,7 @@ struct Stream {
   int prefix;   // min(prefix, len), 0 without one
 };
 
-__device__ __forceinline__ Stream load_stream(const PageAttnParams& p, int shared, int b) {
+__device__ __forceinline__ Stream load_stream(const PageAttnParams& p, int log_t, int shared, int b) {
   Stream s;
   s.q0 = max(0, min(__ldg(p.q_start + b), p.N));
   const int q1 = max(0, min(__ldg(p.q_start + b + 1), p.N));
@@ -243,6 +263,7 @@ __device__ __forceinline__ Stream load_stream(const PageAttnParams& p, int share
   s.plan.floor = max(1, s.prefix);
   s.plan.shared = shared;
   s.plan.log_a = 7 - p.log_g;
+  s.plan.log_t = log_t;
   return s;
 }
 
@@ -260,11 +281,11 @@ struct Walk {
   int t0, count, tiles;   // the part: tiles [t0, t0 + count) of the unit's `tiles`
   long long left;
 
-  __device__ __forceinline__ bool begin(const PageAttnParams& p, int shared, const RunStart& r) {
+  __device__ __forceinline__ bool begin(const PageAttnParams& p, int log_t, int shared, const RunStart& r) {
     left = r.left;
     if (left <= 0) return false;
     b = r.b;
-    s = load_stream(p, shared, b);
+    s = load_stream(p, log_t, shared, b);
     const long long per_head = s.plan.tiles_before(s.plan.row_tiles());
     h = static_cast<int>(r.at / per_head);
     const long long o = r.at - h * per_head;
@@ -287,7 +308,7 @@ struct Walk {
         h = 0;
         do {
           if (++b >= p.pool.B) return false;
-          s = load_stream(p, s.plan.shared, b);
+          s = load_stream(p, s.plan.log_t, s.plan.shared, b);
         } while (s.plan.n == 0);
       }
     }
@@ -309,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
   int* ring_word = reinterpret_cast<int*>(gbase + Lay::OFF_MISC + 8);
   RunStart* run_start = reinterpret_cast<RunStart*>(gbase + Lay::OFF_MISC + 16);      // 24 bytes
   int* run_len = reinterpret_cast<int*>(gbase + Lay::OFF_MISC + 40);
-  uint8_t* not_finite = gbase + Lay::OFF_MISC + 64;                                    // [2][8]
+  uint8_t* not_finite = gbase + Lay::OFF_MISC + 64;                                    // [2][16]
   float* row_sum = reinterpret_cast<float*>(gbase + Lay::OFF_SUM);
   auto BAR = [&](int i) { return sBar + 8u * static_cast<uint32_t>(i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -343,10 +364,11 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
   if (threadIdx.x == 0 && p.st) load_ring_state(p.st, ring_word, ring_word + 1);
   __syncthreads();
   const StoreTiles store = store_tiles(p, ring_word[0], ring_word[1]);
-  const int shared = store.count();
+  constexpr int kLogT = Lay::BN == 128 ? 7 : 6;
+  const int shared = (store.count() * kTileTok + Lay::BN - 1) >> kLogT;   // tiles
   long long* before = reinterpret_cast<long long*>(gbase + Lay::OFF_K);   // [B + 1]
   for (int b = threadIdx.x; b < p.pool.B; b += kThreads) {
-    const Stream s = load_stream(p, shared, b);
+    const Stream s = load_stream(p, kLogT, shared, b);
     before[b + 1] = p.Hkv * s.plan.tiles_before(s.plan.row_tiles());
   }
   __syncthreads();
@@ -365,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
     if (lane == 0) before[0] = 0;
     __syncwarp();
     if (lane == 0) {
-      const long long each = max(static_cast<long long>(kMinRun), (sum + gridDim.x - 1) / gridDim.x);
+      const long long each = max(static_cast<long long>(kMinRunKeys / Lay::BN), (sum + gridDim.x - 1) / gridDim.x);
       const long long w0 = each * blockIdx.x, w1 = min(sum, w0 + each);
       int lo = 0, hi = p.pool.B - 1;
       while (lo < hi) {   // the last stream that begins at or before w0
@@ -387,10 +409,10 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
   const uint32_t tmem = *tmem_slot;
   const uint32_t tO = tmem, tQ = tmem + Lay::T_Q, tS = tmem + Lay::T_S, tP = tmem + Lay::T_P;
   const int lp = p.pool.log_page;
-  const int box = lp < 6 ? 1 << lp : kBN;                 // tokens of one page copy
+  const int box = lp < kLogT ? 1 << lp : Lay::BN;         // tokens of one page copy
 
   Walk w;
-  const bool some = w.begin(p, shared, run);
+  const bool some = w.begin(p, kLogT, shared, run);
   if (some && (warp == 0 || warp == 3)) {
     // ------------------------------------------------------------ copies of K, of V
     // All lanes of a warp go along: they hold the table's next 64 entries (asked
@@ -400,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
     const int slots = isv ? Lay::NV : Lay::NK;
     const int bf = isv ? B_VF : B_KF, be = isv ? B_VE : B_KE;
     const uint32_t ring = isv ? sV : sK;
-    const int log_e = lp < 6 ? 6 - lp : 0;                 // pages of a tile
+    const int log_e = lp < kLogT ? kLogT - lp : 0;         // pages of a tile
     const int i = lane & ((1 << log_e) - 1), kb = lane >> log_e;   // this lane's box
     int slot = 0, round = 0, issued = 0;
     bool more = true, stop = false;
@@ -409,10 +431,10 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
       const int len = w.s.plan.len;
       auto entry = [&](int e) { return (static_cast<long long>(e) << lp) < len ? __ldg(table + e) : -1; };
       const int t_end = w.t0 + w.count;
-      int e_base = max(0, (w.t0 - shared) * kBN) >> lp;
+      int e_base = max(0, (w.t0 - shared) * Lay::BN) >> lp;
       int now = entry(e_base + lane), then = entry(e_base + 32 + lane);
       for (int t = w.t0; t < t_end; ++t) {
-        const int key0 = (t - shared) * kBN;
+        const int key0 = (t - shared) * Lay::BN;
         if (round > 0 && !warp_wait(BAR(be + slot), (round - 1) & 1, abort_flag)) {
           stop = true;
           break;
@@ -420,13 +442,20 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
         const uint32_t dst = ring + slot * Lay::TILE, bar = BAR(bf + slot);
         const uint32_t extra = issued == 0 && !isv && blockIdx.x == 0 ? static_cast<uint32_t>(p.inject_tx) : 0u;
         if (t < shared) {
-          if (lane == 0) {
-            const int region = t < store.n_pin ? 0 : 1;
-            int at = region ? t - store.n_pin : t;
+          // Two (at D = 256 one) tiles of the store; a lane copies 64 columns of one.
+          constexpr int kHalves = Lay::BN / kTileTok;
+          const int t64 = t * kHalves + (lane & (kHalves - 1)), block = lane / kHalves;
+          const bool there = t64 < store.count();
+          const uint32_t tiles = __popc(__ballot_sync(0xffffffffu, there && block == 0));
+          if (lane == 0) mbar_arrive_expect_tx(bar, tiles * Lay::KB * 8192 + extra);
+          __syncwarp();
+          if (there && block < Lay::KB) {
+            const int region = t64 < store.n_pin ? 0 : 1;
+            int at = region ? t64 - store.n_pin : t64;
             if (region && at >= store.hole0) at += store.hole_n;
-            const uint8_t* tiles = isv ? p.v_tiles[region] : p.k_tiles[region];
-            mbar_arrive_expect_tx(bar, Lay::TILE + extra);
-            bulk_load(dst, tiles + w.h * p.head_stride[region] + static_cast<long long>(at) * Lay::TILE, Lay::TILE, bar);
+            const uint8_t* src = (isv ? p.v_tiles[region] : p.k_tiles[region]) + w.h * p.head_stride[region] +
+                                 (static_cast<long long>(at) * Lay::KB + block) * 8192;
+            bulk_load(dst + block * Lay::BLOCK + (lane & (kHalves - 1)) * 8192, src, 8192, bar);
           }
         } else {
           const int e0 = key0 >> lp;
@@ -441,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
           if (lane == 0) mbar_arrive_expect_tx(bar, pages * box * (D * 2) + extra);
           __syncwarp();
           if (named && kb < Lay::KB)
-            tma_load_4d(dst + kb * 8192 + i * box * 128, tm, kb * 64, w.h, lp > 6 ? key0 & ((1 << lp) - 1) : 0, pg, bar);
+            tma_load_4d(dst + kb * Lay::BLOCK + i * box * 128, tm, kb * 64, w.h, lp > kLogT ? key0 & ((1 << lp) - 1) : 0, pg, bar);
         }
         ++issued;
         if (++slot == slots) {
@@ -458,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
     // ------------------------------------------------------------ Q K^T
     // Q is the A operand from tensor memory.  All lanes run the loop, so that its
     // values are the same for the whole warp, and one issues the products.
-    constexpr uint32_t kIdesc = idesc_bf16_f32(kBM, kBN, false, false);
+    constexpr uint32_t kIdesc = idesc_bf16_f32(kBM, Lay::BN, false, false);
     const bool leader = elect_one();
     int j = 0, slot = 0, round = 0, u = 0, asked = 0;
     bool ok = true, more = true;
@@ -492,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            umma_bf16_ts(tS + st * kBN, tQ + kk * 8, desc + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), kIdesc, kk > 0 ? 1u : 0u);
+            umma_bf16_ts(tS + st * Lay::BN, tQ + kk * 8, desc + (((kk >> 2) * Lay::BLOCK + (kk & 3) * 32) >> 4), kIdesc, kk > 0 ? 1u : 0u);
           umma_commit(BAR(B_KE + slot));
           umma_commit(BAR(B_SF + st));
         }
@@ -526,12 +555,12 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
         // O still holds the last unit until the softmax warps have read it.
         if (t == 0 && u > 0 && !warp_wait(BAR(B_OR), (u - 1) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        const uint64_t desc = sdesc_sw128(sV + slot * Lay::TILE, 8192, 1024);
+        const uint64_t desc = sdesc_sw128(sV + slot * Lay::TILE, Lay::BLOCK, 1024);
         const uint32_t more = t > 0 ? 1u : 0u;
         if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < kBN / 16; ++kk)
-            umma_bf16_ts(tO, tP + st * (kBN / 2) + kk * 8, desc + ((kk * 16 * 128) >> 4), kIdesc, kk > 0 ? 1u : more);
+          for (int kk = 0; kk < Lay::BN / 16; ++kk)
+            umma_bf16_ts(tO, tP + (Lay::NP == 2 ? st * (Lay::BN / 2) : 0) + kk * 8, desc + ((kk * 16 * 128) >> 4), kIdesc, kk > 0 ? 1u : more);
           umma_commit(BAR(B_VE + slot));
           umma_commit(BAR(B_PV + st));
         }
@@ -552,8 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
     // A row has two threads, in warps w and w + 4 (a warp reaches the tensor memory
     // lanes of its quarter): each looks at all scores of the row for the maximum, so
     // that both arrive at the same reference without a word, takes the exponentials
-    // of its 32 columns and, later, its half of O's columns.
-    constexpr int kOCols = D / 2;
+    // of half of the columns and, later, its half of O's columns.
+    constexpr int kOCols = D / 2, BN = Lay::BN;
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const int row = quarter * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
@@ -593,66 +622,108 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
       const int lim = row_valid ? max(x0 + t_row + 1, w.s.prefix) : 0;
       const int all = max(x0 + (w.rt << w.s.plan.log_a) + 1, w.s.prefix);
       const int* table = p.pool.table + static_cast<long long>(w.b) * p.pool.max_pages;
-      // This lane's table entry for a tile: its page i = lane, or the tile's page.
-      const int own_at = lp < 6 ? (lane & ((kBN >> lp) - 1)) << lp : 0;
-      auto entry = [&](int t) {
-        const int place = (t - shared) * kBN + own_at;
-        return t >= shared && place < w.s.plan.len ? __ldg(table + (place >> lp)) : 0;
-      };
-      int ent = entry(w.t0);
+      // Which of the 32 table entries from e_base on name a page (those behind the
+      // stream's end pass), and the lanes' entries after them, on their way.
+      const int log_e = lp < kLogT ? kLogT - lp : 0;                // pages of a tile
+      const uint32_t tile_pages = (2u << ((1 << log_e) - 1)) - 1;   // a bit for each
+      auto entry = [&](int e) { return (static_cast<long long>(e) << lp) < w.s.plan.len ? __ldg(table + e) : 0; };
+      auto named_of = [&](int x) { return __ballot_sync(0xffffffffu, static_cast<unsigned int>(x) < static_cast<unsigned int>(p.pool.n_pages)); };
+      int e_base = max(0, (w.t0 - shared) * BN) >> lp;
+      uint32_t named32 = named_of(entry(e_base + lane));
+      int then = entry(e_base + 32 + lane);
+      const int plain = min(w.s.plan.len, all);   // every row sees every key before it
       float m_used = -INFINITY;
       float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       bool poison = false;
       for (int t = w.t0; ok && t < w.t0 + w.count; ++t, ++j) {
         const int st = j & 1;
         // Keys of the tile that are there, and those that this row sees.
-        uint64_t there = ~0ull, mine = ~0ull;
+        Bits<BN> there, mine;
         bool check;
         if (t < shared) {
-          const int nv = store.valid(t);
-          check = nv < kBN;
-          if (check) there = mine = (1ull << nv) - 1;
-        } else {
-          const int key0 = (t - shared) * kBN;
-          const int nv = w.s.plan.len - key0;
-          const uint32_t named = __ballot_sync(0xffffffffu, static_cast<unsigned int>(ent) < static_cast<unsigned int>(p.pool.n_pages));
-          check = named != 0xffffffffu || nv < kBN || key0 + kBN > all;
+          constexpr int kHalves = BN / kTileTok;
+          int nv[kHalves];
+          check = false;
+#pragma unroll
+          for (int i = 0; i < kHalves; ++i) {
+            nv[i] = store.valid(t * kHalves + i);
+            check = check || nv[i] < kTileTok;
+          }
           if (check) {
-            if (named != 0xffffffffu) {
-              there = 0;
-              if (lp < 6)
-                for (int i = 0; i < (kBN >> lp); ++i)
-                  if (named >> i & 1) there |= ((1ull << (1 << lp)) - 1) << (i << lp);
-            }
-            if (nv < kBN) there = nv > 0 ? there & ((1ull << nv) - 1) : 0;
+#pragma unroll
+            for (int i = 0; i < kHalves; ++i) there.w[i] = first_bits(nv[i]);
             mine = there;
-            const int seen = lim - key0;
-            if (seen < kBN) mine = seen > 0 ? mine & ((1ull << seen) - 1) : 0;
+          }
+        } else {
+          const int key0 = (t - shared) * BN;
+          const int e0 = key0 >> lp;
+          if (e0 - e_base >= 32) {
+            e_base += 32;
+            named32 = named_of(then);
+            then = entry(e_base + 32 + lane);
+          }
+          const uint32_t named = named32 >> (e0 - e_base) & tile_pages;
+          check = named != tile_pages || key0 + BN > plain;
+          if (check) {
+            const int nv = w.s.plan.len - key0, seen = lim - key0;
+#pragma unroll
+            for (int i = 0; i < BN / 64; ++i) {
+              uint64_t x = ~0ull;
+              if (named != tile_pages) {
+                x = 0;
+                for (int e = 0; e < max(1, 64 >> lp); ++e) {   // lp >= 6: one page holds the 64 keys
+                  const int page_of = lp < 6 ? (i << (6 - lp)) + e : lp < kLogT ? i : 0;
+                  if (named >> page_of & 1) x |= lp < 6 ? ((1ull << (1 << lp)) - 1) << (e << lp) : ~0ull;
+                }
+              }
+              there.w[i] = x & first_bits(nv - 64 * i);
+              mine.w[i] = there.w[i] & first_bits(seen - 64 * i);
+            }
           }
         }
-        ent = entry(t + 1);
         const int sb = j % Lay::NS;
         if (!warp_wait(BAR(B_SF + sb), (j / Lay::NS) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        float s[32], r[32];   // this thread's columns, the rest of the row
-        tmem_ld32x2(tS + sb * kBN + half * 32 + lane_off, s, tS + sb * kBN + (half ^ 1) * 32 + lane_off, r);
+        float s[BN / 2];   // this thread's columns; the others are looked at only
+        float top;
+        const uint32_t s_own = tS + sb * BN + half * (BN / 2) + lane_off, s_other = tS + sb * BN + (half ^ 1) * (BN / 2) + lane_off;
+        if constexpr (BN == 64) {
+          float r[32];
+          tmem_ld32x2(s_own, s, s_other, r);
+          if (check) {
+            hide(s, static_cast<uint32_t>(mine.w[0] >> (32 * half)));
+            hide(r, static_cast<uint32_t>(mine.w[0] >> (32 - 32 * half)));
+          }
+          top = fmaxf(max32(r), max32(s));
+        } else {
+          float r[64];
+          tmem_ld64(s_other, r);
+          const uint64_t seen_r = half ? mine.w[0] : mine.w[BN / 64 - 1], seen_s = half ? mine.w[BN / 64 - 1] : mine.w[0];
+          if (check) {
+            hide(part(r, 0), static_cast<uint32_t>(seen_r));
+            hide(part(r, 32), static_cast<uint32_t>(seen_r >> 32));
+          }
+          top = fmaxf(max32(part(r, 0)), max32(part(r, 32)));
+          tmem_ld64(s_own, s);
+          if (check) {
+            hide(part(s, 0), static_cast<uint32_t>(seen_s));
+            hide(part(s, 32), static_cast<uint32_t>(seen_s >> 32));
+          }
+          top = fmaxf(top, fmaxf(max32(part(s, 0)), max32(part(s, 32))));
+        }
         tc_fence_before();
         mbar_arrive(BAR(B_SR + sb));
         if (check) {
-          hide(s, static_cast<uint32_t>(mine >> (32 * half)));
-          hide(r, static_cast<uint32_t>(mine >> (32 - 32 * half)));
-        }
-        if (check) {
-          // V's rows: four threads each.  P V of tile j - 2 first: until then
+          // V's rows, some threads each.  P V of tile j - 2 first: until then
           // V's barrier may be one phase behind, and its parity would pass.
           if (j >= 2 && !warp_wait(BAR(B_PV + st), ((j - 2) >> 1) & 1, abort_flag)) { ok = false; break; }
           if (!warp_wait(BAR(B_VF + vslot), vround & 1, abort_flag)) { ok = false; break; }
-          constexpr int kShare = kSoftmax / kBN;   // threads of a V row
+          constexpr int kShare = kSoftmax / BN;   // threads of a V row: 2 or 4
           const int vr = (threadIdx.x - 128) / kShare;
           const uint32_t at = sV + vslot * Lay::TILE + vr * 128;
           constexpr int kChunks = D / 8 / kShare;
           const int c0 = (lane & (kShare - 1)) * kChunks;
-          const bool outside = !(there >> vr & 1);
+          const bool outside = !(there.w[vr >> 6] >> (vr & 63) & 1);
           uint32_t odd = 0;
           if (!outside) {
 #pragma unroll
@@ -661,36 +732,47 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
               uint32_t x[4];
               asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                            : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                           : "r"(at + (c >> 3) * 8192 + (((c & 7) ^ (vr & 7)) << 4)));
+                           : "r"(at + (c >> 3) * Lay::BLOCK + (((c & 7) ^ (vr & 7)) << 4)));
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 odd |= ((x[e] & 0x7F80u) == 0x7F80u) | ((x[e] & 0x7F800000u) == 0x7F800000u);
             }
           }
           odd |= __shfl_xor_sync(0xffffffffu, odd, 1);
-          odd |= __shfl_xor_sync(0xffffffffu, odd, 2);
+          if (kShare == 4) odd |= __shfl_xor_sync(0xffffffffu, odd, 2);
           if (outside || odd) {
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i) st_shared_v4(at + ((c0 + i) >> 3) * 8192 + (((c0 + i) & 7) << 4), 0u, 0u, 0u, 0u);
+            for (int i = 0; i < kChunks; ++i) st_shared_v4(at + ((c0 + i) >> 3) * Lay::BLOCK + (((c0 + i) & 7) << 4), 0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
+          // Every second or fourth lane's bit, close up.
           uint32_t rows = __ballot_sync(0xffffffffu, odd != 0);
-          volatile uint8_t* bits = not_finite + (checks & 1) * 8;
-          rows &= 0x11111111u;   // every fourth lane -> 8 bits
-          rows = (rows | rows >> 3) & 0x03030303u;
-          rows = (rows | rows >> 6) & 0x000F000Fu;
-          rows = (rows | rows >> 12) & 0x000000FFu;
-          if (lane == 0) bits[warp - 4] = static_cast<uint8_t>(rows);
+          volatile uint8_t* bits = not_finite + (checks & 1) * 16;
+          if constexpr (kShare == 4) {
+            rows &= 0x11111111u;
+            rows = (rows | rows >> 3) & 0x03030303u;
+            rows = (rows | rows >> 6) & 0x000F000Fu;
+            rows = (rows | rows >> 12) & 0x000000FFu;
+            if (lane == 0) bits[warp - 4] = static_cast<uint8_t>(rows);
+          } else {
+            rows &= 0x55555555u;
+            rows = (rows | rows >> 1) & 0x33333333u;
+            rows = (rows | rows >> 2) & 0x0F0F0F0Fu;
+            rows = (rows | rows >> 4) & 0x00FF00FFu;
+            rows = (rows | rows >> 8) & 0x0000FFFFu;
+            if (lane == 0) reinterpret_cast<volatile uint16_t*>(bits)[warp - 4] = static_cast<uint16_t>(rows);
+          }
           mbar_arrive(BAR(B_CHK));
           if (!warp_wait(BAR(B_CHK), checks & 1, abort_flag)) { ok = false; break; }
           ++checks;
-          poison = poison || (*reinterpret_cast<volatile uint64_t*>(bits) & mine) != 0;
+#pragma unroll
+          for (int i = 0; i < BN / 64; ++i) poison = poison || (reinterpret_cast<volatile uint64_t*>(bits)[i] & mine.w[i]) != 0;
         }
         if (++vslot == Lay::NV) {
           vslot = 0;
           ++vround;
         }
-        const float m_new = fmaxf(m_used, fmaxf(max32(s), max32(r)) * p.scale_log2);
+        const float m_new = fmaxf(m_used, top * p.scale_log2);
         const bool need = m_new > m_used + kRescale;
         float fac = 1.f;
         if (need) {
@@ -713,16 +795,18 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
         }
         const float nmb = m_used == -INFINITY ? 0.f : -m_used;
         const float2 nmb2 = make_float2(nmb, nmb);
-        uint32_t pk[16];
+        uint32_t pk[BN / 4];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
+        for (int c = 0; c < BN / 4; ++c) {
           float2 e = fma2(make_float2(s[2 * c], s[2 * c + 1]), scale2, nmb2);
           e = make_float2(exp2f(e.x), exp2f(e.y));
           l2[c & 1] = add2(l2[c & 1], e);
           pk[c] = pack_bf16x2(e.x, e.y);
         }
-        if (j >= 2 && !warp_wait(BAR(B_PV + st), ((j - 2) >> 1) & 1, abort_flag)) { ok = false; break; }
-        tmem_st16(tP + st * (kBN / 2) + half * 16 + lane_off, pk);
+        // P's place was last read by P V of tile j - NP.
+        if (j >= Lay::NP && !warp_wait(BAR(B_PV + ((j - Lay::NP) & 1)), ((j - Lay::NP) >> 1) & 1, abort_flag)) { ok = false; break; }
+        if constexpr (BN == 64) tmem_st16(tP + st * (BN / 2) + half * (BN / 4) + lane_off, pk);
+        else tmem_st32(tP + half * (BN / 4) + lane_off, reinterpret_cast<const float*>(pk));
         tc_fence_before();
         mbar_arrive(BAR(B_PF + st));
       }
@@ -990,7 +1074,8 @@ cudaError_t launch_attend_pages(const PageAttention& a, const PagePool& pool, co
     if (!encode_tmap_4d(&p.tm_q, a.q, dims, strides, box)) return cudaErrorInvalidValue;
     const uint64_t pd[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.Hkv), static_cast<uint64_t>(page), static_cast<uint64_t>(pool.n_pages)};
     const uint64_t ps[3] = {D * u, D * u * a.Hkv, D * u * a.Hkv * page};
-    const uint32_t pb[4] = {64, 1, static_cast<uint32_t>(page < kBN ? page : kBN), 1};
+    const int keys = D == 256 ? Layout<256>::BN : Layout<128>::BN;
+    const uint32_t pb[4] = {64, 1, static_cast<uint32_t>(page < keys ? page : keys), 1};
     if (!encode_tmap_4d(&p.tm_k, pool.k, pd, ps, pb) || !encode_tmap_4d(&p.tm_v, pool.v, pd, ps, pb)) return cudaErrorInvalidValue;
   }
   if (al) {

@@ -5,8 +5,8 @@
 // A stream with n new tokens and len keys has R = ceil(n / a) row tiles of a =
 // 128 / G tokens each, for every K/V head.  Token t sees the places below
 // max(len - n + t + 1, min(prefix, len)), so row tile r reads `shared` tiles of
-// the store and ceil(max(len - n + min(n, (r + 1) a), prefix, 1) / 64) tiles of
-// its pages (at least one, which may be empty: it gives the row its zeros).
+// the store and ceil(max(len - n + min(n, (r + 1) a), prefix, 1) / keys) tiles of
+// its pages, a tile being 64 or 128 keys (at least one, which may be empty: it gives the row its zeros).
 // Work is numbered by stream, head, row tile, key tile.  tiles_before() sums
 // the row tiles in closed form, so that a CTA finds its run's start without a
 // list.
@@ -28,6 +28,7 @@ struct StreamPlan {
   int floor;    // max(1, min(prefix, len)): keys that every row tile reads at least
   int shared;   // tiles of the store
   int log_a;    // a = 1 << log_a tokens in a row tile, 1 to 128
+  int log_t;    // keys of a tile: 64 or 128
 
   RX_HD int row_tiles() const { return (n + (1 << log_a) - 1) >> log_a; }
 
@@ -35,7 +36,7 @@ struct StreamPlan {
   RX_HD int tiles(int r) const {
     const int last = (r + 1) << log_a;
     const int x = len - n + (last < n ? last : n);
-    return shared + (((x > floor ? x : floor) + 63) >> 6);
+    return shared + (((x > floor ? x : floor) + (1 << log_t) - 1) >> log_t);
   }
 
   // Key tiles of row tiles [0, r), r <= row_tiles().
@@ -47,19 +48,19 @@ struct StreamPlan {
       --r;
     }
     // Row tiles below r0 end before `floor`; from r0 on they read
-    // ceil((x0 + a (r + 1)) / 64) tiles.
-    const int x0 = len - n, a = 1 << log_a;
+    // ceil((x0 + a (r + 1)) / keys) tiles.
+    const int x0 = len - n, a = 1 << log_a, up = (1 << log_t) - 1;
     int r0 = ((floor - x0 + a - 1) >> log_a) - 1;
     if (r0 < 0) r0 = 0;
     const int low = r < r0 ? r : r0;
-    sum += static_cast<long long>(low) * ((floor + 63) >> 6);
+    sum += static_cast<long long>(low) * ((floor + up) >> log_t);
     if (r > r0) {
-      if (log_a < 6) {       // floor((e + i) / 2^ls) for i = r0 .. r-1
-        const int ls = 6 - log_a;
-        const long long e = (x0 + 63 + a) >> log_a;
+      if (log_a < log_t) {   // floor((e + i) / 2^ls) for i = r0 .. r-1
+        const int ls = log_t - log_a;
+        const long long e = (x0 + up + a) >> log_a;
         sum += steps(e + r, ls) - steps(e + r0, ls);
       } else {               // e + m i
-        const long long e = (x0 + 63 + a) >> 6, m = a >> 6;
+        const long long e = (x0 + up + a) >> log_t, m = a >> log_t;
         sum += e * (r - r0) + m * (static_cast<long long>(r) * (r - 1) - static_cast<long long>(r0) * (r0 - 1)) / 2;
       }
     }

@@ -1047,11 +1047,12 @@ rx_status rx_evict_pages(const rx_pages* pages, int Hkv, int D, const int* len, 
   RX_GUARD_END
 }
 
-rx_status rx_debug_page_plan(int n, int len, int prefix, int shared, int G, int r, long long* before, int* row_tile) {
+rx_status rx_debug_page_plan(int n, int len, int prefix, int shared, int G, int keys, int r, long long* before,
+                             int* row_tile) {
   RX_GUARD_BEGIN
   const int most = 1 << 30;
   if (!before || !row_tile || n < 1 || n > most || len < 0 || len > most || prefix < 0 || shared < 0 || shared > most ||
-      !pow2(G) || G > rx::kBM)
+      !pow2(G) || G > rx::kBM || (keys != 64 && keys != 128))
     return fail(RX_ERR_ARG, "rx_debug_page_plan: argument out of range");
   rx::StreamPlan s;
   s.n = n;
@@ -1060,6 +1061,7 @@ rx_status rx_debug_page_plan(int n, int len, int prefix, int shared, int G, int 
   if (s.floor < 1) s.floor = 1;
   s.shared = shared;
   s.log_a = 7 - log2_of(G);
+  s.log_t = log2_of(keys);
   if (r < 0 || r > s.row_tiles()) return fail(RX_ERR_ARG, "rx_debug_page_plan: r = %d not in [0, %d]", r, s.row_tiles());
   *before = s.tiles_before(r);
   *row_tile = r < s.row_tiles() ? s.row_tile_of(*before) : -1;

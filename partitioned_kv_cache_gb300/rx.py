@@ -124,7 +124,7 @@ _sigs = {
     "rx_attend_pages_workspace": (_i, [_i, _i, _i, _i, ctypes.POINTER(ctypes.c_longlong)]),
     "rx_weigh_pages": (_i, [_vp, _vp, _i, _i, _i, _i, ctypes.POINTER(RxPages), _vp, _vp, _vp, _f, _vp, _vp]),
     "rx_evict_pages": (_i, [ctypes.POINTER(RxPages), _i, _i, _vp, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _vp]),
-    "rx_debug_page_plan": (_i, [_i] * 6 + [ctypes.POINTER(ctypes.c_longlong), ctypes.POINTER(_i)]),
+    "rx_debug_page_plan": (_i, [_i] * 7 + [ctypes.POINTER(ctypes.c_longlong), ctypes.POINTER(_i)]),
     "rx_verify_drafts": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]),
 }
 for _name, (_res, _args) in _sigs.items():
@@ -258,11 +258,11 @@ def choose_stream_partition(t_max: int, units: int, tail_tiles: int, num_sms: in
     return sp.value, ts.value
 
 
-def page_plan(n: int, length: int, prefix: int, shared: int, G: int, r: int):
+def page_plan(n: int, length: int, prefix: int, shared: int, G: int, keys: int, r: int):
     """Test aid: (key tiles before row tile r, that tile's row tile) of a stream in
     attend_pages (rx_debug_page_plan)."""
     before, row_tile = ctypes.c_longlong(0), _i(0)
-    _check(_lib.rx_debug_page_plan(n, length, prefix, shared, G, r, ctypes.byref(before), ctypes.byref(row_tile)),
+    _check(_lib.rx_debug_page_plan(n, length, prefix, shared, G, keys, r, ctypes.byref(before), ctypes.byref(row_tile)),
            "rx_debug_page_plan")
     return before.value, row_tile.value
 

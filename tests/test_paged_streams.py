@@ -71,10 +71,10 @@ def test_plan_of_row_tiles(lib):
         n, shared = int(g.integers(1, 40 if g.random() < 0.5 else 900)), int(g.integers(0, 5))
         length = n + int(g.integers(0, 300)) if g.random() < 0.7 else int(g.integers(0, 900))
         prefix = int(g.integers(0, 900)) if g.random() < 0.3 else 0
-        R = -(-n // a)
-        tiles = [shared + -(-max(1, OP.seen(min(n, (r + 1) * a) - 1, n, length, prefix)) // 64) for r in range(R)]
+        R, keys = -(-n // a), int(g.choice([64, 128]))
+        tiles = [shared + -(-max(1, OP.seen(min(n, (r + 1) * a) - 1, n, length, prefix)) // keys) for r in range(R)]
         r = int(g.integers(0, R + 1))
-        before, row_tile = rx.page_plan(n, length, prefix, shared, G, r)
+        before, row_tile = rx.page_plan(n, length, prefix, shared, G, keys, r)
         assert before == sum(tiles[:r])
         assert row_tile == (r if r < R else -1)
 
