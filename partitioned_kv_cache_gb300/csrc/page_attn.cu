@@ -106,8 +106,8 @@ struct CutUnit {
 };
 
 struct PageAttnParams {
-  CUtensorMap tm_q;            // (D, G, Hkv, N), box (64, G, 1, 128/G)
-  CUtensorMap tm_k;            // (D, Hkv, page, n_pages), box (64, 1, min(page, BN), 1)
+  CUtensorMap tm_q;            // 128 query rows (encode_query_map)
+  CUtensorMap tm_k;            // a page's keys, BN at most (encode_page_map)
   CUtensorMap tm_v;
   const uint8_t* k_tiles[2];   // store: pinned, window of (layer, head 0)
   const uint8_t* v_tiles[2];
@@ -415,15 +415,16 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
   const bool some = w.begin(p, kLogT, shared, run);
   if (some && (warp == 0 || warp == 3)) {
     // ------------------------------------------------------------ copies of K, of V
-    // All lanes of a warp go along: they hold the table's next 64 entries (asked
-    // for a round ahead), and each issues one of a tile's boxes.
+    // The lanes hold the table's next 64 entries, asked for a round ahead; one
+    // issues (copies by several lanes of a warp go one after the other, some 250
+    // cycles each).
+    const bool leader = elect_one();
     const bool isv = warp == 3;
     const CUtensorMap* tm = isv ? &p.tm_v : &p.tm_k;
     const int slots = isv ? Lay::NV : Lay::NK;
     const int bf = isv ? B_VF : B_KF, be = isv ? B_VE : B_KE;
     const uint32_t ring = isv ? sV : sK;
     const int log_e = lp < kLogT ? kLogT - lp : 0;         // pages of a tile
-    const int i = lane & ((1 << log_e) - 1), kb = lane >> log_e;   // this lane's box
     int slot = 0, round = 0, issued = 0;
     bool more = true, stop = false;
     do {
@@ -442,20 +443,26 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
         const uint32_t dst = ring + slot * Lay::TILE, bar = BAR(bf + slot);
         const uint32_t extra = issued == 0 && !isv && blockIdx.x == 0 ? static_cast<uint32_t>(p.inject_tx) : 0u;
         if (t < shared) {
-          // Two (at D = 256 one) tiles of the store; a lane copies 64 columns of one.
+          // Two (at D = 256 one) tiles of the store.
           constexpr int kHalves = Lay::BN / kTileTok;
-          const int t64 = t * kHalves + (lane & (kHalves - 1)), block = lane / kHalves;
-          const bool there = t64 < store.count();
-          const uint32_t tiles = __popc(__ballot_sync(0xffffffffu, there && block == 0));
-          if (lane == 0) mbar_arrive_expect_tx(bar, tiles * Lay::KB * 8192 + extra);
-          __syncwarp();
-          if (there && block < Lay::KB) {
-            const int region = t64 < store.n_pin ? 0 : 1;
-            int at = region ? t64 - store.n_pin : t64;
-            if (region && at >= store.hole0) at += store.hole_n;
-            const uint8_t* src = (isv ? p.v_tiles[region] : p.k_tiles[region]) + w.h * p.head_stride[region] +
-                                 (static_cast<long long>(at) * Lay::KB + block) * 8192;
-            bulk_load(dst + block * Lay::BLOCK + (lane & (kHalves - 1)) * 8192, src, 8192, bar);
+          if (leader) {
+            mbar_arrive_expect_tx(bar, min(kHalves, store.count() - t * kHalves) * Lay::KB * 8192 + extra);
+#pragma unroll
+            for (int i = 0; i < kHalves; ++i) {
+              const int t64 = t * kHalves + i;
+              if (t64 >= store.count()) break;
+              const int region = t64 < store.n_pin ? 0 : 1;
+              int at = region ? t64 - store.n_pin : t64;
+              if (region && at >= store.hole0) at += store.hole_n;
+              const uint8_t* src = (isv ? p.v_tiles[region] : p.k_tiles[region]) + w.h * p.head_stride[region] +
+                                   static_cast<long long>(at) * Lay::KB * 8192;
+              if constexpr (kHalves == 1) {
+                bulk_load(dst, src, Lay::TILE, bar);
+              } else {
+#pragma unroll
+                for (int kb = 0; kb < Lay::KB; ++kb) bulk_load(dst + kb * Lay::BLOCK + i * 8192, src + kb * 8192, 8192, bar);
+              }
+            }
           }
         } else {
           const int e0 = key0 >> lp;
@@ -464,14 +471,15 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
             now = then;
             then = entry(e_base + 32 + lane);
           }
-          const int pg = __shfl_sync(0xffffffffu, now, e0 - e_base + i);
-          const bool named = static_cast<unsigned int>(pg) < static_cast<unsigned int>(p.pool.n_pages);
-          const uint32_t pages = __popc(__ballot_sync(0xffffffffu, named && kb == 0));
-          if (lane == 0) mbar_arrive_expect_tx(bar, pages * box * (D * 2) + extra);
-          __syncwarp();
-          if (named && kb < Lay::KB)
-            tma_load_4d(dst + kb * Lay::BLOCK + i * box * 128, tm, kb * 64, w.h, lp > kLogT ? key0 & ((1 << lp) - 1) : 0, pg, bar);
+          const int at = e0 - e_base, pages = 1 << log_e, row = lp > kLogT ? key0 & ((1 << lp) - 1) : 0;
+          const uint32_t named = __ballot_sync(0xffffffffu, static_cast<unsigned int>(now) < static_cast<unsigned int>(p.pool.n_pages)) >> at & ((2u << (pages - 1)) - 1);
+          if (leader) mbar_arrive_expect_tx(bar, __popc(named) * box * (D * 2) + extra);
+          for (int i = 0; i < pages; ++i) {
+            const int pg = __shfl_sync(0xffffffffu, now, at + i);
+            if (leader && (named >> i & 1)) tma_load_5d(dst + i * box * Lay::KB * 128, tm, 0, 0, w.h * Lay::KB, row >> 3, pg, bar);
+          }
         }
+        __syncwarp();
         ++issued;
         if (++slot == slots) {
           slot = 0;
@@ -494,15 +502,14 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
     auto ask_q = [&](const Walk& x) {        // a unit's Q into shared memory
       if (leader) {
         mbar_arrive_expect_tx(BAR(B_QF), Lay::Q_BYTES);
-        for (int kb = 0; kb < Lay::KB; ++kb)
-          tma_load_4d(sQ + kb * Lay::Q_BLOCK, &p.tm_q, kb * 64, 0, x.h, x.s.q0 + (x.rt << x.s.plan.log_a), BAR(B_QF));
+        tma_load_4d(sQ, &p.tm_q, 0, 0, x.s.q0 + (x.rt << x.s.plan.log_a), (x.h << p.log_g) * Lay::KB, BAR(B_QF));
       }
       __syncwarp();
       ++asked;
     };
     ask_q(w);
     while (more) {
-      const int count = uniform(w.count);
+      const int count = uniform(w.count), first_t = uniform(w.t0);
       Walk coming = w;
       more = coming.next(p);
       ok = warp_wait(BAR(B_QT), u & 1, abort_flag);
@@ -517,11 +524,14 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
         if (j >= Lay::NS && !warp_wait(BAR(B_SR + st), (j / Lay::NS - 1) & 1, abort_flag)) { ok = false; break; }
         if (!warp_wait(BAR(B_KF + slot), round & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        const uint64_t desc = sdesc_sw128(sK + slot * Lay::TILE, 16, 1024);
+        // The store's tiles are [column block][token], the pages' [8 tokens][column block].
+        const bool paged = first_t + t >= shared;
+        const uint64_t desc = sdesc_sw128(sK + slot * Lay::TILE, 16, paged ? Lay::KB * 1024 : 1024);
+        const uint32_t block = (paged ? 1024 : Lay::BLOCK) >> 4;
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            umma_bf16_ts(tS + st * Lay::BN, tQ + kk * 8, desc + (((kk >> 2) * Lay::BLOCK + (kk & 3) * 32) >> 4), kIdesc, kk > 0 ? 1u : 0u);
+            umma_bf16_ts(tS + st * Lay::BN, tQ + kk * 8, desc + ((kk >> 2) * block + (kk & 3) * 2), kIdesc, kk > 0 ? 1u : 0u);
           umma_commit(BAR(B_KE + slot));
           umma_commit(BAR(B_SF + st));
         }
@@ -547,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
     int j = 0, slot = 0, round = 0, u = 0;
     bool ok = true;
     do {
-      const int count = uniform(w.count);
+      const int count = uniform(w.count), first_t = uniform(w.t0);
       for (int t = 0; t < count; ++t) {
         const int st = j & 1;
         if (!warp_wait(BAR(B_PF + st), (j >> 1) & 1, abort_flag)) { ok = false; break; }
@@ -555,12 +565,14 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
         // O still holds the last unit until the softmax warps have read it.
         if (t == 0 && u > 0 && !warp_wait(BAR(B_OR), (u - 1) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        const uint64_t desc = sdesc_sw128(sV + slot * Lay::TILE, Lay::BLOCK, 1024);
+        const bool paged = first_t + t >= shared;
+        const uint64_t desc = sdesc_sw128(sV + slot * Lay::TILE, paged ? 1024 : Lay::BLOCK, paged ? Lay::KB * 1024 : 1024);
+        const uint32_t step = (paged ? Lay::KB * 2048 : 2048) >> 4;   // 16 keys
         const uint32_t more = t > 0 ? 1u : 0u;
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < Lay::BN / 16; ++kk)
-            umma_bf16_ts(tO, tP + (Lay::NP == 2 ? st * (Lay::BN / 2) : 0) + kk * 8, desc + ((kk * 16 * 128) >> 4), kIdesc, kk > 0 ? 1u : more);
+            umma_bf16_ts(tO, tP + (Lay::NP == 2 ? st * (Lay::BN / 2) : 0) + kk * 8, desc + kk * step, kIdesc, kk > 0 ? 1u : more);
           umma_commit(BAR(B_VE + slot));
           umma_commit(BAR(B_PV + st));
         }
@@ -720,7 +732,8 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
           if (!warp_wait(BAR(B_VF + vslot), vround & 1, abort_flag)) { ok = false; break; }
           constexpr int kShare = kSoftmax / BN;   // threads of a V row: 2 or 4
           const int vr = (threadIdx.x - 128) / kShare;
-          const uint32_t at = sV + vslot * Lay::TILE + vr * 128;
+          const uint32_t at = sV + vslot * Lay::TILE + (t < shared ? vr * 128 : (vr >> 3) * (Lay::KB * 1024) + (vr & 7) * 128);
+          const uint32_t block = t < shared ? Lay::BLOCK : 1024;
           constexpr int kChunks = D / 8 / kShare;
           const int c0 = (lane & (kShare - 1)) * kChunks;
           const bool outside = !(there.w[vr >> 6] >> (vr & 63) & 1);
@@ -732,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
               uint32_t x[4];
               asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                            : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                           : "r"(at + (c >> 3) * Lay::BLOCK + (((c & 7) ^ (vr & 7)) << 4)));
+                           : "r"(at + (c >> 3) * block + (((c & 7) ^ (vr & 7)) << 4)));
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 odd |= ((x[e] & 0x7F80u) == 0x7F80u) | ((x[e] & 0x7F800000u) == 0x7F800000u);
@@ -742,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
           if (kShare == 4) odd |= __shfl_xor_sync(0xffffffffu, odd, 2);
           if (outside || odd) {
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i) st_shared_v4(at + ((c0 + i) >> 3) * Lay::BLOCK + (((c0 + i) & 7) << 4), 0u, 0u, 0u, 0u);
+            for (int i = 0; i < kChunks; ++i) st_shared_v4(at + ((c0 + i) >> 3) * block + (((c0 + i) & 7) << 4), 0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
           // Every second or fourth lane's bit, close up.
@@ -1064,20 +1077,13 @@ cudaError_t launch_attend_pages(const PageAttention& a, const PagePool& pool, co
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = device_sm_count(dev, &sms);
   if (e != cudaSuccess) return e;
-  const int G = a.Hq / a.Hkv, D = a.D, page = 1 << pool.log_page;
+  const int G = a.Hq / a.Hkv, D = a.D;
   PageAttnParams p;
   std::memset(&p, 0, sizeof(p));
-  {
-    const uint64_t u = 2, dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(G), static_cast<uint64_t>(a.Hkv), static_cast<uint64_t>(a.N)};
-    const uint64_t strides[3] = {D * u, D * u * G, D * u * a.Hq};
-    const uint32_t box[4] = {64, static_cast<uint32_t>(G), 1, static_cast<uint32_t>(kBM / G)};
-    if (!encode_tmap_4d(&p.tm_q, a.q, dims, strides, box)) return cudaErrorInvalidValue;
-    const uint64_t pd[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.Hkv), static_cast<uint64_t>(page), static_cast<uint64_t>(pool.n_pages)};
-    const uint64_t ps[3] = {D * u, D * u * a.Hkv, D * u * a.Hkv * page};
-    const int keys = D == 256 ? Layout<256>::BN : Layout<128>::BN;
-    const uint32_t pb[4] = {64, 1, static_cast<uint32_t>(page < keys ? page : keys), 1};
-    if (!encode_tmap_4d(&p.tm_k, pool.k, pd, ps, pb) || !encode_tmap_4d(&p.tm_v, pool.v, pd, ps, pb)) return cudaErrorInvalidValue;
-  }
+  const int keys = D == 256 ? Layout<256>::BN : Layout<128>::BN;
+  if (!encode_query_map(&p.tm_q, a.q, a.N, a.Hq, a.Hkv, D, kBM) || !encode_page_map(&p.tm_k, pool.k, pool, a.Hkv, D, keys) ||
+      !encode_page_map(&p.tm_v, pool.v, pool, a.Hkv, D, keys))
+    return cudaErrorInvalidValue;
   if (al) {
     p.k_tiles[0] = static_cast<const uint8_t*>(al->pin_k_tiles);
     p.k_tiles[1] = static_cast<const uint8_t*>(al->win_k_tiles);

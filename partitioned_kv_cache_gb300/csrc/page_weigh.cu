@@ -9,14 +9,19 @@
 // The keys are the M side: scores^T = K Q^T puts one key on each softmax thread,
 // whose sum over the rows (the columns of its lane) needs no exchange and no
 // atomics: the same inputs give the same bits.  A unit is (stream, K/V head, 128
-// keys); it reads its keys once and all row tiles (64 rows: tokens x heads of the
-// group) that see one of them.  CTAs take units in turn, grid apart, since later
-// keys are seen by fewer rows.  One token per stream is bound by the keys' bytes;
+// keys); it reads its keys once and all row tiles (128 rows: tokens x heads of the
+// group) that see one of them.  Later keys are seen by fewer rows, so CTAs share
+// the units by their number of row tiles, summed in closed form.  One token per stream is bound by the keys' bytes;
 // a chunk by Q K^T (both operands from shared memory) and, at D = 64, by the
 // exponentials.
 //
-// Warps (224 threads): 0 = copies (lane 0 keys, lane 1 queries), 1 = tensor
-// memory and K Q^T, 2..5 = exponentials and sums, 6 = the rows' lse.
+// K is the A operand from tensor memory, put there a unit ahead, so that a K slot
+// is free again at once and single tokens' calls keep the memory busy.  What a
+// tile costs the issuing warp, its barriers and products, is some 700 cycles: row
+// tiles of 128 halve their number.
+//
+// Warps: 0 = copies of keys, 1 = tensor memory and K Q^T, 2 = the rows' lse, 3 =
+// copies of queries, from 4 on = exponentials and sums.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -32,35 +37,48 @@
 namespace rx {
 namespace {
 
-constexpr int kThreads = 224;
 constexpr int kKeys = 128;   // of a unit
-constexpr int kRows = 64;    // of a row tile
-constexpr int kBufs = 4;     // score tiles in tensor memory
+constexpr int kRows = 128;   // of a row tile
+constexpr int kLoaders = 2;  // of them bring the keys into tensor memory
+constexpr int kUnitCost = 4; // of a unit beside its row tiles, in row tiles
 
 template <int D>
 struct Layout {
   static constexpr int KB = D / 64;
-  static constexpr int CTAS = D == 256 ? 1 : 2;
-  static constexpr int K_BLOCK = kKeys * 128, Q_BLOCK = kRows * 128;
-  static constexpr int K_TILE = KB * K_BLOCK, Q_TILE = KB * Q_BLOCK;
-  static constexpr int NK = D == 64 ? 3 : 2, NQ = D == 64 ? 4 : 2;
+  static constexpr int Q_BLOCK = kRows * 128;
+  static constexpr int K_TILE = KB * kKeys * 128, Q_TILE = KB * Q_BLOCK;
+  // Queries come from L2, some 1.5 us away: their ring holds what fits.
+  static constexpr int NK = D == 256 ? 1 : 2, NQ = D == 256 ? 2 : D == 128 ? 4 : 8;
+  // Groups of four warps that take the row tiles in turn, each with a score tile of
+  // its own in tensor memory.
+  static constexpr int GROUPS = D == 256 ? 2 : 3;
+  static constexpr int THREADS = 128 + 128 * GROUPS;
   static constexpr int OFF_K = 0;
   static constexpr int OFF_Q = NK * K_TILE;
   static constexpr int OFF_BAR = OFF_Q + NQ * Q_TILE;
-  static constexpr int OFF_LSE = OFF_BAR + 32 * 8;              // [4][64] floats
-  static constexpr int OFF_MISC = OFF_LSE + 4 * kRows * 4;
-  static constexpr int OFF_BEFORE = OFF_MISC + 32;              // long long [B + 1]
-  static constexpr int BYTES = OFF_BEFORE;
-  static_assert(CTAS * (BYTES + 1024 + 1024 + (kMaxPagedStreams + 1) * 8) <= 233472, "shared memory");
+  static constexpr int OFF_MISC = OFF_BAR + 48 * 8;
+  static constexpr int OFF_LSE = OFF_MISC + 32;                 // [GROUPS][128] floats
+  static constexpr int OFF_SUM = OFF_LSE + GROUPS * kRows * 4;   // [groups - 1][128] floats
+  static constexpr int OFF_STREAM = OFF_SUM + (GROUPS - 1) * kKeys * 4;   // StreamInfo [B]
+  static constexpr int OFF_BEFORE = OFF_STREAM + kMaxPagedStreams * 16;   // long long [B + 1]
+  static constexpr int BYTES = OFF_BEFORE + (kMaxPagedStreams + 1) * 8;
+  // Tensor memory: K of two units (the A operand, bf16 pairs), score tiles.
+  static constexpr int T_S = D;
+  static_assert(T_S + GROUPS * kRows <= 512, "tensor memory");
+  static_assert(BYTES + 1024 <= 232448, "shared memory");
 };
 
-// Barriers: K full / empty [3], Q full / empty [4], scores full / empty [4],
-// lse full / empty [4], drained.
-enum : int { B_KF = 0, B_KE = 3, B_QF = 6, B_QE = 10, B_SF = 14, B_SE = 18, B_LF = 22, B_LE = 26, B_DRAIN = 30 };
+// Barriers: K full / empty (shared memory) [2], Q full / empty [8], K in tensor
+// memory [2], a unit's products done [2], scores full / read [4], lse full /
+// read [4], the groups' sums there / taken, drained.
+enum : int {
+  B_KF = 0, B_KE = 2, B_QF = 4, B_QE = 12, B_KT = 20, B_KD = 22, B_SF = 24, B_SR = 28, B_LF = 32, B_LR = 36, B_UF = 40,
+  B_UR = 41, B_DRAIN = 42, B_COUNT = 43
+};
 
 struct WeighParams {
-  CUtensorMap tm_k;   // (D, Hkv, page, n_pages), box (64, 1, min(page, 128), 1)
-  CUtensorMap tm_q;   // (D, G, Hkv, N), box (64, min(G, 64), 1, max(1, 64 / G))
+  CUtensorMap tm_k;   // a page's keys, 128 at most (encode_page_map)
+  CUtensorMap tm_q;   // 128 query rows (encode_query_map)
   PagePool pool;
   const float* lse;
   const int* q_start;
@@ -72,42 +90,142 @@ struct WeighParams {
   float scale_log2;
 };
 
-// One unit: keys [k0, k0 + 128) of a stream, row tiles [r0, r1).
-struct Unit {
-  int b, h, k0, q0, n, len, prefix, x0, r0, r1;
+struct StreamInfo {
+  int q0, n, len, prefix;
 };
 
-__device__ __forceinline__ int new_tokens(const WeighParams& p, int b, int* q0) {
-  *q0 = max(0, min(__ldg(p.q_start + b), p.N));
-  return max(0, max(0, min(__ldg(p.q_start + b + 1), p.N)) - *q0);
-}
-
-__device__ __forceinline__ Unit unit_at(const WeighParams& p, const long long* before, long long u) {
-  int lo = 0, hi = p.pool.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (before[mid] <= u) lo = mid;
-    else hi = mid - 1;
+// The units of one stream and head, 128 keys each, and their cost: the row tiles
+// that see one of the keys, and kUnitCost for bringing the keys.
+struct StreamUnits {
+  StreamInfo s;
+  int log_g;
+  __device__ __forceinline__ int blocks() const { return s.n > 0 ? (s.len + kKeys - 1) / kKeys : 0; }
+  __device__ __forceinline__ int row_tiles() const { return ((s.n << log_g) + kRows - 1) / kRows; }
+  // First row tile that sees a key of block kb: tokens from 128 kb - (len - n) on,
+  // and all of them below the prefix.
+  __device__ __forceinline__ int first(int kb) const {
+    const int k0 = kb * kKeys;
+    return k0 < s.prefix ? 0 : (max(0, k0 - (s.len - s.n)) << log_g) / kRows;
   }
-  Unit x;
-  x.b = lo;
-  x.n = new_tokens(p, lo, &x.q0);
-  x.len = held_keys(p.pool, p.len, lo);
-  x.prefix = p.prefix ? max(0, min(__ldg(p.prefix + lo), x.len)) : 0;
-  const int blocks = (x.len + kKeys - 1) / kKeys;
-  const long long o = u - before[lo];
-  x.h = static_cast<int>(o / blocks);
-  x.k0 = static_cast<int>(o - static_cast<long long>(x.h) * blocks) * kKeys;
-  x.x0 = x.len - x.n;
-  const int first = x.k0 < x.prefix ? 0 : max(0, x.k0 - x.x0);   // first token that sees one of the keys
-  x.r0 = (first << p.log_g) / kRows;
-  x.r1 = ((x.n << p.log_g) + kRows - 1) / kRows;
-  return x;
+  // Cost of blocks [0, kb): first() is 0 up to a block and then grows by G a block.
+  __device__ __forceinline__ long long cost(int kb) const {
+    const int x0 = s.len - s.n;
+    const int flat = max((max(s.prefix, 0) + kKeys - 1) / kKeys, max(0, x0) / kKeys + 1);   // blocks before it start at 0
+    long long sum = static_cast<long long>(kb) * (row_tiles() + kUnitCost);
+    if (kb > flat || (x0 < 0 && kb > 0)) {
+      const int from = x0 < 0 ? min(kb, (max(s.prefix, 0) + kKeys - 1) / kKeys) : flat;
+      // floor((128 i - x0) G / 128) = G i + floor(-x0 G / 128)
+      const long long base = -((static_cast<long long>(x0) << log_g) + kRows - 1 >> 7), step = 1ll << log_g, m = kb - from;
+      sum -= m * base + step * (static_cast<long long>(from) + kb - 1) * m / 2;
+    }
+    return sum;
+  }
+};
+
+// One unit: keys [k0, k0 + 128) of a stream, row tiles [r0, r1).
+struct Unit {
+  StreamInfo s;
+  int b, h, k0, x0, r0, r1;
+};
+
+// A CTA's units: those whose cost begins in its share of the whole.
+struct Units {
+  const StreamInfo* info;
+  const long long* before;   // cost before stream b [B + 1]
+  int B, Hkv, log_g;
+  long long left;            // cost that may still begin here
+
+  __device__ __forceinline__ bool begin(Unit* x) {
+    const long long total = before[B];
+    const long long c0 = total * blockIdx.x / gridDim.x, c1 = total * (blockIdx.x + 1) / gridDim.x;
+    if (c0 >= c1) return false;
+    int lo = 0, hi = B - 1;
+    while (lo < hi) {   // the last stream that begins at or before c0
+      const int mid = (lo + hi + 1) >> 1;
+      if (before[mid] <= c0) lo = mid;
+      else hi = mid - 1;
+    }
+    x->b = lo;
+    const StreamUnits su{info[lo], log_g};
+    const int blocks = su.blocks();
+    const long long each = su.cost(blocks), o = c0 - before[lo];
+    x->h = static_cast<int>(o / each);
+    const long long r = o - x->h * each;
+    int b0 = 0, b1 = blocks;   // the first block that begins at or after r
+    while (b0 < b1) {
+      const int mid = (b0 + b1) >> 1;
+      if (su.cost(mid) >= r) b1 = mid;
+      else b0 = mid + 1;
+    }
+    left = c1 - c0 - (su.cost(b0) - r);
+    x->k0 = b0 * kKeys;
+    x->s = su.s;
+    return settle(x);
+  }
+  __device__ __forceinline__ bool next(Unit* x) {
+    left -= x->r1 - x->r0 + kUnitCost;
+    x->k0 += kKeys;
+    return settle(x);
+  }
+  // Past the end of a head or a stream to the next one with units.
+  __device__ __forceinline__ bool settle(Unit* x) {
+    if (left <= 0) return false;
+    if (x->k0 >= x->s.len) {
+      x->k0 = 0;
+      if (++x->h == Hkv) {
+        x->h = 0;
+        do {
+          if (++x->b >= B) return false;
+          x->s = info[x->b];
+        } while (x->s.n == 0 || x->s.len == 0);
+      }
+    }
+    const StreamUnits su{x->s, log_g};
+    x->x0 = x->s.len - x->s.n;
+    x->r0 = su.first(x->k0 / kKeys);
+    x->r1 = su.row_tiles();
+    return true;
+  }
+};
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(one));
+  return one != 0;
 }
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   const bool ok = mbar_wait(bar, parity, abort);
   return __all_sync(0xffffffffu, ok);
+}
+
+// D += A B^T with the A operand in tensor memory.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Pairs of fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
 }
 
 // A ring position: slot and how often the ring has gone round.
@@ -122,30 +240,36 @@ struct Turn {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, Layout<D>::CTAS) page_weigh_kernel(const __grid_constant__ WeighParams p) {
+__global__ void __launch_bounds__(Layout<D>::THREADS, 1) page_weigh_kernel(const __grid_constant__ WeighParams p) {
   using Lay = Layout<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
   const uint32_t sK = base + Lay::OFF_K, sQ = base + Lay::OFF_Q, sBar = base + Lay::OFF_BAR;
-  float* s_lse = reinterpret_cast<float*>(gbase + Lay::OFF_LSE);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + Lay::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + Lay::OFF_MISC + 4);
+  float* s_lse = reinterpret_cast<float*>(gbase + Lay::OFF_LSE);
+  float* s_sum = reinterpret_cast<float*>(gbase + Lay::OFF_SUM);
+  StreamInfo* info = reinterpret_cast<StreamInfo*>(gbase + Lay::OFF_STREAM);
   long long* before = reinterpret_cast<long long*>(gbase + Lay::OFF_BEFORE);
   auto BAR = [&](int i) { return sBar + 8u * static_cast<uint32_t>(i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 31; ++i) {
-      const int count = (i >= B_SE && i < B_SE + 4) || (i >= B_LE && i < B_LE + 4) ? 128 : i >= B_LF && i < B_LF + 4 ? 32 : 1;
+    for (int i = 0; i < B_COUNT; ++i) {
+      int count = 1;
+      if ((i >= B_KE && i < B_QF) || (i >= B_KT && i < B_KD)) count = 128 * kLoaders;
+      if ((i >= B_SR && i < B_LF) || (i >= B_LR && i < B_UF) || i == B_UR) count = 128;   // one group
+      if (i == B_UF) count = 128 * (Lay::GROUPS - 1);
+      if (i >= B_LF && i < B_LR) count = 32;
       mbar_init(BAR(i), count);
     }
     *abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), kBufs * kRows);
+    tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -153,10 +277,15 @@ __global__ void __launch_bounds__(kThreads, Layout<D>::CTAS) page_weigh_kernel(c
   tc_fence_after();
   grid_dependency_wait();
   grid_launch_dependents();
-  for (int b = threadIdx.x; b < p.pool.B; b += kThreads) {
-    int q0;
-    const int n = new_tokens(p, b, &q0);   // streams without new tokens have no work
-    before[b + 1] = n > 0 ? static_cast<long long>(p.Hkv) * ((held_keys(p.pool, p.len, b) + kKeys - 1) / kKeys) : 0;
+  for (int b = threadIdx.x; b < p.pool.B; b += Lay::THREADS) {
+    StreamInfo s;
+    s.q0 = max(0, min(__ldg(p.q_start + b), p.N));
+    s.n = max(0, max(0, min(__ldg(p.q_start + b + 1), p.N)) - s.q0);
+    s.len = held_keys(p.pool, p.len, b);
+    s.prefix = p.prefix ? max(0, min(__ldg(p.prefix + b), s.len)) : 0;
+    info[b] = s;
+    const StreamUnits su{s, p.log_g};   // (streams without new tokens have none)
+    before[b + 1] = p.Hkv * su.cost(su.blocks());
   }
   __syncthreads();
   if (warp == 0) {
@@ -174,178 +303,254 @@ __global__ void __launch_bounds__(kThreads, Layout<D>::CTAS) page_weigh_kernel(c
     if (lane == 0) before[0] = 0;
   }
   __syncthreads();
-  const long long units = before[p.pool.B];
   const uint32_t tmem = *tmem_slot;
   const int lp = p.pool.log_page;
   const int box = lp < 7 ? 1 << lp : kKeys;
-  const bool some = static_cast<long long>(blockIdx.x) < units;
+  Units units{info, before, p.pool.B, p.Hkv, p.log_g, 0};
+  Unit x;
+  const bool some = units.begin(&x);
 
   if (some && warp == 0) {
-    if (lane == 0) {
-      // ---------------------------------------------------------- keys
-      Turn at;
-      int issued = 0;
-      for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-        const Unit x = unit_at(p, before, u);
-        const int* table = p.pool.table + static_cast<long long>(x.b) * p.pool.max_pages;
-        int pg[8];
-        uint32_t named = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int place = x.k0 + i * box;
-          pg[i] = i * box < kKeys && place < x.len ? __ldg(table + (place >> lp)) : -1;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) named += static_cast<unsigned int>(pg[i]) < static_cast<unsigned int>(p.pool.n_pages);
-        if (at.round > 0 && !mbar_wait(BAR(B_KE + at.slot), (at.round - 1) & 1, abort_flag)) break;
-        const uint32_t bar = BAR(B_KF + at.slot);
-        mbar_arrive_expect_tx(bar, named * box * (D * 2));
-        const int row = lp > 7 ? x.k0 & ((1 << lp) - 1) : 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (static_cast<unsigned int>(pg[i]) >= static_cast<unsigned int>(p.pool.n_pages)) continue;
-          for (int kb = 0; kb < Lay::KB; ++kb)
-            tma_load_4d(sK + at.slot * Lay::K_TILE + kb * Lay::K_BLOCK + i * box * 128, &p.tm_k, kb * 64, x.h, row, pg[i], bar);
-        }
-        ++issued;
-        at.step(Lay::NK);
+    // ---------------------------------------------------------- keys
+    // The lanes hold the pages of a tile; one issues (copies by several lanes of a
+    // warp go one after the other, some 250 cycles each).
+    const bool leader = elect_one();
+    const int pages = lp < 7 ? kKeys >> lp : 1;   // of a tile
+    auto entry = [&]() {
+      const int place = x.k0 + lane * box;
+      return lane < pages && place < x.s.len ? __ldg(p.pool.table + static_cast<long long>(x.b) * p.pool.max_pages + (place >> lp)) : -1;
+    };
+    Turn at;
+    int issued = 0;
+    bool more = true;
+    int pg = entry();
+    while (more) {
+      const int h = x.h, row = lp > 7 ? x.k0 & ((1 << lp) - 1) : 0, page = pg;
+      more = units.next(&x);
+      if (more) pg = entry();   // the next unit's, on its way during the wait
+      if (at.round > 0 && !warp_wait(BAR(B_KE + at.slot), (at.round - 1) & 1, abort_flag)) break;
+      const uint32_t bar = BAR(B_KF + at.slot);
+      const uint32_t named = __ballot_sync(0xffffffffu, static_cast<unsigned int>(page) < static_cast<unsigned int>(p.pool.n_pages));
+      if (leader) mbar_arrive_expect_tx(bar, __popc(named) * box * (D * 2));
+      for (int i = 0; i < pages; ++i) {
+        const int g = __shfl_sync(0xffffffffu, page, i);
+        if (leader && (named >> i & 1))
+          tma_load_5d(sK + at.slot * Lay::K_TILE + i * box * Lay::KB * 128, &p.tm_k, 0, 0, h * Lay::KB, row >> 3, g, bar);
       }
-      volatile int no_abort = 0;
-      for (int i = max(0, issued - Lay::NK); i < issued; ++i) mbar_wait(BAR(B_KF + i % Lay::NK), (i / Lay::NK) & 1, &no_abort);
-    } else if (lane == 1) {
-      // ---------------------------------------------------------- queries
-      Turn at;
-      int issued = 0;
-      bool ok = true;
-      for (long long u = blockIdx.x; ok && u < units; u += gridDim.x) {
-        const Unit x = unit_at(p, before, u);
-        for (int r = x.r0; r < x.r1; ++r) {
-          if (at.round > 0 && !mbar_wait(BAR(B_QE + at.slot), (at.round - 1) & 1, abort_flag)) { ok = false; break; }
-          const uint32_t bar = BAR(B_QF + at.slot);
-          mbar_arrive_expect_tx(bar, Lay::Q_TILE);
-          const int row = r * kRows;
-          for (int kb = 0; kb < Lay::KB; ++kb)
-            tma_load_4d(sQ + at.slot * Lay::Q_TILE + kb * Lay::Q_BLOCK, &p.tm_q, kb * 64, row & ((1 << p.log_g) - 1), x.h,
-                        x.q0 + (row >> p.log_g), bar);
-          ++issued;
-          at.step(Lay::NQ);
-        }
-      }
-      volatile int no_abort = 0;
-      for (int i = max(0, issued - Lay::NQ); i < issued; ++i) mbar_wait(BAR(B_QF + i % Lay::NQ), (i / Lay::NQ) & 1, &no_abort);
+      __syncwarp();
+      ++issued;
+      at.step(Lay::NK);
     }
+    volatile int no_abort = 0;
+    for (int n = max(0, issued - Lay::NK); n < issued; ++n) mbar_wait(BAR(B_KF + n % Lay::NK), (n / Lay::NK) & 1, &no_abort);
+  } else if (some && warp == 3) {
+    // ---------------------------------------------------------- queries
+    const bool leader = elect_one();
+    Turn at;
+    int issued = 0;
+    bool ok = true;
+    do {
+      for (int r = x.r0; r < x.r1; ++r) {
+        if (at.round > 0 && !warp_wait(BAR(B_QE + at.slot), (at.round - 1) & 1, abort_flag)) { ok = false; break; }
+        const uint32_t bar = BAR(B_QF + at.slot);
+        const int row = r * kRows, head = row & ((1 << p.log_g) - 1), token = x.s.q0 + (row >> p.log_g);
+        if (leader) {
+          mbar_arrive_expect_tx(bar, Lay::Q_TILE);
+          tma_load_4d(sQ + at.slot * Lay::Q_TILE, &p.tm_q, 0, head, token, (x.h << p.log_g) * Lay::KB, bar);
+        }
+        __syncwarp();
+        ++issued;
+        at.step(Lay::NQ);
+      }
+    } while (ok && units.next(&x));
+    volatile int no_abort = 0;
+    for (int n = max(0, issued - Lay::NQ); n < issued; ++n) mbar_wait(BAR(B_QF + n % Lay::NQ), (n / Lay::NQ) & 1, &no_abort);
   } else if (some && warp == 1) {
     // ------------------------------------------------------------ K Q^T
-    if (lane == 0) {
-      constexpr uint32_t kIdesc = idesc_bf16_f32(kKeys, kRows, false, false);
-      Turn k, q, s;
-      bool ok = true;
-      for (long long u = blockIdx.x; ok && u < units; u += gridDim.x) {
-        const Unit x = unit_at(p, before, u);
-        if (!mbar_wait(BAR(B_KF + k.slot), k.round & 1, abort_flag)) break;
-        for (int r = x.r0; r < x.r1; ++r) {
-          if (!mbar_wait(BAR(B_QF + q.slot), q.round & 1, abort_flag) ||
-              (s.round > 0 && !mbar_wait(BAR(B_SE + s.slot), (s.round - 1) & 1, abort_flag))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+    constexpr uint32_t kIdesc = idesc_bf16_f32(kKeys, kRows, false, false);
+    const bool leader = elect_one();
+    Turn q, s;
+    int v = 0;   // units so far
+    bool ok = true;
+    do {
+      ok = warp_wait(BAR(B_KT + (v & 1)), (v >> 1) & 1, abort_flag);
+      for (int r = x.r0; ok && r < x.r1; ++r) {
+        if (!warp_wait(BAR(B_QF + q.slot), q.round & 1, abort_flag)) { ok = false; break; }
+        if (s.round > 0 && !warp_wait(BAR(B_SR + s.slot), (s.round - 1) & 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t desc = sdesc_sw128(sQ + q.slot * Lay::Q_TILE, 16, 1024);
+        if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t kb = kk >> 2, ko = (kk & 3) * 32;
-            umma_bf16(tmem + s.slot * kRows, sdesc_sw128(sK + k.slot * Lay::K_TILE + kb * Lay::K_BLOCK + ko, 16, 1024),
-                      sdesc_sw128(sQ + q.slot * Lay::Q_TILE + kb * Lay::Q_BLOCK + ko, 16, 1024), kIdesc, kk > 0 ? 1u : 0u);
-          }
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16_ts(tmem + Lay::T_S + s.slot * kRows, tmem + (v & 1) * (D / 2) + kk * 8,
+                         desc + (((kk >> 2) * Lay::Q_BLOCK + (kk & 3) * 32) >> 4), kIdesc, kk > 0 ? 1u : 0u);
           umma_commit(BAR(B_QE + q.slot));
           umma_commit(BAR(B_SF + s.slot));
-          q.step(Lay::NQ);
-          s.step(kBufs);
+          if (r == x.r1 - 1) umma_commit(BAR(B_KD + (v & 1)));
         }
-        if (ok) umma_commit(BAR(B_KE + k.slot));
-        k.step(Lay::NK);
+        __syncwarp();
+        q.step(Lay::NQ);
+        s.step(Lay::GROUPS);
       }
-      umma_commit(BAR(B_DRAIN));
-      volatile int no_abort = 0;
-      mbar_wait(BAR(B_DRAIN), 0, &no_abort);
-    }
-  } else if (some && warp == 6) {
-    // ------------------------------------------------------------ lse, in log2 units
+      ++v;
+    } while (ok && units.next(&x));
+    if (leader) umma_commit(BAR(B_DRAIN));
+    volatile int no_abort = 0;
+    mbar_wait(BAR(B_DRAIN), 0, &no_abort);
+  } else if (some && warp == 2) {
+    // ------------------------------------------------------------ lse, in log2 units, negative
     Turn at;
     bool ok = true;
-    for (long long u = blockIdx.x; ok && u < units; u += gridDim.x) {
-      const Unit x = unit_at(p, before, u);
-      const int rows = x.n << p.log_g, gm = (1 << p.log_g) - 1;
-      for (int r = x.r0; r < x.r1; ++r) {
-        if (at.round > 0 && !warp_wait(BAR(B_LE + at.slot), (at.round - 1) & 1, abort_flag)) { ok = false; break; }
+    const int gm = (1 << p.log_g) - 1;
+    do {
+      const int rows = x.s.n << p.log_g;
+      const float* src = p.lse + static_cast<size_t>(x.s.q0) * p.Hq + (x.h << p.log_g);
+      auto value = [&](int r, int i) {
+        const int row = r * kRows + 4 * lane + i;
+        return r < x.r1 && row < rows ? __ldg(src + static_cast<size_t>(row >> p.log_g) * p.Hq + (row & gm)) : INFINITY;
+      };
+      // Two tiles' values at a time, the next two on their way to here.
+      constexpr int kAhead = 2;
+      float v[kAhead][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = r * kRows + i * 32 + lane;
-          float v = INFINITY;   // rows behind the stream's, and rows that saw nothing, weigh nothing
-          if (row < rows) {
-            v = __ldg(p.lse + static_cast<size_t>(x.q0 + (row >> p.log_g)) * p.Hq + (x.h << p.log_g) + (row & gm));
-            if (v == -INFINITY) v = INFINITY;
-          }
-          s_lse[at.slot * kRows + i * 32 + lane] = v * 1.44269504088896341f;
+      for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[i][e] = value(x.r0 + i, e);
+      for (int r0 = x.r0; ok && r0 < x.r1; r0 += kAhead) {
+        float n[kAhead][4];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) n[i][e] = value(r0 + kAhead + i, e);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (!ok || r0 + i >= x.r1) break;
+          if (at.round > 0 && !warp_wait(BAR(B_LR + at.slot), (at.round - 1) & 1, abort_flag)) { ok = false; break; }
+          // Rows behind the stream's, and rows that saw nothing, weigh nothing.
+          float4 f;
+          f.x = (v[i][0] == -INFINITY ? INFINITY : v[i][0]) * -1.44269504088896341f;
+          f.y = (v[i][1] == -INFINITY ? INFINITY : v[i][1]) * -1.44269504088896341f;
+          f.z = (v[i][2] == -INFINITY ? INFINITY : v[i][2]) * -1.44269504088896341f;
+          f.w = (v[i][3] == -INFINITY ? INFINITY : v[i][3]) * -1.44269504088896341f;
+          reinterpret_cast<float4*>(s_lse + at.slot * kRows)[lane] = f;
+          mbar_arrive(BAR(B_LF + at.slot));
+          at.step(Lay::GROUPS);
         }
-        mbar_arrive(BAR(B_LF + at.slot));
-        at.step(4);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[i][e] = n[i][e];
       }
-    }
-  } else if (some) {
+    } while (ok && units.next(&x));
+  } else if (some && warp >= 4) {
     // ------------------------------------------------------------ exponentials
-    const int quarter = warp & 3, key = quarter * 32 + lane;
+    // The groups take the row tiles in turn, so that the steps of one run beside the
+    // others'; their sums are added, in the groups' order, at the unit's end.
+    const int quarter = warp & 3, key = quarter * 32 + lane, group = (warp - 4) >> 2;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    Turn at;   // of score and lse tiles, four of each
+    const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
+    Turn k;
     bool ok = true;
-    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-      const Unit x = unit_at(p, before, u);
-      const int j = x.k0 + key;
-      const long long row = j < x.len ? pool_row(p.pool, x.b, j) : -1;
+    // Unit v's keys from shared into tensor memory: the first two groups, half of a
+    // key's values each.
+    auto load_k = [&](int v) {
+      if (group >= kLoaders) return true;
+      if (!warp_wait(BAR(B_KF + k.slot), k.round & 1, abort_flag)) return false;
+      if (v >= 2 && !warp_wait(BAR(B_KD + (v & 1)), ((v >> 1) - 1) & 1, abort_flag)) return false;
+      tc_fence_after();
+      constexpr int kChunks = D / 16;
+#pragma unroll
+      for (int c0 = 0; c0 < kChunks; c0 += 4) {
+        uint32_t y[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = group * kChunks + c0 + i;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(y[4 * i]), "=r"(y[4 * i + 1]), "=r"(y[4 * i + 2]), "=r"(y[4 * i + 3])
+                       : "r"(sK + k.slot * Lay::K_TILE + ((key >> 3) * Lay::KB + (c >> 3)) * 1024 + (key & 7) * 128 + (((c & 7) ^ (key & 7)) << 4)));
+        }
+        tmem_st16(tmem + (v & 1) * (D / 2) + (group * kChunks + c0) * 4 + lane_off, y);
+      }
+      tc_fence_before();
+      mbar_arrive(BAR(B_KT + (v & 1)));
+      mbar_arrive(BAR(B_KE + k.slot));
+      k.step(Lay::NK);
+      return true;
+    };
+    ok = load_k(0);
+    int v = 0, tile = 0;
+    bool more = true;
+    while (more) {
+      const Unit now = x;
+      more = units.next(&x);
+      const int j = now.k0 + key;
+      const long long row = j < now.s.len ? pool_row(p.pool, now.b, j) : -1;
+      const size_t place = static_cast<size_t>(row < 0 ? 0 : row) * p.Hkv + now.h;
+      const float old = group == 0 && row >= 0 && p.decay != 0.f ? p.pool.weight[place] : 0.f;
+      if (ok && more) ok = load_k(v + 1);   // the next unit's keys, ahead of this one's tiles
       // First row that sees the key.
-      const int first = j < x.prefix ? 0 : max(0, j - x.x0) << p.log_g;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int r = x.r0; ok && r < x.r1; ++r) {
-        if (!warp_wait(BAR(B_SF + at.slot), at.round & 1, abort_flag) ||
-            !warp_wait(BAR(B_LF + at.slot), at.round & 1, abort_flag)) {
+      const int first = j < now.s.prefix ? 0 : max(0, j - now.x0) << p.log_g;
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      for (int r = now.r0; r < now.r1; ++r, ++tile) {
+        if (!ok || tile % Lay::GROUPS != group) continue;
+        const int slot = tile % Lay::GROUPS, round = tile / Lay::GROUPS;
+        if (!warp_wait(BAR(B_SF + slot), round & 1, abort_flag) || !warp_wait(BAR(B_LF + slot), round & 1, abort_flag)) {
           ok = false;
-          break;
+          continue;
         }
         tc_fence_after();
-        float s[kRows];
-        tmem_ld64(tmem + at.slot * kRows + lane_off, s);
-        tc_fence_before();
-        mbar_arrive(BAR(B_SE + at.slot));
         const int hidden = first - r * kRows;   // leading rows of the tile that do not see the key
-        if (__any_sync(0xffffffffu, hidden > 0)) {
+        const bool mask = __any_sync(0xffffffffu, hidden > 0);
+        const float4* lse = reinterpret_cast<const float4*>(s_lse + slot * kRows);
 #pragma unroll
-          for (int c = 0; c < kRows; ++c)
-            if (c < hidden) s[c] = -INFINITY;
-        }
-        const float4* lse = reinterpret_cast<const float4*>(s_lse + at.slot * kRows);
+        for (int half = 0; half < 2; ++half) {
+          const bool rows_there = r * kRows + half * 64 < (now.s.n << p.log_g);   // (a single token has few)
+          float s[64];
+          if (rows_there) tmem_ld64(tmem + Lay::T_S + slot * kRows + half * 64 + lane_off, s);
+          if (half == 1) {
+            tc_fence_before();
+            mbar_arrive(BAR(B_SR + slot));
+          }
+          if (!rows_there) continue;
+          if (mask) {
 #pragma unroll
-        for (int c = 0; c < kRows / 4; ++c) {
-          const float4 e = lse[c];
-          sum[0] += exp2f(fmaf(s[4 * c], p.scale_log2, -e.x));
-          sum[1] += exp2f(fmaf(s[4 * c + 1], p.scale_log2, -e.y));
-          sum[2] += exp2f(fmaf(s[4 * c + 2], p.scale_log2, -e.z));
-          sum[3] += exp2f(fmaf(s[4 * c + 3], p.scale_log2, -e.w));
+            for (int c = 0; c < 64; ++c)
+              if (half * 64 + c < hidden) s[c] = -INFINITY;
+          }
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float4 e = lse[half * 16 + c];
+            const float2 a = fma2(make_float2(s[4 * c], s[4 * c + 1]), scale2, make_float2(e.x, e.y));
+            const float2 b = fma2(make_float2(s[4 * c + 2], s[4 * c + 3]), scale2, make_float2(e.z, e.w));
+            sum[0] = add2(sum[0], make_float2(exp2f(a.x), exp2f(a.y)));
+            sum[1] = add2(sum[1], make_float2(exp2f(b.x), exp2f(b.y)));
+          }
         }
-        mbar_arrive(BAR(B_LE + at.slot));
-        at.step(4);
+        mbar_arrive(BAR(B_LR + slot));
       }
-      if (row >= 0) {
-        const size_t i = static_cast<size_t>(row) * p.Hkv + x.h;
-        float got = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      float got = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      if (group > 0) {
+        if (ok && v > 0) ok = warp_wait(BAR(B_UR), (v - 1) & 1, abort_flag);
+        if (ok) {
+          s_sum[(group - 1) * kKeys + key] = got;
+          mbar_arrive(BAR(B_UF));
+        }
+      } else {
+        if (ok) ok = warp_wait(BAR(B_UF), v & 1, abort_flag);
+#pragma unroll
+        for (int i = 0; i < Lay::GROUPS - 1; ++i) got += s_sum[i * kKeys + key];
         if (!ok) got = NAN;   // a wait gave up
-        p.out[i] = p.decay == 0.f ? got : fmaf(p.decay, p.pool.weight[i], got);
+        if (ok) mbar_arrive(BAR(B_UR));
+        if (row >= 0) p.out[place] = p.decay == 0.f ? got : fmaf(p.decay, old, got);
       }
+      ++v;
     }
   }
 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, kBufs * kRows);
+  if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 template <int D>
@@ -353,11 +558,10 @@ cudaError_t launch_d(const WeighParams& p, int dev, int sms, cudaStream_t s) {
   using Lay = Layout<D>;
   static std::atomic<unsigned long long> ready{0};
   cudaError_t e = once_per_device(ready, dev, [] {
-    return cudaFuncSetAttribute(page_weigh_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Lay::BYTES + 1024 + (kMaxPagedStreams + 1) * 8);
+    return cudaFuncSetAttribute(page_weigh_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::BYTES + 1024);
   });
   if (e != cudaSuccess) return e;
-  e = launch_k(page_weigh_kernel<D>, dim3(sms * Lay::CTAS), dim3(kThreads), Lay::BYTES + 1024 + (p.pool.B + 1) * 8, s, p);
+  e = launch_k(page_weigh_kernel<D>, dim3(sms), dim3(Lay::THREADS), Lay::BYTES + 1024, s, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -368,16 +572,10 @@ cudaError_t launch_weigh_pages(const PageWeights& a, const PagePool& pool, cudaS
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = device_sm_count(dev, &sms);
   if (e != cudaSuccess) return e;
-  const int G = a.Hq / a.Hkv, D = a.D, page = 1 << pool.log_page;
+  const int G = a.Hq / a.Hkv, D = a.D;
   WeighParams p;
   std::memset(&p, 0, sizeof(p));
-  const uint64_t u = 2, dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(G), static_cast<uint64_t>(a.Hkv), static_cast<uint64_t>(a.N)};
-  const uint64_t strides[3] = {D * u, D * u * G, D * u * a.Hq};
-  const uint32_t box[4] = {64, static_cast<uint32_t>(G < kRows ? G : kRows), 1, static_cast<uint32_t>(G < kRows ? kRows / G : 1)};
-  const uint64_t pd[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.Hkv), static_cast<uint64_t>(page), static_cast<uint64_t>(pool.n_pages)};
-  const uint64_t ps[3] = {D * u, D * u * a.Hkv, D * u * a.Hkv * page};
-  const uint32_t pb[4] = {64, 1, static_cast<uint32_t>(page < kKeys ? page : kKeys), 1};
-  if (!encode_tmap_4d(&p.tm_q, a.q, dims, strides, box) || !encode_tmap_4d(&p.tm_k, pool.k, pd, ps, pb))
+  if (!encode_query_map(&p.tm_q, a.q, a.N, a.Hq, a.Hkv, D, kRows) || !encode_page_map(&p.tm_k, pool.k, pool, a.Hkv, D, kKeys))
     return cudaErrorInvalidValue;
   p.pool = pool;
   p.lse = a.lse;

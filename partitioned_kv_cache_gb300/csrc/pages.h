@@ -53,6 +53,32 @@ __device__ __forceinline__ int held_keys(const PagePool& p, const int* len, int 
   return max(0, min(__ldg(len + b), pool_capacity(p)));
 }
 
+// Copies by tensor map cost the copy engine some 3 cycles for each row of 128
+// bytes and 100 to 200 each, so one copy takes all column blocks of a page's
+// tokens.  In shared memory they lie as [8 tokens][D/64 column blocks][8 rows of
+// 128 bytes, swizzled]: whatever the page's size, an operand of any number of
+// tokens has one stride between groups of 8, D/64 KB.
+inline bool encode_page_map(CUtensorMap* tm, const void* pool, const PagePool& p, int Hkv, int D, int most) {
+  const uint64_t kb = D / 64, row = static_cast<uint64_t>(Hkv) * D * 2, page = 1ull << p.log_page;
+  const uint64_t dims[5] = {64, 8, Hkv * kb, page / 8, static_cast<uint64_t>(p.n_pages)};
+  const uint64_t strides[4] = {row, 128, 8 * row, page * row};
+  const uint32_t tokens = static_cast<uint32_t>(page) < static_cast<uint32_t>(most) ? static_cast<uint32_t>(page) : static_cast<uint32_t>(most);
+  const uint32_t box[5] = {64, 8, static_cast<uint32_t>(kb), tokens / 8, 1};
+  return encode_tmap_5d(tm, pool, dims, strides, box);
+}
+
+// Query rows (token, head of the group) of packed tokens q [N][Hq][D]: a copy
+// brings `rows` of them as [D/64 column blocks][rows][128 bytes, swizzled];
+// coordinates (0, head within the group, token, first head of the group * D/64).
+inline bool encode_query_map(CUtensorMap* tm, const void* q, int N, int Hq, int Hkv, int D, int rows) {
+  const uint64_t kb = D / 64, G = Hq / Hkv;
+  const uint64_t dims[4] = {64, G, static_cast<uint64_t>(N), Hq * kb};
+  const uint64_t strides[3] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(Hq) * D * 2, 128};
+  const uint32_t g = static_cast<uint32_t>(G < static_cast<uint64_t>(rows) ? G : rows);
+  const uint32_t box[4] = {64, g, static_cast<uint32_t>(rows) / g, static_cast<uint32_t>(kb)};
+  return encode_tmap_4d(tm, q, dims, strides, box);
+}
+
 constexpr int kMaxAxes = 4;
 
 struct HeadRotation {

@@ -57,28 +57,38 @@ __device__ __forceinline__ unsigned long long turn_fraction(float freq) {
   return static_cast<unsigned long long>((t - floor(t)) * 18446744073709551616.0);
 }
 
-// A CTA takes TB tokens at a time.  D/8 lanes hold a head, eight values each;
-// their cosines and sines are computed once per token into shared memory and
-// serve all its heads.  Up to kFlight heads of a lane group are loaded before
-// the first is worked on.
+// A CTA takes TB tokens at a time; the pairs' cosines and sines are computed once
+// per token into shared memory and serve all its heads.  D/16 lanes hold a head,
+// 16 values each as two chunks of eight, R/16 chunks apart: in half pairs a lane
+// then has both values of its pairs and nothing is exchanged but the norm's sum.
+// (With eight values a lane and the partners fetched from other lanes
+// rotate_prompts took 129 us; with two groups of four, whose loads are 8 bytes
+// wide, 192.)  A lane asks for kFlight heads at a time, the first of them before
+// the angles are computed.  Bound by memory: see the figures at launch_d.
 template <int D, int TB>
 __global__ void __launch_bounds__(kThreads) rotate_heads_kernel(const __grid_constant__ RotateParams p) {
-  constexpr int L = D / 8;
+  constexpr int L = D / 16;              // lanes of a head
+  constexpr int kChunks = D / 8;         // 16-byte chunks of a head
   constexpr int kGroups = kThreads / L;
-  constexpr int kFlight = 4;
-  __shared__ float2 s_turn[TB * (D / 2)];            // (cos, sin) of every pair
+  constexpr int kFlight = 2;
+  __shared__ __align__(16) float2 s_turn[TB * (D / 2)];   // (cos, sin) of every pair
+  __shared__ __align__(16) float s_w[2][D];               // norm weights of queries and keys
   __shared__ unsigned long long s_freq[D / 2];
-  __shared__ float s_w[2][D];
   __shared__ int s_stream[TB];
   __shared__ long long s_row[TB];                    // pool row of the token's key and value, -1: dropped
   const int Hq = p.r.Hq, Hkv = p.r.Hkv, H = Hq + 2 * Hkv, pairs = p.r.pairs;
-  const bool paged = p.k == nullptr;
+  const bool paged = p.k == nullptr, adjacent = p.r.adjacent != 0;
+  const int sub = threadIdx.x % L, group = threadIdx.x / L;
+  const int half = pairs / 8;            // chunks of the first halves
+  const bool turned = sub < half;
+  const int c0 = turned ? sub : 2 * half + 2 * (sub - half), c1 = turned ? sub + half : c0 + 1;
+  const bool norm_q = p.r.q_weight != nullptr, norm_k = p.r.k_weight != nullptr;
   grid_dependency_wait();
   grid_launch_dependents();
-  for (int i = threadIdx.x; i < pairs; i += kThreads) s_freq[i] = turn_fraction(p.r.freq[i]);
+  for (int i = threadIdx.x; i < pairs; i += kThreads) s_freq[i] = turn_fraction(__ldg(p.r.freq + i));
   for (int i = threadIdx.x; i < D; i += kThreads) {
-    if (p.r.q_weight) s_w[0][i] = p.r.q_weight[i];
-    if (p.r.k_weight) s_w[1][i] = p.r.k_weight[i];
+    if (norm_q) s_w[0][i] = __ldg(p.r.q_weight + i);
+    if (norm_k) s_w[1][i] = __ldg(p.r.k_weight + i);
   }
   if (paged && p.new_len) {
     for (int b = blockIdx.x * kThreads + threadIdx.x; b < p.pool.B; b += gridDim.x * kThreads) {
@@ -87,14 +97,29 @@ __global__ void __launch_bounds__(kThreads) rotate_heads_kernel(const __grid_con
       p.new_len[b] = len < 0 || len > cap ? len : len + min(max(0, s1 - s0), cap - len);
     }
   }
-  const int sub = threadIdx.x % L, group = threadIdx.x / L;
-  // Half pairs: the lane that holds the other halves of this lane's pairs.
-  const int hl = pairs / 8;                                    // lanes that hold first halves
-  const int lane = threadIdx.x & 31;
-  const int other = (lane - sub) + (sub < hl ? sub + hl : sub < 2 * hl ? sub - hl : sub);
-  const bool turned = p.r.adjacent ? sub * 8 < 2 * pairs : sub < 2 * hl;
   for (int n0 = blockIdx.x * TB; n0 < p.N; n0 += gridDim.x * TB) {
-    __syncthreads();                                           // the last tokens' shared values are done with
+    const int tokens = min(TB, p.N - n0);
+    // This lane group's heads in turn: (t, h), kGroups on each time.
+    int lt = group / H, lh = group - lt * H;         // to load next
+    int pt = lt, ph = lh;                            // to work on next
+    uint4 raw[kFlight][2];
+    auto load = [&]() {
+#pragma unroll
+      for (int f = 0; f < kFlight; ++f) {
+        if (lt < tokens) {
+          const uint4* x = p.x + (n0 + lt) * p.row_vecs + lh * kChunks;
+          raw[f][0] = __ldg(x + c0);
+          raw[f][1] = __ldg(x + c1);
+        }
+        lh += kGroups;
+        while (lh >= H) {
+          lh -= H;
+          ++lt;
+        }
+      }
+    };
+    load();
+    __syncthreads();                                 // the last tokens' shared values are done with
     if (threadIdx.x < TB) s_stream[threadIdx.x] = paged ? -1 : 0;
     __syncthreads();
     if (paged) {
@@ -105,9 +130,8 @@ __global__ void __launch_bounds__(kThreads) rotate_heads_kernel(const __grid_con
           if (n0 + t >= s0 && n0 + t < s1) s_stream[t] = b;
       }
     }
-    for (int i = threadIdx.x; i < TB * pairs; i += kThreads) {
+    for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
       const int t = i / pairs, c = i - t * pairs;
-      if (n0 + t >= p.N) break;
       int axis = 0;
 #pragma unroll
       for (int a = 0; a < kMaxAxes - 1; ++a) axis += a < p.r.axes - 1 && c >= p.r.section_end[a];
@@ -118,96 +142,110 @@ __global__ void __launch_bounds__(kThreads) rotate_heads_kernel(const __grid_con
       s_turn[t * (D / 2) + c] = make_float2(cs, sn);
     }
     __syncthreads();
-    if (paged && threadIdx.x < TB) {
-      const int t = threadIdx.x, b = s_stream[t];
-      long long row = -1;
-      if (b >= 0) {
-        const int len = p.held[b], cap = pool_capacity(p.pool);
-        const long long place = static_cast<long long>(len) + (n0 + t - p.q_start[b]);
-        if (len >= 0 && len <= cap && place < cap) row = pool_row(p.pool, b, static_cast<int>(place));
-        if (row < 0 && p.overflow) atomicOr(p.overflow, 1);
+    if (paged) {
+      if (threadIdx.x < TB) {
+        const int t = threadIdx.x, b = s_stream[t];
+        long long row = -1;
+        if (b >= 0) {
+          const int len = p.held[b], cap = pool_capacity(p.pool);
+          const long long place = static_cast<long long>(len) + (n0 + t - p.q_start[b]);
+          if (len >= 0 && len <= cap && place < cap) row = pool_row(p.pool, b, static_cast<int>(place));
+          if (row < 0 && p.overflow) atomicOr(p.overflow, 1);
+        }
+        s_row[t] = row;
       }
-      s_row[t] = row;
+      __syncthreads();
     }
-    __syncthreads();
-    const int vectors = min(TB, p.N - n0) * H;
+    const int vectors = tokens * H;
     for (int base = 0; base < vectors; base += kGroups * kFlight) {   // the same turns for every lane
-      const int v0 = base + group;
-      uint4 raw[kFlight];
 #pragma unroll
       for (int f = 0; f < kFlight; ++f) {
-        const int i = v0 + f * kGroups;
-        raw[f] = make_uint4(0u, 0u, 0u, 0u);
-        if (i < vectors) {
-          const int t = i / H;
-          raw[f] = __ldg(p.x + static_cast<size_t>(n0 + t) * p.row_vecs + static_cast<size_t>(i - t * H) * L + sub);
+        if (base + f * kGroups >= vectors) break;
+        const int t = pt, h = ph;
+        ph += kGroups;
+        while (ph >= H) {
+          ph -= H;
+          ++pt;
         }
-      }
-#pragma unroll
-      for (int f = 0; f < kFlight; ++f) {
-        if (base + f * kGroups >= vectors) break;              // the same for the whole CTA
-        const int i = v0 + f * kGroups;
-        const int t = min(i, vectors - 1) / H, h = i - t * H;
-        const bool isq = h < Hq, isk = !isq && h < Hq + Hkv;
-        uint32_t w[4] = {raw[f].x, raw[f].y, raw[f].z, raw[f].w};
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[2 * e] = __uint_as_float(w[e] << 16);
-          y[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-        }
-        const float* weight = isq ? p.r.q_weight : isk ? p.r.k_weight : nullptr;
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (weight) {
-          const float r = rsqrtf(ss * (1.f / D) + p.r.eps);
-          const float* ws = s_w[isq ? 0 : 1] + sub * 8;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = y[e] * r * ws[e];
-        }
-        float z[8];
-        if (p.r.adjacent) {
-          const float2* cs = s_turn + t * (D / 2) + min(sub * 4, max(pairs - 4, 0));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 c = cs[e];
-            z[2 * e] = y[2 * e] * c.x - y[2 * e + 1] * c.y;
-            z[2 * e + 1] = y[2 * e + 1] * c.x + y[2 * e] * c.y;
-          }
-        } else {
-          const float2* cs = s_turn + t * (D / 2) + (sub < hl ? sub : turned ? sub - hl : 0) * 8;
+        const bool there = t < tokens, isq = h < Hq, isv = h >= Hq + Hkv;
+        uint32_t w[8] = {raw[f][0].x, raw[f][0].y, raw[f][0].z, raw[f][0].w, raw[f][1].x, raw[f][1].y, raw[f][1].z, raw[f][1].w};
+        if (__any_sync(0xffffffffu, there && !isv)) {
+          float y[16];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float o = __shfl_sync(0xffffffffu, y[e], other);
-            const float2 c = cs[e];
-            z[e] = y[e] * c.x + (sub < hl ? -o : o) * c.y;
+            y[2 * e] = __uint_as_float(w[e] << 16);
+            y[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
           }
-        }
-        if (i >= vectors) continue;
-        if (isq || isk) {
+          if (norm_q || norm_k) {
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ss = fmaf(y[e], y[e], ss);
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (isq ? norm_q : norm_k) {
+              const float r = rsqrtf(ss * (1.f / D) + p.r.eps);
+              const float4* ws = reinterpret_cast<const float4*>(s_w[isq ? 0 : 1]);
+              const float4 g[4] = {ws[2 * c0], ws[2 * c0 + 1], ws[2 * c1], ws[2 * c1 + 1]};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                y[4 * e] *= r * g[e].x;
+                y[4 * e + 1] *= r * g[e].y;
+                y[4 * e + 2] *= r * g[e].z;
+                y[4 * e + 3] *= r * g[e].w;
+              }
+            }
+          }
           if (turned) {
+            // (cos, sin) of two pairs at a time.
+            const float4* cs = reinterpret_cast<const float4*>(s_turn + (there ? t : 0) * (D / 2));
+            if (adjacent) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = z[e];
+              for (int i = 0; i < 4; ++i) {
+                const float4 c = cs[2 * (i < 2 ? c0 : c1) + (i & 1)];
+                float* z = y + 4 * i;
+                const float a0 = z[0], b0 = z[1], a1 = z[2], b1 = z[3];
+                z[0] = a0 * c.x - b0 * c.y;
+                z[1] = b0 * c.x + a0 * c.y;
+                z[2] = a1 * c.z - b1 * c.w;
+                z[3] = b1 * c.z + a1 * c.w;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float4 c = cs[4 * sub + i];
+                const float a0 = y[2 * i], a1 = y[2 * i + 1], b0 = y[2 * i + 8], b1 = y[2 * i + 9];
+                y[2 * i] = a0 * c.x - b0 * c.y;
+                y[2 * i + 8] = b0 * c.x + a0 * c.y;
+                y[2 * i + 1] = a1 * c.z - b1 * c.w;
+                y[2 * i + 9] = b1 * c.z + a1 * c.w;
+              }
+            }
           }
+          if (!isv) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = pack2(y[2 * e], y[2 * e + 1]);
+            for (int e = 0; e < 8; ++e) w[e] = pack2(y[2 * e], y[2 * e + 1]);
+          }
         }
-        const uint4 done = make_uint4(w[0], w[1], w[2], w[3]);
-        const size_t n = n0 + t;
-        const int kv = isq ? 0 : isk ? h - Hq : h - Hq - Hkv;
+        if (!there) continue;
+        uint4* dst = nullptr;
         if (isq) {
-          if (!paged || s_stream[t] >= 0) p.q[(n * Hq + h) * L + sub] = done;
-        } else if (!paged) {
-          (isk ? p.k : p.v)[(n * Hkv + kv) * L + sub] = done;
-        } else if (s_row[t] >= 0) {
-          const size_t row = static_cast<size_t>(s_row[t]) * Hkv + kv;
-          static_cast<uint4*>(isk ? p.pool.k : p.pool.v)[row * L + sub] = done;
-          if (isk && sub == 0 && p.pool.weight) p.pool.weight[row] = 0.f;
+          if (s_stream[t] >= 0) dst = p.q + (static_cast<size_t>(n0 + t) * Hq + h) * kChunks;
+        } else {
+          const int kv = isv ? h - Hq - Hkv : h - Hq;
+          if (!paged) {
+            dst = (isv ? p.v : p.k) + (static_cast<size_t>(n0 + t) * Hkv + kv) * kChunks;
+          } else if (s_row[t] >= 0) {
+            const size_t row = static_cast<size_t>(s_row[t]) * Hkv + kv;
+            dst = static_cast<uint4*>(isv ? p.pool.v : p.pool.k) + row * kChunks;
+            if (!isv && sub == 0 && p.pool.weight) p.pool.weight[row] = 0.f;
+          }
+        }
+        if (dst) {
+          dst[c0] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[c1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
       }
+      if (base + kGroups * kFlight < vectors) load();
     }
   }
 }

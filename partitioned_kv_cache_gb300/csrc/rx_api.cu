@@ -113,6 +113,21 @@ bool encode_tmap_4d(CUtensorMap* tm, const void* base, const uint64_t dims[4],
   return encode_4d(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, base, dims, strides_bytes, box);
 }
 
+bool encode_tmap_5d(CUtensorMap* tm, const void* base, const uint64_t dims[5], const uint64_t strides_bytes[4],
+                    const uint32_t box[5]) {
+  EncodeTiledFn f = encode_tiled();
+  if (!f) return false;
+  cuuint64_t gd[5], gs[4];
+  cuuint32_t bx[5], es[5] = {1, 1, 1, 1, 1};
+  for (int i = 0; i < 5; ++i) {
+    gd[i] = dims[i];
+    bx[i] = box[i];
+  }
+  for (int i = 0; i < 4; ++i) gs[i] = strides_bytes[i];
+  return f(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_tmap_u8_4d(CUtensorMap* tm, const void* base, const uint64_t dims[4],
                        const uint64_t strides_bytes[3], const uint32_t box[4]) {
   return encode_4d(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8,
