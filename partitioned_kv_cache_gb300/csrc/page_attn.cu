@@ -31,8 +31,8 @@
 // holds, it weighs nothing.  A weight of 0 times an infinity or NaN in V would
 // still be NaN: in tiles where not every row sees every key the softmax warps
 // read V's tile in shared memory first and write zeros over rows that are
-// outside or not finite; rows that see a key whose value is not finite become
-// NaN.
+// outside, or not finite and hidden from some row; rows that see one of the
+// latter become NaN.
 //
 // Warps: 0 = copies of K, 1 = tensor memory, copies of Q and Q K^T, 2 = P V, 3 =
 // copies of V, 4..11 = softmax and epilogue.
@@ -625,6 +625,13 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
       mbar_arrive(BAR(B_QE));
       return true;
     };
+    // A lane's entry of the table of the first 32 from a part's start on (0: none).
+    auto entry_of = [&](const Walk& x) {
+      const int e = (max(0, (x.t0 - shared) * BN) >> lp) + lane;
+      return (static_cast<long long>(e) << lp) < x.s.plan.len
+                 ? __ldg(p.pool.table + static_cast<long long>(x.b) * p.pool.max_pages + e) : 0;
+    };
+    int first_entry = more ? entry_of(w) : 0;
     if (more) ok = load_q(0);
     while (more) {
       const int t_row = (w.rt << w.s.plan.log_a) + (row >> p.log_g);
@@ -641,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
       auto entry = [&](int e) { return (static_cast<long long>(e) << lp) < w.s.plan.len ? __ldg(table + e) : 0; };
       auto named_of = [&](int x) { return __ballot_sync(0xffffffffu, static_cast<unsigned int>(x) < static_cast<unsigned int>(p.pool.n_pages)); };
       int e_base = max(0, (w.t0 - shared) * BN) >> lp;
-      uint32_t named32 = named_of(entry(e_base + lane));
+      uint32_t named32 = named_of(first_entry);
       int then = entry(e_base + 32 + lane);
       const int plain = min(w.s.plan.len, all);   // every row sees every key before it
       float m_used = -INFINITY;
@@ -738,7 +745,9 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
           const int c0 = (lane & (kShare - 1)) * kChunks;
           const bool outside = !(there.w[vr >> 6] >> (vr & 63) & 1);
           uint32_t odd = 0;
-          if (!outside) {
+          // (A value that every row sees may do to them what it does.)
+          const int unseen = t < shared ? BN : all - (t - shared) * BN;   // keys before it are seen by all
+          if (!outside && vr >= unseen) {
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
               const int c = c0 + i;
@@ -758,6 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
             for (int i = 0; i < kChunks; ++i) st_shared_v4(at + ((c0 + i) >> 3) * block + (((c0 + i) & 7) << 4), 0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
+          if (unseen < BN) {
           // Every second or fourth lane's bit, close up.
           uint32_t rows = __ballot_sync(0xffffffffu, odd != 0);
           volatile uint8_t* bits = not_finite + (checks & 1) * 16;
@@ -780,6 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
           ++checks;
 #pragma unroll
           for (int i = 0; i < BN / 64; ++i) poison = poison || (reinterpret_cast<volatile uint64_t*>(bits)[i] & mine.w[i]) != 0;
+          }
         }
         if (++vslot == Lay::NV) {
           vslot = 0;
@@ -826,6 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
       // The next unit's Q, so that its scores are on their way during this one's end.
       Walk coming = w;
       more = coming.next(p);
+      if (more) first_entry = entry_of(coming);
       if (more && ok) ok = load_q(u + 1);
       if (ok) ok = warp_wait(BAR(B_PV + ((j - 1) & 1)), ((j - 1) >> 1) & 1, abort_flag);
       tc_fence_after();

@@ -717,33 +717,30 @@ class Heads:
             raise ValueError("at most %d axes" % MAX_AXES)
         if sum(sections) != freq.shape[0]:
             raise ValueError("the sections %s hold %d pairs, freq %d" % (sections, sum(sections), freq.shape[0]))
-        self.Hq, self.Hkv, self.D, self.axes, self.eps = Hq, Hkv, D, len(sections), float(eps)
+        self.Hq, self.Hkv, self.D, self.axes, self.width = Hq, Hkv, D, len(sections), (Hq + 2 * Hkv) * D
         self.freq, self.q_weight, self.k_weight = freq, q_weight, k_weight
-        self._sections, self._adjacent = (_i * MAX_AXES)(*sections), int(bool(adjacent))
-
-    def _specs(self):
-        f32 = torch.float32
-        return ((self.freq, f32, self.freq.shape, "freq"), (self.q_weight, f32, (self.D,), "q_weight"),
-                (self.k_weight, f32, (self.D,), "k_weight"))
-
-    def _c(self, ptrs) -> RxHeads:
-        return RxHeads(*ptrs, self.Hq, self.Hkv, self.D, self.axes, self._sections, self._adjacent, self.eps)
+        if not freq.is_cuda:
+            raise ValueError("freq must be a CUDA tensor")
+        dev, f32, each = freq.get_device(), torch.float32, (D,)
+        ptrs = _addresses(dev, (freq, f32, freq.shape, "freq"), (q_weight, f32, each, "q_weight"), (k_weight, f32, each, "k_weight"))
+        self._device = dev
+        self._c = RxHeads(*ptrs, Hq, Hkv, D, len(sections), (_i * MAX_AXES)(*sections), int(bool(adjacent)), float(eps))
 
 
 def _heads_input(x: torch.Tensor, heads: Heads, pos: torch.Tensor, dev: int):
     """(tokens, row stride) of a projection's rows, which may be apart, and the
     positions as [axes][N]."""
-    width = (heads.Hq + 2 * heads.Hkv) * heads.D
-    if x.dim() != 2 or x.shape[1] != width:
-        raise ValueError("x must have shape [N][%d], got %s" % (width, tuple(x.shape)))
-    if x.dtype != torch.bfloat16:
+    if x.dim() != 2 or x.shape[1] != heads.width:
+        raise ValueError("x must have shape [N][%d], got %s" % (heads.width, tuple(x.shape)))
+    if x.dtype is not torch.bfloat16:
         raise TypeError("x must be %s, got %s" % (torch.bfloat16, x.dtype))
     if x.stride(1) != 1:
         raise ValueError("the values of a row of x must be contiguous")
-    if x.get_device() != dev:
-        raise ValueError("x must be on the current device (cuda:%d), got %s" % (dev, x.device))
+    if x.get_device() != dev or heads._device != dev:
+        raise ValueError("x and the heads' tensors must be on the current device (cuda:%d), got %s and cuda:%d"
+                         % (dev, x.device, heads._device))
     N = x.shape[0]
-    return N, x.stride(0) if N > 1 else width, pos if pos.dim() == 2 else pos.view(1, -1)
+    return N, x.stride(0) if N > 1 else heads.width, pos if pos.dim() == 2 else pos.view(1, -1)
 
 
 def rotate_heads(x: torch.Tensor, heads: Heads, pos: torch.Tensor, q: Optional[torch.Tensor] = None,
@@ -754,14 +751,17 @@ def rotate_heads(x: torch.Tensor, heads: Heads, pos: torch.Tensor, q: Optional[t
     dev, st = _here(stream)
     N, stride, pos = _heads_input(x, heads, pos, dev)
     qs, ks, bf16 = (N, heads.Hq, heads.D), (N, heads.Hkv, heads.D), torch.bfloat16
+    pp, qp, kp, vp = _addresses(dev, (pos, torch.int32, (heads.axes, N), "pos"), (q, bf16, qs, "q"), (k, bf16, ks, "k"),
+                                (v, bf16, ks, "v"))
+    # (Outputs are allocated last: beside the launch of the call before, the
+    # allocator takes some microseconds more than behind the checks.)
     if q is None or k is None or v is None:
         with _outputs(stream):
-            q = torch.empty(qs, dtype=bf16, device=x.device) if q is None else q
-            k = torch.empty(ks, dtype=bf16, device=x.device) if k is None else k
-            v = torch.empty(ks, dtype=bf16, device=x.device) if v is None else v
-    pp, qp, kp, vp, *h = _addresses(dev, (pos, torch.int32, (heads.axes, N), "pos"), (q, bf16, qs, "q"), (k, bf16, ks, "k"),
-                                    (v, bf16, ks, "v"), *heads._specs())
-    _check(_lib.rx_rotate_heads(x.data_ptr(), stride, N, ctypes.byref(heads._c(h)), pp, qp, kp, vp, st), "rx_rotate_heads")
+            q = x.new_empty(qs) if q is None else q
+            k = x.new_empty(ks) if k is None else k
+            v = x.new_empty(ks) if v is None else v
+        qp, kp, vp = q.data_ptr(), k.data_ptr(), v.data_ptr()
+    _check(_lib.rx_rotate_heads(x.data_ptr(), stride, N, ctypes.byref(heads._c), pp, qp, kp, vp, st), "rx_rotate_heads")
     return q, k, v
 
 
@@ -779,16 +779,17 @@ def rotate_heads_paged(x: torch.Tensor, heads: Heads, pos: torch.Tensor, pages: 
     qs, i32 = (N, heads.Hq, heads.D), torch.int32
     if overflow is not None and overflow.numel() < 1:
         raise ValueError("overflow must hold one int32")
-    if pages.k.dim() == 4 and tuple(pages.k.shape[2:]) != (heads.Hkv, heads.D):
+    if pages.k.shape[2:] != (heads.Hkv, heads.D):
         raise ValueError("pages have heads %s, expected %s" % (tuple(pages.k.shape[2:]), (heads.Hkv, heads.D)))
-    if q is None:
-        with _outputs(stream):
-            q = torch.empty(qs, dtype=torch.bfloat16, device=x.device)
-    g, (pp, qp, sp, hp, np_, op, *h) = _pages(dev, pages, (
+    g, (pp, qp, sp, hp, np_, op) = _pages(dev, pages, (
         (pos, i32, (heads.axes, N), "pos"), (q, torch.bfloat16, qs, "q"), (q_start, i32, (B + 1,), "q_start"),
         (held, i32, (B,), "held"), (new_len, i32, (B,), "new_len"),
-        (overflow, i32, None if overflow is None else overflow.shape, "overflow"), *heads._specs()))
-    _check(_lib.rx_rotate_heads_paged(x.data_ptr(), stride, N, ctypes.byref(heads._c(h)), pp, qp, ctypes.byref(g), sp, hp,
+        (overflow, i32, None if overflow is None else overflow.shape, "overflow")))
+    if q is None:
+        with _outputs(stream):
+            q = x.new_empty(qs)
+        qp = q.data_ptr()
+    _check(_lib.rx_rotate_heads_paged(x.data_ptr(), stride, N, ctypes.byref(heads._c), pp, qp, ctypes.byref(g), sp, hp,
                                       np_, op, st), "rx_rotate_heads_paged")
     return q
 
@@ -798,6 +799,10 @@ def attend_pages_workspace(N: int, Hq: int, Hkv: int, D: int) -> int:
     n = ctypes.c_longlong(0)
     _check(_lib.rx_attend_pages_workspace(N, Hq, Hkv, D, ctypes.byref(n)), "rx_attend_pages_workspace")
     return n.value
+
+
+#: attend_pages_workspace() by (device, N, Hq, Hkv, D).
+_workspace_sizes: dict = {}
 
 
 def _attend_pages(cache, layer, q, pages, q_start, length, prefix, out, lse, workspace, stream):
@@ -810,20 +815,32 @@ def _attend_pages(cache, layer, q, pages, q_start, length, prefix, out, lse, wor
         raise ValueError("q has heads %s, the pages %s" % ((Hq, D), tuple(pages.k.shape[2:])))
     dev, st = _here(stream)
     wants_lse = lse is not None and lse is not False
-    with _outputs(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        lse = torch.empty((N, Hq), dtype=f32, device=q.device) if lse is True else lse if wants_lse else None
-        if workspace is None and dev >= 0:
-            workspace = torch.empty(attend_pages_workspace(N, Hq, Hkv, D), dtype=u8, device=q.device)
+    given = lse if wants_lse and lse is not True else None
     rows, each = (N, Hq, D), (B,)
     g, (qp, sp, lp, pp, op, ep, wp) = _pages(dev, pages, (
         (q, bf16, rows, "q"), (q_start, i32, (B + 1,), "q_start"), (length, i32, each, "length"),
-        (prefix, i32, each, "prefix"), (out, bf16, rows, "out"), (lse, f32, (N, Hq), "lse"),
+        (prefix, i32, each, "prefix"), (out, bf16, rows, "out"), (given, f32, (N, Hq), "lse"),
         (workspace, u8, None if workspace is None else workspace.shape, "workspace")))
+    size = 0 if workspace is None else workspace.numel()
+    with _outputs(stream):   # (after the checks, as in rotate_heads)
+        if out is None:
+            out = torch.empty_like(q)
+            op = out.data_ptr()
+        if wants_lse and given is None:
+            given = torch.empty((N, Hq), dtype=f32, device=q.device)
+            ep = given.data_ptr()
+        if workspace is None:
+            key = dev, N, Hq, Hkv, D
+            size = _workspace_sizes.get(key)
+            if size is None:
+                if len(_workspace_sizes) >= 4096:
+                    _workspace_sizes.clear()
+                size = _workspace_sizes[key] = attend_pages_workspace(N, Hq, Hkv, D)
+            workspace = torch.empty(size, dtype=u8, device=q.device)
+            wp = workspace.data_ptr()
     _check(_lib.rx_attend_pages(None if cache is None else cache._h, layer, qp, N, Hq, Hkv, D, ctypes.byref(g), sp, lp, pp,
-                                op, ep, wp, 0 if workspace is None else workspace.numel(), st), "rx_attend_pages")
-    return (out, lse) if wants_lse else out
+                                op, ep, wp, size, st), "rx_attend_pages")
+    return (out, given) if wants_lse else out
 
 
 def attend_pages(q: torch.Tensor, pages: Pages, q_start: torch.Tensor, length: torch.Tensor,
@@ -886,12 +903,13 @@ def evict_pages(pages: Pages, length: torch.Tensor, budget: int, sink: int = 0, 
         raise ValueError("overflow must hold one int32")
     B, (Hkv, D), i32 = pages.table.shape[0], pages.k.shape[2:], torch.int32
     dev, st = _here(stream)
-    if kept is None:
-        with _outputs(stream):
-            kept = torch.empty((B, Hkv, max(0, budget)), dtype=i32, device=pages.k.device)
     g, (lp, tp, np_, kp, op) = _pages(dev, pages, (
         (length, i32, (B,), "length"), (to, i32, None if to is None else to.shape, "to"), (new_len, i32, (B,), "new_len"),
         (kept, i32, (B, Hkv, budget), "kept"), (overflow, i32, None if overflow is None else overflow.shape, "overflow")))
+    if kept is None:
+        with _outputs(stream):
+            kept = torch.empty((B, Hkv, max(0, budget)), dtype=i32, device=pages.k.device)
+        kp = kept.data_ptr()
     _check(_lib.rx_evict_pages(ctypes.byref(g), Hkv, D, lp, sink, recent, budget, tp, 0 if to is None else to.shape[1], np_,
                                kp, op, st), "rx_evict_pages")
     return kept

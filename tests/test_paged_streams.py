@@ -197,7 +197,11 @@ def test_binding_refuses_shapes_and_types(lib):
     k, table, w = z(3, 16, 1, 64, dtype=bf), z(2, 2, dtype=i32), z(3, 16, 1)
     pages = rx.Pages(k, k.clone(), table, w)
     q, qs, ln, lse = z(5, 2, 64, dtype=bf), z(3, dtype=i32), z(2, dtype=i32), z(5, 2)
-    heads = rx.Heads(2, 1, 64, z(32))
+    # (the heads' own tensors are checked when they are made)
+    with pytest.raises(ValueError, match="freq"):
+        rx.Heads(2, 1, 64, z(32))
+    heads = rx.Heads.__new__(rx.Heads)
+    heads.Hq, heads.Hkv, heads.D, heads.axes, heads.width, heads._device = 2, 1, 64, 1, 256, 0
     x, pos = z(5, 256, dtype=bf), z(1, 5, dtype=i32)
     with pytest.raises(ValueError, match="axes"):
         rx.Heads(2, 1, 64, z(40), (8,) * 5)
