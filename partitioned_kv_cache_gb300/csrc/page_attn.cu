@@ -145,6 +145,13 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
       : "memory");
 }
 
+// 32 bytes, 32-byte aligned.
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&x)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
 // Pairs of fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   uint64_t d;
@@ -859,6 +866,9 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
       const bool whole = begins && ends;
       const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (begins ? 1 : 0);
       float4* dst = p.part + slot * (D / 4) * p.part_rows + row;
+      // A thread's 16-byte stores into a row of its own are 32 lines an instruction:
+      // 32-byte ones halve what a part's end costs.
+      const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
       const float inv = l > 0.f ? 1.f / l : l;   // l = 0: a row without keys gets zeros; NaN stays
 #pragma unroll 1
       for (int c = half * kOCols; c < (half + 1) * kOCols; c += 32) {
@@ -869,7 +879,16 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.f;
         }
-        if (row_valid && whole) {
+        if (row_valid && whole && wide) {
+          __nv_bfloat16* dst16 = p.out + at * D + c;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = pack_bf16x2(o[16 * i + 2 * e] * inv, o[16 * i + 2 * e + 1] * inv);
+            st_global_v8(dst16 + 16 * i, y);
+          }
+        } else if (row_valid && whole) {
           uint4* d4 = reinterpret_cast<uint4*>(p.out + at * D + c);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
