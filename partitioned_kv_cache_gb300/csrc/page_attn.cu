@@ -47,13 +47,15 @@
 #include "page_plan.h"
 #include "pages.h"
 #include "rx_internal.h"
-#include "sm103_ptx.cuh"
+#include "pages_ptx.cuh"
 
 namespace rx {
 namespace {
 
 constexpr float kRescale = 8.0f;   // log2 units
 constexpr int kMinRunKeys = 256;   // keys of a CTA's run, at least
+constexpr int kUnitPad = 4;        // tiles that a unit's start and end cost: attend_prompts, with units of 11 to
+                                   // 59 tiles, takes 161 us, and 203 with 0
 constexpr int kMergeThreads = 256;
 constexpr int kMergeFew = 8;       // parts that one thread of the merge takes
 
@@ -130,62 +132,6 @@ struct PageAttnParams {
   float scale_log2;
 };
 
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// 32 bytes, 32-byte aligned.
-__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&x)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
-               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-               : "memory");
-}
-
-// Pairs of fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t d;
-  asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
-  return *reinterpret_cast<float2*>(&d);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t d;
-  asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
-  return *reinterpret_cast<float2*>(&d);
-}
-
-// The largest of 32 values, NaN left out where there is another.
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ float max32(const float (&x)[32]) {
-  float a = x[0], b = x[1], c = x[2], d = x[3];
-#pragma unroll
-  for (int i = 4; i < 28; i += 8) {
-    a = max3(a, x[i], x[i + 1]);
-    b = max3(b, x[i + 2], x[i + 3]);
-    c = max3(c, x[i + 4], x[i + 5]);
-    d = max3(d, x[i + 6], x[i + 7]);
-  }
-  a = max3(a, x[28], x[29]);
-  b = max3(b, x[30], x[31]);
-  return fmaxf(max3(a, b, c), d);
-}
-
 // A bit for every key of a tile.
 template <int BN>
 struct Bits {
@@ -205,29 +151,6 @@ __device__ __forceinline__ void hide(float (&x)[32], uint32_t seen) {
 #pragma unroll
   for (int c = 0; c < 32; ++c)
     if (!(seen >> c & 1)) x[c] = -INFINITY;
-}
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(one));
-  return one != 0;
-}
-__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
-
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  const bool ok = mbar_wait(bar, parity, abort);
-  return __all_sync(0xffffffffu, ok);
 }
 
 // The store's tiles of 64 keys: pinned, then the window in slot order, past the
@@ -271,6 +194,7 @@ __device__ __forceinline__ Stream load_stream(const PageAttnParams& p, int log_t
   s.plan.shared = shared;
   s.plan.log_a = 7 - p.log_g;
   s.plan.log_t = log_t;
+  s.plan.pad = kUnitPad;
   return s;
 }
 
@@ -286,6 +210,7 @@ struct Walk {
   Stream s;
   int b, h, rt;
   int t0, count, tiles;   // the part: tiles [t0, t0 + count) of the unit's `tiles`
+  int taken;              // numbers of the run that it takes, pads among them
   long long left;
 
   __device__ __forceinline__ bool begin(const PageAttnParams& p, int log_t, int shared, const RunStart& r) {
@@ -299,14 +224,15 @@ struct Walk {
     rt = s.plan.row_tile_of(o);
     t0 = static_cast<int>(o - s.plan.tiles_before(rt));
     measure();
-    return true;
+    return count > 0 || next(p);   // (a run may begin in a pad)
   }
   __device__ __forceinline__ void measure() {
     tiles = s.plan.tiles(rt);
-    count = static_cast<int>(min(left, static_cast<long long>(tiles - t0)));
+    taken = static_cast<int>(min(left, static_cast<long long>(tiles + s.plan.pad - t0)));
+    count = min(taken, tiles - t0);
   }
   __device__ __forceinline__ bool next(const PageAttnParams& p) {
-    left -= count;
+    left -= taken;
     if (left <= 0) return false;
     t0 = 0;
     if (++rt == s.plan.row_tiles()) {

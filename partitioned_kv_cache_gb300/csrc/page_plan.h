@@ -29,6 +29,8 @@ struct StreamPlan {
   int shared;   // tiles of the store
   int log_a;    // a = 1 << log_a tokens in a row tile, 1 to 128
   int log_t;    // keys of a tile: 64 or 128
+  int pad;      // what a unit (row tile) costs beside its tiles, in tiles: numbers behind
+                // them that stand for no tile, so that equal runs take equal time
 
   RX_HD int row_tiles() const { return (n + (1 << log_a) - 1) >> log_a; }
 
@@ -39,10 +41,10 @@ struct StreamPlan {
     return shared + (((x > floor ? x : floor) + (1 << log_t) - 1) >> log_t);
   }
 
-  // Key tiles of row tiles [0, r), r <= row_tiles().
+  // Key tiles (and pads) of row tiles [0, r), r <= row_tiles().
   RX_HD long long tiles_before(int r) const {
     const int R = row_tiles();
-    long long sum = static_cast<long long>(shared) * r;
+    long long sum = static_cast<long long>(shared + pad) * r;
     if (r > 0 && r == R) {   // the last row tile may be short
       sum += tiles(R - 1) - shared;
       --r;
@@ -67,7 +69,7 @@ struct StreamPlan {
     return sum;
   }
 
-  // The row tile that holds the stream's tile `at` of one head.
+  // The row tile that holds number `at` of the stream's tiles of one head.
   RX_HD int row_tile_of(long long at) const {
     int lo = 0, hi = row_tiles() - 1;
     while (lo < hi) {

@@ -32,7 +32,7 @@
 
 #include "pages.h"
 #include "rx_internal.h"
-#include "sm103_ptx.cuh"
+#include "pages_ptx.cuh"
 
 namespace rx {
 namespace {
@@ -187,46 +187,6 @@ struct Units {
     return true;
   }
 };
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(one));
-  return one != 0;
-}
-
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  const bool ok = mbar_wait(bar, parity, abort);
-  return __all_sync(0xffffffffu, ok);
-}
-
-// D += A B^T with the A operand in tensor memory.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// Pairs of fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t d;
-  asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
-  return *reinterpret_cast<float2*>(&d);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t d;
-  asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
-  return *reinterpret_cast<float2*>(&d);
-}
 
 // A ring position: slot and how often the ring has gone round.
 struct Turn {
@@ -501,17 +461,16 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) page_weigh_kernel(const
         tc_fence_after();
         const int hidden = first - r * kRows;   // leading rows of the tile that do not see the key
         const bool mask = __any_sync(0xffffffffu, hidden > 0);
+        const bool few = r * kRows + 64 >= (now.s.n << p.log_g);   // rows: a single token's
         const float4* lse = reinterpret_cast<const float4*>(s_lse + slot * kRows);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const bool rows_there = r * kRows + half * 64 < (now.s.n << p.log_g);   // (a single token has few)
           float s[64];
-          if (rows_there) tmem_ld64(tmem + Lay::T_S + slot * kRows + half * 64 + lane_off, s);
-          if (half == 1) {
+          tmem_ld64(tmem + Lay::T_S + slot * kRows + half * 64 + lane_off, s);
+          if (half == 1 || few) {
             tc_fence_before();
             mbar_arrive(BAR(B_SR + slot));
           }
-          if (!rows_there) continue;
           if (mask) {
 #pragma unroll
             for (int c = 0; c < 64; ++c)
@@ -525,6 +484,7 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) page_weigh_kernel(const
             sum[0] = add2(sum[0], make_float2(exp2f(a.x), exp2f(a.y)));
             sum[1] = add2(sum[1], make_float2(exp2f(b.x), exp2f(b.y)));
           }
+          if (few) break;
         }
         mbar_arrive(BAR(B_LR + slot));
       }

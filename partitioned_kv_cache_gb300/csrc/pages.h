@@ -53,6 +53,10 @@ __device__ __forceinline__ int held_keys(const PagePool& p, const int* len, int 
   return max(0, min(__ldg(len + b), pool_capacity(p)));
 }
 
+// Tensor-map encoding for bf16 with the 128-byte swizzle.
+bool encode_tmap_5d(CUtensorMap* tm, const void* base, const uint64_t dims[5], const uint64_t strides_bytes[4],
+                    const uint32_t box[5]);
+
 // Copies by tensor map cost the copy engine some 3 cycles for each row of 128
 // bytes and 100 to 200 each, so one copy takes all column blocks of a page's
 // tokens.  In shared memory they lie as [8 tokens][D/64 column blocks][8 rows of

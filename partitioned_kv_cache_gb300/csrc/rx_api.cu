@@ -932,7 +932,8 @@ static rx_status check_queries(const char* where, const void* q, int N, int Hq, 
   if (N < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv) return fail(RX_ERR_ARG, "%s: N, Hq or Hkv out of range", where);
   const int G = Hq / Hkv;
   if (!pow2(G) || G > rx::kBM) return fail(RX_ERR_UNSUPPORTED, "%s: Hq/Hkv = %d must be a power of two <= 128", where, G);
-  if (static_cast<long long>(N) * Hq > (1LL << 31) - 1) return fail(RX_ERR_ARG, "%s: N*Hq above 2^31", where);
+  if (N > (1 << 30) || static_cast<long long>(N) * Hq > (1LL << 31) - 1)
+    return fail(RX_ERR_ARG, "%s: N above 2^30 or N*Hq above 2^31", where);
   if (N > 0 && (!q || !q_start || !len)) return fail(RX_ERR_ARG, "%s: null pointer", where);
   if (!aligned16(q) || !aligned4(q_start) || !aligned4(len) || !aligned4(prefix))
     return fail(RX_ERR_ARG, "%s: misaligned pointer", where);
@@ -1047,6 +1048,8 @@ rx_status rx_evict_pages(const rx_pages* pages, int Hkv, int D, const int* len, 
     return fail(RX_ERR_ARG, "%s: sink = %d, recent = %d, budget = %d", where, sink, recent, budget);
   if (to && to_max_pages < 1) return fail(RX_ERR_ARG, "%s: to_max_pages < 1", where);
   if (pool.B == 0) return RX_OK;
+  if (to && spans_overlap(to, pool.B * 4LL * to_max_pages, g[3].p, g[3].bytes))
+    return fail(RX_ERR_ARG, "%s: `to` is the pages' own table (NULL evicts in place)", where);
   if (!pool.weight || !len || !kept) return fail(RX_ERR_ARG, "%s: null pointer", where);
   if (!aligned4(len) || !aligned4(to) || !aligned4(new_len) || !aligned4(kept) || !aligned4(overflow))
     return fail(RX_ERR_ARG, "%s: misaligned pointer", where);
@@ -1077,6 +1080,7 @@ rx_status rx_debug_page_plan(int n, int len, int prefix, int shared, int G, int 
   s.shared = shared;
   s.log_a = 7 - log2_of(G);
   s.log_t = log2_of(keys);
+  s.pad = 0;
   if (r < 0 || r > s.row_tiles()) return fail(RX_ERR_ARG, "rx_debug_page_plan: r = %d not in [0, %d]", r, s.row_tiles());
   *before = s.tiles_before(r);
   *row_tile = r < s.row_tiles() ? s.row_tile_of(*before) : -1;

@@ -237,8 +237,6 @@ cudaError_t launch_attention_partials(const AttnLaunch& a, const void* q, int to
 // second for bytes, with the swizzle of the box's row (64 or 128 bytes).
 bool encode_tmap_4d(CUtensorMap* tm, const void* base, const uint64_t dims[4],
                     const uint64_t strides_bytes[3], const uint32_t box[4]);
-bool encode_tmap_5d(CUtensorMap* tm, const void* base, const uint64_t dims[5], const uint64_t strides_bytes[4],
-                    const uint32_t box[5]);   // bf16
 bool encode_tmap_u8_4d(CUtensorMap* tm, const void* base, const uint64_t dims[4],
                        const uint64_t strides_bytes[3], const uint32_t box[4]);
 

@@ -707,7 +707,8 @@ class Heads:
     values, normed where their weight (fp32 [D]) is given, then rotated: freq
     fp32 [R/2] holds the pairs' angles per position, the first sections[0] of
     them turn with axis 0 of the positions, the next sections[1] with axis 1 and
-    so on.  Pair i is elements (i, i + R/2), or (2i, 2i + 1) with adjacent."""
+    so on.  Pair i is elements (i, i + R/2), or (2i, 2i + 1) with adjacent.  Its
+    tensors are checked here, once; calls read what they hold by then."""
 
     def __init__(self, Hq: int, Hkv: int, D: int, freq: torch.Tensor, sections: Sequence[int] = (),
                  q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
@@ -808,6 +809,8 @@ _workspace_sizes: dict = {}
 def _attend_pages(cache, layer, q, pages, q_start, length, prefix, out, lse, workspace, stream):
     if q.dim() != 3 or pages.k.dim() != 4:
         raise ValueError("q must have shape [N][Hq][D] and pages [n_pages][page][Hkv][D]")
+    if cache is not None and not cache._h:
+        raise ValueError("the cache is closed")
     N, Hq, D = q.shape
     B, Hkv = pages.table.shape[0], pages.k.shape[2]
     bf16, f32, i32, u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8

@@ -186,6 +186,7 @@ def test_eviction_refuses_bad_arguments(lib):
     assert call(D=32) == -6 and call(Hkv=0) == -1
     assert call(sink=-1) == -1 and call(recent=-1) == -1 and call(budget=0) == -1 and call(sink=6, recent=3) == -1
     assert call(length=None) == -1 and call(kept=None) == -1 and call(length=ln + 2) == -1 and call(to=to) == -1
+    assert call(to=p + 8448, to_pages=2) == -1         # the pages' own table
     assert call(kept=p) == -1 and call(new_len=ln + 4) == -1 and call(overflow=ln) == -1 and call(kept=to, to=to, to_pages=2) == -1
     del keep
 
@@ -217,6 +218,10 @@ def test_binding_refuses_shapes_and_types(lib):
         rx.rotate_heads(x, heads, pos)
     with pytest.raises(ValueError, match="q must have"):
         rx.attend_pages(q[0], pages, qs, ln)
+    c = rx.Cache.__new__(rx.Cache)
+    c._h = None
+    with pytest.raises(ValueError, match="closed"):
+        c.attend_pages(0, q, pages, qs, ln)
     with pytest.raises(ValueError, match="heads"):
         rx.attend_pages(z(5, 2, 128, dtype=bf), pages, qs, ln)
     with pytest.raises(ValueError, match="q_start"):

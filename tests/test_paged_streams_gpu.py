@@ -399,6 +399,30 @@ def test_attention_over_long_streams(rx, Hq, Hkv, D, lens, new):
     _attend_case(rx, g, Pool(g, lens, 64, Hkv, D).fill(g), new, Hq, edge=0)
 
 
+def test_as_many_streams_as_a_call_takes(rx):
+    """1024 streams, a third of them idle, lengths from 0 on."""
+    g = np.random.default_rng(14)
+    lens = [int(x) for x in g.integers(0, 70, 1024)]
+    new = [min(n, int(x)) for n, x in zip(lens, g.integers(0, 3, 1024))]
+    pool = Pool(g, lens, 16, 1, 64).fill(g)
+    _attend_case(rx, g, pool, new, 2)
+    _weigh_case(rx, g, pool, new, 2)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_outputs_aligned_to_16_bytes_only(rx, D):
+    import torch
+    g = np.random.default_rng(15)
+    pool = Pool(g, [300, 40], 32, 1, D).fill(g)
+    args = (dev(_bits(g, (50, 4, D))), pool.pages(rx), _int([0, 20, 50]), _int([300, 40]))
+    ref = rx.attend_pages(*args)
+    buf = torch.full((50 * 4 * D + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = buf[8:8 + 50 * 4 * D].view(50, 4, D)
+    assert out.data_ptr() % 32 == 16
+    rx.attend_pages(*args, out=out)
+    assert torch.equal(out, ref) and torch.all(buf[:8] == 7) and torch.all(buf[-8:] == 7)
+
+
 def test_large_scores_and_far_apart_maxima(rx):
     """Scores to some hundreds: the running maximum is renewed all along the
     stream, in cut units too."""
