@@ -58,6 +58,7 @@ constexpr int kUnitPad = 4;        // tiles that a unit's start and end cost: at
                                    // 59 tiles, takes 161 us, and 203 with 0
 constexpr int kMergeThreads = 256;
 constexpr int kMergeFew = 8;       // parts that one thread of the merge takes
+constexpr int kMergeFlight = 4;    // of them asked for together: with four CTAs an SM, from L2 at its rate
 
 constexpr int kThreads = 384;
 constexpr int kSoftmax = 256;      // of them two per query row
@@ -868,7 +869,7 @@ struct MergeParams {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) page_merge_kernel(const __grid_constant__ MergeParams p) {
+__global__ void __launch_bounds__(kMergeThreads, 4) page_merge_kernel(const __grid_constant__ MergeParams p) {
   extern __shared__ int s_before[];   // chunks before CTA c's unit [ctas + 1]
   __shared__ float4 s_o[8][32];
   __shared__ float2 s_ml[8][32];
@@ -922,11 +923,11 @@ __global__ void __launch_bounds__(kMergeThreads) page_merge_kernel(const __grid_
     float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     const int first = few ? 0 : warp, step = few ? 1 : 8;
-    for (int s0 = first; s0 < u.parts; s0 += 8 * step) {
-      float4 o[8];
-      float2 ml[8];
+    for (int s0 = first; s0 < u.parts; s0 += kMergeFlight * step) {
+      float4 o[kMergeFlight];
+      float2 ml[kMergeFlight];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kMergeFlight; ++i) {
         const int s = s0 + i * step;
         ml[i] = make_float2(-INFINITY, 0.f);
         o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -938,14 +939,14 @@ __global__ void __launch_bounds__(kMergeThreads) page_merge_kernel(const __grid_
       }
       float m = M;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, ml[i].x);
+      for (int i = 0; i < kMergeFlight; ++i) m = fmaxf(m, ml[i].x);
       const float ref = m == -INFINITY ? 0.f : m;
       const float f = exp2f(M - ref);
       M = m;
       L *= f;
       acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kMergeFlight; ++i) {
         const float g = exp2f(ml[i].x - ref);   // 0 for a part that saw nothing
         L = fmaf(g, ml[i].y, L);
         acc.x = fmaf(g, o[i].x, acc.x);

@@ -53,7 +53,7 @@ __device__ __forceinline__ uint32_t ordered(float w) {
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ uint32_t s_key[];   // [min(candidates, kSelHeld)]
   __shared__ unsigned int s_hist[256];
-  __shared__ int s_pick[2];             // the digit found, and how many keys remain to be found in it
+  __shared__ int s_pick[3];             // the digit found, how many keys remain to be found in it, and are in it
   __shared__ int s_warp[2][kSelWarps];
   __shared__ int s_base[2];
   const int b = blockIdx.x / p.Hkv, h = blockIdx.x - b * p.Hkv;
@@ -74,7 +74,22 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     return row < 0 ? 0u : ordered(__ldg(p.pool.weight + row * p.Hkv + h));
   };
   if (held) {
-    for (int i = threadIdx.x; i < m; i += kSelThreads) s_key[i] = read(i);
+    // Eight keys of a thread at a time: their table entries, then their weights.
+    constexpr int kAhead = 8;
+    for (int i0 = threadIdx.x; i0 < m; i0 += kSelThreads * kAhead) {
+      long long row[kAhead];
+      float w[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * kSelThreads;
+        row[u] = i < m ? pool_row(p.pool, b, lo + i) : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) w[u] = row[u] < 0 ? __uint_as_float(0x7FFFFFFFu) : __ldg(p.pool.weight + row[u] * p.Hkv + h);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (i0 + u * kSelThreads < m) s_key[i0 + u * kSelThreads] = ordered(w[u]);
+    }
   }
   // The want-th largest pattern, eight bits at a time from the top.
   uint32_t found = 0u;
@@ -109,6 +124,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
             if (above + c >= static_cast<unsigned int>(want)) {
               s_pick[0] = 255 - 8 * lane - d;
               s_pick[1] = want - static_cast<int>(above);
+              s_pick[2] = static_cast<int>(c);
               break;
             }
             above += c;
@@ -118,10 +134,12 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
       __syncthreads();
       found |= static_cast<uint32_t>(s_pick[0]) << shift;
       want = s_pick[1];
+      if (want == s_pick[2]) break;   // all of them are kept: whatever is at or above `found`
     }
   }
-  // Kept: above `found`, and the first `want` of those equal to it.
+  // Kept: above `found`, and the first `want` of those equal to it (or all of them).
   const bool any = p.budget > p.sink + p.recent;
+  const bool all = any && want == s_pick[2];
   for (int i = threadIdx.x; i < p.sink; i += kSelThreads) kept[i] = i;
   for (int i = threadIdx.x; i < p.recent; i += kSelThreads) kept[p.budget - p.recent + i] = hi + i;
   if (!any) return;
@@ -130,7 +148,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
   for (int i0 = 0; i0 < m; i0 += kSelThreads) {
     const int i = i0 + threadIdx.x;
     const uint32_t key = i < m ? (held ? s_key[i] : read(i)) : 0u;
-    const bool over = i < m && key > found, same = i < m && key == found;
+    const bool over = i < m && (all ? key >= found : key > found), same = i < m && !all && key == found;
     const unsigned int m_over = __ballot_sync(0xffffffffu, over), m_same = __ballot_sync(0xffffffffu, same);
     if (lane == 0) {
       s_warp[0][warp] = __popc(m_over);
