@@ -469,11 +469,17 @@ rx_status rx_attend_pages_workspace(int N, int Hq, int Hkv, int D, long long* by
  * out: fp32 [n_pages][page][Hkv], may be the pages' weight; NULL means that.  Other
  * places of out are left as they were.  A page may belong to one stream of a call
  * only.  The same inputs give the same bits.  lse: fp32 [N][Hq] DEVICE (-infinity:
- * the row weighs nothing).  out may not overlap another input.
- * Errors: RX_ERR_ARG, RX_ERR_UNSUPPORTED (D, Hq/Hkv), RX_ERR_CUDA. */
+ * the row weighs nothing).  workspace: DEVICE memory of rx_weigh_pages_workspace
+ * bytes, 256-byte aligned, for this call alone while it runs; may be NULL where
+ * that is 0 (few new tokens).  out and the workspace may not overlap another input
+ * or each other.
+ * Errors: RX_ERR_ARG, RX_ERR_UNSUPPORTED (D, Hq/Hkv), RX_ERR_CAPACITY
+ * (workspace_bytes), RX_ERR_CUDA. */
 rx_status rx_weigh_pages(const void* q, const float* lse, int N, int Hq, int Hkv, int D,
                          const rx_pages* pages, const int* q_start, const int* len, const int* prefix,
-                         float decay, float* out, void* stream);
+                         float decay, float* out, void* workspace, long long workspace_bytes,
+                         void* stream);
+rx_status rx_weigh_pages_workspace(int N, int Hq, int Hkv, long long* bytes);
 
 /* Cut streams back to `budget` keys.  Of a stream with len[b] > budget, every K/V
  * head keeps its first `sink` keys, its last `recent`, and of those between the

@@ -11,9 +11,13 @@
 // atomics: the same inputs give the same bits.  A unit is (stream, K/V head, 128
 // keys); it reads its keys once and all row tiles (128 rows: tokens x heads of the
 // group) that see one of them.  Later keys are seen by fewer rows, so CTAs share
-// the units by their number of row tiles, summed in closed form.  One token per stream is bound by the keys' bytes;
-// a chunk by Q K^T (both operands from shared memory) and, at D = 64, by the
-// exponentials.
+// the units by their number of row tiles and kUnitCost each, summed in closed form.
+// A share may end between two row tiles of a unit: its parts' sums go to the
+// workspace, and a second kernel adds them in their order.  Five chunks of up to 999
+// tokens (32/8 heads of 128) over keys to 8000: 62 us so, 68 with whole units
+// (some 8 per CTA); 512 tokens over 2000 keys of one head of 256: 14 and 28.
+// kUnitCost 4, 1 and 0 gave 64, 63 and 69 us, kMinCut 4 63.  A call with too few
+// rows for a cut has no second kernel.
 //
 // K is the A operand from tensor memory, put there a unit ahead, so that a K slot
 // is free again at once and single tokens' calls keep the memory busy.  What a
@@ -40,7 +44,8 @@ namespace {
 constexpr int kKeys = 128;   // of a unit
 constexpr int kRows = 128;   // of a row tile
 constexpr int kLoaders = 2;  // of them bring the keys into tensor memory
-constexpr int kUnitCost = 4; // of a unit beside its row tiles, in row tiles
+constexpr int kUnitCost = 2; // of a unit beside its row tiles, in row tiles (see above)
+constexpr int kMinCut = 2;   // row tiles on either side of a cut
 
 template <int D>
 struct Layout {
@@ -61,7 +66,8 @@ struct Layout {
   static constexpr int OFF_SUM = OFF_LSE + GROUPS * kRows * 4;   // [groups - 1][128] floats
   static constexpr int OFF_STREAM = OFF_SUM + (GROUPS - 1) * kKeys * 4;   // StreamInfo [B]
   static constexpr int OFF_BEFORE = OFF_STREAM + kMaxPagedStreams * 16;   // long long [B + 1]
-  static constexpr int BYTES = OFF_BEFORE + (kMaxPagedStreams + 1) * 8;
+  static constexpr int OFF_EDGE = OFF_BEFORE + (kMaxPagedStreams + 2) * 8;   // Edge [2]
+  static constexpr int BYTES = OFF_EDGE + 32;
   // Tensor memory: K of two units (the A operand, bf16 pairs), score tiles.
   static constexpr int T_S = D;
   static_assert(T_S + GROUPS * kRows <= 512, "tensor memory");
@@ -76,6 +82,8 @@ enum : int {
   B_UR = 41, B_DRAIN = 42, B_COUNT = 43
 };
 
+struct ShareInfo;
+
 struct WeighParams {
   CUtensorMap tm_k;   // a page's keys, 128 at most (encode_page_map)
   CUtensorMap tm_q;   // 128 query rows (encode_query_map)
@@ -85,6 +93,8 @@ struct WeighParams {
   const int* len;
   const int* prefix;
   float* out;
+  float* part;        // sums of cut units' parts [CTA][2][128]
+  ShareInfo* share;   // [CTA]
   int N, Hq, Hkv, log_g;
   float decay;
   float scale_log2;
@@ -122,68 +132,120 @@ struct StreamUnits {
   }
 };
 
-// One unit: keys [k0, k0 + 128) of a stream, row tiles [r0, r1).
+// One unit, or a part of one: keys [k0, k0 + 128) of a stream, row tiles [r0, r1).
+// slot: where the sums of a part go, -1 for a whole unit.
 struct Unit {
   StreamInfo s;
-  int b, h, k0, x0, r0, r1;
+  int b, h, k0, x0, r0, r1, slot;
 };
 
-// A CTA's units: those whose cost begins in its share of the whole.
+// Where a CTA's share begins: at a row tile of a unit; b = B behind the last.
+struct Edge {
+  int b, h, k0, r;
+  __device__ __forceinline__ bool operator==(const Edge& o) const { return b == o.b && h == o.h && k0 == o.k0 && r == o.r; }
+  __device__ __forceinline__ bool same_unit(const Edge& o) const { return b == o.b && h == o.h && k0 == o.k0; }
+};
+
+// What a CTA's share has of cut units, for the kernel that joins their parts.
+struct ShareInfo {
+  int b, h, k0;   // the unit that begins here and goes on (kOpens)
+  int flags;      // and its keys, times kOneKey
+};
+constexpr int kOpens = 1;      // its last unit begins here and goes on in the next share
+constexpr int kAdds = 2;       // it has a part of a unit that began in an earlier share
+constexpr int kPassesOn = 4;   // that unit goes on in the next share
+constexpr int kOneKey = 8;
+
 struct Units {
   const StreamInfo* info;
   const long long* before;   // cost before stream b [B + 1]
+  const Edge* edge;          // [2]: where this CTA's share begins and ends
   int B, Hkv, log_g;
-  long long left;            // cost that may still begin here
 
-  __device__ __forceinline__ bool begin(Unit* x) {
-    const long long total = before[B];
-    const long long c0 = total * blockIdx.x / gridDim.x, c1 = total * (blockIdx.x + 1) / gridDim.x;
-    if (c0 >= c1) return false;
+  // To the first unit at or behind (b, h, k0); false where there is none.
+  __device__ __forceinline__ bool settle(StreamInfo* s, int* b, int* h, int* k0) const {
+    if (*k0 < s->len) return true;
+    *k0 = 0;
+    if (++*h < Hkv) return true;
+    *h = 0;
+    do {
+      if (++*b >= B) return false;
+      *s = info[*b];
+    } while (s->n == 0 || s->len == 0);
+    return true;
+  }
+  // The edge at `pos` of the whole cost.  A unit is cut between its row tiles where
+  // that leaves both sides kMinCut of them (edges stay in the order of pos).
+  __device__ __forceinline__ Edge at(long long pos) const {
+    if (pos >= before[B]) return Edge{B, 0, 0, 0};
     int lo = 0, hi = B - 1;
-    while (lo < hi) {   // the last stream that begins at or before c0
+    while (lo < hi) {   // the last stream that begins at or before pos
       const int mid = (lo + hi + 1) >> 1;
-      if (before[mid] <= c0) lo = mid;
+      if (before[mid] <= pos) lo = mid;
       else hi = mid - 1;
     }
-    x->b = lo;
-    const StreamUnits su{info[lo], log_g};
+    StreamUnits su{info[lo], log_g};
     const int blocks = su.blocks();
-    const long long each = su.cost(blocks), o = c0 - before[lo];
-    x->h = static_cast<int>(o / each);
-    const long long r = o - x->h * each;
-    int b0 = 0, b1 = blocks;   // the first block that begins at or after r
+    const long long each = su.cost(blocks), o = pos - before[lo];
+    Edge e{lo, static_cast<int>(o / each), 0, 0};
+    const long long r = o - e.h * each;
+    int b0 = 0, b1 = blocks - 1;   // the last block that begins at or before r
     while (b0 < b1) {
-      const int mid = (b0 + b1) >> 1;
-      if (su.cost(mid) >= r) b1 = mid;
-      else b0 = mid + 1;
+      const int mid = (b0 + b1 + 1) >> 1;
+      if (su.cost(mid) <= r) b0 = mid;
+      else b1 = mid - 1;
     }
-    left = c1 - c0 - (su.cost(b0) - r);
-    x->k0 = b0 * kKeys;
-    x->s = su.s;
-    return settle(x);
+    const int off = static_cast<int>(r - su.cost(b0)), first = su.first(b0), tiles = su.row_tiles() - first;
+    int t = off - kUnitCost;
+    if (tiles < 2 * kMinCut) t = 2 * off >= tiles + kUnitCost ? tiles : 0;
+    else if (t < kMinCut) t = 0;
+    else if (tiles - t < kMinCut) t = tiles;
+    e.k0 = b0 * kKeys;
+    e.r = first + t;
+    if (t == tiles) {
+      e.k0 += kKeys;
+      if (!settle(&su.s, &e.b, &e.h, &e.k0)) return Edge{B, 0, 0, 0};
+      e.r = su.first(e.k0 / kKeys);
+    }
+    return e;
   }
-  __device__ __forceinline__ bool next(Unit* x) {
-    left -= x->r1 - x->r0 + kUnitCost;
+  __device__ __forceinline__ int first(const Edge& e) const { return e.b < B ? StreamUnits{info[e.b], log_g}.first(e.k0 / kKeys) : 0; }
+  __device__ __forceinline__ ShareInfo share() const {
+    const Edge a = edge[0], e = edge[1];
+    const bool cut0 = a.r > first(a), cut1 = e.r > first(e), same = a.same_unit(e);
+    int flags = 0;
+    if (cut1 && !(same && cut0)) flags |= kOpens | min(kKeys, info[e.b].len - e.k0) * kOneKey;
+    if (cut0 && !(a == e)) flags |= kAdds;
+    if (cut0 && same) flags |= kPassesOn;
+    return ShareInfo{e.b, e.h, e.k0, flags};
+  }
+
+  __device__ __forceinline__ bool begin(Unit* x) const {
+    const Edge e = edge[0];
+    if (e == edge[1]) return false;
+    x->b = e.b;
+    x->h = e.h;
+    x->k0 = e.k0;
+    x->s = info[e.b];
+    return set(x, e.r);
+  }
+  __device__ __forceinline__ bool next(Unit* x) const {
+    if (x->r1 < StreamUnits{x->s, log_g}.row_tiles()) return false;   // cut: the share's end
     x->k0 += kKeys;
-    return settle(x);
+    return settle(&x->s, &x->b, &x->h, &x->k0) && set(x, 0);
   }
-  // Past the end of a head or a stream to the next one with units.
-  __device__ __forceinline__ bool settle(Unit* x) {
-    if (left <= 0) return false;
-    if (x->k0 >= x->s.len) {
-      x->k0 = 0;
-      if (++x->h == Hkv) {
-        x->h = 0;
-        do {
-          if (++x->b >= B) return false;
-          x->s = info[x->b];
-        } while (x->s.n == 0 || x->s.len == 0);
-      }
-    }
+  __device__ __forceinline__ bool set(Unit* x, int from) const {
     const StreamUnits su{x->s, log_g};
+    const Edge e = edge[1];
+    const int first = su.first(x->k0 / kKeys);
     x->x0 = x->s.len - x->s.n;
-    x->r0 = su.first(x->k0 / kKeys);
+    x->r0 = max(from, first);
     x->r1 = su.row_tiles();
+    if (e.same_unit(Edge{x->b, x->h, x->k0, 0})) {
+      if (e.r <= x->r0) return false;
+      x->r1 = e.r;
+    }
+    x->slot = x->r0 > first ? 2 * blockIdx.x : x->r1 < su.row_tiles() ? 2 * blockIdx.x + 1 : -1;
     return true;
   }
 };
@@ -264,9 +326,16 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) page_weigh_kernel(const
   }
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
+  Edge* edge = reinterpret_cast<Edge*>(gbase + Lay::OFF_EDGE);
+  const Units units{info, before, edge, p.pool.B, p.Hkv, p.log_g};
+  if (threadIdx.x == 0 || threadIdx.x == 32) {
+    const int c = blockIdx.x + (threadIdx.x >> 5);
+    edge[threadIdx.x >> 5] = units.at(before[p.pool.B] * c / gridDim.x);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && p.share) p.share[blockIdx.x] = units.share();
   const int lp = p.pool.log_page;
   const int box = lp < 7 ? 1 << lp : kKeys;
-  Units units{info, before, p.pool.B, p.Hkv, p.log_g, 0};
   Unit x;
   const bool some = units.begin(&x);
 
@@ -446,7 +515,7 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) page_weigh_kernel(const
       const int j = now.k0 + key;
       const long long row = j < now.s.len ? pool_row(p.pool, now.b, j) : -1;
       const size_t place = static_cast<size_t>(row < 0 ? 0 : row) * p.Hkv + now.h;
-      const float old = group == 0 && row >= 0 && p.decay != 0.f ? p.pool.weight[place] : 0.f;
+      const float old = group == 0 && now.slot < 0 && row >= 0 && p.decay != 0.f ? p.pool.weight[place] : 0.f;
       if (ok && more) ok = load_k(v + 1);   // the next unit's keys, ahead of this one's tiles
       // First row that sees the key.
       const int first = j < now.s.prefix ? 0 : max(0, j - now.x0) << p.log_g;
@@ -501,7 +570,8 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) page_weigh_kernel(const
         for (int i = 0; i < Lay::GROUPS - 1; ++i) got += s_sum[i * kKeys + key];
         if (!ok) got = NAN;   // a wait gave up
         if (ok) mbar_arrive(BAR(B_UR));
-        if (row >= 0) p.out[place] = p.decay == 0.f ? got : fmaf(p.decay, old, got);
+        if (now.slot >= 0) p.part[now.slot * kKeys + key] = got;
+        else if (row >= 0) p.out[place] = p.decay == 0.f ? got : fmaf(p.decay, old, got);
       }
       ++v;
     }
@@ -513,6 +583,37 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) page_weigh_kernel(const
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+struct JoinParams {
+  PagePool pool;
+  const float* part;
+  const ShareInfo* share;
+  float* out;
+  int Hkv, ctas;
+  float decay;
+};
+
+// A cut unit's sums: its parts added in their order, by the block of the share
+// where it begins.
+__global__ void __launch_bounds__(kKeys) page_weigh_join_kernel(const __grid_constant__ JoinParams p) {
+  extern __shared__ int s_flags[];   // [ctas]
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int key = threadIdx.x, c0 = blockIdx.x;
+  const ShareInfo u = p.share[c0];
+  if (!(u.flags & kOpens)) return;
+  for (int c = c0 + key; c < p.ctas; c += kKeys) s_flags[c] = p.share[c].flags;
+  float sum = __ldcg(p.part + (2 * c0 + 1) * kKeys + key);
+  const long long row = key < u.flags / kOneKey ? pool_row(p.pool, u.b, u.k0 + key) : -1;
+  const size_t place = static_cast<size_t>(row < 0 ? 0 : row) * p.Hkv + u.h;
+  const float old = row >= 0 && p.decay != 0.f ? p.pool.weight[place] : 0.f;
+  __syncthreads();
+  for (int c = c0 + 1; c < p.ctas; ++c) {
+    if (s_flags[c] & kAdds) sum += __ldcg(p.part + 2 * c * kKeys + key);
+    if (!(s_flags[c] & kPassesOn)) break;
+  }
+  if (row >= 0) p.out[place] = p.decay == 0.f ? sum : fmaf(p.decay, old, sum);
+}
+
 template <int D>
 cudaError_t launch_d(const WeighParams& p, int dev, int sms, cudaStream_t s) {
   using Lay = Layout<D>;
@@ -522,12 +623,23 @@ cudaError_t launch_d(const WeighParams& p, int dev, int sms, cudaStream_t s) {
   });
   if (e != cudaSuccess) return e;
   e = launch_k(page_weigh_kernel<D>, dim3(sms), dim3(Lay::THREADS), Lay::BYTES + 1024, s, p);
+  if (e != cudaSuccess) return e;
+  if (p.share) {
+    const JoinParams j{p.pool, p.part, p.share, p.out, p.Hkv, sms, p.decay};
+    e = launch_k(page_weigh_join_kernel, dim3(sms), dim3(kKeys), sms * sizeof(int), s, j);
+  }
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_weigh_pages(const PageWeights& a, const PagePool& pool, cudaStream_t s) {
+// Nothing where no stream can have a unit that is cut.
+size_t weigh_pages_workspace(int N, int G, int num_sms) {
+  if (static_cast<long long>(N) * G <= (2 * kMinCut - 1) * kRows) return 0;
+  return num_sms * (2 * kKeys * sizeof(float) + sizeof(ShareInfo));
+}
+
+cudaError_t launch_weigh_pages(const PageWeights& a, const PagePool& pool, void* ws, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = device_sm_count(dev, &sms);
@@ -543,6 +655,10 @@ cudaError_t launch_weigh_pages(const PageWeights& a, const PagePool& pool, cudaS
   p.len = a.len;
   p.prefix = a.prefix;
   p.out = a.out;
+  if (weigh_pages_workspace(a.N, G, sms)) {
+    p.part = static_cast<float*>(ws);
+    p.share = reinterpret_cast<ShareInfo*>(p.part + static_cast<size_t>(sms) * 2 * kKeys);
+  }
   p.N = a.N;
   p.Hq = a.Hq;
   p.Hkv = a.Hkv;

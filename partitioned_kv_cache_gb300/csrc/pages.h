@@ -132,7 +132,8 @@ struct PageWeights {
   float decay;
   int N, Hq, Hkv, D;
 };
-cudaError_t launch_weigh_pages(const PageWeights& a, const PagePool& pool, cudaStream_t s);
+size_t weigh_pages_workspace(int N, int G, int num_sms);
+cudaError_t launch_weigh_pages(const PageWeights& a, const PagePool& pool, void* ws, cudaStream_t s);
 
 constexpr int kMaxPagedStreams = 1024;   // of one call: their plans go through shared memory
 

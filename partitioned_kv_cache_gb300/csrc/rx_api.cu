@@ -1007,8 +1007,25 @@ rx_status rx_attend_pages(rx_cache_t h, int layer, const void* q, int N, int Hq,
   RX_GUARD_END
 }
 
+rx_status rx_weigh_pages_workspace(int N, int Hq, int Hkv, long long* bytes) {
+  RX_GUARD_BEGIN
+  const char* where = "rx_weigh_pages_workspace";
+  if (!bytes) return fail(RX_ERR_ARG, "%s: null pointer", where);
+  if (N < 0) return fail(RX_ERR_ARG, "%s: N < 0", where);
+  rx_status st = check_queries(where, nullptr, 0, Hq, Hkv, nullptr, nullptr, nullptr);
+  if (st != RX_OK) return st;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = rx::device_sm_count(dev, &sms);
+  if (e != cudaSuccess) return cuda_fail(e, where);
+  *bytes = static_cast<long long>(rx::weigh_pages_workspace(N, Hq / Hkv, sms));
+  return RX_OK;
+  RX_GUARD_END
+}
+
 rx_status rx_weigh_pages(const void* q, const float* lse, int N, int Hq, int Hkv, int D, const rx_pages* pages,
-                         const int* q_start, const int* len, const int* prefix, float decay, float* out, void* stream) {
+                         const int* q_start, const int* len, const int* prefix, float decay, float* out, void* workspace,
+                         long long workspace_bytes, void* stream) {
   RX_GUARD_BEGIN
   const char* where = "rx_weigh_pages";
   rx::PagePool pool{};
@@ -1020,17 +1037,26 @@ rx_status rx_weigh_pages(const void* q, const float* lse, int N, int Hq, int Hkv
   if (N == 0 || pool.B == 0) return RX_OK;
   if (!out) out = pool.weight;
   if (!out || !lse || (decay != 0.f && !pool.weight)) return fail(RX_ERR_ARG, "%s: null pointer", where);
-  if (!aligned4(out) || !aligned4(lse)) return fail(RX_ERR_ARG, "%s: misaligned pointer", where);
+  if (!aligned4(out) || !aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return fail(RX_ERR_ARG, "%s: misaligned pointer", where);
   const long long lens = pool.B * 4LL;
   const long long wb = static_cast<long long>(pool.n_pages) * pages->page * Hkv * 4;
   const Span in[8] = {{q, static_cast<long long>(N) * Hq * D * 2}, {lse, static_cast<long long>(N) * Hq * 4}, g[0], g[3],
                       {q_start, lens + 4}, {len, lens}, {prefix, lens}, out == pool.weight ? Span{nullptr, 0} : g[2]};
-  const Span outs[1] = {{out, wb}};
-  st = check_apart(where, outs, 1, in, 8);
+  const Span outs[2] = {{out, wb}, {workspace, workspace ? workspace_bytes : 0}};
+  st = check_apart(where, outs, 2, in, 8);
   if (st != RX_OK) return st;
   if (spans_overlap(out, wb, g[1].p, g[1].bytes)) return fail(RX_ERR_ARG, "%s: out overlaps the values", where);
+  int dev = -1, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = rx::device_sm_count(dev, &sms);
+  if (e != cudaSuccess) return cuda_fail(e, where);
+  const long long need = static_cast<long long>(rx::weigh_pages_workspace(N, Hq / Hkv, sms));
+  if (need && !workspace) return fail(RX_ERR_ARG, "%s: the call needs a workspace", where);
+  if (workspace_bytes < need)
+    return fail(RX_ERR_CAPACITY, "%s: the workspace has %lld bytes, the call needs %lld", where, workspace_bytes, need);
   const rx::PageWeights a{q, lse, q_start, len, prefix, out, decay, N, Hq, Hkv, D};
-  const cudaError_t e = rx::launch_weigh_pages(a, pool, static_cast<cudaStream_t>(stream));
+  e = rx::launch_weigh_pages(a, pool, workspace, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rx_weigh_pages: launch");
   return RX_OK;
   RX_GUARD_END

@@ -36,7 +36,7 @@ EXPORTS = ("rx_cache_create", "rx_cache_destroy", "rx_pin_prefix", "rx_push_fram
            "rx_attend_suffix_norms", "rx_attend_batch_norms", "rx_tail_append_quant",
            "rx_attend_streams_quant", "rx_verify_drafts", "rx_debug_choose_stream_partition",
            "rx_rotate_heads", "rx_rotate_heads_paged", "rx_attend_pages", "rx_attend_pages_workspace",
-           "rx_weigh_pages", "rx_evict_pages", "rx_debug_page_plan")
+           "rx_weigh_pages", "rx_weigh_pages_workspace", "rx_evict_pages", "rx_debug_page_plan")
 
 
 class RxConfig(ctypes.Structure):
@@ -122,7 +122,8 @@ _sigs = {
     "rx_attend_pages": (_i, [_vp, _i, _vp, _i, _i, _i, _i, ctypes.POINTER(RxPages), _vp, _vp, _vp, _vp, _vp, _vp,
                              ctypes.c_longlong, _vp]),
     "rx_attend_pages_workspace": (_i, [_i, _i, _i, _i, ctypes.POINTER(ctypes.c_longlong)]),
-    "rx_weigh_pages": (_i, [_vp, _vp, _i, _i, _i, _i, ctypes.POINTER(RxPages), _vp, _vp, _vp, _f, _vp, _vp]),
+    "rx_weigh_pages": (_i, [_vp, _vp, _i, _i, _i, _i, ctypes.POINTER(RxPages), _vp, _vp, _vp, _f, _vp, _vp, ctypes.c_longlong, _vp]),
+    "rx_weigh_pages_workspace": (_i, [_i, _i, _i, ctypes.POINTER(ctypes.c_longlong)]),
     "rx_evict_pages": (_i, [ctypes.POINTER(RxPages), _i, _i, _vp, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _vp]),
     "rx_debug_page_plan": (_i, [_i] * 7 + [ctypes.POINTER(ctypes.c_longlong), ctypes.POINTER(_i)]),
     "rx_verify_drafts": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]),
@@ -802,8 +803,18 @@ def attend_pages_workspace(N: int, Hq: int, Hkv: int, D: int) -> int:
     return n.value
 
 
-#: attend_pages_workspace() by (device, N, Hq, Hkv, D).
+#: attend_pages_workspace() by (device, N, Hq, Hkv, D) and weigh_pages_workspace()
+#: by (device, N, Hq, Hkv).
 _workspace_sizes: dict = {}
+
+
+def _workspace_size(dev, of, *shape):
+    size = _workspace_sizes.get((dev,) + shape)
+    if size is None:
+        if len(_workspace_sizes) >= 4096:
+            _workspace_sizes.clear()
+        size = _workspace_sizes[(dev,) + shape] = of(*shape)
+    return size
 
 
 def _attend_pages(cache, layer, q, pages, q_start, length, prefix, out, lse, workspace, stream):
@@ -833,12 +844,7 @@ def _attend_pages(cache, layer, q, pages, q_start, length, prefix, out, lse, wor
             given = torch.empty((N, Hq), dtype=f32, device=q.device)
             ep = given.data_ptr()
         if workspace is None:
-            key = dev, N, Hq, Hkv, D
-            size = _workspace_sizes.get(key)
-            if size is None:
-                if len(_workspace_sizes) >= 4096:
-                    _workspace_sizes.clear()
-                size = _workspace_sizes[key] = attend_pages_workspace(N, Hq, Hkv, D)
+            size = _workspace_size(dev, attend_pages_workspace, N, Hq, Hkv, D)
             workspace = torch.empty(size, dtype=u8, device=q.device)
             wp = workspace.data_ptr()
     _check(_lib.rx_attend_pages(None if cache is None else cache._h, layer, qp, N, Hq, Hkv, D, ctypes.byref(g), sp, lp, pp,
@@ -861,13 +867,22 @@ def attend_pages(q: torch.Tensor, pages: Pages, q_start: torch.Tensor, length: t
     return _attend_pages(None, 0, q, pages, q_start, length, prefix, out, lse, workspace, stream)
 
 
+def weigh_pages_workspace(N: int, Hq: int, Hkv: int) -> int:
+    """Bytes of workspace that weigh_pages needs for N new tokens: 0 for few."""
+    n = ctypes.c_longlong(0)
+    _check(_lib.rx_weigh_pages_workspace(N, Hq, Hkv, ctypes.byref(n)), "rx_weigh_pages_workspace")
+    return n.value
+
+
 def weigh_pages(q: torch.Tensor, lse: torch.Tensor, pages: Pages, q_start: torch.Tensor, length: torch.Tensor,
                 prefix: Optional[torch.Tensor] = None, decay: float = 1.0, out: Optional[torch.Tensor] = None,
-                stream=None) -> torch.Tensor:
+                workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Add the attention weight of a step's new tokens to the keys that they saw:
     out = decay * pages.weight + the sum of exp(score - lse), for every key of a
     stream with new tokens (rx_weigh_pages).  Arguments as of attend_pages, lse
-    its second result.  out: fp32 like pages.weight (None: in place)."""
+    its second result.  out: fp32 like pages.weight (None: in place).  workspace:
+    uint8, weigh_pages_workspace() bytes, for this call alone while it runs;
+    allocated if not given and needed."""
     if q.dim() != 3 or pages.k.dim() != 4:
         raise ValueError("q must have shape [N][Hq][D] and pages [n_pages][page][Hkv][D]")
     N, Hq, D = q.shape
@@ -880,10 +895,17 @@ def weigh_pages(q: torch.Tensor, lse: torch.Tensor, pages: Pages, q_start: torch
     if out is None:
         raise ValueError("the pages have no weight")
     dev, st = _here(stream)
-    g, (qp, ep, sp, lp, pp, op) = _pages(dev, pages, (
+    g, (qp, ep, sp, lp, pp, op, wp) = _pages(dev, pages, (
         (q, torch.bfloat16, (N, Hq, D), "q"), (lse, f32, (N, Hq), "lse"), (q_start, i32, (B + 1,), "q_start"),
-        (length, i32, each, "length"), (prefix, i32, each, "prefix"), (out, f32, pages.k.shape[:3], "out")))
-    _check(_lib.rx_weigh_pages(qp, ep, N, Hq, Hkv, D, ctypes.byref(g), sp, lp, pp, float(decay), op, st), "rx_weigh_pages")
+        (length, i32, each, "length"), (prefix, i32, each, "prefix"), (out, f32, pages.k.shape[:3], "out"),
+        (workspace, torch.uint8, None if workspace is None else workspace.shape, "workspace")))
+    size = _workspace_size(dev, weigh_pages_workspace, N, Hq, Hkv) if workspace is None else workspace.numel()
+    if workspace is None and size:
+        with _outputs(stream):
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+        wp = workspace.data_ptr()
+    _check(_lib.rx_weigh_pages(qp, ep, N, Hq, Hkv, D, ctypes.byref(g), sp, lp, pp, float(decay), op, wp, size, st),
+           "rx_weigh_pages")
     return out
 
 

@@ -146,9 +146,10 @@ def test_attention_and_weights_refuse_bad_arguments(lib):
         return rx._lib.rx_attend_pages(None, 0, q, N, Hq, Hkv, D, ctypes.byref(pages or _pages(rx, p)), q_start, length, prefix, out,
                                        lse, ws, size, None)
 
-    def weigh(N=3, Hq=2, Hkv=1, D=64, pages=None, q=q, q_start=qs, length=ln, prefix=None, out=p + 32768, lse=lse, decay=1.0):
+    def weigh(N=3, Hq=2, Hkv=1, D=64, pages=None, q=q, q_start=qs, length=ln, prefix=None, out=p + 32768, lse=lse, decay=1.0, ws=None,
+              size=0):
         return rx._lib.rx_weigh_pages(q, lse, N, Hq, Hkv, D, ctypes.byref(pages or _pages(rx, p)), q_start, length, prefix, decay,
-                                      out, None)
+                                      out, ws, size, None)
     for call in (attend, weigh):
         assert call(N=0) == 0 and call(pages=_pages(rx, p, B=0)) == 0
         for bad in BAD_PAGES:
@@ -169,6 +170,10 @@ def test_attention_and_weights_refuse_bad_arguments(lib):
     f = rx._lib.rx_attend_pages_workspace
     assert f(1, 2, 1, 64, None) == -1 and f(-1, 2, 1, 64, ctypes.byref(n)) == -1 and f(1, 3, 2, 64, ctypes.byref(n)) == -1
     assert f(1, 6, 1, 64, ctypes.byref(n)) == -6 and f(1, 2, 1, 32, ctypes.byref(n)) == -6
+    assert weigh(ws=ws + 16, size=64) == -1 and weigh(ws=q, size=64) == -1 and weigh(ws=p + 32768, size=64) == -1
+    f = rx._lib.rx_weigh_pages_workspace
+    assert f(1, 2, 1, None) == -1 and f(-1, 2, 1, ctypes.byref(n)) == -1 and f(1, 3, 2, ctypes.byref(n)) == -1
+    assert f(1, 6, 1, ctypes.byref(n)) == -6
     del keep
 
 

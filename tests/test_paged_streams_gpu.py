@@ -550,6 +550,21 @@ def test_weight_with_pages_that_are_not_named_and_rows_that_see_nothing(rx):
     _weigh_case(rx, g, pool, [2, 5, 3, 20, 1], 8)
 
 
+@pytest.mark.parametrize("lens,new,Hq,Hkv,D,page,prefix,decay", [
+    ([400], [300], 8, 1, 256, 64, None, 0.5),             # fewer keys than CTAs have: every share is a part
+    ([130, 700], [127, 260], 4, 1, 64, 16, [60, 300], 1.0),
+    ([900, 0, 333, 1500], [450, 7, 0, 600], 16, 2, 128, 32, [0, 0, 9, 1500], 0.0),
+    ([0, 640, 50], [2, 640, 33], 32, 1, 64, 256, None, 1.0),
+])
+def test_weight_of_chunks_that_several_ctas_share(rx, lens, new, Hq, Hkv, D, page, prefix, decay):
+    """Few keys and many rows: a block of keys is cut between row tiles."""
+    g = np.random.default_rng([lens[0], Hq])
+    pool = Pool(g, lens, page, Hkv, D).fill(g)
+    pool.table[-1][min(2, len(pool.table[-1]) - 1)] = -1
+    assert rx.weigh_pages_workspace(sum(new), Hq, Hkv) > 0
+    _weigh_case(rx, g, pool, new, Hq, prefix=prefix, decay=decay, apart=prefix is not None)
+
+
 def test_weight_without_decay_does_not_read_the_old(rx):
     g = np.random.default_rng(6)
     pool = Pool(g, [100, 20], 32, 2, 64).fill(g)
@@ -856,6 +871,15 @@ def test_workspace_too_small_or_cache_of_other_heads_is_refused(rx):
     rx.attend_pages(*args, workspace=ws)
     with pytest.raises(rx.RxError, match="workspace"):
         rx.attend_pages(*args, workspace=ws[:need - 1])
+    assert rx.weigh_pages_workspace(1, 2, 1) == 0
+    n = 900
+    q, lse = dev(_bits(g, (n, 2, 64))), torch.zeros((n, 2), device="cuda")
+    need = rx.weigh_pages_workspace(n, 2, 1)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    late = (q, lse, args[1], _int([0, n]), _int([20]))
+    rx.weigh_pages(*late, workspace=ws)
+    with pytest.raises(rx.RxError, match="workspace"):
+        rx.weigh_pages(*late, workspace=ws[:need - 1])
     cache = rx.Cache(1, 4, 1, 64, 0, 1, 1, 1)
     with pytest.raises(rx.RxError, match="heads"):
         cache.attend_pages(0, *args)
