@@ -489,6 +489,7 @@ rx_status rx_weigh_pages_workspace(int N, int Hq, int Hkv, long long* bytes);
  * kept[b][h][i].  Shorter streams keep all.  new_len[b] = min(len[b], budget);
  * kept is -1 from there on.
  * to NULL: in place, in pages that belong to one stream of the call each.  Else
+ * (to may not be the pages' own table)
  * the new places are those of the table `to` [B][to_max_pages], whose pages of the
  * same pool are in no other stream's table and not among the old ones (so that a
  * prefix which streams share can be cut for one of them), and the old pages keep

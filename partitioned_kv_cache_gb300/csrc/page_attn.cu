@@ -19,12 +19,26 @@
 // the order of the keys.  Lengths are read on the device.
 //
 // Inside a CTA the steps are those of the suffix's attention: S = Q K^T and
-// O += P V on tcgen05 with accumulators in tensor memory, P (bf16) back to
-// tensor memory as the A operand, O
-// rescaled only when a row's maximum grows by more than 2^8.  A weight enters
-// P V rounded to bf16 (2^-9 of it): beside the output's own rounding it is felt
-// as 0.0017 -> 0.002 in the relative error, and two terms would cost half of
-// P V again.
+// O += P V on tcgen05 with accumulators in tensor memory, Q and P (bf16) the A
+// operands in tensor memory too, O rescaled only when a row's maximum grows by more
+// than 2^8.  (With Q in shared memory a product of 128 x 64 or 128 x 128 takes a
+// quarter longer, for its operand's way out of there.)  A weight enters P V rounded
+// to bf16 (2^-9 of it at most): beside the output's own rounding, 0.0017 relative to
+// the exact result over a call's rows, that makes 0.0023, and two terms would cost
+// P V a second time.
+//
+// What bounds it, and what it took (GB300, a graph of calls):
+//   8 chunks of 2048 tokens, 8 heads over 1 of 256, 8448 shared keys, tails to
+//   8000: the tensor core, 945 us, 1770 TFLOP/s (0.92 of cuBLAS's; hot, at the power
+//   limit, 1560); 1355 us with Q in shared memory and one issuing thread.
+//   32 single tokens, 32/8 heads of 128, tails to 16000: memory, 170 us, 6.1 TB/s.
+//   5 chunks of up to 999 tokens, 32/8 heads of 128, pages of 32: 156 us, 828
+//   TFLOP/s; in the middle of a unit 1086.  A tile of 128 keys there takes some 2200
+//   cycles of which the products are 1030 and the copies 1600 (some 3 cycles for
+//   every 128 bytes of a row and 100 to 200 a copy, whatever the SM count); they
+//   and the softmax's steps meet at every tile's barriers.  (V by 16-byte copies of a
+//   warp of its own instead, beside K's tensor copies: 175 us, and the single tokens
+//   above 202.)
 //
 // Masked places.  Scores are masked by selection, so whatever a place behind
 // the stream's end, in a page that the table does not name, or after a token
@@ -54,8 +68,8 @@ namespace {
 
 constexpr float kRescale = 8.0f;   // log2 units
 constexpr int kMinRunKeys = 256;   // keys of a CTA's run, at least
-constexpr int kUnitPad = 4;        // tiles that a unit's start and end cost: attend_prompts, with units of 11 to
-                                   // 59 tiles, takes 161 us, and 203 with 0
+constexpr int kUnitPad = 4;        // tiles that a unit's start and end cost: chunks with units of 11 to 59 tiles
+                                   // take 161 us, and 203 with 0
 constexpr int kMergeThreads = 256;
 constexpr int kMergeFew = 8;       // parts that one thread of the merge takes
 constexpr int kMergeFlight = 4;    // of them asked for together: with four CTAs an SM, from L2 at its rate
@@ -69,7 +83,8 @@ struct Layout {
   static constexpr int Q_BLOCK = kBM * 128;
   static constexpr int Q_BYTES = KB * Q_BLOCK;
   // Keys of a tile.  A tile's waits, barriers and masks cost the softmax as much as
-  // 64 columns do: 128 keys are better where tensor memory has room for their scores.
+  // 64 columns do: 128 keys are better where tensor memory has room for their scores
+  // (5 chunks of up to 999 tokens, D = 128: 215 us with 64, 208 with 128).
   static constexpr int BN = D == 256 ? 64 : 128;
   static constexpr int BLOCK = BN * 128;                    // 64 columns of a K or V tile
   static constexpr int TILE = KB * BLOCK;
@@ -350,8 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
   if (some && (warp == 0 || warp == 3)) {
     // ------------------------------------------------------------ copies of K, of V
     // The lanes hold the table's next 64 entries, asked for a round ahead; one
-    // issues (copies by several lanes of a warp go one after the other, some 250
-    // cycles each).
+    // issues (copies by several lanes of a warp go one after the other all the same).
     const bool leader = elect_one();
     const bool isv = warp == 3;
     const CUtensorMap* tm = isv ? &p.tm_v : &p.tm_k;
@@ -702,28 +716,28 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
           }
           fence_proxy_async_smem();
           if (unseen < BN) {
-          // Every second or fourth lane's bit, close up.
-          uint32_t rows = __ballot_sync(0xffffffffu, odd != 0);
-          volatile uint8_t* bits = not_finite + (checks & 1) * 16;
-          if constexpr (kShare == 4) {
-            rows &= 0x11111111u;
-            rows = (rows | rows >> 3) & 0x03030303u;
-            rows = (rows | rows >> 6) & 0x000F000Fu;
-            rows = (rows | rows >> 12) & 0x000000FFu;
-            if (lane == 0) bits[warp - 4] = static_cast<uint8_t>(rows);
-          } else {
-            rows &= 0x55555555u;
-            rows = (rows | rows >> 1) & 0x33333333u;
-            rows = (rows | rows >> 2) & 0x0F0F0F0Fu;
-            rows = (rows | rows >> 4) & 0x00FF00FFu;
-            rows = (rows | rows >> 8) & 0x0000FFFFu;
-            if (lane == 0) reinterpret_cast<volatile uint16_t*>(bits)[warp - 4] = static_cast<uint16_t>(rows);
-          }
-          mbar_arrive(BAR(B_CHK));
-          if (!warp_wait(BAR(B_CHK), checks & 1, abort_flag)) { ok = false; break; }
-          ++checks;
+            // Every second or fourth lane's bit, close up.
+            uint32_t rows = __ballot_sync(0xffffffffu, odd != 0);
+            volatile uint8_t* bits = not_finite + (checks & 1) * 16;
+            if constexpr (kShare == 4) {
+              rows &= 0x11111111u;
+              rows = (rows | rows >> 3) & 0x03030303u;
+              rows = (rows | rows >> 6) & 0x000F000Fu;
+              rows = (rows | rows >> 12) & 0x000000FFu;
+              if (lane == 0) bits[warp - 4] = static_cast<uint8_t>(rows);
+            } else {
+              rows &= 0x55555555u;
+              rows = (rows | rows >> 1) & 0x33333333u;
+              rows = (rows | rows >> 2) & 0x0F0F0F0Fu;
+              rows = (rows | rows >> 4) & 0x00FF00FFu;
+              rows = (rows | rows >> 8) & 0x0000FFFFu;
+              if (lane == 0) reinterpret_cast<volatile uint16_t*>(bits)[warp - 4] = static_cast<uint16_t>(rows);
+            }
+            mbar_arrive(BAR(B_CHK));
+            if (!warp_wait(BAR(B_CHK), checks & 1, abort_flag)) { ok = false; break; }
+            ++checks;
 #pragma unroll
-          for (int i = 0; i < BN / 64; ++i) poison = poison || (reinterpret_cast<volatile uint64_t*>(bits)[i] & mine.w[i]) != 0;
+            for (int i = 0; i < BN / 64; ++i) poison = poison || (reinterpret_cast<volatile uint64_t*>(bits)[i] & mine.w[i]) != 0;
           }
         }
         if (++vslot == Lay::NV) {

@@ -19,6 +19,12 @@
 // kUnitCost 4, 1 and 0 gave 64, 63 and 69 us, kMinCut 4 63.  A call with too few
 // rows for a cut has no second kernel.
 //
+// One token per stream is bound by the keys' bytes, at this size by the launch's
+// latency (16 streams of up to 2000 keys: 8 us).  The chunks above run at 910
+// TFLOP/s, at D = 64 chunks run at 430: in both an SM gets through some 12 scores a
+// cycle, so the way from scores to sums is the bound, not K Q^T (half of that time
+// at D = 128) nor memory.
+//
 // K is the A operand from tensor memory, put there a unit ahead, so that a K slot
 // is free again at once and single tokens' calls keep the memory busy.  What a
 // tile costs the issuing warp, its barriers and products, is some 700 cycles: row
@@ -341,8 +347,7 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) page_weigh_kernel(const
 
   if (some && warp == 0) {
     // ---------------------------------------------------------- keys
-    // The lanes hold the pages of a tile; one issues (copies by several lanes of a
-    // warp go one after the other, some 250 cycles each).
+    // The lanes hold the pages of a tile; one issues.
     const bool leader = elect_one();
     const int pages = lp < 7 ? kKeys >> lp : 1;   // of a tile
     auto entry = [&]() {

@@ -62,9 +62,12 @@ __device__ __forceinline__ unsigned long long turn_fraction(float freq) {
 // 16 values each as two chunks of eight, R/16 chunks apart: in half pairs a lane
 // then has both values of its pairs and nothing is exchanged but the norm's sum.
 // (With eight values a lane and the partners fetched from other lanes
-// rotate_prompts took 129 us; with two groups of four, whose loads are 8 bytes
+// the prompts below took 129 us; with two groups of four, whose loads are 8 bytes
 // wide, 192.)  A lane asks for kFlight heads at a time, the first of them before
-// the angles are computed.  Bound by memory: see the figures at launch_d.
+// the angles are computed.  Bound by the loads in flight: 13600 tokens of 48 heads
+// of 128 take 93 us, 4.8 TB/s.  More threads on an SM (64 registers cut to 48 or 40:
+// 117 us), four heads in flight (104) and blocks of 512 threads (105) are slower,
+// blocks of 128 as fast (91; 9.9 for 8.7 us at 2048 tokens).
 template <int D, int TB>
 __global__ void __launch_bounds__(kThreads) rotate_heads_kernel(const __grid_constant__ RotateParams p) {
   constexpr int L = D / 16;              // lanes of a head
@@ -260,8 +263,12 @@ cudaError_t launch_tb(const RotateParams& p, int sms, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_d(const RotateParams& p, int sms, cudaStream_t s) {
-  // One token a CTA while the GPU holds them all at once, else four.
-  return p.N <= sms * 8 ? launch_tb<D, 1>(p, sms, s) : launch_tb<D, 4>(p, sms, s);
+  // One token a CTA while an SM holds all of its CTAs at once (four), else four
+  // tokens, whose angles and streams are looked up together.  With one and with four:
+  // 16 tokens of 10 heads of 256 3.1 and 4.5 us, 600 4.4 and 4.8, 1208 7.5 and 5.9,
+  // 4096 16.5 and 14.1; of 48 heads of 128 600 5.6 and 7.5, 1208 9.9 and 9.0, 4096
+  // 28.2 and 25.0.
+  return p.N <= sms * 4 ? launch_tb<D, 1>(p, sms, s) : launch_tb<D, 4>(p, sms, s);
 }
 
 }  // namespace

@@ -755,8 +755,6 @@ def rotate_heads(x: torch.Tensor, heads: Heads, pos: torch.Tensor, q: Optional[t
     qs, ks, bf16 = (N, heads.Hq, heads.D), (N, heads.Hkv, heads.D), torch.bfloat16
     pp, qp, kp, vp = _addresses(dev, (pos, torch.int32, (heads.axes, N), "pos"), (q, bf16, qs, "q"), (k, bf16, ks, "k"),
                                 (v, bf16, ks, "v"))
-    # (Outputs are allocated last: beside the launch of the call before, the
-    # allocator takes some microseconds more than behind the checks.)
     if q is None or k is None or v is None:
         with _outputs(stream):
             q = x.new_empty(qs) if q is None else q
@@ -836,7 +834,7 @@ def _attend_pages(cache, layer, q, pages, q_start, length, prefix, out, lse, wor
         (prefix, i32, each, "prefix"), (out, bf16, rows, "out"), (given, f32, (N, Hq), "lse"),
         (workspace, u8, None if workspace is None else workspace.shape, "workspace")))
     size = 0 if workspace is None else workspace.numel()
-    with _outputs(stream):   # (after the checks, as in rotate_heads)
+    with _outputs(stream):
         if out is None:
             out = torch.empty_like(q)
             op = out.data_ptr()
