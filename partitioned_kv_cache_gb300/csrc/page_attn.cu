@@ -32,7 +32,7 @@
 //   8000: the tensor core, 945 us, 1770 TFLOP/s (0.92 of cuBLAS's; hot, at the power
 //   limit, 1560); 1355 us with Q in shared memory and one issuing thread.
 //   32 single tokens, 32/8 heads of 128, tails to 16000: memory, 170 us, 6.1 TB/s.
-//   5 chunks of up to 999 tokens, 32/8 heads of 128, pages of 32: 156 us, 828
+//   5 chunks of up to 999 tokens, 32/8 heads of 128, pages of 32: 153 us, 842
 //   TFLOP/s; in the middle of a unit 1086.  A tile of 128 keys there takes some 2200
 //   cycles of which the products are 1030 and the copies 1600 (some 3 cycles for
 //   every 128 bytes of a row and 100 to 200 a copy, whatever the SM count); they
@@ -71,8 +71,13 @@ constexpr int kMinRunKeys = 256;   // keys of a CTA's run, at least
 constexpr int kUnitPad = 4;        // tiles that a unit's start and end cost: chunks with units of 11 to 59 tiles
                                    // take 161 us, and 203 with 0
 constexpr int kMergeThreads = 256;
-constexpr int kMergeFew = 8;       // parts that one thread of the merge takes
-constexpr int kMergeFlight = 4;    // of them asked for together: with four CTAs an SM, from L2 at its rate
+// The merge is bound by its instructions and the depth of its loads.  Up to kMergeFew
+// parts one thread joins 16 columns of a row, two parts at a time: 153 us for the five
+// chunks above, where a thread per four columns took 155, and 47 us for a chunk of 512
+// beside 16 single tokens, where one part at a time took 48.5.  More parts are shared by
+// eight warps, kMergeFlight of a warp's asked for together.
+constexpr int kMergeFew = 8;
+constexpr int kMergeFlight = 4;
 
 constexpr int kThreads = 384;
 constexpr int kSoftmax = 256;      // of them two per query row
@@ -883,7 +888,7 @@ struct MergeParams {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads, 4) page_merge_kernel(const __grid_constant__ MergeParams p) {
+__global__ void __launch_bounds__(kMergeThreads, 3) page_merge_kernel(const __grid_constant__ MergeParams p) {
   extern __shared__ int s_before[];   // chunks before CTA c's unit [ctas + 1]
   __shared__ float4 s_o[8][32];
   __shared__ float2 s_ml[8][32];
@@ -897,8 +902,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) page_merge_kernel(const __gr
     int x = 0;
     if (c < p.ctas) {
       const CutUnit u = p.cut[c];
-      const int per = u.parts <= kMergeFew ? kMergeThreads : 32;
-      x = (u.rows * (D / 4) + per - 1) / per;
+      x = u.parts <= kMergeFew ? (u.rows * (D / 16) + kMergeThreads - 1) / kMergeThreads : (u.rows * (D / 4) + 31) / 32;
     }
     int y = x;
 #pragma unroll
@@ -926,29 +930,84 @@ __global__ void __launch_bounds__(kMergeThreads, 4) page_merge_kernel(const __gr
       else hi = mid - 1;
     }
     const CutUnit u = p.cut[lo];
-    const bool few = u.parts <= kMergeFew;
+    const int G = 1 << p.log_g, nth = chunk - s_before[lo];
+    auto slot_of = [&](int s) { return s == 0 ? 2 * static_cast<size_t>(lo) + 1 : 2 * static_cast<size_t>(lo + s); };
+    auto place_of = [&](int row) { return static_cast<size_t>(u.token + (row >> p.log_g)) * p.Hq + u.head * G + (row & (G - 1)); };
+    auto write_lse = [&](size_t at, float M, float L) {
+      if (p.lse) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
+    };
+    const size_t stride = static_cast<size_t>(D / 4) * p.part_rows;
+    if (u.parts <= kMergeFew) {
+      // A thread takes 16 columns of a row.
+      const int item = nth * kMergeThreads + static_cast<int>(threadIdx.x);
+      if (item >= u.rows * (D / 16)) continue;
+      const int row = item % u.rows, k = item / u.rows * 4;
+      float2 ml[kMergeFew];
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int i = 0; i < kMergeFew; ++i)
+        ml[i] = i < u.parts ? __ldcg(p.part_ml + slot_of(i) * p.part_rows + row) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int i = 0; i < kMergeFew; ++i) M = fmaxf(M, ml[i].x);
+      const float ref = M == -INFINITY ? 0.f : M;
+      float4 acc[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i0 = 0; i0 < kMergeFew; i0 += 2) {   // two parts asked for together
+        if (i0 >= u.parts) break;
+        float4 o[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int i = min(i0 + j, u.parts - 1);   // (a part behind the last weighs nothing)
+          const float4* po = p.part + slot_of(i) * stride + static_cast<size_t>(k) * p.part_rows + row;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[j][c] = __ldcg(po + c * p.part_rows);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (i0 + j >= u.parts) break;
+          const float g = exp2f(ml[i0 + j].x - ref);   // 0 for a part that saw nothing
+          L = fmaf(g, ml[i0 + j].y, L);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            acc[c].x = fmaf(g, o[j][c].x, acc[c].x);
+            acc[c].y = fmaf(g, o[j][c].y, acc[c].y);
+            acc[c].z = fmaf(g, o[j][c].z, acc[c].z);
+            acc[c].w = fmaf(g, o[j][c].w, acc[c].w);
+          }
+        }
+      }
+      const float inv = L > 0.f ? 1.f / L : L;
+      const size_t at = place_of(row);
+      uint4* out = reinterpret_cast<uint4*>(p.out + at * D + k * 4);
+#pragma unroll
+      for (int c = 0; c < 4; c += 2)
+        out[c / 2] = make_uint4(pack_bf16x2(acc[c].x * inv, acc[c].y * inv), pack_bf16x2(acc[c].z * inv, acc[c].w * inv),
+                                pack_bf16x2(acc[c + 1].x * inv, acc[c + 1].y * inv), pack_bf16x2(acc[c + 1].z * inv, acc[c + 1].w * inv));
+      if (k == 0) write_lse(at, M, L);
+      continue;
+    }
+    // Many parts: a warp takes every eighth of them, four columns of a row a lane.
     const int items = u.rows * (D / 4);
-    const int want = (chunk - s_before[lo]) * (few ? kMergeThreads : 32) + (few ? static_cast<int>(threadIdx.x) : lane);
+    const int want = nth * 32 + lane;
     const int item = min(want, items - 1);
     const int row = item % u.rows, k = item / u.rows;
     const float4* po = p.part + static_cast<size_t>(k) * p.part_rows + row;
     const float2* pm = p.part_ml + row;
-    const size_t stride = static_cast<size_t>(D / 4) * p.part_rows;
     float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int first = few ? 0 : warp, step = few ? 1 : 8;
-    for (int s0 = first; s0 < u.parts; s0 += kMergeFlight * step) {
+    for (int s0 = warp; s0 < u.parts; s0 += kMergeFlight * 8) {
       float4 o[kMergeFlight];
       float2 ml[kMergeFlight];
 #pragma unroll
       for (int i = 0; i < kMergeFlight; ++i) {
-        const int s = s0 + i * step;
+        const int s = s0 + i * 8;
         ml[i] = make_float2(-INFINITY, 0.f);
         o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (s < u.parts) {
-          const size_t slot = s == 0 ? 2 * static_cast<size_t>(lo) + 1 : 2 * static_cast<size_t>(lo + s);
-          ml[i] = __ldcg(pm + slot * p.part_rows);
-          o[i] = __ldcg(po + slot * stride);
+          ml[i] = __ldcg(pm + slot_of(s) * p.part_rows);
+          o[i] = __ldcg(po + slot_of(s) * stride);
         }
       }
       float m = M;
@@ -969,38 +1028,35 @@ __global__ void __launch_bounds__(kMergeThreads, 4) page_merge_kernel(const __gr
         acc.w = fmaf(g, o[i].w, acc.w);
       }
     }
-    if (!few) {
-      s_o[warp][lane] = acc;
-      s_ml[warp][lane] = make_float2(M, L);
-      __syncthreads();
-      if (warp == 0) {
+    s_o[warp][lane] = acc;
+    s_ml[warp][lane] = make_float2(M, L);
+    __syncthreads();
+    if (warp == 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) M = fmaxf(M, s_ml[i][lane].x);
-        const float ref = M == -INFINITY ? 0.f : M;
-        L = 0.f;
-        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < 8; ++i) M = fmaxf(M, s_ml[i][lane].x);
+      const float ref = M == -INFINITY ? 0.f : M;
+      L = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 ml = s_ml[i][lane];
-          const float4 o = s_o[i][lane];
-          const float g = exp2f(ml.x - ref);
-          L = fmaf(g, ml.y, L);
-          acc.x = fmaf(g, o.x, acc.x);
-          acc.y = fmaf(g, o.y, acc.y);
-          acc.z = fmaf(g, o.z, acc.z);
-          acc.w = fmaf(g, o.w, acc.w);
-        }
+      for (int i = 0; i < 8; ++i) {
+        const float2 ml = s_ml[i][lane];
+        const float4 o = s_o[i][lane];
+        const float g = exp2f(ml.x - ref);
+        L = fmaf(g, ml.y, L);
+        acc.x = fmaf(g, o.x, acc.x);
+        acc.y = fmaf(g, o.y, acc.y);
+        acc.z = fmaf(g, o.z, acc.z);
+        acc.w = fmaf(g, o.w, acc.w);
       }
     }
-    if (want < items && (few || warp == 0)) {
+    if (want < items && warp == 0) {
       const float inv = L > 0.f ? 1.f / L : L;
-      const int G = 1 << p.log_g;
-      const size_t at = static_cast<size_t>(u.token + (row >> p.log_g)) * p.Hq + u.head * G + (row & (G - 1));
+      const size_t at = place_of(row);
       *reinterpret_cast<uint2*>(p.out + at * D + k * 4) =
           make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-      if (k == 0 && p.lse) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
+      if (k == 0) write_lse(at, M, L);
     }
-    if (!few) __syncthreads();
+    __syncthreads();
   }
 }
 
@@ -1033,7 +1089,7 @@ cudaError_t launch_d(const PageAttnParams& p, const Workspace& w, int dev, int n
   e = launch_k(page_attn_kernel<D>, dim3(w.ctas), dim3(kThreads), Lay::ALLOC, s, p);
   if (e != cudaSuccess) return e;
   MergeParams m{p.part, p.part_ml, p.cut, w.ctas, p.part_rows, p.out, p.lse, p.Hq, p.log_g};
-  e = launch_k(page_merge_kernel<D>, dim3(num_sms * 4), dim3(kMergeThreads), (w.ctas + 1) * sizeof(int), s, m);
+  e = launch_k(page_merge_kernel<D>, dim3(num_sms * 3), dim3(kMergeThreads), (w.ctas + 1) * sizeof(int), s, m);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
