@@ -8,11 +8,12 @@
 // Two launches.  select_kernel, one CTA per (stream, head), finds the weight of
 // the last key that still fits by a radix search over the weights' ordered bit
 // patterns, eight bits a pass, ended early where all keys with the digits found are
-// kept, and writes kept[] by an ordered scan: 41 us for 512 heads of 3000 to 9000
-// keys (53 us with one key of a thread asked for at a time and no early end; 512
-// threads: 256 and 1024 are slower).  The move is bound by memory:
+// kept, and writes kept[] in a second look at the keys, a warp's consecutive ones
+// each: some 32 us for 512 heads of 3000 to 9000 keys (50 with one key of a thread
+// asked for at a time, no early end and an ordered scan with a barrier for every 512
+// keys; 512 threads: 256 and 1024 are slower).  The move is bound by memory:
 // kept keys and values are read and written once.  64 streams of 8 heads cut to
-// 4096 keys of 128: 327 us, 6.5 TB/s.  Into other pages all rows
+// 4096 keys of 128: 322 us, 6.4 TB/s.  Into other pages all rows
 // move at once (copy_kernel); within the same pages a CTA owns 64 bytes of every
 // row of its head and takes rows in ascending order, reading a batch of rows
 // before it writes one: new places never lie behind old ones, so what a later
@@ -32,7 +33,7 @@ namespace {
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 // Keys whose ordered weights a select CTA keeps in shared memory; beyond, it
-// reads them from the pool again in each of its passes (four at most, and the scan).
+// reads them from the pool again in each of its passes (four at most, and two to write kept[]).
 constexpr int kSelHeld = 24576;
 
 struct EvictParams {
@@ -59,7 +60,6 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
   __shared__ unsigned int s_hist[256];
   __shared__ int s_pick[3];             // the digit found, how many keys remain to be found in it, and are in it
   __shared__ int s_warp[2][kSelWarps];
-  __shared__ int s_base[2];
   const int b = blockIdx.x / p.Hkv, h = blockIdx.x - b * p.Hkv;
   grid_dependency_wait();
   grid_launch_dependents();
@@ -105,10 +105,13 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
         const int i = i0 + threadIdx.x;
         const uint32_t key = i < m ? (held ? s_key[i] : read(i)) : 0u;
         const bool in = i < m && (shift == 24 || (key >> (shift + 8)) == (found >> (shift + 8)));
-        // Lanes with the same digit add once.
         const unsigned int digit = in ? (key >> shift) & 255u : 256u;
-        const unsigned int same = __match_any_sync(0xffffffffu, digit);
-        if (in && lane == __ffs(same) - 1) atomicAdd(&s_hist[digit], static_cast<unsigned int>(__popc(same)));
+        if (__popc(__ballot_sync(0xffffffffu, in)) <= 8) {
+          if (in) atomicAdd(&s_hist[digit], 1u);
+        } else {   // lanes with the same digit add once
+          const unsigned int same = __match_any_sync(0xffffffffu, digit);
+          if (in && lane == __ffs(same) - 1) atomicAdd(&s_hist[digit], static_cast<unsigned int>(__popc(same)));
+        }
       }
       __syncthreads();
       if (warp == 0) {   // lane l: digits 255 - 8 l down to 248 - 8 l
@@ -147,33 +150,41 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
   for (int i = threadIdx.x; i < p.sink; i += kSelThreads) kept[i] = i;
   for (int i = threadIdx.x; i < p.recent; i += kSelThreads) kept[p.budget - p.recent + i] = hi + i;
   if (!any) return;
-  if (threadIdx.x < 2) s_base[threadIdx.x] = 0;
+  // A warp takes consecutive keys: it counts them, and with the counts of the warps
+  // before it knows their places.
+  const int per = (m + kSelThreads - 1) / kSelThreads * 32;
+  const int w0 = warp * per, w1 = min(m, w0 + per);
+  auto look = [&](int i, unsigned int* over, unsigned int* same) {
+    const uint32_t key = i < w1 ? (held ? s_key[i] : read(i)) : 0u;
+    *over = __ballot_sync(0xffffffffu, i < w1 && (all ? key >= found : key > found));
+    *same = __ballot_sync(0xffffffffu, i < w1 && !all && key == found);
+  };
+  int n_over = 0, n_same = 0;
+  unsigned int over, same;
+#pragma unroll 4
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    look(i0 + lane, &over, &same);
+    n_over += __popc(over);
+    n_same += __popc(same);
+  }
+  if (lane == 0) {
+    s_warp[0][warp] = n_over;
+    s_warp[1][warp] = n_same;
+  }
   __syncthreads();
-  for (int i0 = 0; i0 < m; i0 += kSelThreads) {
-    const int i = i0 + threadIdx.x;
-    const uint32_t key = i < m ? (held ? s_key[i] : read(i)) : 0u;
-    const bool over = i < m && (all ? key >= found : key > found), same = i < m && !all && key == found;
-    const unsigned int m_over = __ballot_sync(0xffffffffu, over), m_same = __ballot_sync(0xffffffffu, same);
-    if (lane == 0) {
-      s_warp[0][warp] = __popc(m_over);
-      s_warp[1][warp] = __popc(m_same);
-    }
-    __syncthreads();
-    int n_over = s_base[0], n_same = s_base[1];   // before this warp
-    for (int w = 0; w < warp; ++w) {
-      n_over += s_warp[0][w];
-      n_same += s_warp[1][w];
-    }
-    const unsigned int below = (1u << lane) - 1u;
-    n_over += __popc(m_over & below);
-    n_same += __popc(m_same & below);
-    if (over || (same && n_same < want)) kept[p.sink + n_over + min(n_same, want)] = lo + i;
-    __syncthreads();
-    if (threadIdx.x == kSelThreads - 1) {
-      s_base[0] = n_over + (over ? 1 : 0);
-      s_base[1] = n_same + (same ? 1 : 0);
-    }
-    __syncthreads();
+  n_over = n_same = 0;
+  for (int w = 0; w < warp; ++w) {
+    n_over += s_warp[0][w];
+    n_same += s_warp[1][w];
+  }
+  const unsigned int below = (1u << lane) - 1u;
+#pragma unroll 4
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    look(i0 + lane, &over, &same);
+    const int o = n_over + __popc(over & below), e = n_same + __popc(same & below);
+    if ((over >> lane & 1) || ((same >> lane & 1) && e < want)) kept[p.sink + o + min(e, want)] = lo + i0 + lane;
+    n_over += __popc(over);
+    n_same += __popc(same);
   }
 }
 
@@ -192,7 +203,7 @@ __device__ __forceinline__ long long to_row(const EvictParams& p, int b, int i) 
 }
 
 // D/8 lanes move a row of K and of V; a thread has two rows of each in flight (64
-// streams of 8 heads cut to 4096 keys: 362 us so, 368 with four).
+// streams of 8 heads cut to 4096 keys: a call took 362 us so, 368 with four).
 // Rows: blockIdx.x over (stream, head), blockIdx.y over places.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyRows = 2;
