@@ -466,10 +466,12 @@ rx_status rx_attend_pages_workspace(int N, int Hq, int Hkv, int D, long long* by
  *   out[j][h] = decay * weight[j][h] + sum exp(q . k_j / sqrt(D) - lse)
  * over the new tokens that see j (as in rx_attend_pages, with the same q, lens and
  * prefix, after it) and the query heads of group h.  decay 0: weight is not read.
+ * Rows of other streams' tokens, of tokens in no stream and of tokens that do not see
+ * j have no part in it, whatever their q and lse hold.
  * out: fp32 [n_pages][page][Hkv], may be the pages' weight; NULL means that.  Other
  * places of out are left as they were.  A page may belong to one stream of a call
- * only.  The same inputs give the same bits.  lse: fp32 [N][Hq] DEVICE (-infinity:
- * the row weighs nothing).  workspace: DEVICE memory of rx_weigh_pages_workspace
+ * only.  The same inputs give the same bits.  lse: fp32 [N][Hq] DEVICE (infinite:
+ * the row weighs nothing; NaN: the keys that it sees weigh NaN).  workspace: DEVICE memory of rx_weigh_pages_workspace
  * bytes, 256-byte aligned, for this call alone while it runs; may be NULL where
  * that is 0 (few new tokens).  out and the workspace may not overlap another input
  * or each other.

@@ -14,13 +14,24 @@
 // the units by their number of row tiles and kUnitCost each, summed in closed form.
 // A share may end between two row tiles of a unit: its parts' sums go to the
 // workspace, and a second kernel adds them in their order.  Five chunks of up to 999
-// tokens (32/8 heads of 128) over keys to 8000: 62 us so, 68 with whole units
-// (some 8 per CTA); 512 tokens over 2000 keys of one head of 256: 14 and 28.
+// tokens (32/8 heads of 128) over keys to 8000: 65 us so; before what the next
+// paragraph adds 62, and 68 with whole units (some 8 per CTA); 512 tokens over 2000
+// keys of one head of 256: 14 and 28.
 // kUnitCost 4, 1 and 0 gave 64, 63 and 69 us, kMinCut 4 63.  A call with too few
 // rows for a cut has no second kernel.
 //
+// Whose rows count.  A row tile's columns are packed tokens: behind the stream's come
+// whoever's are next.  A row takes part by its score and its lse alone: scores of rows
+// that do not see the key are -infinity by selection; rows of others, and those that
+// weigh nothing, have lse infinity and scores that are clamped to finite ones, since an
+// infinity or NaN among them would outlast it; a row whose lse is NaN has a finite lse
+// that lets any score through but -infinity, which makes the sums of the keys that it
+// sees infinite and, at the unit's end, NaN.  One minimum a score in tiles that have
+// such rows: the chunks above take 65 us, 70 with a selection by row and 71 with the
+// queries overwritten in shared memory before their product.
+//
 // One token per stream is bound by the keys' bytes, at this size by the launch's
-// latency (16 streams of up to 2000 keys: 8 us).  The chunks above run at 910
+// latency (16 streams of up to 2000 keys: 8 us).  The chunks above run at 880
 // TFLOP/s, at D = 64 chunks run at 430: in both an SM gets through some 12 scores a
 // cycle, so the way from scores to sums is the bound, not K Q^T (half of that time
 // at D = 128) nor memory.
@@ -277,6 +288,7 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) page_weigh_kernel(const
   const uint32_t sK = base + Lay::OFF_K, sQ = base + Lay::OFF_Q, sBar = base + Lay::OFF_BAR;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + Lay::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + Lay::OFF_MISC + 4);
+  volatile int* s_mute = reinterpret_cast<volatile int*>(gbase + Lay::OFF_MISC + 8);   // [GROUPS]: a row of the stream weighs nothing
   float* s_lse = reinterpret_cast<float*>(gbase + Lay::OFF_LSE);
   float* s_sum = reinterpret_cast<float*>(gbase + Lay::OFF_SUM);
   StreamInfo* info = reinterpret_cast<StreamInfo*>(gbase + Lay::OFF_STREAM);
@@ -459,14 +471,22 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) page_weigh_kernel(const
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
           if (!ok || r0 + i >= x.r1) break;
+          // Rows behind the stream's, and rows that saw nothing, weigh nothing.  A row whose
+          // lse is NaN gives the keys that it sees an infinite weight (NaN would pass a
+          // hidden score's -infinity), which becomes NaN in the end.
+          const int left = rows - (r0 + i) * kRows - 4 * lane;
+          float f[4];
+          bool mute = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool off = fabsf(v[i][e]) == INFINITY;
+            f[e] = off ? -INFINITY : v[i][e] == v[i][e] ? v[i][e] * -1.44269504088896341f : 3.0e38f;
+            mute = mute || (off && e < left);
+          }
+          mute = __any_sync(0xffffffffu, mute);
           if (at.round > 0 && !warp_wait(BAR(B_LR + at.slot), (at.round - 1) & 1, abort_flag)) { ok = false; break; }
-          // Rows behind the stream's, and rows that saw nothing, weigh nothing.
-          float4 f;
-          f.x = (v[i][0] == -INFINITY ? INFINITY : v[i][0]) * -1.44269504088896341f;
-          f.y = (v[i][1] == -INFINITY ? INFINITY : v[i][1]) * -1.44269504088896341f;
-          f.z = (v[i][2] == -INFINITY ? INFINITY : v[i][2]) * -1.44269504088896341f;
-          f.w = (v[i][3] == -INFINITY ? INFINITY : v[i][3]) * -1.44269504088896341f;
-          reinterpret_cast<float4*>(s_lse + at.slot * kRows)[lane] = f;
+          reinterpret_cast<float4*>(s_lse + at.slot * kRows)[lane] = make_float4(f[0], f[1], f[2], f[3]);
+          if (lane == 0) s_mute[at.slot] = mute;
           mbar_arrive(BAR(B_LF + at.slot));
           at.step(Lay::GROUPS);
         }
@@ -535,7 +555,9 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) page_weigh_kernel(const
         tc_fence_after();
         const int hidden = first - r * kRows;   // leading rows of the tile that do not see the key
         const bool mask = __any_sync(0xffffffffu, hidden > 0);
-        const bool few = r * kRows + 64 >= (now.s.n << p.log_g);   // rows: a single token's
+        const int rows = (now.s.n << p.log_g) - r * kRows;   // of the stream; behind them lie other tokens'
+        const bool few = rows <= 64;   // a single token's
+        const bool mute = s_mute[slot] != 0;
         const float4* lse = reinterpret_cast<const float4*>(s_lse + slot * kRows);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -544,6 +566,13 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) page_weigh_kernel(const
           if (half == 1 || few) {
             tc_fence_before();
             mbar_arrive(BAR(B_SR + slot));
+          }
+          // A row that weighs nothing has lse infinity here: enough beside any score but
+          // infinity and NaN, which are made finite (those of the stream's own rows have
+          // an lse of NaN).
+          if (mute || rows < half * 64 + 64) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) s[c] = fminf(s[c], 3.0e38f);
           }
           if (mask) {
 #pragma unroll
@@ -573,7 +602,7 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) page_weigh_kernel(const
         if (ok) ok = warp_wait(BAR(B_UF), v & 1, abort_flag);
 #pragma unroll
         for (int i = 0; i < Lay::GROUPS - 1; ++i) got += s_sum[i * kKeys + key];
-        if (!ok) got = NAN;   // a wait gave up
+        if (!ok || got == INFINITY) got = NAN;   // a wait gave up, a row's lse is NaN
         if (ok) mbar_arrive(BAR(B_UR));
         if (now.slot >= 0) p.part[now.slot * kKeys + key] = got;
         else if (row >= 0) p.out[place] = p.decay == 0.f ? got : fmaf(p.decay, old, got);

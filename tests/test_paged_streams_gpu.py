@@ -597,6 +597,99 @@ def test_weight_of_long_chunks_gives_the_same_bits_twice(rx):
         np.testing.assert_allclose(got.cpu().numpy(), new[b] * 4, rtol=1e-4)
 
 
+@pytest.mark.parametrize("what", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 1, 256), (8, 2, 128), (4, 4, 64), (128, 1, 64)])
+@pytest.mark.parametrize("new,lens", [
+    ([1, 1, 1, 1], [130, 40, 77, 300]),           # decoding streams side by side
+    ([40, 9, 33, 150], [90, 20, 33, 400]),
+    ([300, 3, 260], [500, 200, 700]),             # blocks of keys that several CTAs share
+])
+def test_weight_is_of_the_streams_own_rows(rx, what, Hq, Hkv, D, new, lens):
+    """Queries of the next stream and of tokens in no stream that are not finite:
+    the other streams' weights are bit for bit as without them."""
+    import torch
+    g = np.random.default_rng([D, new[0]])
+    pool = Pool(g, lens, 32, Hkv, D).fill(g)
+    start = _starts(new) + 2
+    N = start[-1] + 5
+    q = _bits(g, (N, Hq, D))
+    bad = q.copy()
+    value = W.to_bf16_bits(np.array([what], np.float32))[0]
+    for rows in (slice(0, 2), slice(start[1], start[2]), slice(start[-1], N)):
+        bad[rows, :, 3] = value
+    got = []
+    for bits in (q, bad):
+        pages = pool.pages(rx)
+        args = (pages, _int(start), _int(lens))
+        _, lse = rx.attend_pages(dev(bits), *args, lse=torch.zeros((N, Hq), device="cuda"))
+        rx.weigh_pages(dev(bits), lse, *args, decay=0.5)
+        got.append((pages.weight.cpu().numpy().reshape(pool.w.shape), lse.cpu().numpy()))
+    for b in range(len(new)):
+        if b == 1:
+            continue
+        np.testing.assert_array_equal(got[1][1][start[b]:start[b + 1]], got[0][1][start[b]:start[b + 1]])
+        assert np.all(np.isfinite(got[0][0][pool.rows(b)]))
+        np.testing.assert_array_equal(got[1][0][pool.rows(b)], got[0][0][pool.rows(b)])
+
+
+@pytest.mark.parametrize("what", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 1, 256), (8, 2, 128), (4, 4, 64)])
+def test_weight_is_of_the_rows_that_see_the_key(rx, what, Hq, Hkv, D):
+    """A chunk's token 10 whose query is not finite, its lse NaN or what the
+    attention makes of it: keys behind token 10, which it does not see, weigh bit
+    for bit what they weigh without it.  With lse -infinity it weighs nothing
+    anywhere."""
+    import torch
+    g = np.random.default_rng(D)
+    n, held, t = 200, 150, 10
+    pool = Pool(g, [held + n], 16, Hkv, D).fill(g)
+    q = _bits(g, (n, Hq, D))
+    bad = q.copy()
+    bad[t, :, 5] = W.to_bf16_bits(np.array([what], np.float32))[0]
+    pages = pool.pages(rx)
+    args = (pages, _int([0, n]), _int([held + n]))
+    def weigh(bits, lse):
+        return rx.weigh_pages(dev(bits), lse, *args, decay=0.0, out=torch.zeros_like(pages.weight)).cpu().numpy().reshape(pool.w.shape)
+    lse = rx.attend_pages(dev(q), *args, lse=True)[1]
+    lse_bad = rx.attend_pages(dev(bad), *args, lse=True)[1]
+    lse_nan = lse.clone()
+    lse_nan[t] = float("nan")
+    clean = weigh(q, lse)
+    hidden = pool.rows(0)[held + t + 1:]
+    assert np.all(np.isfinite(clean[hidden]))
+    for e in (lse_bad, lse_nan):
+        np.testing.assert_array_equal(weigh(bad, e)[hidden], clean[hidden])
+    np.testing.assert_array_equal(weigh(q, lse_nan)[hidden], clean[hidden])
+    assert np.all(np.isnan(weigh(q, lse_nan)[pool.rows(0)[:held + t + 1]]))
+    off = lse.clone()
+    off[t] = -float("inf")
+    np.testing.assert_array_equal(weigh(bad, off), weigh(q, off))
+    assert np.all(np.isfinite(weigh(bad, off)[pool.rows(0)]))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 1, 256), (8, 2, 128), (2, 2, 64)])
+@pytest.mark.parametrize("new,lens", [([1, 1, 1], [130, 40, 77]), ([40, 9, 150], [90, 20, 400])])
+def test_weight_of_a_key_that_no_row_can_weigh(rx, Hq, Hkv, D, new, lens):
+    """An infinite key whose scores are all -infinity in its stream, and would be
+    +infinity in the others: it gathers nothing, and the lse stays finite."""
+    g = np.random.default_rng([D, new[0]])
+    pool = Pool(g, lens, 32, Hkv, D).fill(g)
+    start = _starts(new) + 1
+    N = start[-1] + 1
+    q = np.abs(f64(_bits(g, (N, Hq, D)))) + 1
+    q[start[0]:start[1], :, 5] *= -1
+    q = W.to_bf16_bits(q.astype(np.float32))
+    pool.k[pool.rows(0)[17], :, 5] = W.to_bf16_bits(np.array([np.inf], np.float32))[0]
+    pages = pool.pages(rx)
+    args = (pages, _int(start), _int(lens))
+    _, lse = rx.attend_pages(dev(q), *args, lse=True)
+    rx.weigh_pages(dev(q), lse, *args, decay=0.5)
+    got = pages.weight.cpu().numpy().reshape(pool.w.shape)
+    assert np.all(np.isfinite(lse[1:N - 1].cpu().numpy()))
+    np.testing.assert_array_equal(got[pool.rows(0)[17]], np.float32(0.5) * pool.w[pool.rows(0)[17]])
+    assert all(np.all(np.isfinite(got[pool.rows(b)])) for b in range(len(new)))
+
+
 # ---------------------------------------------------------------- eviction
 def _evict_case(rx, pool, sink, recent, budget, copy, alias=False, table_to=None):
     import torch
