@@ -38,7 +38,9 @@
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *    stream).  Calls enqueue work and return without synchronising, except
  *    where stated.  Work for one cache must stay in stream order: the cache
- *    owns one workspace and one device-side {head, valid} state.
+ *    owns one workspace and one device-side {head, valid} state.  Two calls
+ *    say how they may run beside others: rx_push_frame_async and
+ *    rx_attend_pages.
  *  - Shapes: L layers, Hq query heads, Hkv key/value heads (Hq = G*Hkv, G a
  *    power of two <= 128; query head h reads key/value head h / G), head
  *    dimension D in {64, 128, 256}.
@@ -130,10 +132,10 @@ rx_status rx_push_frame(rx_cache_t cache, const void* k, const void* v,
  * the window after the previous push or after this one, and the slot this push
  * overwrites can only be read by work that the producer waited for.  The push
  * runs concurrently with consumer work enqueued after the call.
- * (rx_attend_streams_quant reads the state once for a whole call.  In the other
- * attention calls each CTA reads it as it starts: a push that publishes while
- * they start, which takes about a microsecond if all are resident together and
- * most of the call if they are not, is seen by those after it.)
+ * (rx_attend_streams_quant and rx_attend_pages read the state once for a whole
+ * call.  In the other attention calls each CTA reads it as it starts: a push that
+ * publishes while they start, which takes about a microsecond if all are resident
+ * together and most of the call if they are not, is seen by those after it.)
  * Errors: RX_ERR_STATE (cache without a spare slot), RX_ERR_ARG, RX_ERR_CUDA. */
 rx_status rx_push_frame_async(rx_cache_t cache, const void* k, const void* v,
                               int* evicted, void* producer_stream,
@@ -450,9 +452,12 @@ rx_status rx_rotate_heads_paged(const void* x, long long row_stride, int N, cons
  * D are the cache's where one is given.  workspace: DEVICE memory of
  * rx_attend_pages_workspace bytes, 256-byte aligned, for this call alone while
  * it runs.  out, lse and the workspace may not overlap an input or each other.
- * All rows of a call see the same window of a ring with a spare slot.  A wait
- * that gives up makes its rows NaN and, with a cache, sets bit 3 of its error
- * word.  Errors: RX_ERR_ARG, RX_ERR_LAYER, RX_ERR_UNSUPPORTED (D, Hq/Hkv),
+ * All rows of a call see the same window of a ring with a spare slot.  Calls of
+ * one cache may run beside each other and beside its other attention calls, each
+ * in its own workspace.  A push waits only for the stream that it is given: calls on
+ * other streams have to be ordered before the second push that follows them (the
+ * first without a spare slot).  A wait that gives up makes its rows NaN and, with a
+ * cache, sets bit 3 of its error word.  Errors: RX_ERR_ARG, RX_ERR_LAYER, RX_ERR_UNSUPPORTED (D, Hq/Hkv),
  * RX_ERR_CAPACITY (workspace_bytes), RX_ERR_STATE (the cache is on another
  * device), RX_ERR_CUDA. */
 rx_status rx_attend_pages(rx_cache_t cache, int layer, const void* q, int N, int Hq, int Hkv, int D,

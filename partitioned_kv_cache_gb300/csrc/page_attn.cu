@@ -1062,7 +1062,7 @@ __global__ void __launch_bounds__(kMergeThreads, 3) page_merge_kernel(const __gr
 
 struct Workspace {
   int ctas, part_rows;
-  size_t part, ml, cut, bytes;   // offsets
+  size_t part, ml, cut, held, bytes;   // offsets
 };
 
 Workspace workspace(int N, int G, int D, int num_sms) {   // one CTA per SM
@@ -1074,7 +1074,8 @@ Workspace workspace(int N, int G, int D, int num_sms) {   // one CTA per SM
   w.part = 0;
   w.ml = w.part + slots * w.part_rows * D * 4;
   w.cut = w.ml + slots * w.part_rows * 8;
-  w.bytes = w.cut + static_cast<size_t>(w.ctas) * sizeof(CutUnit);
+  w.held = w.cut + static_cast<size_t>(w.ctas) * sizeof(CutUnit);
+  w.bytes = w.held + sizeof(DevState);
   return w;
 }
 
@@ -1143,6 +1144,12 @@ cudaError_t launch_attend_pages(const PageAttention& a, const PagePool& pool, co
   p.part_ml = reinterpret_cast<float2*>(at + w.ml);
   p.cut = reinterpret_cast<CutUnit*>(at + w.cut);
   p.part_rows = w.part_rows;
+  if (al && al->slots > al->N) {   // a push may publish meanwhile: one state for all CTAs, the call's own
+    DevState* held = reinterpret_cast<DevState*>(at + w.held);
+    e = launch_hold_ring_state(al->st, held, s);
+    if (e != cudaSuccess) return e;
+    p.st = held;
+  }
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
   switch (D) {
     case 64: return launch_d<64>(p, w, dev, sms, s);

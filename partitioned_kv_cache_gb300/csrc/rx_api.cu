@@ -992,14 +992,7 @@ rx_status rx_attend_pages(rx_cache_t h, int layer, const void* q, int N, int Hq,
     return fail(RX_ERR_CAPACITY, "%s: the workspace has %lld bytes, the call needs %lld", where, workspace_bytes, need);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   rx::AttnLaunch al{};
-  if (h) {
-    al = make_launch(h, layer);
-    if (h->fork.held) {   // a push may publish meanwhile: one state for all CTAs
-      e = rx::launch_hold_ring_state(h->dstate, h->fork.held, s);
-      if (e != cudaSuccess) return cuda_fail(e, "rx_attend_pages: launch");
-      al.st = h->fork.held;
-    }
-  }
+  if (h) al = make_launch(h, layer);
   const rx::PageAttention a{q, out, lse, q_start, len, prefix, N, Hq, Hkv, D};
   e = rx::launch_attend_pages(a, pool, h ? &al : nullptr, workspace, s);
   if (e != cudaSuccess) return cuda_fail(e, "rx_attend_pages: launch");

@@ -914,6 +914,83 @@ def test_two_captured_calls_of_one_cache_replayed_side_by_side(rx):
     cache.close()
 
 
+def test_calls_of_one_cache_side_by_side_beside_pushes(rx):
+    """A ring with a spare slot; two calls on streams of their own, and a push that
+    publishes between them while other work holds SMs, so that some of the first
+    call's CTAs start after all that: every call's rows are those of one window, the
+    one before the push or the one after it."""
+    import torch
+    g = np.random.default_rng(31)
+    Hq, Hkv, D, N, F, steps = 8, 1, 256, 3, 128, 6
+    frames = [tuple(dev(_bits(g, (1, F, Hkv, D))) for _ in range(2)) for _ in range(steps + 1)]
+    caches = [rx.Cache(1, Hq, Hkv, D, 0, N, F, 1, spare_slot=1) for _ in range(2)]
+    calls = []
+    for lens, new in (([6000] * 8, [2048] * 8), ([2500, 30], [1, 1])):   # the first takes some 0.5 ms
+        pool = Pool(g, lens, 64, Hkv, D).fill(g)
+        calls.append((dev(_bits(g, (sum(new), Hq, D))), pool.pages(rx), _int(_starts(new)), _int(lens)))
+    refs = []                                       # by window, one call after the other
+    for f in frames:
+        caches[0].push_frame(*f)
+        refs.append([caches[0].attend_pages(0, *c, lse=True) for c in calls])
+    # 64 CTAs for 0.8 ms.
+    V = 1 << 25
+    p, draft, none, r = torch.rand(8, 1, V, device="cuda"), _int(np.zeros((8, 0))), torch.rand(8, 0, device="cuda"), torch.rand(8, device="cuda")
+    caches[1].push_frame(*frames[0])
+    streams = [torch.cuda.Stream(priority=p) for p in (0, -1, -1, 0)]   # the push gets its places before the first call's rest
+    for s, c in zip(streams, calls + calls):        # (loads everything)
+        caches[1].attend_pages(0, *c, stream=s)
+    rx.verify_drafts(p, None, draft, none, r, stream=streams[3])
+    torch.cuda.synchronize()
+    for i in range(steps):
+        rx.verify_drafts(p, None, draft, none, r, stream=streams[3])
+        one = caches[1].attend_pages(0, *calls[0], lse=True, stream=streams[0])
+        caches[1].push_frame_async(*frames[i + 1], streams[2], streams[1])
+        streams[1].wait_stream(streams[2])
+        two = caches[1].attend_pages(0, *calls[1], lse=True, stream=streams[1])
+        torch.cuda.synchronize()
+        for call, got in enumerate((one, two)):
+            assert any(torch.equal(got[0], refs[w][call][0]) and torch.equal(got[1], refs[w][call][1]) for w in (i, i + 1)), (i, call)
+    assert caches[1].get_state()[2] == steps + 1
+    for c in caches:
+        assert c.check_device_error() == 0
+        c.close()
+
+
+def test_two_captured_calls_of_a_cache_with_a_spare_slot(rx):
+    """Graphs of one cache replayed side by side follow its window, pushes between
+    the replays."""
+    import torch
+    g = np.random.default_rng(32)
+    Hq, Hkv, D, F = 8, 2, 128, 64
+    cache, _, _ = _store(rx, g, Hq, Hkv, D, 64, 2, F, 1, spare=1)
+    cases = []
+    for lens in ([3000], [1500, 700]):
+        pool = Pool(g, lens, 64, Hkv, D).fill(g)
+        n = len(lens)
+        args = (dev(_bits(g, (n, Hq, D))), pool.pages(rx), _int(range(n + 1)), _int(lens))
+        out, lse = cache.attend_pages(0, *args, lse=True)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(5):
+                cache.attend_pages(0, *args, out=out, lse=lse)
+        cases.append((graph, out, lse, torch.cuda.Stream(), args))
+    for _ in range(5):
+        cache.push_frame(*(dev(_bits(g, (1, F, Hkv, D))) for _ in range(2)))
+        refs = [cache.attend_pages(0, *c[4], lse=True) for c in cases]
+        for _, out, lse, _, _ in cases:
+            out.zero_()
+            lse.zero_()
+        torch.cuda.synchronize()
+        for graph, _, _, s, _ in cases:
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for (_, out, lse, _, _), ref in zip(cases, refs):
+            assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+    assert cache.check_device_error() == 0
+    cache.close()
+
+
 def test_calls_on_another_stream(rx):
     """stream= orders a call on that stream, its own outputs allocated there."""
     import torch
