@@ -389,8 +389,8 @@ typedef struct rx_pages {
 } rx_pages;
 
 /* What the heads of a projection become: an RMS norm of each query and key head
- * (where its weight is given), y_i = x_i * rsqrt(mean x^2 + eps) * w_i, then the
- * rotation of its pairs by the token's position, pair i by the angle
+ * (where its weight is given), y_i = x_i * rsqrt(mean x^2 + eps) * w_i, for values
+ * of every size that bf16 holds, then the rotation of its pairs by the token's position, pair i by the angle
  * pos[axis(i)] * freq[i]:
  *   (a, b) -> (a cos - b sin, b cos + a sin).
  * Pair i is elements (i, i + R/2), or (2i, 2i + 1) with adjacent = 1, where R/2

@@ -57,6 +57,36 @@ __device__ __forceinline__ unsigned long long turn_fraction(float freq) {
   return static_cast<unsigned long long>((t - floor(t)) * 18446744073709551616.0);
 }
 
+// bf16's values reach as far as fp32's, their squares do not stay within it.  Where
+// the mean of a head's squares is not near enough to 1, the lanes that hold the head
+// bring its values to the scale of the larger of their largest and sqrt(eps), a power
+// of two, and get the mean (eps in it) in that scale.  All lanes of a warp call it;
+// heads that are near or not `normed` stay as they are.  The vote on it costs 95 us for
+// 93 (13600 tokens of 48 heads of 128).
+constexpr float kNear = 8.6736173798840355e-19f;   // 2^-60
+template <int D>
+__device__ __forceinline__ float scaled_mean(float (&y)[16], float eps, float mean, bool normed) {
+  constexpr int L = D / 16;
+  float top = 0.f;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(y[e]));
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float base = fmaxf(top, sqrtf(eps));
+  // (zeros without eps, and a head with an infinity, have no scale)
+  const bool far = normed && !(mean >= kNear && mean <= 1.f / kNear) && base > 0.f && base < INFINITY;
+  const int k = far ? ilogbf(base) : 0;
+  float ss = 0.f;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    y[e] = scalbnf(y[e], -k);
+    ss = fmaf(y[e], y[e], ss);
+  }
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  return far ? ss * (1.f / D) + scalbnf(eps, -2 * k) : mean;
+}
+
 // A CTA takes TB tokens at a time; the pairs' cosines and sines are computed once
 // per token into shared memory and serve all its heads.  D/16 lanes hold a head,
 // 16 values each as two chunks of eight, R/16 chunks apart: in half pairs a lane
@@ -65,7 +95,7 @@ __device__ __forceinline__ unsigned long long turn_fraction(float freq) {
 // the prompts below took 129 us; with two groups of four, whose loads are 8 bytes
 // wide, 192.)  A lane asks for kFlight heads at a time, the first of them before
 // the angles are computed.  Bound by the loads in flight: 13600 tokens of 48 heads
-// of 128 take 93 us, 4.8 TB/s.  More threads on an SM (64 registers cut to 48 or 40:
+// of 128 take 95 us, 4.7 TB/s.  More threads on an SM (64 registers cut to 48 or 40:
 // 117 us), four heads in flight (104) and blocks of 512 threads (105) are slower,
 // blocks of 128 as fast (91; 9.9 for 8.7 us at 2048 tokens).
 template <int D, int TB>
@@ -185,8 +215,11 @@ __global__ void __launch_bounds__(kThreads) rotate_heads_kernel(const __grid_con
             for (int e = 0; e < 16; ++e) ss = fmaf(y[e], y[e], ss);
 #pragma unroll
             for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (isq ? norm_q : norm_k) {
-              const float r = rsqrtf(ss * (1.f / D) + p.r.eps);
+            const bool normed = isq ? norm_q : norm_k;
+            float mean = ss * (1.f / D) + p.r.eps;
+            if (__any_sync(0xffffffffu, !(mean >= kNear && mean <= 1.f / kNear))) mean = scaled_mean<D>(y, p.r.eps, mean, normed);
+            if (normed) {
+              const float r = rsqrtf(mean);
               const float4* ws = reinterpret_cast<const float4*>(s_w[isq ? 0 : 1]);
               const float4 g[4] = {ws[2 * c0], ws[2 * c0 + 1], ws[2 * c1], ws[2 * c1 + 1]};
 #pragma unroll

@@ -168,6 +168,36 @@ def test_rotation_at_far_positions_and_over_bf16s_range(rx):
         assert np.all(np.abs(host64(got) - ref) <= tol)
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 1e-30])
+@pytest.mark.parametrize("N,Hq,Hkv,D", [(70, 2, 1, 64), (70, 1, 1, 128), (70, 1, 2, 256), (700, 3, 1, 64)])
+def test_norm_over_bf16s_range(rx, eps, N, Hq, Hkv, D):
+    """Heads from bf16's smallest values to its largest: squares that fp32 cannot
+    hold, rows of zeros, and one large value among small ones."""
+    import torch
+    g = np.random.default_rng([N, D])
+    H = Hq + 2 * Hkv
+    x = g.standard_normal((N, H, D), dtype=np.float32).clip(-3, 3) * 2.0 ** g.integers(-133, 126, (N, H, 1)).astype(np.float32)
+    x[::7, :, 5] = 2.0 ** 120
+    x[1::7] = 2.0 ** -133
+    if eps:
+        x[2::7] = 0
+    x = W.to_bf16_bits(x)
+    freq = (100.0 ** -(np.arange(D // 2) / (D // 2))).astype(np.float32)
+    pos = g.integers(0, 500, (1, N))
+    wq, wk = (1 + 0.25 * g.standard_normal(D, dtype=np.float32) for _ in range(2))
+    cuda = lambda a: torch.from_numpy(a).cuda()
+    heads = rx.Heads(Hq, Hkv, D, cuda(freq), (), cuda(wq), cuda(wk), eps)
+    q, k, v = rx.rotate_heads(dev(x).view(N, -1), heads, _int(pos))
+    y = f64(x)
+    live = np.any(y != 0, -1)
+    assert eps or np.all(live)
+    eps32 = float(np.float32(eps))
+    yq, tq, yk, tk = _rotated(y, Hq, Hkv, wq, wk, eps32, pos, freq, (D // 2,), False)
+    assert np.all(np.abs(host64(q) - yq) <= tq)
+    assert np.all(np.abs(host64(k) - yk) <= tk)
+    _same(v, np.ascontiguousarray(x[:, Hq + Hkv:]))
+
+
 @pytest.mark.parametrize("page,held,new", [
     (16, [0], [1]),
     (16, [0, 15, 16, 31], [1, 1, 1, 2]),
