@@ -390,14 +390,15 @@ typedef struct rx_pages {
 
 /* What the heads of a projection become: an RMS norm of each query and key head
  * (where its weight is given), y_i = x_i * rsqrt(mean x^2 + eps) * w_i, for values
- * of every size that bf16 holds, then the rotation of its pairs by the token's position, pair i by the angle
- * pos[axis(i)] * freq[i]:
+ * of every size that bf16 holds, then the rotation of its pairs by the token's
+ * position, pair i by the angle pos[axis(i)] * freq[i]:
  *   (a, b) -> (a cos - b sin, b cos + a sin).
  * Pair i is elements (i, i + R/2), or (2i, 2i + 1) with adjacent = 1, where R/2
  * is the sum of the sections; elements from R on are not rotated.  The first
  * sections[0] pairs turn with axis 0, the next sections[1] with axis 1, and so
- * on (time, height and width of a video's tokens).  Angles keep their fraction
- * of a turn to 2^-31 at every 32-bit position. */
+ * on (time, height and width of a video's tokens).  An angle is off by 2^-25 of a
+ * turn and |pos| |freq| 2^-52 radians at most (|pos| (|freq| + 2) 2^-52 where freq is
+ * negative): no turn is lost at any 32-bit position. */
 #define RX_MAX_AXES 4
 typedef struct rx_heads {
   const float* freq;       /* DEVICE fp32 [R/2], finite                          */

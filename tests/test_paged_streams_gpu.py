@@ -168,6 +168,41 @@ def test_rotation_at_far_positions_and_over_bf16s_range(rx):
         assert np.all(np.abs(host64(got) - ref) <= tol)
 
 
+def test_rotation_where_an_angles_error_shows(rx):
+    """Positions at which a pair turns by nearly half a turn or a whole one: a sine
+    near zero is the angle's own error and nothing else.  The error: a 32-bit
+    fraction of a turn rounded to fp32, 2^-26 + 2^-32 of a turn, and for each position
+    the rounding of freq / 2 pi, freq 2^-52 radians, of its fraction, 2^-64 of a turn,
+    and of a negative one's distance from a whole turn, 2^-54."""
+    import torch
+    from fractions import Fraction
+    D, R2 = 64, 32
+    freq = np.array([1.0, 0.7, 6.25, 123.4, -1.0, -0.003] + [10000.0 ** -(i / 26) for i in range(26)], np.float32)
+    two_pi = 2 * Fraction(314159265358979323846264338327950288419716939937510, 10 ** 50)
+    g = np.random.default_rng(5)
+    pos = [355, 104348, 5419351, 80143857, 245850922, 411557987, -411557987, 2 ** 31 - 1, -2 ** 31]
+    many = g.integers(-2 ** 31, 2 ** 31, 400000)
+    for f in freq:   # of many positions those whose sine is smallest
+        pos += [int(p) for p in many[np.argsort(np.abs(np.sin(many * np.float64(f))))[:4]]]
+    N = len(pos)
+    turn = np.empty((N, R2))
+    for n, p in enumerate(pos):
+        for i, f in enumerate(freq):
+            a = Fraction(p) * Fraction(float(f))
+            turn[n, i] = float(a - two_pi * round(a / two_pi))
+    assert np.min(np.abs(np.sin(turn))) < 1e-8
+    x = np.zeros((N, 3, D), np.float32)
+    x[..., R2:] = 1                                           # (0, 1) -> (-sin, cos)
+    heads = rx.Heads(1, 1, D, torch.from_numpy(freq).cuda())
+    q, _, _ = rx.rotate_heads(dev(W.to_bf16_bits(x)).view(N, -1), heads, _int(pos))
+    far = np.abs(np.array(pos, np.float64))[:, None]
+    angle = 2 * np.pi * (2.0 ** -26 + 2.0 ** -32 + far * (2.0 ** -64 + (freq < 0) * 2.0 ** -54)) + far * np.abs(freq) * 2.0 ** -52
+    got = host64(q)[:, 0]
+    for ref, at in ((-np.sin(turn), slice(0, R2)), (np.cos(turn), slice(R2, D))):
+        # sincospi is good to 2 of fp32's last places, the output is rounded once.
+        assert np.all(np.abs(got[:, at] - ref) <= angle + (2.0 ** -8 + 2.0 ** -21) * np.abs(ref))
+
+
 @pytest.mark.parametrize("eps", [0.0, 1e-6, 1e-30])
 @pytest.mark.parametrize("N,Hq,Hkv,D", [(70, 2, 1, 64), (70, 1, 1, 128), (70, 1, 2, 256), (700, 3, 1, 64)])
 def test_norm_over_bf16s_range(rx, eps, N, Hq, Hkv, D):
