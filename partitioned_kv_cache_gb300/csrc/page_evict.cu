@@ -272,9 +272,17 @@ __global__ void __launch_bounds__(kCloseThreads) close_up_kernel(const __grid_co
   grid_launch_dependents();
   write_len(p, b, h);
   const int* kept = p.kept + static_cast<size_t>(blockIdx.x) * p.budget;
-  if (kept[p.budget - 1] <= p.budget - 1) return;      // nothing was dropped (or the stream is shorter: -1)
   const int piece = blockIdx.y;
   const bool weights = piece == 2 * kPieces;
+  if (weights && p.overflow) {
+    // Keys that stay are the first ones, so a page that holds any begins with one.
+    const int slots = ((p.budget - 1) >> p.pool.log_page) + 1;
+    for (int slot = threadIdx.x; slot < slots; slot += kCloseThreads) {
+      const int i = slot << p.pool.log_page;
+      if (__ldcg(kept + i) == i && pool_row(p.pool, b, i) < 0) atomicOr(p.overflow, 1);
+    }
+  }
+  if (kept[p.budget - 1] <= p.budget - 1) return;      // nothing was dropped (or the stream is shorter: -1)
   uint4* base = static_cast<uint4*>(piece < kPieces ? p.pool.k : p.pool.v) + (piece % kPieces) * 4 + (threadIdx.x & 3);
   uint4 x[2][kCloseRows];
   long long dst[2][kCloseRows];

@@ -838,6 +838,40 @@ def test_eviction_with_pages_that_are_not_named(rx, copy):
     _evict_case(rx, pool, 2, 5, 64, copy)
 
 
+@pytest.mark.parametrize("copy", [False, True])
+def test_eviction_reports_every_kept_key_without_a_page(rx, copy):
+    """A kept key in a page that is not named sets the flag whether it would move
+    or stay: a sink, a key of a stream that is short enough to keep all.  A key
+    that goes anyway does not."""
+    import torch
+    g = np.random.default_rng(16)
+    budget, sink, recent, page = 64, 20, 5, 16
+
+    def flag(lens, hole, entry=-1):
+        pool = Pool(g, lens, page, 2, 64, spare=20).fill(g)
+        pool.w[:] = np.where(np.isnan(pool.w), pool.w, 1.0)            # equal: the earliest stay
+        if hole is not None:
+            pool.table[hole] = entry
+        to, tab = None, pool.table
+        if copy:
+            tab = np.array([[pool.free[5 * b + i] for i in range(4)] for b in range(len(lens))])
+            to = _int(tab)
+        over, new_len = _int([0]), _int([-1] * len(lens))
+        pages = pool.pages(rx)
+        kept = rx.evict_pages(pages, _int(lens), budget, sink=sink, recent=recent, to=to, new_len=new_len, overflow=over)
+        assert torch.equal(kept, rx.evict_pages(pool.pages(rx), _int(lens), budget, sink=sink, recent=recent, to=to))
+        assert new_len.tolist() == [min(n, budget) for n in lens]
+        return over.item()
+
+    assert flag([64, 100], None) == 0 and flag([0, 1], None) == 0
+    assert flag([30, 3], (0, 1)) == 1                       # short streams keep all where it is
+    assert flag([3, 30], (1, 0), 10 ** 6) == 1
+    assert flag([64, 3], (0, 3)) == 1                       # as many keys as the budget
+    assert flag([100, 40], (0, 0)) == 1                     # sinks, and weights that stay in front
+    assert flag([40, 200], (1, 6)) == 0                     # keys 96 to 111 go
+    assert flag([40, 3], (0, 3)) == 0                       # no key lies there
+
+
 # ------------------------------------------------------------ run together
 def test_a_captured_step_of_all_four(rx):
     """Two layers; each step rotates and stores a step's tokens, attends over
