@@ -447,8 +447,10 @@ rx_status rx_rotate_heads_paged(const void* x, long long row_stride, int N, cons
  * enters its product with V rounded to bf16, out is rounded once to bf16.  A row
  * that sees no key gets zeros and lse -infinity.  Rows of tokens in no stream's
  * range are left as they were.  Whatever lies at places that a row does not see,
- * infinities and NaN among it, has no part in it; a row that sees a key or value
- * that is not finite is not finite.  q_start: int32 [B+1], not decreasing; len,
+ * infinities and NaN among it, has no part in it.  A score of -infinity weighs
+ * nothing; a row with one of +infinity or NaN is not finite, nor is its lse.  A row
+ * that sees a value that is not finite is not finite there (elsewhere it may be NaN),
+ * its lse as without that value.  q_start: int32 [B+1], not decreasing; len,
  * prefix: int32 [B] (len clamped to [0, max_pages*page]), all DEVICE.  Hq, Hkv and
  * D are the cache's where one is given.  workspace: DEVICE memory of
  * rx_attend_pages_workspace bytes, 256-byte aligned, for this call alone while
@@ -458,9 +460,9 @@ rx_status rx_rotate_heads_paged(const void* x, long long row_stride, int N, cons
  * in its own workspace.  A push waits only for the stream that it is given: calls on
  * other streams have to be ordered before the second push that follows them (the
  * first without a spare slot).  A wait that gives up makes its rows NaN and, with a
- * cache, sets bit 3 of its error word.  Errors: RX_ERR_ARG, RX_ERR_LAYER, RX_ERR_UNSUPPORTED (D, Hq/Hkv),
- * RX_ERR_CAPACITY (workspace_bytes), RX_ERR_STATE (the cache is on another
- * device), RX_ERR_CUDA. */
+ * cache, sets bit 3 of its error word.
+ * Errors: RX_ERR_ARG, RX_ERR_LAYER, RX_ERR_UNSUPPORTED (D, Hq/Hkv), RX_ERR_CAPACITY
+ * (workspace_bytes), RX_ERR_STATE (the cache is on another device), RX_ERR_CUDA. */
 rx_status rx_attend_pages(rx_cache_t cache, int layer, const void* q, int N, int Hq, int Hkv, int D,
                           const rx_pages* pages, const int* q_start, const int* len, const int* prefix,
                           void* out, float* lse, void* workspace, long long workspace_bytes,

@@ -45,8 +45,8 @@
 // holds, it weighs nothing.  A weight of 0 times an infinity or NaN in V would
 // still be NaN: in tiles where not every row sees every key the softmax warps
 // read V's tile in shared memory first and write zeros over rows that are
-// outside, or not finite and hidden from some row; rows that see one of the
-// latter become NaN.
+// outside, or not finite and hidden from some row; outputs of rows that see one of
+// the latter become NaN.
 //
 // Warps: 0 = copies of K, 1 = tensor memory, copies of Q and Q K^T, 2 = P V, 3 =
 // copies of V, 4..11 = softmax and epilogue.
@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
         ok = warp_wait(BAR(B_SUM), u & 1, abort_flag);
         l = row_sum[row] + row_sum[kBM + row];   // the same in both threads
       }
-      if (poison || !ok) l = NAN;
+      if (!ok) l = NAN;
       // ---- the part's end
       const bool begins = w.t0 == 0, ends = w.t0 + w.count == w.tiles;
       const int first = (w.rt << w.s.plan.log_a);
@@ -824,6 +824,10 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        }
+        if (poison) {   // (lse is of the scores alone)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = NAN;
         }
         if (row_valid && whole && wide) {
           __nv_bfloat16* dst16 = p.out + at * D + c;

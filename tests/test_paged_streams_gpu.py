@@ -452,6 +452,57 @@ def test_values_that_are_not_finite_stay_with_the_rows_that_see_them(rx, D, Hq, 
         assert np.all(np.isnan(o[20:, first * G:])) and np.all(np.isnan(e[20:, first * G:]))
 
 
+@pytest.mark.parametrize("D,Hq,Hkv", [(256, 8, 1), (128, 4, 2), (64, 4, 4)])
+@pytest.mark.parametrize("what", [np.inf, np.nan])
+@pytest.mark.parametrize("n,held", [(40, 50), (1, 700), (200, 9000)])
+def test_values_have_no_part_in_lse(rx, D, Hq, Hkv, what, n, held):
+    """Values that are not finite, at places that some rows of a tile see and some
+    do not and at places that all see: lse, which is of the scores alone, is bit
+    for bit as without them, and so is what is gathered by it."""
+    import torch
+    g = np.random.default_rng([D, n])
+    pool = Pool(g, [held + n, 60], 16, Hkv, D).fill(g)
+    q = dev(_bits(g, (n + 60, Hq, D)))
+    args = (_int([0, n, n + 60]), _int([held + n, 60]))
+    clean = pool.pages(rx)
+    ref, ref_lse = rx.attend_pages(q, clean, *args, lse=True)
+    bad = W.to_bf16_bits(np.array([what], np.float32))[0]
+    pool.v[pool.rows(0)[[3, held + n - 1]], :, 3] = bad
+    pool.v[pool.rows(1)[7], Hkv - 1, 1] = bad
+    pages = pool.pages(rx)
+    out, lse = rx.attend_pages(q, pages, *args, lse=True)
+    assert torch.equal(lse, ref_lse) and torch.all(torch.isfinite(lse))
+    assert not torch.any(torch.isfinite(out[:n, :, 3])) and not torch.any(torch.isfinite(out[n + 7:, Hq - 1, 1]))
+    assert torch.equal(out[n:n + 7], ref[n:n + 7])
+    rx.weigh_pages(q, lse, pages, *args)
+    rx.weigh_pages(q, ref_lse, clean, *args)
+    r = np.concatenate([pool.rows(0), pool.rows(1)])
+    a, b = (p.weight.view(-1, Hkv).cpu().numpy()[r] for p in (pages, clean))
+    assert np.all(np.isfinite(a)) and np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(256, 8, 1), (128, 4, 2), (64, 4, 4)])
+def test_infinite_keys(rx, D, Hq, Hkv):
+    """A key with an infinity: rows to whose queries it is opposite get a score of
+    -infinity and are as without it; the others, +infinity, are not finite."""
+    import torch
+    g = np.random.default_rng(D)
+    n, held = 30, 100
+    pool = Pool(g, [held + n], 32, Hkv, D).fill(g)
+    q = f64(_bits(g, (n, Hq, D)))
+    q[..., 5] = np.where(np.arange(n)[:, None] % 2, 1, -1) * (1 + np.abs(q[..., 5]))
+    bits = W.to_bf16_bits(q.astype(np.float32))
+    there = np.ones(held + n, bool)
+    at = [40, held + 12]
+    there[at] = False
+    ref = OP.attend(f64(bits), f64(pool.k[pool.rows(0)]), f64(pool.v[pool.rows(0)]), there, 0)
+    pool.k[pool.rows(0)[at], :, 5] = W.to_bf16_bits(np.array([np.inf], np.float32))[0]
+    out, lse = rx.attend_pages(dev(bits), pool.pages(rx), _int([0, n]), _int([held + n]), lse=True)
+    o, e = host64(out), lse.double().cpu().numpy()
+    _check_attention(o[::2], e[::2], *(x[::2] for x in ref))
+    assert not np.any(np.isfinite(o[1::2])) and not np.any(np.isfinite(e[1::2]))
+
+
 @pytest.mark.parametrize("Hq,Hkv,D,lens,new", [
     (8, 1, 256, [20000], [1]),                    # one stream over all SMs
     (8, 1, 256, [9000, 100, 5000], [1, 1, 8]),
