@@ -40,6 +40,13 @@
 //   warp of its own instead, beside K's tensor copies: 175 us, and the single tokens
 //   above 202.)
 //
+// Long sums.  The tensor core drops what an addition has below fp32's last place, so a
+// sum over n keys of one sign comes out too small by some 6 10^-9 n of itself: 8 10^-4
+// at 2^17 keys, 3.3 10^-3 at 2^19, more than bf16's rounding.  After 16384 keys (8 10^-5)
+// O and the row's sum are put away in fp32, in the slot that the unit's part has anyway,
+// and start again.  (The first case above has up to 16 496 keys; its time is as without. One
+// loop over all tiles that looks for a sum's end cost 3% at D = 256.)
+//
 // Masked places.  Scores are masked by selection, so whatever a place behind
 // the stream's end, in a page that the table does not name, or after a token
 // holds, it weighs nothing.  A weight of 0 times an infinity or NaN in V would
@@ -68,6 +75,7 @@ namespace {
 
 constexpr float kRescale = 8.0f;   // log2 units
 constexpr int kMinRunKeys = 256;   // keys of a CTA's run, at least
+constexpr int kSegmentKeys = 16384;   // of a sum of products (see above)
 constexpr int kUnitPad = 4;        // tiles that a unit's start and end cost: chunks with units of 11 to 59 tiles
                                    // take 161 us, and 203 with 0
 constexpr int kMergeThreads = 256;
@@ -93,6 +101,7 @@ struct Layout {
   static constexpr int BN = D == 256 ? 64 : 128;
   static constexpr int BLOCK = BN * 128;                    // 64 columns of a K or V tile
   static constexpr int TILE = KB * BLOCK;
+  static constexpr int SEGMENT = kSegmentKeys / BN;         // tiles of a sum of products, a power of two
   static constexpr int NK = D == 64 ? 5 : 3;
   static constexpr int NV = D == 64 ? 5 : D == 128 ? 3 : 2;
   static constexpr int OFF_Q = 0;
@@ -507,21 +516,22 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
     // ------------------------------------------------------------ P V
     constexpr uint32_t kIdesc = idesc_bf16_f32(kBM, D, false, true);
     const bool leader = elect_one();
-    int j = 0, slot = 0, round = 0, u = 0;
+    int j = 0, slot = 0, round = 0, opened = 0;   // sums opened so far
     bool ok = true;
     do {
-      const int count = uniform(w.count), first_t = uniform(w.t0);
-      for (int t = 0; t < count; ++t) {
+      const int end = uniform(w.t0) + uniform(w.count);
+      for (int t0 = end - uniform(w.count), t = t0; t < end; ++t) {
         const int st = j & 1;
+        if (t - t0 == Lay::SEGMENT) t0 = t;   // a sum's first tile
         if (!warp_wait(BAR(B_PF + st), (j >> 1) & 1, abort_flag)) { ok = false; break; }
         if (!warp_wait(BAR(B_VF + slot), round & 1, abort_flag)) { ok = false; break; }
-        // O still holds the last unit until the softmax warps have read it.
-        if (t == 0 && u > 0 && !warp_wait(BAR(B_OR), (u - 1) & 1, abort_flag)) { ok = false; break; }
+        // O still holds the last sum until the softmax warps have read it.
+        if (t == t0 && opened++ > 0 && !warp_wait(BAR(B_OR), opened & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        const bool paged = first_t + t >= shared;
+        const bool paged = t >= shared;
         const uint64_t desc = sdesc_sw128(sV + slot * Lay::TILE, paged ? 1024 : Lay::BLOCK, paged ? Lay::KB * 1024 : 1024);
         const uint32_t step = (paged ? Lay::KB * 2048 : 2048) >> 4;   // 16 keys
-        const uint32_t more = t > 0 ? 1u : 0u;
+        const uint32_t more = t > t0 ? 1u : 0u;
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < Lay::BN / 16; ++kk)
@@ -536,7 +546,6 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
           ++round;
         }
       }
-      ++u;
     } while (ok && w.next(p));
     if (leader) umma_commit(BAR(B_DRAIN));
     volatile int no_abort = 0;
@@ -607,185 +616,232 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
       float m_used = -INFINITY;
       float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       bool poison = false;
-      for (int t = w.t0; ok && t < w.t0 + w.count; ++t, ++j) {
-        const int st = j & 1;
-        // Keys of the tile that are there, and those that this row sees.
-        Bits<BN> there, mine;
-        bool check;
-        if (t < shared) {
-          constexpr int kHalves = BN / kTileTok;
-          int nv[kHalves];
-          check = false;
+      // What of closed sums lies in the part's place: O in the scale of m_kept.
+      auto kept = [&](int column) {
+        const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
+        return p.part + (slot * (D / 4) + column / 4) * p.part_rows + row;
+      };
+      float m_kept = -INFINITY, l_kept = 0.f;
+      // 32 columns of O, with those of closed sums where there are any.
+      auto read_o = [&](int c, float f, bool closed, float (&o)[32]) {
+        tmem_ld32(tO + c + lane_off, o);
+        if (closed && row_valid) {
+          const float4* from = kept(c);
 #pragma unroll
-          for (int i = 0; i < kHalves; ++i) {
-            nv[i] = store.valid(t * kHalves + i);
-            check = check || nv[i] < kTileTok;
-          }
-          if (check) {
-#pragma unroll
-            for (int i = 0; i < kHalves; ++i) there.w[i] = first_bits(nv[i]);
-            mine = there;
-          }
-        } else {
-          const int key0 = (t - shared) * BN;
-          const int e0 = key0 >> lp;
-          if (e0 - e_base >= 32) {
-            e_base += 32;
-            named32 = named_of(then);
-            then = entry(e_base + 32 + lane);
-          }
-          const uint32_t named = named32 >> (e0 - e_base) & tile_pages;
-          check = named != tile_pages || key0 + BN > plain;
-          if (check) {
-            const int nv = w.s.plan.len - key0, seen = lim - key0;
-#pragma unroll
-            for (int i = 0; i < BN / 64; ++i) {
-              uint64_t x = ~0ull;
-              if (named != tile_pages) {
-                x = 0;
-                for (int e = 0; e < max(1, 64 >> lp); ++e) {   // lp >= 6: one page holds the 64 keys
-                  const int page_of = lp < 6 ? (i << (6 - lp)) + e : lp < kLogT ? i : 0;
-                  if (named >> page_of & 1) x |= lp < 6 ? ((1ull << (1 << lp)) - 1) << (e << lp) : ~0ull;
-                }
-              }
-              there.w[i] = x & first_bits(nv - 64 * i);
-              mine.w[i] = there.w[i] & first_bits(seen - 64 * i);
-            }
+          for (int i = 0; i < 8; ++i) {
+            const float4 x = from[static_cast<size_t>(i) * p.part_rows];
+            o[4 * i] = fmaf(x.x, f, o[4 * i]);
+            o[4 * i + 1] = fmaf(x.y, f, o[4 * i + 1]);
+            o[4 * i + 2] = fmaf(x.z, f, o[4 * i + 2]);
+            o[4 * i + 3] = fmaf(x.w, f, o[4 * i + 3]);
           }
         }
-        const int sb = j % Lay::NS;
-        if (!warp_wait(BAR(B_SF + sb), (j / Lay::NS) & 1, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        float s[BN / 2];   // this thread's columns; the others are looked at only
-        float top;
-        const uint32_t s_own = tS + sb * BN + half * (BN / 2) + lane_off, s_other = tS + sb * BN + (half ^ 1) * (BN / 2) + lane_off;
-        if constexpr (BN == 64) {
-          float r[32];
-          tmem_ld32x2(s_own, s, s_other, r);
-          if (check) {
-            hide(s, static_cast<uint32_t>(mine.w[0] >> (32 * half)));
-            hide(r, static_cast<uint32_t>(mine.w[0] >> (32 - 32 * half)));
-          }
-          top = fmaxf(max32(r), max32(s));
-        } else {
-          float r[64];
-          tmem_ld64(s_other, r);
-          const uint64_t seen_r = half ? mine.w[0] : mine.w[BN / 64 - 1], seen_s = half ? mine.w[BN / 64 - 1] : mine.w[0];
-          if (check) {
-            hide(part(r, 0), static_cast<uint32_t>(seen_r));
-            hide(part(r, 32), static_cast<uint32_t>(seen_r >> 32));
-          }
-          top = fmaxf(max32(part(r, 0)), max32(part(r, 32)));
-          tmem_ld64(s_own, s);
-          if (check) {
-            hide(part(s, 0), static_cast<uint32_t>(seen_s));
-            hide(part(s, 32), static_cast<uint32_t>(seen_s >> 32));
-          }
-          top = fmaxf(top, fmaxf(max32(part(s, 0)), max32(part(s, 32))));
-        }
-        tc_fence_before();
-        mbar_arrive(BAR(B_SR + sb));
-        if (check) {
-          // V's rows, some threads each.  P V of tile j - 2 first: until then
-          // V's barrier may be one phase behind, and its parity would pass.
-          if (j >= 2 && !warp_wait(BAR(B_PV + st), ((j - 2) >> 1) & 1, abort_flag)) { ok = false; break; }
-          if (!warp_wait(BAR(B_VF + vslot), vround & 1, abort_flag)) { ok = false; break; }
-          constexpr int kShare = kSoftmax / BN;   // threads of a V row: 2 or 4
-          const int vr = (threadIdx.x - 128) / kShare;
-          const uint32_t at = sV + vslot * Lay::TILE + (t < shared ? vr * 128 : (vr >> 3) * (Lay::KB * 1024) + (vr & 7) * 128);
-          const uint32_t block = t < shared ? Lay::BLOCK : 1024;
-          constexpr int kChunks = D / 8 / kShare;
-          const int c0 = (lane & (kShare - 1)) * kChunks;
-          const bool outside = !(there.w[vr >> 6] >> (vr & 63) & 1);
-          uint32_t odd = 0;
-          // (A value that every row sees may do to them what it does.)
-          const int unseen = t < shared ? BN : all - (t - shared) * BN;   // keys before it are seen by all
-          if (!outside && vr >= unseen) {
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-              const int c = c0 + i;
-              uint32_t x[4];
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                           : "r"(at + (c >> 3) * block + (((c & 7) ^ (vr & 7)) << 4)));
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                odd |= ((x[e] & 0x7F80u) == 0x7F80u) | ((x[e] & 0x7F800000u) == 0x7F800000u);
-            }
-          }
-          odd |= __shfl_xor_sync(0xffffffffu, odd, 1);
-          if (kShare == 4) odd |= __shfl_xor_sync(0xffffffffu, odd, 2);
-          if (outside || odd) {
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i) st_shared_v4(at + ((c0 + i) >> 3) * block + (((c0 + i) & 7) << 4), 0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-          if (unseen < BN) {
-            // Every second or fourth lane's bit, close up.
-            uint32_t rows = __ballot_sync(0xffffffffu, odd != 0);
-            volatile uint8_t* bits = not_finite + (checks & 1) * 16;
-            if constexpr (kShare == 4) {
-              rows &= 0x11111111u;
-              rows = (rows | rows >> 3) & 0x03030303u;
-              rows = (rows | rows >> 6) & 0x000F000Fu;
-              rows = (rows | rows >> 12) & 0x000000FFu;
-              if (lane == 0) bits[warp - 4] = static_cast<uint8_t>(rows);
-            } else {
-              rows &= 0x55555555u;
-              rows = (rows | rows >> 1) & 0x33333333u;
-              rows = (rows | rows >> 2) & 0x0F0F0F0Fu;
-              rows = (rows | rows >> 4) & 0x00FF00FFu;
-              rows = (rows | rows >> 8) & 0x0000FFFFu;
-              if (lane == 0) reinterpret_cast<volatile uint16_t*>(bits)[warp - 4] = static_cast<uint16_t>(rows);
-            }
-            mbar_arrive(BAR(B_CHK));
-            if (!warp_wait(BAR(B_CHK), checks & 1, abort_flag)) { ok = false; break; }
-            ++checks;
-#pragma unroll
-            for (int i = 0; i < BN / 64; ++i) poison = poison || (reinterpret_cast<volatile uint64_t*>(bits)[i] & mine.w[i]) != 0;
-          }
-        }
-        if (++vslot == Lay::NV) {
-          vslot = 0;
-          ++vround;
-        }
-        const float m_new = fmaxf(m_used, top * p.scale_log2);
-        const bool need = m_new > m_used + kRescale;
-        float fac = 1.f;
-        if (need) {
-          fac = exp2f(m_used - m_new);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) l2[i] = make_float2(l2[i].x * fac, l2[i].y * fac);
-          m_used = m_new;
-        }
-        if (__any_sync(0xffffffffu, need && t > w.t0)) {
+      };
+      auto kept_scale = [&]() { return m_kept == m_used ? 1.f : exp2f(m_kept - m_used); };
+      const int t_end = w.t0 + w.count;
+      for (int sum_t = w.t0; ok && sum_t < t_end; sum_t += Lay::SEGMENT) {
+        if (sum_t > w.t0) {   // close the last sums
           if (!warp_wait(BAR(B_PV + ((j - 1) & 1)), ((j - 1) >> 1) & 1, abort_flag)) { ok = false; break; }
           tc_fence_after();
+          const float f = kept_scale();
 #pragma unroll 1
           for (int c = half * kOCols; c < (half + 1) * kOCols; c += 32) {
             float o[32];
-            tmem_ld32(tO + c + lane_off, o);
+            read_o(c, f, sum_t - w.t0 > Lay::SEGMENT, o);
+            if (row_valid) {
+              float4* to = kept(c);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= fac;
-            tmem_st32(tO + c + lane_off, o);
+              for (int i = 0; i < 8; ++i)
+                to[static_cast<size_t>(i) * p.part_rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
           }
+          tc_fence_before();
+          mbar_arrive(BAR(B_OR));
+          l_kept = fmaf(l_kept, f, (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y));
+          l2[0] = l2[1] = make_float2(0.f, 0.f);
+          m_kept = m_used;
         }
-        const float nmb = m_used == -INFINITY ? 0.f : -m_used;
-        const float2 nmb2 = make_float2(nmb, nmb);
-        uint32_t pk[BN / 4];
+        const int sum_end = min(t_end, sum_t + Lay::SEGMENT);
+        for (int t = sum_t; ok && t < sum_end; ++t, ++j) {
+          const int st = j & 1;
+          // Keys of the tile that are there, and those that this row sees.
+          Bits<BN> there, mine;
+          bool check;
+          if (t < shared) {
+            constexpr int kHalves = BN / kTileTok;
+            int nv[kHalves];
+            check = false;
 #pragma unroll
-        for (int c = 0; c < BN / 4; ++c) {
-          float2 e = fma2(make_float2(s[2 * c], s[2 * c + 1]), scale2, nmb2);
-          e = make_float2(exp2f(e.x), exp2f(e.y));
-          l2[c & 1] = add2(l2[c & 1], e);
-          pk[c] = pack_bf16x2(e.x, e.y);
+            for (int i = 0; i < kHalves; ++i) {
+              nv[i] = store.valid(t * kHalves + i);
+              check = check || nv[i] < kTileTok;
+            }
+            if (check) {
+#pragma unroll
+              for (int i = 0; i < kHalves; ++i) there.w[i] = first_bits(nv[i]);
+              mine = there;
+            }
+          } else {
+            const int key0 = (t - shared) * BN;
+            const int e0 = key0 >> lp;
+            if (e0 - e_base >= 32) {
+              e_base += 32;
+              named32 = named_of(then);
+              then = entry(e_base + 32 + lane);
+            }
+            const uint32_t named = named32 >> (e0 - e_base) & tile_pages;
+            check = named != tile_pages || key0 + BN > plain;
+            if (check) {
+              const int nv = w.s.plan.len - key0, seen = lim - key0;
+#pragma unroll
+              for (int i = 0; i < BN / 64; ++i) {
+                uint64_t x = ~0ull;
+                if (named != tile_pages) {
+                  x = 0;
+                  for (int e = 0; e < max(1, 64 >> lp); ++e) {   // lp >= 6: one page holds the 64 keys
+                    const int page_of = lp < 6 ? (i << (6 - lp)) + e : lp < kLogT ? i : 0;
+                    if (named >> page_of & 1) x |= lp < 6 ? ((1ull << (1 << lp)) - 1) << (e << lp) : ~0ull;
+                  }
+                }
+                there.w[i] = x & first_bits(nv - 64 * i);
+                mine.w[i] = there.w[i] & first_bits(seen - 64 * i);
+              }
+            }
+          }
+          const int sb = j % Lay::NS;
+          if (!warp_wait(BAR(B_SF + sb), (j / Lay::NS) & 1, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          float s[BN / 2];   // this thread's columns; the others are looked at only
+          float top;
+          const uint32_t s_own = tS + sb * BN + half * (BN / 2) + lane_off, s_other = tS + sb * BN + (half ^ 1) * (BN / 2) + lane_off;
+          if constexpr (BN == 64) {
+            float r[32];
+            tmem_ld32x2(s_own, s, s_other, r);
+            if (check) {
+              hide(s, static_cast<uint32_t>(mine.w[0] >> (32 * half)));
+              hide(r, static_cast<uint32_t>(mine.w[0] >> (32 - 32 * half)));
+            }
+            top = fmaxf(max32(r), max32(s));
+          } else {
+            float r[64];
+            tmem_ld64(s_other, r);
+            const uint64_t seen_r = half ? mine.w[0] : mine.w[BN / 64 - 1], seen_s = half ? mine.w[BN / 64 - 1] : mine.w[0];
+            if (check) {
+              hide(part(r, 0), static_cast<uint32_t>(seen_r));
+              hide(part(r, 32), static_cast<uint32_t>(seen_r >> 32));
+            }
+            top = fmaxf(max32(part(r, 0)), max32(part(r, 32)));
+            tmem_ld64(s_own, s);
+            if (check) {
+              hide(part(s, 0), static_cast<uint32_t>(seen_s));
+              hide(part(s, 32), static_cast<uint32_t>(seen_s >> 32));
+            }
+            top = fmaxf(top, fmaxf(max32(part(s, 0)), max32(part(s, 32))));
+          }
+          tc_fence_before();
+          mbar_arrive(BAR(B_SR + sb));
+          if (check) {
+            // V's rows, some threads each.  P V of tile j - 2 first: until then
+            // V's barrier may be one phase behind, and its parity would pass.
+            if (j >= 2 && !warp_wait(BAR(B_PV + st), ((j - 2) >> 1) & 1, abort_flag)) { ok = false; break; }
+            if (!warp_wait(BAR(B_VF + vslot), vround & 1, abort_flag)) { ok = false; break; }
+            constexpr int kShare = kSoftmax / BN;   // threads of a V row: 2 or 4
+            const int vr = (threadIdx.x - 128) / kShare;
+            const uint32_t at = sV + vslot * Lay::TILE + (t < shared ? vr * 128 : (vr >> 3) * (Lay::KB * 1024) + (vr & 7) * 128);
+            const uint32_t block = t < shared ? Lay::BLOCK : 1024;
+            constexpr int kChunks = D / 8 / kShare;
+            const int c0 = (lane & (kShare - 1)) * kChunks;
+            const bool outside = !(there.w[vr >> 6] >> (vr & 63) & 1);
+            uint32_t odd = 0;
+            // (A value that every row sees may do to them what it does.)
+            const int unseen = t < shared ? BN : all - (t - shared) * BN;   // keys before it are seen by all
+            if (!outside && vr >= unseen) {
+#pragma unroll
+              for (int i = 0; i < kChunks; ++i) {
+                const int c = c0 + i;
+                uint32_t x[4];
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                             : "r"(at + (c >> 3) * block + (((c & 7) ^ (vr & 7)) << 4)));
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  odd |= ((x[e] & 0x7F80u) == 0x7F80u) | ((x[e] & 0x7F800000u) == 0x7F800000u);
+              }
+            }
+            odd |= __shfl_xor_sync(0xffffffffu, odd, 1);
+            if (kShare == 4) odd |= __shfl_xor_sync(0xffffffffu, odd, 2);
+            if (outside || odd) {
+#pragma unroll
+              for (int i = 0; i < kChunks; ++i) st_shared_v4(at + ((c0 + i) >> 3) * block + (((c0 + i) & 7) << 4), 0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            if (unseen < BN) {
+              // Every second or fourth lane's bit, close up.
+              uint32_t rows = __ballot_sync(0xffffffffu, odd != 0);
+              volatile uint8_t* bits = not_finite + (checks & 1) * 16;
+              if constexpr (kShare == 4) {
+                rows &= 0x11111111u;
+                rows = (rows | rows >> 3) & 0x03030303u;
+                rows = (rows | rows >> 6) & 0x000F000Fu;
+                rows = (rows | rows >> 12) & 0x000000FFu;
+                if (lane == 0) bits[warp - 4] = static_cast<uint8_t>(rows);
+              } else {
+                rows &= 0x55555555u;
+                rows = (rows | rows >> 1) & 0x33333333u;
+                rows = (rows | rows >> 2) & 0x0F0F0F0Fu;
+                rows = (rows | rows >> 4) & 0x00FF00FFu;
+                rows = (rows | rows >> 8) & 0x0000FFFFu;
+                if (lane == 0) reinterpret_cast<volatile uint16_t*>(bits)[warp - 4] = static_cast<uint16_t>(rows);
+              }
+              mbar_arrive(BAR(B_CHK));
+              if (!warp_wait(BAR(B_CHK), checks & 1, abort_flag)) { ok = false; break; }
+              ++checks;
+#pragma unroll
+              for (int i = 0; i < BN / 64; ++i) poison = poison || (reinterpret_cast<volatile uint64_t*>(bits)[i] & mine.w[i]) != 0;
+            }
+          }
+          if (++vslot == Lay::NV) {
+            vslot = 0;
+            ++vround;
+          }
+          const float m_new = fmaxf(m_used, top * p.scale_log2);
+          const bool need = m_new > m_used + kRescale;
+          float fac = 1.f;
+          if (need) {
+            fac = exp2f(m_used - m_new);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) l2[i] = make_float2(l2[i].x * fac, l2[i].y * fac);
+            m_used = m_new;
+          }
+          if (__any_sync(0xffffffffu, need && t > sum_t)) {
+            if (!warp_wait(BAR(B_PV + ((j - 1) & 1)), ((j - 1) >> 1) & 1, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = half * kOCols; c < (half + 1) * kOCols; c += 32) {
+              float o[32];
+              tmem_ld32(tO + c + lane_off, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= fac;
+              tmem_st32(tO + c + lane_off, o);
+            }
+          }
+          const float nmb = m_used == -INFINITY ? 0.f : -m_used;
+          const float2 nmb2 = make_float2(nmb, nmb);
+          uint32_t pk[BN / 4];
+#pragma unroll
+          for (int c = 0; c < BN / 4; ++c) {
+            float2 e = fma2(make_float2(s[2 * c], s[2 * c + 1]), scale2, nmb2);
+            e = make_float2(exp2f(e.x), exp2f(e.y));
+            l2[c & 1] = add2(l2[c & 1], e);
+            pk[c] = pack_bf16x2(e.x, e.y);
+          }
+          // P's place was last read by P V of tile j - NP.
+          if (j >= Lay::NP && !warp_wait(BAR(B_PV + ((j - Lay::NP) & 1)), ((j - Lay::NP) >> 1) & 1, abort_flag)) { ok = false; break; }
+          if constexpr (BN == 64) tmem_st16(tP + st * (BN / 2) + half * (BN / 4) + lane_off, pk);
+          else tmem_st32(tP + half * (BN / 4) + lane_off, reinterpret_cast<const float*>(pk));
+          tc_fence_before();
+          mbar_arrive(BAR(B_PF + st));
         }
-        // P's place was last read by P V of tile j - NP.
-        if (j >= Lay::NP && !warp_wait(BAR(B_PV + ((j - Lay::NP) & 1)), ((j - Lay::NP) >> 1) & 1, abort_flag)) { ok = false; break; }
-        if constexpr (BN == 64) tmem_st16(tP + st * (BN / 2) + half * (BN / 4) + lane_off, pk);
-        else tmem_st32(tP + half * (BN / 4) + lane_off, reinterpret_cast<const float*>(pk));
-        tc_fence_before();
-        mbar_arrive(BAR(B_PF + st));
       }
       // The next unit's Q, so that its scores are on their way during this one's end.
       Walk coming = w;
@@ -794,7 +850,10 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
       if (more && ok) ok = load_q(u + 1);
       if (ok) ok = warp_wait(BAR(B_PV + ((j - 1) & 1)), ((j - 1) >> 1) & 1, abort_flag);
       tc_fence_after();
+      const bool closed = w.count > Lay::SEGMENT;
+      const float f = kept_scale();
       float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+      if (closed) l = fmaf(l_kept, f, l);
       if (ok) {
         // (The next unit's sums are written behind its last P V, which waits for
         // every thread of this one to have come on.)
@@ -811,7 +870,6 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
       const size_t at = static_cast<size_t>(w.s.q0 + t_row) * p.Hq + h;
       const bool whole = begins && ends;
       const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (begins ? 1 : 0);
-      float4* dst = p.part + slot * (D / 4) * p.part_rows + row;
       // A thread's 16-byte stores into a row of its own are 32 lines an instruction:
       // 32-byte ones halve what a part's end costs.
       const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
@@ -820,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
       for (int c = half * kOCols; c < (half + 1) * kOCols; c += 32) {
         float o[32];
         if (ok) {
-          tmem_ld32(tO + c + lane_off, o);
+          read_o(c, f, closed, o);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.f;
@@ -845,9 +903,10 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
             d4[i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
                                pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
         } else if (row_valid) {
+          float4* to = kept(c);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            dst[static_cast<size_t>(c / 4 + i) * p.part_rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            to[static_cast<size_t>(i) * p.part_rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       }
       if (ok) {

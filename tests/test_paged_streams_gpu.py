@@ -574,6 +574,40 @@ def test_full_size_chunks_give_the_same_bits_twice(rx):
             _check_attention(o[start[b] + t:start[b] + t + 1], e[start[b] + t:start[b] + t + 1], *got)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("one_cta,n", [(True, 300_000), (False, 4_000_005)])
+def test_sums_over_very_many_keys(rx, D, one_cta, n):
+    """Hundreds of thousands of keys in one CTA, units whole and cut, over pages that
+    the table names again and again; values of one sign, where an accumulator that
+    drops its last places is always off to the same side.  16384 keys are 1024
+    additions of 16 products, each of which costs up to two last places, 2^-22, of the
+    sum so far, on average half of the whole: 2^-13 of the result at most; longer sums
+    are closed in fp32.  The outputs' own rounding
+    and the weights' average out over the heads: a mean over 152 x 64 outputs that are
+    off by up to 2^-9 has a deviation of 1.2e-5, over 2 x 64 1e-4, and is held to five
+    times that."""
+    import torch
+    H = torch.cuda.get_device_properties(0).multi_processor_count if one_cta else 2
+    torch.manual_seed(D)
+    page, each = 256, 4                                            # the second half's keys are larger
+    k = torch.randn(2 * each, page, H, D, device="cuda") * torch.tensor([0.5] * each + [1.5] * each, device="cuda")[:, None, None, None]
+    k, v = k.bfloat16(), (0.5 + 0.5 * torch.rand(2 * each, page, H, D, device="cuda")).bfloat16()
+    q = torch.randn(1, H, D, device="cuda").bfloat16()
+    slots = torch.arange(-(-n // page), device="cuda")
+    table = (slots % each + each * (slots >= len(slots) // 2)).to(torch.int32)
+    out, lse = rx.attend_pages(q, rx.Pages(k, v, table[None]), _int([0, 1]), _int([n]), lse=True)
+    times = torch.bincount(table[:-1].long(), minlength=2 * each).double()[:, None].repeat(1, page)
+    times[table[-1].long(), :n - (len(slots) - 1) * page] += 1
+    z = torch.einsum("hd,khd->hk", q[0].double(), k.view(-1, H, D).double()) / D ** 0.5 + times.view(-1).log()
+    ref = torch.einsum("hk,khd->hd", torch.softmax(z, -1), v.view(-1, H, D).double())
+    off = (out[0].double() - ref) / ref
+    assert off.abs().max().item() <= 2.0 ** -8 + 2.0 ** -8 + 2.0 ** -11
+    assert abs(off.mean().item()) <= 2.0 ** -13 + (2.0 ** -14 if one_cta else 2.0 ** -11)
+    reach = (q[0].double().abs() * k.view(-1, H, D).double().abs()).sum(-1).max().item() / D ** 0.5
+    ref_lse = torch.logsumexp(z, -1)
+    assert torch.all((lse[0].double() - ref_lse).abs() <= _err_s(D, reach) + 2.0 ** -20 + 2.0 ** -22 * ref_lse.abs())
+
+
 def test_pools_beyond_32_bits(rx):
     """Places whose bytes lie beyond 2^32 in the pool: rotation, attention,
     weight and eviction."""
