@@ -477,12 +477,13 @@ rx_status rx_attend_pages_workspace(int N, int Hq, int Hkv, int D, long long* by
  * Rows of other streams' tokens, of tokens in no stream and of tokens that do not see
  * j have no part in it, whatever their q and lse hold.
  * out: fp32 [n_pages][page][Hkv], may be the pages' weight; NULL means that.  Other
- * places of out are left as they were.  A page may belong to one stream of a call
- * only.  The same inputs give the same bits.  lse: fp32 [N][Hq] DEVICE (infinite:
- * the row weighs nothing; NaN: the keys that it sees weigh NaN).  workspace: DEVICE memory of rx_weigh_pages_workspace
- * bytes, 256-byte aligned, for this call alone while it runs; may be NULL where
- * that is 0 (few new tokens).  out and the workspace may not overlap another input
- * or each other.
+ * places of out are left as they were.  A page may belong to one of the call's
+ * streams with new tokens only (streams that share one take a call each).  The same
+ * inputs give the same bits.  lse: fp32 [N][Hq] DEVICE (infinite: the row weighs
+ * nothing; NaN: the keys that it sees weigh NaN).  workspace: DEVICE memory of
+ * rx_weigh_pages_workspace bytes, 256-byte aligned, for this call alone while it
+ * runs; may be NULL where that is 0 (few new tokens).  out and the workspace may not
+ * overlap another input or each other.
  * Errors: RX_ERR_ARG, RX_ERR_UNSUPPORTED (D, Hq/Hkv), RX_ERR_CAPACITY
  * (workspace_bytes), RX_ERR_CUDA. */
 rx_status rx_weigh_pages(const void* q, const float* lse, int N, int Hq, int Hkv, int D,

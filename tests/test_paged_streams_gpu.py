@@ -747,6 +747,32 @@ def test_weight_of_long_chunks_gives_the_same_bits_twice(rx):
         np.testing.assert_allclose(got.cpu().numpy(), new[b] * 4, rtol=1e-4)
 
 
+def test_weight_of_a_prefix_that_streams_share(rx):
+    """A call for each stream: those without new tokens leave the shared pages alone."""
+    import torch
+    g = np.random.default_rng(17)
+    Hq, Hkv, D, page = 8, 2, 128, 32
+    pool = Pool(g, [200, 150], page, Hkv, D).fill(g)
+    pool.table[1, :2] = pool.table[0, :2]                    # 64 places
+    pool.w[:] = 0
+    new = [20, 33]
+    q = _bits(g, (sum(new), Hq, D))
+    pages, ln = pool.pages(rx), _int(pool.lens)
+    lse = rx.attend_pages(dev(q), pages, _int([0, 20, 53]), ln, lse=True)[1]
+    for start in ([0, 20, 20], [20, 20, 53]):
+        rx.weigh_pages(dev(q), lse, pages, _int(start), ln)
+    got = pages.weight.cpu().numpy().reshape(pool.w.shape)
+    want, e = np.zeros(pool.w.shape), lse.double().cpu().numpy()
+    rel = 0.0
+    for b, s in enumerate((slice(0, 20), slice(20, 53))):
+        r = pool.rows(b)
+        k = f64(pool.k[r])
+        want[r] += OP.gather(f64(q[s]), e[s], k, np.ones(len(r), bool), 0)
+        reach = np.max(np.abs(k).sum(-1)) * np.max(np.abs(f64(q[s]))) / np.sqrt(D)
+        rel = max(rel, _err_s(D, reach) + 2.0 ** -22 * (np.max(np.abs(e[s])) + reach) + 2.0 ** -20)
+    assert np.all(np.abs(got - want) <= (rel + 2.0 ** -23) * want)
+
+
 @pytest.mark.parametrize("what", [np.inf, -np.inf, np.nan])
 @pytest.mark.parametrize("Hq,Hkv,D", [(8, 1, 256), (8, 2, 128), (4, 4, 64), (128, 1, 64)])
 @pytest.mark.parametrize("new,lens", [
