@@ -935,10 +935,10 @@ __global__ void __launch_bounds__(kThreads, 1) page_attn_kernel(const __grid_con
 }
 
 // Joins the parts of cut units: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
-// Part s of CTA c's unit is in slot 2 c + 1 (s = 0) or 2 (c + s).  An item is four
-// columns of a row, rows fastest.  Units of up to kMergeFew parts: a thread per
-// item; of more: a warp takes every eighth part of 32 items and the eight warps
-// meet in shared memory.
+// Part s of CTA c's unit is in slot 2 c + 1 (s = 0) or 2 (c + s).  Units of up to
+// kMergeFew parts: a thread joins 16 columns of a row, rows fastest.  Of more: an item
+// is four columns of a row, a warp takes every eighth part of 32 items and the eight
+// warps meet in shared memory.
 struct MergeParams {
   const float4* part;
   const float2* part_ml;

@@ -16,9 +16,8 @@
 // workspace, and a second kernel adds them in their order.  Five chunks of up to 999
 // tokens (32/8 heads of 128) over keys to 8000: 65 us so; before what the next
 // paragraph adds 62, and 68 with whole units (some 8 per CTA); 512 tokens over 2000
-// keys of one head of 256: 14 and 28.
-// kUnitCost 4, 1 and 0 gave 64, 63 and 69 us, kMinCut 4 63.  A call with too few
-// rows for a cut has no second kernel.
+// keys of one head of 256: 14 and 28.  (Of those 62 kUnitCost 4, 1 and 0 made 64, 63
+// and 69 us, kMinCut 4 63.)  A call with too few rows for a cut has no second kernel.
 //
 // Whose rows count.  A row tile's columns are packed tokens: behind the stream's come
 // whoever's are next.  A row takes part by its score and its lse alone: scores of rows
@@ -33,8 +32,9 @@
 // One token per stream is bound by the keys' bytes, at this size by the launch's
 // latency (16 streams of up to 2000 keys: 8 us).  The chunks above run at 880
 // TFLOP/s, at D = 64 chunks run at 430: in both an SM gets through some 12 scores a
-// cycle, so the way from scores to sums is the bound, not K Q^T (half of that time
-// at D = 128) nor memory.
+// cycle.  Neither the issue slots (47%) nor the exponents' unit (42%) nor the tensor
+// pipe (43%) is full there: a group has one score tile, whose next product waits for
+// the last scores to be read, so what bounds them is the latency of that round.
 //
 // K is the A operand from tensor memory, put there a unit ahead, so that a K slot
 // is free again at once and single tokens' calls keep the memory busy.  What a
