@@ -472,15 +472,16 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) page_weigh_kernel(const
         for (int i = 0; i < kAhead; ++i) {
           if (!ok || r0 + i >= x.r1) break;
           // Rows behind the stream's, and rows that saw nothing, weigh nothing.  A row whose
-          // lse is NaN gives the keys that it sees an infinite weight (NaN would pass a
-          // hidden score's -infinity), which becomes NaN in the end.
+          // lse is NaN (or below -2 10^38) gives the keys that it sees an infinite weight,
+          // which becomes NaN in the end: NaN or infinity here would pass a hidden score's
+          // -infinity.
           const int left = rows - (r0 + i) * kRows - 4 * lane;
           float f[4];
           bool mute = false;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const bool off = fabsf(v[i][e]) == INFINITY;
-            f[e] = off ? -INFINITY : v[i][e] == v[i][e] ? v[i][e] * -1.44269504088896341f : 3.0e38f;
+            f[e] = off ? -INFINITY : fminf(v[i][e] * -1.44269504088896341f, 3.0e38f);   // (NaN: 3e38)
             mute = mute || (off && e < left);
           }
           mute = __any_sync(0xffffffffu, mute);

@@ -828,14 +828,14 @@ def test_weight_is_of_the_rows_that_see_the_key(rx, what, Hq, Hkv, D):
         return rx.weigh_pages(dev(bits), lse, *args, decay=0.0, out=torch.zeros_like(pages.weight)).cpu().numpy().reshape(pool.w.shape)
     lse = rx.attend_pages(dev(q), *args, lse=True)[1]
     lse_bad = rx.attend_pages(dev(bad), *args, lse=True)[1]
-    lse_nan = lse.clone()
-    lse_nan[t] = float("nan")
+    lse_nan, lse_low = lse.clone(), lse.clone()
+    lse_nan[t], lse_low[t] = float("nan"), -3.2e38
     clean = weigh(q, lse)
     hidden = pool.rows(0)[held + t + 1:]
     assert np.all(np.isfinite(clean[hidden]))
-    for e in (lse_bad, lse_nan):
+    for e in (lse_bad, lse_nan, lse_low):
         np.testing.assert_array_equal(weigh(bad, e)[hidden], clean[hidden])
-    np.testing.assert_array_equal(weigh(q, lse_nan)[hidden], clean[hidden])
+        np.testing.assert_array_equal(weigh(q, e)[hidden], clean[hidden])
     assert np.all(np.isnan(weigh(q, lse_nan)[pool.rows(0)[:held + t + 1]]))
     off = lse.clone()
     off[t] = -float("inf")
